@@ -133,7 +133,7 @@ def _randn(shape, g, std=1.0):
 def _scales(x):
     """Exponent byte (bias 127) of the smallest power of two s >= 2^-60 with max|x| / s <= 448, over the last axis."""
     m, e = torch.frexp(x.abs().amax(-1))
-    return (e - torch.where(m <= 0.875, 9, 8)).clamp(-60, 120) + 127
+    return torch.where(m > 0, e - torch.where(m <= 0.875, 9, 8), -60).clamp(-60, 120) + 127
 
 
 def _power(byte):
