@@ -29,6 +29,7 @@ BD_ERR_DEVICE_TIMEOUT = 6
 BD_ERR_BAD_VARIANT_ID = 7
 BD_ERR_NO_SPACE = 8
 BD_ERR_DEVICE_BOUNDS = 9
+BD_ERR_BAD_INDEX = 10
 BD_ALPHA_SCALAR = 0
 BD_ALPHA_PER_ROW = 1
 BD_MAX_VARIANTS = 64
@@ -37,6 +38,15 @@ BD_LINEAR_BATCH_MAX = 256
 BD_COMPRESS_BATCH_MAX = 4096
 BD_COMPRESS_BATCH_PER_LAUNCH = 8
 BD_LINEAR_BATCH_PER_LAUNCH = 8
+BD_Y_BF16 = 0
+BD_Y_E4M3 = 1
+BD_KV_BF16 = 0
+BD_KV_E4M3 = 1
+BD_LOGITS_BF16 = 0
+BD_LOGITS_F32 = 1
+BD_NORM_MAX_N = 32768
+BD_KV_MAX_HEADS = 1024
+BD_SAMPLE_MAX_VOCAB = 262144
 BD_OPT_COMPRESS_FORM = 1
 BD_OPT_GROUPED_PATH = 2
 BD_OPT_BATCH_KERNEL = 3
@@ -63,6 +73,13 @@ class CompressDesc(ctypes.Structure):
     _fields_ = [("w_base", ctypes.c_void_p), ("w_ft", ctypes.c_void_p), ("bits_out", ctypes.c_void_p),
                 ("alpha_out", ctypes.c_void_p), ("n_out", ctypes.c_int64), ("n_in", ctypes.c_int64),
                 ("alpha_mode", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class KVCacheDesc(ctypes.Structure):
+    """bd_kv_cache: the pools of one layer's paged key-value cache (device pointers and sizes)."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("n_pages", ctypes.c_int64), ("kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("page_size", ctypes.c_int32), ("kv_type", ctypes.c_int32)]
 
 
 class BitDeltaError(RuntimeError):
@@ -137,6 +154,19 @@ def load_library(path: str | None = None):
         lib.bd_linear_grouped_workspace_size.restype = SZ
         lib.bd_linear_grouped.argtypes = [V, V, I64, V, V, V, V, I32, I64, I64, V, V, SZ, V]
         lib.bd_linear_grouped.restype = I32
+        F32, CACHE = ctypes.c_float, ctypes.POINTER(KVCacheDesc)
+        lib.bd_rmsnorm.argtypes = [V, V, V, V, I32, I64, I64, F32, V, I32, V, I32, V, V]
+        lib.bd_rmsnorm.restype = I32
+        lib.bd_kv_append.argtypes = [CACHE, V, I32, V, V, I64, V, V, V, I32, I32, V, I64, V, V]
+        lib.bd_kv_append.restype = I32
+        lib.bd_kv_read.argtypes = [CACHE, V, I32, I32, V, I64, V, V, V]
+        lib.bd_kv_read.restype = I32
+        lib.bd_attention_workspace_size.argtypes = [CACHE, I32, I32]
+        lib.bd_attention_workspace_size.restype = SZ
+        lib.bd_attention_decode.argtypes = [CACHE, V, I32, V, V, I32, I32, F32, I32, V, V, V, SZ, V]
+        lib.bd_attention_decode.restype = I32
+        lib.bd_sample.argtypes = [V, I32, I64, I64, V, V, V, V, V, V, V, V]
+        lib.bd_sample.restype = I32
         _lib = lib
         return lib
 
@@ -391,3 +421,163 @@ def bd_linear_grouped(x: torch.Tensor, variant_ids: torch.Tensor, w_base: torch.
                                           modes_arr, n_var, n_out, n_in, _ptr(y), _ptr(workspace),
                                           workspace.numel() * workspace.element_size(), _stream(stream))
     _check(rc, "bd_linear_grouped")
+
+
+# ---- the rest of a decode step: norm, key-value cache, attention, sampling ----------------
+# Tensors are checked here for type and shape, because the library sees only their addresses.
+
+
+def _arg(t: torch.Tensor | None, name: str, shape, dtype) -> int | None:
+    """Address of a contiguous tensor of the given shape and type (None stays NULL)."""
+    if t is None:
+        return None
+    if t.dtype != dtype:
+        raise ValueError(f"{name}: expected {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: tensors passed to libbitdelta must be contiguous")
+    return t.data_ptr()
+
+
+def _raw_stream(stream) -> int:
+    s = stream if stream is not None else torch.cuda.current_stream()
+    return s.cuda_stream if hasattr(s, "cuda_stream") else int(s)
+
+
+def bd_rmsnorm(x: torch.Tensor, weight: torch.Tensor, eps: float, y: torch.Tensor, residual: torch.Tensor | None = None,
+               residual_out: torch.Tensor | None = None, y_scale: torch.Tensor | None = None,
+               weight_ids: torch.Tensor | None = None, stream=None) -> None:
+    """y = rms-norm of x + residual, scaled by weight[weight_ids[row]] (weight is [n] or [n_weights, n]).
+
+    `residual_out` receives bf16(x + residual) and may be `residual` itself.  A bf16 `y` is
+    rounded once; a float8_e4m3fn `y` comes with `y_scale`, fp32 [m, n / 128] (a scale per
+    128 columns) or [m, 1] (one per row)."""
+    m, n = x.shape
+    bf16 = torch.bfloat16
+    n_weights = weight.shape[0] if weight.dim() == 2 else 1
+    y_type = BD_Y_E4M3 if y.dtype == torch.float8_e4m3fn else BD_Y_BF16
+    scale_cols = 0
+    if y_scale is not None:
+        cols = y_scale.shape[1] if y_scale.dim() == 2 else 0
+        if cols < 1 or n % cols != 0:
+            raise ValueError("y_scale: expected [m, n / 128] or [m, 1]")
+        scale_cols = n // cols
+    rc = load_library().bd_rmsnorm(
+        _arg(x, "x", (m, n), bf16), _arg(residual, "residual", (m, n), bf16),
+        _arg(weight, "weight", weight.shape[:-1] + (n,) if weight.dim() in (1, 2) else (n_weights, n), bf16),
+        _arg(weight_ids, "weight_ids", (m,), torch.int32), n_weights, m, n, eps,
+        _arg(y, "y", (m, n), torch.float8_e4m3fn if y_type else bf16), y_type,
+        _arg(y_scale, "y_scale", (m, n // scale_cols if scale_cols else 0), torch.float32), scale_cols,
+        _arg(residual_out, "residual_out", (m, n), bf16), _raw_stream(stream))
+    _check(rc, "bd_rmsnorm")
+
+
+class KVCache:
+    """The pools of one layer's paged key-value cache (bd_kv_cache); keeps the tensors alive.
+
+    k, v: [n_pages, kv_heads, page_size, head_dim], bf16, or float8_e4m3fn with k_scale and
+    v_scale, the exponent bytes of their rows' power-of-two scales, uint8 [n_pages, kv_heads,
+    page_size]."""
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor, k_scale: torch.Tensor | None = None,
+                 v_scale: torch.Tensor | None = None):
+        if k.dim() != 4:
+            raise ValueError("k: expected [n_pages, kv_heads, page_size, head_dim]")
+        if k.dtype not in (torch.bfloat16, torch.float8_e4m3fn):
+            raise ValueError(f"k: expected torch.bfloat16 or torch.float8_e4m3fn, got {k.dtype}")
+        e4m3 = k.dtype == torch.float8_e4m3fn
+        if e4m3 != (k_scale is not None) or e4m3 != (v_scale is not None):
+            raise ValueError("k_scale and v_scale come with an 8-bit cache, and only with one")
+        n_pages, self.kv_heads, self.page_size, self.head_dim = k.shape
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        d = self.desc = KVCacheDesc()
+        d.k, d.v = _arg(k, "k", k.shape, k.dtype), _arg(v, "v", k.shape, k.dtype)
+        d.k_scale = _arg(k_scale, "k_scale", k.shape[:3], torch.uint8)
+        d.v_scale = _arg(v_scale, "v_scale", k.shape[:3], torch.uint8)
+        d.n_pages, d.kv_heads, d.head_dim, d.page_size = n_pages, self.kv_heads, self.head_dim, self.page_size
+        d.kv_type = BD_KV_E4M3 if e4m3 else BD_KV_BF16
+        self._ref = ctypes.byref(d)
+
+
+def _table(page_table: torch.Tensor):
+    if page_table.dim() != 2:
+        raise ValueError("page_table: expected [n_seqs, max_pages]")
+    return _arg(page_table, "page_table", page_table.shape, torch.int32), *page_table.shape
+
+
+def bd_kv_append(cache: KVCache, q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor, positions: torch.Tensor,
+                 page_table: torch.Tensor, rope: torch.Tensor | None, q_out: torch.Tensor | None,
+                 seq_ids: torch.Tensor | None = None, stream=None) -> None:
+    """Rotate q [t, q_heads, head_dim] into q_out and k [t, kv_heads, head_dim]; write k and v to the cache.
+
+    Token i goes to position positions[i] of sequence seq_ids[i] (of sequence i without
+    seq_ids); a negative position skips it.  `rope` is fp32 [positions, head_dim], cosines then
+    sines; without it nothing is rotated and q and q_out are None.  q_out may be q."""
+    n, dim, bf16 = k.shape[0], cache.head_dim, torch.bfloat16
+    q_heads = q.shape[1] if q is not None and q.dim() == 3 else 0
+    rope_len = rope.shape[0] if rope is not None else 0
+    table, n_seqs, max_pages = _table(page_table)
+    rc = load_library().bd_kv_append(
+        cache._ref, _arg(q, "q", (n, q_heads, dim), bf16), q_heads, _arg(k, "k", (n, cache.kv_heads, dim), bf16),
+        _arg(v, "v", (n, cache.kv_heads, dim), bf16), n, _arg(seq_ids, "seq_ids", (n,), torch.int32),
+        _arg(positions, "positions", (n,), torch.int32), table, n_seqs, max_pages,
+        _arg(rope, "rope", (rope_len, dim), torch.float32), rope_len, _arg(q_out, "q_out", (n, q_heads, dim), bf16),
+        _raw_stream(stream))
+    _check(rc, "bd_kv_append")
+
+
+def bd_kv_read(cache: KVCache, page_table: torch.Tensor, offsets: torch.Tensor, k_out: torch.Tensor,
+               v_out: torch.Tensor, stream=None) -> None:
+    """The first offsets[i + 1] - offsets[i] cached tokens of sequence i, as bf16 rows offsets[i] .. of k_out and v_out."""
+    table, n_seqs, max_pages = _table(page_table)
+    total = k_out.shape[0]
+    shape = (total, cache.kv_heads, cache.head_dim)
+    rc = load_library().bd_kv_read(
+        cache._ref, table, n_seqs, max_pages, _arg(offsets, "offsets", (n_seqs + 1,), torch.int32), total,
+        _arg(k_out, "k_out", shape, torch.bfloat16), _arg(v_out, "v_out", shape, torch.bfloat16), _raw_stream(stream))
+    _check(rc, "bd_kv_read")
+
+
+def bd_attention_workspace_size(cache: KVCache, n_seqs: int, q_heads: int) -> int:
+    """Bytes of the workspace of bd_attention_decode (zero-filled once by the caller)."""
+    return int(load_library().bd_attention_workspace_size(cache._ref, n_seqs, q_heads))
+
+
+def bd_attention_decode(cache: KVCache, q: torch.Tensor, page_table: torch.Tensor, lengths: torch.Tensor,
+                        out: torch.Tensor, workspace: torch.Tensor, scale: float | None = None, window: int = 0,
+                        lse: torch.Tensor | None = None, stream=None) -> None:
+    """Attention of one query per sequence, q [n_seqs, q_heads, head_dim], over its first lengths[i] cached tokens.
+
+    `scale` defaults to head_dim ** -0.5; `window` > 0 lets a query see the last `window` tokens only.
+    `workspace` is a zero-filled device buffer of at least bd_attention_workspace_size bytes (left
+    ready for the next call)."""
+    table, n_seqs, max_pages = _table(page_table)
+    q_heads = q.shape[1] if q.dim() == 3 else 0
+    shape = (n_seqs, q_heads, cache.head_dim)
+    rc = load_library().bd_attention_decode(
+        cache._ref, _arg(q, "q", shape, torch.bfloat16), q_heads, table,
+        _arg(lengths, "lengths", (n_seqs,), torch.int32), n_seqs, max_pages,
+        cache.head_dim ** -0.5 if scale is None else scale, window, _arg(out, "out", shape, torch.bfloat16),
+        _arg(lse, "lse", (n_seqs, q_heads), torch.float32), workspace.data_ptr(),
+        workspace.numel() * workspace.element_size(), _raw_stream(stream))
+    _check(rc, "bd_attention_decode")
+
+
+def bd_sample(logits: torch.Tensor, noise: torch.Tensor, ids: torch.Tensor, temperature: torch.Tensor | None = None,
+              top_k: torch.Tensor | None = None, top_p: torch.Tensor | None = None, min_p: torch.Tensor | None = None,
+              logprob: torch.Tensor | None = None, stream=None) -> None:
+    """Draw ids [m] int32 from logits [m, vocab] (bf16 or fp32) with the given Gumbel noise, fp32 [m, vocab].
+
+    `temperature`, `top_k` (int32), `top_p` and `min_p` hold one setting per row; None leaves the
+    filter off (temperature 1).  `logprob` receives the drawn token's log probability before the filters."""
+    m, vocab = logits.shape
+    f32 = torch.float32
+    bf16_logits = logits.dtype == torch.bfloat16
+    rc = load_library().bd_sample(
+        _arg(logits, "logits", (m, vocab), torch.bfloat16 if bf16_logits else f32),
+        BD_LOGITS_BF16 if bf16_logits else BD_LOGITS_F32, m, vocab, _arg(temperature, "temperature", (m,), f32),
+        _arg(top_k, "top_k", (m,), torch.int32), _arg(top_p, "top_p", (m,), f32), _arg(min_p, "min_p", (m,), f32),
+        _arg(noise, "noise", (m, vocab), f32), _arg(ids, "ids", (m,), torch.int32),
+        _arg(logprob, "logprob", (m,), f32), _raw_stream(stream))
+    _check(rc, "bd_sample")

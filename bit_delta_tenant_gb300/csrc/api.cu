@@ -156,6 +156,7 @@ BD_API const char *bd_status_string(int32_t status) {
         case BD_ERR_BAD_VARIANT_ID: return "variant id outside [0, n_variants)";
         case BD_ERR_NO_SPACE: return "delta cache: no evictable delta leaves room for the request";
         case BD_ERR_DEVICE_BOUNDS: return "bounds-checked build: a device index failed its check (access skipped)";
+        case BD_ERR_BAD_INDEX: return "page id, sequence id, position or length outside its range";
         default: return "unknown status";
     }
 }
@@ -195,6 +196,7 @@ BD_API int32_t bd_get_device_status(void *stream) {
     if (word & bd::kDevBounds) return BD_ERR_DEVICE_BOUNDS;
     if (word & bd::kDevTimeout) return BD_ERR_DEVICE_TIMEOUT;
     if (word & bd::kDevBadVariant) return BD_ERR_BAD_VARIANT_ID;
+    if (word & bd::kDevBadIndex) return BD_ERR_BAD_INDEX;
     return BD_OK;
 }
 

@@ -15,6 +15,7 @@ namespace bd {
 // and cleared by the host).
 constexpr unsigned kDevTimeout = 1u;
 constexpr unsigned kDevBadVariant = 2u;
+constexpr unsigned kDevBadIndex = 8u;
 constexpr unsigned kDevBounds = 4u;  // bounds-checked build: an index failed its check (access skipped)
 
 // Per-launch context every kernel receives: where to record device-side
@@ -198,6 +199,35 @@ size_t grouped_workspace_size(int64_t m, int32_t n_variants, int64_t n_out, int6
 cudaError_t launch_grouped(const void *x, const int32_t *ids, int64_t m, const void *w_base,
                            const GroupedVariants &vars, int64_t n_out, int64_t n_in, void *y, void *ws,
                            size_t ws_bytes, const DevCtx &ctx, cudaStream_t stream);
+
+// ---- decode-step operators around the linears (validated arguments, see bitdelta.h) ----
+struct NormProblem {
+    const void *x, *residual, *weight;
+    const int32_t *ids;
+    void *y, *residual_out;
+    float *y_scale;
+    int64_t m, n;
+    int32_t n_weights, y_type, scale_cols;
+    float eps;
+};
+cudaError_t launch_rmsnorm(const NormProblem &p, const DevCtx &ctx, cudaStream_t stream);
+
+cudaError_t launch_kv_append(const bd_kv_cache &c, const void *q, int32_t q_heads, const void *k, const void *v,
+                             int64_t n_tokens, const int32_t *seq_ids, const int32_t *positions,
+                             const int32_t *page_table, int32_t n_seqs, int32_t max_pages, const float *rope,
+                             int64_t rope_len, void *q_out, const DevCtx &ctx, cudaStream_t stream);
+cudaError_t launch_kv_read(const bd_kv_cache &c, const int32_t *page_table, int32_t n_seqs, int32_t max_pages,
+                           const int32_t *offsets, int64_t total, void *k_out, void *v_out, const DevCtx &ctx,
+                           cudaStream_t stream);
+
+size_t attention_workspace_size(const bd_kv_cache &c, int32_t n_seqs, int32_t q_heads, int num_sms);
+cudaError_t launch_attention(const bd_kv_cache &c, const void *q, int32_t q_heads, const int32_t *page_table,
+                             const int32_t *lengths, int32_t n_seqs, int32_t max_pages, float scale, int32_t window,
+                             void *out, float *lse, void *workspace, const DevCtx &ctx, cudaStream_t stream);
+
+cudaError_t launch_sample(const void *logits, int32_t logits_type, int64_t m, int64_t vocab, const float *temperature,
+                          const int32_t *top_k, const float *top_p, const float *min_p, const float *noise,
+                          int32_t *ids, float *logprob, const DevCtx &ctx, cudaStream_t stream);
 
 // ---- driver entry point for tensor maps (resolved through the runtime) ---------------
 bool encode_tensor_map_2d(CUtensorMap *map, CUtensorMapDataType dtype, const void *base, uint64_t inner,

@@ -1,0 +1,287 @@
+// kv_cache.cu -- writing new tokens into the paged key-value cache (rotary
+// positions, quantisation) and reading cached tokens back as bf16.
+//
+// Bound: HBM for long inputs, latency for a decode step's few tokens.  Each
+// input is read once and each output written once.  A row of head_dim elements
+// belongs to head_dim / 8 neighbouring lanes, 16 bytes of bf16 each, so its
+// rotation partner and its maximum are a few shuffles away.
+#include <cuda_fp8.h>
+
+#include "bd_device.cuh"
+#include "bd_internal.h"
+
+namespace bd {
+namespace {
+
+__device__ __forceinline__ void unpack8(const uint4 &v, float (&f)[8]) {
+    f[0] = bf16lo_to_f32(v.x), f[1] = bf16hi_to_f32(v.x);
+    f[2] = bf16lo_to_f32(v.y), f[3] = bf16hi_to_f32(v.y);
+    f[4] = bf16lo_to_f32(v.z), f[5] = bf16hi_to_f32(v.z);
+    f[6] = bf16lo_to_f32(v.w), f[7] = bf16hi_to_f32(v.w);
+}
+__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
+    return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
+                      pack_bf16x2(f[6], f[7]));
+}
+
+// ---- append ----------------------------------------------------------------------------
+
+constexpr int kAppendThreads = 256;
+
+struct AppendArgs {
+    const uint8_t *q, *k, *v;  // bf16
+    uint8_t *q_out, *ck, *cv, *ck_scale, *cv_scale;
+    const int32_t *seq_ids, *positions, *page_table;
+    const float *rope;
+    unsigned *status;
+    int64_t rope_len, n_pages;
+    int32_t q_heads, kv_heads, page_size, n_seqs, max_pages;
+};
+
+// Exponent byte (bias 127) of the smallest power of two s with top <= 448 s, kept within 2^-60 .. 2^120.
+// 448 = 1.75 * 2^8, so a maximum of mantissa <= 1.75 and exponent e takes 2^(e - 8), a larger one 2^(e - 7).
+__device__ __forceinline__ int scale_byte(float top) {
+    const uint32_t b = __float_as_uint(top);
+    const int e = static_cast<int>(b >> 23) - 8 + ((b & 0x7FFFFFu) > 0x600000u ? 1 : 0);
+    return min(max(e, 127 - 60), 127 + 120);
+}
+
+// One CTA per token; rows are its q heads, then k heads, then v heads.
+template <int kDim, bool kE4m3>
+__global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const AppendArgs a) {
+    constexpr int kLanes = kDim / 8;  // lanes of one row
+    constexpr int kRowsPerPass = kAppendThreads / kLanes;
+    pdl_trigger_and_wait();
+    const int64_t t = blockIdx.x;
+    const int32_t pos = a.positions[t];
+    if (pos < 0) return;  // padding
+    const int64_t seq = a.seq_ids ? a.seq_ids[t] : t;
+    const int64_t page_at = pos / a.page_size;
+    const int slot = pos % a.page_size;
+    int64_t page = -1;
+    if (seq >= 0 && seq < a.n_seqs && page_at < a.max_pages && (a.rope == nullptr || pos < a.rope_len))
+        page = a.page_table[seq * a.max_pages + page_at];
+    if (page < 0 || page >= a.n_pages) {
+        if (threadIdx.x == 0) flag_status(a.status, kDevBadIndex);
+        return;
+    }
+    const int lane = threadIdx.x % kLanes;
+    float c[8] = {}, s[8] = {};
+    if (a.rope != nullptr) {
+        const float *r = a.rope + pos * static_cast<int64_t>(kDim) + lane % (kLanes / 2) * 8;
+#pragma unroll
+        for (int j = 0; j < 8; j += 4) {
+            const float4 cv = *reinterpret_cast<const float4 *>(r + j);
+            const float4 sv = *reinterpret_cast<const float4 *>(r + kDim / 2 + j);
+            c[j] = cv.x, c[j + 1] = cv.y, c[j + 2] = cv.z, c[j + 3] = cv.w;
+            s[j] = sv.x, s[j + 1] = sv.y, s[j + 2] = sv.z, s[j + 3] = sv.w;
+        }
+    }
+    const bool upper = lane >= kLanes / 2;
+    const int q_rows = a.q ? a.q_heads : 0;
+    const int rows = q_rows + 2 * a.kv_heads;
+    for (int r0 = 0; r0 < rows; r0 += kRowsPerPass) {
+        const int r = r0 + threadIdx.x / kLanes;
+        const bool on = r < rows;
+        const bool is_q = r < q_rows, is_v = r >= q_rows + a.kv_heads;
+        const int head = is_q ? r : r - q_rows - (is_v ? a.kv_heads : 0);
+        uint4 in = make_uint4(0, 0, 0, 0);
+        if (on) {
+            const uint8_t *src = is_q ? a.q + (t * a.q_heads + head) * (kDim * 2)
+                                      : (is_v ? a.v : a.k) + (t * a.kv_heads + head) * (kDim * 2);
+            in = *reinterpret_cast<const uint4 *>(src + lane * 16);
+        }
+        float x[8];
+        unpack8(in, x);
+        if (a.rope != nullptr) {  // every lane shuffles; rows of v keep x
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float o = __shfl_xor_sync(0xFFFFFFFFu, x[j], kLanes / 2);
+                const float turned = upper ? __fadd_rn(__fmul_rn(x[j], c[j]), __fmul_rn(o, s[j]))
+                                           : __fsub_rn(__fmul_rn(x[j], c[j]), __fmul_rn(o, s[j]));
+                if (!is_v) x[j] = turned;
+            }
+        }
+        float top = 0.f;
+        if constexpr (kE4m3) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float m = fabsf(x[j]);
+                if (m < INFINITY) top = fmaxf(top, m);  // neither infinity nor NaN
+            }
+#pragma unroll
+            for (int o = kLanes / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+        }
+        if (!on) continue;
+        if (is_q) {
+            *reinterpret_cast<uint4 *>(a.q_out + (t * a.q_heads + head) * (kDim * 2) + lane * 16) = pack8(x);
+            continue;
+        }
+        const int64_t at = (page * a.kv_heads + head) * a.page_size + slot;
+        uint8_t *dst = is_v ? a.cv : a.ck;
+        if constexpr (!kE4m3) {
+            *reinterpret_cast<uint4 *>(dst + at * (kDim * 2) + lane * 16) = pack8(x);
+        } else {
+            const int e = scale_byte(top);
+            const float inv = __uint_as_float(static_cast<uint32_t>(254 - e) << 23);  // 2^(127 - e), exact
+            uint32_t b[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                b[j] = __nv_cvt_float2_to_fp8x2(make_float2(x[2 * j] * inv, x[2 * j + 1] * inv), __NV_SATFINITE,
+                                                __NV_E4M3);
+            *reinterpret_cast<uint2 *>(dst + at * kDim + lane * 8) = make_uint2(b[0] | b[1] << 16, b[2] | b[3] << 16);
+            if (lane == 0) (is_v ? a.cv_scale : a.ck_scale)[at] = static_cast<uint8_t>(e);
+        }
+    }
+}
+
+// ---- read ------------------------------------------------------------------------------
+
+constexpr int kReadThreads = 256;
+constexpr int kReadTokens = 16;  // output rows of one CTA
+
+struct ReadArgs {
+    const uint8_t *ck, *cv, *ck_scale, *cv_scale;
+    const int32_t *page_table, *offsets;
+    uint8_t *k_out, *v_out;
+    unsigned *status;
+    int64_t n_pages, total;
+    int32_t kv_heads, page_size, n_seqs, max_pages;
+};
+
+// Two e4m3 values times 2^(e - 127), as a bf16 pair (exact down to bf16's subnormals).
+__device__ __forceinline__ uint32_t e4m3x2_to_bf16x2(uint32_t two, float scale) {
+    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(two), __NV_E4M3);
+    const float2 f = __half22float2(__half2(h));
+    return pack_bf16x2(f.x * scale, f.y * scale);
+}
+
+template <int kDim, bool kE4m3>
+__global__ void __launch_bounds__(kReadThreads) kv_read_kernel(const ReadArgs a) {
+    constexpr int kChunk = kE4m3 ? kDim / 16 : kDim / 8;  // 16-byte chunks of a stored row
+    __shared__ int64_t first[kReadTokens];                // (page * kv_heads) * page_size + slot; -1: nothing, -2: zeros
+    pdl_trigger_and_wait();
+    const int64_t t0 = static_cast<int64_t>(blockIdx.x) * kReadTokens;
+    if (threadIdx.x < kReadTokens) {
+        const int64_t t = t0 + threadIdx.x;
+        int64_t at = -1;
+        if (t < a.total && t < a.offsets[a.n_seqs]) {
+            int lo = 0, hi = a.n_seqs;  // the last sequence that starts at or before t
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) / 2;
+                if (a.offsets[mid] <= t) lo = mid;
+                else hi = mid;
+            }
+            const int64_t pos = t - a.offsets[lo];
+            const int64_t p = pos / a.page_size;
+            const int64_t page = pos >= 0 && p < a.max_pages ? a.page_table[static_cast<int64_t>(lo) * a.max_pages + p] : -1;
+            at = page >= 0 && page < a.n_pages ? page * a.kv_heads * a.page_size + pos % a.page_size : -2;
+            if (at == -2) flag_status(a.status, kDevBadIndex);
+        }
+        first[threadIdx.x] = at;
+    }
+    __syncthreads();
+    const int per_token = a.kv_heads * kChunk;
+    const int items = kReadTokens * per_token;
+    for (int which = 0; which < 2; ++which) {
+        const uint8_t *src = which ? a.cv : a.ck;
+        const uint8_t *sc = which ? a.cv_scale : a.ck_scale;
+        uint8_t *out = which ? a.v_out : a.k_out;
+        for (int i = threadIdx.x; i < items; i += kReadThreads) {
+            const int tok = i / per_token, rest = i % per_token;
+            const int head = rest / kChunk, c = rest % kChunk;
+            const int64_t f = first[tok];
+            if (f == -1) continue;
+            const int64_t row = f + static_cast<int64_t>(head) * a.page_size;
+            uint4 v = make_uint4(0, 0, 0, 0);
+            if (f >= 0) v = ldg_stream(src + (row * kChunk + c) * 16);
+            uint8_t *dst = out + (((t0 + tok) * a.kv_heads + head) * kChunk + c) * (kE4m3 ? 32 : 16);
+            if constexpr (!kE4m3) {
+                *reinterpret_cast<uint4 *>(dst) = v;
+            } else {
+                const float s = f >= 0 ? __uint_as_float(static_cast<uint32_t>(sc[row]) << 23) : 0.f;
+                uint4 *d = reinterpret_cast<uint4 *>(dst);
+                d[0] = make_uint4(e4m3x2_to_bf16x2(v.x & 0xFFFFu, s), e4m3x2_to_bf16x2(v.x >> 16, s),
+                                  e4m3x2_to_bf16x2(v.y & 0xFFFFu, s), e4m3x2_to_bf16x2(v.y >> 16, s));
+                d[1] = make_uint4(e4m3x2_to_bf16x2(v.z & 0xFFFFu, s), e4m3x2_to_bf16x2(v.z >> 16, s),
+                                  e4m3x2_to_bf16x2(v.w & 0xFFFFu, s), e4m3x2_to_bf16x2(v.w >> 16, s));
+            }
+        }
+    }
+}
+
+template <class Args>
+cudaError_t launch_pdl(void (*kernel)(const Args), int64_t grid, int threads, const Args &a, cudaStream_t stream) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(grid));
+    cfg.blockDim = dim3(threads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, a);
+}
+
+}  // namespace
+
+cudaError_t launch_kv_append(const bd_kv_cache &c, const void *q, int32_t q_heads, const void *k, const void *v,
+                             int64_t n_tokens, const int32_t *seq_ids, const int32_t *positions,
+                             const int32_t *page_table, int32_t n_seqs, int32_t max_pages, const float *rope,
+                             int64_t rope_len, void *q_out, const DevCtx &ctx, cudaStream_t stream) {
+    AppendArgs a;
+    a.q = static_cast<const uint8_t *>(q);
+    a.k = static_cast<const uint8_t *>(k);
+    a.v = static_cast<const uint8_t *>(v);
+    a.q_out = static_cast<uint8_t *>(q_out);
+    a.ck = static_cast<uint8_t *>(c.k);
+    a.cv = static_cast<uint8_t *>(c.v);
+    a.ck_scale = c.k_scale;
+    a.cv_scale = c.v_scale;
+    a.seq_ids = seq_ids;
+    a.positions = positions;
+    a.page_table = page_table;
+    a.rope = rope;
+    a.status = ctx.status;
+    a.rope_len = rope_len;
+    a.n_pages = c.n_pages;
+    a.q_heads = q_heads;
+    a.kv_heads = c.kv_heads;
+    a.page_size = c.page_size;
+    a.n_seqs = n_seqs;
+    a.max_pages = max_pages;
+    const bool e = c.kv_type == BD_KV_E4M3;
+    if (c.head_dim == 128)
+        return launch_pdl(e ? kv_append_kernel<128, true> : kv_append_kernel<128, false>, n_tokens, kAppendThreads, a,
+                          stream);
+    return launch_pdl(e ? kv_append_kernel<64, true> : kv_append_kernel<64, false>, n_tokens, kAppendThreads, a, stream);
+}
+
+cudaError_t launch_kv_read(const bd_kv_cache &c, const int32_t *page_table, int32_t n_seqs, int32_t max_pages,
+                           const int32_t *offsets, int64_t total, void *k_out, void *v_out, const DevCtx &ctx,
+                           cudaStream_t stream) {
+    ReadArgs a;
+    a.ck = static_cast<const uint8_t *>(c.k);
+    a.cv = static_cast<const uint8_t *>(c.v);
+    a.ck_scale = c.k_scale;
+    a.cv_scale = c.v_scale;
+    a.page_table = page_table;
+    a.offsets = offsets;
+    a.k_out = static_cast<uint8_t *>(k_out);
+    a.v_out = static_cast<uint8_t *>(v_out);
+    a.status = ctx.status;
+    a.n_pages = c.n_pages;
+    a.total = total;
+    a.kv_heads = c.kv_heads;
+    a.page_size = c.page_size;
+    a.n_seqs = n_seqs;
+    a.max_pages = max_pages;
+    const int64_t grid = (total + kReadTokens - 1) / kReadTokens;
+    const bool e = c.kv_type == BD_KV_E4M3;
+    if (c.head_dim == 128)
+        return launch_pdl(e ? kv_read_kernel<128, true> : kv_read_kernel<128, false>, grid, kReadThreads, a, stream);
+    return launch_pdl(e ? kv_read_kernel<64, true> : kv_read_kernel<64, false>, grid, kReadThreads, a, stream);
+}
+
+}  // namespace bd

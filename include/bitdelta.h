@@ -61,8 +61,10 @@ typedef enum bd_status {
     BD_ERR_DEVICE_TIMEOUT = 6,    /* a bounded device-side wait ran out         */
     BD_ERR_BAD_VARIANT_ID = 7,    /* a variant id outside [0, n_variants)       */
     BD_ERR_NO_SPACE = 8,          /* delta cache: nothing evictable leaves room  */
-    BD_ERR_DEVICE_BOUNDS = 9      /* bounds-checked build only: a device index
+    BD_ERR_DEVICE_BOUNDS = 9,     /* bounds-checked build only: a device index
                                      failed its check and the access was skipped */
+    BD_ERR_BAD_INDEX = 10         /* a page id, sequence id, position or length on
+                                     the device lies outside its range          */
 } bd_status;
 
 /* How alpha is stored ([math]: one per matrix; [infra]: one per output row). */
@@ -387,6 +389,213 @@ int32_t bd_cache_get_stats(bd_cache *cache, bd_cache_stats *out);
 int32_t bd_cache_is_resident(bd_cache *cache, int32_t variant);
 
 /* ------------------------------------------------------------------------ *
+ * The rest of a decode step.  [serve] describes requests of many variants
+ * running over one resident base; between two fused linears such a step
+ * normalises, writes and reads a key-value cache and, at its end, draws a
+ * token.  The page prints none of these; the entry points below define them.
+ * None of them allocates, waits on the host or needs a size that only the
+ * device knows, so a whole step can be captured in a CUDA graph.
+ * ------------------------------------------------------------------------ */
+
+/* ------------------------------------------------------------------------ *
+ * Residual addition and root-mean-square norm, in bf16 or 8 bits
+ *
+ *   h[t, j] = x[t, j] + residual[t, j]                 (fp32; residual may be NULL: h = x)
+ *   residual_out[t, j] = bf16(h[t, j])                 (NULL: not written)
+ *   y[t, j] = h[t, j] * rsqrt(mean_j h[t, j]^2 + eps) * weight[w(t), j]
+ * with w(t) = weight_ids[t], or 0 when weight_ids is NULL: the linears of a
+ * variant are compressed, its norm weights are small and kept whole, one row
+ * each.  The sum of squares and y are fp32; the norm uses the unrounded h.
+ * y_type BD_Y_BF16 rounds y once.  BD_Y_E4M3 stores q = e4m3(y / s) with
+ * s = max|y| / 448 over scale_cols columns: 128, or n for one scale per row;
+ * y ~= q * s.  s is 1 where max|h * weight| is below 2^-100 (zeros among
+ * them).  NaN does not enter the maximum.
+ *
+ *   x, residual   bf16 [m, n]            (read; residual may be NULL)
+ *   weight        bf16 [n_weights, n]    (read)
+ *   weight_ids    int32 [m] or NULL      (read, device; then n_weights >= 1)
+ *   y             bf16 or e4m3 [m, n]    (written)
+ *   y_scale       float [m, n / scale_cols] for BD_Y_E4M3, else NULL (written)
+ *   residual_out  bf16 [m, n] or NULL    (written; may be residual or x itself)
+ * n: a multiple of 8, at most BD_NORM_MAX_N; for scale_cols = 128 a multiple
+ * of 128.  m = 0 launches nothing.  An id outside [0, n_weights) sets
+ * BD_ERR_BAD_VARIANT_ID in the device status word and leaves the row unwritten.
+ * Errors: BD_ERR_INVALID_ARG, BD_ERR_UNSUPPORTED_SHAPE, BD_ERR_MISALIGNED,
+ *         BD_ERR_CUDA.
+ * ------------------------------------------------------------------------ */
+#define BD_NORM_MAX_N 32768
+typedef enum bd_y_type { BD_Y_BF16 = 0, BD_Y_E4M3 = 1 } bd_y_type;
+
+int32_t bd_rmsnorm(const void *x, const void *residual, const void *weight, const int32_t *weight_ids,
+                   int32_t n_weights, int64_t m, int64_t n, float eps, void *y, int32_t y_type, float *y_scale,
+                   int32_t scale_cols, void *residual_out, void *stream);
+
+/* ------------------------------------------------------------------------ *
+ * Paged key-value cache of one layer
+ *
+ * K and V each are a pool of pages [n_pages, kv_heads, page_size, head_dim]:
+ * the tokens of one page and head are contiguous.  Token p of a sequence lies
+ * in slot p % page_size of page page_table[sequence][p / page_size].  Types:
+ *   BD_KV_BF16  the values; k_scale and v_scale are NULL
+ *   BD_KV_E4M3  8-bit values and one scale per (page, head, slot), a power of
+ *               two kept as its exponent byte e (value 2^(e - 127)), uint8
+ *               [n_pages, kv_heads, page_size]
+ * A row is quantised as it is written: s is the smallest power of two with
+ * max|x| / s <= 448 (the largest e4m3 number), at least 2^-60 and at most
+ * 2^120, the maximum taken over the row's finite values; q = e4m3(x / s), to
+ * nearest even, infinities to +-448, NaN kept.  A floating-point format loses
+ * nothing to a power-of-two scale, x / s and q * s are exact, and q * s is a
+ * bf16 number (infinite from 2^128), so reading back into bf16 rounds nothing.
+ *
+ * page_size: a multiple of 16, 16 .. 1024.  head_dim: 64 or 128.  kv_heads:
+ * 1 .. BD_KV_MAX_HEADS.  Pointers 16-byte aligned.  The struct is read during
+ * the call only.
+ * ------------------------------------------------------------------------ */
+#define BD_KV_MAX_HEADS 1024
+typedef enum bd_kv_type { BD_KV_BF16 = 0, BD_KV_E4M3 = 1 } bd_kv_type;
+typedef struct bd_kv_cache {
+    void *k;            /* [n_pages, kv_heads, page_size, head_dim] */
+    void *v;
+    uint8_t *k_scale;   /* [n_pages, kv_heads, page_size], BD_KV_E4M3 only */
+    uint8_t *v_scale;
+    int64_t n_pages;
+    int32_t kv_heads;
+    int32_t head_dim;
+    int32_t page_size;
+    int32_t kv_type;    /* bd_kv_type */
+} bd_kv_cache;
+
+/* ------------------------------------------------------------------------ *
+ * Rotary positions and cache write of new tokens
+ *
+ * Token t belongs to sequence seq_ids[t] (t itself when seq_ids is NULL) at
+ * position p = positions[t].  Its q and k rows are rotated: with d = head_dim
+ * / 2, c = rope[p, i] and s = rope[p, d + i], 0 <= i < d,
+ *   x'[i] = x[i] c - x[d + i] s,   x'[d + i] = x[d + i] c + x[i] s
+ * (each product and the sum rounded to fp32 on its own).  q' is rounded to
+ * bf16 into q_out; k' and v go to the cache as its type stores them.  A
+ * negative position skips the token (a padded batch): nothing is written.
+ * rope NULL: no rotation (k as given; q and q_out must be NULL).  q NULL: only
+ * the cache is written.
+ *
+ *   q           bf16 [n_tokens, q_heads, head_dim] or NULL   (read)
+ *   k, v        bf16 [n_tokens, kv_heads, head_dim]          (read)
+ *   seq_ids     int32 [n_tokens] or NULL                     (read)
+ *   positions   int32 [n_tokens]                             (read)
+ *   page_table  int32 [n_seqs, max_pages]                    (read)
+ *   rope        float [rope_len, head_dim] or NULL           (read)
+ *   q_out       bf16 [n_tokens, q_heads, head_dim]           (written; may be q)
+ * Two tokens of one call must not name the same slot.  A sequence id, position
+ * (against max_pages and rope_len) or page id out of range sets
+ * BD_ERR_BAD_INDEX in the device status word and skips that token.
+ * Errors: BD_ERR_INVALID_ARG, BD_ERR_UNSUPPORTED_SHAPE, BD_ERR_MISALIGNED,
+ *         BD_ERR_CUDA.
+ * ------------------------------------------------------------------------ */
+int32_t bd_kv_append(const bd_kv_cache *cache, const void *q, int32_t q_heads, const void *k, const void *v,
+                     int64_t n_tokens, const int32_t *seq_ids, const int32_t *positions, const int32_t *page_table,
+                     int32_t n_seqs, int32_t max_pages, const float *rope, int64_t rope_len, void *q_out,
+                     void *stream);
+
+/* ------------------------------------------------------------------------ *
+ * Cache read-back
+ *
+ * Positions 0 .. offsets[i + 1] - offsets[i] - 1 of sequence i become rows
+ * offsets[i] .. offsets[i + 1] - 1 of k_out and v_out, as bf16 (q * s, exact).
+ *   offsets     int32 [n_seqs + 1], ascending from 0          (read)
+ *   page_table  int32 [n_seqs, max_pages]                     (read)
+ *   k_out, v_out  bf16 [total, kv_heads, head_dim]            (written)
+ * Rows from offsets[n_seqs] up to total are left as they are.  A position
+ * beyond the table or a page id out of range sets BD_ERR_BAD_INDEX and gives a
+ * row of zeros.
+ * Errors: as bd_kv_append.
+ * ------------------------------------------------------------------------ */
+int32_t bd_kv_read(const bd_kv_cache *cache, const int32_t *page_table, int32_t n_seqs, int32_t max_pages,
+                   const int32_t *offsets, int64_t total, void *k_out, void *v_out, void *stream);
+
+/* ------------------------------------------------------------------------ *
+ * Attention of one new token per sequence over its cached keys
+ *
+ * Query head h reads KV head h / (q_heads / kv_heads).  Over the positions j
+ * the query sees -- 0 <= j < lengths[i], and j >= lengths[i] - window when
+ * window > 0 --
+ *   s_j = scale * sum_d q[i, h, d] K_j[d],   out[i, h] = sum_j softmax(s)_j V_j
+ *   lse[i, h] = log sum_j exp(s_j)
+ * (the new token's own key is in the cache: bd_kv_append comes first).  A
+ * sequence of length 0 gives zeros and lse = -inf.  Slots no query sees are
+ * not read into the result whatever they hold, and pages wholly outside the
+ * window are not touched.  Scores, softmax statistics and the output's sums
+ * are fp32; out is rounded once to bf16.  The softmax weights enter the
+ * tensor cores as two 16-bit parts each (about 2^-16 of each weight); an
+ * infinite V that a query sees may therefore give NaN.
+ *
+ *   q           bf16 [n_seqs, q_heads, head_dim]        (read)
+ *   page_table  int32 [n_seqs, max_pages]               (read)
+ *   lengths     int32 [n_seqs]                          (read)
+ *   out         bf16 [n_seqs, q_heads, head_dim]        (written)
+ *   lse         float [n_seqs, q_heads] or NULL         (written)
+ *   workspace   device buffer of at least bd_attention_workspace_size bytes,
+ *               256-byte aligned, ZERO-FILLED before its first use; every call
+ *               leaves it ready for the next one of any size it is large
+ *               enough for.  Calls that may run concurrently need one each.
+ * The key tiles of all sequences and heads are split evenly over the GPU's
+ * CTAs; a (sequence, head) that several CTAs share is joined by the last of
+ * them to finish, in key order, so results do not depend on timing.  No CTA
+ * waits for another.  q_heads: a multiple of kv_heads.
+ * A length below 0 or beyond max_pages * page_size, or a page id out of range,
+ * sets BD_ERR_BAD_INDEX; the length counts as the nearest allowed one and the
+ * keys of such a page as unseen.
+ * Errors: BD_ERR_INVALID_ARG, BD_ERR_UNSUPPORTED_SHAPE, BD_ERR_MISALIGNED,
+ *         BD_ERR_WORKSPACE, BD_ERR_CUDA.
+ * ------------------------------------------------------------------------ */
+size_t bd_attention_workspace_size(const bd_kv_cache *cache, int32_t n_seqs, int32_t q_heads);
+
+int32_t bd_attention_decode(const bd_kv_cache *cache, const void *q, int32_t q_heads, const int32_t *page_table,
+                            const int32_t *lengths, int32_t n_seqs, int32_t max_pages, float scale, int32_t window,
+                            void *out, float *lse, void *workspace, size_t workspace_bytes, void *stream);
+
+/* ------------------------------------------------------------------------ *
+ * Draw of the next token, each row with its own settings
+ *
+ * Row by row, with M = max_i x_i and T the row's temperature,
+ *   z_i = (x_i - M) * (1 / T)              (fp32, each operation rounded)
+ *   w_i = exp(z_i),  logprob = z_id - log sum_i w_i  (before any filter)
+ * The tokens are ordered by logit, larger first, equal logits by lower index.
+ * Kept are, in this order of the filters:
+ *   top_k  the first k                     (k <= 0: off)
+ *   top_p  of those, the shortest prefix whose share of their summed w is at
+ *          least p: a token stays while the w before it sum to less than
+ *          p * sum.  The first always stays; p >= 1: off.
+ *   min_p  those with w_i >= min_p         (<= 0: off; the largest w is 1 and
+ *          always stays)
+ * The token drawn is the kept one with the largest z_i + noise_i, the lowest
+ * index on ties.  With noise_i = -log(-log u_i), u_i uniform on (0, 1), this
+ * is a draw with probabilities w_i / sum of the kept w.  T <= 0: the first
+ * token of the order (T counts as 1 in logprob).  A NaN logit counts as -inf;
+ * a logit of -inf is never drawn; a row of nothing else gives id -1 and
+ * logprob -inf.  With a logit of +inf all weight is on those equal to it.
+ * NaN settings count as: T 0, p and min_p off.  NaN noise counts as -inf.
+ * Results do not depend on timing.
+ *
+ *   logits       bf16 or float [m, vocab]   (read)
+ *   noise        float [m, vocab]           (read where it can decide: at kept
+ *                tokens)
+ *   temperature  float [m] or NULL (1)      (read, device)
+ *   top_k        int32 [m] or NULL (off)
+ *   top_p, min_p float [m] or NULL (off)
+ *   ids          int32 [m]                  (written)
+ *   logprob      float [m] or NULL          (written)
+ * vocab: 1 .. BD_SAMPLE_MAX_VOCAB.  The [m] arrays need only 4-byte alignment.
+ * Errors: BD_ERR_INVALID_ARG, BD_ERR_UNSUPPORTED_SHAPE, BD_ERR_MISALIGNED,
+ *         BD_ERR_CUDA.
+ * ------------------------------------------------------------------------ */
+#define BD_SAMPLE_MAX_VOCAB 262144
+typedef enum bd_logits_type { BD_LOGITS_BF16 = 0, BD_LOGITS_F32 = 1 } bd_logits_type;
+
+int32_t bd_sample(const void *logits, int32_t logits_type, int64_t m, int64_t vocab, const float *temperature,
+                  const int32_t *top_k, const float *top_p, const float *min_p, const float *noise, int32_t *ids,
+                  float *logprob, void *stream);
+
+/* ------------------------------------------------------------------------ *
  * Status and debugging
  * ------------------------------------------------------------------------ */
 
@@ -395,7 +604,8 @@ const char *bd_status_string(int32_t status);
 
 /* Synchronises `stream`, then reads and clears the device status word of the
  * current device: BD_OK, BD_ERR_DEVICE_BOUNDS (bounds-checked build only),
- * BD_ERR_DEVICE_TIMEOUT or BD_ERR_BAD_VARIANT_ID (in that order of precedence).
+ * BD_ERR_DEVICE_TIMEOUT, BD_ERR_BAD_VARIANT_ID or BD_ERR_BAD_INDEX (in that
+ * order of precedence).
  * BD_ERR_CUDA if the sync itself fails. */
 int32_t bd_get_device_status(void *stream);
 
