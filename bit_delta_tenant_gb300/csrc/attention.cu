@@ -14,20 +14,24 @@
 // of its part in the workspace, and the last part to arrive joins all parts in
 // key order.  No CTA waits for another.
 //
-// A warp.  Each of the four warps owns 16 keys of a block and keeps its own
+// A warp.  Each of the four warps owns a tile of a block's keys and keeps its own
 // running state; 16 keys of one page and head are one contiguous piece of
 // memory, copied with cp.async into the warp's own ring (swizzled so that the
-// fragment loads meet no bank conflict).  Query heads are the rows of
-// m16n8k16: S = Q K^T, then O += P V with the score fragment reused as P's.
+// fragment loads meet no bank conflict), the page ids read a batch ahead.
+// S = Q K^T has the query heads as rows; O^T += V^T P^T has them as columns, so
+// S's accumulator is P^T's operand as it stands and 8 heads fill a column tile.
 // mma.sync, not tcgen05: 4 to 16 rows of a 128-row tile would be used, and the
-// kernel needs under a tenth of the legacy rate.
+// kernel needs about a quarter of the legacy rate.
 //
-// Rounding.  P enters as a 16-bit part and its remainder.  With at most 8 query
-// heads the remainder takes rows 8..15 of the same product, which would
-// otherwise be empty; with more it takes a second product.
-// e4m3 keys and values become fp16 (exact); q is scaled by a power of two into
-// fp16's range, K's scale multiplies the score, and V's scale is folded into
-// the weight before the maximum is taken, so that weights never exceed 1.
+// Rounding.  P enters as a 16-bit part and its 16-bit remainder: bf16 (2^-16 of a
+// weight) beside a bf16 V, fp16 (2^-21, or 2^-25 of the largest) beside an e4m3 V,
+// which fp16 holds exactly.  An e4m3 V's scale is folded into the
+// weight before the maximum is taken, so that no weight exceeds 1; its K is
+// multiplied as it stands, by q in two e4m3 parts: q is scaled by a power of two
+// so that its row's largest value lies in [128, 256), where the parts hold a bf16
+// value's 8 bits exactly (values far below the largest to 2^-21 of it); with at most 8
+// heads the second part takes rows 8..15 of the same product.  Accumulation is
+// fp32 in every product (measured for the e4m3 one: 2^-25 of sum |q k|).
 #include <cuda_fp8.h>
 
 #include <algorithm>
@@ -40,12 +44,12 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
-constexpr int kTile = 16;              // keys of a warp's step
-constexpr int kBlock = kWarps * kTile; // keys of a work item
-constexpr int kRows = 16;              // query heads of one tile
-constexpr int kCtasPerSm = 3;
-constexpr int64_t kMaxKeys = 0x7FFFF000;  // positions stay int32, a block beyond the last one included
+constexpr int kRows = 16;  // query heads of one tile
+constexpr int kMaxCtasPerSm = 3;
+constexpr int kDepth = 2;  // tiles in a warp's ring
+constexpr int64_t kMaxKeys = 1 << 30;  // the division by the page size is exact, positions stay int32
 constexpr int kSlotFloats = kRows * 128 + 2 * kRows;  // a part's output, maxima and sums
+constexpr uint32_t kNoPage = 0xFFFFFFFFu;
 
 struct AttnArgs {
     const uint8_t *q, *ck, *cv, *ck_scale, *cv_scale;
@@ -56,7 +60,8 @@ struct AttnArgs {
     unsigned *status;
     int64_t n_pages;
     int32_t n_seqs, max_pages, kv_heads, page_size, q_heads, group, subs, window;
-    float scale_log2;  // scale * log2(e): scores are kept in base 2
+    uint32_t page_tiles, page_magic;  // page_size / 16, and ceil(2^32 / that) for divisions by it
+    float scale_log2;                 // scale * log2(e): scores are kept in base 2
 };
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool full) {
@@ -92,25 +97,37 @@ __device__ __forceinline__ void mma16(float (&d)[4], uint32_t a0, uint32_t a1, u
     else
         mma_bf16_16816(d, a0, a1, a2, a3, b0, b1);
 }
-__device__ __forceinline__ uint32_t e4m3x2_to_half2(uint32_t two) {
-    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(two), __NV_E4M3);
-    return static_cast<uint32_t>(h.x) | static_cast<uint32_t>(h.y) << 16;
+__device__ __forceinline__ void mma_e4m3(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 "
+        "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// Four e4m3 bytes as two fp16 pairs.
+__device__ __forceinline__ void e4m3x4_to_half2x2(uint32_t four, uint32_t &lo, uint32_t &hi) {
+    asm("{\n\t.reg .b16 a, b;\n\t"
+        "mov.b32 {a, b}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, a;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(four));
 }
 __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
     const __half2 h = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<const uint32_t *>(&h);
 }
-// The 16-bit pair nearest to (x, y), and the pair nearest to what that leaves.
-template <bool kHalf>
-__device__ __forceinline__ void split_pair(float x, float y, uint32_t &hi, uint32_t &lo) {
-    if constexpr (kHalf) {
-        hi = pack_half2(x, y);
-        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&hi));
-        lo = pack_half2(x - f.x, y - f.y);
-    } else {
-        hi = pack_bf16x2(x, y);
-        lo = pack_bf16x2(x - bf16lo_to_f32(hi), y - bf16hi_to_f32(hi));
-    }
+__device__ __forceinline__ float ex2(float x) {  // 2^x, 0 for -inf
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
+    return __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
+}
+__device__ __forceinline__ float2 from_e4m3x2(uint32_t two) {
+    return __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(two), __NV_E4M3)));
 }
 
 // Byte offset of 16-byte chunk c of row r in a tile of kRow-byte rows: eight rows of one
@@ -125,6 +142,7 @@ __device__ __forceinline__ uint32_t tile_at(int r, int c) {
 struct Span {
     int32_t start, len, first, blocks;
 };
+template <int kBlock>
 __device__ __forceinline__ Span span_of(const AttnArgs &a, int64_t b) {
     const int64_t most = min(static_cast<int64_t>(a.max_pages) * a.page_size, kMaxKeys);
     int64_t len = a.lengths[b];
@@ -149,34 +167,37 @@ __device__ __forceinline__ int64_t warp_scan(int64_t v) {  // inclusive
     return v;
 }
 
-template <int kDim, bool kE4m3>
-constexpr int tile_bytes() {
-    return kTile * kDim * (kE4m3 ? 1 : 2);
-}
-template <int kDim, bool kE4m3>
-constexpr int stage_bytes() {  // K tile, V tile, and their 16 scale bytes each
-    return 2 * tile_bytes<kDim, kE4m3>() + (kE4m3 ? 32 : 0);
-}
 template <bool kE4m3>
-constexpr int ring_depth() {
-    return kE4m3 ? 4 : 2;
+constexpr int kTileOf = kE4m3 ? 32 : 16;  // keys of a warp's step: 8 KB of K and V at head_dim 128 in either type
+template <bool kE4m3>
+constexpr int kBlockOf = kWarps *kTileOf<kE4m3>;  // keys of a work item
+template <int kDim, bool kE4m3>
+constexpr int stage_bytes() {  // K tile, V tile, and their scale bytes
+    return 2 * kTileOf<kE4m3> * kDim * (kE4m3 ? 1 : 2) + (kE4m3 ? 2 * kTileOf<kE4m3> : 0);
 }
 template <int kDim, bool kE4m3>
 constexpr int smem_bytes() {
-    return kWarps * ring_depth<kE4m3>() * stage_bytes<kDim, kE4m3>();
+    return kWarps * kDepth * stage_bytes<kDim, kE4m3>();
 }
 
-// kPack: at most 8 query heads, the remainders of P in rows 8..15.
+// CTAs per SM: the second column tile of more than 8 heads takes the registers of the third CTA.
+template <bool kPack>
+constexpr int kCtasOf = kPack ? 3 : 2;
+
+// kPack: at most 8 query heads.
 template <int kDim, bool kE4m3, bool kPack>
-__global__ void __launch_bounds__(kThreads, kCtasPerSm) attention_kernel(const AttnArgs a) {
+__global__ void __launch_bounds__(kThreads, kCtasOf<kPack>) attention_kernel(const AttnArgs a) {
+    constexpr int kTile = kTileOf<kE4m3>, kBlock = kBlockOf<kE4m3>;
+    constexpr int kSub = kTile / 16;              // 16-key pieces of a tile, each within one page
     constexpr int kRow = kDim * (kE4m3 ? 1 : 2);  // bytes of one key
     constexpr int kChunks = kRow / 16;
-    constexpr int kTileBytes = tile_bytes<kDim, kE4m3>();
+    constexpr int kPiece = 16 * kRow;             // bytes of 16 keys
+    constexpr int kTileBytes = kSub * kPiece;
     constexpr int kStage = stage_bytes<kDim, kE4m3>();
-    constexpr int kDepth = ring_depth<kE4m3>();
-    constexpr int kUsed = kPack ? 8 : 16;  // rows that carry heads
-    constexpr int kSteps = kDim / 16;      // k steps of Q K^T
-    constexpr int kCols = kDim / 8;        // n tiles of P V
+    constexpr int kHalves = kPack ? 1 : 2;   // column tiles of 8 heads
+    constexpr int kSteps = kRow / 32;        // k steps of Q K^T: 32 bytes of a key each
+    constexpr int kRowTiles = kDim / 16;     // row tiles of V^T P^T
+    constexpr int kBatch = 32 / kSub;        // tiles whose page ids a warp holds at a time
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ int64_t s_sum[kWarps];
     __shared__ int64_t s_found[2];
@@ -188,7 +209,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attention_kernel(const A
 
     // sequences with nothing to see: zeros
     for (int64_t b = blockIdx.x; b < a.n_seqs; b += gridDim.x) {
-        if (span_of(a, b).blocks > 0) continue;
+        if (span_of<kBlock>(a, b).blocks > 0) continue;
         uint4 *o = reinterpret_cast<uint4 *>(a.out + b * a.q_heads * (kDim * 2));
         for (int i = tid; i < a.q_heads * (kDim / 8); i += kThreads) o[i] = make_uint4(0, 0, 0, 0);
         if (a.lse)
@@ -197,7 +218,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attention_kernel(const A
 
     // all items, and this CTA's range of them
     int64_t mine = 0;
-    for (int64_t b = tid; b < a.n_seqs; b += kThreads) mine += span_of(a, b).blocks;
+    for (int64_t b = tid; b < a.n_seqs; b += kThreads) mine += span_of<kBlock>(a, b).blocks;
     mine = warp_scan(mine);
     if (lane == 31) s_sum[warp] = mine;
     __syncthreads();
@@ -211,7 +232,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attention_kernel(const A
         int64_t before = 0;
         for (int64_t b0 = 0; b0 < a.n_seqs; b0 += kThreads) {
             __syncthreads();
-            const int64_t n = b0 + tid < a.n_seqs ? span_of(a, b0 + tid).blocks : 0;
+            const int64_t n = b0 + tid < a.n_seqs ? span_of<kBlock>(a, b0 + tid).blocks : 0;
             const int64_t in = warp_scan(n);
             if (lane == 31) s_sum[warp] = in;
             __syncthreads();
@@ -223,235 +244,321 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attention_kernel(const A
         __syncthreads();
     }
     int64_t b = s_found[0], blocks_before = s_found[1];
-    Span sp = span_of(a, b);
+    Span sp = span_of<kBlock>(a, b);
     int vh = static_cast<int>((begin - blocks_before * vheads) / sp.blocks);
     int blk = static_cast<int>((begin - blocks_before * vheads) % sp.blocks);
     const uint32_t ring = smem_u32(smem) + warp * (kDepth * kStage);
+    const uint8_t *ring_ptr = smem + warp * (kDepth * kStage);
 
     for (int64_t it = begin; it < end;) {
         const int n = static_cast<int>(min(end - it, static_cast<int64_t>(sp.blocks - blk)));
         const int kvh = vh / a.subs, row0 = vh % a.subs * kRows;
         const int rows = min(kRows, a.group - row0);
         const int64_t head0 = b * a.q_heads + kvh * a.group + row0;
+        const int key_first = (sp.first + blk) * kBlock + warp * kTile;  // this warp's tile of block j: + j * kBlock
 
-        // Q fragments.  bf16: natural column order.  e4m3: the order in which a lane meets
-        // four neighbouring bytes of K (slots 2t, 2t+1 and 2t+8, 2t+9 hold columns 4t .. 4t+3).
-        uint32_t qa[kSteps][kPack ? 2 : 4];
+        // 16-key piece `lane` of the batch of tiles from j0: its page id
+        const int32_t *table = a.page_table + b * a.max_pages;
+        auto piece_of = [&](int j0) { return static_cast<uint32_t>(key_first + (j0 + lane / kSub) * kBlock) / 16 + lane % kSub; };
+        auto page_index = [&](uint32_t piece) { return a.page_tiles == 1 ? piece : __umulhi(piece, a.page_magic); };
+        auto fetch_page = [&](int j0) {
+            const uint32_t p = piece_of(j0);
+            const bool on = j0 + lane / kSub < n && static_cast<int>(p * 16) < sp.len && static_cast<int>(p * 16 + 16) > sp.start;
+            return on ? table[page_index(p)] : 0;
+        };
+        // its place in the pool, in units of 16 keys
+        auto place_of = [&](int j0, int32_t page) {
+            if (page < 0 || page >= a.n_pages) {
+                flag_status(a.status, kDevBadIndex);
+                return kNoPage;
+            }
+            const uint32_t p = piece_of(j0);
+            return (static_cast<uint32_t>(page) * a.kv_heads + kvh) * a.page_tiles + (p - page_index(p) * a.page_tiles);
+        };
+        int32_t next_pages = fetch_page(0);
+
+        // Q fragments: rows are heads, and with kPack rows 8..15 the second part of e4m3 queries
+        constexpr int kParts = kE4m3 && !kPack ? 2 : 1;
+        uint32_t qa[kParts][kSteps][kPack && !kE4m3 ? 2 : 4];
         float rscale[2] = {a.scale_log2, a.scale_log2};
 #pragma unroll
-        for (int half = 0; half < (kPack ? 1 : 2); ++half) {
+        for (int half = 0; half < kHalves; ++half) {
             const bool on = g + half * 8 < rows;
             const uint8_t *src = a.q + (head0 + g + half * 8) * (kDim * 2);
-            uint32_t v[kSteps][2];
+            if constexpr (!kE4m3) {
 #pragma unroll
-            for (int k = 0; k < kSteps; ++k) {
-                if constexpr (kE4m3) {
-                    const uint2 u = on ? *reinterpret_cast<const uint2 *>(src + k * 32 + t4 * 8) : make_uint2(0, 0);
-                    v[k][0] = u.x, v[k][1] = u.y;
-                } else {
-                    v[k][0] = on ? *reinterpret_cast<const uint32_t *>(src + k * 32 + t4 * 4) : 0;
-                    v[k][1] = on ? *reinterpret_cast<const uint32_t *>(src + k * 32 + 16 + t4 * 4) : 0;
-                }
-            }
-            if constexpr (kE4m3) {
+                for (int k = 0; k < kSteps; ++k)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const uint32_t v = on ? *reinterpret_cast<const uint32_t *>(src + k * 32 + i * 16 + t4 * 4) : 0;
+                        qa[0][k][kPack ? i : 2 * i + half] = v;
+                    }
+            } else {
+                uint2 v[kSteps][2];
                 float top = 0.f;
 #pragma unroll
                 for (int k = 0; k < kSteps; ++k)
 #pragma unroll
-                    for (int i = 0; i < 2; ++i)
-                        top = fmaxf(top, fmaxf(fabsf(bf16lo_to_f32(v[k][i])), fabsf(bf16hi_to_f32(v[k][i]))));
+                    for (int i = 0; i < 2; ++i) {  // columns 32 k + 16 i + 4 t .. + 3
+                        v[k][i] = on ? *reinterpret_cast<const uint2 *>(src + k * 64 + i * 32 + t4 * 8) : make_uint2(0, 0);
+                        top = fmaxf(top, fmaxf(fmaxf(fabsf(bf16lo_to_f32(v[k][i].x)), fabsf(bf16hi_to_f32(v[k][i].x))),
+                                               fmaxf(fabsf(bf16lo_to_f32(v[k][i].y)), fabsf(bf16hi_to_f32(v[k][i].y)))));
+                    }
                 top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
                 top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
-                // q * 2^-e lies below 2 in magnitude; rows of zeros or infinities keep e = 0
+                // 2^e <= top < 2^(e + 1); rows of zeros, next to zero or infinite take e = 0
                 int e = static_cast<int>(__float_as_uint(top) >> 23);
                 e = e < 27 || e > 227 ? 127 : e;
-                const float down = __uint_as_float(static_cast<uint32_t>(254 - e) << 23);
-                rscale[half] = a.scale_log2 * __uint_as_float(static_cast<uint32_t>(e) << 23);
+                const float up = __uint_as_float(static_cast<uint32_t>(254 + 7 - e) << 23);  // 2^(7 - e)
+                rscale[half] = a.scale_log2 * __uint_as_float(static_cast<uint32_t>(e - 7) << 23);
+                // neither infinity nor NaN has an e4m3 form that keeps it through a product: such a head is NaN throughout
+                if (!(top < INFINITY)) rscale[half] = NAN;
+                bool nan = false;
 #pragma unroll
                 for (int k = 0; k < kSteps; ++k)
 #pragma unroll
-                    for (int i = 0; i < 2; ++i)
-                        v[k][i] = pack_half2(bf16lo_to_f32(v[k][i]) * down, bf16hi_to_f32(v[k][i]) * down);
-            }
-#pragma unroll
-            for (int k = 0; k < kSteps; ++k) {
-                if constexpr (kPack) {
-                    qa[k][0] = v[k][0], qa[k][1] = v[k][1];
-                } else {
-                    qa[k][half] = v[k][0], qa[k][2 + half] = v[k][1];
-                }
+                    for (int i = 0; i < 2; ++i) {
+                        const float x[4] = {bf16lo_to_f32(v[k][i].x) * up, bf16hi_to_f32(v[k][i].x) * up,
+                                            bf16lo_to_f32(v[k][i].y) * up, bf16hi_to_f32(v[k][i].y) * up};
+                        nan |= x[0] != x[0] || x[1] != x[1] || x[2] != x[2] || x[3] != x[3];
+                        const uint32_t h0 = e4m3x2(x[0], x[1]), h1 = e4m3x2(x[2], x[3]);
+                        const float2 f0 = from_e4m3x2(h0), f1 = from_e4m3x2(h1);
+                        const uint32_t l0 = e4m3x2((x[0] - f0.x) * 16.f, (x[1] - f0.y) * 16.f);
+                        const uint32_t l1 = e4m3x2((x[2] - f1.x) * 16.f, (x[3] - f1.y) * 16.f);
+                        if constexpr (kPack) {
+                            qa[0][k][2 * i] = h0 | h1 << 16, qa[0][k][2 * i + 1] = l0 | l1 << 16;
+                        } else {
+                            qa[0][k][2 * i + half] = h0 | h1 << 16, qa[1][k][2 * i + half] = l0 | l1 << 16;
+                        }
+                    }
+                const unsigned who = __ballot_sync(0xFFFFFFFFu, nan);
+                if (who >> (lane & ~3) & 0xFu) rscale[half] = NAN;
             }
         }
 
-        float o[kCols][4] = {};
-        float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-
-        // this warp's 16 keys of block j of the segment
-        auto key_of = [&](int j) { return (sp.first + blk + j) * kBlock + warp * kTile; };
-        auto load = [&](int j) {
-            const int key0 = key_of(j);
-            if (j < n && key0 < sp.len && key0 + kTile > sp.start) {
-                const uint32_t dst = ring + j % kDepth * kStage;
-                int64_t page = a.page_table[b * a.max_pages + key0 / a.page_size];
-                const bool good = page >= 0 && page < a.n_pages;
-                if (!good) {
-                    if (lane == 0) flag_status(a.status, kDevBadIndex);
-                    page = 0;
-                }
-                const int64_t at = (page * a.kv_heads + kvh) * a.page_size + key0 % a.page_size;
+        float o[kRowTiles][kHalves][4] = {};
+        float m[kHalves], l[kHalves];
 #pragma unroll
-                for (int i = lane; i < kTile * kChunks; i += 32) {
-                    const int r = i / kChunks, c = i % kChunks;
-                    const bool seen = good && key0 + r < sp.len && key0 + r >= sp.start;
-                    const uint32_t d = dst + tile_at<kRow>(r, c);
-                    cp_async16(d, a.ck + at * kRow + i * 16, seen);
-                    cp_async16(d + kTileBytes, a.cv + at * kRow + i * 16, seen);
+        for (int h = 0; h < kHalves; ++h) m[h] = -INFINITY, l[h] = 0.f;
+
+        uint32_t places = place_of(0, next_pages);
+        next_pages = fetch_page(kBatch);
+        uint32_t bad = 0;  // pieces in the ring whose page id is out of range
+        auto load = [&](int j) {
+            if (j >= n) return;
+            if (j > 0 && j % kBatch == 0) {
+                places = place_of(j, next_pages);
+                next_pages = fetch_page(j + kBatch);
+            }
+            const int key0 = key_first + j * kBlock, slot = j % kDepth;
+            if (key0 >= sp.len || key0 + kTile <= sp.start) return;
+            const uint32_t dst = ring + slot * kStage;
+            const bool inside = key0 >= sp.start && key0 + kTile <= sp.len;
+#pragma unroll
+            for (int u = 0; u < kSub; ++u) {
+                uint32_t place = __shfl_sync(0xFFFFFFFFu, places, j % kBatch * kSub + u);
+                const bool good = place != kNoPage;
+                bad = (bad & ~(1u << (slot * kSub + u))) | (good ? 0u : 1u << (slot * kSub + u));
+                place = good ? place : 0;
+                const uint8_t *ks = a.ck + static_cast<int64_t>(place) * kPiece + lane * 16;
+                const uint8_t *vs = a.cv + static_cast<int64_t>(place) * kPiece + lane * 16;
+#pragma unroll
+                for (int i = 0; i < 16 * kChunks / 32; ++i) {
+                    const int r = (lane + 32 * i) / kChunks, c = lane % kChunks;
+                    const int key = key0 + u * 16 + r;
+                    const bool seen = good && (inside || (key < sp.len && key >= sp.start));
+                    const uint32_t d = dst + tile_at<kRow>(u * 16 + r, c);
+                    cp_async16(d, ks + i * 512, seen);
+                    cp_async16(d + kTileBytes, vs + i * 512, seen);
                 }
                 if constexpr (kE4m3)
-                    if (lane < 2) cp_async16(dst + 2 * kTileBytes + lane * 16, (lane ? a.cv_scale : a.ck_scale) + at, good);
-                if (!good) return false;
+                    if (lane < 2)
+                        cp_async16(dst + 2 * kTileBytes + lane * kTile + u * 16,
+                                   (lane ? a.cv_scale : a.ck_scale) + static_cast<int64_t>(place) * 16, good);
             }
-            return true;
         };
-        uint32_t bad = 0;  // ring slots whose page id was out of range
+#pragma unroll
         for (int j = 0; j < kDepth - 1; ++j) {
-            if (!load(j)) bad |= 1u << j;
+            load(j);
             cp_commit();
         }
         for (int j = 0; j < n; ++j) {
-            const int ahead = j + kDepth - 1;
-            if (!load(ahead)) bad |= 1u << (ahead % kDepth);
-            else bad &= ~(1u << (ahead % kDepth));
+            load(j + kDepth - 1);
             cp_commit();
             cp_wait<kDepth - 1>();
             __syncwarp();
-            const int key0 = key_of(j);
-            if (key0 < sp.len && key0 + kTile > sp.start && !(bad >> (j % kDepth) & 1)) {
-                const uint32_t kt = ring + j % kDepth * kStage, vt = kt + kTileBytes;
-                float s[2][4] = {};
+            const int key0 = key_first + j * kBlock, slot = j % kDepth;
+            if (key0 < sp.len && key0 + kTile > sp.start) {
+                const uint32_t kt = ring + slot * kStage, vt = kt + kTileBytes;
+                const uint8_t *vp = ring_ptr + slot * kStage + kTileBytes, *scales = vp + kTileBytes;
+                // K: matrices of 8 keys x 16 bytes, two chunks for keys 0..7, then for keys 8..15 of a piece
+                float s[2 * kSub][4] = {};
 #pragma unroll
-                for (int k = 0; k < kSteps; k += kE4m3 ? 2 : 1) {
-                    uint32_t r[4];
-                    if constexpr (kE4m3) {
-                        // matrices: keys 0..7 and 8..15 of chunk k, then of chunk k + 1
-                        ldsm4(r, kt + tile_at<kRow>(lane % 16, k + lane / 16));
+                for (int k = 0; k < kSteps; ++k)
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const uint32_t b0 = e4m3x2_to_half2(r[i] & 0xFFFFu), b1 = e4m3x2_to_half2(r[i] >> 16);
-                            const int kk = k + i / 2;
-                            if constexpr (kPack) mma16<true>(s[i % 2], qa[kk][0], 0, qa[kk][1], 0, b0, b1);
-                            else mma16<true>(s[i % 2], qa[kk][0], qa[kk][1], qa[kk][2], qa[kk][3], b0, b1);
-                        }
-                    } else {
-                        // matrices: columns 0..7 and 8..15 of the step for keys 0..7, then keys 8..15
-                        ldsm4(r, kt + tile_at<kRow>(lane % 8 + lane / 16 * 8, 2 * k + lane / 8 % 2));
+                    for (int u = 0; u < kSub; ++u) {
+                        uint32_t r[4];
+                        ldsm4(r, kt + tile_at<kRow>(u * 16 + lane % 8 + lane / 16 * 8, 2 * k + lane / 8 % 2));
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
-                            if constexpr (kPack) mma16<false>(s[i], qa[k][0], 0, qa[k][1], 0, r[2 * i], r[2 * i + 1]);
+                            float(&d)[4] = s[2 * u + i];
+                            if constexpr (kE4m3)
+                                mma_e4m3(d, qa[0][k][0], qa[0][k][1], qa[0][k][2], qa[0][k][3], r[2 * i], r[2 * i + 1]);
+                            else if constexpr (kPack)
+                                mma16<false>(d, qa[0][k][0], 0, qa[0][k][1], 0, r[2 * i], r[2 * i + 1]);
                             else
-                                mma16<false>(s[i], qa[k][0], qa[k][1], qa[k][2], qa[k][3], r[2 * i], r[2 * i + 1]);
+                                mma16<false>(d, qa[0][k][0], qa[0][k][1], qa[0][k][2], qa[0][k][3], r[2 * i], r[2 * i + 1]);
                         }
                     }
+                if constexpr (kE4m3 && !kPack) {  // the second parts of q, 1/16 of the weight
+                    float s2[2 * kSub][4] = {};
+#pragma unroll
+                    for (int k = 0; k < kSteps; ++k)
+#pragma unroll
+                        for (int u = 0; u < kSub; ++u) {
+                            uint32_t r[4];
+                            ldsm4(r, kt + tile_at<kRow>(u * 16 + lane % 8 + lane / 16 * 8, 2 * k + lane / 8 % 2));
+#pragma unroll
+                            for (int i = 0; i < 2; ++i)
+                                mma_e4m3(s2[2 * u + i], qa[1][k][0], qa[1][k][1], qa[1][k][2], qa[1][k][3], r[2 * i],
+                                         r[2 * i + 1]);
+                        }
+#pragma unroll
+                    for (int i = 0; i < 2 * kSub; ++i)
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) s[i][c] = fmaf(s2[i][c], 0.0625f, s[i][c]);
                 }
-                // scores in base 2, V's scale exponent beside them, unseen keys -inf
-                float lv[2][2] = {};
+                // scores in base 2; V's scale, as a factor and as its exponent
+                float vscale[2 * kSub][2], vexp[2 * kSub][2];
 #pragma unroll
-                for (int i = 0; i < 2; ++i)
-#pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        const int key = i * 8 + t4 * 2 + c;
-                        float ks = 1.f;
-                        if constexpr (kE4m3) {
-                            const uint8_t *sc = smem + (vt - smem_u32(smem)) + kTileBytes;
-                            ks = __uint_as_float(static_cast<uint32_t>(sc[key]) << 23);
-                            lv[i][c] = static_cast<float>(static_cast<int>(sc[16 + key]) - 127);
-                        }
-                        const bool seen = key0 + key < sp.len && key0 + key >= sp.start;
-                        s[i][c] = seen ? s[i][c] * ks * rscale[0] : -INFINITY;
-                        if (!kPack) s[i][2 + c] = seen ? s[i][2 + c] * ks * rscale[1] : -INFINITY;
-                    }
-                float fix[2] = {1.f, 1.f};
-#pragma unroll
-                for (int h = 0; h < (kPack ? 1 : 2); ++h) {
-                    float top = fmaxf(fmaxf(s[0][2 * h] + lv[0][0], s[0][2 * h + 1] + lv[0][1]),
-                                      fmaxf(s[1][2 * h] + lv[1][0], s[1][2 * h + 1] + lv[1][1]));
-                    top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
-                    top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
-                    top = fmaxf(top, m[h]);
-                    const float base = top == -INFINITY ? 0.f : top;  // nothing yet: all weights 0
-                    fix[h] = exp2f(m[h] - base);
-                    m[h] = top;
-                    l[h] *= fix[h];
-#pragma unroll
-                    for (int i = 0; i < 2; ++i)
+                for (int i = 0; i < 2 * kSub; ++i) {
+                    float ks[2] = {1.f, 1.f};
+                    if constexpr (kE4m3) {
+                        const uint32_t kb = *reinterpret_cast<const uint16_t *>(scales + i * 8 + t4 * 2);
+                        const uint32_t vb = *reinterpret_cast<const uint16_t *>(scales + kTile + i * 8 + t4 * 2);
 #pragma unroll
                         for (int c = 0; c < 2; ++c) {
-                            float &x = s[i][2 * h + c];
-                            const float e = exp2f(x - base);
-                            l[h] += e;
-                            x = kE4m3 ? exp2f(x + lv[i][c] - base) : e;
-                        }
-                }
-                if constexpr (kPack) fix[1] = fix[0];
-                if (__any_sync(0xFFFFFFFFu, fix[0] != 1.f || fix[1] != 1.f)) {
-#pragma unroll
-                    for (int c = 0; c < kCols; ++c) {
-                        o[c][0] *= fix[0], o[c][1] *= fix[0];
-                        o[c][2] *= fix[1], o[c][3] *= fix[1];
-                    }
-                }
-                uint32_t p[4], p2[4];  // P and, for kPack false, its remainder
-                if constexpr (kPack) {
-                    split_pair<kE4m3>(s[0][0], s[0][1], p[0], p[1]);
-                    split_pair<kE4m3>(s[1][0], s[1][1], p[2], p[3]);
-                } else {
-                    split_pair<kE4m3>(s[0][0], s[0][1], p[0], p2[0]);
-                    split_pair<kE4m3>(s[0][2], s[0][3], p[1], p2[1]);
-                    split_pair<kE4m3>(s[1][0], s[1][1], p[2], p2[2]);
-                    split_pair<kE4m3>(s[1][2], s[1][3], p[3], p2[3]);
-                }
-                if constexpr (kE4m3) {
-                    // rows 2t, 2t+1, 2t+8, 2t+9; the lane's piece of a row holds columns g * kCols ..,
-                    // so n tile c takes columns g * kCols + c
-                    constexpr int kWords = kCols / 4;
-                    uint32_t w[4][kWords];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int r = t4 * 2 + i % 2 + i / 2 * 8;
-                        const uint8_t *src = smem + (vt - smem_u32(smem));
-                        if constexpr (kWords == 4) {
-                            const uint4 u = *reinterpret_cast<const uint4 *>(src + tile_at<kRow>(r, g));
-                            w[i][0] = u.x, w[i][1] = u.y, w[i][2] = u.z, w[i][3] = u.w;
-                        } else {
-                            const uint2 u = *reinterpret_cast<const uint2 *>(src + tile_at<kRow>(r, g / 2) + g % 2 * 8);
-                            w[i][0] = u.x, w[i][1] = u.y;
+                            ks[c] = __uint_as_float((kb >> 8 * c & 0xFFu) << 23);
+                            vscale[i][c] = __uint_as_float((vb >> 8 * c & 0xFFu) << 23);
+                            vexp[i][c] = __uint_as_float(0x4B000000u | (vb >> 8 * c & 0xFFu)) - (8388608.f + 127.f);
                         }
                     }
 #pragma unroll
-                    for (int i = 0; i < kWords; ++i)
+                    for (int c = 0; c < 2; ++c) {
+                        if constexpr (kE4m3 && kPack) s[i][c] = fmaf(s[i][2 + c], 0.0625f, s[i][c]);
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            // bytes 2h, 2h+1 of two rows, side by side
-                            const uint32_t x = __byte_perm(w[0][i], w[1][i], h ? 0x7362 : 0x5140);
-                            const uint32_t y = __byte_perm(w[2][i], w[3][i], h ? 0x7362 : 0x5140);
+                        for (int h = 0; h < kHalves; ++h)
+                            s[i][2 * h + c] *= kE4m3 ? ks[c] * rscale[h] : rscale[h];
+                    }
+                }
+                const uint32_t bad_here = bad >> slot * kSub & ((1u << kSub) - 1);
+                if (key0 < sp.start || key0 + kTile > sp.len || bad_here) {
 #pragma unroll
-                            for (int e = 0; e < 2; ++e) {
-                                const uint32_t b0 = e4m3x2_to_half2(e ? x >> 16 : x & 0xFFFFu);
-                                const uint32_t b1 = e4m3x2_to_half2(e ? y >> 16 : y & 0xFFFFu);
-                                float(&d)[4] = o[4 * i + 2 * h + e];
-                                mma16<true>(d, p[0], p[1], p[2], p[3], b0, b1);
-                                if constexpr (!kPack) mma16<true>(d, p2[0], p2[1], p2[2], p2[3], b0, b1);
-                            }
+                    for (int i = 0; i < 2 * kSub; ++i)
+#pragma unroll
+                        for (int c = 0; c < 2; ++c) {
+                            const int key = key0 + i * 8 + t4 * 2 + c;
+                            const bool seen = key < sp.len && key >= sp.start && !(bad_here >> i / 2 & 1);
+#pragma unroll
+                            for (int h = 0; h < kHalves; ++h) s[i][2 * h + c] = seen ? s[i][2 * h + c] : -INFINITY;
+                            if (kE4m3 && !seen) vscale[i][c] = vexp[i][c] = 0.f;  // the byte may be anything
                         }
-                } else {
+                }
+                float fix[kHalves];
+                bool moved = false;
 #pragma unroll
-                    for (int c = 0; c < kCols; c += 2) {
-                        uint32_t r[4];
-                        ldsm4_trans(r, vt + tile_at<kRow>(lane % 16, c + lane / 16));
+                for (int h = 0; h < kHalves; ++h) {
+                    float top = m[h];
+#pragma unroll
+                    for (int i = 0; i < 2 * kSub; ++i)
+#pragma unroll
+                        for (int c = 0; c < 2; ++c)
+                            top = fmaxf(top, kE4m3 ? s[i][2 * h + c] + vexp[i][c] : s[i][2 * h + c]);
+                    top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+                    top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+                    const float base = top == -INFINITY ? 0.f : top;  // nothing yet: all weights 0
+                    fix[h] = ex2(m[h] - base);
+                    moved |= fix[h] != 1.f;
+                    m[h] = top;
+                    float sum = 0.f;
+#pragma unroll
+                    for (int i = 0; i < 2 * kSub; ++i)
+#pragma unroll
+                        for (int c = 0; c < 2; ++c) {
+                            const float e = ex2(s[i][2 * h + c] - base);
+                            sum += e;
+                            s[i][2 * h + c] = kE4m3 ? e * vscale[i][c] : e;
+                        }
+                    l[h] = fmaf(l[h], fix[h], sum);
+                }
+                if (__any_sync(0xFFFFFFFFu, moved)) {
+#pragma unroll
+                    for (int h = 0; h < kHalves; ++h) {  // columns 2t, 2t+1 of O^T: the factors sit in those heads' lanes
+                        const float f0 = __shfl_sync(0xFFFFFFFFu, fix[h], t4 * 8);
+                        const float f1 = __shfl_sync(0xFFFFFFFFu, fix[h], t4 * 8 + 4);
+#pragma unroll
+                        for (int c = 0; c < kRowTiles; ++c) {
+                            o[c][h][0] *= f0, o[c][h][1] *= f1;
+                            o[c][h][2] *= f0, o[c][h][3] *= f1;
+                        }
+                    }
+                }
+#pragma unroll
+                for (int u = 0; u < kSub; ++u) {
+                    uint32_t p[kHalves][2], p2[kHalves][2];  // P^T and its remainder
+#pragma unroll
+                    for (int h = 0; h < kHalves; ++h)
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
-                            mma16<false>(o[c + i], p[0], p[1], p[2], p[3], r[2 * i], r[2 * i + 1]);
-                            if constexpr (!kPack) mma16<false>(o[c + i], p2[0], p2[1], p2[2], p2[3], r[2 * i], r[2 * i + 1]);
+                            const float x = s[2 * u + i][2 * h], y = s[2 * u + i][2 * h + 1];
+                            if constexpr (kE4m3) {
+                                p[h][i] = pack_half2(x, y);
+                                const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&p[h][i]));
+                                p2[h][i] = pack_half2(x - f.x, y - f.y);
+                            } else {
+                                p[h][i] = pack_bf16x2(x, y);
+                                p2[h][i] = pack_bf16x2(x - bf16lo_to_f32(p[h][i]), y - bf16hi_to_f32(p[h][i]));
+                            }
+                        }
+                    if constexpr (kE4m3) {
+                        // rows 2t, 2t+1, 2t+8, 2t+9; the lane's piece of a row holds columns g * kDim / 8 ..,
+                        // rows g and g + 8 of row tile c are its columns 2c and 2c + 1
+                        constexpr int kWords = kDim / 32;
+                        uint32_t w[4][kWords];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int r = u * 16 + t4 * 2 + i % 2 + i / 2 * 8;
+                            if constexpr (kWords == 4) {
+                                const uint4 x = *reinterpret_cast<const uint4 *>(vp + tile_at<kRow>(r, g));
+                                w[i][0] = x.x, w[i][1] = x.y, w[i][2] = x.z, w[i][3] = x.w;
+                            } else {
+                                const uint2 x = *reinterpret_cast<const uint2 *>(vp + tile_at<kRow>(r, g / 2) + g % 2 * 8);
+                                w[i][0] = x.x, w[i][1] = x.y;
+                            }
+                        }
+#pragma unroll
+                        for (int i = 0; i < kWords; ++i)
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                uint32_t v[4];  // two columns' bytes of two keys, side by side
+                                e4m3x4_to_half2x2(__byte_perm(w[0][i], w[1][i], e ? 0x7362 : 0x5140), v[0], v[1]);
+                                e4m3x4_to_half2x2(__byte_perm(w[2][i], w[3][i], e ? 0x7362 : 0x5140), v[2], v[3]);
+#pragma unroll
+                                for (int h = 0; h < kHalves; ++h) {
+                                    mma16<true>(o[2 * i + e][h], v[0], v[1], v[2], v[3], p[h][0], p[h][1]);
+                                    mma16<true>(o[2 * i + e][h], v[0], v[1], v[2], v[3], p2[h][0], p2[h][1]);
+                                }
+                            }
+                    } else {
+#pragma unroll
+                        for (int c = 0; c < kRowTiles; ++c) {
+                            uint32_t v[4];
+                            ldsm4_trans(v, vt + tile_at<kRow>(u * 16 + lane % 8 + lane / 16 * 8, 2 * c + lane / 8 % 2));
+#pragma unroll
+                            for (int h = 0; h < kHalves; ++h) {
+                                mma16<false>(o[c][h], v[0], v[1], v[2], v[3], p[h][0], p[h][1]);
+                                mma16<false>(o[c][h], v[0], v[1], v[2], v[3], p2[h][0], p2[h][1]);
+                            }
                         }
                     }
                 }
@@ -462,18 +569,19 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attention_kernel(const A
         __syncthreads();
 
         // the four warps' states, joined in shared memory
+        constexpr int kUsed = 8 * kHalves;
         float *merge = reinterpret_cast<float *>(smem);  // [warp][row][kDim]
 #pragma unroll
-        for (int h = 0; h < (kPack ? 1 : 2); ++h) {
+        for (int h = 0; h < kHalves; ++h) {
             l[h] += __shfl_xor_sync(0xFFFFFFFFu, l[h], 1);
             l[h] += __shfl_xor_sync(0xFFFFFFFFu, l[h], 2);
             if (t4 == 0) s_m[warp][g + 8 * h] = m[h], s_l[warp][g + 8 * h] = l[h];
 #pragma unroll
-            for (int c = 0; c < kCols; ++c)
+            for (int c = 0; c < kRowTiles; ++c)
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int d = kE4m3 ? (2 * t4 + e) * kCols + c : c * 8 + 2 * t4 + e;
-                    merge[(warp * kUsed + g + 8 * h) * kDim + d] = kPack ? o[c][e] + o[c][2 + e] : o[c][2 * h + e];
+                for (int e = 0; e < 4; ++e) {
+                    const int d = kE4m3 ? g * (kDim / 8) + 2 * c + e / 2 : c * 16 + g + e / 2 * 8;
+                    merge[(warp * kUsed + 8 * h + 2 * t4 + e % 2) * kDim + d] = o[c][h][e];
                 }
         }
         __syncthreads();
@@ -489,7 +597,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attention_kernel(const A
             float sum = 0.f, acc = 0.f;
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) {
-                const float f = exp2f(s_m[w][r] - base);
+                const float f = ex2(s_m[w][r] - base);
                 sum += s_l[w][r] * f;
                 acc += merge[(w * kUsed + r) * kDim + d] * f;
             }
@@ -530,7 +638,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attention_kernel(const A
                     float sum = 0.f;
                     for (int c = lane; c < parts; c += 32) {
                         const float *sl = slot_of(c0 + c) + kRows * 128;
-                        const float w = exp2f(__ldcg(sl + r) - base);
+                        const float w = ex2(__ldcg(sl + r) - base);
                         f[c * kRows + r] = w;
                         sum += __ldcg(sl + kRows + r) * w;
                     }
@@ -565,7 +673,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attention_kernel(const A
         if (++vh == vheads && it < end) {
             vh = 0;
             blocks_before += sp.blocks;
-            do sp = span_of(a, ++b);
+            do sp = span_of<kBlock>(a, ++b);
             while (sp.blocks == 0);
         }
     }
@@ -574,12 +682,12 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attention_kernel(const A
 template <int kDim, bool kE4m3, bool kPack>
 cudaError_t launch_typed(const AttnArgs &a, int num_sms, cudaStream_t stream) {
     // the join keeps one factor per part and row in the same memory
-    const int smem_size = std::max<int>(smem_bytes<kDim, kE4m3>(), num_sms * kCtasPerSm * kRows * sizeof(float));
+    const int smem_size = std::max<int>(smem_bytes<kDim, kE4m3>(), num_sms * kCtasOf<kPack> * kRows * sizeof(float));
     auto kernel = attention_kernel<kDim, kE4m3, kPack>;
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_size);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(num_sms * kCtasPerSm));
+    cfg.gridDim = dim3(static_cast<unsigned>(num_sms * kCtasOf<kPack>));
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = smem_size;
     cfg.stream = stream;
@@ -592,7 +700,7 @@ cudaError_t launch_typed(const AttnArgs &a, int num_sms, cudaStream_t stream) {
 }
 
 size_t part_bytes(int num_sms) {
-    return static_cast<size_t>(2 * num_sms * kCtasPerSm) * kSlotFloats * sizeof(float);
+    return static_cast<size_t>(2 * num_sms * kMaxCtasPerSm) * kSlotFloats * sizeof(float);
 }
 
 int subs_of(int group) { return (group + kRows - 1) / kRows; }
@@ -630,6 +738,9 @@ cudaError_t launch_attention(const bd_kv_cache &c, const void *q, int32_t q_head
     a.group = q_heads / c.kv_heads;
     a.subs = subs_of(a.group);
     a.window = window;
+    a.page_tiles = static_cast<uint32_t>(c.page_size / 16);
+    // exact while piece * (page_tiles - 1) < 2^32: pieces stay below 2^26, page_tiles at most 64
+    a.page_magic = static_cast<uint32_t>(((uint64_t{1} << 32) + a.page_tiles - 1) / a.page_tiles);
     a.scale_log2 = scale * 1.44269504088896f;
     const bool e = c.kv_type == BD_KV_E4M3, pack = a.group <= 8;
     if (c.head_dim == 128) {

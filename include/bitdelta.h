@@ -525,8 +525,9 @@ int32_t bd_kv_read(const bd_kv_cache *cache, const int32_t *page_table, int32_t 
  * not read into the result whatever they hold, and pages wholly outside the
  * window are not touched.  Scores, softmax statistics and the output's sums
  * are fp32; out is rounded once to bf16.  The softmax weights enter the
- * tensor cores as two 16-bit parts each (about 2^-16 of each weight); an
- * infinite V that a query sees may therefore give NaN.
+ * tensor cores as two 16-bit parts each (2^-16 of a weight or better; an
+ * infinite V that a query sees may therefore give NaN), q over an 8-bit cache to
+ * 2^-21 of its head's largest value.
  *
  *   q           bf16 [n_seqs, q_heads, head_dim]        (read)
  *   page_table  int32 [n_seqs, max_pages]               (read)
@@ -541,7 +542,7 @@ int32_t bd_kv_read(const bd_kv_cache *cache, const int32_t *page_table, int32_t 
  * CTAs; a (sequence, head) that several CTAs share is joined by the last of
  * them to finish, in key order, so results do not depend on timing.  No CTA
  * waits for another.  q_heads: a multiple of kv_heads.
- * A length below 0 or beyond max_pages * page_size, or a page id out of range,
+ * A length below 0 or beyond max_pages * page_size or 2^30, or a page id out of range,
  * sets BD_ERR_BAD_INDEX; the length counts as the nearest allowed one and the
  * keys of such a page as unseen.
  * Errors: BD_ERR_INVALID_ARG, BD_ERR_UNSUPPORTED_SHAPE, BD_ERR_MISALIGNED,
