@@ -49,6 +49,7 @@ constexpr int kMaxCtasPerSm = 3;
 constexpr int kDepth = 2;  // tiles in a warp's ring
 constexpr int64_t kMaxKeys = 1 << 30;  // the division by the page size is exact, positions stay int32
 constexpr int kSlotFloats = kRows * 128 + 2 * kRows;  // a part's output, maxima and sums
+constexpr int kSetup = 2;  // what a (sequence, head) costs a CTA beside its blocks, in blocks
 constexpr uint32_t kNoPage = 0xFFFFFFFFu;
 
 struct AttnArgs {
@@ -138,9 +139,10 @@ __device__ __forceinline__ uint32_t tile_at(int r, int c) {
     return r * kRow + ((c ^ (r & 7)) * 16);
 }
 
-// What a sequence's query sees: keys [start, len), cut into `blocks` blocks from block `first`.
+// What a sequence's query sees: keys [start, len), cut into `blocks` blocks from block `first`; with
+// a head's setup and join that is `units` of work per head.
 struct Span {
-    int32_t start, len, first, blocks;
+    int32_t start, len, first, blocks, units;
 };
 template <int kBlock>
 __device__ __forceinline__ Span span_of(const AttnArgs &a, int64_t b) {
@@ -155,6 +157,7 @@ __device__ __forceinline__ Span span_of(const AttnArgs &a, int64_t b) {
     s.start = a.window > 0 && len > a.window ? s.len - a.window : 0;
     s.first = s.start / kBlock;
     s.blocks = (s.len + kBlock - 1) / kBlock - s.first;
+    s.units = s.blocks > 0 ? s.blocks + kSetup : 0;
     return s;
 }
 
@@ -216,9 +219,9 @@ __global__ void __launch_bounds__(kThreads, kCtasOf<kPack>) attention_kernel(con
             for (int i = tid; i < a.q_heads; i += kThreads) a.lse[b * a.q_heads + i] = -INFINITY;
     }
 
-    // all items, and this CTA's range of them
+    // all units of work, and this CTA's range of them
     int64_t mine = 0;
-    for (int64_t b = tid; b < a.n_seqs; b += kThreads) mine += span_of<kBlock>(a, b).blocks;
+    for (int64_t b = tid; b < a.n_seqs; b += kThreads) mine += span_of<kBlock>(a, b).units;
     mine = warp_scan(mine);
     if (lane == 31) s_sum[warp] = mine;
     __syncthreads();
@@ -227,12 +230,12 @@ __global__ void __launch_bounds__(kThreads, kCtasOf<kPack>) attention_kernel(con
     if (blockIdx.x >= grid) return;
     const int64_t begin = total * blockIdx.x / grid, end = total * (blockIdx.x + 1) / grid;
 
-    // the sequence that holds item `begin`, and the blocks before it
+    // the sequence that holds unit `begin`, and the units before it
     {
         int64_t before = 0;
         for (int64_t b0 = 0; b0 < a.n_seqs; b0 += kThreads) {
             __syncthreads();
-            const int64_t n = b0 + tid < a.n_seqs ? span_of<kBlock>(a, b0 + tid).blocks : 0;
+            const int64_t n = b0 + tid < a.n_seqs ? span_of<kBlock>(a, b0 + tid).units : 0;
             const int64_t in = warp_scan(n);
             if (lane == 31) s_sum[warp] = in;
             __syncthreads();
@@ -243,15 +246,19 @@ __global__ void __launch_bounds__(kThreads, kCtasOf<kPack>) attention_kernel(con
         }
         __syncthreads();
     }
-    int64_t b = s_found[0], blocks_before = s_found[1];
+    int64_t b = s_found[0], units_before = s_found[1];
     Span sp = span_of<kBlock>(a, b);
-    int vh = static_cast<int>((begin - blocks_before * vheads) / sp.blocks);
-    int blk = static_cast<int>((begin - blocks_before * vheads) % sp.blocks);
+    int vh = static_cast<int>((begin - units_before * vheads) / sp.units);
     const uint32_t ring = smem_u32(smem) + warp * (kDepth * kStage);
     const uint8_t *ring_ptr = smem + warp * (kDepth * kStage);
 
-    for (int64_t it = begin; it < end;) {
-        const int n = static_cast<int>(min(end - it, static_cast<int64_t>(sp.blocks - blk)));
+    for (int64_t at = begin; at < end;) {
+        // this head's units start at i0, its setup first; what lies in this CTA's range of its blocks
+        const int64_t i0 = units_before * vheads + static_cast<int64_t>(vh) * sp.units;
+        const int64_t stop = min(end, i0 + sp.units);
+        const int blk = max(0, static_cast<int>(at - i0) - kSetup);
+        const int n = max(0, static_cast<int>(stop - i0) - kSetup) - blk;
+        if (n > 0) {
         const int kvh = vh / a.subs, row0 = vh % a.subs * kRows;
         const int rows = min(kRows, a.group - row0);
         const int64_t head0 = b * a.q_heads + kvh * a.group + row0;
@@ -586,8 +593,7 @@ __global__ void __launch_bounds__(kThreads, kCtasOf<kPack>) attention_kernel(con
         }
         __syncthreads();
         const bool whole = blk == 0 && n == sp.blocks;
-        const int64_t i0 = blocks_before * vheads + static_cast<int64_t>(vh) * sp.blocks;
-        float *slot = a.parts + (2 * blockIdx.x + (it == begin ? 0 : 1)) * static_cast<int64_t>(kSlotFloats);
+        float *slot = a.parts + (2 * blockIdx.x + (at == begin ? 0 : 1)) * static_cast<int64_t>(kSlotFloats);
         for (int i = tid; i < rows * kDim; i += kThreads) {
             const int r = i / kDim, d = i % kDim;
             float top = s_m[0][r];
@@ -611,8 +617,8 @@ __global__ void __launch_bounds__(kThreads, kCtasOf<kPack>) attention_kernel(con
             }
         }
         if (!whole) {
-            const int c0 = static_cast<int>(((i0 + 1) * grid - 1) / total);
-            const int c1 = static_cast<int>(((i0 + sp.blocks) * grid - 1) / total);
+            const int c0 = static_cast<int>(((i0 + kSetup + 1) * grid - 1) / total);
+            const int c1 = static_cast<int>(((i0 + sp.units) * grid - 1) / total);
             __threadfence();
             __syncthreads();
             if (tid == 0) {
@@ -626,18 +632,19 @@ __global__ void __launch_bounds__(kThreads, kCtasOf<kPack>) attention_kernel(con
                 __threadfence();
                 const int parts = c1 - c0 + 1;
                 float *f = reinterpret_cast<float *>(smem);  // [part][row]: a part's factor
-                auto slot_of = [&](int c) {
-                    return a.parts + (2 * c + (total * c / grid >= i0 ? 0 : 1)) * static_cast<int64_t>(kSlotFloats);
-                };
+                // part c lies in the first slot of its CTA; the first part in the second one if its CTA began before it
+                const float *first = a.parts + (2 * c0 + (total * c0 / grid >= i0 ? 0 : 1)) * static_cast<int64_t>(kSlotFloats);
+                const float *others = a.parts + 2 * c0 * static_cast<int64_t>(kSlotFloats);
+                auto slot_of = [&](int c) { return c ? others + c * static_cast<int64_t>(2 * kSlotFloats) : first; };
                 for (int r = warp; r < rows; r += kWarps) {
                     float top = -INFINITY;
-                    for (int c = lane; c < parts; c += 32) top = fmaxf(top, __ldcg(slot_of(c0 + c) + kRows * 128 + r));
+                    for (int c = lane; c < parts; c += 32) top = fmaxf(top, __ldcg(slot_of(c) + kRows * 128 + r));
 #pragma unroll
                     for (int x = 16; x > 0; x /= 2) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, x));
                     const float base = top == -INFINITY ? 0.f : top;
                     float sum = 0.f;
                     for (int c = lane; c < parts; c += 32) {
-                        const float *sl = slot_of(c0 + c) + kRows * 128;
+                        const float *sl = slot_of(c) + kRows * 128;
                         const float w = ex2(__ldcg(sl + r) - base);
                         f[c * kRows + r] = w;
                         sum += __ldcg(sl + kRows + r) * w;
@@ -653,11 +660,18 @@ __global__ void __launch_bounds__(kThreads, kCtasOf<kPack>) attention_kernel(con
                 for (int i = tid; i < rows * (kDim / 4); i += kThreads) {
                     const int r = i / (kDim / 4), d = i % (kDim / 4) * 4;
                     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-                    for (int c = 0; c < parts; ++c) {
-                        const float4 x = __ldcg(reinterpret_cast<const float4 *>(slot_of(c0 + c) + r * kDim + d));
-                        const float w = f[c * kRows + r];
-                        acc.x += x.x * w, acc.y += x.y * w, acc.z += x.z * w, acc.w += x.w * w;
+                    auto add = [&](const float4 &x, float w) { acc.x += x.x * w, acc.y += x.y * w, acc.z += x.z * w, acc.w += x.w * w; };
+                    add(__ldcg(reinterpret_cast<const float4 *>(first + r * kDim + d)), f[r]);
+                    const float *src = others + r * kDim + d;
+                    constexpr int kAtOnce = 16;  // loads in flight
+                    for (int c = 1; c < parts; c += kAtOnce) {
+                        float4 x[kAtOnce];
+#pragma unroll
+                        for (int u = 0; u < kAtOnce; ++u)
+                            if (c + u < parts) x[u] = __ldcg(reinterpret_cast<const float4 *>(src + (c + u) * static_cast<int64_t>(2 * kSlotFloats)));
+#pragma unroll
+                        for (int u = 0; u < kAtOnce; ++u)
+                            if (c + u < parts) add(x[u], f[(c + u) * kRows + r]);
                     }
                     const float sum = s_l[0][r];
                     const float inv = sum == 0.f ? 0.f : 1.f / sum;
@@ -667,14 +681,13 @@ __global__ void __launch_bounds__(kThreads, kCtasOf<kPack>) attention_kernel(con
             }
         }
         __syncthreads();  // shared memory is free again
-
-        it += n;
-        blk = 0;
-        if (++vh == vheads && it < end) {
+        }
+        at = stop;
+        if (++vh == vheads && at < end) {
             vh = 0;
-            blocks_before += sp.blocks;
+            units_before += sp.units;
             do sp = span_of<kBlock>(a, ++b);
-            while (sp.blocks == 0);
+            while (sp.units == 0);
         }
     }
 }
