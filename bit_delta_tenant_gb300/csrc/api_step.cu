@@ -109,7 +109,7 @@ int32_t check_heads(const bd_kv_cache *c, int32_t n_seqs, int32_t q_heads) {
 BD_API size_t bd_attention_workspace_size(const bd_kv_cache *cache, int32_t n_seqs, int32_t q_heads) {
     bd::DevCtx ctx;
     if (check_heads(cache, n_seqs, q_heads) != BD_OK || bd::make_dev_ctx(&ctx) != BD_OK) return 0;
-    return bd::attention_workspace_size(*cache, n_seqs, q_heads, ctx.num_sms);
+    return bd::attention_workspace_size(ctx.num_sms);
 }
 
 BD_API int32_t bd_attention_decode(const bd_kv_cache *cache, const void *q, int32_t q_heads, const int32_t *page_table,
@@ -127,7 +127,7 @@ BD_API int32_t bd_attention_decode(const bd_kv_cache *cache, const void *q, int3
     bd::DevCtx ctx;
     const int32_t rc = bd::make_dev_ctx(&ctx);
     if (rc != BD_OK) return rc;
-    if (workspace_bytes < bd::attention_workspace_size(*cache, n_seqs, q_heads, ctx.num_sms)) return BD_ERR_WORKSPACE;
+    if (workspace_bytes < bd::attention_workspace_size(ctx.num_sms)) return BD_ERR_WORKSPACE;
     return status_of(bd::launch_attention(*cache, q, q_heads, page_table, lengths, n_seqs, max_pages, scale, window, out,
                                           lse, workspace, ctx, static_cast<cudaStream_t>(stream)));
 }

@@ -50,6 +50,8 @@ constexpr int kDepth = 2;  // tiles in a warp's ring
 constexpr int64_t kMaxKeys = 1 << 30;  // the division by the page size is exact, positions stay int32
 constexpr int kSlotFloats = kRows * 128 + 2 * kRows;  // a part's output, maxima and sums
 constexpr int kSetup = 2;  // what a (sequence, head) costs a CTA beside its blocks, in blocks
+constexpr int kFan = 8;      // parts joined at a time
+constexpr int kLevels = 4;   // enough for kFan^4 parts
 constexpr uint32_t kNoPage = 0xFFFFFFFFu;
 
 struct AttnArgs {
@@ -57,10 +59,11 @@ struct AttnArgs {
     const int32_t *page_table, *lengths;
     uint8_t *out;
     float *lse, *parts;
-    int32_t *counters;
+    int32_t *counters;  // [kLevels][level_counters], one per slot
     unsigned *status;
     int64_t n_pages;
     int32_t n_seqs, max_pages, kv_heads, page_size, q_heads, group, subs, window;
+    int32_t level_counters;
     uint32_t page_tiles, page_magic;  // page_size / 16, and ceil(2^32 / that) for divisions by it
     float scale_log2;                 // scale * log2(e): scores are kept in base 2
 };
@@ -161,6 +164,27 @@ __device__ __forceinline__ Span span_of(const AttnArgs &a, int64_t b) {
     return s;
 }
 
+// x / y of whole numbers; the quick form where both fit 32 bits.
+__device__ __forceinline__ int64_t quotient(int64_t x, int64_t y) {
+    if ((x | y) >> 32) return x / y;
+    return static_cast<uint32_t>(x) / static_cast<uint32_t>(y);
+}
+
+// `total` units over at most `most` CTAs, the first `extra` of them with one unit more.
+struct Share {
+    int64_t ctas, each, extra;
+    __device__ __forceinline__ Share(int64_t total, int64_t most) {
+        ctas = min(most, total);
+        each = ctas ? quotient(total, ctas) : 0;
+        extra = total - each * ctas;
+    }
+    __device__ __forceinline__ int64_t begin(int64_t c) const { return each * c + min(c, extra); }
+    __device__ __forceinline__ int64_t owner(int64_t unit) const {  // the CTA whose range holds the unit
+        const int64_t head = (each + 1) * extra;
+        return unit < head ? quotient(unit, each + 1) : extra + quotient(unit - head, each);
+    }
+};
+
 __device__ __forceinline__ int64_t warp_scan(int64_t v) {  // inclusive
 #pragma unroll
     for (int o = 1; o < 32; o *= 2) {
@@ -205,33 +229,37 @@ __global__ void __launch_bounds__(kThreads, kCtasOf<kPack>) attention_kernel(con
     __shared__ int64_t s_sum[kWarps];
     __shared__ int64_t s_found[2];
     __shared__ float s_m[kWarps][kRows], s_l[kWarps][kRows];
+    __shared__ float s_jm[kFan][kRows], s_jl[kFan][kRows];
     __shared__ int s_last;
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, g = lane / 4, t4 = lane % 4;
     const int vheads = a.kv_heads * a.subs;
     pdl_trigger_and_wait();
 
-    // sequences with nothing to see: zeros
-    for (int64_t b = blockIdx.x; b < a.n_seqs; b += gridDim.x) {
-        if (span_of<kBlock>(a, b).blocks > 0) continue;
+    auto clear = [&](int64_t b) {  // a sequence with nothing to see
         uint4 *o = reinterpret_cast<uint4 *>(a.out + b * a.q_heads * (kDim * 2));
         for (int i = tid; i < a.q_heads * (kDim / 8); i += kThreads) o[i] = make_uint4(0, 0, 0, 0);
         if (a.lse)
             for (int i = tid; i < a.q_heads; i += kThreads) a.lse[b * a.q_heads + i] = -INFINITY;
-    }
+    };
+    for (int64_t b = blockIdx.x; b < a.n_seqs; b += gridDim.x)
+        if (span_of<kBlock>(a, b).units == 0) clear(b);
 
     // all units of work, and this CTA's range of them
     int64_t mine = 0;
     for (int64_t b = tid; b < a.n_seqs; b += kThreads) mine += span_of<kBlock>(a, b).units;
-    mine = warp_scan(mine);
-    if (lane == 31) s_sum[warp] = mine;
+    const int64_t upto = warp_scan(mine);
+    if (lane == 31) s_sum[warp] = upto;
     __syncthreads();
-    const int64_t total = (s_sum[0] + s_sum[1] + s_sum[2] + s_sum[3]) * vheads;
-    const int64_t grid = min(static_cast<int64_t>(gridDim.x), total);
-    if (blockIdx.x >= grid) return;
-    const int64_t begin = total * blockIdx.x / grid, end = total * (blockIdx.x + 1) / grid;
+    const Share share(static_cast<uint64_t>(s_sum[0] + s_sum[1] + s_sum[2] + s_sum[3]) * vheads, gridDim.x);
+    if (blockIdx.x >= share.ctas) return;
+    const int64_t begin = share.begin(blockIdx.x), end = share.begin(blockIdx.x + 1);
 
     // the sequence that holds unit `begin`, and the units before it
-    {
+    if (a.n_seqs <= kThreads) {  // one sequence per thread: the sums above are the positions
+        int64_t p = upto - mine;
+        for (int w = 0; w < warp; ++w) p += s_sum[w];
+        if (mine > 0 && p * vheads <= begin && begin < (p + mine) * vheads) s_found[0] = tid, s_found[1] = p;
+    } else {
         int64_t before = 0;
         for (int64_t b0 = 0; b0 < a.n_seqs; b0 += kThreads) {
             __syncthreads();
@@ -244,11 +272,11 @@ __global__ void __launch_bounds__(kThreads, kCtasOf<kPack>) attention_kernel(con
             if (n > 0 && p * vheads <= begin && begin < (p + n) * vheads) s_found[0] = b0 + tid, s_found[1] = p;
             before += s_sum[0] + s_sum[1] + s_sum[2] + s_sum[3];
         }
-        __syncthreads();
     }
+    __syncthreads();
     int64_t b = s_found[0], units_before = s_found[1];
     Span sp = span_of<kBlock>(a, b);
-    int vh = static_cast<int>((begin - units_before * vheads) / sp.units);
+    int vh = static_cast<int>(quotient(begin - units_before * vheads, sp.units));
     const uint32_t ring = smem_u32(smem) + warp * (kDepth * kStage);
     const uint8_t *ring_ptr = smem + warp * (kDepth * kStage);
 
@@ -577,108 +605,125 @@ __global__ void __launch_bounds__(kThreads, kCtasOf<kPack>) attention_kernel(con
 
         // the four warps' states, joined in shared memory
         constexpr int kUsed = 8 * kHalves;
-        float *merge = reinterpret_cast<float *>(smem);  // [warp][row][kDim]
+        constexpr int kStride = kDim + 4;                  // rows of heads 2t fall into different banks
+        float *merge = reinterpret_cast<float *>(smem);    // [warp][row][kStride]
 #pragma unroll
         for (int h = 0; h < kHalves; ++h) {
             l[h] += __shfl_xor_sync(0xFFFFFFFFu, l[h], 1);
             l[h] += __shfl_xor_sync(0xFFFFFFFFu, l[h], 2);
             if (t4 == 0) s_m[warp][g + 8 * h] = m[h], s_l[warp][g + 8 * h] = l[h];
+            float *mine = merge + (warp * kUsed + 8 * h + 2 * t4) * kStride;
 #pragma unroll
-            for (int c = 0; c < kRowTiles; ++c)
+            for (int e = 0; e < 2; ++e, mine += kStride) {
+                if constexpr (kE4m3) {
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int d = kE4m3 ? g * (kDim / 8) + 2 * c + e / 2 : c * 16 + g + e / 2 * 8;
-                    merge[(warp * kUsed + 8 * h + 2 * t4 + e % 2) * kDim + d] = o[c][h][e];
+                    for (int c = 0; c < kRowTiles; c += 2)
+                        *reinterpret_cast<float4 *>(mine + g * (kDim / 8) + 2 * c) =
+                            make_float4(o[c][h][e], o[c][h][2 + e], o[c + 1][h][e], o[c + 1][h][2 + e]);
+                } else {
+#pragma unroll
+                    for (int c = 0; c < kRowTiles; ++c) mine[c * 16 + g] = o[c][h][e], mine[c * 16 + g + 8] = o[c][h][2 + e];
                 }
+            }
         }
         __syncthreads();
         const bool whole = blk == 0 && n == sp.blocks;
-        float *slot = a.parts + (2 * blockIdx.x + (at == begin ? 0 : 1)) * static_cast<int64_t>(kSlotFloats);
-        for (int i = tid; i < rows * kDim; i += kThreads) {
-            const int r = i / kDim, d = i % kDim;
+        auto finish = [&](int r, int d, float4 x, float top, float sum) {  // four columns of a row, and once its lse
+            const float inv = sum == 0.f ? 0.f : 1.f / sum;
+            *reinterpret_cast<uint2 *>(a.out + ((head0 + r) * kDim + d) * 2) =
+                make_uint2(pack_bf16x2(x.x * inv, x.y * inv), pack_bf16x2(x.z * inv, x.w * inv));
+            if (a.lse && d == 0) a.lse[head0 + r] = (top + log2f(sum)) * 0.693147180559945f;
+        };
+        auto store_part = [&](float *slot, int r, int d, float4 x, float top, float sum) {
+            *reinterpret_cast<float4 *>(slot + r * kDim + d) = x;
+            if (d == 0) slot[kRows * 128 + r] = top, slot[kRows * 128 + kRows + r] = sum;
+        };
+        // part c of this (sequence, head) lies in the first slot of its CTA, or in the second one where that
+        // CTA's range began before the head
+        const int c0 = static_cast<int>(share.owner(i0 + kSetup)), parts = static_cast<int>(share.owner(i0 + sp.units - 1)) - c0 + 1;
+        const int id0 = 2 * c0 + (share.begin(c0) >= i0 ? 0 : 1);
+        auto id_of = [&](int c) { return c ? 2 * (c0 + c) : id0; };
+        auto slot_of = [&](int c) { return a.parts + id_of(c) * static_cast<int64_t>(kSlotFloats); };
+        for (int i = tid; i < rows * (kDim / 4); i += kThreads) {
+            const int r = i / (kDim / 4), d = i % (kDim / 4) * 4;
             float top = s_m[0][r];
 #pragma unroll
             for (int w = 1; w < kWarps; ++w) top = fmaxf(top, s_m[w][r]);
             const float base = top == -INFINITY ? 0.f : top;
-            float sum = 0.f, acc = 0.f;
+            float sum = 0.f;
+            float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) {
                 const float f = ex2(s_m[w][r] - base);
-                sum += s_l[w][r] * f;
-                acc += merge[(w * kUsed + r) * kDim + d] * f;
+                const float4 y = *reinterpret_cast<const float4 *>(merge + (w * kUsed + r) * kStride + d);
+                sum = fmaf(s_l[w][r], f, sum);
+                x.x = fmaf(y.x, f, x.x), x.y = fmaf(y.y, f, x.y), x.z = fmaf(y.z, f, x.z), x.w = fmaf(y.w, f, x.w);
             }
-            if (whole) {
-                const __nv_bfloat16 y = __float2bfloat16_rn(sum == 0.f ? 0.f : acc / sum);
-                reinterpret_cast<__nv_bfloat16 *>(a.out)[(head0 + r) * kDim + d] = y;
-                if (a.lse && d == 0) a.lse[head0 + r] = (top + log2f(sum)) * 0.693147180559945f;
-            } else {
-                slot[r * kDim + d] = acc;
-                if (d == 0) slot[kRows * 128 + r] = top, slot[kRows * 128 + kRows + r] = sum;
-            }
+            if (whole) finish(r, d, x, top, sum);
+            else store_part(slot_of(blockIdx.x - c0), r, d, x, top, sum);
         }
-        if (!whole) {
-            const int c0 = static_cast<int>(((i0 + kSetup + 1) * grid - 1) / total);
-            const int c1 = static_cast<int>(((i0 + sp.units) * grid - 1) / total);
-            __threadfence();
-            __syncthreads();
+        // Join of the parts: eight neighbours by the last of them to arrive, then eight of these, and so on;
+        // which parts meet is fixed, so the result does not depend on who was last.
+        int index = blockIdx.x - c0, stride = 1;
+        for (int level = 0; !whole; ++level) {
+            const int left = (parts + stride - 1) / stride;  // parts of this level
+            if (left == 1) break;
+            const int lead = index / kFan * kFan, count = min(kFan, left - lead);
+            __syncthreads();  // this CTA's part is written; the fence below publishes it for all threads
             if (tid == 0) {
-                int32_t *ctr = a.counters + b * vheads + vh;
-                const int arrived = atomicAdd(ctr, 1);
-                s_last = arrived == c1 - c0;
+                int32_t *ctr = a.counters + level * a.level_counters + id_of(lead * stride);
+                int before;
+                asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;" : "=r"(before) : "l"(ctr) : "memory");
+                s_last = before == count - 1;
                 if (s_last) *ctr = 0;  // ready for the next call
             }
             __syncthreads();
-            if (s_last) {
-                __threadfence();
-                const int parts = c1 - c0 + 1;
-                float *f = reinterpret_cast<float *>(smem);  // [part][row]: a part's factor
-                // part c lies in the first slot of its CTA; the first part in the second one if its CTA began before it
-                const float *first = a.parts + (2 * c0 + (total * c0 / grid >= i0 ? 0 : 1)) * static_cast<int64_t>(kSlotFloats);
-                const float *others = a.parts + 2 * c0 * static_cast<int64_t>(kSlotFloats);
-                auto slot_of = [&](int c) { return c ? others + c * static_cast<int64_t>(2 * kSlotFloats) : first; };
-                for (int r = warp; r < rows; r += kWarps) {
-                    float top = -INFINITY;
-                    for (int c = lane; c < parts; c += 32) top = fmaxf(top, __ldcg(slot_of(c) + kRows * 128 + r));
+            if (!s_last) break;
+            if (tid < kFan * kRows) {
+                const int q = tid / kRows, r = tid % kRows;
+                const bool on = q < count && r < rows;
+                const float *slot = slot_of((lead + (on ? q : 0)) * stride) + kRows * 128;
+                s_jm[q][r] = on ? __ldcg(slot + r) : -INFINITY;
+                s_jl[q][r] = on ? __ldcg(slot + kRows + r) : 0.f;
+            }
+            constexpr int kEach = kUsed * (kDim / 4) / kThreads;  // column quadruples of a thread
 #pragma unroll
-                    for (int x = 16; x > 0; x /= 2) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, x));
-                    const float base = top == -INFINITY ? 0.f : top;
-                    float sum = 0.f;
-                    for (int c = lane; c < parts; c += 32) {
-                        const float *sl = slot_of(c) + kRows * 128;
-                        const float w = ex2(__ldcg(sl + r) - base);
-                        f[c * kRows + r] = w;
-                        sum += __ldcg(sl + kRows + r) * w;
-                    }
+            for (int e = 0; e < kEach; e += 2) {
+                float4 y[2][kFan];
 #pragma unroll
-                    for (int x = 16; x > 0; x /= 2) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, x);
-                    if (lane == 0) {
-                        s_l[0][r] = sum;
-                        if (a.lse) a.lse[head0 + r] = (top + log2f(sum)) * 0.693147180559945f;
-                    }
+                for (int w = 0; w < 2; ++w) {
+                    const int i = tid + (e + w) * kThreads;
+#pragma unroll
+                    for (int q = 0; q < kFan; ++q)
+                        if (e + w < kEach && q < count && i < rows * (kDim / 4))
+                            y[w][q] = __ldcg(reinterpret_cast<const float4 *>(slot_of((lead + q) * stride)) + i);
                 }
                 __syncthreads();
-                for (int i = tid; i < rows * (kDim / 4); i += kThreads) {
+#pragma unroll
+                for (int w = 0; w < 2; ++w) {
+                    const int i = tid + (e + w) * kThreads;
+                    if (e + w >= kEach || i >= rows * (kDim / 4)) continue;
                     const int r = i / (kDim / 4), d = i % (kDim / 4) * 4;
-                    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-                    auto add = [&](const float4 &x, float w) { acc.x += x.x * w, acc.y += x.y * w, acc.z += x.z * w, acc.w += x.w * w; };
-                    add(__ldcg(reinterpret_cast<const float4 *>(first + r * kDim + d)), f[r]);
-                    const float *src = others + r * kDim + d;
-                    constexpr int kAtOnce = 16;  // loads in flight
-                    for (int c = 1; c < parts; c += kAtOnce) {
-                        float4 x[kAtOnce];
+                    float top = s_jm[0][r];
 #pragma unroll
-                        for (int u = 0; u < kAtOnce; ++u)
-                            if (c + u < parts) x[u] = __ldcg(reinterpret_cast<const float4 *>(src + (c + u) * static_cast<int64_t>(2 * kSlotFloats)));
+                    for (int q = 1; q < kFan; ++q) top = fmaxf(top, s_jm[q][r]);
+                    const float base = top == -INFINITY ? 0.f : top;
+                    float sum = 0.f;
+                    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-                        for (int u = 0; u < kAtOnce; ++u)
-                            if (c + u < parts) add(x[u], f[(c + u) * kRows + r]);
+                    for (int q = 0; q < kFan; ++q) {
+                        if (q >= count) continue;
+                        const float f = ex2(s_jm[q][r] - base);
+                        sum = fmaf(s_jl[q][r], f, sum);
+                        x.x = fmaf(y[w][q].x, f, x.x), x.y = fmaf(y[w][q].y, f, x.y);
+                        x.z = fmaf(y[w][q].z, f, x.z), x.w = fmaf(y[w][q].w, f, x.w);
                     }
-                    const float sum = s_l[0][r];
-                    const float inv = sum == 0.f ? 0.f : 1.f / sum;
-                    *reinterpret_cast<uint2 *>(a.out + ((head0 + r) * kDim + d) * 2) =
-                        make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+                    if (left <= kFan) finish(r, d, x, top, sum);
+                    else store_part(slot_of(lead * stride), r, d, x, top, sum);  // in place of the first of the eight
                 }
             }
+            index /= kFan;
+            stride *= kFan;
         }
         __syncthreads();  // shared memory is free again
         }
@@ -694,8 +739,7 @@ __global__ void __launch_bounds__(kThreads, kCtasOf<kPack>) attention_kernel(con
 
 template <int kDim, bool kE4m3, bool kPack>
 cudaError_t launch_typed(const AttnArgs &a, int num_sms, cudaStream_t stream) {
-    // the join keeps one factor per part and row in the same memory
-    const int smem_size = std::max<int>(smem_bytes<kDim, kE4m3>(), num_sms * kCtasOf<kPack> * kRows * sizeof(float));
+    constexpr int smem_size = smem_bytes<kDim, kE4m3>();
     auto kernel = attention_kernel<kDim, kE4m3, kPack>;
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_size);
     if (e != cudaSuccess) return e;
@@ -712,18 +756,16 @@ cudaError_t launch_typed(const AttnArgs &a, int num_sms, cudaStream_t stream) {
     return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 
-size_t part_bytes(int num_sms) {
-    return static_cast<size_t>(2 * num_sms * kMaxCtasPerSm) * kSlotFloats * sizeof(float);
-}
+int slots_of(int num_sms) { return 2 * num_sms * kMaxCtasPerSm; }
+size_t part_bytes(int num_sms) { return static_cast<size_t>(slots_of(num_sms)) * kSlotFloats * sizeof(float); }
 
 int subs_of(int group) { return (group + kRows - 1) / kRows; }
 
 }  // namespace
 
-// The parts come first, at a size fixed by the device, so that the counters lie at the same place for every batch.
-size_t attention_workspace_size(const bd_kv_cache &c, int32_t n_seqs, int32_t q_heads, int num_sms) {
-    const size_t vheads = static_cast<size_t>(c.kv_heads) * subs_of(q_heads / c.kv_heads);
-    return part_bytes(num_sms) + (static_cast<size_t>(n_seqs) * vheads * sizeof(int32_t) + 255) / 256 * 256;
+// Slots and counters belong to CTAs, so the workspace has one size for every batch.
+size_t attention_workspace_size(int num_sms) {
+    return part_bytes(num_sms) + (static_cast<size_t>(kLevels) * slots_of(num_sms) * sizeof(int32_t) + 255) / 256 * 256;
 }
 
 cudaError_t launch_attention(const bd_kv_cache &c, const void *q, int32_t q_heads, const int32_t *page_table,
@@ -741,6 +783,7 @@ cudaError_t launch_attention(const bd_kv_cache &c, const void *q, int32_t q_head
     a.lse = lse;
     a.parts = static_cast<float *>(workspace);
     a.counters = reinterpret_cast<int32_t *>(static_cast<uint8_t *>(workspace) + part_bytes(ctx.num_sms));
+    a.level_counters = slots_of(ctx.num_sms);
     a.status = ctx.status;
     a.n_pages = c.n_pages;
     a.n_seqs = n_seqs;

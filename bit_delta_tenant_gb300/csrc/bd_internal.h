@@ -220,7 +220,7 @@ cudaError_t launch_kv_read(const bd_kv_cache &c, const int32_t *page_table, int3
                            const int32_t *offsets, int64_t total, void *k_out, void *v_out, const DevCtx &ctx,
                            cudaStream_t stream);
 
-size_t attention_workspace_size(const bd_kv_cache &c, int32_t n_seqs, int32_t q_heads, int num_sms);
+size_t attention_workspace_size(int num_sms);
 cudaError_t launch_attention(const bd_kv_cache &c, const void *q, int32_t q_heads, const int32_t *page_table,
                              const int32_t *lengths, int32_t n_seqs, int32_t max_pages, float scale, int32_t window,
                              void *out, float *lse, void *workspace, const DevCtx &ctx, cudaStream_t stream);
