@@ -424,25 +424,39 @@ def bd_linear_grouped(x: torch.Tensor, variant_ids: torch.Tensor, w_base: torch.
 
 
 # ---- the rest of a decode step: norm, key-value cache, attention, sampling ----------------
-# Tensors are checked here for type and shape, because the library sees only their addresses.
+# Tensors are checked here for type, shape and layout, because the library sees only their
+# addresses.  A decode step makes many of these calls on small inputs, so the checks are kept to a
+# few attribute reads per tensor and the stream is read as a raw handle.
+
+
+def _refuse(t: torch.Tensor, name: str, shape, dtype) -> None:
+    if t.dtype != dtype:
+        raise ValueError(f"{name}: expected {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    raise ValueError(f"{name}: tensors passed to libbitdelta must be contiguous")
 
 
 def _arg(t: torch.Tensor | None, name: str, shape, dtype) -> int | None:
     """Address of a contiguous tensor of the given shape and type (None stays NULL)."""
     if t is None:
         return None
-    if t.dtype != dtype:
-        raise ValueError(f"{name}: expected {dtype}, got {t.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name}: tensors passed to libbitdelta must be contiguous")
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
+        _refuse(t, name, shape, dtype)
     return t.data_ptr()
 
 
-def _raw_stream(stream) -> int:
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return s.cuda_stream if hasattr(s, "cuda_stream") else int(s)
+def _raw_stream(stream, t: torch.Tensor) -> int:
+    """Handle of `stream`, or of the current stream of the device that holds t."""
+    if stream is None:
+        device = t.get_device()
+        if device < 0:
+            raise ValueError("tensors passed to libbitdelta must be on a CUDA device")
+        return torch._C._cuda_getCurrentRawStream(device)
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+_BF16, _E4M3, _F32, _I32, _U8 = torch.bfloat16, torch.float8_e4m3fn, torch.float32, torch.int32, torch.uint8
 
 
 def bd_rmsnorm(x: torch.Tensor, weight: torch.Tensor, eps: float, y: torch.Tensor, residual: torch.Tensor | None = None,
@@ -453,24 +467,25 @@ def bd_rmsnorm(x: torch.Tensor, weight: torch.Tensor, eps: float, y: torch.Tenso
     `residual_out` receives bf16(x + residual) and may be `residual` itself.  A bf16 `y` is
     rounded once; a float8_e4m3fn `y` comes with `y_scale`, fp32 [m, n / 128] (a scale per
     128 columns) or [m, 1] (one per row)."""
-    m, n = x.shape
-    bf16 = torch.bfloat16
-    n_weights = weight.shape[0] if weight.dim() == 2 else 1
-    y_type = BD_Y_E4M3 if y.dtype == torch.float8_e4m3fn else BD_Y_BF16
-    scale_cols = 0
-    if y_scale is not None:
-        cols = y_scale.shape[1] if y_scale.dim() == 2 else 0
+    shape = x.shape
+    m, n = shape
+    n_weights, w_shape = (weight.shape[0], (weight.shape[0], n)) if weight.dim() == 2 else (1, (n,))
+    y_type, scale_cols, scale = BD_Y_BF16, 0, None
+    if y.dtype is _E4M3:
+        y_type = BD_Y_E4M3
+        cols = y_scale.shape[1] if y_scale is not None and y_scale.dim() == 2 else 0
         if cols < 1 or n % cols != 0:
-            raise ValueError("y_scale: expected [m, n / 128] or [m, 1]")
-        scale_cols = n // cols
-    rc = load_library().bd_rmsnorm(
-        _arg(x, "x", (m, n), bf16), _arg(residual, "residual", (m, n), bf16),
-        _arg(weight, "weight", weight.shape[:-1] + (n,) if weight.dim() in (1, 2) else (n_weights, n), bf16),
-        _arg(weight_ids, "weight_ids", (m,), torch.int32), n_weights, m, n, eps,
-        _arg(y, "y", (m, n), torch.float8_e4m3fn if y_type else bf16), y_type,
-        _arg(y_scale, "y_scale", (m, n // scale_cols if scale_cols else 0), torch.float32), scale_cols,
-        _arg(residual_out, "residual_out", (m, n), bf16), _raw_stream(stream))
-    _check(rc, "bd_rmsnorm")
+            raise ValueError("y_scale: an 8-bit y comes with scales of shape [m, n / 128] or [m, 1]")
+        scale_cols, scale = n // cols, _arg(y_scale, "y_scale", (m, cols), _F32)
+    elif y_scale is not None:
+        raise ValueError("y_scale: only an 8-bit y has scales")
+    rc = (_lib or load_library()).bd_rmsnorm(
+        _arg(x, "x", shape, _BF16), None if residual is None else _arg(residual, "residual", shape, _BF16),
+        _arg(weight, "weight", w_shape, _BF16), None if weight_ids is None else _arg(weight_ids, "weight_ids", (m,), _I32),
+        n_weights, m, n, eps, _arg(y, "y", shape, _E4M3 if y_type else _BF16), y_type, scale, scale_cols,
+        None if residual_out is None else _arg(residual_out, "residual_out", shape, _BF16), _raw_stream(stream, x))
+    if rc:
+        _check(rc, "bd_rmsnorm")
 
 
 class KVCache:
@@ -484,26 +499,28 @@ class KVCache:
                  v_scale: torch.Tensor | None = None):
         if k.dim() != 4:
             raise ValueError("k: expected [n_pages, kv_heads, page_size, head_dim]")
-        if k.dtype not in (torch.bfloat16, torch.float8_e4m3fn):
+        if k.dtype not in (_BF16, _E4M3):
             raise ValueError(f"k: expected torch.bfloat16 or torch.float8_e4m3fn, got {k.dtype}")
-        e4m3 = k.dtype == torch.float8_e4m3fn
+        e4m3 = k.dtype == _E4M3
         if e4m3 != (k_scale is not None) or e4m3 != (v_scale is not None):
             raise ValueError("k_scale and v_scale come with an 8-bit cache, and only with one")
         n_pages, self.kv_heads, self.page_size, self.head_dim = k.shape
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
         d = self.desc = KVCacheDesc()
         d.k, d.v = _arg(k, "k", k.shape, k.dtype), _arg(v, "v", k.shape, k.dtype)
-        d.k_scale = _arg(k_scale, "k_scale", k.shape[:3], torch.uint8)
-        d.v_scale = _arg(v_scale, "v_scale", k.shape[:3], torch.uint8)
+        d.k_scale = _arg(k_scale, "k_scale", k.shape[:3], _U8)
+        d.v_scale = _arg(v_scale, "v_scale", k.shape[:3], _U8)
         d.n_pages, d.kv_heads, d.head_dim, d.page_size = n_pages, self.kv_heads, self.head_dim, self.page_size
         d.kv_type = BD_KV_E4M3 if e4m3 else BD_KV_BF16
         self._ref = ctypes.byref(d)
 
 
 def _table(page_table: torch.Tensor):
-    if page_table.dim() != 2:
+    """(address, n_seqs, max_pages) of a page table."""
+    shape = page_table.shape
+    if len(shape) != 2:
         raise ValueError("page_table: expected [n_seqs, max_pages]")
-    return _arg(page_table, "page_table", page_table.shape, torch.int32), *page_table.shape
+    return _arg(page_table, "page_table", shape, _I32), shape[0], shape[1]
 
 
 def bd_kv_append(cache: KVCache, q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor, positions: torch.Tensor,
@@ -514,29 +531,35 @@ def bd_kv_append(cache: KVCache, q: torch.Tensor | None, k: torch.Tensor, v: tor
     Token i goes to position positions[i] of sequence seq_ids[i] (of sequence i without
     seq_ids); a negative position skips it.  `rope` is fp32 [positions, head_dim], cosines then
     sines; without it nothing is rotated and q and q_out are None.  q_out may be q."""
-    n, dim, bf16 = k.shape[0], cache.head_dim, torch.bfloat16
-    q_heads = q.shape[1] if q is not None and q.dim() == 3 else 0
-    rope_len = rope.shape[0] if rope is not None else 0
+    n, dim = k.shape[0], cache.head_dim
+    kv_shape = (n, cache.kv_heads, dim)
+    q_heads, qp, qo = 0, None, None
+    if q is not None or q_out is not None:
+        if q is None or q_out is None or q.dim() != 3:
+            raise ValueError("q, q_out: both [tokens, q_heads, head_dim], or neither")
+        q_heads = q.shape[1]
+        qp, qo = _arg(q, "q", (n, q_heads, dim), _BF16), _arg(q_out, "q_out", (n, q_heads, dim), _BF16)
+    rope_len = 0 if rope is None else rope.shape[0]
     table, n_seqs, max_pages = _table(page_table)
-    rc = load_library().bd_kv_append(
-        cache._ref, _arg(q, "q", (n, q_heads, dim), bf16), q_heads, _arg(k, "k", (n, cache.kv_heads, dim), bf16),
-        _arg(v, "v", (n, cache.kv_heads, dim), bf16), n, _arg(seq_ids, "seq_ids", (n,), torch.int32),
-        _arg(positions, "positions", (n,), torch.int32), table, n_seqs, max_pages,
-        _arg(rope, "rope", (rope_len, dim), torch.float32), rope_len, _arg(q_out, "q_out", (n, q_heads, dim), bf16),
-        _raw_stream(stream))
-    _check(rc, "bd_kv_append")
+    rc = (_lib or load_library()).bd_kv_append(
+        cache._ref, qp, q_heads, _arg(k, "k", kv_shape, _BF16), _arg(v, "v", kv_shape, _BF16), n,
+        None if seq_ids is None else _arg(seq_ids, "seq_ids", (n,), _I32), _arg(positions, "positions", (n,), _I32), table,
+        n_seqs, max_pages, None if rope is None else _arg(rope, "rope", (rope_len, dim), _F32), rope_len, qo,
+        _raw_stream(stream, k))
+    if rc:
+        _check(rc, "bd_kv_append")
 
 
 def bd_kv_read(cache: KVCache, page_table: torch.Tensor, offsets: torch.Tensor, k_out: torch.Tensor,
                v_out: torch.Tensor, stream=None) -> None:
     """The first offsets[i + 1] - offsets[i] cached tokens of sequence i, as bf16 rows offsets[i] .. of k_out and v_out."""
     table, n_seqs, max_pages = _table(page_table)
-    total = k_out.shape[0]
-    shape = (total, cache.kv_heads, cache.head_dim)
-    rc = load_library().bd_kv_read(
-        cache._ref, table, n_seqs, max_pages, _arg(offsets, "offsets", (n_seqs + 1,), torch.int32), total,
-        _arg(k_out, "k_out", shape, torch.bfloat16), _arg(v_out, "v_out", shape, torch.bfloat16), _raw_stream(stream))
-    _check(rc, "bd_kv_read")
+    shape = (k_out.shape[0], cache.kv_heads, cache.head_dim)
+    rc = (_lib or load_library()).bd_kv_read(
+        cache._ref, table, n_seqs, max_pages, _arg(offsets, "offsets", (n_seqs + 1,), _I32), shape[0],
+        _arg(k_out, "k_out", shape, _BF16), _arg(v_out, "v_out", shape, _BF16), _raw_stream(stream, k_out))
+    if rc:
+        _check(rc, "bd_kv_read")
 
 
 def bd_attention_workspace_size(cache: KVCache, n_seqs: int, q_heads: int) -> int:
@@ -555,13 +578,13 @@ def bd_attention_decode(cache: KVCache, q: torch.Tensor, page_table: torch.Tenso
     table, n_seqs, max_pages = _table(page_table)
     q_heads = q.shape[1] if q.dim() == 3 else 0
     shape = (n_seqs, q_heads, cache.head_dim)
-    rc = load_library().bd_attention_decode(
-        cache._ref, _arg(q, "q", shape, torch.bfloat16), q_heads, table,
-        _arg(lengths, "lengths", (n_seqs,), torch.int32), n_seqs, max_pages,
-        cache.head_dim ** -0.5 if scale is None else scale, window, _arg(out, "out", shape, torch.bfloat16),
-        _arg(lse, "lse", (n_seqs, q_heads), torch.float32), workspace.data_ptr(),
-        workspace.numel() * workspace.element_size(), _raw_stream(stream))
-    _check(rc, "bd_attention_decode")
+    rc = (_lib or load_library()).bd_attention_decode(
+        cache._ref, _arg(q, "q", shape, _BF16), q_heads, table, _arg(lengths, "lengths", (n_seqs,), _I32), n_seqs, max_pages,
+        cache.head_dim ** -0.5 if scale is None else scale, window, _arg(out, "out", shape, _BF16),
+        None if lse is None else _arg(lse, "lse", (n_seqs, q_heads), _F32), workspace.data_ptr(), workspace.nbytes,
+        _raw_stream(stream, q))
+    if rc:
+        _check(rc, "bd_attention_decode")
 
 
 def bd_sample(logits: torch.Tensor, noise: torch.Tensor, ids: torch.Tensor, temperature: torch.Tensor | None = None,
@@ -571,13 +594,16 @@ def bd_sample(logits: torch.Tensor, noise: torch.Tensor, ids: torch.Tensor, temp
 
     `temperature`, `top_k` (int32), `top_p` and `min_p` hold one setting per row; None leaves the
     filter off (temperature 1).  `logprob` receives the drawn token's log probability before the filters."""
-    m, vocab = logits.shape
-    f32 = torch.float32
-    bf16_logits = logits.dtype == torch.bfloat16
-    rc = load_library().bd_sample(
-        _arg(logits, "logits", (m, vocab), torch.bfloat16 if bf16_logits else f32),
-        BD_LOGITS_BF16 if bf16_logits else BD_LOGITS_F32, m, vocab, _arg(temperature, "temperature", (m,), f32),
-        _arg(top_k, "top_k", (m,), torch.int32), _arg(top_p, "top_p", (m,), f32), _arg(min_p, "min_p", (m,), f32),
-        _arg(noise, "noise", (m, vocab), f32), _arg(ids, "ids", (m,), torch.int32),
-        _arg(logprob, "logprob", (m,), f32), _raw_stream(stream))
-    _check(rc, "bd_sample")
+    shape = logits.shape
+    m, vocab = shape
+    row = (m,)
+    half = logits.dtype is _BF16
+    rc = (_lib or load_library()).bd_sample(
+        _arg(logits, "logits", shape, _BF16 if half else _F32), BD_LOGITS_BF16 if half else BD_LOGITS_F32, m, vocab,
+        None if temperature is None else _arg(temperature, "temperature", row, _F32),
+        None if top_k is None else _arg(top_k, "top_k", row, _I32), None if top_p is None else _arg(top_p, "top_p", row, _F32),
+        None if min_p is None else _arg(min_p, "min_p", row, _F32), _arg(noise, "noise", shape, _F32),
+        _arg(ids, "ids", row, _I32), None if logprob is None else _arg(logprob, "logprob", row, _F32),
+        _raw_stream(stream, logits))
+    if rc:
+        _check(rc, "bd_sample")

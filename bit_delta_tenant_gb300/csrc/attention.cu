@@ -46,7 +46,7 @@ constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kRows = 16;  // query heads of one tile
 constexpr int kMaxCtasPerSm = 3;
-constexpr int kDepth = 2;  // tiles in a warp's ring
+constexpr int kDepth = 2;  // tiles in a warp's ring: one in use, one in flight
 constexpr int64_t kMaxKeys = 1 << 30;  // the division by the page size is exact, positions stay int32
 constexpr int kSlotFloats = kRows * 128 + 2 * kRows;  // a part's output, maxima and sums
 constexpr int kSetup = 2;  // what a (sequence, head) costs a CTA beside its blocks, in blocks
@@ -71,6 +71,9 @@ struct AttnArgs {
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool full) {
     const int n = full ? 16 : 0;  // 0: nothing is read, 16 zero bytes are written
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -278,6 +281,15 @@ __global__ void __launch_bounds__(kThreads, kCtasOf<kPack>) attention_kernel(con
     Span sp = span_of<kBlock>(a, b);
     int vh = static_cast<int>(quotient(begin - units_before * vheads, sp.units));
     const uint32_t ring = smem_u32(smem) + warp * (kDepth * kStage);
+    // Lane offsets that repeat: the swizzle turns with the row, so a copy has kTurns of them and a
+    // fragment load one per chunk pair within 128 bytes; everything else is a constant.
+    constexpr int kTurns = kChunks / 4, kPairs = kSteps < 4 ? kSteps : 4;
+    uint32_t copy_at[kTurns], load_at[kPairs];
+#pragma unroll
+    for (int i = 0; i < kTurns; ++i) copy_at[i] = ring + tile_at<kRow>((lane + 32 * i) / kChunks, lane % kChunks);
+#pragma unroll
+    for (int k = 0; k < kPairs; ++k)
+        load_at[k] = ring + tile_at<kRow>(lane % 8 + lane / 16 * 8, 2 * k + lane / 8 % 2);
     const uint8_t *ring_ptr = smem + warp * (kDepth * kStage);
 
     for (int64_t at = begin; at < end;) {
@@ -379,61 +391,66 @@ __global__ void __launch_bounds__(kThreads, kCtasOf<kPack>) attention_kernel(con
         uint32_t places = place_of(0, next_pages);
         next_pages = fetch_page(kBatch);
         uint32_t bad = 0;  // pieces in the ring whose page id is out of range
-        auto load = [&](int j) {
+        auto load = [&](int j, const int slot) {
             if (j >= n) return;
             if (j > 0 && j % kBatch == 0) {
                 places = place_of(j, next_pages);
                 next_pages = fetch_page(j + kBatch);
             }
-            const int key0 = key_first + j * kBlock, slot = j % kDepth;
+            const int key0 = key_first + j * kBlock;
             if (key0 >= sp.len || key0 + kTile <= sp.start) return;
-            const uint32_t dst = ring + slot * kStage;
+            const uint32_t to = slot * kStage;
             const bool inside = key0 >= sp.start && key0 + kTile <= sp.len;
 #pragma unroll
             for (int u = 0; u < kSub; ++u) {
                 uint32_t place = __shfl_sync(0xFFFFFFFFu, places, j % kBatch * kSub + u);
                 const bool good = place != kNoPage;
-                bad = (bad & ~(1u << (slot * kSub + u))) | (good ? 0u : 1u << (slot * kSub + u));
-                place = good ? place : 0;
+                if (!good) bad |= 1u << (slot * kSub + u), place = 0;
                 const uint8_t *ks = a.ck + static_cast<int64_t>(place) * kPiece + lane * 16;
                 const uint8_t *vs = a.cv + static_cast<int64_t>(place) * kPiece + lane * 16;
+                // chunk lane + 32 i of the piece; the offsets repeat after kTurns copies of 512 bytes
+                if (inside && good) {
 #pragma unroll
-                for (int i = 0; i < 16 * kChunks / 32; ++i) {
-                    const int r = (lane + 32 * i) / kChunks, c = lane % kChunks;
-                    const int key = key0 + u * 16 + r;
-                    const bool seen = good && (inside || (key < sp.len && key >= sp.start));
-                    const uint32_t d = dst + tile_at<kRow>(u * 16 + r, c);
-                    cp_async16(d, ks + i * 512, seen);
-                    cp_async16(d + kTileBytes, vs + i * 512, seen);
+                    for (int i = 0; i < 16 * kChunks / 32; ++i) {
+                        const uint32_t d = copy_at[i % kTurns] + to + u * kPiece + i / kTurns * (kTurns * 512);
+                        cp_async16(d, ks + i * 512);
+                        cp_async16(d + kTileBytes, vs + i * 512);
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 16 * kChunks / 32; ++i) {
+                        const uint32_t d = copy_at[i % kTurns] + to + u * kPiece + i / kTurns * (kTurns * 512);
+                        const int key = key0 + u * 16 + (lane + 32 * i) / kChunks;
+                        const bool seen = good && key < sp.len && key >= sp.start;
+                        cp_async16(d, ks + i * 512, seen);
+                        cp_async16(d + kTileBytes, vs + i * 512, seen);
+                    }
                 }
                 if constexpr (kE4m3)
                     if (lane < 2)
-                        cp_async16(dst + 2 * kTileBytes + lane * kTile + u * 16,
+                        cp_async16(ring + to + 2 * kTileBytes + lane * kTile + u * 16,
                                    (lane ? a.cv_scale : a.ck_scale) + static_cast<int64_t>(place) * 16, good);
             }
         };
-#pragma unroll
-        for (int j = 0; j < kDepth - 1; ++j) {
-            load(j);
+        // one tile: the copy of the next one is started, then this one is waited for and used
+        auto step = [&](int j, const int slot) {
+            load(j + 1, slot ^ 1);
             cp_commit();
-        }
-        for (int j = 0; j < n; ++j) {
-            load(j + kDepth - 1);
-            cp_commit();
-            cp_wait<kDepth - 1>();
+            cp_wait<1>();
             __syncwarp();
-            const int key0 = key_first + j * kBlock, slot = j % kDepth;
+            const int key0 = key_first + j * kBlock;
             if (key0 < sp.len && key0 + kTile > sp.start) {
-                const uint32_t kt = ring + slot * kStage, vt = kt + kTileBytes;
-                const uint8_t *vp = ring_ptr + slot * kStage + kTileBytes, *scales = vp + kTileBytes;
-                // K: matrices of 8 keys x 16 bytes, two chunks for keys 0..7, then for keys 8..15 of a piece
+                const uint32_t to = slot * kStage;
+                const uint8_t *vp = ring_ptr + to + kTileBytes, *scales = vp + kTileBytes;
+                // 8 keys x 16 bytes per matrix: a chunk pair for keys 0..7, then for keys 8..15 of a piece
+                auto pair_at = [&](int u, int k) { return load_at[k % kPairs] + to + u * kPiece + k / kPairs * 128; };
                 float s[2 * kSub][4] = {};
 #pragma unroll
                 for (int k = 0; k < kSteps; ++k)
 #pragma unroll
                     for (int u = 0; u < kSub; ++u) {
                         uint32_t r[4];
-                        ldsm4(r, kt + tile_at<kRow>(u * 16 + lane % 8 + lane / 16 * 8, 2 * k + lane / 8 % 2));
+                        ldsm4(r, pair_at(u, k));
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
                             float(&d)[4] = s[2 * u + i];
@@ -452,7 +469,7 @@ __global__ void __launch_bounds__(kThreads, kCtasOf<kPack>) attention_kernel(con
 #pragma unroll
                         for (int u = 0; u < kSub; ++u) {
                             uint32_t r[4];
-                            ldsm4(r, kt + tile_at<kRow>(u * 16 + lane % 8 + lane / 16 * 8, 2 * k + lane / 8 % 2));
+                            ldsm4(r, pair_at(u, k));
 #pragma unroll
                             for (int i = 0; i < 2; ++i)
                                 mma_e4m3(s2[2 * u + i], qa[1][k][0], qa[1][k][1], qa[1][k][2], qa[1][k][3], r[2 * i],
@@ -588,7 +605,7 @@ __global__ void __launch_bounds__(kThreads, kCtasOf<kPack>) attention_kernel(con
 #pragma unroll
                         for (int c = 0; c < kRowTiles; ++c) {
                             uint32_t v[4];
-                            ldsm4_trans(v, vt + tile_at<kRow>(u * 16 + lane % 8 + lane / 16 * 8, 2 * c + lane / 8 % 2));
+                            ldsm4_trans(v, pair_at(u, c) + kTileBytes);
 #pragma unroll
                             for (int h = 0; h < kHalves; ++h) {
                                 mma16<false>(o[c][h], v[0], v[1], v[2], v[3], p[h][0], p[h][1]);
@@ -598,7 +615,14 @@ __global__ void __launch_bounds__(kThreads, kCtasOf<kPack>) attention_kernel(con
                     }
                 }
             }
+            bad &= ~(((1u << kSub) - 1) << slot * kSub);
             __syncwarp();  // the slot may be refilled
+        };
+        load(0, 0);
+        cp_commit();
+        for (int j = 0; j < n; j += 2) {
+            step(j, 0);
+            if (j + 1 < n) step(j + 1, 1);
         }
         cp_wait<0>();
         __syncthreads();
@@ -738,13 +762,13 @@ __global__ void __launch_bounds__(kThreads, kCtasOf<kPack>) attention_kernel(con
 }
 
 template <int kDim, bool kE4m3, bool kPack>
-cudaError_t launch_typed(const AttnArgs &a, int num_sms, cudaStream_t stream) {
+cudaError_t launch_typed(const AttnArgs &a, const DevCtx &ctx, cudaStream_t stream) {
     constexpr int smem_size = smem_bytes<kDim, kE4m3>();
-    auto kernel = attention_kernel<kDim, kE4m3, kPack>;
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_size);
+    constexpr auto kernel = attention_kernel<kDim, kE4m3, kPack>;
+    const cudaError_t e = allow_smem<kernel>(smem_size, ctx.device);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(num_sms * kCtasOf<kPack>));
+    cfg.gridDim = dim3(static_cast<unsigned>(ctx.num_sms * kCtasOf<kPack>));
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = smem_size;
     cfg.stream = stream;
@@ -800,11 +824,11 @@ cudaError_t launch_attention(const bd_kv_cache &c, const void *q, int32_t q_head
     a.scale_log2 = scale * 1.44269504088896f;
     const bool e = c.kv_type == BD_KV_E4M3, pack = a.group <= 8;
     if (c.head_dim == 128) {
-        if (e) return pack ? launch_typed<128, true, true>(a, ctx.num_sms, stream) : launch_typed<128, true, false>(a, ctx.num_sms, stream);
-        return pack ? launch_typed<128, false, true>(a, ctx.num_sms, stream) : launch_typed<128, false, false>(a, ctx.num_sms, stream);
+        if (e) return pack ? launch_typed<128, true, true>(a, ctx, stream) : launch_typed<128, true, false>(a, ctx, stream);
+        return pack ? launch_typed<128, false, true>(a, ctx, stream) : launch_typed<128, false, false>(a, ctx, stream);
     }
-    if (e) return pack ? launch_typed<64, true, true>(a, ctx.num_sms, stream) : launch_typed<64, true, false>(a, ctx.num_sms, stream);
-    return pack ? launch_typed<64, false, true>(a, ctx.num_sms, stream) : launch_typed<64, false, false>(a, ctx.num_sms, stream);
+    if (e) return pack ? launch_typed<64, true, true>(a, ctx, stream) : launch_typed<64, true, false>(a, ctx, stream);
+    return pack ? launch_typed<64, false, true>(a, ctx, stream) : launch_typed<64, false, false>(a, ctx, stream);
 }
 
 }  // namespace bd

@@ -7,6 +7,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "bitdelta.h"
 
 namespace bd {
@@ -199,6 +201,18 @@ size_t grouped_workspace_size(int64_t m, int32_t n_variants, int64_t n_out, int6
 cudaError_t launch_grouped(const void *x, const int32_t *ids, int64_t m, const void *w_base,
                            const GroupedVariants &vars, int64_t n_out, int64_t n_in, void *y, void *ws,
                            size_t ws_bytes, const DevCtx &ctx, cudaStream_t stream);
+
+// Raises a kernel's dynamic shared memory limit once per device.
+template <auto kKernel>
+cudaError_t allow_smem(int bytes, int device) {
+    static std::atomic<uint64_t> done[2] = {};
+    std::atomic<uint64_t> &word = done[device / 64 % 2];
+    const uint64_t bit = uint64_t{1} << device % 64;
+    if (word.load(std::memory_order_acquire) & bit) return cudaSuccess;
+    const cudaError_t e = cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) word.fetch_or(bit, std::memory_order_release);
+    return e;
+}
 
 // ---- decode-step operators around the linears (validated arguments, see bitdelta.h) ----
 struct NormProblem {

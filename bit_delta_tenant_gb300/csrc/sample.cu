@@ -36,6 +36,7 @@ constexpr float kPerUnit = 64.f;  // bins per unit of t; the last bin takes ever
 constexpr int kCap = kThreads;    // tokens ordered exactly, one per thread
 constexpr int kIndexBits = 18;    // BD_SAMPLE_MAX_VOCAB = 2^18
 constexpr int kMaxCluster = 8;
+constexpr int kMaxSmem = 227 * 1024;
 constexpr float kFloor = 63.f / 64.f;
 constexpr float kFrac = 4194304.f;  // 2^22
 constexpr float kFixed = 1099511627776.f;  // 2^40
@@ -537,7 +538,8 @@ cudaError_t launch_sample(const void *logits, int32_t logits_type, int64_t m, in
     a.slice_groups = static_cast<int32_t>((groups + size - 1) / size);
     const size_t smem = sizeof(Shared) + static_cast<size_t>(a.slice_groups) * 8 * (f32 ? 4 : 2);
     auto kernel = f32 ? sample_kernel<true> : sample_kernel<false>;
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    const cudaError_t e = f32 ? allow_smem<sample_kernel<true>>(kMaxSmem, ctx.device)
+                              : allow_smem<sample_kernel<false>>(kMaxSmem, ctx.device);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(m * size));
