@@ -130,11 +130,14 @@ __device__ __forceinline__ float ex2(float x) {  // 2^x, 0 for -inf
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
-    return __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
-}
-__device__ __forceinline__ float2 from_e4m3x2(uint32_t two) {
-    return __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(two), __NV_E4M3)));
+// A bf16 pair times `up` as e4m3 bytes, and 16 times what they leave as e4m3 bytes.  In fp16 the
+// scaled values (at most 256, 8 bits) and the differences are exact down to 2^-24.
+__device__ __forceinline__ void split_e4m3(uint32_t pair, float up, uint32_t &hi, uint32_t &lo) {
+    const __half2 x = __floats2half2_rn(bf16lo_to_f32(pair) * up, bf16hi_to_f32(pair) * up);
+    const __nv_fp8x2_storage_t h = __nv_cvt_halfraw2_to_fp8x2(x, __NV_SATFINITE, __NV_E4M3);
+    const __half2 left = __hmul2(__hsub2(x, __half2(__nv_cvt_fp8x2_to_halfraw2(h, __NV_E4M3))), __float2half2_rn(16.f));
+    hi = h;
+    lo = __nv_cvt_halfraw2_to_fp8x2(left, __NV_SATFINITE, __NV_E4M3);
 }
 
 // Byte offset of 16-byte chunk c of row r in a tile of kRow-byte rows: eight rows of one
@@ -341,45 +344,38 @@ __global__ void __launch_bounds__(kThreads, kCtasOf<kPack>) attention_kernel(con
                         qa[0][k][kPack ? i : 2 * i + half] = v;
                     }
             } else {
-                uint2 v[kSteps][2];
-                float top = 0.f;
+                uint32_t v[kSteps][2][2], top2 = 0;
 #pragma unroll
                 for (int k = 0; k < kSteps; ++k)
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {  // columns 32 k + 16 i + 4 t .. + 3
-                        v[k][i] = on ? *reinterpret_cast<const uint2 *>(src + k * 64 + i * 32 + t4 * 8) : make_uint2(0, 0);
-                        top = fmaxf(top, fmaxf(fmaxf(fabsf(bf16lo_to_f32(v[k][i].x)), fabsf(bf16hi_to_f32(v[k][i].x))),
-                                               fmaxf(fabsf(bf16lo_to_f32(v[k][i].y)), fabsf(bf16hi_to_f32(v[k][i].y)))));
+                        const uint2 x = on ? *reinterpret_cast<const uint2 *>(src + k * 64 + i * 32 + t4 * 8) : make_uint2(0, 0);
+                        v[k][i][0] = x.x, v[k][i][1] = x.y;
+                        // magnitudes of bf16 pairs compare as whole numbers, NaN above infinity
+                        top2 = __vmaxu2(top2, __vmaxu2(x.x & 0x7FFF7FFFu, x.y & 0x7FFF7FFFu));
                     }
-                top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
-                top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
-                // 2^e <= top < 2^(e + 1); rows of zeros, next to zero or infinite take e = 0
-                int e = static_cast<int>(__float_as_uint(top) >> 23);
+                top2 = __vmaxu2(top2, __shfl_xor_sync(0xFFFFFFFFu, top2, 1));
+                top2 = __vmaxu2(top2, __shfl_xor_sync(0xFFFFFFFFu, top2, 2));
+                const uint32_t top = max(top2 & 0xFFFFu, top2 >> 16);
+                // 2^(e - 127) <= largest < 2^(e - 126); rows of zeros, next to zero or next to infinity take e = 127
+                int e = static_cast<int>(top >> 7);
                 e = e < 27 || e > 227 ? 127 : e;
-                const float up = __uint_as_float(static_cast<uint32_t>(254 + 7 - e) << 23);  // 2^(7 - e)
-                rscale[half] = a.scale_log2 * __uint_as_float(static_cast<uint32_t>(e - 7) << 23);
+                const float up = __uint_as_float(static_cast<uint32_t>(254 + 7 - e) << 23);  // to [128, 256)
                 // neither infinity nor NaN has an e4m3 form that keeps it through a product: such a head is NaN throughout
-                if (!(top < INFINITY)) rscale[half] = NAN;
-                bool nan = false;
+                rscale[half] = top >= 0x7F80u ? NAN : a.scale_log2 * __uint_as_float(static_cast<uint32_t>(e - 7) << 23);
 #pragma unroll
                 for (int k = 0; k < kSteps; ++k)
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        const float x[4] = {bf16lo_to_f32(v[k][i].x) * up, bf16hi_to_f32(v[k][i].x) * up,
-                                            bf16lo_to_f32(v[k][i].y) * up, bf16hi_to_f32(v[k][i].y) * up};
-                        nan |= x[0] != x[0] || x[1] != x[1] || x[2] != x[2] || x[3] != x[3];
-                        const uint32_t h0 = e4m3x2(x[0], x[1]), h1 = e4m3x2(x[2], x[3]);
-                        const float2 f0 = from_e4m3x2(h0), f1 = from_e4m3x2(h1);
-                        const uint32_t l0 = e4m3x2((x[0] - f0.x) * 16.f, (x[1] - f0.y) * 16.f);
-                        const uint32_t l1 = e4m3x2((x[2] - f1.x) * 16.f, (x[3] - f1.y) * 16.f);
+                        uint32_t hi[2], lo[2];
+#pragma unroll
+                        for (int w = 0; w < 2; ++w) split_e4m3(v[k][i][w], up, hi[w], lo[w]);
                         if constexpr (kPack) {
-                            qa[0][k][2 * i] = h0 | h1 << 16, qa[0][k][2 * i + 1] = l0 | l1 << 16;
+                            qa[0][k][2 * i] = hi[0] | hi[1] << 16, qa[0][k][2 * i + 1] = lo[0] | lo[1] << 16;
                         } else {
-                            qa[0][k][2 * i + half] = h0 | h1 << 16, qa[1][k][2 * i + half] = l0 | l1 << 16;
+                            qa[0][k][2 * i + half] = hi[0] | hi[1] << 16, qa[1][k][2 * i + half] = lo[0] | lo[1] << 16;
                         }
                     }
-                const unsigned who = __ballot_sync(0xFFFFFFFFu, nan);
-                if (who >> (lane & ~3) & 0xFu) rscale[half] = NAN;
             }
         }
 
