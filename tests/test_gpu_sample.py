@@ -50,7 +50,8 @@ DTYPES = [torch.bfloat16, torch.float32]
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
-@pytest.mark.parametrize("vocab", [1, 2, 7, 8, 9, 1000, 1003, 16384, 16385, 32001, 50000, 128256, 262144])
+@pytest.mark.parametrize("vocab", [1, 2, 7, 8, 9, 1000, 1003, 16384, 16385, 32001, 50000, 128256, 131071, 131072,
+                                   200003, 262139, 262144])
 def test_vocabularies_with_mixed_settings(dtype, vocab):
     m = 9
     x, g = logits(m, vocab, vocab, dtype), gumbel(m, vocab, vocab)
