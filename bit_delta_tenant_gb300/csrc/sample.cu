@@ -145,12 +145,17 @@ struct Bins {
     __device__ __forceinline__ uint32_t part(float t, int b) const {
         return b == kBins - 1 ? 0u : __float2uint_rn(fmaxf(ex2((b * width - t) * kLog2e) - (1.f - width), 0.f) * unit);
     }
+    // fp32 from whole numbers: the same on every CTA, 2^-22 of the weight
     __device__ __forceinline__ u64 mass(int b, uint32_t count, u64 parts) const {
         if (b == kBins - 1) return 0;
-        const double w = static_cast<double>(count) * (1.f - width) + static_cast<double>(parts) * (width / 65535.f);
-        return static_cast<u64>(w * (static_cast<double>(ex2(b * width * -kLog2e)) * kFixed));
+        const float w = fmaf(static_cast<float>(parts), width * (1.f / 65535.f), static_cast<float>(count) * (1.f - width));
+        return __float2ull_rn(w * (ex2(b * width * -kLog2e) * kFixed));
     }
 };
+// floor(p * mass) for 0 < p < 1, at least 1: the first token always stays
+__device__ __forceinline__ u64 share_of(float p, u64 mass) {
+    return max(__umul64hi(__float2ull_rz(p * 18446744073709551616.f), mass), u64{1});
+}
 
 template <bool kF32>
 struct Sampler {
@@ -281,15 +286,16 @@ struct Sampler {
     }
     // The cluster's totals of this thread's bin, and the count of each CTA (four 16-bit fields a word).
     __device__ Scan totals(const Bins &bins, const Level &at, u64 (&each)[2]) {
+        uint2 v[kMaxCluster];
+#pragma unroll
+        for (int c = 0; c < kMaxCluster; ++c) v[c] = c < size ? ld_remote(remote(&s.bins[tid], c)) : make_uint2(0, 0);
         uint32_t n = 0;
         u64 parts = 0;
         each[0] = each[1] = 0;
 #pragma unroll
         for (int c = 0; c < kMaxCluster; ++c) {
-            if (c >= size) break;
-            const uint2 v = ld_remote(remote(&s.bins[tid], c));
-            n += v.x, parts += v.y;
-            each[c / 4] |= static_cast<u64>(v.x) << 16 * (c % 4);
+            n += v[c].x, parts += v[c].y;
+            each[c / 4] |= static_cast<u64>(v[c].x) << 16 * (c % 4);
         }
         return scan(n, bins.mass(at.depth == 0 ? tid : at.bin, n, parts));
     }
@@ -347,8 +353,7 @@ struct Sampler {
             const int last = static_cast<int>(min(need, static_cast<u64>(n))) - 1;
             if (tid == last) s.kept_mass = c.mass_upto;
             __syncthreads();
-            const double target = static_cast<double>(share) * static_cast<double>(s.kept_mass);
-            keep = keep && (tid == 0 || static_cast<double>(lighter) < target);
+            keep = keep && lighter < share_of(share, s.kept_mass);
         }
         const int kept = __syncthreads_count(keep);  // they are the first ones
         if (half == 0 && i < n && before == kept - 1) s.threshold = mine;
@@ -542,25 +547,34 @@ __device__ void Sampler<kF32>::run(int64_t r) {
         }
     };
     if (!filtered) {  // every token, or those of min-p
-        for (int i = tid; i < units; i += kThreads) {
-            const int64_t e = (u0 + i) * kPer;
-            float x[kPer], noise[kPer] = {};
-            unpack(data[i], x);
-            const bool whole = low == 0.f && e >= e0 && e + kPer <= e1;
-            if (!greedy && whole) {
+        constexpr int kBatch = kF32 ? 4 : 2;  // 16 noise values in flight per thread
+        for (int i0 = tid; i0 < units; i0 += kBatch * kThreads) {
+            float noise[kBatch][kPer];
+            bool whole[kBatch];
+#pragma unroll
+            for (int q = 0; q < kBatch; ++q) {
+                const int64_t e = (u0 + i0 + q * kThreads) * kPer;
+                whole[q] = !greedy && low == 0.f && i0 + q * kThreads < units && e >= e0 && e + kPer <= e1;
 #pragma unroll
                 for (int j = 0; j < kPer; j += 4) {
-                    const float4 v = *reinterpret_cast<const float4 *>(a.noise + e + j);
-                    noise[j] = v.x, noise[j + 1] = v.y, noise[j + 2] = v.z, noise[j + 3] = v.w;
+                    const float4 v = whole[q] ? *reinterpret_cast<const float4 *>(a.noise + e + j) : make_float4(0.f, 0.f, 0.f, 0.f);
+                    noise[q][j] = v.x, noise[q][j + 1] = v.y, noise[q][j + 2] = v.z, noise[q][j + 3] = v.w;
                 }
             }
 #pragma unroll
-            for (int j = 0; j < kPer; ++j) {
-                if (x[j] == -INFINITY) continue;
-                const float t = row.t_of(x[j]);
-                if (low > 0.f && expf(-t) < low) continue;
-                if (!greedy && !whole) noise[j] = a.noise[e + j];
-                offer(t, noise[j], static_cast<int>(e - e0) + j);
+            for (int q = 0; q < kBatch; ++q) {
+                const int i = i0 + q * kThreads;
+                if (i >= units) break;
+                const int first = base + i * kPer;
+                float x[kPer];
+                unpack(data[i], x);
+#pragma unroll
+                for (int j = 0; j < kPer; ++j) {
+                    if (x[j] == -INFINITY) continue;
+                    const float t = row.t_of(x[j]);
+                    if (low > 0.f && expf(-t) < low) continue;
+                    offer(t, greedy || whole[q] ? noise[q][j] : a.noise[e0 + first + j], first + j);
+                }
             }
         }
         answer_of_all();
@@ -586,32 +600,32 @@ __device__ void Sampler<kF32>::run(int64_t r) {
     }
     if (tid == 0) s.maybe_n = 0;
     __syncthreads();
-    for (int i0 = 0; i0 < units; i0 += kThreads) {
-        const int i = i0 + tid;
+    constexpr int kRound = 32 / kPer;  // units whose tokens are one mask of 32 bits
+    for (int i0 = 0; i0 < units; i0 += kRound * kThreads) {
         uint32_t mask = 0;
-        if (i < units) {
+#pragma unroll
+        for (int q = 0; q < kRound; ++q) {
+            const int i = i0 + q * kThreads + tid;
+            if (i >= units) break;
             float x[kPer];
             unpack(data[i], x);
 #pragma unroll
-            for (int j = 0; j < kPer; ++j) mask |= (x[j] >= reach && x[j] > -INFINITY ? 1u : 0u) << j;
+            for (int j = 0; j < kPer; ++j) mask |= (x[j] >= reach ? 1u : 0u) << (q * kPer + j);
         }
-        if (!__any_sync(0xFFFFFFFFu, mask != 0)) continue;
-        const int n = __popc(mask);
-        int place = n;
+        int place = __popc(mask);
+        const int n = place;
 #pragma unroll
         for (int o = 1; o < 32; o *= 2) {
             const int v = __shfl_up_sync(0xFFFFFFFFu, place, o);
             if (lane >= o) place += v;
         }
         uint32_t first = 0;
-        if (lane == 31) first = atomicAdd(&s.maybe_n, static_cast<uint32_t>(place));
+        if (lane == 31 && place > 0) first = atomicAdd(&s.maybe_n, static_cast<uint32_t>(place));
         place += static_cast<int>(__shfl_sync(0xFFFFFFFFu, first, 31)) - n;
-#pragma unroll
-        for (int j = 0; j < kPer; ++j)
-            if (mask >> j & 1) {
-                if (place < kMaybe) s.maybe[place] = static_cast<uint16_t>(i * kPer + j);
-                ++place;
-            }
+        for (; mask && place < kMaybe; mask &= mask - 1) {
+            const int bit = __ffs(mask) - 1;
+            s.maybe[place++] = static_cast<uint16_t>((i0 + bit / kPer * kThreads + tid) * kPer + bit % kPer);
+        }
     }
     __syncthreads();
     some = s.maybe_n <= kMaybe;
@@ -647,7 +661,7 @@ __device__ void Sampler<kF32>::run(int64_t r) {
         u64 kept;
         threshold = refine(bins, d, false, need, here, each[0], each[1], ~0ull, false, &kept);
         if (p < 1.f) {  // the share p of what is kept: it ends in a bin before d, or in what is kept of d
-            const u64 target = max(static_cast<u64>(static_cast<double>(p) * static_cast<double>(before_mass + kept)), u64{1});
+            const u64 target = share_of(p, before_mass + kept);
             cluster_sync_all();  // nobody reads the list any more
             if (target <= before_mass) {
                 const int d2 = find(c, true, target);
@@ -657,8 +671,7 @@ __device__ void Sampler<kF32>::run(int64_t r) {
             }
         }
     } else {
-        const double all = pruned ? static_cast<double>(weight) * kFixed : static_cast<double>(c.mass_all);
-        const u64 need = max(static_cast<u64>(static_cast<double>(p) * all), u64{1});
+        const u64 need = share_of(p, pruned ? __float2ull_rn(weight * kFixed) : c.mass_all);
         const int d = find(c, true, need);
         u64 kept;
         threshold = refine(bins, d, true, need - min(s.before_mass, need - 1), s.here, each[0], each[1], ~0ull, false, &kept);
