@@ -4,20 +4,24 @@
 //   z_i = (x_i - M) / T,  w_i = exp(z_i),  id = argmax over kept of z_i + g_i
 //
 // Bound: HBM for many rows (the logits once, the noise at kept tokens), latency
-// for one.  A row belongs to a cluster of CTAs, each with a slice of it in shared
-// memory, so global memory is read once but for noise.  The passes are short
-// loops: the same steps unrolled over registers were bound by fetching their code.
+// for one.  A row belongs to a cluster of CTAs with a slice of it each.  A slice is
+// read twice, the second time out of L2: holding it in shared memory between left
+// room for two CTAs per SM only, and a row is a chain of short steps with cluster
+// barriers between them that other rows' CTAs have to fill.  The passes are short
+// loops: unrolled over a row in registers they were bound by fetching their code.
 //
-// The filters are a threshold in the order (x descending, index ascending), found
-// without sorting:
+// The first pass takes the largest logit and the sum of weights relative to it, the
+// second one draws from an unfiltered row, or packs the tokens that a filter may keep
+// into shared memory.  The filters are a threshold in the order (x descending, index
+// ascending), found without sorting:
 //  1. Tokens that cannot be kept are left out.  top-k: every warp of the cluster has
 //     j = ceil(k / warps) threads whose largest logit reaches the warp's j-th largest, so
 //     k tokens reach the smallest of these.  top-p: tokens with t = -z above
 //     ln(V / ((1 - p) sum w)) weigh less than (1 - p) sum w together, so the prefix
 //     ends before them.
-//  2. A histogram over t, one bin per thread, holds each bin's count and weight.  Every
-//     CTA adds up the cluster's bins and scans them, and finds the bin that the k-th
-//     token or the share p falls into.
+//  2. A histogram over t holds each bin's count and weight.  Every CTA adds up the
+//     cluster's bins and scans them, and finds the bin that the k-th token or the share p
+//     falls into.
 //  3. The tokens of that bin (all bins up to it, if those are few: top-k as used) are
 //     sent to every CTA and ordered exactly.  A bin with too many tokens is split again,
 //     by the remaining bits of t, then by the bits of (x, index), which differ for any two.
@@ -34,16 +38,12 @@
 namespace bd {
 namespace {
 
-constexpr int kThreads = 512;
-constexpr int kWarps = kThreads / 32;
-constexpr int kBins = kThreads;
-constexpr int kBits = 9;            // a digit: one bin
-constexpr int kCap = 256;           // tokens ordered exactly
-constexpr int kMaybe = 2048;        // places of tokens that may be kept; with more of them passes go over the slice
-constexpr int kIndexBits = 18;      // BD_SAMPLE_MAX_VOCAB = 2^18
+constexpr int kBins = 512;
+constexpr int kBits = 9;          // a digit: one bin
+constexpr int kCap = 512;         // tokens ordered exactly
+constexpr int kIndexBits = 18;    // BD_SAMPLE_MAX_VOCAB = 2^18
 constexpr int kMaxCluster = 8;
-constexpr int kMaxSmem = 160 * 1024;  // a slice of 32768 fp32 logits and the rest
-constexpr float kRange = 31.5f;     // weights below exp(-31.5) of the largest count as 0 in a prefix's sum
+constexpr float kRange = 31.5f;   // weights below exp(-31.5) of the largest count as 0 in a prefix's sum
 constexpr float kFixed = 1099511627776.f;  // 2^40
 constexpr float kLog2e = 1.44269504088896f;
 
@@ -57,24 +57,26 @@ struct SampleArgs {
     float *logprob;
     int64_t m;
     int32_t vocab, slice_units;  // 16-byte units of logits in a CTA's slice
+    int32_t most;                // tokens that may be kept for which there is room; with more the passes go over the slice
 };
 
 struct alignas(16) Shared {
+    static constexpr int kMaxWarps = 16;
     uint2 bins[kBins];  // count, weight
     u64 list_order[kCap], list_mass[kCap], sorted_mass[kCap];
-    uint16_t maybe[kMaybe];
-    u64 warp_mass[kWarps], warp_parts[2][kWarps];
-    uint32_t warp_count[kWarps];
-    float warp_value[3][kWarps];
+    u64 warp_mass[kMaxWarps], warp_parts[2][kMaxWarps];
+    uint32_t warp_count[kMaxWarps];
+    float warp_value[3][kMaxWarps];
     // written by the cluster's CTAs
-    float rank_top[kMaxCluster], rank_sum[kMaxCluster], rank_low[kMaxCluster];
-    u64 rank_best[kMaxCluster];
+    struct Rank {
+        float top, sum, low;
+        u64 best;
+    } ranks[kMaxCluster];
     // written by one thread for its CTA
     u64 before_mass, kept_mass, threshold;
     uint32_t before_count, here, list_n, maybe_n;
     int found;
 };
-static_assert(sizeof(Shared) % 16 == 0, "the slice of logits behind it is stored in 16-byte units");
 
 // ---- cluster shared memory ----------------------------------------------------------
 __device__ __forceinline__ void cluster_sync_all() {
@@ -111,9 +113,9 @@ __device__ __forceinline__ float ex2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-// Bits that ascend with the value (no NaN, no -0), and back.
+// Bits that ascend with the value (no NaN), and back.
 __device__ __forceinline__ uint32_t ascending(float f) {
-    const uint32_t u = __float_as_uint(f);
+    const uint32_t u = __float_as_uint(f + 0.f);  // -0 to +0
     return u ^ (u >> 31 ? 0xFFFFFFFFu : 0x80000000u);
 }
 __device__ __forceinline__ float value_of(uint32_t a) {
@@ -157,25 +159,33 @@ __device__ __forceinline__ u64 share_of(float p, u64 mass) {
     return max(__umul64hi(__float2ull_rz(p * 18446744073709551616.f), mass), u64{1});
 }
 
-template <bool kF32>
+template <bool kF32, int kThreads>
 struct Sampler {
     static constexpr int kPer = kF32 ? 4 : 8;  // logits of a unit
+    static constexpr int kWarps = kThreads / 32;
+    static constexpr int kMine = kBins / kThreads;  // bins of a thread, neighbours
+    static_assert(kCap == kBins, "a list is scanned as the bins are");
 
     Shared &s;
     const SampleArgs &a;
-    uint8_t *slice;
+    float *maybe_x;      // tokens that may be kept,
+    uint16_t *maybe_at;  // and their places in the slice
     const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32, rank = cluster_rank(), size = cluster_size();
-    int base = 0, units = 0;  // token of the slice's first element, units in the slice
-    int tokens = 0;           // how many tokens the passes of a filter go over
-    bool some = false;        // ... those in s.maybe, or all of the slice
-    float reach = -INFINITY;  // tokens below it are not kept
+    int64_t e0 = 0, e1 = 0, u0 = 0;  // the row's first element and the one after its last, the slice's first unit
+    int base = 0, units = 0;         // token of the slice's first element, units in the slice
+    int whole_from = 0, whole_to = 0;  // units that lie wholly in the row
+    int tokens = 0;                  // how many may be kept
+    float reach = -INFINITY;         // they have at least this logit
     Row row;
 
-    __device__ Sampler(Shared &shared, uint8_t *data, const SampleArgs &args) : s(shared), a(args), slice(data) {}
+    __device__ Sampler(Shared &shared, uint8_t *data, const SampleArgs &args)
+        : s(shared), a(args), maybe_x(reinterpret_cast<float *>(data)), maybe_at(reinterpret_cast<uint16_t *>(data + args.most * 4)) {}
 
-    __device__ __forceinline__ float at(int e) const {
-        if constexpr (kF32) return reinterpret_cast<const float *>(slice)[e];
-        return __uint_as_float(static_cast<uint32_t>(reinterpret_cast<const uint16_t *>(slice)[e]) << 16);
+    // ---- the slice --------------------------------------------------------------------
+    static __device__ __forceinline__ float clean(float x) { return fmaxf(x, -INFINITY); }  // NaN to -inf
+    __device__ __forceinline__ float logit(int64_t e) const {
+        if constexpr (kF32) return clean(__ldg(reinterpret_cast<const float *>(a.logits) + e));
+        return clean(__uint_as_float(static_cast<uint32_t>(__ldg(reinterpret_cast<const uint16_t *>(a.logits) + e)) << 16));
     }
     static __device__ __forceinline__ void unpack(const uint4 &u, float (&x)[kPer]) {
         if constexpr (kF32) {
@@ -184,20 +194,64 @@ struct Sampler {
             x[0] = bf16lo_to_f32(u.x), x[1] = bf16hi_to_f32(u.x), x[2] = bf16lo_to_f32(u.y), x[3] = bf16hi_to_f32(u.y);
             x[4] = bf16lo_to_f32(u.z), x[5] = bf16hi_to_f32(u.z), x[6] = bf16lo_to_f32(u.w), x[7] = bf16hi_to_f32(u.w);
         }
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) x[j] = fmaxf(x[j], -INFINITY);  // NaN to -inf; -0 is told from +0 nowhere but in order_of
     }
-    static __device__ __forceinline__ uint4 pack(const float (&x)[kPer]) {
-        if constexpr (kF32)
-            return make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
-        else
-            return make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
+    __device__ __forceinline__ bool inside(int i) const { return i >= whole_from && i < whole_to; }
+    __device__ __forceinline__ uint4 fetch(int i) const {
+        uint4 v;
+        asm volatile("ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                     : "l"(a.logits + (u0 + i) * 16));
+        return v;
+    }
+    // x of unit i; a unit at a ragged end of the row element by element, -inf outside the row
+    __device__ __forceinline__ void read(int i, bool in, const uint4 &raw, float (&x)[kPer]) const {
+        if (in) {
+            unpack(raw, x);
+        } else {
+            for (int j = 0; j < kPer; ++j) {
+                const int64_t e = (u0 + i) * kPer + j;
+                const float v = e >= e0 && e < e1 ? logit(e) : -INFINITY;
+#pragma unroll
+                for (int q = 0; q < kPer; ++q)
+                    if (q == j) x[q] = v;
+            }
+        }
+    }
+    // f(i, x) for this thread's units of the slice, kAtOnce loads in flight
+    template <int kAtOnce, class F>
+    __device__ __forceinline__ void each_unit(F f) const {
+        for (int i0 = tid; i0 < units; i0 += kAtOnce * kThreads) {
+            uint4 raw[kAtOnce];
+            bool in[kAtOnce];
+#pragma unroll
+            for (int q = 0; q < kAtOnce; ++q) {
+                in[q] = inside(i0 + q * kThreads);
+                raw[q] = in[q] ? fetch(i0 + q * kThreads) : make_uint4(0, 0, 0, 0);
+            }
+#pragma unroll
+            for (int q = 0; q < kAtOnce; ++q) {
+                const int i = i0 + q * kThreads;
+                if (i >= units) break;
+                float x[kPer];
+                read(i, in[q], raw[q], x);
+                f(i, x);
+            }
+        }
     }
     // f(x, token) for this thread's share of the tokens that may be kept
     template <class F>
     __device__ __forceinline__ void each_token(F f) const {
-        for (int i = tid; i < tokens; i += kThreads) {
-            const int e = some ? s.maybe[i] : i;
-            const float x = at(e);
-            if (x >= reach && x > -INFINITY) f(x, base + e);
+        if (tokens <= a.most) {
+            for (int i = tid; i < tokens; i += kThreads) f(maybe_x[i], base + maybe_at[i]);
+        } else {
+            for (int i = tid; i < units * kPer; i += kThreads) {
+                const int64_t e = u0 * kPer + i;
+                if (e < e0 || e >= e1) continue;
+                const float x = logit(e);
+                if (x >= reach && x > -INFINITY) f(x, base + i);
+            }
         }
     }
 
@@ -216,48 +270,62 @@ struct Sampler {
         return r;
     }
 
-    // Counts and weights of the bins up to each thread's one.
+    // ---- bins -------------------------------------------------------------------------
+    // Counts and weights of a thread's places (bins, or tokens of a list) and of all up to each.
     struct Scan {
-        uint32_t count, count_upto, count_all;
-        u64 mass, mass_upto, mass_all;
+        uint32_t count[kMine], count_upto[kMine], count_all;
+        u64 mass[kMine], mass_upto[kMine], mass_all;
     };
-    __device__ __forceinline__ Scan scan(uint32_t count, u64 mass) {
-        Scan r = {count, count, 0, mass, mass, 0};
+    __device__ __forceinline__ void scan(Scan &r) {
+        uint32_t n = 0;
+        u64 w = 0;
+#pragma unroll
+        for (int i = 0; i < kMine; ++i) {
+            n += r.count[i], w += r.mass[i];
+            r.count_upto[i] = n, r.mass_upto[i] = w;
+        }
+        uint32_t n_in = n;
+        u64 w_in = w;
 #pragma unroll
         for (int o = 1; o < 32; o *= 2) {
-            const uint32_t n = __shfl_up_sync(0xFFFFFFFFu, r.count_upto, o);
-            const u64 w = __shfl_up_sync(0xFFFFFFFFu, r.mass_upto, o);
-            if (lane >= o) r.count_upto += n, r.mass_upto += w;
+            const uint32_t u = __shfl_up_sync(0xFFFFFFFFu, n_in, o);
+            const u64 v = __shfl_up_sync(0xFFFFFFFFu, w_in, o);
+            if (lane >= o) n_in += u, w_in += v;
         }
         __syncthreads();
-        if (lane == 31) s.warp_count[warp] = r.count_upto, s.warp_mass[warp] = r.mass_upto;
+        if (lane == 31) s.warp_count[warp] = n_in, s.warp_mass[warp] = w_in;
         __syncthreads();
+        n_in -= n, w_in -= w;
+        r.count_all = 0, r.mass_all = 0;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-            const uint32_t n = s.warp_count[w];
-            const u64 m = s.warp_mass[w];
-            if (w < warp) r.count_upto += n, r.mass_upto += m;
-            r.count_all += n, r.mass_all += m;
+        for (int q = 0; q < kWarps; ++q) {
+            const uint32_t u = s.warp_count[q];
+            const u64 v = s.warp_mass[q];
+            if (q < warp) n_in += u, w_in += v;
+            r.count_all += u, r.mass_all += v;
         }
-        return r;
+#pragma unroll
+        for (int i = 0; i < kMine; ++i) r.count_upto[i] += n_in, r.mass_upto[i] += w_in;
     }
     // The first bin at which the count or the weight reaches `need`, what precedes it in s.before_*, its own
     // count in s.here.  Where rounding leaves the sum of all bins short, the last bin that holds a token.
     __device__ __forceinline__ int find(const Scan &c, bool by_mass, u64 need) {
-        const u64 all = by_mass ? c.mass_all : c.count_all;
-        bool here;
-        if (all >= need) {
-            here = by_mass ? c.mass_upto >= need && c.mass_upto - c.mass < need : c.count_upto >= need && c.count_upto - c.count < need;
-        } else {
-            here = c.count > 0 && c.count_upto == c.count_all;
-        }
+        const bool reached = (by_mass ? c.mass_all : c.count_all) >= need;
         __syncthreads();
-        if (here) s.found = tid, s.before_count = c.count_upto - c.count, s.before_mass = c.mass_upto - c.mass, s.here = c.count;
+#pragma unroll
+        for (int i = 0; i < kMine; ++i) {
+            const uint32_t n = c.count_upto[i] - c.count[i];
+            const u64 w = c.mass_upto[i] - c.mass[i];
+            bool here;
+            if (!reached) here = c.count[i] > 0 && c.count_upto[i] == c.count_all;
+            else here = by_mass ? c.mass_upto[i] >= need && w < need : c.count_upto[i] >= need && n < need;
+            if (here) s.found = tid * kMine + i, s.before_count = n, s.before_mass = w, s.here = c.count[i];
+        }
         __syncthreads();
         return s.found;
     }
 
-    // This CTA's tokens with order <= limit in the set chosen so far, one histogram digit each.
+    // The set of tokens chosen so far, of which a histogram tells one digit.
     struct Level {
         int depth, bin, sub, shift;
         u64 prefix;
@@ -272,7 +340,8 @@ struct Sampler {
         return static_cast<int>(o >> at.shift) & (kBins - 1);
     }
     __device__ void histogram(const Bins &bins, const Level &at, u64 limit) {
-        s.bins[tid] = make_uint2(0, 0);
+#pragma unroll
+        for (int i = 0; i < kMine; ++i) s.bins[tid + i * kThreads] = make_uint2(0, 0);
         __syncthreads();
         each_token([&](float x, int i) {
             const float t = row.t_of(x);
@@ -284,35 +353,47 @@ struct Sampler {
             atomicAdd(&s.bins[d].y, bins.part(t, at.depth == 0 ? d : at.bin));
         });
     }
-    // The cluster's totals of this thread's bin, and the count of each CTA (four 16-bit fields a word).
-    __device__ Scan totals(const Bins &bins, const Level &at, u64 (&each)[2]) {
-        uint2 v[kMaxCluster];
+    // The cluster's totals of this thread's bins, and each CTA's counts in them (four 16-bit fields a word).
+    struct Each {
+        u64 lo[kMine], hi[kMine];
+    };
+    __device__ __forceinline__ void totals(const Bins &bins, const Level &at, Scan &c, Each &each) {
 #pragma unroll
-        for (int c = 0; c < kMaxCluster; ++c) v[c] = c < size ? ld_remote(remote(&s.bins[tid], c)) : make_uint2(0, 0);
-        uint32_t n = 0;
-        u64 parts = 0;
-        each[0] = each[1] = 0;
+        for (int i = 0; i < kMine; ++i) {
+            const int d = tid * kMine + i;
+            uint2 v[kMaxCluster];
 #pragma unroll
-        for (int c = 0; c < kMaxCluster; ++c) {
-            n += v[c].x, parts += v[c].y;
-            each[c / 4] |= static_cast<u64>(v[c].x) << 16 * (c % 4);
+            for (int q = 0; q < kMaxCluster; ++q) v[q] = q < size ? ld_remote(remote(&s.bins[d], q)) : make_uint2(0, 0);
+            uint32_t n = 0;
+            u64 parts = 0;
+            each.lo[i] = each.hi[i] = 0;
+#pragma unroll
+            for (int q = 0; q < kMaxCluster; ++q) {
+                n += v[q].x, parts += v[q].y;
+                (q < 4 ? each.lo[i] : each.hi[i]) |= static_cast<u64>(v[q].x) << 16 * (q % 4);
+            }
+            c.count[i] = n;
+            c.mass[i] = bins.mass(at.depth == 0 ? d : at.bin, n, parts);
         }
-        return scan(n, bins.mass(at.depth == 0 ? tid : at.bin, n, parts));
+        scan(c);
     }
-    // Sends this CTA's tokens of one set to every CTA's list.  `upto`: all bins up to at.bin, else the set of
-    // digit d at level `at`.  The places follow from the counts that every CTA has of every other.
-    __device__ void gather(const Bins &bins, const Level &at, int d, bool upto, u64 limit, const u64 (&each)[2]) {
-        const bool mine = upto ? tid <= d : tid == d;
-        u64 e0 = mine ? each[0] : 0, e1 = mine ? each[1] : 0;
+    // Sends this CTA's tokens of one set to every CTA's list: digit d at level `at`, or with `upto` all bins up to d.
+    // The places follow from the counts that every CTA has of every other.
+    __device__ void gather(const Bins &bins, const Level &at, int d, bool upto, u64 limit, const Each &each) {
+        u64 lo = 0, hi = 0;
 #pragma unroll
-        for (int o = 16; o > 0; o /= 2) e0 += __shfl_xor_sync(0xFFFFFFFFu, e0, o), e1 += __shfl_xor_sync(0xFFFFFFFFu, e1, o);
-        if (lane == 0) s.warp_parts[0][warp] = e0, s.warp_parts[1][warp] = e1;
+        for (int i = 0; i < kMine; ++i)
+            if (upto ? tid * kMine + i <= d : tid * kMine + i == d) lo += each.lo[i], hi += each.hi[i];
+#pragma unroll
+        for (int o = 16; o > 0; o /= 2) lo += __shfl_xor_sync(0xFFFFFFFFu, lo, o), hi += __shfl_xor_sync(0xFFFFFFFFu, hi, o);
+        if (lane == 0) s.warp_parts[0][warp] = lo, s.warp_parts[1][warp] = hi;
         if (tid == 0) s.list_n = 0;
         __syncthreads();
-        e0 = e1 = 0;
-        for (int w = 0; w < kWarps; ++w) e0 += s.warp_parts[0][w], e1 += s.warp_parts[1][w];
+        lo = hi = 0;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) lo += s.warp_parts[0][w], hi += s.warp_parts[1][w];
         uint32_t first = 0;
-        for (int c = 0; c < rank; ++c) first += static_cast<uint32_t>((c < 4 ? e0 : e1) >> 16 * (c % 4)) & 0xFFFFu;
+        for (int c = 0; c < rank; ++c) first += static_cast<uint32_t>((c < 4 ? lo : hi) >> 16 * (c % 4)) & 0xFFFFu;
         each_token([&](float x, int i) {
             const float t = row.t_of(x);
             const u64 o = order_of(x, i);
@@ -330,43 +411,67 @@ struct Sampler {
     // `need`; with share < 1, of the first `need` those before which less than that share of their weight lies.  The
     // last kept token's order and the kept weight go to s.threshold and s.kept_mass.
     __device__ void cut(uint32_t n, bool by_mass, u64 need, float share) {
-        if (tid >= n && tid < kCap) s.list_order[tid] = ~0ull, s.list_mass[tid] = 0;
+        for (int i = n + tid; i < kCap; i += kThreads) s.list_order[i] = ~0ull, s.list_mass[i] = 0, s.sorted_mass[i] = 0;
         __syncthreads();
-        // rank by counting, two threads a token, each over half of the list
-        const int i = tid / 2, half = tid % 2;
-        const u64 mine = s.list_order[i];
-        uint32_t before = 0;
-        const uint32_t end = (n + 1) / 2;  // pairs
-        for (uint32_t j = half; j < end; j += 2) {
-            const ulonglong2 two = *reinterpret_cast<const ulonglong2 *>(&s.list_order[2 * j]);
-            before += (two.x < mine) + (two.y < mine);
+        // ranks by counting, as many threads to a token as the list leaves
+        const int lanes = n * 8 <= kThreads ? 8 : n * 4 <= kThreads ? 4 : n * 2 <= kThreads ? 2 : 1;
+        const uint32_t pairs = (n + 1) / 2;
+        uint32_t ranks[kCap / kThreads];
+#pragma unroll
+        for (int q = 0; q < kCap / kThreads; ++q) {
+            const int i = (tid + q * kThreads) / lanes, part = tid % lanes;
+            const u64 mine = s.list_order[i];
+            uint32_t before = 0;
+            if (q == 0 || tid + q * kThreads < n)
+                for (uint32_t j = part; j < pairs; j += lanes) {
+                    const ulonglong2 two = *reinterpret_cast<const ulonglong2 *>(&s.list_order[2 * j]);
+                    before += (two.x < mine) + (two.y < mine);
+                }
+            if (lanes > 1) before += __shfl_xor_sync(0xFFFFFFFFu, before, 1);
+            if (lanes > 2) before += __shfl_xor_sync(0xFFFFFFFFu, before, 2);
+            if (lanes > 4) before += __shfl_xor_sync(0xFFFFFFFFu, before, 4);
+            const bool on = i < n && part == 0 && (q == 0 || lanes == 1);
+            ranks[q] = on ? before : kCap;
+            if (on) s.sorted_mass[before] = s.list_mass[i];
         }
-        before += __shfl_xor_sync(0xFFFFFFFFu, before, 1);
-        if (half == 0 && i < n) s.sorted_mass[before] = s.list_mass[i];
         __syncthreads();
-        // weights in that order, one thread a place
-        const u64 w = tid < n ? s.sorted_mass[tid] : 0;
-        const Scan c = scan(tid < n, w);
-        const u64 lighter = c.mass_upto - w;
-        bool keep = tid < n && (by_mass ? lighter < need : static_cast<u64>(tid) < need);
+        // weights in that order, neighbouring places to a thread
+        Scan c;
+#pragma unroll
+        for (int i = 0; i < kMine; ++i) c.count[i] = tid * kMine + i < n, c.mass[i] = s.sorted_mass[tid * kMine + i];
+        scan(c);
+        u64 end = need;
         if (share < 1.f) {
-            const int last = static_cast<int>(min(need, static_cast<u64>(n))) - 1;
-            if (tid == last) s.kept_mass = c.mass_upto;
+            const uint32_t last = static_cast<uint32_t>(min(need, static_cast<u64>(n))) - 1;
+#pragma unroll
+            for (int i = 0; i < kMine; ++i)
+                if (tid * kMine + i == last) s.kept_mass = c.mass_upto[i];
             __syncthreads();
-            keep = keep && lighter < share_of(share, s.kept_mass);
+            end = share_of(share, s.kept_mass);
         }
-        const int kept = __syncthreads_count(keep);  // they are the first ones
-        if (half == 0 && i < n && before == kept - 1) s.threshold = mine;
-        if (tid == kept - 1) s.kept_mass = c.mass_upto;
+        int kept = 0;
+#pragma unroll
+        for (int i = 0; i < kMine; ++i) {
+            const int place = tid * kMine + i;
+            const bool keep = place < n && (by_mass || static_cast<u64>(place) < need) &&
+                              (!(by_mass || share < 1.f) || c.mass_upto[i] - c.mass[i] < end);
+            kept += __syncthreads_count(keep);  // they are the first ones
+        }
+#pragma unroll
+        for (int i = 0; i < kMine; ++i)
+            if (tid * kMine + i == kept - 1) s.kept_mass = c.mass_upto[i];
+#pragma unroll
+        for (int q = 0; q < kCap / kThreads; ++q)
+            if (ranks[q] == kept - 1) s.threshold = s.list_order[(tid + q * kThreads) / lanes];
         __syncthreads();
     }
 
     // The order of the last token to keep of level-0 bin d (`here` tokens, counts by CTA in `each`): its first `need`
     // tokens, or those before which its weight stays below `need`.  `limited`: the bin's counts include tokens
     // beyond `limit`.  *kept receives the weight of the bin's kept tokens.
-    __device__ u64 refine(const Bins &bins, int d, bool by_mass, u64 need, uint32_t here, u64 each0, u64 each1, u64 limit, bool limited, u64 *kept) {
+    __device__ u64 refine(const Bins &bins, int d, bool by_mass, u64 need, uint32_t here, Each each, u64 limit, bool limited,
+                          u64 *kept) {
         Level at = {0, d, 0, 0, 0};
-        u64 each[2] = {each0, each1};
         int digit = d;
         *kept = 0;
         while (here > kCap || limited) {
@@ -378,7 +483,8 @@ struct Sampler {
             cluster_sync_all();  // nobody reads the bins any more
             histogram(bins, at, limit);
             cluster_sync_all();
-            const Scan c = totals(bins, at, each);
+            Scan c;
+            totals(bins, at, c, each);
             digit = find(c, by_mass, need);
             need -= by_mass ? s.before_mass : s.before_count;
             *kept += s.before_mass;
@@ -394,13 +500,15 @@ struct Sampler {
     __device__ void run(int64_t r);
 };
 
-template <bool kF32>
-__device__ void Sampler<kF32>::run(int64_t r) {
+template <bool kF32, int kThreads>
+__device__ void Sampler<kF32, kThreads>::run(int64_t r) {
     // units at multiples of kPer of the whole array: 16-byte aligned logits, and 16-byte aligned noise
-    const int64_t e0 = r * a.vocab, e1 = e0 + a.vocab;
-    const int64_t u0 = e0 / kPer + static_cast<int64_t>(rank) * a.slice_units;
+    e0 = r * a.vocab, e1 = e0 + a.vocab;
+    u0 = e0 / kPer + static_cast<int64_t>(rank) * a.slice_units;
     units = static_cast<int>(max(min(u0 + a.slice_units, (e1 + kPer - 1) / kPer) - u0, int64_t{0}));
     base = static_cast<int>(u0 * kPer - e0);
+    whole_from = base < 0 ? 1 : 0;
+    whole_to = static_cast<int>(min(e1 / kPer - u0, static_cast<int64_t>(units)));
     // settings
     const float temp = a.temperature ? a.temperature[r] : 1.f;
     const int top_k = a.top_k ? a.top_k[r] : 0;
@@ -413,47 +521,32 @@ __device__ void Sampler<kF32>::run(int64_t r) {
     if (!(p > 0.f && p < 1.f) || k == 1) p = 1.f;
     low = low > 0.f ? fminf(low, 1.f) : 0.f;
     const bool filtered = !greedy && (k > 0 || p < 1.f);
-
-    // the slice, eight loads in flight per thread
-    uint4 *data = reinterpret_cast<uint4 *>(slice);
-    float top = -INFINITY;
-    constexpr int kAtOnce = 8;
-    for (int i0 = tid; i0 < units; i0 += kAtOnce * kThreads) {
-        uint4 raw[kAtOnce];
-#pragma unroll
-        for (int q = 0; q < kAtOnce; ++q) {
-            const int i = i0 + q * kThreads;
-            const int64_t e = (u0 + i) * kPer;
-            if (i < units && e >= e0 && e + kPer <= e1) raw[q] = ldg_stream(a.logits + (u0 + i) * 16);
-        }
-#pragma unroll
-        for (int q = 0; q < kAtOnce; ++q) {
-            const int i = i0 + q * kThreads;
-            if (i >= units) break;
-            const int64_t e = (u0 + i) * kPer;
-            float x[kPer];
-            if (e >= e0 && e + kPer <= e1) {
-                unpack(raw[q], x);
-            } else {  // the row's ragged ends, element by element
-                for (int j = 0; j < kPer; ++j) {
-                    float v = -INFINITY;
-                    if (e + j >= e0 && e + j < e1) {
-                        if constexpr (kF32) v = reinterpret_cast<const float *>(a.logits)[e + j];
-                        else v = __uint_as_float(static_cast<uint32_t>(reinterpret_cast<const uint16_t *>(a.logits)[e + j]) << 16);
-                    }
-                    if constexpr (kF32) reinterpret_cast<float *>(slice)[i * kPer + j] = v;
-                    else reinterpret_cast<uint16_t *>(slice)[i * kPer + j] = static_cast<uint16_t>(__float_as_uint(v) >> 16);
-                }
-                unpack(data[i], x);
-            }
-#pragma unroll
-            for (int j = 0; j < kPer; ++j) {
-                x[j] = fmaxf(x[j], -INFINITY) + 0.f;  // NaN to -inf, -0 to +0
-                top = fmaxf(top, x[j]);
-            }
-            data[i] = pack(x);
-        }
+    // noise that will be read whole is on its way into L2 meanwhile
+    if (tid == 0 && !filtered && !greedy && low == 0.f) {
+        const int64_t n = min(static_cast<int64_t>(units), a.m * a.vocab / kPer - u0);
+        if (n > 0)
+            asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(a.noise + u0 * kPer), "r"(static_cast<uint32_t>(n * kPer * 4))
+                         : "memory");
     }
+
+    // First pass: each thread's largest logit and the unit it is first met in, and the sum of its weights relative to
+    // the largest so far, or rather to `shift`, which is that times per rounded: x per - shift is one operation.
+    const float per = row.inv_t * kLog2e;
+    const bool plain = per > 0.f && per < INFINITY;
+    float top = -INFINITY, shift = 0.f, sum = 0.f;
+    int top_unit = 0;
+    each_unit<kF32 ? 8 : 4>([&](int i, const float (&x)[kPer]) {
+        float here = x[0];
+#pragma unroll
+        for (int j = 1; j < kPer; ++j) here = fmaxf(here, x[j]);
+        if (here > top) {
+            const float to = here * per;
+            sum = top > -INFINITY ? sum * ex2(shift - to) : 0.f;
+            top = here, shift = to, top_unit = i;
+        }
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) sum += ex2(fmaf(x[j], per, -shift));
+    });
 
     // This CTA's largest logit, the sum of its weights relative to it, and for top-k its bound: j threads of every
     // warp reach it.
@@ -469,35 +562,31 @@ __device__ void Sampler<kF32>::run(int64_t r) {
         reach = jth > ascending(-INFINITY) ? value_of(jth) : -INFINITY;
         if (lane == 0) s.warp_value[0][warp] = reach;
     }
-    const float cta_top = block_fold<true>(top, s.warp_value[1]);  // (also: the slice is complete)
-    const float per = row.inv_t * kLog2e;
-    float sum = 0.f;
-    if (cta_top < INFINITY && per > 0.f && per < INFINITY && cta_top > -INFINITY) {
-#pragma unroll 2
-        for (int i = tid; i < units; i += kThreads) {
-            float x[kPer];
-            unpack(data[i], x);
-#pragma unroll
-            for (int j = 0; j < kPer; ++j) sum += ex2((x[j] - cta_top) * per);
-        }
-    } else if (cta_top > -INFINITY) {  // a logit or a setting at the end of its range
-        for (int i = tid; i < units * kPer; i += kThreads) {
-            const Row own = {cta_top, row.inv_t};
-            if (at(i) > -INFINITY) sum += ex2(own.t_of(at(i)) * -kLog2e);
+    const float cta_top = block_fold<true>(top, s.warp_value[1]);
+    if (plain && fabsf(cta_top * per) < 32768.f) {
+        // a thread whose largest logit lies beyond the range of its own sum weighs nothing beside that
+        sum = top > -INFINITY && fabsf(shift) < 65536.f ? sum * ex2(fmaf(-cta_top, per, shift)) : 0.f;
+    } else {  // a logit or a setting at the end of its range
+        sum = 0.f;
+        const Row own = {cta_top, row.inv_t};
+        for (int i = tid; i < units * kPer && cta_top > -INFINITY; i += kThreads) {
+            const int64_t e = u0 * kPer + i;
+            const float x = e >= e0 && e < e1 ? logit(e) : -INFINITY;
+            if (x > -INFINITY) sum += ex2(own.t_of(x) * -kLog2e);
         }
     }
     sum = block_fold<false>(sum, s.warp_value[2]);
+    __syncwarp();
     cluster_wait_acquire();  // every CTA of the cluster runs: its shared memory may be written
     if (tid < size) {
         if (filtered && k > 0)
             for (int w = 0; w < kWarps; ++w) reach = fminf(reach, s.warp_value[0][w]);
-        st_remote(remote(&s.rank_top[rank], tid), cta_top);
-        st_remote(remote(&s.rank_sum[rank], tid), sum);
-        st_remote(remote(&s.rank_low[rank], tid), reach);
+        const uint32_t to = remote(&s.ranks[rank], tid);
+        st_remote(to, cta_top), st_remote(to + 4, sum), st_remote(to + 8, reach);
     }
     cluster_sync_all();
-    row.top = s.rank_top[0];
-    for (int c = 1; c < size; ++c) row.top = fmaxf(row.top, s.rank_top[c]);
+    row.top = s.ranks[0].top;
+    for (int c = 1; c < size; ++c) row.top = fmaxf(row.top, s.ranks[c].top);
     if (row.top == -INFINITY) {  // nothing may be drawn; the whole cluster leaves
         if (rank == 0 && tid == 0) {
             a.ids[r] = -1;
@@ -507,15 +596,14 @@ __device__ void Sampler<kF32>::run(int64_t r) {
     }
     float weight = 0.f;
     for (int c = 0; c < size; ++c) {
-        const float v = s.rank_top[c];
-        if (v > -INFINITY) weight = fmaf(s.rank_sum[c], ex2(row.t_of(v) * -kLog2e), weight);
+        const float v = s.ranks[c].top;
+        if (v > -INFINITY) weight = fmaf(s.ranks[c].sum, ex2(row.t_of(v) * -kLog2e), weight);
     }
 
     u64 best = 0;
     auto offer = [&](float t, float noise, int i) {
-        float score = -t;
-        if (!greedy) score = fmaxf(__fadd_rn(score, fmaxf(noise, -INFINITY)), -INFINITY);
-        const u64 c = static_cast<u64>(ascending(score + 0.f)) << 32 | (0xFFFFFFFFu - static_cast<unsigned>(i));
+        const float score = fmaxf(__fadd_rn(-t, fmaxf(noise, -INFINITY)), -INFINITY);
+        const u64 c = static_cast<u64>(ascending(score)) << 32 | (0xFFFFFFFFu - static_cast<unsigned>(i));
         best = c > best ? c : best;
     };
     auto fold_best = [&] {
@@ -531,66 +619,91 @@ __device__ void Sampler<kF32>::run(int64_t r) {
     auto answer = [&] {  // by one thread of the cluster
         const int id = static_cast<int>(0xFFFFFFFFu - static_cast<uint32_t>(best));
         a.ids[r] = id;
-        if (a.logprob == nullptr) return;
-        float v;
-        if constexpr (kF32) v = reinterpret_cast<const float *>(a.logits)[e0 + id];
-        else v = __uint_as_float(static_cast<uint32_t>(reinterpret_cast<const uint16_t *>(a.logits)[e0 + id]) << 16);
-        a.logprob[r] = -row.t_of(v) - logf(weight);
+        if (a.logprob) a.logprob[r] = -row.t_of(logit(e0 + id)) - logf(weight);
     };
     auto answer_of_all = [&] {
         fold_best();
-        if (tid == 0) st_remote(remote(&s.rank_best[rank], 0), best);
+        if (tid == 0) st_remote(remote(&s.ranks[rank].best, 0), best);
         cluster_sync_all();
         if (rank == 0 && tid == 0) {
-            for (int c = 0; c < size; ++c) best = s.rank_best[c] > best ? s.rank_best[c] : best;
+            for (int c = 0; c < size; ++c) best = s.ranks[c].best > best ? s.ranks[c].best : best;
             answer();
         }
     };
-    if (!filtered) {  // every token, or those of min-p
-        constexpr int kBatch = kF32 ? 4 : 2;  // 16 noise values in flight per thread
-        for (int i0 = tid; i0 < units; i0 += kBatch * kThreads) {
-            float noise[kBatch][kPer];
-            bool whole[kBatch];
+    if (greedy) {  // the first pass has met it
+        if (top == row.top) {
+            float x[kPer];
+            read(top_unit, inside(top_unit), inside(top_unit) ? fetch(top_unit) : make_uint4(0, 0, 0, 0), x);
 #pragma unroll
-            for (int q = 0; q < kBatch; ++q) {
-                const int64_t e = (u0 + i0 + q * kThreads) * kPer;
-                whole[q] = !greedy && low == 0.f && i0 + q * kThreads < units && e >= e0 && e + kPer <= e1;
-#pragma unroll
-                for (int j = 0; j < kPer; j += 4) {
-                    const float4 v = whole[q] ? *reinterpret_cast<const float4 *>(a.noise + e + j) : make_float4(0.f, 0.f, 0.f, 0.f);
-                    noise[q][j] = v.x, noise[q][j + 1] = v.y, noise[q][j + 2] = v.z, noise[q][j + 3] = v.w;
-                }
-            }
-#pragma unroll
-            for (int q = 0; q < kBatch; ++q) {
-                const int i = i0 + q * kThreads;
-                if (i >= units) break;
-                const int first = base + i * kPer;
-                float x[kPer];
-                unpack(data[i], x);
-#pragma unroll
-                for (int j = 0; j < kPer; ++j) {
-                    if (x[j] == -INFINITY) continue;
-                    const float t = row.t_of(x[j]);
-                    if (low > 0.f && expf(-t) < low) continue;
-                    offer(t, greedy || whole[q] ? noise[q][j] : a.noise[e0 + first + j], first + j);
-                }
-            }
+            for (int j = kPer - 1; j >= 0; --j)
+                if (x[j] == top) best = 1ull << 32 | (0xFFFFFFFFu - static_cast<unsigned>(base + top_unit * kPer + j));
         }
         answer_of_all();
         return;
     }
+    if (!filtered && low == 0.f && plain && row.top < INFINITY) {  // every token
+        float most = -INFINITY;
+        int first = -1;  // of equal scores the one met first has the lowest index
+        each_unit<kF32 ? 4 : 2>([&](int i, const float (&x)[kPer]) {
+            const float *g = a.noise + (e0 + base) + static_cast<int64_t>(i) * kPer;
+            float noise[kPer];
+            if (inside(i)) {
+#pragma unroll
+                for (int j = 0; j < kPer; j += 4) {
+                    const float4 v = __ldg(reinterpret_cast<const float4 *>(g + j));
+                    noise[j] = v.x, noise[j + 1] = v.y, noise[j + 2] = v.z, noise[j + 3] = v.w;
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < kPer; ++j) noise[j] = x[j] > -INFINITY ? g[j] : 0.f;
+            }
+#pragma unroll
+            for (int j = 0; j < kPer; ++j) {
+                const float score = __fadd_rn(__fmul_rn(__fsub_rn(x[j], row.top), row.inv_t), noise[j]);
+                if (score > most) most = score, first = i * kPer + j;
+            }
+        });
+        if (first >= 0) best = static_cast<u64>(ascending(most)) << 32 | (0xFFFFFFFFu - static_cast<unsigned>(base + first));
+        if (!__syncthreads_or(first >= 0)) {  // a slice whose scores are all -inf (or NaN, which counts as -inf): its first token
+            each_unit<1>([&](int i, const float (&x)[kPer]) {
+#pragma unroll
+                for (int j = 0; j < kPer; ++j)
+                    if (x[j] > -INFINITY) offer(INFINITY, -INFINITY, base + i * kPer + j);
+            });
+        }
+        answer_of_all();
+        return;
+    }
+    if (!filtered) {  // the tokens of min-p, or settings and logits at the end of their range
+        float least = plain && row.top < INFINITY && low > 0.f ? row.top + logf(low) * temp : -INFINITY;
+        least -= fabsf(least) * 1e-6f + temp * 1e-6f;  // below any token that the exact test keeps
+        if (!(least > -INFINITY)) least = -INFINITY;
+        each_unit<kF32 ? 8 : 4>([&](int i, const float (&x)[kPer]) {
+            float here = x[0];
+#pragma unroll
+            for (int j = 1; j < kPer; ++j) here = fmaxf(here, x[j]);
+            if (here < least) return;
+#pragma unroll
+            for (int j = 0; j < kPer; ++j) {
+                if (x[j] == -INFINITY) continue;
+                const float t = row.t_of(x[j]);
+                if (low == 0.f || expf(-t) >= low) offer(t, a.noise[e0 + base + i * kPer + j], base + i * kPer + j);
+            }
+        });
+        answer_of_all();
+        return;
+    }
 
-    // tokens that may be kept: x >= reach, t < range
+    // tokens that may be kept: x >= reach
     float range = kRange;
     bool pruned = false;  // by weight
     if (k > 0) {
-        reach = s.rank_low[0];
-        for (int c = 1; c < size; ++c) reach = fminf(reach, s.rank_low[c]);
+        reach = s.ranks[0].low;
+        for (int c = 1; c < size; ++c) reach = fminf(reach, s.ranks[c].low);
         if (reach > -INFINITY) range = fminf(range, row.t_of(reach) * 1.0001f + 1e-6f);
     } else if (p < 1.f - 1e-5f) {  // a longer prefix is summed over everything, so that it ends by the sum of its own bins
         const float bound = logf(static_cast<float>(a.vocab) / ((1.f - p) * 0.99f * weight));
-        if (bound < kRange && row.top < INFINITY && per > 0.f && per < INFINITY) {
+        if (bound < kRange && row.top < INFINITY && plain) {
             pruned = true;
             range = fmaxf(bound, 1e-3f);
             reach = row.top - range * temp;
@@ -600,43 +713,32 @@ __device__ void Sampler<kF32>::run(int64_t r) {
     }
     if (tid == 0) s.maybe_n = 0;
     __syncthreads();
-    constexpr int kRound = 32 / kPer;  // units whose tokens are one mask of 32 bits
-    for (int i0 = 0; i0 < units; i0 += kRound * kThreads) {
+    each_unit<kF32 ? 8 : 4>([&](int i, const float (&x)[kPer]) {
+        float here = x[0];
+#pragma unroll
+        for (int j = 1; j < kPer; ++j) here = fmaxf(here, x[j]);
+        if (!(here >= reach)) return;
         uint32_t mask = 0;
 #pragma unroll
-        for (int q = 0; q < kRound; ++q) {
-            const int i = i0 + q * kThreads + tid;
-            if (i >= units) break;
-            float x[kPer];
-            unpack(data[i], x);
+        for (int j = 0; j < kPer; ++j) mask |= (x[j] >= reach && x[j] > -INFINITY ? 1u : 0u) << j;
+        uint32_t place = atomicAdd(&s.maybe_n, static_cast<uint32_t>(__popc(mask)));
 #pragma unroll
-            for (int j = 0; j < kPer; ++j) mask |= (x[j] >= reach ? 1u : 0u) << (q * kPer + j);
-        }
-        int place = __popc(mask);
-        const int n = place;
-#pragma unroll
-        for (int o = 1; o < 32; o *= 2) {
-            const int v = __shfl_up_sync(0xFFFFFFFFu, place, o);
-            if (lane >= o) place += v;
-        }
-        uint32_t first = 0;
-        if (lane == 31 && place > 0) first = atomicAdd(&s.maybe_n, static_cast<uint32_t>(place));
-        place += static_cast<int>(__shfl_sync(0xFFFFFFFFu, first, 31)) - n;
-        for (; mask && place < kMaybe; mask &= mask - 1) {
-            const int bit = __ffs(mask) - 1;
-            s.maybe[place++] = static_cast<uint16_t>((i0 + bit / kPer * kThreads + tid) * kPer + bit % kPer);
-        }
-    }
+        for (int j = 0; j < kPer; ++j)
+            if (mask >> j & 1) {
+                if (place < a.most) maybe_x[place] = x[j], maybe_at[place] = static_cast<uint16_t>(i * kPer + j);
+                ++place;
+            }
+    });
     __syncthreads();
-    some = s.maybe_n <= kMaybe;
-    tokens = some ? static_cast<int>(s.maybe_n) : units * kPer;
+    tokens = static_cast<int>(s.maybe_n);
 
     const Bins bins(range);
     const Level level0 = {0, 0, 0, 0, 0};
     histogram(bins, level0, ~0ull);
     cluster_sync_all();
-    u64 each[2];
-    const Scan c = totals(bins, level0, each);
+    Each each;
+    Scan c;
+    totals(bins, level0, c, each);
     u64 threshold = ~0ull;
     if (k > 0) {
         const int d = find(c, false, k);
@@ -647,11 +749,12 @@ __device__ void Sampler<kF32>::run(int64_t r) {
             cluster_sync_all();
             if (rank != 0) return;
             cut(upto, false, k, p);
-            if (tid < upto && s.list_order[tid] <= s.threshold) {
-                const float v = value_of(~static_cast<uint32_t>(s.list_order[tid] >> kIndexBits));
-                const int i = static_cast<int>(s.list_order[tid] & ((1u << kIndexBits) - 1));
-                const float t = row.t_of(v);
-                if (low == 0.f || expf(-t) >= low) offer(t, a.noise[e0 + i], i);
+            for (int i = tid; i < upto; i += kThreads) {
+                const u64 o = s.list_order[i];
+                if (o > s.threshold) continue;
+                const int token = static_cast<int>(o & ((1u << kIndexBits) - 1));
+                const float t = row.t_of(value_of(~static_cast<uint32_t>(o >> kIndexBits)));
+                if (low == 0.f || expf(-t) >= low) offer(t, a.noise[e0 + token], token);
             }
             __syncthreads();
             fold_best();
@@ -659,37 +762,69 @@ __device__ void Sampler<kF32>::run(int64_t r) {
             return;
         }
         u64 kept;
-        threshold = refine(bins, d, false, need, here, each[0], each[1], ~0ull, false, &kept);
+        threshold = refine(bins, d, false, need, here, each, ~0ull, false, &kept);
         if (p < 1.f) {  // the share p of what is kept: it ends in a bin before d, or in what is kept of d
             const u64 target = share_of(p, before_mass + kept);
             cluster_sync_all();  // nobody reads the list any more
             if (target <= before_mass) {
                 const int d2 = find(c, true, target);
-                threshold = refine(bins, d2, true, target - s.before_mass, s.here, each[0], each[1], ~0ull, false, &kept);
+                threshold = refine(bins, d2, true, target - s.before_mass, s.here, each, ~0ull, false, &kept);
             } else {
-                threshold = refine(bins, d, true, target - before_mass, here, each[0], each[1], threshold, true, &kept);
+                threshold = refine(bins, d, true, target - before_mass, here, each, threshold, true, &kept);
             }
         }
     } else {
         const u64 need = share_of(p, pruned ? __float2ull_rn(weight * kFixed) : c.mass_all);
         const int d = find(c, true, need);
         u64 kept;
-        threshold = refine(bins, d, true, need - min(s.before_mass, need - 1), s.here, each[0], each[1], ~0ull, false, &kept);
+        threshold = refine(bins, d, true, need - min(s.before_mass, need - 1), s.here, each, ~0ull, false, &kept);
     }
     each_token([&](float v, int i) {
         const float t = row.t_of(v);
         if (order_of(v, i) <= threshold && (low == 0.f || expf(-t) >= low)) offer(t, a.noise[e0 + i], i);
     });
+    __syncthreads();
     answer_of_all();
 }
 
-template <bool kF32>
-__global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a) {
+template <bool kF32, int kThreads>
+__global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(const SampleArgs a) {
     extern __shared__ __align__(16) uint8_t smem[];
     cluster_arrive_release();  // waited for before the first access to another CTA's shared memory
     pdl_trigger_and_wait();
-    Sampler<kF32> sampler(*reinterpret_cast<Shared *>(smem), smem + sizeof(Shared), a);
+    Sampler<kF32, kThreads> sampler(*reinterpret_cast<Shared *>(smem), smem + sizeof(Shared), a);
     sampler.run(blockIdx.x / cluster_size());
+}
+
+template <bool kF32, int kThreads>
+cudaError_t launch_typed(SampleArgs &a, const DevCtx &ctx, cudaStream_t stream) {
+    constexpr int kPer = kF32 ? 4 : 8;
+    // slices of about 16384 logits
+    int size = 1;
+    while (size < kMaxCluster && a.vocab > size * 16384) size *= 2;
+    const int units = a.vocab % kPer ? (a.vocab + 2 * kPer - 2) / kPer : a.vocab / kPer;  // what a row touches, at worst
+    a.slice_units = (units + size - 1) / size;
+    // room for as many tokens as lets all the CTAs that the registers allow share an SM
+    const int room = (226 * 1024 / (1024 / kThreads) - 1024 - static_cast<int>(sizeof(Shared))) / 6 / 16 * 16;
+    a.most = std::min((a.slice_units * kPer + 15) / 16 * 16, room);
+    constexpr auto kernel = sample_kernel<kF32, kThreads>;
+    const cudaError_t e = allow_smem<kernel>(227 * 1024, ctx.device);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(a.m * size));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = sizeof(Shared) + static_cast<size_t>(a.most) * 6;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = size;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 
 }  // namespace
@@ -709,31 +844,8 @@ cudaError_t launch_sample(const void *logits, int32_t logits_type, int64_t m, in
     a.m = m;
     a.vocab = static_cast<int32_t>(vocab);
     const bool f32 = logits_type == BD_LOGITS_F32;
-    // slices of about 16384 logits
-    int size = 1;
-    while (size < kMaxCluster && vocab > size * int64_t{16384}) size *= 2;
-    const int per = f32 ? 4 : 8;
-    const int64_t units = vocab % per ? (vocab + 2 * per - 2) / per : vocab / per;  // what a row touches, at worst
-    a.slice_units = static_cast<int32_t>((units + size - 1) / size);
-    const size_t smem = sizeof(Shared) + static_cast<size_t>(a.slice_units) * 16;
-    const cudaError_t e = f32 ? allow_smem<sample_kernel<true>>(kMaxSmem, ctx.device)
-                              : allow_smem<sample_kernel<false>>(kMaxSmem, ctx.device);
-    if (e != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(a.m * size));
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = size;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[1].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 2;
-    return f32 ? cudaLaunchKernelEx(&cfg, sample_kernel<true>, a) : cudaLaunchKernelEx(&cfg, sample_kernel<false>, a);
+    if (m <= 1000000) return f32 ? launch_typed<true, 512>(a, ctx, stream) : launch_typed<false, 512>(a, ctx, stream);
+    return f32 ? launch_typed<true, 256>(a, ctx, stream) : launch_typed<false, 256>(a, ctx, stream);
 }
 
 }  // namespace bd
