@@ -7,6 +7,8 @@
 // rotation partner and its maximum are a few shuffles away.
 #include <cuda_fp8.h>
 
+#include <type_traits>
+
 #include "bd_device.cuh"
 #include "bd_internal.h"
 
@@ -24,9 +26,17 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
                       pack_bf16x2(f[6], f[7]));
 }
 
+// A load that stays where it is written (the query may be rotated in place).
+__device__ __forceinline__ uint4 ldg_plain(const uint8_t *p) {
+    uint4 v;
+    asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p) : "memory");
+    return v;
+}
+
 // ---- append ----------------------------------------------------------------------------
 
-constexpr int kAppendThreads = 256;
+constexpr int kAppendThreads = 128;  // per token: 64, 128, 256, 512 take 38, 40, 45, 65 us for long prompts, 3.2, 2.4, 2.4, 2.5 for 64 tokens
+constexpr int kAppendAtOnce = 3;     // rows of a lane in flight
 
 struct AppendArgs {
     const uint8_t *q, *k, *v;  // bf16
@@ -46,13 +56,34 @@ __device__ __forceinline__ int scale_byte(float top) {
     return min(max(e, 127 - 60), 127 + 120);
 }
 
-// One CTA per token; rows are its q heads, then k heads, then v heads.
+// One CTA per token; rows are its q heads, then k heads, then v heads.  A lane holds 8 elements of a row's lower
+// half and the 8 they are rotated with, so the rotation needs no exchange: with one 16-byte piece per lane, whose
+// partner is half a row of lanes away, the kernel was bound by its instructions (8 prompts of up to 4096 tokens, 64
+// and 8 heads: 49 us).
 template <int kDim, bool kE4m3>
-__global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const AppendArgs a) {
-    constexpr int kLanes = kDim / 8;  // lanes of one row
+__global__ void __launch_bounds__(kAppendThreads, 5) kv_append_kernel(const AppendArgs a) {
+    constexpr int kLanes = kDim / 16;  // lanes of one row
     constexpr int kRowsPerPass = kAppendThreads / kLanes;
     pdl_trigger_and_wait();
     const int64_t t = blockIdx.x;
+    const int lane = threadIdx.x % kLanes, row0 = threadIdx.x / kLanes;
+    const int q_rows = a.q ? a.q_heads : 0;
+    const int rows = q_rows + 2 * a.kv_heads;
+    uint4 in[kAppendAtOnce][2];
+    auto load = [&](int r0) {  // rows r0, r0 + kRowsPerPass, ..: this lane's two pieces of each
+#pragma unroll
+        for (int u = 0; u < kAppendAtOnce; ++u) {
+            const int r = r0 + u * kRowsPerPass;
+            in[u][0] = in[u][1] = make_uint4(0, 0, 0, 0);
+            if (r >= rows) continue;
+            const bool is_v = r >= q_rows + a.kv_heads;
+            const uint8_t *src = r < q_rows ? a.q + (t * a.q_heads + r) * (kDim * 2)
+                                            : (is_v ? a.v : a.k) + (t * a.kv_heads + r - q_rows - (is_v ? a.kv_heads : 0)) * (kDim * 2);
+            in[u][0] = ldg_plain(src + lane * 16);
+            in[u][1] = ldg_plain(src + kDim + lane * 16);
+        }
+    };
+    load(row0);  // under way while the position and the page are looked up
     const int32_t pos = a.positions[t];
     if (pos < 0) return;  // padding
     const int64_t seq = a.seq_ids ? a.seq_ids[t] : t;
@@ -65,72 +96,72 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const AppendA
         if (threadIdx.x == 0) flag_status(a.status, kDevBadIndex);
         return;
     }
-    const int lane = threadIdx.x % kLanes;
     float c[8] = {}, s[8] = {};
     if (a.rope != nullptr) {
-        const float *r = a.rope + pos * static_cast<int64_t>(kDim) + lane % (kLanes / 2) * 8;
+        const float *r = a.rope + pos * static_cast<int64_t>(kDim) + lane * 8;
 #pragma unroll
         for (int j = 0; j < 8; j += 4) {
-            const float4 cv = *reinterpret_cast<const float4 *>(r + j);
-            const float4 sv = *reinterpret_cast<const float4 *>(r + kDim / 2 + j);
+            const float4 cv = __ldg(reinterpret_cast<const float4 *>(r + j));
+            const float4 sv = __ldg(reinterpret_cast<const float4 *>(r + kDim / 2 + j));
             c[j] = cv.x, c[j + 1] = cv.y, c[j + 2] = cv.z, c[j + 3] = cv.w;
             s[j] = sv.x, s[j + 1] = sv.y, s[j + 2] = sv.z, s[j + 3] = sv.w;
         }
     }
-    const bool upper = lane >= kLanes / 2;
-    const int q_rows = a.q ? a.q_heads : 0;
-    const int rows = q_rows + 2 * a.kv_heads;
-    for (int r0 = 0; r0 < rows; r0 += kRowsPerPass) {
-        const int r = r0 + threadIdx.x / kLanes;
-        const bool on = r < rows;
-        const bool is_q = r < q_rows, is_v = r >= q_rows + a.kv_heads;
-        const int head = is_q ? r : r - q_rows - (is_v ? a.kv_heads : 0);
-        uint4 in = make_uint4(0, 0, 0, 0);
-        if (on) {
-            const uint8_t *src = is_q ? a.q + (t * a.q_heads + head) * (kDim * 2)
-                                      : (is_v ? a.v : a.k) + (t * a.kv_heads + head) * (kDim * 2);
-            in = *reinterpret_cast<const uint4 *>(src + lane * 16);
-        }
-        float x[8];
-        unpack8(in, x);
-        if (a.rope != nullptr) {  // every lane shuffles; rows of v keep x
+    const int64_t slot_row = page * a.kv_heads * a.page_size + slot;
+    for (int r0 = row0; r0 - row0 < rows; r0 += kAppendAtOnce * kRowsPerPass) {  // as often for every lane: maxima are shuffled
+        if (r0 != row0) load(r0);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float o = __shfl_xor_sync(0xFFFFFFFFu, x[j], kLanes / 2);
-                const float turned = upper ? __fadd_rn(__fmul_rn(x[j], c[j]), __fmul_rn(o, s[j]))
-                                           : __fsub_rn(__fmul_rn(x[j], c[j]), __fmul_rn(o, s[j]));
-                if (!is_v) x[j] = turned;
+        for (int u = 0; u < kAppendAtOnce; ++u) {
+            const int r = r0 + u * kRowsPerPass;
+            const bool is_q = r < q_rows, is_v = r >= q_rows + a.kv_heads;
+            float x[8], y[8];
+            unpack8(in[u][0], x);
+            unpack8(in[u][1], y);
+            if (a.rope != nullptr && !is_v) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const float low = __fsub_rn(__fmul_rn(x[j], c[j]), __fmul_rn(y[j], s[j]));
+                    y[j] = __fadd_rn(__fmul_rn(y[j], c[j]), __fmul_rn(x[j], s[j]));
+                    x[j] = low;
+                }
             }
-        }
-        float top = 0.f;
-        if constexpr (kE4m3) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float m = fabsf(x[j]);
-                if (m < INFINITY) top = fmaxf(top, m);  // neither infinity nor NaN
+            if (is_q) {
+                uint8_t *dst = a.q_out + (t * a.q_heads + r) * (kDim * 2) + lane * 16;
+                *reinterpret_cast<uint4 *>(dst) = pack8(x);
+                *reinterpret_cast<uint4 *>(dst + kDim) = pack8(y);
             }
+            if (__all_sync(0xFFFFFFFFu, is_q || r >= rows)) continue;
+            float top = 0.f;
+            if constexpr (kE4m3) {
 #pragma unroll
-            for (int o = kLanes / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-        }
-        if (!on) continue;
-        if (is_q) {
-            *reinterpret_cast<uint4 *>(a.q_out + (t * a.q_heads + head) * (kDim * 2) + lane * 16) = pack8(x);
-            continue;
-        }
-        const int64_t at = (page * a.kv_heads + head) * a.page_size + slot;
-        uint8_t *dst = is_v ? a.cv : a.ck;
-        if constexpr (!kE4m3) {
-            *reinterpret_cast<uint4 *>(dst + at * (kDim * 2) + lane * 16) = pack8(x);
-        } else {
-            const int e = scale_byte(top);
-            const float inv = __uint_as_float(static_cast<uint32_t>(254 - e) << 23);  // 2^(127 - e), exact
-            uint32_t b[4];
+                for (int j = 0; j < 8; ++j) {  // neither infinity nor NaN
+                    if (fabsf(x[j]) < INFINITY) top = fmaxf(top, fabsf(x[j]));
+                    if (fabsf(y[j]) < INFINITY) top = fmaxf(top, fabsf(y[j]));
+                }
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                b[j] = __nv_cvt_float2_to_fp8x2(make_float2(x[2 * j] * inv, x[2 * j + 1] * inv), __NV_SATFINITE,
-                                                __NV_E4M3);
-            *reinterpret_cast<uint2 *>(dst + at * kDim + lane * 8) = make_uint2(b[0] | b[1] << 16, b[2] | b[3] << 16);
-            if (lane == 0) (is_v ? a.cv_scale : a.ck_scale)[at] = static_cast<uint8_t>(e);
+                for (int o = kLanes / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+            }
+            if (is_q || r >= rows) continue;
+            const int64_t at = slot_row + static_cast<int64_t>(r - q_rows - (is_v ? a.kv_heads : 0)) * a.page_size;
+            uint8_t *dst = is_v ? a.cv : a.ck;
+            if constexpr (!kE4m3) {
+                *reinterpret_cast<uint4 *>(dst + at * (kDim * 2) + lane * 16) = pack8(x);
+                *reinterpret_cast<uint4 *>(dst + at * (kDim * 2) + kDim + lane * 16) = pack8(y);
+            } else {
+                const int e = scale_byte(top);
+                const float inv = __uint_as_float(static_cast<uint32_t>(254 - e) << 23);  // 2^(127 - e), exact
+                auto eight = [&](const float (&v)[8]) {
+                    uint32_t b[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        b[j] = __nv_cvt_float2_to_fp8x2(make_float2(v[2 * j] * inv, v[2 * j + 1] * inv), __NV_SATFINITE,
+                                                        __NV_E4M3);
+                    return make_uint2(b[0] | b[1] << 16, b[2] | b[3] << 16);
+                };
+                *reinterpret_cast<uint2 *>(dst + at * kDim + lane * 8) = eight(x);
+                *reinterpret_cast<uint2 *>(dst + at * kDim + kDim / 2 + lane * 8) = eight(y);
+                if (lane == 0) (is_v ? a.cv_scale : a.ck_scale)[at] = static_cast<uint8_t>(e);
+            }
         }
     }
 }
@@ -138,7 +169,8 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const AppendA
 // ---- read ------------------------------------------------------------------------------
 
 constexpr int kReadThreads = 256;
-constexpr int kReadTokens = 16;  // output rows of one CTA
+constexpr int kReadTokens = 16;  // output rows of one CTA, at most
+constexpr int kReadAtOnce = 4;   // chunks of K and of V in flight per thread
 
 struct ReadArgs {
     const uint8_t *ck, *cv, *ck_scale, *cv_scale;
@@ -146,7 +178,8 @@ struct ReadArgs {
     uint8_t *k_out, *v_out;
     unsigned *status;
     int64_t n_pages, total;
-    int32_t kv_heads, page_size, n_seqs, max_pages;
+    int32_t kv_heads, page_size, n_seqs, max_pages, tokens;  // tokens: output rows of one CTA
+    uint32_t per_token, magic;  // 16-byte pieces of a token's row in k_out, and ceil(2^32 / that)
 };
 
 // Two e4m3 values times 2^(e - 127), as a bf16 pair (exact down to bf16's subnormals).
@@ -158,11 +191,12 @@ __device__ __forceinline__ uint32_t e4m3x2_to_bf16x2(uint32_t two, float scale) 
 
 template <int kDim, bool kE4m3>
 __global__ void __launch_bounds__(kReadThreads) kv_read_kernel(const ReadArgs a) {
-    constexpr int kChunk = kE4m3 ? kDim / 16 : kDim / 8;  // 16-byte chunks of a stored row
+    constexpr int kChunk = kDim / 8;  // 8 elements: 16 bytes of the output
+    using Raw = typename std::conditional<kE4m3, uint2, uint4>::type;
     __shared__ int64_t first[kReadTokens];                // (page * kv_heads) * page_size + slot; -1: nothing, -2: zeros
     pdl_trigger_and_wait();
-    const int64_t t0 = static_cast<int64_t>(blockIdx.x) * kReadTokens;
-    if (threadIdx.x < kReadTokens) {
+    const int64_t t0 = static_cast<int64_t>(blockIdx.x) * a.tokens;
+    if (static_cast<int>(threadIdx.x) < a.tokens) {
         const int64_t t = t0 + threadIdx.x;
         int64_t at = -1;
         if (t < a.total && t < a.offsets[a.n_seqs]) {
@@ -181,30 +215,44 @@ __global__ void __launch_bounds__(kReadThreads) kv_read_kernel(const ReadArgs a)
         first[threadIdx.x] = at;
     }
     __syncthreads();
-    const int per_token = a.kv_heads * kChunk;
-    const int items = kReadTokens * per_token;
-    for (int which = 0; which < 2; ++which) {
-        const uint8_t *src = which ? a.cv : a.ck;
-        const uint8_t *sc = which ? a.cv_scale : a.ck_scale;
-        uint8_t *out = which ? a.v_out : a.k_out;
-        for (int i = threadIdx.x; i < items; i += kReadThreads) {
-            const int tok = i / per_token, rest = i % per_token;
-            const int head = rest / kChunk, c = rest % kChunk;
+    const uint32_t items = a.tokens * a.per_token;
+    for (uint32_t i0 = threadIdx.x; i0 < items; i0 += kReadAtOnce * kReadThreads) {
+        Raw v[kReadAtOnce][2];
+        float s[kReadAtOnce][2];
+        int64_t to[kReadAtOnce];
+#pragma unroll
+        for (int u = 0; u < kReadAtOnce; ++u) {
+            const uint32_t i = i0 + u * kReadThreads;
+            to[u] = -1;
+            if (i >= items) continue;
+            const uint32_t tok = a.per_token == 1 ? i : __umulhi(i, a.magic), rest = i - tok * a.per_token;
             const int64_t f = first[tok];
             if (f == -1) continue;
-            const int64_t row = f + static_cast<int64_t>(head) * a.page_size;
-            uint4 v = make_uint4(0, 0, 0, 0);
-            if (f >= 0) v = ldg_stream(src + (row * kChunk + c) * 16);
-            uint8_t *dst = out + (((t0 + tok) * a.kv_heads + head) * kChunk + c) * (kE4m3 ? 32 : 16);
-            if constexpr (!kE4m3) {
-                *reinterpret_cast<uint4 *>(dst) = v;
-            } else {
-                const float s = f >= 0 ? __uint_as_float(static_cast<uint32_t>(sc[row]) << 23) : 0.f;
-                uint4 *d = reinterpret_cast<uint4 *>(dst);
-                d[0] = make_uint4(e4m3x2_to_bf16x2(v.x & 0xFFFFu, s), e4m3x2_to_bf16x2(v.x >> 16, s),
-                                  e4m3x2_to_bf16x2(v.y & 0xFFFFu, s), e4m3x2_to_bf16x2(v.y >> 16, s));
-                d[1] = make_uint4(e4m3x2_to_bf16x2(v.z & 0xFFFFu, s), e4m3x2_to_bf16x2(v.z >> 16, s),
-                                  e4m3x2_to_bf16x2(v.w & 0xFFFFu, s), e4m3x2_to_bf16x2(v.w >> 16, s));
+            to[u] = (t0 + tok) * a.per_token + rest;
+            const int64_t row = f + static_cast<int64_t>(rest / kChunk) * a.page_size;
+#pragma unroll
+            for (int w = 0; w < 2; ++w) {
+                v[u][w] = Raw{};
+                s[u][w] = 0.f;
+                if (f < 0) continue;
+                v[u][w] = __ldcs(reinterpret_cast<const Raw *>(w ? a.cv : a.ck) + row * kChunk + rest % kChunk);
+                if constexpr (kE4m3) s[u][w] = __uint_as_float(static_cast<uint32_t>((w ? a.cv_scale : a.ck_scale)[row]) << 23);
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < kReadAtOnce; ++u) {
+            if (to[u] < 0) continue;
+#pragma unroll
+            for (int w = 0; w < 2; ++w) {
+                uint4 *d = reinterpret_cast<uint4 *>(w ? a.v_out : a.k_out) + to[u];
+                const Raw x = v[u][w];
+                if constexpr (!kE4m3) {
+                    *d = x;
+                } else {
+                    const float f = s[u][w];
+                    *d = make_uint4(e4m3x2_to_bf16x2(x.x & 0xFFFFu, f), e4m3x2_to_bf16x2(x.x >> 16, f),
+                                    e4m3x2_to_bf16x2(x.y & 0xFFFFu, f), e4m3x2_to_bf16x2(x.y >> 16, f));
+                }
             }
         }
     }
@@ -277,7 +325,12 @@ cudaError_t launch_kv_read(const bd_kv_cache &c, const int32_t *page_table, int3
     a.page_size = c.page_size;
     a.n_seqs = n_seqs;
     a.max_pages = max_pages;
-    const int64_t grid = (total + kReadTokens - 1) / kReadTokens;
+    // 16 tokens a CTA, fewer where they would leave SMs without one
+    a.tokens = kReadTokens;
+    while (a.tokens > 1 && (total + a.tokens - 1) / a.tokens < 4 * ctx.num_sms) a.tokens /= 2;
+    a.per_token = static_cast<uint32_t>(c.kv_heads * (c.head_dim / 8));
+    a.magic = static_cast<uint32_t>(((uint64_t{1} << 32) + a.per_token - 1) / a.per_token);  // exact for 16 x 16384 pieces
+    const int64_t grid = (total + a.tokens - 1) / a.tokens;
     const bool e = c.kv_type == BD_KV_E4M3;
     if (c.head_dim == 128)
         return launch_pdl(e ? kv_read_kernel<128, true> : kv_read_kernel<128, false>, grid, kReadThreads, a, stream);

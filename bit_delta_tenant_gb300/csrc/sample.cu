@@ -27,10 +27,11 @@
 //     by the remaining bits of t, then by the bits of (x, index), which differ for any two.
 //
 // Sums of weights do not depend on the order of atomics: within a bin of width d,
-// w = exp(-bin d) w' with w' in [1 - d, 1], and a bin sums round((w' - 1 + d) 65535 / d)
-// in 32 bits beside its count; across bins weights are fixed-point with 40 fractional
+// w = exp(-bin d) w' with w' in [1 - d, 1], and a bin sums round((w' - 1 + d) P / d) in
+// 32 bits beside its count, P = 65535 or what a long slice leaves room for; across bins weights are fixed-point with 40 fractional
 // bits.  The sum of all weights is fp32 in an order fixed by the shape.
 #include <algorithm>
+#include <cmath>
 
 #include "bd_device.cuh"
 #include "bd_internal.h"
@@ -38,9 +39,12 @@
 namespace bd {
 namespace {
 
-constexpr int kBins = 512;
+constexpr int kThreads = 512;
+constexpr int kCtasPerSm = 2;     // by registers
+constexpr int kWarps = kThreads / 32;
+constexpr int kBins = kThreads;   // one per thread
 constexpr int kBits = 9;          // a digit: one bin
-constexpr int kCap = 512;         // tokens ordered exactly
+constexpr int kCap = kBins;       // tokens ordered exactly: a list is scanned as the bins are
 constexpr int kIndexBits = 18;    // BD_SAMPLE_MAX_VOCAB = 2^18
 constexpr int kMaxCluster = 8;
 constexpr float kRange = 31.5f;   // weights below exp(-31.5) of the largest count as 0 in a prefix's sum
@@ -57,16 +61,16 @@ struct SampleArgs {
     float *logprob;
     int64_t m;
     int32_t vocab, slice_units;  // 16-byte units of logits in a CTA's slice
+    float parts;                 // of a bin's width: what all tokens of a slice add up to still fits 32 bits
     int32_t most;                // tokens that may be kept for which there is room; with more the passes go over the slice
 };
 
 struct alignas(16) Shared {
-    static constexpr int kMaxWarps = 16;
     uint2 bins[kBins];  // count, weight
     u64 list_order[kCap], list_mass[kCap], sorted_mass[kCap];
-    u64 warp_mass[kMaxWarps], warp_parts[2][kMaxWarps];
-    uint32_t warp_count[kMaxWarps];
-    float warp_value[3][kMaxWarps];
+    u64 warp_mass[kWarps], warp_parts[2][kWarps];
+    uint32_t warp_count[kWarps];
+    float warp_value[3][kWarps];
     // written by the cluster's CTAs
     struct Rank {
         float top, sum, low;
@@ -135,9 +139,9 @@ struct Row {
 };
 // Bins of equal width over [0, range); the last one takes everything from `range` on and weighs nothing.
 struct Bins {
-    float scale, width, unit;  // 1 / width, width, 65535 / width
-    __device__ __forceinline__ explicit Bins(float range)
-        : scale((kBins - 1) / range), width(range / (kBins - 1)), unit(65535.f * scale) {}
+    float scale, width, unit, parts_of, most;  // 1 / width, width, parts / width and its inverse, parts
+    __device__ __forceinline__ Bins(float range, float parts)
+        : scale((kBins - 1) / range), width(range / (kBins - 1)), unit(parts * scale), parts_of(width / parts), most(parts) {}
     __device__ __forceinline__ int bin(float t) const {
         return t < width * (kBins - 1) ? min(static_cast<int>(t * scale), kBins - 2) : kBins - 1;
     }
@@ -145,12 +149,12 @@ struct Bins {
         return b == kBins - 1 ? 0 : min(max(static_cast<int>((t * scale - b) * kBins), 0), kBins - 1);
     }
     __device__ __forceinline__ uint32_t part(float t, int b) const {
-        return b == kBins - 1 ? 0u : __float2uint_rn(fmaxf(ex2((b * width - t) * kLog2e) - (1.f - width), 0.f) * unit);
+        return b == kBins - 1 ? 0u : __float2uint_rn(fminf(fmaxf(ex2((b * width - t) * kLog2e) - (1.f - width), 0.f) * unit, most));
     }
     // fp32 from whole numbers: the same on every CTA, 2^-22 of the weight
     __device__ __forceinline__ u64 mass(int b, uint32_t count, u64 parts) const {
         if (b == kBins - 1) return 0;
-        const float w = fmaf(static_cast<float>(parts), width * (1.f / 65535.f), static_cast<float>(count) * (1.f - width));
+        const float w = fmaf(static_cast<float>(parts), parts_of, static_cast<float>(count) * (1.f - width));
         return __float2ull_rn(w * (ex2(b * width * -kLog2e) * kFixed));
     }
 };
@@ -159,17 +163,14 @@ __device__ __forceinline__ u64 share_of(float p, u64 mass) {
     return max(__umul64hi(__float2ull_rz(p * 18446744073709551616.f), mass), u64{1});
 }
 
-template <bool kF32, int kThreads>
+template <bool kF32>
 struct Sampler {
     static constexpr int kPer = kF32 ? 4 : 8;  // logits of a unit
-    static constexpr int kWarps = kThreads / 32;
-    static constexpr int kMine = kBins / kThreads;  // bins of a thread, neighbours
-    static_assert(kCap == kBins, "a list is scanned as the bins are");
 
     Shared &s;
     const SampleArgs &a;
     float *maybe_x;      // tokens that may be kept,
-    uint16_t *maybe_at;  // and their places in the slice
+    uint32_t *maybe_at;  // and which they are
     const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32, rank = cluster_rank(), size = cluster_size();
     int64_t e0 = 0, e1 = 0, u0 = 0;  // the row's first element and the one after its last, the slice's first unit
     int base = 0, units = 0;         // token of the slice's first element, units in the slice
@@ -179,7 +180,7 @@ struct Sampler {
     Row row;
 
     __device__ Sampler(Shared &shared, uint8_t *data, const SampleArgs &args)
-        : s(shared), a(args), maybe_x(reinterpret_cast<float *>(data)), maybe_at(reinterpret_cast<uint16_t *>(data + args.most * 4)) {}
+        : s(shared), a(args), maybe_x(reinterpret_cast<float *>(data)), maybe_at(reinterpret_cast<uint32_t *>(data + args.most * 4)) {}
 
     // ---- the slice --------------------------------------------------------------------
     static __device__ __forceinline__ float clean(float x) { return fmaxf(x, -INFINITY); }  // NaN to -inf
@@ -196,6 +197,12 @@ struct Sampler {
         }
 #pragma unroll
         for (int j = 0; j < kPer; ++j) x[j] = fmaxf(x[j], -INFINITY);  // NaN to -inf; -0 is told from +0 nowhere but in order_of
+    }
+    static __device__ __forceinline__ float largest(const float (&x)[kPer]) {
+        float m = x[0];
+#pragma unroll
+        for (int j = 1; j < kPer; ++j) m = fmaxf(m, x[j]);
+        return m;
     }
     __device__ __forceinline__ bool inside(int i) const { return i >= whole_from && i < whole_to; }
     __device__ __forceinline__ uint4 fetch(int i) const {
@@ -240,18 +247,55 @@ struct Sampler {
             }
         }
     }
+    // f(i, x, noise) for this thread's units, the logits and the noise of kAtOnce units in flight together
+    template <int kAtOnce, class F>
+    __device__ __forceinline__ void each_scored(F f) const {
+        for (int i0 = tid; i0 < units; i0 += kAtOnce * kThreads) {
+            uint4 raw[kAtOnce];
+            float noise[kAtOnce][kPer];
+#pragma unroll
+            for (int q = 0; q < kAtOnce; ++q) {
+                const int i = i0 + q * kThreads;
+                if (!inside(i)) continue;
+                raw[q] = fetch(i);
+                const float *g = a.noise + (e0 + base) + static_cast<int64_t>(i) * kPer;
+#pragma unroll
+                for (int j = 0; j < kPer; j += 4) {
+                    const float4 v = __ldg(reinterpret_cast<const float4 *>(g + j));
+                    noise[q][j] = v.x, noise[q][j + 1] = v.y, noise[q][j + 2] = v.z, noise[q][j + 3] = v.w;
+                }
+            }
+#pragma unroll
+            for (int q = 0; q < kAtOnce; ++q) {
+                const int i = i0 + q * kThreads;
+                if (i >= units) break;
+                float x[kPer];
+                read(i, inside(i), raw[q], x);
+                if (!inside(i)) {
+#pragma unroll
+                    for (int j = 0; j < kPer; ++j)
+                        noise[q][j] = x[j] > -INFINITY ? a.noise[e0 + base + static_cast<int64_t>(i) * kPer + j] : 0.f;
+                }
+                f(i, x, noise[q]);
+            }
+        }
+    }
     // f(x, token) for this thread's share of the tokens that may be kept
     template <class F>
     __device__ __forceinline__ void each_token(F f) const {
         if (tokens <= a.most) {
-            for (int i = tid; i < tokens; i += kThreads) f(maybe_x[i], base + maybe_at[i]);
+            for (int i = tid; i < tokens; i += kThreads) f(maybe_x[i], static_cast<int>(maybe_at[i]));
         } else {
-            for (int i = tid; i < units * kPer; i += kThreads) {
-                const int64_t e = u0 * kPer + i;
-                if (e < e0 || e >= e1) continue;
-                const float x = logit(e);
-                if (x >= reach && x > -INFINITY) f(x, base + i);
-            }
+            each_unit<4>([&](int i, const float (&x)[kPer]) {
+                if (!(largest(x) >= reach)) return;
+#pragma unroll 1
+                for (int j = 0; j < kPer; ++j) {
+                    float v = x[0];
+#pragma unroll
+                    for (int q = 1; q < kPer; ++q) v = q == j ? x[q] : v;
+                    if (v >= reach && v > -INFINITY) f(v, base + i * kPer + j);
+                }
+            });
         }
     }
 
@@ -271,56 +315,41 @@ struct Sampler {
     }
 
     // ---- bins -------------------------------------------------------------------------
-    // Counts and weights of a thread's places (bins, or tokens of a list) and of all up to each.
+    // Count and weight of a thread's place (a bin, or a token of a list), and of all places up to it.
     struct Scan {
-        uint32_t count[kMine], count_upto[kMine], count_all;
-        u64 mass[kMine], mass_upto[kMine], mass_all;
+        uint32_t count, count_upto, count_all;
+        u64 mass, mass_upto, mass_all;
     };
-    __device__ __forceinline__ void scan(Scan &r) {
-        uint32_t n = 0;
-        u64 w = 0;
-#pragma unroll
-        for (int i = 0; i < kMine; ++i) {
-            n += r.count[i], w += r.mass[i];
-            r.count_upto[i] = n, r.mass_upto[i] = w;
-        }
-        uint32_t n_in = n;
-        u64 w_in = w;
+    __device__ __forceinline__ Scan scan(uint32_t count, u64 mass) {
+        Scan r = {count, count, 0, mass, mass, 0};
 #pragma unroll
         for (int o = 1; o < 32; o *= 2) {
-            const uint32_t u = __shfl_up_sync(0xFFFFFFFFu, n_in, o);
-            const u64 v = __shfl_up_sync(0xFFFFFFFFu, w_in, o);
-            if (lane >= o) n_in += u, w_in += v;
+            const uint32_t u = __shfl_up_sync(0xFFFFFFFFu, r.count_upto, o);
+            const u64 v = __shfl_up_sync(0xFFFFFFFFu, r.mass_upto, o);
+            if (lane >= o) r.count_upto += u, r.mass_upto += v;
         }
         __syncthreads();
-        if (lane == 31) s.warp_count[warp] = n_in, s.warp_mass[warp] = w_in;
+        if (lane == 31) s.warp_count[warp] = r.count_upto, s.warp_mass[warp] = r.mass_upto;
         __syncthreads();
-        n_in -= n, w_in -= w;
-        r.count_all = 0, r.mass_all = 0;
 #pragma unroll
         for (int q = 0; q < kWarps; ++q) {
             const uint32_t u = s.warp_count[q];
             const u64 v = s.warp_mass[q];
-            if (q < warp) n_in += u, w_in += v;
+            if (q < warp) r.count_upto += u, r.mass_upto += v;
             r.count_all += u, r.mass_all += v;
         }
-#pragma unroll
-        for (int i = 0; i < kMine; ++i) r.count_upto[i] += n_in, r.mass_upto[i] += w_in;
+        return r;
     }
     // The first bin at which the count or the weight reaches `need`, what precedes it in s.before_*, its own
     // count in s.here.  Where rounding leaves the sum of all bins short, the last bin that holds a token.
     __device__ __forceinline__ int find(const Scan &c, bool by_mass, u64 need) {
-        const bool reached = (by_mass ? c.mass_all : c.count_all) >= need;
+        const uint32_t n = c.count_upto - c.count;
+        const u64 w = c.mass_upto - c.mass;
+        bool here;
+        if ((by_mass ? c.mass_all : c.count_all) < need) here = c.count > 0 && c.count_upto == c.count_all;
+        else here = by_mass ? c.mass_upto >= need && w < need : c.count_upto >= need && n < need;
         __syncthreads();
-#pragma unroll
-        for (int i = 0; i < kMine; ++i) {
-            const uint32_t n = c.count_upto[i] - c.count[i];
-            const u64 w = c.mass_upto[i] - c.mass[i];
-            bool here;
-            if (!reached) here = c.count[i] > 0 && c.count_upto[i] == c.count_all;
-            else here = by_mass ? c.mass_upto[i] >= need && w < need : c.count_upto[i] >= need && n < need;
-            if (here) s.found = tid * kMine + i, s.before_count = n, s.before_mass = w, s.here = c.count[i];
-        }
+        if (here) s.found = tid, s.before_count = n, s.before_mass = w, s.here = c.count;
         __syncthreads();
         return s.found;
     }
@@ -339,10 +368,12 @@ struct Sampler {
         if (c != at.sub || (at.depth > 2 && o >> (at.shift + kBits) != at.prefix)) return -1;
         return static_cast<int>(o >> at.shift) & (kBins - 1);
     }
-    __device__ void histogram(const Bins &bins, const Level &at, u64 limit) {
-#pragma unroll
-        for (int i = 0; i < kMine; ++i) s.bins[tid + i * kThreads] = make_uint2(0, 0);
+    __device__ __forceinline__ void clear_bins() {
+        s.bins[tid] = make_uint2(0, 0);
         __syncthreads();
+    }
+    __device__ void histogram(const Bins &bins, const Level &at, u64 limit) {
+        clear_bins();
         each_token([&](float x, int i) {
             const float t = row.t_of(x);
             const u64 o = order_of(x, i);
@@ -353,37 +384,30 @@ struct Sampler {
             atomicAdd(&s.bins[d].y, bins.part(t, at.depth == 0 ? d : at.bin));
         });
     }
-    // The cluster's totals of this thread's bins, and each CTA's counts in them (four 16-bit fields a word).
+    // The cluster's totals of this thread's bin, and each CTA's count in it (four 16-bit fields a word; what is
+    // gathered by them is at most kCap tokens).
     struct Each {
-        u64 lo[kMine], hi[kMine];
+        u64 lo, hi;
     };
-    __device__ __forceinline__ void totals(const Bins &bins, const Level &at, Scan &c, Each &each) {
+    __device__ __forceinline__ Scan totals(const Bins &bins, const Level &at, Each &each) {
+        uint2 v[kMaxCluster];
 #pragma unroll
-        for (int i = 0; i < kMine; ++i) {
-            const int d = tid * kMine + i;
-            uint2 v[kMaxCluster];
+        for (int q = 0; q < kMaxCluster; ++q) v[q] = q < size ? ld_remote(remote(&s.bins[tid], q)) : make_uint2(0, 0);
+        uint32_t n = 0;
+        u64 parts = 0;
+        each.lo = each.hi = 0;
 #pragma unroll
-            for (int q = 0; q < kMaxCluster; ++q) v[q] = q < size ? ld_remote(remote(&s.bins[d], q)) : make_uint2(0, 0);
-            uint32_t n = 0;
-            u64 parts = 0;
-            each.lo[i] = each.hi[i] = 0;
-#pragma unroll
-            for (int q = 0; q < kMaxCluster; ++q) {
-                n += v[q].x, parts += v[q].y;
-                (q < 4 ? each.lo[i] : each.hi[i]) |= static_cast<u64>(v[q].x) << 16 * (q % 4);
-            }
-            c.count[i] = n;
-            c.mass[i] = bins.mass(at.depth == 0 ? d : at.bin, n, parts);
+        for (int q = 0; q < kMaxCluster; ++q) {
+            n += v[q].x, parts += v[q].y;
+            (q < 4 ? each.lo : each.hi) |= static_cast<u64>(min(v[q].x, 0xFFFFu)) << 16 * (q % 4);
         }
-        scan(c);
+        return scan(n, bins.mass(at.depth == 0 ? tid : at.bin, n, parts));
     }
     // Sends this CTA's tokens of one set to every CTA's list: digit d at level `at`, or with `upto` all bins up to d.
     // The places follow from the counts that every CTA has of every other.
     __device__ void gather(const Bins &bins, const Level &at, int d, bool upto, u64 limit, const Each &each) {
-        u64 lo = 0, hi = 0;
-#pragma unroll
-        for (int i = 0; i < kMine; ++i)
-            if (upto ? tid * kMine + i <= d : tid * kMine + i == d) lo += each.lo[i], hi += each.hi[i];
+        const bool mine = upto ? tid <= d : tid == d;
+        u64 lo = mine ? each.lo : 0, hi = mine ? each.hi : 0;
 #pragma unroll
         for (int o = 16; o > 0; o /= 2) lo += __shfl_xor_sync(0xFFFFFFFFu, lo, o), hi += __shfl_xor_sync(0xFFFFFFFFu, hi, o);
         if (lane == 0) s.warp_parts[0][warp] = lo, s.warp_parts[1][warp] = hi;
@@ -416,53 +440,33 @@ struct Sampler {
         // ranks by counting, as many threads to a token as the list leaves
         const int lanes = n * 8 <= kThreads ? 8 : n * 4 <= kThreads ? 4 : n * 2 <= kThreads ? 2 : 1;
         const uint32_t pairs = (n + 1) / 2;
-        uint32_t ranks[kCap / kThreads];
-#pragma unroll
-        for (int q = 0; q < kCap / kThreads; ++q) {
-            const int i = (tid + q * kThreads) / lanes, part = tid % lanes;
-            const u64 mine = s.list_order[i];
-            uint32_t before = 0;
-            if (q == 0 || tid + q * kThreads < n)
-                for (uint32_t j = part; j < pairs; j += lanes) {
-                    const ulonglong2 two = *reinterpret_cast<const ulonglong2 *>(&s.list_order[2 * j]);
-                    before += (two.x < mine) + (two.y < mine);
-                }
-            if (lanes > 1) before += __shfl_xor_sync(0xFFFFFFFFu, before, 1);
-            if (lanes > 2) before += __shfl_xor_sync(0xFFFFFFFFu, before, 2);
-            if (lanes > 4) before += __shfl_xor_sync(0xFFFFFFFFu, before, 4);
-            const bool on = i < n && part == 0 && (q == 0 || lanes == 1);
-            ranks[q] = on ? before : kCap;
-            if (on) s.sorted_mass[before] = s.list_mass[i];
+        const int i = tid / lanes, part = tid % lanes;
+        const u64 mine = s.list_order[i];
+        uint32_t rank_of = 0;
+        for (uint32_t j = part; j < pairs; j += lanes) {
+            const ulonglong2 two = *reinterpret_cast<const ulonglong2 *>(&s.list_order[2 * j]);
+            rank_of += (two.x < mine) + (two.y < mine);
         }
+        if (lanes > 1) rank_of += __shfl_xor_sync(0xFFFFFFFFu, rank_of, 1);
+        if (lanes > 2) rank_of += __shfl_xor_sync(0xFFFFFFFFu, rank_of, 2);
+        if (lanes > 4) rank_of += __shfl_xor_sync(0xFFFFFFFFu, rank_of, 4);
+        const bool on = i < n && part == 0;
+        if (on) s.sorted_mass[rank_of] = s.list_mass[i];
         __syncthreads();
-        // weights in that order, neighbouring places to a thread
-        Scan c;
-#pragma unroll
-        for (int i = 0; i < kMine; ++i) c.count[i] = tid * kMine + i < n, c.mass[i] = s.sorted_mass[tid * kMine + i];
-        scan(c);
+        // weights in that order, a place to a thread
+        const u64 w = s.sorted_mass[tid];
+        const Scan c = scan(tid < n, w);
         u64 end = need;
         if (share < 1.f) {
-            const uint32_t last = static_cast<uint32_t>(min(need, static_cast<u64>(n))) - 1;
-#pragma unroll
-            for (int i = 0; i < kMine; ++i)
-                if (tid * kMine + i == last) s.kept_mass = c.mass_upto[i];
+            if (tid == static_cast<uint32_t>(min(need, static_cast<u64>(n))) - 1) s.kept_mass = c.mass_upto;
             __syncthreads();
             end = share_of(share, s.kept_mass);
         }
-        int kept = 0;
-#pragma unroll
-        for (int i = 0; i < kMine; ++i) {
-            const int place = tid * kMine + i;
-            const bool keep = place < n && (by_mass || static_cast<u64>(place) < need) &&
-                              (!(by_mass || share < 1.f) || c.mass_upto[i] - c.mass[i] < end);
-            kept += __syncthreads_count(keep);  // they are the first ones
-        }
-#pragma unroll
-        for (int i = 0; i < kMine; ++i)
-            if (tid * kMine + i == kept - 1) s.kept_mass = c.mass_upto[i];
-#pragma unroll
-        for (int q = 0; q < kCap / kThreads; ++q)
-            if (ranks[q] == kept - 1) s.threshold = s.list_order[(tid + q * kThreads) / lanes];
+        const bool keep = tid < n && (by_mass || static_cast<u64>(tid) < need) &&
+                          (!(by_mass || share < 1.f) || c.mass_upto - w < end);
+        const int kept = __syncthreads_count(keep);  // they are the first ones
+        if (tid == kept - 1) s.kept_mass = c.mass_upto;
+        if (on && rank_of == kept - 1) s.threshold = mine;
         __syncthreads();
     }
 
@@ -483,8 +487,7 @@ struct Sampler {
             cluster_sync_all();  // nobody reads the bins any more
             histogram(bins, at, limit);
             cluster_sync_all();
-            Scan c;
-            totals(bins, at, c, each);
+            const Scan c = totals(bins, at, each);
             digit = find(c, by_mass, need);
             need -= by_mass ? s.before_mass : s.before_count;
             *kept += s.before_mass;
@@ -500,8 +503,8 @@ struct Sampler {
     __device__ void run(int64_t r);
 };
 
-template <bool kF32, int kThreads>
-__device__ void Sampler<kF32, kThreads>::run(int64_t r) {
+template <bool kF32>
+__device__ void Sampler<kF32>::run(int64_t r) {
     // units at multiples of kPer of the whole array: 16-byte aligned logits, and 16-byte aligned noise
     e0 = r * a.vocab, e1 = e0 + a.vocab;
     u0 = e0 / kPer + static_cast<int64_t>(rank) * a.slice_units;
@@ -521,8 +524,8 @@ __device__ void Sampler<kF32, kThreads>::run(int64_t r) {
     if (!(p > 0.f && p < 1.f) || k == 1) p = 1.f;
     low = low > 0.f ? fminf(low, 1.f) : 0.f;
     const bool filtered = !greedy && (k > 0 || p < 1.f);
-    // noise that will be read whole is on its way into L2 meanwhile
-    if (tid == 0 && !filtered && !greedy && low == 0.f) {
+    // noise of which most will be read is on its way into L2 meanwhile
+    if (tid == 0 && !greedy && k == 0 && low == 0.f) {
         const int64_t n = min(static_cast<int64_t>(units), a.m * a.vocab / kPer - u0);
         if (n > 0)
             asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(a.noise + u0 * kPer), "r"(static_cast<uint32_t>(n * kPer * 4))
@@ -536,9 +539,7 @@ __device__ void Sampler<kF32, kThreads>::run(int64_t r) {
     float top = -INFINITY, shift = 0.f, sum = 0.f;
     int top_unit = 0;
     each_unit<kF32 ? 8 : 4>([&](int i, const float (&x)[kPer]) {
-        float here = x[0];
-#pragma unroll
-        for (int j = 1; j < kPer; ++j) here = fmaxf(here, x[j]);
+        const float here = largest(x);
         if (here > top) {
             const float to = here * per;
             sum = top > -INFINITY ? sum * ex2(shift - to) : 0.f;
@@ -641,28 +642,19 @@ __device__ void Sampler<kF32, kThreads>::run(int64_t r) {
         answer_of_all();
         return;
     }
+    auto score_of = [&](float x, float noise) {  // where nothing is at the end of its range
+        return __fadd_rn(__fmul_rn(__fsub_rn(x, row.top), row.inv_t), noise);
+    };
     if (!filtered && low == 0.f && plain && row.top < INFINITY) {  // every token
         float most = -INFINITY;
         int first = -1;  // of equal scores the one met first has the lowest index
-        each_unit<kF32 ? 4 : 2>([&](int i, const float (&x)[kPer]) {
-            const float *g = a.noise + (e0 + base) + static_cast<int64_t>(i) * kPer;
-            float noise[kPer];
-            if (inside(i)) {
+        each_scored<kF32 ? 4 : 2>([&](int i, const float (&x)[kPer], const float (&noise)[kPer]) {
 #pragma unroll
-                for (int j = 0; j < kPer; j += 4) {
-                    const float4 v = __ldg(reinterpret_cast<const float4 *>(g + j));
-                    noise[j] = v.x, noise[j + 1] = v.y, noise[j + 2] = v.z, noise[j + 3] = v.w;
-                }
-            } else {
-#pragma unroll
-                for (int j = 0; j < kPer; ++j) noise[j] = x[j] > -INFINITY ? g[j] : 0.f;
-            }
-#pragma unroll
-            for (int j = 0; j < kPer; ++j) {
-                const float score = __fadd_rn(__fmul_rn(__fsub_rn(x[j], row.top), row.inv_t), noise[j]);
-                if (score > most) most = score, first = i * kPer + j;
-            }
-        });
+                                            for (int j = 0; j < kPer; ++j) {
+                                                const float score = score_of(x[j], noise[j]);
+                                                if (score > most) most = score, first = i * kPer + j;
+                                            }
+                                        });
         if (first >= 0) best = static_cast<u64>(ascending(most)) << 32 | (0xFFFFFFFFu - static_cast<unsigned>(base + first));
         if (!__syncthreads_or(first >= 0)) {  // a slice whose scores are all -inf (or NaN, which counts as -inf): its first token
             each_unit<1>([&](int i, const float (&x)[kPer]) {
@@ -679,10 +671,7 @@ __device__ void Sampler<kF32, kThreads>::run(int64_t r) {
         least -= fabsf(least) * 1e-6f + temp * 1e-6f;  // below any token that the exact test keeps
         if (!(least > -INFINITY)) least = -INFINITY;
         each_unit<kF32 ? 8 : 4>([&](int i, const float (&x)[kPer]) {
-            float here = x[0];
-#pragma unroll
-            for (int j = 1; j < kPer; ++j) here = fmaxf(here, x[j]);
-            if (here < least) return;
+            if (largest(x) < least) return;
 #pragma unroll
             for (int j = 0; j < kPer; ++j) {
                 if (x[j] == -INFINITY) continue;
@@ -711,34 +700,41 @@ __device__ void Sampler<kF32, kThreads>::run(int64_t r) {
             if (!(reach > -INFINITY)) reach = -INFINITY;
         }
     }
-    if (tid == 0) s.maybe_n = 0;
-    __syncthreads();
-    each_unit<kF32 ? 8 : 4>([&](int i, const float (&x)[kPer]) {
-        float here = x[0];
-#pragma unroll
-        for (int j = 1; j < kPer; ++j) here = fmaxf(here, x[j]);
-        if (!(here >= reach)) return;
-        uint32_t mask = 0;
-#pragma unroll
-        for (int j = 0; j < kPer; ++j) mask |= (x[j] >= reach && x[j] > -INFINITY ? 1u : 0u) << j;
-        uint32_t place = atomicAdd(&s.maybe_n, static_cast<uint32_t>(__popc(mask)));
-#pragma unroll
-        for (int j = 0; j < kPer; ++j)
-            if (mask >> j & 1) {
-                if (place < a.most) maybe_x[place] = x[j], maybe_at[place] = static_cast<uint16_t>(i * kPer + j);
-                ++place;
-            }
-    });
-    __syncthreads();
-    tokens = static_cast<int>(s.maybe_n);
-
-    const Bins bins(range);
+    const Bins bins(range, a.parts);
     const Level level0 = {0, 0, 0, 0, 0};
-    histogram(bins, level0, ~0ull);
+    auto keep = [&](float x, int token) {  // one more token of which the bins are told, or that is ordered
+        const uint32_t place = atomicAdd(&s.maybe_n, 1u);
+        if (place < a.most) maybe_x[place] = x, maybe_at[place] = static_cast<uint32_t>(token);
+    };
+    if (tid == 0) s.maybe_n = 0;
+    if (k > 0) {  // few tokens: packed, then counted
+        __syncthreads();
+        each_unit<kF32 ? 8 : 4>([&](int i, const float (&x)[kPer]) {
+            if (!(largest(x) >= reach)) return;
+#pragma unroll
+            for (int j = 0; j < kPer; ++j)
+                if (x[j] >= reach && x[j] > -INFINITY) keep(x[j], base + i * kPer + j);
+        });
+        __syncthreads();
+        tokens = static_cast<int>(s.maybe_n);
+        histogram(bins, level0, ~0ull);
+    } else {  // many: counted as they are read
+        clear_bins();
+        each_unit<kF32 ? 4 : 2>([&](int, const float (&x)[kPer]) {
+            if (!(largest(x) >= reach)) return;
+#pragma unroll
+            for (int j = 0; j < kPer; ++j) {
+                if (!(x[j] >= reach && x[j] > -INFINITY)) continue;
+                const float t = row.t_of(x[j]);
+                const int d = bins.bin(t);
+                atomicAdd(&s.bins[d].x, 1u);
+                atomicAdd(&s.bins[d].y, bins.part(t, d));
+            }
+        });
+    }
     cluster_sync_all();
     Each each;
-    Scan c;
-    totals(bins, level0, c, each);
+    const Scan c = totals(bins, level0, each);
     u64 threshold = ~0ull;
     if (k > 0) {
         const int d = find(c, false, k);
@@ -776,8 +772,54 @@ __device__ void Sampler<kF32, kThreads>::run(int64_t r) {
     } else {
         const u64 need = share_of(p, pruned ? __float2ull_rn(weight * kFixed) : c.mass_all);
         const int d = find(c, true, need);
+        const u64 before_mass = s.before_mass;
+        const uint32_t here = s.here;
+        // Tokens of the bins before d are kept: score them now, and pack those of bin d.  x >= sure lies before d and
+        // x < edge beyond it, so few have to be told by their bin.
+        const float slack = fabsf(row.top) * 1e-6f + (bins.width * temp) * 1e-2f + range * temp * 1e-6f;
+        float edge = d < kBins - 1 ? row.top - (d + 1) * bins.width * temp - slack : -INFINITY;
+        edge = edge > reach ? edge : reach;  // (NaN: reach)
+        float sure = d < kBins - 1 ? row.top - d * bins.width * temp + slack : INFINITY;
+        if (!(plain && row.top < INFINITY && low == 0.f && sure < INFINITY)) sure = INFINITY;
+        float most = -INFINITY;
+        int first = -1;
+        each_scored<kF32 ? 4 : 2>(
+            [&](int i, const float (&x)[kPer], const float (&noise)[kPer]) {
+                if (!(largest(x) >= edge)) return;
+                bool close = false;
+#pragma unroll
+                for (int j = 0; j < kPer; ++j) {
+                    const float score = score_of(x[j], noise[j]);
+                    if (x[j] >= sure && score > most) most = score, first = i * kPer + j;
+                    close |= x[j] < sure && x[j] >= edge;
+                }
+                if (!close) return;
+#pragma unroll 1
+                for (int j = 0; j < kPer; ++j) {
+                    float v = x[0], g = noise[0];
+#pragma unroll
+                    for (int q = 1; q < kPer; ++q) v = q == j ? x[q] : v, g = q == j ? noise[q] : g;
+                    if (!(v >= edge && v < sure && v > -INFINITY) && !(sure == INFINITY && v == INFINITY)) continue;
+                    const float t = row.t_of(v);
+                    const int bin = bins.bin(t);
+                    if (bin == d) keep(v, base + i * kPer + j);
+                    if (bin < d && (low == 0.f || expf(-t) >= low)) offer(t, g, base + i * kPer + j);
+                }
+            });
+        if (first >= 0) {
+            const u64 v = static_cast<u64>(ascending(most)) << 32 | (0xFFFFFFFFu - static_cast<unsigned>(base + first));
+            best = v > best ? v : best;
+        } else if (sure < INFINITY && row.top >= sure) {  // scores of -inf (or NaN, which counts as -inf) only: the first kept token
+            each_unit<1>([&](int i, const float (&x)[kPer]) {
+#pragma unroll
+                for (int j = 0; j < kPer; ++j)
+                    if (x[j] >= sure) offer(INFINITY, -INFINITY, base + i * kPer + j);
+            });
+        }
+        __syncthreads();
+        tokens = static_cast<int>(s.maybe_n);
         u64 kept;
-        threshold = refine(bins, d, true, need - min(s.before_mass, need - 1), s.here, each, ~0ull, false, &kept);
+        threshold = refine(bins, d, true, need - min(before_mass, need - 1), here, each, ~0ull, false, &kept);
     }
     each_token([&](float v, int i) {
         const float t = row.t_of(v);
@@ -787,33 +829,35 @@ __device__ void Sampler<kF32, kThreads>::run(int64_t r) {
     answer_of_all();
 }
 
-template <bool kF32, int kThreads>
-__global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(const SampleArgs a) {
+template <bool kF32>
+__global__ void __launch_bounds__(kThreads, kCtasPerSm) sample_kernel(const SampleArgs a) {
     extern __shared__ __align__(16) uint8_t smem[];
     cluster_arrive_release();  // waited for before the first access to another CTA's shared memory
     pdl_trigger_and_wait();
-    Sampler<kF32, kThreads> sampler(*reinterpret_cast<Shared *>(smem), smem + sizeof(Shared), a);
+    Sampler<kF32> sampler(*reinterpret_cast<Shared *>(smem), smem + sizeof(Shared), a);
     sampler.run(blockIdx.x / cluster_size());
 }
 
-template <bool kF32, int kThreads>
+template <bool kF32>
 cudaError_t launch_typed(SampleArgs &a, const DevCtx &ctx, cudaStream_t stream) {
     constexpr int kPer = kF32 ? 4 : 8;
-    // slices of about 16384 logits
+    // The largest cluster of which two waves hold all rows, and slices of 2048 logits at least: a row gains from more CTAs
+    // until they have to queue (256 rows of 128256 fp32 logits: clusters of 1, 2, 4, 8 135, 101, 104, 138 us).
     int size = 1;
-    while (size < kMaxCluster && a.vocab > size * 16384) size *= 2;
+    while (size < kMaxCluster && a.m * size * 2 <= 2 * kCtasPerSm * ctx.num_sms && a.vocab > size * 4096) size *= 2;
     const int units = a.vocab % kPer ? (a.vocab + 2 * kPer - 2) / kPer : a.vocab / kPer;  // what a row touches, at worst
     a.slice_units = (units + size - 1) / size;
+    a.parts = std::min(65535.f, std::floor(4294960000.f / static_cast<float>(a.slice_units * kPer)));
     // room for as many tokens as lets all the CTAs that the registers allow share an SM
-    const int room = (226 * 1024 / (1024 / kThreads) - 1024 - static_cast<int>(sizeof(Shared))) / 6 / 16 * 16;
+    const int room = (226 * 1024 / kCtasPerSm - 1024 - static_cast<int>(sizeof(Shared))) / 8 / 16 * 16;
     a.most = std::min((a.slice_units * kPer + 15) / 16 * 16, room);
-    constexpr auto kernel = sample_kernel<kF32, kThreads>;
+    constexpr auto kernel = sample_kernel<kF32>;
     const cudaError_t e = allow_smem<kernel>(227 * 1024, ctx.device);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(a.m * size));
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = sizeof(Shared) + static_cast<size_t>(a.most) * 6;
+    cfg.dynamicSmemBytes = sizeof(Shared) + static_cast<size_t>(a.most) * 8;
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -844,8 +888,7 @@ cudaError_t launch_sample(const void *logits, int32_t logits_type, int64_t m, in
     a.m = m;
     a.vocab = static_cast<int32_t>(vocab);
     const bool f32 = logits_type == BD_LOGITS_F32;
-    if (m <= 1000000) return f32 ? launch_typed<true, 512>(a, ctx, stream) : launch_typed<false, 512>(a, ctx, stream);
-    return f32 ? launch_typed<true, 256>(a, ctx, stream) : launch_typed<false, 256>(a, ctx, stream);
+    return f32 ? launch_typed<true>(a, ctx, stream) : launch_typed<false>(a, ctx, stream);
 }
 
 }  // namespace bd

@@ -28,12 +28,12 @@ def draw(x, noise, t=None, k=None, p=None, low=None, logprob=True):
     return ids.cpu().numpy(), None if lp is None else lp.cpu().numpy()
 
 
-def check(x, noise, t=1.0, k=0, p=1.0, low=0.0):
+def check(x, noise, t=1.0, k=0, p=1.0, low=0.0, rows=None):
     ids, lp = draw(x, noise, t, k, p, low)
     m = x.shape[0]
     t, k, p, low = (np.broadcast_to(np.asarray(v), (m,)) for v in (t, k, p, low))
     xf = x.float().numpy()
-    for r in range(m):
+    for r in range(m) if rows is None else rows:
         f = np.float32
         tr, pr, lr = f(t[r]), float(f(p[r])), float(f(low[r]))
         ok = {sample(xf[r], noise[r], tr, k[r], pr * c if pr < 1 else pr, lr) for c in (1, 1 - 2.0 ** -18, 1 + 2.0 ** -18)}
@@ -161,6 +161,18 @@ def test_many_rows_repeat_identically():
     kw = dict(t=1.5, k=np.arange(300) * 7 % 1000, p=0.9)
     a, b = draw(x, g, **kw), draw(x, g, **kw)
     assert np.array_equal(a[0], b[0]) and np.array_equal(a[1], b[1])
+
+
+@pytest.mark.parametrize("t", [1.0, 300.0])
+def test_more_rows_than_the_gpu_holds(t):
+    """One CTA per row: at t = 300 all 70001 tokens of it lie in a few bins."""
+    m, v = 700, 70001
+    x = logits(m, v, 6, torch.bfloat16)
+    u = torch.rand((m, v), generator=torch.Generator().manual_seed(1)).clamp_(1e-7, 1 - 1e-7)
+    g = u.log_().neg_().log_().neg_().numpy()
+    k = np.where(np.arange(m) % 3 == 0, 30000, 0)
+    p = np.where(np.arange(m) % 3 == 1, 0.9, 1.0)
+    check(x, g, t=t, k=k, p=p, rows=[0, 1, 2, 349, 350, 697, 699])
 
 
 def test_no_rows_and_refusals():
