@@ -61,12 +61,13 @@ struct SampleArgs {
     float *logprob;
     int64_t m;
     int32_t vocab, slice_units;  // 16-byte units of logits in a CTA's slice
+    int32_t sorted;              // long rows are taken first
     float parts;                 // of a bin's width: what all tokens of a slice add up to still fits 32 bits
     int32_t most;                // tokens that may be kept for which there is room; with more the passes go over the slice
 };
 
 struct alignas(16) Shared {
-    uint2 bins[kBins];  // count, weight
+    uint32_t count[kBins], parts[kBins];  // apart: side by side they would share half of the banks
     u64 list_order[kCap], list_mass[kCap], sorted_mass[kCap];
     u64 warp_mass[kWarps], warp_parts[2][kWarps];
     uint32_t warp_count[kWarps];
@@ -95,9 +96,9 @@ __device__ __forceinline__ void st_remote(uint32_t at, float v) {
 __device__ __forceinline__ void st_remote(uint32_t at, u64 v) {
     asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(at), "l"(v) : "memory");
 }
-__device__ __forceinline__ uint2 ld_remote(uint32_t at) {
-    uint2 v;
-    asm volatile("ld.shared::cluster.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(at) : "memory");
+__device__ __forceinline__ uint32_t ld_remote(uint32_t at) {
+    uint32_t v;
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
     return v;
 }
 __device__ __forceinline__ int cluster_rank() {
@@ -369,7 +370,7 @@ struct Sampler {
         return static_cast<int>(o >> at.shift) & (kBins - 1);
     }
     __device__ __forceinline__ void clear_bins() {
-        s.bins[tid] = make_uint2(0, 0);
+        s.count[tid] = s.parts[tid] = 0;
         __syncthreads();
     }
     __device__ void histogram(const Bins &bins, const Level &at, u64 limit) {
@@ -380,8 +381,8 @@ struct Sampler {
             if (o > limit) return;
             const int d = digit_of(bins, at, t, o);
             if (d < 0) return;
-            atomicAdd(&s.bins[d].x, 1u);
-            atomicAdd(&s.bins[d].y, bins.part(t, at.depth == 0 ? d : at.bin));
+            atomicAdd(&s.count[d], 1u);
+            atomicAdd(&s.parts[d], bins.part(t, at.depth == 0 ? d : at.bin));
         });
     }
     // The cluster's totals of this thread's bin, and each CTA's count in it (four 16-bit fields a word; what is
@@ -390,16 +391,19 @@ struct Sampler {
         u64 lo, hi;
     };
     __device__ __forceinline__ Scan totals(const Bins &bins, const Level &at, Each &each) {
-        uint2 v[kMaxCluster];
+        uint32_t v[kMaxCluster], w[kMaxCluster];
 #pragma unroll
-        for (int q = 0; q < kMaxCluster; ++q) v[q] = q < size ? ld_remote(remote(&s.bins[tid], q)) : make_uint2(0, 0);
+        for (int q = 0; q < kMaxCluster; ++q) {
+            v[q] = q < size ? ld_remote(remote(&s.count[tid], q)) : 0;
+            w[q] = q < size ? ld_remote(remote(&s.parts[tid], q)) : 0;
+        }
         uint32_t n = 0;
         u64 parts = 0;
         each.lo = each.hi = 0;
 #pragma unroll
         for (int q = 0; q < kMaxCluster; ++q) {
-            n += v[q].x, parts += v[q].y;
-            (q < 4 ? each.lo : each.hi) |= static_cast<u64>(min(v[q].x, 0xFFFFu)) << 16 * (q % 4);
+            n += v[q], parts += w[q];
+            (q < 4 ? each.lo : each.hi) |= static_cast<u64>(min(v[q], 0xFFFFu)) << 16 * (q % 4);
         }
         return scan(n, bins.mass(at.depth == 0 ? tid : at.bin, n, parts));
     }
@@ -478,7 +482,7 @@ struct Sampler {
         Level at = {0, d, 0, 0, 0};
         int digit = d;
         *kept = 0;
-        while (here > kCap || limited) {
+        while ((here > kCap || limited) && at.depth < 7) {  // (7 digits tell any two tokens apart)
             limited = false;
             if (at.depth == 1) at.sub = digit;
             if (at.depth > 1) at.prefix = at.prefix << kBits | static_cast<unsigned>(digit);
@@ -500,8 +504,41 @@ struct Sampler {
         return s.threshold;
     }
 
+    __device__ int64_t row_of(int64_t turn);
     __device__ void run(int64_t r);
 };
+
+// The row that the cluster of this number takes: rows with a share p alone first, as they take two to three times as
+// long as others and would otherwise end last (256 rows of every kind: 112 us in their own order, 97 us so).
+template <bool kF32>
+__device__ int64_t Sampler<kF32>::row_of(int64_t turn) {
+    if (!a.sorted) return turn;
+    auto is_long = [&](int64_t r) {
+        const float p = a.top_p[r];
+        const int k = a.top_k ? a.top_k[r] : 0;
+        return p > 0.f && p < 1.f && (k <= 0 || k >= a.vocab) && (!a.temperature || a.temperature[r] > 0.f);
+    };
+    int mine = 0;
+    for (int64_t r = tid; r < a.m; r += kThreads) mine += is_long(r);
+    const int all = __syncthreads_or(mine) ? static_cast<int>(scan(mine, 0).count_all) : 0;
+    if (all == 0) return turn;
+    const bool want = turn < all;
+    int64_t left = want ? turn : turn - all;  // rows of this sort before the one that is wanted
+    for (int64_t r0 = 0; r0 < a.m; r0 += kThreads) {
+        const bool on = r0 + tid < a.m && is_long(r0 + tid) == want;
+        const Scan c = scan(on, 0);
+        if (left >= c.count_all) {
+            left -= c.count_all;
+            continue;
+        }
+        if (on && c.count_upto == left + 1) s.found = static_cast<int>(r0 + tid);
+        __syncthreads();
+        const int64_t r = s.found;
+        __syncthreads();
+        return r;
+    }
+    return turn;  // never
+}
 
 template <bool kF32>
 __device__ void Sampler<kF32>::run(int64_t r) {
@@ -727,8 +764,8 @@ __device__ void Sampler<kF32>::run(int64_t r) {
                 if (!(x[j] >= reach && x[j] > -INFINITY)) continue;
                 const float t = row.t_of(x[j]);
                 const int d = bins.bin(t);
-                atomicAdd(&s.bins[d].x, 1u);
-                atomicAdd(&s.bins[d].y, bins.part(t, d));
+                atomicAdd(&s.count[d], 1u);
+                atomicAdd(&s.parts[d], bins.part(t, d));
             }
         });
     }
@@ -774,8 +811,8 @@ __device__ void Sampler<kF32>::run(int64_t r) {
         const int d = find(c, true, need);
         const u64 before_mass = s.before_mass;
         const uint32_t here = s.here;
-        // Tokens of the bins before d are kept: score them now, and pack those of bin d.  x >= sure lies before d and
-        // x < edge beyond it, so few have to be told by their bin.
+        // Tokens of the bins before d are kept: score them now.  x >= sure lies before d and x < edge beyond it; the
+        // few between are packed and told apart by the threshold.
         const float slack = fabsf(row.top) * 1e-6f + (bins.width * temp) * 1e-2f + range * temp * 1e-6f;
         float edge = d < kBins - 1 ? row.top - (d + 1) * bins.width * temp - slack : -INFINITY;
         edge = edge > reach ? edge : reach;  // (NaN: reach)
@@ -783,29 +820,24 @@ __device__ void Sampler<kF32>::run(int64_t r) {
         if (!(plain && row.top < INFINITY && low == 0.f && sure < INFINITY)) sure = INFINITY;
         float most = -INFINITY;
         int first = -1;
-        each_scored<kF32 ? 4 : 2>(
-            [&](int i, const float (&x)[kPer], const float (&noise)[kPer]) {
-                if (!(largest(x) >= edge)) return;
-                bool close = false;
+        each_scored<kF32 ? 4 : 2>([&](int i, const float (&x)[kPer], const float (&noise)[kPer]) {
+            if (!(largest(x) >= edge)) return;
 #pragma unroll
-                for (int j = 0; j < kPer; ++j) {
+            for (int j = 0; j < kPer; ++j) {
+                if (x[j] >= sure) {
                     const float score = score_of(x[j], noise[j]);
-                    if (x[j] >= sure && score > most) most = score, first = i * kPer + j;
-                    close |= x[j] < sure && x[j] >= edge;
+                    if (score > most) most = score, first = i * kPer + j;
+                } else if (x[j] >= edge && x[j] > -INFINITY) {
+                    keep(x[j], base + i * kPer + j);
                 }
-                if (!close) return;
-#pragma unroll 1
-                for (int j = 0; j < kPer; ++j) {
-                    float v = x[0], g = noise[0];
+            }
+            if (sure == INFINITY) {  // +inf is no score, but a token
 #pragma unroll
-                    for (int q = 1; q < kPer; ++q) v = q == j ? x[q] : v, g = q == j ? noise[q] : g;
-                    if (!(v >= edge && v < sure && v > -INFINITY) && !(sure == INFINITY && v == INFINITY)) continue;
-                    const float t = row.t_of(v);
-                    const int bin = bins.bin(t);
-                    if (bin == d) keep(v, base + i * kPer + j);
-                    if (bin < d && (low == 0.f || expf(-t) >= low)) offer(t, g, base + i * kPer + j);
-                }
-            });
+                for (int j = 0; j < kPer; ++j)
+                    if (x[j] == INFINITY) keep(x[j], base + i * kPer + j);
+            }
+        });
+        if (sure == INFINITY) first = -1;
         if (first >= 0) {
             const u64 v = static_cast<u64>(ascending(most)) << 32 | (0xFFFFFFFFu - static_cast<unsigned>(base + first));
             best = v > best ? v : best;
@@ -818,6 +850,7 @@ __device__ void Sampler<kF32>::run(int64_t r) {
         }
         __syncthreads();
         tokens = static_cast<int>(s.maybe_n);
+        reach = edge;
         u64 kept;
         threshold = refine(bins, d, true, need - min(before_mass, need - 1), here, each, ~0ull, false, &kept);
     }
@@ -835,14 +868,14 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) sample_kernel(const Samp
     cluster_arrive_release();  // waited for before the first access to another CTA's shared memory
     pdl_trigger_and_wait();
     Sampler<kF32> sampler(*reinterpret_cast<Shared *>(smem), smem + sizeof(Shared), a);
-    sampler.run(blockIdx.x / cluster_size());
+    sampler.run(sampler.row_of(blockIdx.x / cluster_size()));
 }
 
 template <bool kF32>
 cudaError_t launch_typed(SampleArgs &a, const DevCtx &ctx, cudaStream_t stream) {
     constexpr int kPer = kF32 ? 4 : 8;
     // The largest cluster of which two waves hold all rows, and slices of 2048 logits at least: a row gains from more CTAs
-    // until they have to queue (256 rows of 128256 fp32 logits: clusters of 1, 2, 4, 8 135, 101, 104, 138 us).
+    // until they have to queue (256 rows of 128256 fp32 logits: clusters of 1, 2, 4 149, 97, 106 us).
     int size = 1;
     while (size < kMaxCluster && a.m * size * 2 <= 2 * kCtasPerSm * ctx.num_sms && a.vocab > size * 4096) size *= 2;
     const int units = a.vocab % kPer ? (a.vocab + 2 * kPer - 2) / kPer : a.vocab / kPer;  // what a row touches, at worst
@@ -854,6 +887,8 @@ cudaError_t launch_typed(SampleArgs &a, const DevCtx &ctx, cudaStream_t stream) 
     constexpr auto kernel = sample_kernel<kF32>;
     const cudaError_t e = allow_smem<kernel>(227 * 1024, ctx.device);
     if (e != cudaSuccess) return e;
+    // in more than one wave, and while looking through all rows takes less time than a row
+    a.sorted = a.top_p != nullptr && a.m * size > kCtasPerSm * ctx.num_sms && a.m <= 4096;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(a.m * size));
     cfg.blockDim = dim3(kThreads);
