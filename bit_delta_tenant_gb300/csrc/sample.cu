@@ -75,7 +75,7 @@ struct alignas(16) Shared {
     // written by the cluster's CTAs
     struct Rank {
         float top, sum, low;
-        u64 best;
+        u64 best, in[2], rest[2];
     } ranks[kMaxCluster];
     // written by one thread for its CTA
     u64 before_mass, kept_mass, threshold;
@@ -151,6 +151,13 @@ struct Bins {
     }
     __device__ __forceinline__ uint32_t part(float t, int b) const {
         return b == kBins - 1 ? 0u : __float2uint_rn(fminf(fmaxf(ex2((b * width - t) * kLog2e) - (1.f - width), 0.f) * unit, most));
+    }
+    // The weight in one word, for a bin whose count is not needed.
+    __device__ __forceinline__ uint32_t whole(float t, int b) const {
+        return b == kBins - 1 ? 0u : __float2uint_rn(fminf(ex2((b * width - t) * kLog2e), 1.f) * most);
+    }
+    __device__ __forceinline__ u64 mass_of_whole(int b, u64 parts) const {
+        return b == kBins - 1 ? 0 : __float2ull_rn(static_cast<float>(parts) / most * (ex2(b * width * -kLog2e) * kFixed));
     }
     // fp32 from whole numbers: the same on every CTA, 2^-22 of the weight
     __device__ __forceinline__ u64 mass(int b, uint32_t count, u64 parts) const {
@@ -407,6 +414,12 @@ struct Sampler {
         }
         return scan(n, bins.mass(at.depth == 0 ? tid : at.bin, n, parts));
     }
+    __device__ __forceinline__ Scan totals_of_whole(const Bins &bins) {
+        u64 parts = 0;
+#pragma unroll
+        for (int q = 0; q < kMaxCluster; ++q) parts += q < size ? ld_remote(remote(&s.parts[tid], q)) : 0;
+        return scan(parts > 0, bins.mass_of_whole(tid, parts));
+    }
     // Sends this CTA's tokens of one set to every CTA's list: digit d at level `at`, or with `upto` all bins up to d.
     // The places follow from the counts that every CTA has of every other.
     __device__ void gather(const Bins &bins, const Level &at, int d, bool upto, u64 limit, const Each &each) {
@@ -644,15 +657,14 @@ __device__ void Sampler<kF32>::run(int64_t r) {
         const u64 c = static_cast<u64>(ascending(score)) << 32 | (0xFFFFFFFFu - static_cast<unsigned>(i));
         best = c > best ? c : best;
     };
-    auto fold_best = [&] {
+    auto fold_max = [&](u64 v) {  // over the CTA
 #pragma unroll
-        for (int o = 16; o > 0; o /= 2) {
-            const u64 u = __shfl_xor_sync(0xFFFFFFFFu, best, o);
-            best = u > best ? u : best;
-        }
-        if (lane == 0) s.warp_mass[warp] = best;
+        for (int o = 16; o > 0; o /= 2) v = max(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
         __syncthreads();
-        for (int w = 0; w < kWarps; ++w) best = s.warp_mass[w] > best ? s.warp_mass[w] : best;
+        if (lane == 0) s.warp_mass[warp] = v;
+        __syncthreads();
+        for (int w = 0; w < kWarps; ++w) v = max(v, s.warp_mass[w]);
+        return v;
     };
     auto answer = [&] {  // by one thread of the cluster
         const int id = static_cast<int>(0xFFFFFFFFu - static_cast<uint32_t>(best));
@@ -660,7 +672,7 @@ __device__ void Sampler<kF32>::run(int64_t r) {
         if (a.logprob) a.logprob[r] = -row.t_of(logit(e0 + id)) - logf(weight);
     };
     auto answer_of_all = [&] {
-        fold_best();
+        best = fold_max(best);
         if (tid == 0) st_remote(remote(&s.ranks[rank].best, 0), best);
         cluster_sync_all();
         if (rank == 0 && tid == 0) {
@@ -744,6 +756,8 @@ __device__ void Sampler<kF32>::run(int64_t r) {
         if (place < a.most) maybe_x[place] = x, maybe_at[place] = static_cast<uint32_t>(token);
     };
     if (tid == 0) s.maybe_n = 0;
+    u64 threshold = ~0ull;
+    Each each;
     if (k > 0) {  // few tokens: packed, then counted
         __syncthreads();
         each_unit<kF32 ? 8 : 4>([&](int i, const float (&x)[kPer]) {
@@ -755,25 +769,8 @@ __device__ void Sampler<kF32>::run(int64_t r) {
         __syncthreads();
         tokens = static_cast<int>(s.maybe_n);
         histogram(bins, level0, ~0ull);
-    } else {  // many: counted as they are read
-        clear_bins();
-        each_unit<kF32 ? 4 : 2>([&](int, const float (&x)[kPer]) {
-            if (!(largest(x) >= reach)) return;
-#pragma unroll
-            for (int j = 0; j < kPer; ++j) {
-                if (!(x[j] >= reach && x[j] > -INFINITY)) continue;
-                const float t = row.t_of(x[j]);
-                const int d = bins.bin(t);
-                atomicAdd(&s.count[d], 1u);
-                atomicAdd(&s.parts[d], bins.part(t, d));
-            }
-        });
-    }
-    cluster_sync_all();
-    Each each;
-    const Scan c = totals(bins, level0, each);
-    u64 threshold = ~0ull;
-    if (k > 0) {
+        cluster_sync_all();
+        const Scan c = totals(bins, level0, each);
         const int d = find(c, false, k);
         const uint32_t upto = s.before_count + s.here, need = k - min(s.before_count, k), here = s.here;
         const u64 before_mass = s.before_mass;
@@ -789,8 +786,7 @@ __device__ void Sampler<kF32>::run(int64_t r) {
                 const float t = row.t_of(value_of(~static_cast<uint32_t>(o >> kIndexBits)));
                 if (low == 0.f || expf(-t) >= low) offer(t, a.noise[e0 + token], token);
             }
-            __syncthreads();
-            fold_best();
+            best = fold_max(best);
             if (tid == 0) answer();
             return;
         }
@@ -807,52 +803,104 @@ __device__ void Sampler<kF32>::run(int64_t r) {
             }
         }
     } else {
-        const u64 need = share_of(p, pruned ? __float2ull_rn(weight * kFixed) : c.mass_all);
-        const int d = find(c, true, need);
-        const u64 before_mass = s.before_mass;
-        const uint32_t here = s.here;
-        // Tokens of the bins before d are kept: score them now.  x >= sure lies before d and x < edge beyond it; the
-        // few between are packed and told apart by the threshold.
-        const float slack = fabsf(row.top) * 1e-6f + (bins.width * temp) * 1e-2f + range * temp * 1e-6f;
-        float edge = d < kBins - 1 ? row.top - (d + 1) * bins.width * temp - slack : -INFINITY;
-        edge = edge > reach ? edge : reach;  // (NaN: reach)
-        float sure = d < kBins - 1 ? row.top - d * bins.width * temp + slack : INFINITY;
-        if (!(plain && row.top < INFINITY && low == 0.f && sure < INFINITY)) sure = INFINITY;
+        // The weights of bins, and each thread's best draw among tokens that may be kept.
+        auto key_of = [&](float score, int i) { return static_cast<u64>(ascending(score)) << 32 | (0xFFFFFFFFu - static_cast<unsigned>(i)); };
         float most = -INFINITY;
         int first = -1;
+        clear_bins();
         each_scored<kF32 ? 4 : 2>([&](int i, const float (&x)[kPer], const float (&noise)[kPer]) {
-            if (!(largest(x) >= edge)) return;
+            if (!(largest(x) >= reach)) return;
 #pragma unroll
             for (int j = 0; j < kPer; ++j) {
-                if (x[j] >= sure) {
-                    const float score = score_of(x[j], noise[j]);
-                    if (score > most) most = score, first = i * kPer + j;
-                } else if (x[j] >= edge && x[j] > -INFINITY) {
-                    keep(x[j], base + i * kPer + j);
-                }
-            }
-            if (sure == INFINITY) {  // +inf is no score, but a token
-#pragma unroll
-                for (int j = 0; j < kPer; ++j)
-                    if (x[j] == INFINITY) keep(x[j], base + i * kPer + j);
+                if (!(x[j] >= reach && x[j] > -INFINITY)) continue;
+                const float t = row.t_of(x[j]), score = __fadd_rn(-t, noise[j]);
+                const int b = bins.bin(t);
+                atomicAdd(&s.parts[b], bins.whole(t, b));
+                if (score > most) most = score, first = i * kPer + j;
             }
         });
-        if (sure == INFINITY) first = -1;
+        cluster_sync_all();
+        const Scan c = totals_of_whole(bins);
+        const u64 need = share_of(p, pruned ? __float2ull_rn(weight * kFixed) : c.mass_all);
+        const int d = find(c, true, need);
+        const u64 need_here = need - min(s.before_mass, need - 1);
+        // Of the threads' best draws those before bin d are kept.  Where one that is not (or is of bin d) would beat
+        // them all, its thread looks through its tokens again; mostly none does.
+        auto place = [&](float x, float &t) {  // 0: kept, 1: of bin d, 2: not kept
+            t = row.t_of(x);
+            const int b = bins.bin(t);
+            return low > 0.f && !(expf(-t) >= low) ? 2 : b < d ? 0 : b == d ? 1 : 2;
+        };
+        auto exchange = [&](int round, u64 &in, u64 &rest) {
+            in = fold_max(in), rest = fold_max(rest);
+            if (tid < size) st_remote(remote(&s.ranks[rank].in[round], tid), in), st_remote(remote(&s.ranks[rank].rest[round], tid), rest);
+            cluster_sync_all();
+            for (int q = 0; q < size; ++q) {
+                in = max(in, s.ranks[q].in[round]);
+                rest = max(rest, s.ranks[q].rest[round]);
+            }
+        };
+        u64 own = 0, in = 0, rest = 0;
         if (first >= 0) {
-            const u64 v = static_cast<u64>(ascending(most)) << 32 | (0xFFFFFFFFu - static_cast<unsigned>(base + first));
-            best = v > best ? v : best;
-        } else if (sure < INFINITY && row.top >= sure) {  // scores of -inf (or NaN, which counts as -inf) only: the first kept token
-            each_unit<1>([&](int i, const float (&x)[kPer]) {
-#pragma unroll
-                for (int j = 0; j < kPer; ++j)
-                    if (x[j] >= sure) offer(INFINITY, -INFINITY, base + i * kPer + j);
-            });
+            float t;
+            own = key_of(most, base + first);
+            (place(logit(e0 + base + first), t) == 0 ? in : rest) = own;
         }
+        const bool out = rest > 0;
+        exchange(0, in, rest);
+        if (rest > in && d > 0 && in > 0) {
+            u64 more = 0;
+            rest = 0;
+            if (out && own > in)
+                each_scored<kF32 ? 4 : 2>([&](int i, const float (&x)[kPer], const float (&noise)[kPer]) {
+#pragma unroll 1
+                    for (int j = 0; j < kPer; ++j) {
+                        float v = x[0], g = noise[0], t;
+#pragma unroll
+                        for (int q = 1; q < kPer; ++q) v = q == j ? x[q] : v, g = q == j ? noise[q] : g;
+                        if (!(v >= reach && v > -INFINITY)) continue;
+                        const int where = place(v, t);
+                        const float score = __fadd_rn(-t, g);
+                        if (where == 2 || !(score > -INFINITY)) continue;
+                        const u64 key = key_of(score, base + i * kPer + j);
+                        if (where == 0) more = max(more, key);
+                        else rest = max(rest, key);
+                    }
+                });
+            exchange(1, more, rest);
+            in = max(in, more);
+        }
+        best = in;
+        if (in > rest) {
+            if (rank == 0 && tid == 0) answer();
+            return;
+        }
+        // A token of bin d may be drawn: the bin's tokens are packed and ordered.  Without a draw before it (all of
+        // them -inf, or NaN, which counts as -inf) the tokens before it are offered one by one.
+        each_unit<kF32 ? 4 : 2>([&](int i, const float (&x)[kPer]) {
+            if (!(largest(x) >= reach)) return;
+#pragma unroll 1
+            for (int j = 0; j < kPer; ++j) {
+                float v = x[0];
+#pragma unroll
+                for (int q = 1; q < kPer; ++q) v = q == j ? x[q] : v;
+                if (!(v >= reach && v > -INFINITY)) continue;
+                const float t = row.t_of(v);
+                const int b = bins.bin(t), token = base + i * kPer + j;
+                if (b == d) keep(v, token);
+                else if (in == 0 && b < d && (low == 0.f || expf(-t) >= low)) offer(t, a.noise[e0 + token], token);
+            }
+        });
         __syncthreads();
         tokens = static_cast<int>(s.maybe_n);
-        reach = edge;
+        cluster_sync_all();  // nobody reads the bins any more
+        histogram(bins, level0, ~0ull);
+        cluster_sync_all();
+        const Scan all = totals(bins, level0, each);
+        if (tid == d) s.here = all.count;
+        __syncthreads();
         u64 kept;
-        threshold = refine(bins, d, true, need - min(before_mass, need - 1), here, each, ~0ull, false, &kept);
+        threshold = refine(bins, d, true, need_here, s.here, each, ~0ull, false, &kept);
     }
     each_token([&](float v, int i) {
         const float t = row.t_of(v);
