@@ -32,6 +32,7 @@
 // bits.  The sum of all weights is fp32 in an order fixed by the shape.
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "bd_device.cuh"
 #include "bd_internal.h"
@@ -138,32 +139,39 @@ struct Row {
         return x == top ? 0.f : fminf(__fmul_rn(__fsub_rn(top, x), inv_t), INFINITY);
     }
 };
-// Bins of equal width over [0, range); the last one takes everything from `range` on and weighs nothing.
+// Bins of equal width around multiples of it, up to t = range; the last one takes everything beyond and weighs nothing.
+// Whole numbers come from adding 2^23, which leaves them in a sum's low bits: conversions have an eighth of that rate.
 struct Bins {
-    float scale, width, unit, parts_of, most;  // 1 / width, width, parts / width and its inverse, parts
+    static constexpr float kWhole = 8388608.f;  // 2^23
+    float scale, width, unit, parts_of, most, all, width2;  // 1 / width, width, parts / width, its inverse, parts; see add()
     __device__ __forceinline__ Bins(float range, float parts)
-        : scale((kBins - 1) / range), width(range / (kBins - 1)), unit(parts * scale), parts_of(width / parts), most(parts) {}
-    __device__ __forceinline__ int bin(float t) const {
-        return t < width * (kBins - 1) ? min(static_cast<int>(t * scale), kBins - 2) : kBins - 1;
-    }
+        : scale((kBins - 2) / range), width(range / (kBins - 2)), unit(parts * scale), parts_of(width / parts), most(parts),
+          all(parts * 0.96f), width2(width * kLog2e) {}
+    static __device__ __forceinline__ int whole(float sum) { return __float_as_int(sum) - __float_as_int(kWhole); }  // sum = 2^23 + n
+    __device__ __forceinline__ int bin(float t) const { return min(whole(fmaf(t, scale, kWhole)), kBins - 1); }
+    __device__ __forceinline__ float start(int b) const { return (b - 0.5f) * width; }
     __device__ __forceinline__ int sub(float t, int b) const {  // the same again within a bin
-        return b == kBins - 1 ? 0 : min(max(static_cast<int>((t * scale - b) * kBins), 0), kBins - 1);
+        return b == kBins - 1 ? 0 : min(max(static_cast<int>((t * scale - b + 0.5f) * kBins), 0), kBins - 1);
     }
     __device__ __forceinline__ uint32_t part(float t, int b) const {
-        return b == kBins - 1 ? 0u : __float2uint_rn(fminf(fmaxf(ex2((b * width - t) * kLog2e) - (1.f - width), 0.f) * unit, most));
-    }
-    // The weight in one word, for a bin whose count is not needed.
-    __device__ __forceinline__ uint32_t whole(float t, int b) const {
-        return b == kBins - 1 ? 0u : __float2uint_rn(fminf(ex2((b * width - t) * kLog2e), 1.f) * most);
-    }
-    __device__ __forceinline__ u64 mass_of_whole(int b, u64 parts) const {
-        return b == kBins - 1 ? 0 : __float2ull_rn(static_cast<float>(parts) / most * (ex2(b * width * -kLog2e) * kFixed));
+        return b == kBins - 1 ? 0u : __float2uint_rn(fminf(fmaxf(ex2((start(b) - t) * kLog2e) - (1.f - width), 0.f) * unit, most));
     }
     // fp32 from whole numbers: the same on every CTA, 2^-22 of the weight
     __device__ __forceinline__ u64 mass(int b, uint32_t count, u64 parts) const {
         if (b == kBins - 1) return 0;
         const float w = fmaf(static_cast<float>(parts), parts_of, static_cast<float>(count) * (1.f - width));
-        return __float2ull_rn(w * (ex2(b * width * -kLog2e) * kFixed));
+        return __float2ull_rn(w * (ex2(start(b) * -kLog2e) * kFixed));
+    }
+    // Adds a token to bins that hold their weight in one word, in parts of exp(-b width), and no count: 2^-17 of the
+    // weight, of which the sum of a bin's tokens keeps less.
+    __device__ __forceinline__ void add(uint32_t *bins, float t) const {
+        const float at = fmaf(t, scale, kWhole);
+        const int b = whole(at);
+        const float w = ex2(fmaf(at - kWhole, width2, t * -kLog2e));  // exp(-width / 2) .. exp(width / 2) < 1 / 0.96
+        if (b < kBins - 1) atomicAdd(&bins[b], static_cast<uint32_t>(whole(fmaf(w, all, kWhole))));
+    }
+    __device__ __forceinline__ u64 mass_of(int b, u64 parts) const {
+        return b == kBins - 1 ? 0 : __float2ull_rn(static_cast<float>(parts) / all * (ex2(b * -width2) * kFixed));
     }
 };
 // floor(p * mass) for 0 < p < 1, at least 1: the first token always stays
@@ -287,6 +295,19 @@ struct Sampler {
                 f(i, x, noise[q]);
             }
         }
+    }
+    // x and noise of one unit
+    __device__ __forceinline__ void read_scored(int i, float (&x)[kPer], float (&noise)[kPer]) const {
+        const bool in = inside(i);
+        const float *g = a.noise + (e0 + base) + static_cast<int64_t>(i) * kPer;
+        const uint4 raw = in ? fetch(i) : make_uint4(0, 0, 0, 0);
+        if (in)
+#pragma unroll
+            for (int j = 0; j < kPer; ++j) noise[j] = __ldg(g + j);
+        read(i, in, raw, x);
+        if (!in)
+#pragma unroll
+            for (int j = 0; j < kPer; ++j) noise[j] = x[j] > -INFINITY ? g[j] : 0.f;
     }
     // f(x, token) for this thread's share of the tokens that may be kept
     template <class F>
@@ -418,7 +439,7 @@ struct Sampler {
         u64 parts = 0;
 #pragma unroll
         for (int q = 0; q < kMaxCluster; ++q) parts += q < size ? ld_remote(remote(&s.parts[tid], q)) : 0;
-        return scan(parts > 0, bins.mass_of_whole(tid, parts));
+        return scan(parts > 0, bins.mass_of(tid, parts));
     }
     // Sends this CTA's tokens of one set to every CTA's list: digit d at level `at`, or with `upto` all bins up to d.
     // The places follow from the counts that every CTA has of every other.
@@ -806,19 +827,24 @@ __device__ void Sampler<kF32>::run(int64_t r) {
         // The weights of bins, and each thread's best draw among tokens that may be kept.
         auto key_of = [&](float score, int i) { return static_cast<u64>(ascending(score)) << 32 | (0xFFFFFFFFu - static_cast<unsigned>(i)); };
         float most = -INFINITY;
-        int first = -1;
+        int unit = -1;
         clear_bins();
-        each_scored<kF32 ? 4 : 2>([&](int i, const float (&x)[kPer], const float (&noise)[kPer]) {
-            if (!(largest(x) >= reach)) return;
+        auto weigh = [&](auto exact) {
+            each_scored<kF32 ? 4 : 2>([&](int i, const float (&x)[kPer], const float (&noise)[kPer]) {
+                if (!(largest(x) >= reach)) return;
+                float score[kPer];
 #pragma unroll
-            for (int j = 0; j < kPer; ++j) {
-                if (!(x[j] >= reach && x[j] > -INFINITY)) continue;
-                const float t = row.t_of(x[j]), score = __fadd_rn(-t, noise[j]);
-                const int b = bins.bin(t);
-                atomicAdd(&s.parts[b], bins.whole(t, b));
-                if (score > most) most = score, first = i * kPer + j;
-            }
-        });
+                for (int j = 0; j < kPer; ++j) {
+                    const float t = exact ? row.t_of(x[j]) : __fmul_rn(__fsub_rn(row.top, x[j]), row.inv_t);
+                    score[j] = __fadd_rn(-t, noise[j]);
+                    bins.add(s.parts, t);
+                }
+                const float here = largest(score);
+                if (here > most) most = here, unit = i;
+            });
+        };
+        if (plain && row.top < INFINITY) weigh(std::false_type{});
+        else weigh(std::true_type{});
         cluster_sync_all();
         const Scan c = totals_of_whole(bins);
         const u64 need = share_of(p, pruned ? __float2ull_rn(weight * kFixed) : c.mass_all);
@@ -832,19 +858,32 @@ __device__ void Sampler<kF32>::run(int64_t r) {
             return low > 0.f && !(expf(-t) >= low) ? 2 : b < d ? 0 : b == d ? 1 : 2;
         };
         auto exchange = [&](int round, u64 &in, u64 &rest) {
-            in = fold_max(in), rest = fold_max(rest);
-            if (tid < size) st_remote(remote(&s.ranks[rank].in[round], tid), in), st_remote(remote(&s.ranks[rank].rest[round], tid), rest);
-            cluster_sync_all();
-            for (int q = 0; q < size; ++q) {
-                in = max(in, s.ranks[q].in[round]);
-                rest = max(rest, s.ranks[q].rest[round]);
+#pragma unroll
+            for (int o = 16; o > 0; o /= 2) {
+                in = max(in, __shfl_xor_sync(0xFFFFFFFFu, in, o));
+                rest = max(rest, __shfl_xor_sync(0xFFFFFFFFu, rest, o));
             }
+            __syncthreads();
+            if (lane == 0) s.warp_parts[0][warp] = in, s.warp_parts[1][warp] = rest;
+            __syncthreads();
+            if (warp == 0 && lane < size) {
+                for (int w = 0; w < kWarps; ++w) in = max(in, s.warp_parts[0][w]), rest = max(rest, s.warp_parts[1][w]);
+                st_remote(remote(&s.ranks[rank].in[round], lane), in), st_remote(remote(&s.ranks[rank].rest[round], lane), rest);
+            }
+            cluster_sync_all();
+            in = rest = 0;
+            for (int q = 0; q < size; ++q) in = max(in, s.ranks[q].in[round]), rest = max(rest, s.ranks[q].rest[round]);
         };
         u64 own = 0, in = 0, rest = 0;
-        if (first >= 0) {
+        if (unit >= 0) {
+            float x[kPer], noise[kPer], at = -INFINITY;
+            read_scored(unit, x, noise);
+#pragma unroll
+            for (int j = kPer - 1; j >= 0; --j)  // the first of the unit's tokens with that score
+                if (x[j] > -INFINITY && __fadd_rn(-row.t_of(x[j]), noise[j]) == most) own = key_of(most, base + unit * kPer + j), at = x[j];
             float t;
-            own = key_of(most, base + first);
-            (place(logit(e0 + base + first), t) == 0 ? in : rest) = own;
+            in = place(at, t) == 0 ? own : 0;
+            rest = in ? 0 : own;
         }
         const bool out = rest > 0;
         exchange(0, in, rest);
@@ -853,18 +892,16 @@ __device__ void Sampler<kF32>::run(int64_t r) {
             rest = 0;
             if (out && own > in)
                 each_scored<kF32 ? 4 : 2>([&](int i, const float (&x)[kPer], const float (&noise)[kPer]) {
-#pragma unroll 1
-                    for (int j = 0; j < kPer; ++j) {
-                        float v = x[0], g = noise[0], t;
+                    if (!(largest(x) >= reach)) return;
+                    const float least = value_of(static_cast<uint32_t>(in >> 32));
 #pragma unroll
-                        for (int q = 1; q < kPer; ++q) v = q == j ? x[q] : v, g = q == j ? noise[q] : g;
-                        if (!(v >= reach && v > -INFINITY)) continue;
-                        const int where = place(v, t);
-                        const float score = __fadd_rn(-t, g);
-                        if (where == 2 || !(score > -INFINITY)) continue;
-                        const u64 key = key_of(score, base + i * kPer + j);
+                    for (int j = 0; j < kPer; ++j) {
+                        if (!(__fadd_rn(-row.t_of(x[j]), noise[j]) >= least) || x[j] == -INFINITY) continue;
+                        float t;
+                        const int where = place(x[j], t);
+                        const u64 key = key_of(__fadd_rn(-t, noise[j]), base + i * kPer + j);
                         if (where == 0) more = max(more, key);
-                        else rest = max(rest, key);
+                        if (where == 1) rest = max(rest, key);
                     }
                 });
             exchange(1, more, rest);
@@ -877,22 +914,29 @@ __device__ void Sampler<kF32>::run(int64_t r) {
         }
         // A token of bin d may be drawn: the bin's tokens are packed and ordered.  Without a draw before it (all of
         // them -inf, or NaN, which counts as -inf) the tokens before it are offered one by one.
-        each_unit<kF32 ? 4 : 2>([&](int i, const float (&x)[kPer]) {
-            if (!(largest(x) >= reach)) return;
-#pragma unroll 1
-            for (int j = 0; j < kPer; ++j) {
-                float v = x[0];
+        const float slack = fabsf(row.top) * 1e-6f + (bins.width * temp) * 1e-2f + range * temp * 1e-6f;
+        float edge = row.top - (d + 0.5f) * bins.width * temp - slack;  // below any token of bin d
+        if (!(edge > reach && d < kBins - 1 && plain && row.top < INFINITY)) edge = reach;
+        float sure = row.top - (d - 0.5f) * bins.width * temp + slack;  // above any
+        if (!(edge > reach && in > 0)) sure = INFINITY;
+        each_unit<kF32 ? 8 : 4>([&](int i, const float (&x)[kPer]) {
+            if (!(largest(x) >= edge)) return;
 #pragma unroll
-                for (int q = 1; q < kPer; ++q) v = q == j ? x[q] : v;
-                if (!(v >= reach && v > -INFINITY)) continue;
-                const float t = row.t_of(v);
-                const int b = bins.bin(t), token = base + i * kPer + j;
-                if (b == d) keep(v, token);
-                else if (in == 0 && b < d && (low == 0.f || expf(-t) >= low)) offer(t, a.noise[e0 + token], token);
+            for (int j = 0; j < kPer; ++j) {
+                if (!(x[j] >= edge && x[j] > -INFINITY && !(x[j] > sure))) continue;
+                if (in > 0) {
+                    keep(x[j], base + i * kPer + j);  // of bin d or beside it
+                } else {
+                    const float t = row.t_of(x[j]);
+                    const int b = bins.bin(t), token = base + i * kPer + j;
+                    if (b == d) keep(x[j], token);
+                    else if (b < d && (low == 0.f || expf(-t) >= low)) offer(t, a.noise[e0 + token], token);
+                }
             }
         });
         __syncthreads();
         tokens = static_cast<int>(s.maybe_n);
+        reach = edge;
         cluster_sync_all();  // nobody reads the bins any more
         histogram(bins, level0, ~0ull);
         cluster_sync_all();
