@@ -5,31 +5,38 @@
 //
 // Bound: HBM for many rows (the logits once, the noise at kept tokens), latency
 // for one.  A row belongs to a cluster of CTAs with a slice of it each.  A slice is
-// read twice, the second time out of L2: holding it in shared memory between left
-// room for two CTAs per SM only, and a row is a chain of short steps with cluster
+// read again out of L2 where a filter needs that: holding it in shared memory between
+// left room for two CTAs per SM only, and a row is a chain of short steps with cluster
 // barriers between them that other rows' CTAs have to fill.  The passes are short
 // loops: unrolled over a row in registers they were bound by fetching their code.
 //
-// The first pass takes the largest logit and the sum of weights relative to it, the
-// second one draws from an unfiltered row, or packs the tokens that a filter may keep
-// into shared memory.  The filters are a threshold in the order (x descending, index
-// ascending), found without sorting:
+// The first pass takes the largest logit and the sum of weights relative to it, and
+// draws from an unfiltered row, to within rounding (see `open`).  The filters are a
+// threshold in the order (x descending, index ascending), found without sorting:
 //  1. Tokens that cannot be kept are left out.  top-k: every warp of the cluster has
 //     j = ceil(k / warps) threads whose largest logit reaches the warp's j-th largest, so
 //     k tokens reach the smallest of these.  top-p: tokens with t = -z above
 //     ln(V / ((1 - p) sum w)) weigh less than (1 - p) sum w together, so the prefix
 //     ends before them.
-//  2. A histogram over t holds each bin's count and weight.  Every CTA adds up the
-//     cluster's bins and scans them, and finds the bin that the k-th token or the share p
-//     falls into.
-//  3. The tokens of that bin (all bins up to it, if those are few: top-k as used) are
-//     sent to every CTA and ordered exactly.  A bin with too many tokens is split again,
-//     by the remaining bits of t, then by the bits of (x, index), which differ for any two.
+//  2. A histogram over t holds each bin's weight, and for top-k its count.  Every CTA adds
+//     up the cluster's bins and scans them, and finds the bin that the k-th token or the
+//     share p falls into.  top-k has packed its few tokens into shared memory before;
+//     top-p counts what may be most of the row as it reads it, and keeps each thread's best
+//     draw.  The best of these is the answer if it lies before that bin, which it does
+//     with about probability p; else the threads that had a better one look again.
+//  3. For top-k, and where the answer may lie in that very bin, the bin's tokens (for top-k
+//     all bins up to it, if those are few) are sent to every CTA and ordered exactly.  A bin
+//     with too many tokens is split again, by the remaining bits of t, then by the bits of
+//     (x, index), which differ for any two.
+// Measured, rows of 128256 fp32 logits: one row with top-k and top-p 14.5 us; 256 rows unfiltered 57 us (4.6 TB/s),
+// top-k 65, top-p 137, min-p 49, greedy 31, of every kind 77.
 //
-// Sums of weights do not depend on the order of atomics: within a bin of width d,
-// w = exp(-bin d) w' with w' in [1 - d, 1], and a bin sums round((w' - 1 + d) P / d) in
-// 32 bits beside its count, P = 65535 or what a long slice leaves room for; across bins weights are fixed-point with 40 fractional
-// bits.  The sum of all weights is fp32 in an order fixed by the shape.
+// Sums of weights do not depend on the order of atomics: they are whole numbers.  Within a
+// bin of width d, w = exp(-start) w' with w' in [1 - d, 1], and a bin sums
+// round((w' - 1 + d) P / d) in 32 bits beside its count, P = 65535 or what a long slice
+// leaves room for; top-p's first histogram, which needs no counts, sums round(w' P).
+// Across bins weights are fixed-point with 40 fractional bits.  The sum of all weights is
+// fp32 in an order fixed by the shape.
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
@@ -72,10 +79,10 @@ struct alignas(16) Shared {
     u64 list_order[kCap], list_mass[kCap], sorted_mass[kCap];
     u64 warp_mass[kWarps], warp_parts[2][kWarps];
     uint32_t warp_count[kWarps];
-    float warp_value[3][kWarps];
+    float warp_value[5][kWarps];
     // written by the cluster's CTAs
     struct Rank {
-        float top, sum, low;
+        float top, sum, low, draw, noise;
         u64 best, in[2], rest[2];
     } ranks[kMaxCluster];
     // written by one thread for its CTA
@@ -242,72 +249,71 @@ struct Sampler {
             }
         }
     }
-    // f(i, x) for this thread's units of the slice, kAtOnce loads in flight
-    template <int kAtOnce, class F>
+    // f(i, x) for this thread's units of the slice, a few loads ahead (twice as many at once, or loads of a batch
+    // before its use, spill and take 3 to 10% longer)
+    template <class F>
     __device__ __forceinline__ void each_unit(F f) const {
-        for (int i0 = tid; i0 < units; i0 += kAtOnce * kThreads) {
-            uint4 raw[kAtOnce];
-            bool in[kAtOnce];
+        constexpr int kAhead = kF32 ? 4 : 3;
+        uint4 raw[kAhead];
+        auto load = [&](int q, int i) { raw[q] = inside(i) ? fetch(i) : make_uint4(0, 0, 0, 0); };
 #pragma unroll
-            for (int q = 0; q < kAtOnce; ++q) {
-                in[q] = inside(i0 + q * kThreads);
-                raw[q] = in[q] ? fetch(i0 + q * kThreads) : make_uint4(0, 0, 0, 0);
-            }
+        for (int q = 0; q < kAhead; ++q) load(q, tid + q * kThreads);
+        for (int i0 = tid; i0 < units; i0 += kAhead * kThreads) {
 #pragma unroll
-            for (int q = 0; q < kAtOnce; ++q) {
-                const int i = i0 + q * kThreads;
-                if (i >= units) break;
-                float x[kPer];
-                read(i, in[q], raw[q], x);
-                f(i, x);
-            }
-        }
-    }
-    // f(i, x, noise) for this thread's units, the logits and the noise of kAtOnce units in flight together
-    template <int kAtOnce, class F>
-    __device__ __forceinline__ void each_scored(F f) const {
-        for (int i0 = tid; i0 < units; i0 += kAtOnce * kThreads) {
-            uint4 raw[kAtOnce];
-            float noise[kAtOnce][kPer];
-#pragma unroll
-            for (int q = 0; q < kAtOnce; ++q) {
-                const int i = i0 + q * kThreads;
-                if (!inside(i)) continue;
-                raw[q] = fetch(i);
-                const float *g = a.noise + (e0 + base) + static_cast<int64_t>(i) * kPer;
-#pragma unroll
-                for (int j = 0; j < kPer; j += 4) {
-                    const float4 v = __ldg(reinterpret_cast<const float4 *>(g + j));
-                    noise[q][j] = v.x, noise[q][j + 1] = v.y, noise[q][j + 2] = v.z, noise[q][j + 3] = v.w;
-                }
-            }
-#pragma unroll
-            for (int q = 0; q < kAtOnce; ++q) {
+            for (int q = 0; q < kAhead; ++q) {
                 const int i = i0 + q * kThreads;
                 if (i >= units) break;
                 float x[kPer];
                 read(i, inside(i), raw[q], x);
-                if (!inside(i)) {
-#pragma unroll
-                    for (int j = 0; j < kPer; ++j)
-                        noise[q][j] = x[j] > -INFINITY ? a.noise[e0 + base + static_cast<int64_t>(i) * kPer + j] : 0.f;
-                }
-                f(i, x, noise[q]);
+                load(q, i + kAhead * kThreads);
+                f(i, x);
             }
+        }
+    }
+    // f(i, x, noise) for this thread's units, one ahead (two: 256 unfiltered bf16 rows 69 us, one 54)
+    template <class F>
+    __device__ __forceinline__ void each_scored(F f) const {
+        uint4 raw;
+        float next[kPer];
+        auto load = [&](int i) {
+            if (inside(i)) raw = fetch(i), fetch_noise(i, next);
+        };
+        load(tid);
+        for (int i = tid; i < units; i += kThreads) {
+            float x[kPer], noise[kPer];
+            read(i, inside(i), raw, x);
+            finish_noise(i, x, next, noise);
+            load(i + kThreads);
+            f(i, x, noise);
+        }
+    }
+    __device__ __forceinline__ void fetch_noise(int i, float (&noise)[kPer]) const {
+        const float *g = a.noise + (e0 + base) + static_cast<int64_t>(i) * kPer;
+#pragma unroll
+        for (int j = 0; j < kPer; j += 4)
+            asm volatile("ld.global.nc.v4.f32 {%0, %1, %2, %3}, [%4];"
+                         : "=f"(noise[j]), "=f"(noise[j + 1]), "=f"(noise[j + 2]), "=f"(noise[j + 3])
+                         : "l"(g + j));
+    }
+    // the same of a unit at a ragged end, for its tokens in the row
+    __device__ __forceinline__ void finish_noise(int i, const float (&x)[kPer], const float (&fetched)[kPer], float (&noise)[kPer]) const {
+        if (inside(i)) {
+#pragma unroll
+            for (int j = 0; j < kPer; ++j) noise[j] = fetched[j];
+        } else {
+#pragma unroll
+            for (int j = 0; j < kPer; ++j)
+                noise[j] = x[j] > -INFINITY ? a.noise[e0 + base + static_cast<int64_t>(i) * kPer + j] : 0.f;
         }
     }
     // x and noise of one unit
     __device__ __forceinline__ void read_scored(int i, float (&x)[kPer], float (&noise)[kPer]) const {
         const bool in = inside(i);
-        const float *g = a.noise + (e0 + base) + static_cast<int64_t>(i) * kPer;
-        const uint4 raw = in ? fetch(i) : make_uint4(0, 0, 0, 0);
-        if (in)
-#pragma unroll
-            for (int j = 0; j < kPer; ++j) noise[j] = __ldg(g + j);
+        uint4 raw = make_uint4(0, 0, 0, 0);
+        float fetched[kPer];
+        if (in) raw = fetch(i), fetch_noise(i, fetched);
         read(i, in, raw, x);
-        if (!in)
-#pragma unroll
-            for (int j = 0; j < kPer; ++j) noise[j] = x[j] > -INFINITY ? g[j] : 0.f;
+        finish_noise(i, x, fetched, noise);
     }
     // f(x, token) for this thread's share of the tokens that may be kept
     template <class F>
@@ -315,7 +321,7 @@ struct Sampler {
         if (tokens <= a.most) {
             for (int i = tid; i < tokens; i += kThreads) f(maybe_x[i], static_cast<int>(maybe_at[i]));
         } else {
-            each_unit<4>([&](int i, const float (&x)[kPer]) {
+            each_unit([&](int i, const float (&x)[kPer]) {
                 if (!(largest(x) >= reach)) return;
 #pragma unroll 1
                 for (int j = 0; j < kPer; ++j) {
@@ -543,7 +549,7 @@ struct Sampler {
 };
 
 // The row that the cluster of this number takes: rows with a share p alone first, as they take two to three times as
-// long as others and would otherwise end last (256 rows of every kind: 112 us in their own order, 97 us so).
+// long as others and would otherwise end last (256 rows of every kind: 87 us in their own order, 77 us so).
 template <bool kF32>
 __device__ int64_t Sampler<kF32>::row_of(int64_t turn) {
     if (!a.sorted) return turn;
@@ -595,8 +601,9 @@ __device__ void Sampler<kF32>::run(int64_t r) {
     if (!(p > 0.f && p < 1.f) || k == 1) p = 1.f;
     low = low > 0.f ? fminf(low, 1.f) : 0.f;
     const bool filtered = !greedy && (k > 0 || p < 1.f);
-    // noise of which most will be read is on its way into L2 meanwhile
-    if (tid == 0 && !greedy && k == 0 && low == 0.f) {
+    const bool open = !greedy && !filtered && low == 0.f;
+    // noise of which most will be read later is on its way into L2 meanwhile
+    if (tid == 0 && !greedy && k == 0 && p < 1.f) {
         const int64_t n = min(static_cast<int64_t>(units), a.m * a.vocab / kPer - u0);
         if (n > 0)
             asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(a.noise + u0 * kPer), "r"(static_cast<uint32_t>(n * kPer * 4))
@@ -609,7 +616,7 @@ __device__ void Sampler<kF32>::run(int64_t r) {
     const bool plain = per > 0.f && per < INFINITY;
     float top = -INFINITY, shift = 0.f, sum = 0.f;
     int top_unit = 0;
-    each_unit<kF32 ? 8 : 4>([&](int i, const float (&x)[kPer]) {
+    auto weigh = [&](int i, const float (&x)[kPer]) {
         const float here = largest(x);
         if (here > top) {
             const float to = here * per;
@@ -618,7 +625,24 @@ __device__ void Sampler<kF32>::run(int64_t r) {
         }
 #pragma unroll
         for (int j = 0; j < kPer; ++j) sum += ex2(fmaf(x[j], per, -shift));
-    });
+    };
+    // An unfiltered row is drawn from in the same pass: scores without M, x / T + g, are off by little, so the threads
+    // that may have met the best one are known once all have, and look at it again.
+    float most = -INFINITY, second = -INFINITY, loudest = -INFINITY;
+    int draw_unit = -1;
+    if (open)
+        each_scored([&](int i, const float (&x)[kPer], const float (&noise)[kPer]) {
+            weigh(i, x);
+            float score[kPer];
+#pragma unroll
+            for (int j = 0; j < kPer; ++j) score[j] = fmaf(x[j], row.inv_t, noise[j]);
+            const float here = largest(score);
+            loudest = fmaxf(loudest, largest(noise));
+            if (here > most) second = most, most = here, draw_unit = i;
+            else second = fmaxf(second, here);
+        });
+    else
+        each_unit(weigh);
 
     // This CTA's largest logit, the sum of its weights relative to it, and for top-k its bound: j threads of every
     // warp reach it.
@@ -648,13 +672,15 @@ __device__ void Sampler<kF32>::run(int64_t r) {
         }
     }
     sum = block_fold<false>(sum, s.warp_value[2]);
+    float cta_most = -INFINITY;
+    if (open) cta_most = block_fold<true>(most, s.warp_value[3]), loudest = block_fold<true>(loudest, s.warp_value[4]);
     __syncwarp();
     cluster_wait_acquire();  // every CTA of the cluster runs: its shared memory may be written
     if (tid < size) {
         if (filtered && k > 0)
             for (int w = 0; w < kWarps; ++w) reach = fminf(reach, s.warp_value[0][w]);
         const uint32_t to = remote(&s.ranks[rank], tid);
-        st_remote(to, cta_top), st_remote(to + 4, sum), st_remote(to + 8, reach);
+        st_remote(to, cta_top), st_remote(to + 4, sum), st_remote(to + 8, reach), st_remote(to + 12, cta_most), st_remote(to + 16, loudest);
     }
     cluster_sync_all();
     row.top = s.ranks[0].top;
@@ -712,22 +738,32 @@ __device__ void Sampler<kF32>::run(int64_t r) {
         answer_of_all();
         return;
     }
-    auto score_of = [&](float x, float noise) {  // where nothing is at the end of its range
-        return __fadd_rn(__fmul_rn(__fsub_rn(x, row.top), row.inv_t), noise);
-    };
-    if (!filtered && low == 0.f && plain && row.top < INFINITY) {  // every token
-        float most = -INFINITY;
+    if (open && plain && row.top < INFINITY) {
+        for (int c = 0; c < size; ++c) cta_most = fmaxf(cta_most, s.ranks[c].draw), loudest = fmaxf(loudest, s.ranks[c].noise);
+        // A first look is off by 2^-24 of itself, the score by that of itself and twice that of z, all of which
+        // this bounds for the best of either; `least` is below the first look of the best score.
+        const float size_of = fabsf(row.top * row.inv_t) + fabsf(cta_most) + fabsf(loudest);
+        const bool sharp = size_of < 1e30f;  // (not with NaN)
+        const float least = sharp ? cta_most - size_of * 9.5367431640625e-7f : -INFINITY;  // 2^-20
+        float score = -INFINITY;
         int first = -1;  // of equal scores the one met first has the lowest index
-        each_scored<kF32 ? 4 : 2>([&](int i, const float (&x)[kPer], const float (&noise)[kPer]) {
+        auto look = [&](int i, const float (&x)[kPer], const float (&noise)[kPer]) {
 #pragma unroll
-                                            for (int j = 0; j < kPer; ++j) {
-                                                const float score = score_of(x[j], noise[j]);
-                                                if (score > most) most = score, first = i * kPer + j;
-                                            }
-                                        });
-        if (first >= 0) best = static_cast<u64>(ascending(most)) << 32 | (0xFFFFFFFFu - static_cast<unsigned>(base + first));
-        if (!__syncthreads_or(first >= 0)) {  // a slice whose scores are all -inf (or NaN, which counts as -inf): its first token
-            each_unit<1>([&](int i, const float (&x)[kPer]) {
+            for (int j = 0; j < kPer; ++j) {
+                const float v = __fadd_rn(__fmul_rn(__fsub_rn(x[j], row.top), row.inv_t), noise[j]);
+                if (v > score) score = v, first = i * kPer + j;
+            }
+        };
+        if (second >= least) {
+            each_scored(look);
+        } else if (most >= least && draw_unit >= 0) {
+            float x[kPer], noise[kPer];
+            read_scored(draw_unit, x, noise);
+            look(draw_unit, x, noise);
+        }
+        if (first >= 0) best = static_cast<u64>(ascending(score)) << 32 | (0xFFFFFFFFu - static_cast<unsigned>(base + first));
+        if (!sharp && !__syncthreads_or(first >= 0)) {  // a slice whose scores are all -inf (or NaN, which counts as -inf): its first token
+            each_unit([&](int i, const float (&x)[kPer]) {
 #pragma unroll
                 for (int j = 0; j < kPer; ++j)
                     if (x[j] > -INFINITY) offer(INFINITY, -INFINITY, base + i * kPer + j);
@@ -740,7 +776,7 @@ __device__ void Sampler<kF32>::run(int64_t r) {
         float least = plain && row.top < INFINITY && low > 0.f ? row.top + logf(low) * temp : -INFINITY;
         least -= fabsf(least) * 1e-6f + temp * 1e-6f;  // below any token that the exact test keeps
         if (!(least > -INFINITY)) least = -INFINITY;
-        each_unit<kF32 ? 8 : 4>([&](int i, const float (&x)[kPer]) {
+        each_unit([&](int i, const float (&x)[kPer]) {
             if (largest(x) < least) return;
 #pragma unroll
             for (int j = 0; j < kPer; ++j) {
@@ -781,7 +817,7 @@ __device__ void Sampler<kF32>::run(int64_t r) {
     Each each;
     if (k > 0) {  // few tokens: packed, then counted
         __syncthreads();
-        each_unit<kF32 ? 8 : 4>([&](int i, const float (&x)[kPer]) {
+        each_unit([&](int i, const float (&x)[kPer]) {
             if (!(largest(x) >= reach)) return;
 #pragma unroll
             for (int j = 0; j < kPer; ++j)
@@ -826,11 +862,10 @@ __device__ void Sampler<kF32>::run(int64_t r) {
     } else {
         // The weights of bins, and each thread's best draw among tokens that may be kept.
         auto key_of = [&](float score, int i) { return static_cast<u64>(ascending(score)) << 32 | (0xFFFFFFFFu - static_cast<unsigned>(i)); };
-        float most = -INFINITY;
         int unit = -1;
         clear_bins();
-        auto weigh = [&](auto exact) {
-            each_scored<kF32 ? 4 : 2>([&](int i, const float (&x)[kPer], const float (&noise)[kPer]) {
+        auto weigh_bins = [&](auto exact) {
+            each_scored([&](int i, const float (&x)[kPer], const float (&noise)[kPer]) {
                 if (!(largest(x) >= reach)) return;
                 float score[kPer];
 #pragma unroll
@@ -843,8 +878,8 @@ __device__ void Sampler<kF32>::run(int64_t r) {
                 if (here > most) most = here, unit = i;
             });
         };
-        if (plain && row.top < INFINITY) weigh(std::false_type{});
-        else weigh(std::true_type{});
+        if (plain && row.top < INFINITY) weigh_bins(std::false_type{});
+        else weigh_bins(std::true_type{});
         cluster_sync_all();
         const Scan c = totals_of_whole(bins);
         const u64 need = share_of(p, pruned ? __float2ull_rn(weight * kFixed) : c.mass_all);
@@ -891,7 +926,7 @@ __device__ void Sampler<kF32>::run(int64_t r) {
             u64 more = 0;
             rest = 0;
             if (out && own > in)
-                each_scored<kF32 ? 4 : 2>([&](int i, const float (&x)[kPer], const float (&noise)[kPer]) {
+                each_scored([&](int i, const float (&x)[kPer], const float (&noise)[kPer]) {
                     if (!(largest(x) >= reach)) return;
                     const float least = value_of(static_cast<uint32_t>(in >> 32));
 #pragma unroll
@@ -919,7 +954,7 @@ __device__ void Sampler<kF32>::run(int64_t r) {
         if (!(edge > reach && d < kBins - 1 && plain && row.top < INFINITY)) edge = reach;
         float sure = row.top - (d - 0.5f) * bins.width * temp + slack;  // above any
         if (!(edge > reach && in > 0)) sure = INFINITY;
-        each_unit<kF32 ? 8 : 4>([&](int i, const float (&x)[kPer]) {
+        each_unit([&](int i, const float (&x)[kPer]) {
             if (!(largest(x) >= edge)) return;
 #pragma unroll
             for (int j = 0; j < kPer; ++j) {
@@ -966,10 +1001,12 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) sample_kernel(const Samp
 template <bool kF32>
 cudaError_t launch_typed(SampleArgs &a, const DevCtx &ctx, cudaStream_t stream) {
     constexpr int kPer = kF32 ? 4 : 8;
-    // The largest cluster of which two waves hold all rows, and slices of 2048 logits at least: a row gains from more CTAs
-    // until they have to queue (256 rows of 128256 fp32 logits: clusters of 1, 2, 4 149, 97, 106 us).
+    // The largest cluster of which the resident CTAs hold all rows at once, or twice that number where rows may take
+    // top-p or min-p, whose times differ; and slices of 2048 logits at least.  256 rows of 128256 fp32 logits in clusters of 1, 2, 4, 8:
+    // every kind 116, 77, 92, 138 us, min-p 54, 49, 60, 86, but unfiltered 57, 65, 78, 99, top-k 65, 68, 89, 145, greedy 31, 36, 46, 68.
+    const int64_t ctas = (a.top_p || a.min_p ? 2 : 1) * kCtasPerSm * ctx.num_sms;
     int size = 1;
-    while (size < kMaxCluster && a.m * size * 2 <= 2 * kCtasPerSm * ctx.num_sms && a.vocab > size * 4096) size *= 2;
+    while (size < kMaxCluster && a.m * size * 2 <= ctas && a.vocab > size * 4096) size *= 2;
     const int units = a.vocab % kPer ? (a.vocab + 2 * kPer - 2) / kPer : a.vocab / kPer;  // what a row touches, at worst
     a.slice_units = (units + size - 1) / size;
     a.parts = std::min(65535.f, std::floor(4294960000.f / static_cast<float>(a.slice_units * kPer)));
