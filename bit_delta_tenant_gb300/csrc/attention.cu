@@ -6,13 +6,14 @@
 // Bound: HBM (each K and V element is used by the few query heads that share
 // its KV head).  One pass over the cache with a running maximum and sum.
 //
-// Work.  The keys of every (sequence, KV head) are cut into blocks of 64;
-// the blocks of the whole batch, numbered sequence by sequence, head by head,
-// are split evenly over the resident CTAs, so ragged lengths leave no CTA idle
-// and the host needs no length.  A CTA streams its range; where the range ends
-// inside a (sequence, head) it leaves the unnormalised output, maximum and sum
-// of its part in the workspace, and the last part to arrive joins all parts in
-// key order.  No CTA waits for another.
+// Work.  The keys of every (sequence, KV head) are cut into blocks of a tile per warp
+// (64 keys in bf16, 128 in 8 bits); the blocks of the whole batch, numbered sequence by
+// sequence, head by head, are split evenly over the resident CTAs, so ragged lengths
+// leave no CTA idle and the host needs no length.  A CTA streams its range; where the
+// range ends inside a (sequence, head) it leaves the unnormalised output, maximum and sum
+// of its part in the workspace; the last of eight neighbouring parts to arrive joins
+// them in key order, the last of eight such joins those, and so on.  No CTA waits for
+// another.  Where no sequence can be long, each warp takes whole heads and nothing is joined.
 //
 // A warp.  Each of the four warps owns a tile of a block's keys and keeps its own
 // running state; 16 keys of one page and head are one contiguous piece of
@@ -20,8 +21,9 @@
 // fragment loads meet no bank conflict), the page ids read a batch ahead.
 // S = Q K^T has the query heads as rows; O^T += V^T P^T has them as columns, so
 // S's accumulator is P^T's operand as it stands and 8 heads fill a column tile.
-// mma.sync, not tcgen05: 4 to 16 rows of a 128-row tile would be used, and the
-// kernel needs about a quarter of the legacy rate.
+// mma.sync, not tcgen05: 4 to 16 rows of a 128-row tile would be used, and at HBM's rate
+// the products take a sixth of mma.sync's (bf16, at most 8 heads to a KV head: 32 products
+// for 8 KB of K and V, 14 us of the 88 below).
 //
 // Rounding.  P enters as a 16-bit part and its 16-bit remainder: bf16 (2^-16 of a
 // weight) beside a bf16 V, fp16 (2^-21, or 2^-25 of the largest) beside an e4m3 V,
@@ -32,6 +34,10 @@
 // value's 8 bits exactly (values far below the largest to 2^-21 of it); with at most 8
 // heads the second part takes rows 8..15 of the same product.  Accumulation is
 // fp32 in every product (measured for the e4m3 one: 2^-25 of sum |q k|).
+//
+// Measured (head_dim 128): 130001 tokens, 64 and 8 heads, bf16 88 us (6.0 TB/s: SMs' streams end between 64 and
+// 82 us, then the joins); 64 sequences of up to 8191 tokens, 32 and 8 heads, 8 bits 33 us (3.7 TB/s: one to two heads
+// to a CTA, whose setup and joins are half of its time); 777 tokens, bf16 8.4 us, a chain of latencies.
 #include <cuda_fp8.h>
 
 #include <algorithm>
@@ -217,9 +223,11 @@ constexpr int smem_bytes() {
 template <bool kPack>
 constexpr int kCtasOf = kPack ? 3 : 2;
 
+// The heads of units begin .. end, or alone: of heads begin, begin + every warp of the grid, .. below end by this warp.
 // kPack: at most 8 query heads.
-template <int kDim, bool kE4m3, bool kPack>
-__global__ void __launch_bounds__(kThreads, kCtasOf<kPack>) attention_kernel(const AttnArgs a) {
+template <int kDim, bool kE4m3, bool kPack, bool alone>
+__device__ __forceinline__ void stream(const AttnArgs &a, uint8_t *smem, const Share &share, int64_t begin, int64_t end, int64_t b,
+                                       int64_t units_before) {
     constexpr int kTile = kTileOf<kE4m3>, kBlock = kBlockOf<kE4m3>;
     constexpr int kSub = kTile / 16;              // 16-key pieces of a tile, each within one page
     constexpr int kRow = kDim * (kE4m3 ? 1 : 2);  // bytes of one key
@@ -231,58 +239,14 @@ __global__ void __launch_bounds__(kThreads, kCtasOf<kPack>) attention_kernel(con
     constexpr int kSteps = kRow / 32;        // k steps of Q K^T: 32 bytes of a key each
     constexpr int kRowTiles = kDim / 16;     // row tiles of V^T P^T
     constexpr int kBatch = 32 / kSub;        // tiles whose page ids a warp holds at a time
-    extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ int64_t s_sum[kWarps];
-    __shared__ int64_t s_found[2];
+    constexpr int stride_keys = alone ? kTile : kBlock;  // from a warp's tile to its next
     __shared__ float s_m[kWarps][kRows], s_l[kWarps][kRows];
     __shared__ float s_jm[kFan][kRows], s_jl[kFan][kRows];
     __shared__ int s_last;
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, g = lane / 4, t4 = lane % 4;
     const int vheads = a.kv_heads * a.subs;
-    pdl_trigger_and_wait();
-
-    auto clear = [&](int64_t b) {  // a sequence with nothing to see
-        uint4 *o = reinterpret_cast<uint4 *>(a.out + b * a.q_heads * (kDim * 2));
-        for (int i = tid; i < a.q_heads * (kDim / 8); i += kThreads) o[i] = make_uint4(0, 0, 0, 0);
-        if (a.lse)
-            for (int i = tid; i < a.q_heads; i += kThreads) a.lse[b * a.q_heads + i] = -INFINITY;
-    };
-    for (int64_t b = blockIdx.x; b < a.n_seqs; b += gridDim.x)
-        if (span_of<kBlock>(a, b).units == 0) clear(b);
-
-    // all units of work, and this CTA's range of them
-    int64_t mine = 0;
-    for (int64_t b = tid; b < a.n_seqs; b += kThreads) mine += span_of<kBlock>(a, b).units;
-    const int64_t upto = warp_scan(mine);
-    if (lane == 31) s_sum[warp] = upto;
-    __syncthreads();
-    const Share share(static_cast<uint64_t>(s_sum[0] + s_sum[1] + s_sum[2] + s_sum[3]) * vheads, gridDim.x);
-    if (blockIdx.x >= share.ctas) return;
-    const int64_t begin = share.begin(blockIdx.x), end = share.begin(blockIdx.x + 1);
-
-    // the sequence that holds unit `begin`, and the units before it
-    if (a.n_seqs <= kThreads) {  // one sequence per thread: the sums above are the positions
-        int64_t p = upto - mine;
-        for (int w = 0; w < warp; ++w) p += s_sum[w];
-        if (mine > 0 && p * vheads <= begin && begin < (p + mine) * vheads) s_found[0] = tid, s_found[1] = p;
-    } else {
-        int64_t before = 0;
-        for (int64_t b0 = 0; b0 < a.n_seqs; b0 += kThreads) {
-            __syncthreads();
-            const int64_t n = b0 + tid < a.n_seqs ? span_of<kBlock>(a, b0 + tid).units : 0;
-            const int64_t in = warp_scan(n);
-            if (lane == 31) s_sum[warp] = in;
-            __syncthreads();
-            int64_t p = before + in - n;
-            for (int w = 0; w < warp; ++w) p += s_sum[w];
-            if (n > 0 && p * vheads <= begin && begin < (p + n) * vheads) s_found[0] = b0 + tid, s_found[1] = p;
-            before += s_sum[0] + s_sum[1] + s_sum[2] + s_sum[3];
-        }
-    }
-    __syncthreads();
-    int64_t b = s_found[0], units_before = s_found[1];
     Span sp = span_of<kBlock>(a, b);
-    int vh = static_cast<int>(quotient(begin - units_before * vheads, sp.units));
+    int vh = alone ? 0 : static_cast<int>(quotient(begin - units_before * vheads, sp.units));
     const uint32_t ring = smem_u32(smem) + warp * (kDepth * kStage);
     // Lane offsets that repeat: the swizzle turns with the row, so a copy has kTurns of them and a
     // fragment load one per chunk pair within 128 bytes; everything else is a constant.
@@ -296,20 +260,25 @@ __global__ void __launch_bounds__(kThreads, kCtasOf<kPack>) attention_kernel(con
     const uint8_t *ring_ptr = smem + warp * (kDepth * kStage);
 
     for (int64_t at = begin; at < end;) {
+        if (alone) {
+            b = quotient(at, vheads);
+            vh = static_cast<int>(at - b * vheads);
+            sp = span_of<kBlock>(a, b);
+        }
         // this head's units start at i0, its setup first; what lies in this CTA's range of its blocks
         const int64_t i0 = units_before * vheads + static_cast<int64_t>(vh) * sp.units;
-        const int64_t stop = min(end, i0 + sp.units);
-        const int blk = max(0, static_cast<int>(at - i0) - kSetup);
-        const int n = max(0, static_cast<int>(stop - i0) - kSetup) - blk;
+        const int64_t stop = alone ? at + static_cast<int64_t>(gridDim.x) * kWarps : min(end, i0 + sp.units);
+        const int blk = alone ? 0 : max(0, static_cast<int>(at - i0) - kSetup);
+        const int n = alone ? (sp.len + kTile - 1) / kTile - sp.start / kTile : max(0, static_cast<int>(stop - i0) - kSetup) - blk;
         if (n > 0) {
         const int kvh = vh / a.subs, row0 = vh % a.subs * kRows;
         const int rows = min(kRows, a.group - row0);
         const int64_t head0 = b * a.q_heads + kvh * a.group + row0;
-        const int key_first = (sp.first + blk) * kBlock + warp * kTile;  // this warp's tile of block j: + j * kBlock
+        const int key_first = alone ? sp.start / kTile * kTile : (sp.first + blk) * kBlock + warp * kTile;  // tile j: + j * stride_keys
 
         // 16-key piece `lane` of the batch of tiles from j0: its page id
         const int32_t *table = a.page_table + b * a.max_pages;
-        auto piece_of = [&](int j0) { return static_cast<uint32_t>(key_first + (j0 + lane / kSub) * kBlock) / 16 + lane % kSub; };
+        auto piece_of = [&](int j0) { return static_cast<uint32_t>(key_first + (j0 + lane / kSub) * stride_keys) / 16 + lane % kSub; };
         auto page_index = [&](uint32_t piece) { return a.page_tiles == 1 ? piece : __umulhi(piece, a.page_magic); };
         auto fetch_page = [&](int j0) {
             const uint32_t p = piece_of(j0);
@@ -393,7 +362,7 @@ __global__ void __launch_bounds__(kThreads, kCtasOf<kPack>) attention_kernel(con
                 places = place_of(j, next_pages);
                 next_pages = fetch_page(j + kBatch);
             }
-            const int key0 = key_first + j * kBlock;
+            const int key0 = key_first + j * stride_keys;
             if (key0 >= sp.len || key0 + kTile <= sp.start) return;
             const uint32_t to = slot * kStage;
             const bool inside = key0 >= sp.start && key0 + kTile <= sp.len;
@@ -434,10 +403,11 @@ __global__ void __launch_bounds__(kThreads, kCtasOf<kPack>) attention_kernel(con
             cp_commit();
             cp_wait<1>();
             __syncwarp();
-            const int key0 = key_first + j * kBlock;
+            const int key0 = key_first + j * stride_keys;
             if (key0 < sp.len && key0 + kTile > sp.start) {
                 const uint32_t to = slot * kStage;
-                const uint8_t *vp = ring_ptr + to + kTileBytes, *scales = vp + kTileBytes;
+                const uint8_t *vp = ring_ptr + to + kTileBytes;
+                [[maybe_unused]] const uint8_t *scales = vp + kTileBytes;
                 // 8 keys x 16 bytes per matrix: a chunk pair for keys 0..7, then for keys 8..15 of a piece
                 auto pair_at = [&](int u, int k) { return load_at[k % kPairs] + to + u * kPiece + k / kPairs * 128; };
                 float s[2 * kSub][4] = {};
@@ -621,18 +591,21 @@ __global__ void __launch_bounds__(kThreads, kCtasOf<kPack>) attention_kernel(con
             if (j + 1 < n) step(j + 1, 1);
         }
         cp_wait<0>();
-        __syncthreads();
+        __syncwarp();
+        if (!alone) __syncthreads();
 
-        // the four warps' states, joined in shared memory
+        // the warps' states in shared memory, [warp][row][kStride], where a warp alone keeps to its ring
         constexpr int kUsed = 8 * kHalves;
-        constexpr int kStride = kDim + 4;                  // rows of heads 2t fall into different banks
-        float *merge = reinterpret_cast<float *>(smem);    // [warp][row][kStride]
+        constexpr int kStride = kDim + 4;  // rows of heads 2t fall into different banks
+        static_assert(kUsed * kStride * 4 <= kDepth * kStage && kStage % 16 == 0);
+        float *merge = reinterpret_cast<float *>(smem);
+        float *own = alone ? reinterpret_cast<float *>(smem + warp * (kDepth * kStage)) : merge + warp * kUsed * kStride;
 #pragma unroll
         for (int h = 0; h < kHalves; ++h) {
             l[h] += __shfl_xor_sync(0xFFFFFFFFu, l[h], 1);
             l[h] += __shfl_xor_sync(0xFFFFFFFFu, l[h], 2);
             if (t4 == 0) s_m[warp][g + 8 * h] = m[h], s_l[warp][g + 8 * h] = l[h];
-            float *mine = merge + (warp * kUsed + 8 * h + 2 * t4) * kStride;
+            float *mine = own + (8 * h + 2 * t4) * kStride;
 #pragma unroll
             for (int e = 0; e < 2; ++e, mine += kStride) {
                 if constexpr (kE4m3) {
@@ -646,14 +619,24 @@ __global__ void __launch_bounds__(kThreads, kCtasOf<kPack>) attention_kernel(con
                 }
             }
         }
-        __syncthreads();
-        const bool whole = blk == 0 && n == sp.blocks;
         auto finish = [&](int r, int d, float4 x, float top, float sum) {  // four columns of a row, and once its lse
             const float inv = sum == 0.f ? 0.f : 1.f / sum;
             *reinterpret_cast<uint2 *>(a.out + ((head0 + r) * kDim + d) * 2) =
                 make_uint2(pack_bf16x2(x.x * inv, x.y * inv), pack_bf16x2(x.z * inv, x.w * inv));
             if (a.lse && d == 0) a.lse[head0 + r] = (top + log2f(sum)) * 0.693147180559945f;
         };
+        if (alone) {
+            __syncwarp();
+            for (int i = lane; i < rows * (kDim / 4); i += 32) {
+                const int r = i / (kDim / 4), d = i % (kDim / 4) * 4;
+                finish(r, d, *reinterpret_cast<const float4 *>(own + r * kStride + d), s_m[warp][r], s_l[warp][r]);
+            }
+            __syncwarp();  // the ring is free again
+            at = stop;
+            continue;
+        }
+        __syncthreads();
+        const bool whole = blk == 0 && n == sp.blocks;
         auto store_part = [&](float *slot, int r, int d, float4 x, float top, float sum) {
             *reinterpret_cast<float4 *>(slot + r * kDim + d) = x;
             if (d == 0) slot[kRows * 128 + r] = top, slot[kRows * 128 + kRows + r] = sum;
@@ -748,7 +731,7 @@ __global__ void __launch_bounds__(kThreads, kCtasOf<kPack>) attention_kernel(con
         __syncthreads();  // shared memory is free again
         }
         at = stop;
-        if (++vh == vheads && at < end) {
+        if (!alone && ++vh == vheads && at < end) {
             vh = 0;
             units_before += sp.units;
             do sp = span_of<kBlock>(a, ++b);
@@ -756,11 +739,77 @@ __global__ void __launch_bounds__(kThreads, kCtasOf<kPack>) attention_kernel(con
         }
     }
 }
+// Sequences with nothing to see.
+template <int kDim, int kBlock>
+__device__ __forceinline__ void clear_unseen(const AttnArgs &a) {
+    for (int64_t b = blockIdx.x; b < a.n_seqs; b += gridDim.x) {
+        if (span_of<kBlock>(a, b).units != 0) continue;
+        uint4 *o = reinterpret_cast<uint4 *>(a.out + b * a.q_heads * (kDim * 2));
+        for (int i = threadIdx.x; i < a.q_heads * (kDim / 8); i += kThreads) o[i] = make_uint4(0, 0, 0, 0);
+        if (a.lse)
+            for (int i = threadIdx.x; i < a.q_heads; i += kThreads) a.lse[b * a.q_heads + i] = -INFINITY;
+    }
+}
+
+// Each warp takes whole heads.
+template <int kDim, bool kE4m3, bool kPack>
+__global__ void __launch_bounds__(kThreads, kCtasOf<kPack>) attention_alone_kernel(const AttnArgs a) {
+    extern __shared__ __align__(128) uint8_t smem[];
+    pdl_trigger_and_wait();
+    clear_unseen<kDim, kBlockOf<kE4m3>>(a);
+    const int64_t first = static_cast<int64_t>(blockIdx.x) * kWarps + threadIdx.x / 32;
+    stream<kDim, kE4m3, kPack, true>(a, smem, Share(0, 0), first, static_cast<int64_t>(a.n_seqs) * a.kv_heads * a.subs, 0, 0);
+}
 
 template <int kDim, bool kE4m3, bool kPack>
-cudaError_t launch_typed(const AttnArgs &a, const DevCtx &ctx, cudaStream_t stream) {
+__global__ void __launch_bounds__(kThreads, kCtasOf<kPack>) attention_kernel(const AttnArgs a) {
+    constexpr int kBlock = kBlockOf<kE4m3>;
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ int64_t s_sum[kWarps];
+    __shared__ int64_t s_found[2];
+    const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+    const int vheads = a.kv_heads * a.subs;
+    pdl_trigger_and_wait();
+
+    clear_unseen<kDim, kBlock>(a);
+
+    // all units of work, and this CTA's range of them
+    int64_t mine = 0;
+    for (int64_t b = tid; b < a.n_seqs; b += kThreads) mine += span_of<kBlock>(a, b).units;
+    const int64_t upto = warp_scan(mine);
+    if (lane == 31) s_sum[warp] = upto;
+    __syncthreads();
+    const Share share(static_cast<uint64_t>(s_sum[0] + s_sum[1] + s_sum[2] + s_sum[3]) * vheads, gridDim.x);
+    if (blockIdx.x >= share.ctas) return;
+    const int64_t begin = share.begin(blockIdx.x), end = share.begin(blockIdx.x + 1);
+
+    // the sequence that holds unit `begin`, and the units before it
+    if (a.n_seqs <= kThreads) {  // one sequence per thread: the sums above are the positions
+        int64_t p = upto - mine;
+        for (int w = 0; w < warp; ++w) p += s_sum[w];
+        if (mine > 0 && p * vheads <= begin && begin < (p + mine) * vheads) s_found[0] = tid, s_found[1] = p;
+    } else {
+        int64_t before = 0;
+        for (int64_t b0 = 0; b0 < a.n_seqs; b0 += kThreads) {
+            __syncthreads();
+            const int64_t n = b0 + tid < a.n_seqs ? span_of<kBlock>(a, b0 + tid).units : 0;
+            const int64_t in = warp_scan(n);
+            if (lane == 31) s_sum[warp] = in;
+            __syncthreads();
+            int64_t p = before + in - n;
+            for (int w = 0; w < warp; ++w) p += s_sum[w];
+            if (n > 0 && p * vheads <= begin && begin < (p + n) * vheads) s_found[0] = b0 + tid, s_found[1] = p;
+            before += s_sum[0] + s_sum[1] + s_sum[2] + s_sum[3];
+        }
+    }
+    __syncthreads();
+    stream<kDim, kE4m3, kPack, false>(a, smem, share, begin, end, s_found[0], s_found[1]);
+}
+
+template <int kDim, bool kE4m3, bool kPack, bool alone>
+cudaError_t launch_form(const AttnArgs &a, const DevCtx &ctx, cudaStream_t stream) {
     constexpr int smem_size = smem_bytes<kDim, kE4m3>();
-    constexpr auto kernel = attention_kernel<kDim, kE4m3, kPack>;
+    constexpr auto kernel = alone ? attention_alone_kernel<kDim, kE4m3, kPack> : attention_kernel<kDim, kE4m3, kPack>;
     const cudaError_t e = allow_smem<kernel>(smem_size, ctx.device);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
@@ -774,6 +823,22 @@ cudaError_t launch_typed(const AttnArgs &a, const DevCtx &ctx, cudaStream_t stre
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, kernel, a);
+}
+
+template <int kDim, bool kE4m3, bool kPack>
+cudaError_t launch_typed(const AttnArgs &a, const DevCtx &ctx, cudaStream_t stream) {
+    // The host has no lengths, but the page table's width and the window bound them.  With few keys to a head a CTA's
+    // steps are mostly its setup and joins, so each warp takes heads by itself where that is not many more steps.  By
+    // CTAs and by warps, 32 and 8 heads, bf16: 256 sequences of up to 64, 128, 256, 512, 1024 tokens 16.9 / 9.7,
+    // 17.8 / 12.6, 21.7 / 18.4, 25.7 / 29.6, 35.4 / 56.9 us; 64 of up to 64, 128, 256: 7.5 / 5.8, 7.7 / 8.1, 10.5 / 11.8.
+    int64_t most = static_cast<int64_t>(a.max_pages) * a.page_size;
+    if (a.window > 0) most = std::min<int64_t>(most, a.window + kTileOf<kE4m3> - 1);
+    const int64_t heads = static_cast<int64_t>(a.n_seqs) * a.kv_heads * a.subs, ctas = ctx.num_sms * kCtasOf<kPack>;
+    const int64_t tiles = (most + kTileOf<kE4m3> - 1) / kTileOf<kE4m3>, blocks = (tiles + kWarps - 1) / kWarps;
+    const int64_t steps = (heads * (blocks + kSetup) + ctas - 1) / ctas;
+    const int64_t steps_alone = (heads + ctas * kWarps - 1) / (ctas * kWarps) * (tiles + kSetup);
+    if (steps_alone <= steps + steps / 4 + 5) return launch_form<kDim, kE4m3, kPack, true>(a, ctx, stream);
+    return launch_form<kDim, kE4m3, kPack, false>(a, ctx, stream);
 }
 
 int slots_of(int num_sms) { return 2 * num_sms * kMaxCtasPerSm; }
