@@ -17,6 +17,7 @@
 
 #include "bd_device.cuh"
 #include "bd_internal.h"
+#include "bd_rows.cuh"
 
 namespace bd {
 namespace {
@@ -33,18 +34,6 @@ struct NormArgs {
     int32_t n, n_weights, row_scale;  // row_scale: one scale per row instead of one per 128 columns
     float eps, inv_n;
 };
-
-__device__ __forceinline__ void unpack8(const uint4 &v, float (&f)[8]) {
-    f[0] = bf16lo_to_f32(v.x), f[1] = bf16hi_to_f32(v.x);
-    f[2] = bf16lo_to_f32(v.y), f[3] = bf16hi_to_f32(v.y);
-    f[4] = bf16lo_to_f32(v.z), f[5] = bf16hi_to_f32(v.z);
-    f[6] = bf16lo_to_f32(v.w), f[7] = bf16hi_to_f32(v.w);
-}
-
-__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
-    return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
-                      pack_bf16x2(f[6], f[7]));
-}
 
 // Sum or maximum over the kWarps warps that share a row, the same value in every thread of theirs.
 template <int kWarps, bool kMax>
