@@ -35,7 +35,7 @@
 // Sums of weights do not depend on the order of atomics: they are whole numbers.  Within a
 // bin of width d, w = exp(-start) w' with w' in [1 - d, 1], and a bin sums
 // round((w' - 1 + d) P / d) in 32 bits beside its count, P = 65535 or what a long slice
-// leaves room for; top-p's first histogram, which needs no counts, sums round(w' P).
+// leaves room for; top-p's first histogram, which needs no counts, sums whole parts of w' (Bins::add).
 // Across bins weights are fixed-point with 40 fractional bits.  The sum of all weights is
 // fp32 in an order fixed by the shape.
 #include <algorithm>
@@ -151,10 +151,11 @@ struct Row {
 // Whole numbers come from adding 2^23, which leaves them in a sum's low bits: conversions have an eighth of that rate.
 struct Bins {
     static constexpr float kWhole = 8388608.f;  // 2^23
-    float scale, width, unit, parts_of, most, all, width2;  // 1 / width, width, parts / width, its inverse, parts; see add()
+    float scale, width, unit, parts_of, most;  // 1 / width, width, parts / width, its inverse, parts
+    float all, width2, dither;                 // of add()
     __device__ __forceinline__ Bins(float range, float parts)
         : scale((kBins - 2) / range), width(range / (kBins - 2)), unit(parts * scale), parts_of(width / parts), most(parts),
-          all(parts * 0.96f), width2(width * kLog2e) {}
+          all(floorf(parts * 0.96f)), width2(width * kLog2e), dither((threadIdx.x % 32 - 15.5f) / 32) {}
     static __device__ __forceinline__ int whole(float sum) { return __float_as_int(sum) - __float_as_int(kWhole); }  // sum = 2^23 + n
     __device__ __forceinline__ int bin(float t) const { return min(whole(fmaf(t, scale, kWhole)), kBins - 1); }
     __device__ __forceinline__ float start(int b) const { return (b - 0.5f) * width; }
@@ -170,13 +171,14 @@ struct Bins {
         const float w = fmaf(static_cast<float>(parts), parts_of, static_cast<float>(count) * (1.f - width));
         return __float2ull_rn(w * (ex2(start(b) * -kLog2e) * kFixed));
     }
-    // Adds a token to bins that hold their weight in one word, in parts of exp(-b width), and no count: 2^-17 of the
-    // weight, of which the sum of a bin's tokens keeps less.
-    __device__ __forceinline__ void add(uint32_t *bins, float t) const {
+    // Adds a token to bins that hold their weight in one word, in whole parts of exp(-b width), and no count.  A weight is
+    // rounded to 2^-17 of itself, equal ones at other places up or down (`dither`, within a half, by lane and by `odd`),
+    // so a bin's sum keeps the error of one token over the root of their number; a weight of 1 is exact.
+    __device__ __forceinline__ void add(uint32_t *bins, float t, bool odd) const {
         const float at = fmaf(t, scale, kWhole);
         const int b = whole(at);
         const float w = ex2(fmaf(at - kWhole, width2, t * -kLog2e));  // exp(-width / 2) .. exp(width / 2) < 1 / 0.96
-        if (b < kBins - 1) atomicAdd(&bins[b], static_cast<uint32_t>(whole(fmaf(w, all, kWhole))));
+        if (b < kBins - 1) atomicAdd(&bins[b], static_cast<uint32_t>(whole(fmaf(w, all, odd ? -dither : dither) + kWhole)));
     }
     __device__ __forceinline__ u64 mass_of(int b, u64 parts) const {
         return b == kBins - 1 ? 0 : __float2ull_rn(static_cast<float>(parts) / all * (ex2(b * -width2) * kFixed));
@@ -873,7 +875,7 @@ __device__ void Sampler<kF32>::run(int64_t r) {
                 for (int j = 0; j < kPer; ++j) {
                     const float t = exact ? row.t_of(x[j]) : __fmul_rn(__fsub_rn(row.top, x[j]), row.inv_t);
                     score[j] = __fadd_rn(-t, noise[j]);
-                    bins.add(s.parts, t);
+                    bins.add(s.parts, t, j % 2);
                 }
                 const float here = largest(score);
                 if (here > most) most = here, unit = i;
