@@ -28,9 +28,8 @@
 //     all bins up to it, if those are few) are sent to every CTA and ordered exactly.  A bin
 //     with too many tokens is split again, by the remaining bits of t, then by the bits of
 //     (x, index), which differ for any two.
-// Measured, rows of 128256 fp32 logits: one row with top-k and top-p (bf16) 14.6 us, a chain of latencies; 256 rows
-// unfiltered 65 us (4.0 TB/s), top-k 68, top-p 137, min-p 49, greedy 36, of every kind 76 (57, 65, 31 us unfiltered,
-// top-k and greedy where the call gives neither top-p nor min-p).
+// Measured, rows of 128256 fp32 logits: one row with top-k and top-p (bf16) 15.0 us, a chain of latencies; 256 rows
+// unfiltered 66 us (4.0 TB/s), top-k 68, top-p 137, min-p 41, greedy 37, of every kind 76.
 //
 // Sums of weights do not depend on the order of atomics: they are whole numbers.  Within a
 // bin of width d, w = exp(-start) w' with w' in [1 - d, 1], and a bin sums
@@ -191,7 +190,8 @@ __device__ __forceinline__ u64 share_of(float p, u64 mass) {
 
 template <bool kF32>
 struct Sampler {
-    static constexpr int kPer = kF32 ? 4 : 8;  // logits of a unit
+    static constexpr int kPer = kF32 ? 4 : 8;    // logits of a unit
+    static constexpr int kAhead = kF32 ? 4 : 3;  // units of logits in flight
 
     Shared &s;
     const SampleArgs &a;
@@ -256,7 +256,6 @@ struct Sampler {
     // before its use, spill and take 3 to 10% longer)
     template <class F>
     __device__ __forceinline__ void each_unit(F f) const {
-        constexpr int kAhead = kF32 ? 4 : 3;
         uint4 raw[kAhead];
         auto load = [&](int q, int i) { raw[q] = inside(i) ? fetch(i) : make_uint4(0, 0, 0, 0); };
 #pragma unroll
@@ -617,14 +616,17 @@ __device__ void Sampler<kF32>::run(int64_t r) {
     // the largest so far, or rather to `shift`, which is that times per rounded: x per - shift is one operation.
     const float per = row.inv_t * kLog2e;
     const bool plain = per > 0.f && per < INFINITY;
-    float top = -INFINITY, shift = 0.f, sum = 0.f;
+    float top = -INFINITY, next_top = -INFINITY, shift = 0.f, sum = 0.f;  // next_top: the largest logit of other units
     int top_unit = 0;
-    auto weigh = [&](int i, const float (&x)[kPer]) {
+    auto weigh = [&](int i, const float (&x)[kPer], auto next) {
         const float here = largest(x);
         if (here > top) {
             const float to = here * per;
             sum = top > -INFINITY ? sum * ex2(shift - to) : 0.f;
+            if constexpr (next) next_top = top;
             top = here, shift = to, top_unit = i;
+        } else if constexpr (next) {
+            next_top = fmaxf(next_top, here);
         }
 #pragma unroll
         for (int j = 0; j < kPer; ++j) sum += ex2(fmaf(x[j], per, -shift));
@@ -635,7 +637,7 @@ __device__ void Sampler<kF32>::run(int64_t r) {
     int draw_unit = -1;
     if (open)
         each_scored([&](int i, const float (&x)[kPer], const float (&noise)[kPer]) {
-            weigh(i, x);
+            weigh(i, x, std::false_type{});
             float score[kPer];
 #pragma unroll
             for (int j = 0; j < kPer; ++j) score[j] = fmaf(x[j], row.inv_t, noise[j]);
@@ -645,7 +647,7 @@ __device__ void Sampler<kF32>::run(int64_t r) {
             else second = fmaxf(second, here);
         });
     else
-        each_unit(weigh);
+        each_unit([&](int i, const float (&x)[kPer]) { weigh(i, x, std::true_type{}); });
 
     // This CTA's largest logit, the sum of its weights relative to it, and for top-k its bound: j threads of every
     // warp reach it.
@@ -700,6 +702,28 @@ __device__ void Sampler<kF32>::run(int64_t r) {
         const float v = s.ranks[c].top;
         if (v > -INFINITY) weight = fmaf(s.ranks[c].sum, ex2(row.t_of(v) * -kLog2e), weight);
     }
+
+    // f(i, x) for the units that hold a logit of at least `bound`, and some others.  Most threads have none or one, which
+    // the first pass has left; through all units of a thread with more the warp looks together, or each such thread by
+    // itself where that takes no more rounds of loads.
+    auto candidates = [&](float bound, auto f) {
+        const bool more = next_top >= bound;
+        float x[kPer];
+        if (!more && top >= bound) {
+            read(top_unit, inside(top_unit), inside(top_unit) ? fetch(top_unit) : make_uint4(0, 0, 0, 0), x);
+            f(top_unit, x);
+        }
+        unsigned who = __ballot_sync(0xFFFFFFFFu, more);
+        if (__popc(who) * (kAhead * kThreads) > units) {
+            if (more) each_unit(f);
+        } else {
+            for (; who; who &= who - 1)
+                for (int i = tid - lane + __ffs(who) - 1 + lane * kThreads; i < units; i += 32 * kThreads) {
+                    read(i, inside(i), inside(i) ? fetch(i) : make_uint4(0, 0, 0, 0), x);
+                    f(i, x);
+                }
+        }
+    };
 
     u64 best = 0;
     auto offer = [&](float t, float noise, int i) {
@@ -779,7 +803,7 @@ __device__ void Sampler<kF32>::run(int64_t r) {
         float least = plain && row.top < INFINITY && low > 0.f ? row.top + logf(low) * temp : -INFINITY;
         least -= fabsf(least) * 1e-6f + temp * 1e-6f;  // below any token that the exact test keeps
         if (!(least > -INFINITY)) least = -INFINITY;
-        each_unit([&](int i, const float (&x)[kPer]) {
+        candidates(least, [&](int i, const float (&x)[kPer]) {
             if (largest(x) < least) return;
 #pragma unroll
             for (int j = 0; j < kPer; ++j) {
@@ -1005,9 +1029,9 @@ template <bool kF32>
 cudaError_t launch_typed(SampleArgs &a, const DevCtx &ctx, cudaStream_t stream) {
     constexpr int kPer = kF32 ? 4 : 8;
     // The largest cluster of which the resident CTAs hold all rows at once, or twice that number where rows may take
-    // top-p or min-p, whose times differ; and slices of 2048 logits at least.  256 rows of 128256 fp32 logits in clusters of 1, 2, 4, 8:
-    // every kind 116, 77, 92, 138 us, min-p 54, 49, 60, 86, but unfiltered 57, 65, 78, 99, top-k 65, 68, 89, 145, greedy 31, 36, 46, 68.
-    const int64_t ctas = (a.top_p || a.min_p ? 2 : 1) * kCtasPerSm * ctx.num_sms;
+    // top-p, which takes longer; and slices of 2048 logits at least.  256 rows of 128256 fp32 logits in clusters of 1, 2, 4:
+    // every kind 113, 75, 91 us, but unfiltered 58, 67, 80, top-k 65, 68, 89, min-p 36, 41, 53, greedy 31, 37, 47.
+    const int64_t ctas = (a.top_p ? 2 : 1) * kCtasPerSm * ctx.num_sms;
     int size = 1;
     while (size < kMaxCluster && a.m * size * 2 <= ctas && a.vocab > size * 4096) size *= 2;
     const int units = a.vocab % kPer ? (a.vocab + 2 * kPer - 2) / kPer : a.vocab / kPer;  // what a row touches, at worst
