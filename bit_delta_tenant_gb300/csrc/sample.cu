@@ -13,9 +13,8 @@
 // The first pass takes the largest logit and the sum of weights relative to it, and
 // draws from an unfiltered row, to within rounding (see `open`).  The filters are a
 // threshold in the order (x descending, index ascending), found without sorting:
-//  1. Tokens that cannot be kept are left out.  top-k: every warp of the cluster has
-//     j = ceil(k / warps) threads whose largest logit reaches the warp's j-th largest, so
-//     k tokens reach the smallest of these.  top-p: tokens with t = -z above
+//  1. Tokens that cannot be kept are left out.  top-k: the k-th of the cluster's largest
+//     thread maxima is reached by k tokens, and by few more.  top-p: tokens with t = -z above
 //     ln(V / ((1 - p) sum w)) weigh less than (1 - p) sum w together, so the prefix
 //     ends before them.
 //  2. A histogram over t holds each bin's weight, and for top-k its count.  Every CTA adds
@@ -25,11 +24,12 @@
 //     draw.  The best of these is the answer if it lies before that bin, which it does
 //     with about probability p; else the threads that had a better one look again.
 //  3. For top-k, and where the answer may lie in that very bin, the bin's tokens (for top-k
-//     all bins up to it, if those are few) are sent to every CTA and ordered exactly.  A bin
+//     all bins up to it, if those are few; as used, all that step 1 leaves, without a
+//     histogram) are sent to every CTA and ordered exactly.  A bin
 //     with too many tokens is split again, by the remaining bits of t, then by the bits of
 //     (x, index), which differ for any two.
-// Measured, rows of 128256 fp32 logits: one row with top-k and top-p (bf16) 15.0 us, a chain of latencies; 256 rows
-// unfiltered 66 us (4.0 TB/s), top-k 68, top-p 137, min-p 41, greedy 37, of every kind 76.
+// Measured, rows of 128256 fp32 logits: one row with top-k and top-p (bf16) 12.9 us, a chain of latencies; 256 rows
+// unfiltered 67 us (3.9 TB/s), top-k 64, top-p 139, min-p 41, greedy 37, of every kind 76.
 //
 // Sums of weights do not depend on the order of atomics: they are whole numbers.  Within a
 // bin of width d, w = exp(-start) w' with w' in [1 - d, 1], and a bin sums
@@ -55,6 +55,7 @@ constexpr int kBits = 9;          // a digit: one bin
 constexpr int kCap = kBins;       // tokens ordered exactly: a list is scanned as the bins are
 constexpr int kIndexBits = 18;    // BD_SAMPLE_MAX_VOCAB = 2^18
 constexpr int kMaxCluster = 8;
+constexpr int kTops = 256;        // thread maxima from which top-k's bound is taken: two of every warp of the largest cluster
 constexpr float kRange = 31.5f;   // weights below exp(-31.5) of the largest count as 0 in a prefix's sum
 constexpr float kFixed = 1099511627776.f;  // 2^40
 constexpr float kLog2e = 1.44269504088896f;
@@ -77,17 +78,20 @@ struct SampleArgs {
 struct alignas(16) Shared {
     uint32_t count[kBins], parts[kBins];  // apart: side by side they would share half of the banks
     u64 list_order[kCap], list_mass[kCap], sorted_mass[kCap];
+    uint32_t tops[kTops];
     u64 warp_mass[kWarps], warp_parts[2][kWarps];
     uint32_t warp_count[kWarps];
-    float warp_value[5][kWarps];
+    float warp_value[4][kWarps];
     // written by the cluster's CTAs
     struct Rank {
-        float top, sum, low, draw, noise;
+        float top, sum, draw, noise;
+        uint32_t n;
         u64 best, in[2], rest[2];
     } ranks[kMaxCluster];
+    alignas(16) uint32_t all_tops[kTops];
     // written by one thread for its CTA
     u64 before_mass, kept_mass, threshold;
-    uint32_t before_count, here, list_n, maybe_n;
+    uint32_t before_count, here, list_n, maybe_n, first, bound;
     int found;
 };
 
@@ -103,6 +107,14 @@ __device__ __forceinline__ void st_remote(uint32_t at, float v) {
 }
 __device__ __forceinline__ void st_remote(uint32_t at, u64 v) {
     asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(at), "l"(v) : "memory");
+}
+__device__ __forceinline__ void st_remote(uint32_t at, uint32_t v) {
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(at), "r"(v) : "memory");
+}
+__device__ __forceinline__ uint32_t add_remote(uint32_t at, uint32_t v) {  // what was there before
+    uint32_t before;
+    asm volatile("atom.shared::cluster.add.u32 %0, [%1], %2;" : "=r"(before) : "r"(at), "r"(v) : "memory");
+    return before;
 }
 __device__ __forceinline__ uint32_t ld_remote(uint32_t at) {
     uint32_t v;
@@ -489,6 +501,7 @@ struct Sampler {
         const int i = tid / lanes, part = tid % lanes;
         const u64 mine = s.list_order[i];
         uint32_t rank_of = 0;
+#pragma unroll 1
         for (uint32_t j = part; j < pairs; j += lanes) {
             const ulonglong2 two = *reinterpret_cast<const ulonglong2 *>(&s.list_order[2 * j]);
             rank_of += (two.x < mine) + (two.y < mine);
@@ -649,21 +662,25 @@ __device__ void Sampler<kF32>::run(int64_t r) {
     else
         each_unit([&](int i, const float (&x)[kPer]) { weigh(i, x, std::true_type{}); });
 
-    // This CTA's largest logit, the sum of its weights relative to it, and for top-k its bound: j threads of every
-    // warp reach it.
+    // This CTA's largest logit and the sum of its weights relative to it.  For top-k the largest of each warp's thread
+    // maxima, kTops in the cluster, of which the k-th is a bound that k tokens reach; for a larger k each warp's j-th
+    // largest, of which the smallest is one.
+    const int per_warp = kTops / (size * kWarps);
+    const bool by_rank = k <= kTops;
+    const int sent = by_rank ? kWarps * per_warp : kWarps;  // by this CTA
     if (filtered && k > 0) {
-        const uint32_t j = (k + size * kWarps - 1) / (size * kWarps);
+        const uint32_t j = by_rank ? per_warp : (k + size * kWarps - 1) / (size * kWarps);
         uint32_t left = ascending(top), jth = 0;  // 0: below every logit
         if (j <= 32)
             for (uint32_t i = 0; i < j; ++i) {
                 jth = __reduce_max_sync(0xFFFFFFFFu, left);
                 const unsigned who = __ballot_sync(0xFFFFFFFFu, left == jth);
                 if (lane == __ffs(who) - 1) left = 0;
+                if (by_rank && lane == 0) s.tops[warp * per_warp + i] = jth;
             }
-        reach = jth > ascending(-INFINITY) ? value_of(jth) : -INFINITY;
-        if (lane == 0) s.warp_value[0][warp] = reach;
+        if (!by_rank && lane == 0) s.tops[warp] = jth;
     }
-    const float cta_top = block_fold<true>(top, s.warp_value[1]);
+    const float cta_top = block_fold<true>(top, s.warp_value[0]);
     if (plain && fabsf(cta_top * per) < 32768.f) {
         // a thread whose largest logit lies beyond the range of its own sum weighs nothing beside that
         sum = top > -INFINITY && fabsf(shift) < 65536.f ? sum * ex2(fmaf(-cta_top, per, shift)) : 0.f;
@@ -676,17 +693,20 @@ __device__ void Sampler<kF32>::run(int64_t r) {
             if (x > -INFINITY) sum += ex2(own.t_of(x) * -kLog2e);
         }
     }
-    sum = block_fold<false>(sum, s.warp_value[2]);
+    sum = block_fold<false>(sum, s.warp_value[1]);
     float cta_most = -INFINITY;
-    if (open) cta_most = block_fold<true>(most, s.warp_value[3]), loudest = block_fold<true>(loudest, s.warp_value[4]);
+    if (open) cta_most = block_fold<true>(most, s.warp_value[2]), loudest = block_fold<true>(loudest, s.warp_value[3]);
     __syncwarp();
     cluster_wait_acquire();  // every CTA of the cluster runs: its shared memory may be written
     if (tid < size) {
-        if (filtered && k > 0)
-            for (int w = 0; w < kWarps; ++w) reach = fminf(reach, s.warp_value[0][w]);
         const uint32_t to = remote(&s.ranks[rank], tid);
-        st_remote(to, cta_top), st_remote(to + 4, sum), st_remote(to + 8, reach), st_remote(to + 12, cta_most), st_remote(to + 16, loudest);
+        st_remote(to, cta_top), st_remote(to + 4, sum), st_remote(to + 8, cta_most), st_remote(to + 12, loudest);
     }
+    if (filtered && k > 0 && tid < sent * size) {  // sent: a power of two
+        const int i = tid & (sent - 1);
+        st_remote(remote(&s.all_tops[rank * sent + i], tid >> (__ffs(sent) - 1)), s.tops[i]);
+    }
+    if (tid == 0) s.list_n = s.maybe_n = 0;
     cluster_sync_all();
     row.top = s.ranks[0].top;
     for (int c = 1; c < size; ++c) row.top = fmaxf(row.top, s.ranks[c].top);
@@ -820,8 +840,31 @@ __device__ void Sampler<kF32>::run(int64_t r) {
     float range = kRange;
     bool pruned = false;  // by weight
     if (k > 0) {
-        reach = s.ranks[0].low;
-        for (int c = 1; c < size; ++c) reach = fminf(reach, s.ranks[c].low);
+        if (warp == 0) {  // bit by bit, of the bits in which they differ
+            uint32_t v[kTops / 32], bound = 0xFFFFFFFFu;
+            if (by_rank) {
+                uint32_t some = 0, every = 0xFFFFFFFFu;
+#pragma unroll
+                for (int i = 0; i < kTops / 32; ++i) v[i] = s.all_tops[lane + 32 * i], some |= v[i], every &= v[i];
+                some = __reduce_or_sync(0xFFFFFFFFu, some), every = __reduce_and_sync(0xFFFFFFFFu, every);
+                bound = every;
+#pragma unroll 1
+                for (uint32_t bits = some & ~every; bits;) {
+                    const uint32_t bit = 1u << (31 - __clz(bits)), least = bound | bit;
+                    bits ^= bit;
+                    uint32_t reached = 0;
+#pragma unroll
+                    for (int i = 0; i < kTops / 32; ++i) reached += v[i] >= least;
+                    if (__reduce_add_sync(0xFFFFFFFFu, reached) >= k) bound = least;
+                }
+            } else {
+                for (int i = lane; i < sent * size; i += 32) bound = min(bound, s.all_tops[i]);
+                bound = __reduce_min_sync(0xFFFFFFFFu, bound);
+            }
+            if (lane == 0) s.bound = bound;
+        }
+        __syncthreads();
+        reach = s.bound > ascending(-INFINITY) ? value_of(s.bound) : -INFINITY;
         if (reach > -INFINITY) range = fminf(range, row.t_of(reach) * 1.0001f + 1e-6f);
     } else if (p < 1.f - 1e-5f) {  // a longer prefix is summed over everything, so that it ends by the sum of its own bins
         const float bound = logf(static_cast<float>(a.vocab) / ((1.f - p) * 0.99f * weight));
@@ -839,11 +882,9 @@ __device__ void Sampler<kF32>::run(int64_t r) {
         const uint32_t place = atomicAdd(&s.maybe_n, 1u);
         if (place < a.most) maybe_x[place] = x, maybe_at[place] = static_cast<uint32_t>(token);
     };
-    if (tid == 0) s.maybe_n = 0;
     u64 threshold = ~0ull;
     Each each;
     if (k > 0) {  // few tokens: packed, then counted
-        __syncthreads();
         each_unit([&](int i, const float (&x)[kPer]) {
             if (!(largest(x) >= reach)) return;
 #pragma unroll
@@ -852,18 +893,10 @@ __device__ void Sampler<kF32>::run(int64_t r) {
         });
         __syncthreads();
         tokens = static_cast<int>(s.maybe_n);
-        histogram(bins, level0, ~0ull);
-        cluster_sync_all();
-        const Scan c = totals(bins, level0, each);
-        const int d = find(c, false, k);
-        const uint32_t upto = s.before_count + s.here, need = k - min(s.before_count, k), here = s.here;
-        const u64 before_mass = s.before_mass;
-        if (upto <= kCap) {  // few enough to finish here: order all of them, take the share p, draw
-            gather(bins, level0, d, true, ~0ull, each);
-            cluster_sync_all();
-            if (rank != 0) return;
-            cut(upto, false, k, p);
-            for (int i = tid; i < upto; i += kThreads) {
+        // orders a list, takes the share p, draws
+        auto draw_of_list = [&](uint32_t n) {
+            cut(n, false, k, p);
+            for (int i = tid; i < n; i += kThreads) {
                 const u64 o = s.list_order[i];
                 if (o > s.threshold) continue;
                 const int token = static_cast<int>(o & ((1u << kIndexBits) - 1));
@@ -872,6 +905,35 @@ __device__ void Sampler<kF32>::run(int64_t r) {
             }
             best = fold_max(best);
             if (tid == 0) answer();
+        };
+        // As used they are few: straight to the first CTA's list.
+        if (tid < size) st_remote(remote(&s.ranks[rank].n, tid), static_cast<uint32_t>(tokens));
+        if (tid == 0) s.first = add_remote(remote(&s.list_n, 0), static_cast<uint32_t>(min(tokens, kCap + 1)));
+        __syncthreads();
+        if (s.first + tokens <= kCap && tokens <= a.most)
+            for (int i = tid; i < tokens; i += kThreads) {
+                const float x = maybe_x[i], t = row.t_of(x);
+                const int b = bins.bin(t);
+                st_remote(remote(&s.list_order[s.first + i], 0), order_of(x, static_cast<int>(maybe_at[i])));
+                st_remote(remote(&s.list_mass[s.first + i], 0), bins.mass(b, 1, bins.part(t, b)));
+            }
+        cluster_sync_all();
+        uint64_t in_all = 0;
+        for (int c = 0; c < size; ++c) in_all += s.ranks[c].n;
+        if (in_all <= min(kCap, a.most)) {
+            if (rank == 0) draw_of_list(static_cast<uint32_t>(in_all));
+            return;
+        }
+        histogram(bins, level0, ~0ull);
+        cluster_sync_all();
+        const Scan c = totals(bins, level0, each);
+        const int d = find(c, false, k);
+        const uint32_t upto = s.before_count + s.here, need = k - min(s.before_count, k), here = s.here;
+        const u64 before_mass = s.before_mass;
+        if (upto <= kCap) {
+            gather(bins, level0, d, true, ~0ull, each);
+            cluster_sync_all();
+            if (rank == 0) draw_of_list(upto);
             return;
         }
         u64 kept;
