@@ -59,6 +59,7 @@ constexpr int kTops = 256;        // thread maxima from which top-k's bound is t
 constexpr float kRange = 31.5f;   // weights below exp(-31.5) of the largest count as 0 in a prefix's sum
 constexpr float kFixed = 1099511627776.f;  // 2^40
 constexpr float kLog2e = 1.44269504088896f;
+constexpr float kInRange = 65536.f;  // logits over T, in base 2, whose weights relative to one another are summed as they come
 
 using u64 = unsigned long long;
 
@@ -635,7 +636,9 @@ __device__ void Sampler<kF32>::run(int64_t r) {
         const float here = largest(x);
         if (here > top) {
             const float to = here * per;
-            sum = top > -INFINITY ? sum * ex2(shift - to) : 0.f;
+            // beyond this range a sum means nothing (`shift` may be infinite, so may the sum), and any larger logit that
+            // is in range outweighs it wholly
+            sum = top > -INFINITY && fabsf(shift) < kInRange ? sum * ex2(shift - to) : 0.f;
             if constexpr (next) next_top = top;
             top = here, shift = to, top_unit = i;
         } else if constexpr (next) {
@@ -681,9 +684,9 @@ __device__ void Sampler<kF32>::run(int64_t r) {
         if (!by_rank && lane == 0) s.tops[warp] = jth;
     }
     const float cta_top = block_fold<true>(top, s.warp_value[0]);
-    if (plain && fabsf(cta_top * per) < 32768.f) {
+    if (plain && fabsf(cta_top * per) < kInRange / 2) {
         // a thread whose largest logit lies beyond the range of its own sum weighs nothing beside that
-        sum = top > -INFINITY && fabsf(shift) < 65536.f ? sum * ex2(fmaf(-cta_top, per, shift)) : 0.f;
+        sum = top > -INFINITY && fabsf(shift) < kInRange ? sum * ex2(fmaf(-cta_top, per, shift)) : 0.f;
     } else {  // a logit or a setting at the end of its range
         sum = 0.f;
         const Row own = {cta_top, row.inv_t};
