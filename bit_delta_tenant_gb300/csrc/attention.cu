@@ -832,7 +832,7 @@ cudaError_t launch_typed(const AttnArgs &a, const DevCtx &ctx, cudaStream_t stre
     // CTAs and by warps, 32 and 8 heads, bf16: 256 sequences of up to 64, 128, 256, 512, 1024 tokens 16.9 / 9.7,
     // 17.8 / 12.6, 21.7 / 18.4, 25.7 / 29.6, 35.4 / 56.9 us; 64 of up to 64, 128, 256: 7.5 / 5.8, 7.7 / 8.1, 10.5 / 11.8.
     int64_t most = static_cast<int64_t>(a.max_pages) * a.page_size;
-    if (a.window > 0) most = std::min<int64_t>(most, a.window + kTileOf<kE4m3> - 1);
+    if (a.window > 0) most = std::min(most, static_cast<int64_t>(a.window) + kTileOf<kE4m3> - 1);
     const int64_t heads = static_cast<int64_t>(a.n_seqs) * a.kv_heads * a.subs, ctas = ctx.num_sms * kCtasOf<kPack>;
     const int64_t tiles = (most + kTileOf<kE4m3> - 1) / kTileOf<kE4m3>, blocks = (tiles + kWarps - 1) / kWarps;
     const int64_t steps = (heads * (blocks + kSetup) + ctas - 1) / ctas;
