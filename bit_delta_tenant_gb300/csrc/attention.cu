@@ -55,6 +55,7 @@ constexpr int kMaxCtasPerSm = 3;
 constexpr int kDepth = 2;  // tiles in a warp's ring: one in use, one in flight
 constexpr int64_t kMaxKeys = 1 << 30;  // the division by the page size is exact, positions stay int32
 constexpr int kSlotFloats = kRows * 128 + 2 * kRows;  // a part's output, maxima and sums
+constexpr int64_t kAloneKeys = 512;  // keys of a head that a warp may be given by itself
 constexpr int kSetup = 2;  // what a (sequence, head) costs a CTA beside its blocks, in blocks
 constexpr int kFan = 8;      // parts joined at a time
 constexpr int kLevels = 4;   // enough for kFan^4 parts
@@ -828,16 +829,21 @@ cudaError_t launch_form(const AttnArgs &a, const DevCtx &ctx, cudaStream_t strea
 template <int kDim, bool kE4m3, bool kPack>
 cudaError_t launch_typed(const AttnArgs &a, const DevCtx &ctx, cudaStream_t stream) {
     // The host has no lengths, but the page table's width and the window bound them.  With few keys to a head a CTA's
-    // steps are mostly its setup and joins, so each warp takes heads by itself where that is not many more steps.  By
-    // CTAs and by warps, 32 and 8 heads, bf16: 256 sequences of up to 64, 128, 256, 512, 1024 tokens 16.9 / 9.7,
-    // 17.8 / 12.6, 21.7 / 18.4, 25.7 / 29.6, 35.4 / 56.9 us; 64 of up to 64, 128, 256: 7.5 / 5.8, 7.7 / 8.1, 10.5 / 11.8.
-    int64_t most = static_cast<int64_t>(a.max_pages) * a.page_size;
-    if (a.window > 0) most = std::min(most, static_cast<int64_t>(a.window) + kTileOf<kE4m3> - 1);
+    // steps are mostly its setup and joins, so each warp takes heads by itself where that is not many more steps and no
+    // head can have more than kAloneKeys keys: beyond that one long sequence among short ones keeps its few warps busy
+    // alone (224 sequences, 8 KV heads, one of 65536 tokens, the others of 64: 59 us split, 2254 alone).  By CTAs and by
+    // warps, 32 and 8 heads, bf16, us, all sequences as long as the table allows / lengths spread in their logarithm:
+    //   200 sequences up to  64: 15.5, 8.1 / 14.7, 7.1;   256: 42.5, 36.2 / 18.7, 13.8;  512: 71.0, 65.3 / 21.4, 22.4
+    //                      4096: 487, 482 / -;           8191: - / 121, 308
+    //   64 sequences up to   64: 8.3, 6.7 / 8.0, 6.2;     192: 13.2, 12.5 / 10.8, 10.4;  256: 14.6, 15.2 / 10.8, 12.2
+    const int64_t width = static_cast<int64_t>(a.max_pages) * a.page_size;
+    const int64_t keys = a.window > 0 ? std::min<int64_t>(width, a.window) : width;  // that a query may see,
+    const int64_t most = a.window > 0 ? std::min<int64_t>(width, keys + kTileOf<kE4m3> - 1) : width;  // and with what else their tiles hold
     const int64_t heads = static_cast<int64_t>(a.n_seqs) * a.kv_heads * a.subs, ctas = ctx.num_sms * kCtasOf<kPack>;
     const int64_t tiles = (most + kTileOf<kE4m3> - 1) / kTileOf<kE4m3>, blocks = (tiles + kWarps - 1) / kWarps;
     const int64_t steps = (heads * (blocks + kSetup) + ctas - 1) / ctas;
     const int64_t steps_alone = (heads + ctas * kWarps - 1) / (ctas * kWarps) * (tiles + kSetup);
-    if (steps_alone <= steps + steps / 4 + 5) return launch_form<kDim, kE4m3, kPack, true>(a, ctx, stream);
+    if (keys <= kAloneKeys && steps_alone <= steps + steps / 4 + 5) return launch_form<kDim, kE4m3, kPack, true>(a, ctx, stream);
     return launch_form<kDim, kE4m3, kPack, false>(a, ctx, stream);
 }
 

@@ -29,3 +29,29 @@ def test_the_largest_window_is_no_window(kv):
         check(pool, q, out, lse)
         assert split
         assert torch.equal(out, plain[0]) and torch.equal(lse, plain[1])
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("seqs,kv_heads,longest", [(200, 8, 3001), (57, 32, 777), (224, 8, 6000)])
+def test_a_long_sequence_among_short_ones_is_split(kv, seqs, kv_heads, longest):
+    """So many heads that they come to one per warp, under a table of 8192 tokens."""
+    lengths = np.random.default_rng(seqs).integers(0, 20, seqs).tolist()
+    lengths[seqs // 3] = longest
+    pool = widened(Pool(lengths, kv_heads, 64, 32, kv, seed=2), 256)
+    q = randn((seqs, kv_heads, 64), 9, 2.0).bfloat16()
+    out, lse, split = run_and_tell(pool, q)
+    assert split
+    check(pool, q, out, lse, seqs=[0, 1, seqs // 3, seqs - 1])
+    assert bd.bd_get_device_status() == bd.BD_OK
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("window,pages", [(0, 8), (100, 256)])
+def test_short_heads_are_taken_whole(kv, window, pages):
+    """Under a narrow table, or a wide one with a window; with as many heads as warps."""
+    lengths = np.random.default_rng(5).integers(0, 250, 200).tolist()
+    pool = widened(Pool(lengths, 8, 64, 32, kv, seed=3), pages)
+    q = randn((200, 8, 64), 9, 2.0).bfloat16()
+    out, lse, split = run_and_tell(pool, q, window)
+    assert not split
+    check(pool, q, out, lse, window=window, seqs=[0, 1, 77, 199])
