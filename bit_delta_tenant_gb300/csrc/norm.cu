@@ -92,8 +92,18 @@ __global__ void __launch_bounds__(kThreads, (kChunks == 1 ? 2048 : kChunks == 2 
         }
         if (c < chunks && a.residual_out) *reinterpret_cast<uint4 *>(a.residual_out + base + c * 16) = pack8(h[u]);
     }
-    // divided by n before the reduction, so that only a mean beyond fp32 overflows
-    const float rstd = rsqrtf(row_reduce<kWarps, false>(ss * a.inv_n, red[0]) + a.eps);
+    // Divided by n before the reduction, and where a thread's own squares pass fp32 (an element beyond 1.8e19) each of
+    // them before it is added, so that only a mean beyond fp32 overflows.  Not always so: squares of less than n 2^-126,
+    // which matter where eps is 0, would lose digits.
+    float mean = ss * a.inv_n;
+    if (!(ss < INFINITY)) {
+        mean = 0.f;
+#pragma unroll
+        for (int u = 0; u < kChunks; ++u)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) mean = fmaf(h[u][j] * a.inv_n, h[u][j], mean);
+    }
+    const float rstd = rsqrtf(row_reduce<kWarps, false>(mean, red[0]) + a.eps);
     float top = 0.f;
 #pragma unroll
     for (int u = 0; u < kChunks; ++u) {
