@@ -823,8 +823,11 @@ __device__ void Sampler<kF32>::run(int64_t r) {
         return;
     }
     if (!filtered) {  // the tokens of min-p, or settings and logits at the end of their range
-        float least = plain && row.top < INFINITY && low > 0.f ? row.top + logf(low) * temp : -INFINITY;
-        least -= fabsf(least) * 1e-6f + temp * 1e-6f;  // below any token that the exact test keeps
+        // Below any token that the exact test keeps: t, logf(low) * temp and their sum with the largest logit are off
+        // by less than 2^-21 of themselves, and expf(-t) by less than 2^-21.
+        const float down = low > 0.f ? logf(low) * temp : -INFINITY;
+        float least = plain && row.top < INFINITY ? row.top + down : -INFINITY;
+        least -= (fabsf(least) + fabsf(down) + temp) * 1e-6f;
         if (!(least > -INFINITY)) least = -INFINITY;
         candidates(least, [&](int i, const float (&x)[kPer]) {
             if (largest(x) < least) return;
