@@ -34,7 +34,7 @@
 // Sums of weights do not depend on the order of atomics: they are whole numbers.  Within a
 // bin of width d, w = exp(-start) w' with w' in [1 - d, 1], and a bin sums
 // round((w' - 1 + d) P / d) in 32 bits beside its count, P = 65535 or what a long slice
-// leaves room for; top-p's first histogram, which needs no counts, sums whole parts of w' (Bins::add).
+// leaves room for; top-p's first histogram, which needs no counts, sums parts of 2^-22 in two words (Bins::add).
 // Across bins weights are fixed-point with 40 fractional bits.  The sum of all weights is
 // fp32 in an order fixed by the shape.
 #include <algorithm>
@@ -164,10 +164,10 @@ struct Row {
 struct Bins {
     static constexpr float kWhole = 8388608.f;  // 2^23
     float scale, width, unit, parts_of, most;  // 1 / width, width, parts / width, its inverse, parts
-    float all, width2, dither;                 // of add()
+    float width2;                              // of add()
     __device__ __forceinline__ Bins(float range, float parts)
         : scale((kBins - 2) / range), width(range / (kBins - 2)), unit(parts * scale), parts_of(width / parts), most(parts),
-          all(floorf(parts * 0.96f)), width2(width * kLog2e), dither((threadIdx.x % 32 - 15.5f) / 32) {}
+          width2(width * kLog2e) {}
     static __device__ __forceinline__ int whole(float sum) { return __float_as_int(sum) - __float_as_int(kWhole); }  // sum = 2^23 + n
     __device__ __forceinline__ int bin(float t) const { return min(whole(fmaf(t, scale, kWhole)), kBins - 1); }
     __device__ __forceinline__ float start(int b) const { return (b - 0.5f) * width; }
@@ -183,17 +183,20 @@ struct Bins {
         const float w = fmaf(static_cast<float>(parts), parts_of, static_cast<float>(count) * (1.f - width));
         return __float2ull_rn(w * (ex2(start(b) * -kLog2e) * kFixed));
     }
-    // Adds a token to bins that hold their weight in one word, in whole parts of exp(-b width), and no count.  A weight is
-    // rounded to 2^-17 of itself, equal ones at other places up or down (`dither`, within a half, by lane and by `odd`),
-    // so a bin's sum keeps the error of one token over the root of their number; a weight of 1 is exact.
-    __device__ __forceinline__ void add(uint32_t *bins, float t, bool odd) const {
+    // Adds a token to bins that hold a weight's whole part of exp(-b width) 2^-22 in two words, its upper bits in one and
+    // the lower kLow in the other, and no count: two words that 2^18 tokens do not fill.  (One word has room for 14 to 16
+    // bits of a weight only: a prefix of two or three heavy tokens then ends one token too early or late.)
+    static constexpr int kLow = 11;
+    static constexpr float kOne = 4194304.f;  // 2^22
+    __device__ __forceinline__ void add(uint32_t *high, uint32_t *low, float t) const {
         const float at = fmaf(t, scale, kWhole);
         const int b = whole(at);
-        const float w = ex2(fmaf(at - kWhole, width2, t * -kLog2e));  // exp(-width / 2) .. exp(width / 2) < 1 / 0.96
-        if (b < kBins - 1) atomicAdd(&bins[b], static_cast<uint32_t>(whole(fmaf(w, all, odd ? -dither : dither) + kWhole)));
+        const float w = ex2(fmaf(at - kWhole, width2, t * -kLog2e));  // exp(-width / 2) .. exp(width / 2) < 1.04
+        const uint32_t n = static_cast<uint32_t>(whole(fmaf(w, kOne, kWhole)));
+        if (b < kBins - 1) atomicAdd(&high[b], n >> kLow), atomicAdd(&low[b], n & ((1u << kLow) - 1));
     }
     __device__ __forceinline__ u64 mass_of(int b, u64 parts) const {
-        return b == kBins - 1 ? 0 : __float2ull_rn(static_cast<float>(parts) / all * (ex2(b * -width2) * kFixed));
+        return b == kBins - 1 ? 0 : __float2ull_rn(static_cast<float>(parts) * (ex2(b * -width2) * (kFixed / kOne)));
     }
 };
 // floor(p * mass) for 0 < p < 1, at least 1: the first token always stays
@@ -459,7 +462,8 @@ struct Sampler {
     __device__ __forceinline__ Scan totals_of_whole(const Bins &bins) {
         u64 parts = 0;
 #pragma unroll
-        for (int q = 0; q < kMaxCluster; ++q) parts += q < size ? ld_remote(remote(&s.parts[tid], q)) : 0;
+        for (int q = 0; q < kMaxCluster; ++q)
+            if (q < size) parts += (static_cast<u64>(ld_remote(remote(&s.count[tid], q))) << Bins::kLow) + ld_remote(remote(&s.parts[tid], q));
         return scan(parts > 0, bins.mass_of(tid, parts));
     }
     // Sends this CTA's tokens of one set to every CTA's list: digit d at level `at`, or with `upto` all bins up to d.
@@ -967,7 +971,7 @@ __device__ void Sampler<kF32>::run(int64_t r) {
                 for (int j = 0; j < kPer; ++j) {
                     const float t = exact ? row.t_of(x[j]) : __fmul_rn(__fsub_rn(row.top, x[j]), row.inv_t);
                     score[j] = __fadd_rn(-t, noise[j]);
-                    bins.add(s.parts, t, j % 2);
+                    bins.add(s.count, s.parts, t);
                 }
                 const float here = largest(score);
                 if (here > most) most = here, unit = i;

@@ -565,7 +565,9 @@ int32_t bd_attention_decode(const bd_kv_cache *cache, const void *q, int32_t q_h
  *   top_k  the first k                     (k <= 0: off)
  *   top_p  of those, the shortest prefix whose share of their summed w is at
  *          least p: a token stays while the w before it sum to less than
- *          p * sum.  The first always stays; p >= 1: off.
+ *          p * sum.  The first always stays; p >= 1: off.  (Both sums are
+ *          within 2^-18 of their value: a p that close to a prefix's share
+ *          may end the prefix one token beside it.)
  *   min_p  those with w_i >= min_p         (<= 0: off; the largest w is 1 and
  *          always stays)
  * The token drawn is the kept one with the largest z_i + noise_i, the lowest
