@@ -176,9 +176,24 @@ def _stream(stream=None) -> ctypes.c_void_p:
     return ctypes.c_void_p(s.cuda_stream if hasattr(s, "cuda_stream") else int(s))
 
 
+_NOT_ON_DEVICE = "tensors passed to libbitdelta must be on a CUDA device"
+
+
+def _address(t: torch.Tensor) -> int:
+    """Address of a contiguous tensor in device memory: the kernels read it without further checks."""
+    if not t.is_contiguous():
+        raise ValueError("tensors passed to libbitdelta must be contiguous")
+    if not t.is_cuda:
+        raise ValueError(_NOT_ON_DEVICE)
+    return t.data_ptr()
+
+
 def _ptr(t: torch.Tensor | None) -> ctypes.c_void_p:
-    if t is None:
-        return ctypes.c_void_p(0)
+    return ctypes.c_void_p(0 if t is None else _address(t))
+
+
+def _host_ptr(t: torch.Tensor) -> ctypes.c_void_p:
+    """Address of a contiguous tensor that the library reads or writes from the host or by copies."""
     if not t.is_contiguous():
         raise ValueError("tensors passed to libbitdelta must be contiguous")
     return ctypes.c_void_p(t.data_ptr())
@@ -252,13 +267,14 @@ class DeltaCache:
         self._keep = {}
         self._handle = ctypes.c_void_p()
         self._host = bool(host_arena)
-        rc = lib.bd_cache_create(ctypes.addressof(self._state), size, int(max_variants), _ptr(arena),
+        rc = lib.bd_cache_create(ctypes.addressof(self._state), size, int(max_variants),
+                                 _host_ptr(arena) if host_arena else _ptr(arena),
                                  arena.numel() * arena.element_size(), float(half_life_s), 1 if host_arena else 0,
                                  ctypes.byref(self._handle))
         _check(rc, "bd_cache_create")
 
     def register(self, variant: int, bits: torch.Tensor, alpha: torch.Tensor) -> None:
-        rc = load_library().bd_cache_register(self._handle, int(variant), _ptr(bits), bits.numel(), _ptr(alpha),
+        rc = load_library().bd_cache_register(self._handle, int(variant), _host_ptr(bits), bits.numel(), _host_ptr(alpha),
                                               alpha.numel() * 4)
         _check(rc, "bd_cache_register")
         self._keep[variant] = (bits, alpha)
@@ -414,8 +430,8 @@ def bd_linear_grouped(x: torch.Tensor, variant_ids: torch.Tensor, w_base: torch.
         raise ValueError("bits_v, alpha_v and alpha_modes_v must have one entry per variant")
     m = x.shape[0]
     n_out, n_in = w_base.shape
-    bits_arr = (ctypes.c_void_p * n_var)(*[b.data_ptr() for b in bits_v])
-    alpha_arr = (ctypes.c_void_p * n_var)(*[a.data_ptr() for a in alpha_v])
+    bits_arr = (ctypes.c_void_p * n_var)(*[_address(b) for b in bits_v])
+    alpha_arr = (ctypes.c_void_p * n_var)(*[_address(a) for a in alpha_v])
     modes_arr = (ctypes.c_int32 * n_var)(*[int(md) for md in alpha_modes_v])
     rc = load_library().bd_linear_grouped(_ptr(x), _ptr(variant_ids), m, _ptr(w_base), bits_arr, alpha_arr,
                                           modes_arr, n_var, n_out, n_in, _ptr(y), _ptr(workspace),
@@ -424,34 +440,43 @@ def bd_linear_grouped(x: torch.Tensor, variant_ids: torch.Tensor, w_base: torch.
 
 
 # ---- the rest of a decode step: norm, key-value cache, attention, sampling ----------------
-# Tensors are checked here for type, shape and layout, because the library sees only their
+# Tensors are checked here for type, shape, layout and device, because the library sees only their
 # addresses.  A decode step makes many of these calls on small inputs, so the checks are kept to a
 # few attribute reads per tensor and the stream is read as a raw handle.
 
 
-def _refuse(t: torch.Tensor, name: str, shape, dtype) -> None:
+def _refuse(t: torch.Tensor, name: str, shape, dtype, device) -> None:
     if t.dtype != dtype:
         raise ValueError(f"{name}: expected {dtype}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.get_device() < 0:
+        raise ValueError(f"{name}: {_NOT_ON_DEVICE}")
+    if t.get_device() != device:
+        raise ValueError(f"{name}: expected a tensor on CUDA device {device}, got one on {t.get_device()}")
     raise ValueError(f"{name}: tensors passed to libbitdelta must be contiguous")
 
 
-def _arg(t: torch.Tensor | None, name: str, shape, dtype) -> int | None:
-    """Address of a contiguous tensor of the given shape and type (None stays NULL)."""
+def _device(t: torch.Tensor, name: str) -> int:
+    """The CUDA device that holds t, on which all other tensors of its call have to be."""
+    device = t.get_device()
+    if device < 0:
+        raise ValueError(f"{name}: {_NOT_ON_DEVICE}")
+    return device
+
+
+def _arg(t: torch.Tensor | None, name: str, shape, dtype, device: int) -> int | None:
+    """Address of a contiguous tensor of the given shape and type on that device (None stays NULL)."""
     if t is None:
         return None
-    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
-        _refuse(t, name, shape, dtype)
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or t.get_device() != device:
+        _refuse(t, name, shape, dtype, device)
     return t.data_ptr()
 
 
-def _raw_stream(stream, t: torch.Tensor) -> int:
-    """Handle of `stream`, or of the current stream of the device that holds t."""
+def _raw_stream(stream, device: int) -> int:
+    """Handle of `stream`, or of the device's current stream."""
     if stream is None:
-        device = t.get_device()
-        if device < 0:
-            raise ValueError("tensors passed to libbitdelta must be on a CUDA device")
         return torch._C._cuda_getCurrentRawStream(device)
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
@@ -467,7 +492,7 @@ def bd_rmsnorm(x: torch.Tensor, weight: torch.Tensor, eps: float, y: torch.Tenso
     `residual_out` receives bf16(x + residual) and may be `residual` itself.  A bf16 `y` is
     rounded once; a float8_e4m3fn `y` comes with `y_scale`, fp32 [m, n / 128] (a scale per
     128 columns) or [m, 1] (one per row)."""
-    shape = x.shape
+    device, shape = _device(x, "x"), x.shape
     m, n = shape
     n_weights, w_shape = (weight.shape[0], (weight.shape[0], n)) if weight.dim() == 2 else (1, (n,))
     y_type, scale_cols, scale = BD_Y_BF16, 0, None
@@ -476,14 +501,15 @@ def bd_rmsnorm(x: torch.Tensor, weight: torch.Tensor, eps: float, y: torch.Tenso
         cols = y_scale.shape[1] if y_scale is not None and y_scale.dim() == 2 else 0
         if cols < 1 or n % cols != 0:
             raise ValueError("y_scale: an 8-bit y comes with scales of shape [m, n / 128] or [m, 1]")
-        scale_cols, scale = n // cols, _arg(y_scale, "y_scale", (m, cols), _F32)
+        scale_cols, scale = n // cols, _arg(y_scale, "y_scale", (m, cols), _F32, device)
     elif y_scale is not None:
         raise ValueError("y_scale: only an 8-bit y has scales")
     rc = (_lib or load_library()).bd_rmsnorm(
-        _arg(x, "x", shape, _BF16), None if residual is None else _arg(residual, "residual", shape, _BF16),
-        _arg(weight, "weight", w_shape, _BF16), None if weight_ids is None else _arg(weight_ids, "weight_ids", (m,), _I32),
-        n_weights, m, n, eps, _arg(y, "y", shape, _E4M3 if y_type else _BF16), y_type, scale, scale_cols,
-        None if residual_out is None else _arg(residual_out, "residual_out", shape, _BF16), _raw_stream(stream, x))
+        _arg(x, "x", shape, _BF16, device), None if residual is None else _arg(residual, "residual", shape, _BF16, device),
+        _arg(weight, "weight", w_shape, _BF16, device),
+        None if weight_ids is None else _arg(weight_ids, "weight_ids", (m,), _I32, device),
+        n_weights, m, n, eps, _arg(y, "y", shape, _E4M3 if y_type else _BF16, device), y_type, scale, scale_cols,
+        None if residual_out is None else _arg(residual_out, "residual_out", shape, _BF16, device), _raw_stream(stream, device))
     if rc:
         _check(rc, "bd_rmsnorm")
 
@@ -506,21 +532,22 @@ class KVCache:
             raise ValueError("k_scale and v_scale come with an 8-bit cache, and only with one")
         n_pages, self.kv_heads, self.page_size, self.head_dim = k.shape
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        device = self.device = _device(k, "k")
         d = self.desc = KVCacheDesc()
-        d.k, d.v = _arg(k, "k", k.shape, k.dtype), _arg(v, "v", k.shape, k.dtype)
-        d.k_scale = _arg(k_scale, "k_scale", k.shape[:3], _U8)
-        d.v_scale = _arg(v_scale, "v_scale", k.shape[:3], _U8)
+        d.k, d.v = _arg(k, "k", k.shape, k.dtype, device), _arg(v, "v", k.shape, k.dtype, device)
+        d.k_scale = _arg(k_scale, "k_scale", k.shape[:3], _U8, device)
+        d.v_scale = _arg(v_scale, "v_scale", k.shape[:3], _U8, device)
         d.n_pages, d.kv_heads, d.head_dim, d.page_size = n_pages, self.kv_heads, self.head_dim, self.page_size
         d.kv_type = BD_KV_E4M3 if e4m3 else BD_KV_BF16
         self._ref = ctypes.byref(d)
 
 
-def _table(page_table: torch.Tensor):
+def _table(page_table: torch.Tensor, device: int):
     """(address, n_seqs, max_pages) of a page table."""
     shape = page_table.shape
     if len(shape) != 2:
         raise ValueError("page_table: expected [n_seqs, max_pages]")
-    return _arg(page_table, "page_table", shape, _I32), shape[0], shape[1]
+    return _arg(page_table, "page_table", shape, _I32, device), shape[0], shape[1]
 
 
 def bd_kv_append(cache: KVCache, q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor, positions: torch.Tensor,
@@ -531,21 +558,21 @@ def bd_kv_append(cache: KVCache, q: torch.Tensor | None, k: torch.Tensor, v: tor
     Token i goes to position positions[i] of sequence seq_ids[i] (of sequence i without
     seq_ids); a negative position skips it.  `rope` is fp32 [positions, head_dim], cosines then
     sines; without it nothing is rotated and q and q_out are None.  q_out may be q."""
-    n, dim = k.shape[0], cache.head_dim
+    n, dim, device = k.shape[0], cache.head_dim, cache.device
     kv_shape = (n, cache.kv_heads, dim)
     q_heads, qp, qo = 0, None, None
     if q is not None or q_out is not None:
         if q is None or q_out is None or q.dim() != 3:
             raise ValueError("q, q_out: both [tokens, q_heads, head_dim], or neither")
         q_heads = q.shape[1]
-        qp, qo = _arg(q, "q", (n, q_heads, dim), _BF16), _arg(q_out, "q_out", (n, q_heads, dim), _BF16)
+        qp, qo = _arg(q, "q", (n, q_heads, dim), _BF16, device), _arg(q_out, "q_out", (n, q_heads, dim), _BF16, device)
     rope_len = 0 if rope is None else rope.shape[0]
-    table, n_seqs, max_pages = _table(page_table)
+    table, n_seqs, max_pages = _table(page_table, device)
     rc = (_lib or load_library()).bd_kv_append(
-        cache._ref, qp, q_heads, _arg(k, "k", kv_shape, _BF16), _arg(v, "v", kv_shape, _BF16), n,
-        None if seq_ids is None else _arg(seq_ids, "seq_ids", (n,), _I32), _arg(positions, "positions", (n,), _I32), table,
-        n_seqs, max_pages, None if rope is None else _arg(rope, "rope", (rope_len, dim), _F32), rope_len, qo,
-        _raw_stream(stream, k))
+        cache._ref, qp, q_heads, _arg(k, "k", kv_shape, _BF16, device), _arg(v, "v", kv_shape, _BF16, device), n,
+        None if seq_ids is None else _arg(seq_ids, "seq_ids", (n,), _I32, device),
+        _arg(positions, "positions", (n,), _I32, device), table, n_seqs, max_pages, None if rope is None else _arg(rope, "rope", (rope_len, dim), _F32, device), rope_len, qo,
+        _raw_stream(stream, device))
     if rc:
         _check(rc, "bd_kv_append")
 
@@ -553,11 +580,12 @@ def bd_kv_append(cache: KVCache, q: torch.Tensor | None, k: torch.Tensor, v: tor
 def bd_kv_read(cache: KVCache, page_table: torch.Tensor, offsets: torch.Tensor, k_out: torch.Tensor,
                v_out: torch.Tensor, stream=None) -> None:
     """The first offsets[i + 1] - offsets[i] cached tokens of sequence i, as bf16 rows offsets[i] .. of k_out and v_out."""
-    table, n_seqs, max_pages = _table(page_table)
+    device = cache.device
+    table, n_seqs, max_pages = _table(page_table, device)
     shape = (k_out.shape[0], cache.kv_heads, cache.head_dim)
     rc = (_lib or load_library()).bd_kv_read(
-        cache._ref, table, n_seqs, max_pages, _arg(offsets, "offsets", (n_seqs + 1,), _I32), shape[0],
-        _arg(k_out, "k_out", shape, _BF16), _arg(v_out, "v_out", shape, _BF16), _raw_stream(stream, k_out))
+        cache._ref, table, n_seqs, max_pages, _arg(offsets, "offsets", (n_seqs + 1,), _I32, device), shape[0],
+        _arg(k_out, "k_out", shape, _BF16, device), _arg(v_out, "v_out", shape, _BF16, device), _raw_stream(stream, device))
     if rc:
         _check(rc, "bd_kv_read")
 
@@ -575,14 +603,15 @@ def bd_attention_decode(cache: KVCache, q: torch.Tensor, page_table: torch.Tenso
     `scale` defaults to head_dim ** -0.5; `window` > 0 lets a query see the last `window` tokens only.
     `workspace` is a zero-filled device buffer of at least bd_attention_workspace_size bytes (left
     ready for the next call)."""
-    table, n_seqs, max_pages = _table(page_table)
+    device = cache.device
+    table, n_seqs, max_pages = _table(page_table, device)
     q_heads = q.shape[1] if q.dim() == 3 else 0
     shape = (n_seqs, q_heads, cache.head_dim)
     rc = (_lib or load_library()).bd_attention_decode(
-        cache._ref, _arg(q, "q", shape, _BF16), q_heads, table, _arg(lengths, "lengths", (n_seqs,), _I32), n_seqs, max_pages,
-        cache.head_dim ** -0.5 if scale is None else scale, window, _arg(out, "out", shape, _BF16),
-        None if lse is None else _arg(lse, "lse", (n_seqs, q_heads), _F32), workspace.data_ptr(), workspace.nbytes,
-        _raw_stream(stream, q))
+        cache._ref, _arg(q, "q", shape, _BF16, device), q_heads, table, _arg(lengths, "lengths", (n_seqs,), _I32, device),
+        n_seqs, max_pages, cache.head_dim ** -0.5 if scale is None else scale, window, _arg(out, "out", shape, _BF16, device),
+        None if lse is None else _arg(lse, "lse", (n_seqs, q_heads), _F32, device),
+        _arg(workspace, "workspace", workspace.shape, workspace.dtype, device), workspace.nbytes, _raw_stream(stream, device))
     if rc:
         _check(rc, "bd_attention_decode")
 
@@ -594,16 +623,17 @@ def bd_sample(logits: torch.Tensor, noise: torch.Tensor, ids: torch.Tensor, temp
 
     `temperature`, `top_k` (int32), `top_p` and `min_p` hold one setting per row; None leaves the
     filter off (temperature 1).  `logprob` receives the drawn token's log probability before the filters."""
-    shape = logits.shape
+    device, shape = _device(logits, "logits"), logits.shape
     m, vocab = shape
     row = (m,)
     half = logits.dtype is _BF16
     rc = (_lib or load_library()).bd_sample(
-        _arg(logits, "logits", shape, _BF16 if half else _F32), BD_LOGITS_BF16 if half else BD_LOGITS_F32, m, vocab,
-        None if temperature is None else _arg(temperature, "temperature", row, _F32),
-        None if top_k is None else _arg(top_k, "top_k", row, _I32), None if top_p is None else _arg(top_p, "top_p", row, _F32),
-        None if min_p is None else _arg(min_p, "min_p", row, _F32), _arg(noise, "noise", shape, _F32),
-        _arg(ids, "ids", row, _I32), None if logprob is None else _arg(logprob, "logprob", row, _F32),
-        _raw_stream(stream, logits))
+        _arg(logits, "logits", shape, _BF16 if half else _F32, device), BD_LOGITS_BF16 if half else BD_LOGITS_F32, m, vocab,
+        None if temperature is None else _arg(temperature, "temperature", row, _F32, device),
+        None if top_k is None else _arg(top_k, "top_k", row, _I32, device),
+        None if top_p is None else _arg(top_p, "top_p", row, _F32, device),
+        None if min_p is None else _arg(min_p, "min_p", row, _F32, device), _arg(noise, "noise", shape, _F32, device),
+        _arg(ids, "ids", row, _I32, device), None if logprob is None else _arg(logprob, "logprob", row, _F32, device),
+        _raw_stream(stream, device))
     if rc:
         _check(rc, "bd_sample")
