@@ -10,6 +10,11 @@ namespace {
 
 bool aligned(const void *p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
 
+// A page table without entries (nothing cached yet) has no address.
+bool no_table(const int32_t *page_table, int32_t n_seqs, int32_t max_pages) {
+    return !page_table && n_seqs > 0 && max_pages > 0;
+}
+
 int32_t status_of(cudaError_t e) { return e == cudaSuccess ? BD_OK : BD_ERR_CUDA; }
 
 int32_t check_cache(const bd_kv_cache *c) {
@@ -64,7 +69,7 @@ BD_API int32_t bd_kv_append(const bd_kv_cache *cache, const void *q, int32_t q_h
     if (n_tokens < 0 || n_seqs < 0 || max_pages < 0 || q_heads < 0 || rope_len < 0) return BD_ERR_INVALID_ARG;
     if ((q != nullptr) != (q_out != nullptr) && n_tokens > 0) return BD_ERR_INVALID_ARG;
     if (q && (!rope || q_heads < 1)) return BD_ERR_INVALID_ARG;
-    if (n_tokens > 0 && (!k || !v || !positions || !page_table)) return BD_ERR_INVALID_ARG;
+    if (n_tokens > 0 && (!k || !v || !positions || no_table(page_table, n_seqs, max_pages))) return BD_ERR_INVALID_ARG;
     if (n_tokens >= BD_MAX_DIM || q_heads > BD_KV_MAX_HEADS * 16) return BD_ERR_UNSUPPORTED_SHAPE;
     if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(rope, 16) || !aligned(q_out, 16))
         return BD_ERR_MISALIGNED;
@@ -82,7 +87,8 @@ BD_API int32_t bd_kv_read(const bd_kv_cache *cache, const int32_t *page_table, i
     const int32_t c = check_cache(cache);
     if (c != BD_OK) return c;
     if (total < 0 || n_seqs < 0 || max_pages < 0) return BD_ERR_INVALID_ARG;
-    if (total > 0 && n_seqs > 0 && (!page_table || !offsets || !k_out || !v_out)) return BD_ERR_INVALID_ARG;
+    if (total > 0 && n_seqs > 0 && (no_table(page_table, n_seqs, max_pages) || !offsets || !k_out || !v_out))
+        return BD_ERR_INVALID_ARG;
     if (total >= BD_MAX_DIM) return BD_ERR_UNSUPPORTED_SHAPE;
     if (!aligned(k_out, 16) || !aligned(v_out, 16) || !aligned(page_table, 4) || !aligned(offsets, 4))
         return BD_ERR_MISALIGNED;
@@ -119,7 +125,7 @@ BD_API int32_t bd_attention_decode(const bd_kv_cache *cache, const void *q, int3
     const int32_t c = check_heads(cache, n_seqs, q_heads);
     if (c != BD_OK) return c;
     if (max_pages < 0 || window < 0 || !(scale - scale == 0.f)) return BD_ERR_INVALID_ARG;
-    if (n_seqs > 0 && (!q || !page_table || !lengths || !out)) return BD_ERR_INVALID_ARG;
+    if (n_seqs > 0 && (!q || no_table(page_table, n_seqs, max_pages) || !lengths || !out)) return BD_ERR_INVALID_ARG;
     if (!aligned(q, 16) || !aligned(out, 16) || !aligned(page_table, 4) || !aligned(lengths, 4) || !aligned(lse, 4))
         return BD_ERR_MISALIGNED;
     if (n_seqs == 0) return BD_OK;

@@ -447,6 +447,8 @@ int32_t bd_rmsnorm(const void *x, const void *residual, const void *weight, cons
  * nothing to a power-of-two scale, x / s and q * s are exact, and q * s is a
  * bf16 number (infinite from 2^128), so reading back into bf16 rounds nothing.
  *
+ * A page table of no entries (n_seqs or max_pages 0: nothing cached yet) may be NULL.
+ *
  * page_size: a multiple of 16, 16 .. 1024.  head_dim: 64 or 128.  kv_heads:
  * 1 .. BD_KV_MAX_HEADS.  Pointers 16-byte aligned.  The struct is read during
  * the call only.
