@@ -609,7 +609,8 @@ def bd_attention_decode(cache: KVCache, q: torch.Tensor, page_table: torch.Tenso
     shape = (n_seqs, q_heads, cache.head_dim)
     rc = (_lib or load_library()).bd_attention_decode(
         cache._ref, _arg(q, "q", shape, _BF16, device), q_heads, table, _arg(lengths, "lengths", (n_seqs,), _I32, device),
-        n_seqs, max_pages, cache.head_dim ** -0.5 if scale is None else scale, window, _arg(out, "out", shape, _BF16, device),
+        n_seqs, max_pages, cache.head_dim ** -0.5 if scale is None else scale, max(-1, min(window, 0x7FFFFFFF)),
+        _arg(out, "out", shape, _BF16, device),
         None if lse is None else _arg(lse, "lse", (n_seqs, q_heads), _F32, device),
         _arg(workspace, "workspace", workspace.shape, workspace.dtype, device), workspace.nbytes, _raw_stream(stream, device))
     if rc:
