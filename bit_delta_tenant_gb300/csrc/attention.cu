@@ -26,9 +26,9 @@
 // for 8 KB of K and V, 14 us of the 88 below).
 //
 // Rounding.  P enters as a 16-bit part and its 16-bit remainder: bf16 (2^-16 of a
-// weight) beside a bf16 V, fp16 (2^-21, or 2^-25 of the largest) beside an e4m3 V,
+// weight) beside a bf16 V, fp16 (2^-21, or 2^-40 of the largest) beside an e4m3 V,
 // which fp16 holds exactly.  An e4m3 V's scale is folded into the
-// weight before the maximum is taken, so that no weight exceeds 1; its K is
+// weight before the maximum is taken, so that no weight exceeds 2^15; its K is
 // multiplied as it stands, by q in two e4m3 parts: q is scaled by a power of two
 // so that its row's largest value lies in [128, 256), where the parts hold a bf16
 // value's 8 bits exactly (values far below the largest to 2^-21 of it); with at most 8
@@ -206,6 +206,11 @@ __device__ __forceinline__ int64_t warp_scan(int64_t v) {  // inclusive
     }
     return v;
 }
+
+// Weights are kept times 2^kLift: beside an e4m3 V they are fp16, whose range below 1 ends at 2^-24, and a token whose V
+// has a small scale weighs little beside one with a large scale, yet is all there is in columns where that one is 0.
+template <bool kE4m3>
+constexpr float kLift = kE4m3 ? 15.f : 0.f;  // the largest is 2^15
 
 template <bool kE4m3>
 constexpr int kTileOf = kE4m3 ? 32 : 16;  // keys of a warp's step: 8 KB of K and V at head_dim 128 in either type
@@ -495,8 +500,8 @@ __device__ __forceinline__ void stream(const AttnArgs &a, uint8_t *smem, const S
                             top = fmaxf(top, kE4m3 ? s[i][2 * h + c] + vexp[i][c] : s[i][2 * h + c]);
                     top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
                     top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
-                    const float base = top == -INFINITY ? 0.f : top;  // nothing yet: all weights 0
-                    fix[h] = ex2(m[h] - base);
+                    const float now = top == -INFINITY ? 0.f : top, base = now - kLift<kE4m3>;  // nothing yet: all weights 0
+                    fix[h] = ex2(m[h] - now);
                     moved |= fix[h] != 1.f;
                     m[h] = top;
                     float sum = 0.f;
@@ -624,7 +629,7 @@ __device__ __forceinline__ void stream(const AttnArgs &a, uint8_t *smem, const S
             const float inv = sum == 0.f ? 0.f : 1.f / sum;
             *reinterpret_cast<uint2 *>(a.out + ((head0 + r) * kDim + d) * 2) =
                 make_uint2(pack_bf16x2(x.x * inv, x.y * inv), pack_bf16x2(x.z * inv, x.w * inv));
-            if (a.lse && d == 0) a.lse[head0 + r] = (top + log2f(sum)) * 0.693147180559945f;
+            if (a.lse && d == 0) a.lse[head0 + r] = (top - kLift<kE4m3> + log2f(sum)) * 0.693147180559945f;
         };
         if (alone) {
             __syncwarp();

@@ -527,9 +527,10 @@ int32_t bd_kv_read(const bd_kv_cache *cache, const int32_t *page_table, int32_t 
  * not read into the result whatever they hold, and pages wholly outside the
  * window are not touched.  Scores, softmax statistics and the output's sums
  * are fp32; out is rounded once to bf16.  The softmax weights enter the
- * tensor cores as two 16-bit parts each (2^-16 of a weight or better; an
- * infinite V that a query sees may therefore give NaN), q over an 8-bit cache to
- * 2^-21 of its head's largest value.
+ * tensor cores as two 16-bit parts each (2^-16 of a weight or better, over an
+ * 8-bit cache, where V's scale is part of the weight, or 2^-40 of the head's
+ * largest; an infinite V that a query sees may therefore give NaN), q over an
+ * 8-bit cache to 2^-21 of its head's largest value.
  *
  *   q           bf16 [n_seqs, q_heads, head_dim]        (read)
  *   page_table  int32 [n_seqs, max_pages]               (read)
