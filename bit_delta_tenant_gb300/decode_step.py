@@ -137,9 +137,14 @@ class Tenants:
     def prefill(self, i: int, prompt, piece: int = 512) -> None:
         """Cache all of a prompt of sequence i but its last token, which the next step takes."""
         s, dev = self.shape, self.tokens.device
-        prompt = torch.as_tensor(prompt, dtype=torch.int32, device=dev)
-        if not 0 < prompt.numel() <= self.max_tokens:
+        prompt = torch.as_tensor(prompt)
+        if not 0 <= i < self.m:
+            raise ValueError(f"a sequence is one of 0 to {self.m - 1}")
+        if prompt.dim() != 1 or not 0 < prompt.numel() <= self.max_tokens:
             raise ValueError(f"a prompt has 1 to {self.max_tokens} tokens")
+        if int(prompt.min()) < 0 or int(prompt.max()) >= s.vocab:  # rows of the embedding, unchecked from here on
+            raise ValueError(f"a token is one of 0 to {s.vocab - 1}")
+        prompt = prompt.to(dev, torch.int32)
         table = self.page_table[i:i + 1]
 
         for start in range(0, prompt.numel() - 1, piece):
