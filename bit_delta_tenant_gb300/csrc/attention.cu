@@ -289,7 +289,8 @@ __device__ __forceinline__ void stream(const AttnArgs &a, uint8_t *smem, const S
         auto fetch_page = [&](int j0) {
             const uint32_t p = piece_of(j0);
             const bool on = j0 + lane / kSub < n && static_cast<int>(p * 16) < sp.len && static_cast<int>(p * 16 + 16) > sp.start;
-            return on ? table[page_index(p)] : 0;
+            const bool there = on && in_bounds(b < a.n_seqs && page_index(p) < static_cast<uint32_t>(a.max_pages), a.status);
+            return there ? table[page_index(p)] : 0;
         };
         // its place in the pool, in units of 16 keys
         auto place_of = [&](int j0, int32_t page) {
@@ -308,7 +309,8 @@ __device__ __forceinline__ void stream(const AttnArgs &a, uint8_t *smem, const S
         float rscale[2] = {a.scale_log2, a.scale_log2};
 #pragma unroll
         for (int half = 0; half < kHalves; ++half) {
-            const bool on = g + half * 8 < rows;
+            const bool on = g + half * 8 < rows &&
+                            in_bounds(head0 + g + half * 8 < static_cast<int64_t>(a.n_seqs) * a.q_heads, a.status);
             const uint8_t *src = a.q + (head0 + g + half * 8) * (kDim * 2);
             if constexpr (!kE4m3) {
 #pragma unroll
@@ -375,7 +377,8 @@ __device__ __forceinline__ void stream(const AttnArgs &a, uint8_t *smem, const S
 #pragma unroll
             for (int u = 0; u < kSub; ++u) {
                 uint32_t place = __shfl_sync(0xFFFFFFFFu, places, j % kBatch * kSub + u);
-                const bool good = place != kNoPage;
+                const bool good = place != kNoPage &&
+                                  in_bounds(place < static_cast<uint64_t>(a.n_pages) * a.kv_heads * a.page_tiles, a.status);
                 if (!good) bad |= 1u << (slot * kSub + u), place = 0;
                 const uint8_t *ks = a.ck + static_cast<int64_t>(place) * kPiece + lane * 16;
                 const uint8_t *vs = a.cv + static_cast<int64_t>(place) * kPiece + lane * 16;
@@ -626,6 +629,7 @@ __device__ __forceinline__ void stream(const AttnArgs &a, uint8_t *smem, const S
             }
         }
         auto finish = [&](int r, int d, float4 x, float top, float sum) {  // four columns of a row, and once its lse
+            if (!in_bounds(head0 + r < static_cast<int64_t>(a.n_seqs) * a.q_heads, a.status)) return;
             const float inv = sum == 0.f ? 0.f : 1.f / sum;
             *reinterpret_cast<uint2 *>(a.out + ((head0 + r) * kDim + d) * 2) =
                 make_uint2(pack_bf16x2(x.x * inv, x.y * inv), pack_bf16x2(x.z * inv, x.w * inv));
@@ -643,7 +647,12 @@ __device__ __forceinline__ void stream(const AttnArgs &a, uint8_t *smem, const S
         }
         __syncthreads();
         const bool whole = blk == 0 && n == sp.blocks;
+        [[maybe_unused]] auto in_slots = [&](const float *slot) {  // one whole slot of the workspace
+            const int64_t at = slot - a.parts;
+            return in_bounds(at >= 0 && at <= (a.level_counters - int64_t{1}) * kSlotFloats, a.status);
+        };
         auto store_part = [&](float *slot, int r, int d, float4 x, float top, float sum) {
+            if (!in_slots(slot)) return;
             *reinterpret_cast<float4 *>(slot + r * kDim + d) = x;
             if (d == 0) slot[kRows * 128 + r] = top, slot[kRows * 128 + kRows + r] = sum;
         };
@@ -680,17 +689,21 @@ __device__ __forceinline__ void stream(const AttnArgs &a, uint8_t *smem, const S
             const int lead = index / kFan * kFan, count = min(kFan, left - lead);
             __syncthreads();  // this CTA's part is written; the fence below publishes it for all threads
             if (tid == 0) {
-                int32_t *ctr = a.counters + level * a.level_counters + id_of(lead * stride);
-                int before;
-                asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;" : "=r"(before) : "l"(ctr) : "memory");
-                s_last = before == count - 1;
-                if (s_last) *ctr = 0;  // ready for the next call
+                const int id = id_of(lead * stride);
+                s_last = 0;
+                if (in_bounds(level < kLevels && id >= 0 && id < a.level_counters, a.status)) {
+                    int32_t *ctr = a.counters + level * a.level_counters + id;
+                    int before;
+                    asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;" : "=r"(before) : "l"(ctr) : "memory");
+                    s_last = before == count - 1;
+                    if (s_last) *ctr = 0;  // ready for the next call
+                }
             }
             __syncthreads();
             if (!s_last) break;
             if (tid < kFan * kRows) {
                 const int q = tid / kRows, r = tid % kRows;
-                const bool on = q < count && r < rows;
+                const bool on = q < count && r < rows && in_slots(slot_of((lead + q) * stride));
                 const float *slot = slot_of((lead + (on ? q : 0)) * stride) + kRows * 128;
                 s_jm[q][r] = on ? __ldcg(slot + r) : -INFINITY;
                 s_jl[q][r] = on ? __ldcg(slot + kRows + r) : 0.f;
@@ -704,7 +717,7 @@ __device__ __forceinline__ void stream(const AttnArgs &a, uint8_t *smem, const S
                     const int i = tid + (e + w) * kThreads;
 #pragma unroll
                     for (int q = 0; q < kFan; ++q)
-                        if (e + w < kEach && q < count && i < rows * (kDim / 4))
+                        if (e + w < kEach && q < count && i < rows * (kDim / 4) && in_slots(slot_of((lead + q) * stride)))
                             y[w][q] = __ldcg(reinterpret_cast<const float4 *>(slot_of((lead + q) * stride)) + i);
                 }
                 __syncthreads();

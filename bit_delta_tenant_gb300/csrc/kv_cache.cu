@@ -70,6 +70,7 @@ __global__ void __launch_bounds__(kAppendThreads, 5) kv_append_kernel(const Appe
             in[u][0] = in[u][1] = make_uint4(0, 0, 0, 0);
             if (r >= rows) continue;
             const bool is_v = r >= q_rows + a.kv_heads;
+            if (!in_bounds(r >= 0 && r < q_rows + 2 * a.kv_heads, a.status)) continue;
             const uint8_t *src = r < q_rows ? a.q + (t * a.q_heads + r) * (kDim * 2)
                                             : (is_v ? a.v : a.k) + (t * a.kv_heads + r - q_rows - (is_v ? a.kv_heads : 0)) * (kDim * 2);
             in[u][0] = ldg_plain(src + lane * 16);
@@ -118,7 +119,7 @@ __global__ void __launch_bounds__(kAppendThreads, 5) kv_append_kernel(const Appe
                     x[j] = low;
                 }
             }
-            if (is_q) {
+            if (is_q && in_bounds(r < a.q_heads, a.status)) {
                 uint8_t *dst = a.q_out + (t * a.q_heads + r) * (kDim * 2) + lane * 16;
                 *reinterpret_cast<uint4 *>(dst) = pack8(x);
                 *reinterpret_cast<uint4 *>(dst + kDim) = pack8(y);
@@ -136,6 +137,7 @@ __global__ void __launch_bounds__(kAppendThreads, 5) kv_append_kernel(const Appe
             }
             if (is_q || r >= rows) continue;
             const int64_t at = slot_row + static_cast<int64_t>(r - q_rows - (is_v ? a.kv_heads : 0)) * a.page_size;
+            if (!in_bounds(at >= 0 && at < a.n_pages * a.kv_heads * a.page_size, a.status)) continue;
             uint8_t *dst = is_v ? a.cv : a.ck;
             if constexpr (!kE4m3) {
                 *reinterpret_cast<uint4 *>(dst + at * (kDim * 2) + lane * 16) = pack8(x);
@@ -227,14 +229,14 @@ __global__ void __launch_bounds__(kReadThreads) kv_read_kernel(const ReadArgs a)
             for (int w = 0; w < 2; ++w) {
                 v[u][w] = Raw{};
                 s[u][w] = 0.f;
-                if (f < 0) continue;
+                if (f < 0 || !in_bounds(row < a.n_pages * a.kv_heads * a.page_size, a.status)) continue;
                 v[u][w] = __ldcs(reinterpret_cast<const Raw *>(w ? a.cv : a.ck) + row * kChunk + rest % kChunk);
                 if constexpr (kE4m3) s[u][w] = __uint_as_float(static_cast<uint32_t>((w ? a.cv_scale : a.ck_scale)[row]) << 23);
             }
         }
 #pragma unroll
         for (int u = 0; u < kReadAtOnce; ++u) {
-            if (to[u] < 0) continue;
+            if (to[u] < 0 || !in_bounds(to[u] < a.total * a.per_token, a.status)) continue;
 #pragma unroll
             for (int w = 0; w < 2; ++w) {
                 uint4 *d = reinterpret_cast<uint4 *>(w ? a.v_out : a.k_out) + to[u];

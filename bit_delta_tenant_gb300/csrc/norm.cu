@@ -68,8 +68,9 @@ __global__ void __launch_bounds__(kThreads, (kChunks == 1 ? 2048 : kChunks == 2 
         if (id >= a.n_weights) id = -1;
         if (id < 0 && lane == 0) flag_status(a.status, kDevBadVariant);
     }
-    const int chunks = id >= 0 ? a.n / 8 : 0;  // a row beyond the last or with a bad id: nothing is read or written
+    const int chunks = id >= 0 && in_bounds(row < a.m && id < a.n_weights, a.status) ? a.n / 8 : 0;  // a row beyond the last or with a bad id: nothing is read or written
     const int64_t base = row * a.n * 2;
+    [[maybe_unused]] auto in_rows = [&](int c) { return in_bounds(row * a.n + c * 8 + 8 <= a.m * a.n, a.status); };
     float h[kChunks][8];
     uint4 w[kChunks];
     float ss = 0.f;
@@ -90,7 +91,7 @@ __global__ void __launch_bounds__(kThreads, (kChunks == 1 ? 2048 : kChunks == 2 
             if (a.residual) h[u][j] += r[j];
             ss = fmaf(h[u][j], h[u][j], ss);
         }
-        if (c < chunks && a.residual_out) *reinterpret_cast<uint4 *>(a.residual_out + base + c * 16) = pack8(h[u]);
+        if (c < chunks && a.residual_out && in_rows(c)) *reinterpret_cast<uint4 *>(a.residual_out + base + c * 16) = pack8(h[u]);
     }
     // Divided by n before the reduction, and where a thread's own squares pass fp32 (an element beyond 1.8e19) each of
     // them before it is added, so that only a mean beyond fp32 overflows.  Not always so: squares of less than n 2^-126,
@@ -114,7 +115,7 @@ __global__ void __launch_bounds__(kThreads, (kChunks == 1 ? 2048 : kChunks == 2 
 #pragma unroll
         for (int j = 0; j < 8; ++j) h[u][j] = kE4m3 ? h[u][j] * g[j] : h[u][j] * rstd * g[j];
         if constexpr (!kE4m3) {
-            if (c < chunks) *reinterpret_cast<uint4 *>(a.y + base + c * 16) = pack8(h[u]);
+            if (c < chunks && in_rows(c)) *reinterpret_cast<uint4 *>(a.y + base + c * 16) = pack8(h[u]);
         } else if (a.row_scale) {
 #pragma unroll
             for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(h[u][j]));
@@ -138,7 +139,7 @@ __global__ void __launch_bounds__(kThreads, (kChunks == 1 ? 2048 : kChunks == 2 
             const bool some = top >= kTiny;
             const float s = some ? __fdiv_rn(top * rstd, 448.f) : 1.f;
             const float inv = some ? __fdiv_rn(448.f, top) : rstd;
-            if (c >= chunks) continue;
+            if (c >= chunks || !in_rows(c)) continue;
             uint32_t q[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j)

@@ -54,10 +54,11 @@ __device__ __forceinline__ uint32_t rebuild_pair(uint32_t w, uint32_t byte, int 
 __global__ void __launch_bounds__(kThreads) reconstruct_kernel(const uint4 *__restrict__ wb,
                                                               const uint8_t *__restrict__ bits,
                                                               const float *__restrict__ alpha, int32_t mode,
-                                                              int64_t row_chunks, int64_t total, int64_t per_block,
-                                                              uint4 *__restrict__ out) {
+                                                              int64_t row_chunks, int64_t rows, int64_t per_block,
+                                                              uint4 *__restrict__ out, unsigned *status) {
     pdl_trigger_and_wait();
     const int64_t lo = static_cast<int64_t>(blockIdx.x) * per_block;
+    const int64_t total = rows * row_chunks;
     const int64_t hi = min(lo + per_block, total);
     int64_t c = lo + threadIdx.x;
     if (c >= hi) return;
@@ -70,7 +71,7 @@ __global__ void __launch_bounds__(kThreads) reconstruct_kernel(const uint4 *__re
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) {
             const int64_t cu = c + u * kThreads;
-            if (cu < hi) {
+            if (cu < hi && in_bounds(cu < total, status)) {
                 w[u] = ldg_nc(wb + cu);
                 b[u] = bits[cu];
             }
@@ -84,6 +85,7 @@ __global__ void __launch_bounds__(kThreads) reconstruct_kernel(const uint4 *__re
                         ++row;
                         row_end += row_chunks;
                     }
+                    if (!in_bounds(row < rows, status)) continue;
                     a = alpha[row];
                 }
                 uint4 r;
@@ -91,7 +93,7 @@ __global__ void __launch_bounds__(kThreads) reconstruct_kernel(const uint4 *__re
                 r.y = rebuild_pair(w[u].y, b[u], 1, a);
                 r.z = rebuild_pair(w[u].z, b[u], 2, a);
                 r.w = rebuild_pair(w[u].w, b[u], 3, a);
-                stg_cs(out + cu, r);
+                if (in_bounds(cu < total, status)) stg_cs(out + cu, r);
             }
         }
     }
@@ -121,7 +123,7 @@ cudaError_t launch_reconstruct(const void *w_base, const uint8_t *bits, const fl
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, reconstruct_kernel, static_cast<const uint4 *>(w_base), bits, alpha, alpha_mode,
-                              row_chunks, total, per_block, static_cast<uint4 *>(w_eff));
+                              row_chunks, n_out, per_block, static_cast<uint4 *>(w_eff), ctx.status);
 }
 
 }  // namespace bd

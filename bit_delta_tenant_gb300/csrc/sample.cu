@@ -69,6 +69,7 @@ struct SampleArgs {
     const int32_t *top_k;
     int32_t *ids;
     float *logprob;
+    unsigned *status;
     int64_t m;
     int32_t vocab, slice_units;  // 16-byte units of logits in a CTA's slice
     int32_t sorted;              // long rows are taken first
@@ -226,7 +227,12 @@ struct Sampler {
 
     // ---- the slice --------------------------------------------------------------------
     static __device__ __forceinline__ float clean(float x) { return fmaxf(x, -INFINITY); }  // NaN to -inf
+    __device__ __forceinline__ bool in_array(int64_t first, int n) const {  // elements of the logits, and of the noise
+        return in_bounds(first >= 0 && first + n <= a.m * a.vocab, a.status);
+    }
+    __device__ __forceinline__ float noise_of(int64_t e) const { return in_array(e, 1) ? a.noise[e] : 0.f; }
     __device__ __forceinline__ float logit(int64_t e) const {
+        if (!in_array(e, 1)) return -INFINITY;
         if constexpr (kF32) return clean(__ldg(reinterpret_cast<const float *>(a.logits) + e));
         return clean(__uint_as_float(static_cast<uint32_t>(__ldg(reinterpret_cast<const uint16_t *>(a.logits) + e)) << 16));
     }
@@ -248,6 +254,7 @@ struct Sampler {
     }
     __device__ __forceinline__ bool inside(int i) const { return i >= whole_from && i < whole_to; }
     __device__ __forceinline__ uint4 fetch(int i) const {
+        if (!in_array((u0 + i) * kPer, kPer)) return make_uint4(0, 0, 0, 0);
         uint4 v;
         asm volatile("ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];"
                      : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
@@ -307,6 +314,7 @@ struct Sampler {
     }
     __device__ __forceinline__ void fetch_noise(int i, float (&noise)[kPer]) const {
         const float *g = a.noise + (e0 + base) + static_cast<int64_t>(i) * kPer;
+        if (!in_array(g - a.noise, kPer)) return;
 #pragma unroll
         for (int j = 0; j < kPer; j += 4)
             asm volatile("ld.global.nc.v4.f32 {%0, %1, %2, %3}, [%4];"
@@ -321,7 +329,7 @@ struct Sampler {
         } else {
 #pragma unroll
             for (int j = 0; j < kPer; ++j)
-                noise[j] = x[j] > -INFINITY ? a.noise[e0 + base + static_cast<int64_t>(i) * kPer + j] : 0.f;
+                noise[j] = x[j] > -INFINITY ? noise_of(e0 + base + static_cast<int64_t>(i) * kPer + j) : 0.f;
         }
     }
     // x and noise of one unit
@@ -625,7 +633,7 @@ __device__ void Sampler<kF32>::run(int64_t r) {
     // noise of which most will be read later is on its way into L2 meanwhile
     if (tid == 0 && !greedy && k == 0 && p < 1.f) {
         const int64_t n = min(static_cast<int64_t>(units), a.m * a.vocab / kPer - u0);
-        if (n > 0)
+        if (n > 0 && in_bounds(u0 >= 0 && (u0 + n) * kPer <= a.m * a.vocab, a.status))
             asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(a.noise + u0 * kPer), "r"(static_cast<uint32_t>(n * kPer * 4))
                          : "memory");
     }
@@ -718,7 +726,7 @@ __device__ void Sampler<kF32>::run(int64_t r) {
     row.top = s.ranks[0].top;
     for (int c = 1; c < size; ++c) row.top = fmaxf(row.top, s.ranks[c].top);
     if (row.top == -INFINITY) {  // nothing may be drawn; the whole cluster leaves
-        if (rank == 0 && tid == 0) {
+        if (rank == 0 && tid == 0 && in_bounds(r >= 0 && r < a.m, a.status)) {
             a.ids[r] = -1;
             if (a.logprob) a.logprob[r] = -INFINITY;
         }
@@ -769,6 +777,7 @@ __device__ void Sampler<kF32>::run(int64_t r) {
     };
     auto answer = [&] {  // by one thread of the cluster
         const int id = static_cast<int>(0xFFFFFFFFu - static_cast<uint32_t>(best));
+        if (!in_bounds(r >= 0 && r < a.m && id >= 0 && id < a.vocab, a.status)) return;
         a.ids[r] = id;
         if (a.logprob) a.logprob[r] = -row.t_of(logit(e0 + id)) - logf(weight);
     };
@@ -839,7 +848,7 @@ __device__ void Sampler<kF32>::run(int64_t r) {
             for (int j = 0; j < kPer; ++j) {
                 if (x[j] == -INFINITY) continue;
                 const float t = row.t_of(x[j]);
-                if (low == 0.f || expf(-t) >= low) offer(t, a.noise[e0 + base + i * kPer + j], base + i * kPer + j);
+                if (low == 0.f || expf(-t) >= low) offer(t, noise_of(e0 + base + i * kPer + j), base + i * kPer + j);
             }
         });
         answer_of_all();
@@ -911,7 +920,7 @@ __device__ void Sampler<kF32>::run(int64_t r) {
                 if (o > s.threshold) continue;
                 const int token = static_cast<int>(o & ((1u << kIndexBits) - 1));
                 const float t = row.t_of(value_of(~static_cast<uint32_t>(o >> kIndexBits)));
-                if (low == 0.f || expf(-t) >= low) offer(t, a.noise[e0 + token], token);
+                if (low == 0.f || expf(-t) >= low) offer(t, noise_of(e0 + token), token);
             }
             best = fold_max(best);
             if (tid == 0) answer();
@@ -1064,7 +1073,7 @@ __device__ void Sampler<kF32>::run(int64_t r) {
                     const float t = row.t_of(x[j]);
                     const int b = bins.bin(t), token = base + i * kPer + j;
                     if (b == d) keep(x[j], token);
-                    else if (b < d && (low == 0.f || expf(-t) >= low)) offer(t, a.noise[e0 + token], token);
+                    else if (b < d && (low == 0.f || expf(-t) >= low)) offer(t, noise_of(e0 + token), token);
                 }
             }
         });
@@ -1082,7 +1091,7 @@ __device__ void Sampler<kF32>::run(int64_t r) {
     }
     each_token([&](float v, int i) {
         const float t = row.t_of(v);
-        if (order_of(v, i) <= threshold && (low == 0.f || expf(-t) >= low)) offer(t, a.noise[e0 + i], i);
+        if (order_of(v, i) <= threshold && (low == 0.f || expf(-t) >= low)) offer(t, noise_of(e0 + i), i);
     });
     __syncthreads();
     answer_of_all();
@@ -1148,6 +1157,7 @@ cudaError_t launch_sample(const void *logits, int32_t logits_type, int64_t m, in
     a.noise = noise;
     a.ids = ids;
     a.logprob = logprob;
+    a.status = ctx.status;
     a.m = m;
     a.vocab = static_cast<int32_t>(vocab);
     const bool f32 = logits_type == BD_LOGITS_F32;
