@@ -457,12 +457,12 @@ def _refuse(t: torch.Tensor, name: str, shape, dtype, device) -> None:
     raise ValueError(f"{name}: tensors passed to libbitdelta must be contiguous")
 
 
-def _device(t: torch.Tensor, name: str) -> int:
-    """The CUDA device that holds t, on which all other tensors of its call have to be."""
+def _first(t: torch.Tensor, name: str, dtype) -> tuple[int, int]:
+    """Address of a contiguous tensor of the given type, and the CUDA device on which all other tensors of its call have to be."""
     device = t.get_device()
-    if device < 0:
-        raise ValueError(f"{name}: {_NOT_ON_DEVICE}")
-    return device
+    if device < 0 or t.dtype is not dtype or not t.is_contiguous():
+        _refuse(t, name, t.shape, dtype, device)
+    return t.data_ptr(), device
 
 
 def _arg(t: torch.Tensor | None, name: str, shape, dtype, device: int) -> int | None:
@@ -492,7 +492,7 @@ def bd_rmsnorm(x: torch.Tensor, weight: torch.Tensor, eps: float, y: torch.Tenso
     `residual_out` receives bf16(x + residual) and may be `residual` itself.  A bf16 `y` is
     rounded once; a float8_e4m3fn `y` comes with `y_scale`, fp32 [m, n / 128] (a scale per
     128 columns) or [m, 1] (one per row)."""
-    device, shape = _device(x, "x"), x.shape
+    (xp, device), shape = _first(x, "x", _BF16), x.shape
     m, n = shape
     n_weights, w_shape = (weight.shape[0], (weight.shape[0], n)) if weight.dim() == 2 else (1, (n,))
     y_type, scale_cols, scale = BD_Y_BF16, 0, None
@@ -505,9 +505,8 @@ def bd_rmsnorm(x: torch.Tensor, weight: torch.Tensor, eps: float, y: torch.Tenso
     elif y_scale is not None:
         raise ValueError("y_scale: only an 8-bit y has scales")
     rc = (_lib or load_library()).bd_rmsnorm(
-        _arg(x, "x", shape, _BF16, device), None if residual is None else _arg(residual, "residual", shape, _BF16, device),
-        _arg(weight, "weight", w_shape, _BF16, device),
-        None if weight_ids is None else _arg(weight_ids, "weight_ids", (m,), _I32, device),
+        xp, None if residual is None else _arg(residual, "residual", shape, _BF16, device),
+        _arg(weight, "weight", w_shape, _BF16, device), None if weight_ids is None else _arg(weight_ids, "weight_ids", (m,), _I32, device),
         n_weights, m, n, eps, _arg(y, "y", shape, _E4M3 if y_type else _BF16, device), y_type, scale, scale_cols,
         None if residual_out is None else _arg(residual_out, "residual_out", shape, _BF16, device), _raw_stream(stream, device))
     if rc:
@@ -532,9 +531,10 @@ class KVCache:
             raise ValueError("k_scale and v_scale come with an 8-bit cache, and only with one")
         n_pages, self.kv_heads, self.page_size, self.head_dim = k.shape
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
-        device = self.device = _device(k, "k")
         d = self.desc = KVCacheDesc()
-        d.k, d.v = _arg(k, "k", k.shape, k.dtype, device), _arg(v, "v", k.shape, k.dtype, device)
+        d.k, device = _first(k, "k", k.dtype)
+        self.device = device
+        d.v = _arg(v, "v", k.shape, k.dtype, device)
         d.k_scale = _arg(k_scale, "k_scale", k.shape[:3], _U8, device)
         d.v_scale = _arg(v_scale, "v_scale", k.shape[:3], _U8, device)
         d.n_pages, d.kv_heads, d.head_dim, d.page_size = n_pages, self.kv_heads, self.head_dim, self.page_size
@@ -624,12 +624,12 @@ def bd_sample(logits: torch.Tensor, noise: torch.Tensor, ids: torch.Tensor, temp
 
     `temperature`, `top_k` (int32), `top_p` and `min_p` hold one setting per row; None leaves the
     filter off (temperature 1).  `logprob` receives the drawn token's log probability before the filters."""
-    device, shape = _device(logits, "logits"), logits.shape
+    half = logits.dtype is _BF16
+    (lp, device), shape = _first(logits, "logits", _BF16 if half else _F32), logits.shape
     m, vocab = shape
     row = (m,)
-    half = logits.dtype is _BF16
     rc = (_lib or load_library()).bd_sample(
-        _arg(logits, "logits", shape, _BF16 if half else _F32, device), BD_LOGITS_BF16 if half else BD_LOGITS_F32, m, vocab,
+        lp, BD_LOGITS_BF16 if half else BD_LOGITS_F32, m, vocab,
         None if temperature is None else _arg(temperature, "temperature", row, _F32, device),
         None if top_k is None else _arg(top_k, "top_k", row, _I32, device),
         None if top_p is None else _arg(top_p, "top_p", row, _F32, device),
