@@ -174,7 +174,7 @@ struct ReadArgs {
     unsigned *status;
     int64_t n_pages, total;
     int32_t kv_heads, page_size, n_seqs, max_pages, tokens;  // tokens: output rows of one CTA
-    uint32_t per_token, magic;  // 16-byte pieces of a token's row in k_out, and ceil(2^32 / that)
+    uint32_t per_token, magic;  // 16-byte pieces of a token's row in k_out (8 at least), and ceil(2^32 / that)
 };
 
 // Two e4m3 values times 2^(e - 127), as a bf16 pair (exact down to bf16's subnormals).
@@ -220,7 +220,7 @@ __global__ void __launch_bounds__(kReadThreads) kv_read_kernel(const ReadArgs a)
             const uint32_t i = i0 + u * kReadThreads;
             to[u] = -1;
             if (i >= items) continue;
-            const uint32_t tok = a.per_token == 1 ? i : __umulhi(i, a.magic), rest = i - tok * a.per_token;
+            const uint32_t tok = __umulhi(i, a.magic), rest = i - tok * a.per_token;
             const int64_t f = first[tok];
             if (f == -1) continue;
             to[u] = (t0 + tok) * a.per_token + rest;
