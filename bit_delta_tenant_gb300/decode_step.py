@@ -226,8 +226,8 @@ def main() -> None:
     start, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
     text, ms = [], 0.0
     for _ in range(a.steps):
+        start.record()  # the noise of a step's draws is part of the step
         t.draw_noise(g)
-        start.record()
         graph.replay()
         end.record()
         text.append(t.tokens.tolist())
