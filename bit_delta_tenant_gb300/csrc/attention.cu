@@ -35,9 +35,12 @@
 // heads the second part takes rows 8..15 of the same product.  Accumulation is
 // fp32 in every product (measured for the e4m3 one: 2^-25 of sum |q k|).
 //
-// Measured (head_dim 128): 130001 tokens, 64 and 8 heads, bf16 88 us (6.0 TB/s: SMs' streams end between 64 and
-// 82 us, then the joins); 64 sequences of up to 8191 tokens, 32 and 8 heads, 8 bits 33 us (3.7 TB/s: one to two heads
-// to a CTA, whose setup and joins are half of its time); 777 tokens, bf16 8.4 us, a chain of latencies.
+// Measured (head_dim 128): 130001 tokens, 64 and 8 heads, bf16 89 us (6.0 TB/s: SMs' streams end between 64 and
+// 82 us, then the joins), 8 bits 56 (4.8 TB/s); sequences of up to 8191 tokens, lengths spread in their logarithm, 32
+// and 8 heads, 8 bits: 64 of them 33 us (3.7 TB/s), 200 85 (4.5 TB/s), one to six heads to a CTA that drains its ring
+// at each head's end before the next head's first copy; 200 of them in bf16 122 (6.1 TB/s); 777 tokens, bf16 8.2 us,
+// a chain of latencies.  More than 16 query heads to a KV head read it once per 16: 64 sequences of up to 4000 tokens,
+// one KV head, bf16, 16 query heads 13.1 us, 48 17.2.
 #include <cuda_fp8.h>
 
 #include <algorithm>

@@ -28,8 +28,9 @@
 //     histogram) are sent to every CTA and ordered exactly.  A bin
 //     with too many tokens is split again, by the remaining bits of t, then by the bits of
 //     (x, index), which differ for any two.
-// Measured, rows of 128256 fp32 logits: one row with top-k and top-p (bf16) 12.9 us, a chain of latencies; 256 rows
-// unfiltered 67 us (3.9 TB/s), top-k 64, top-p 139, min-p 41, greedy 37, of every kind 76.
+// Measured, rows of 128256 fp32 logits, each call on other logits than the one before: one row with top-k and top-p
+// (bf16) 12.8 us, a chain of latencies; 256 rows unfiltered 65 us (4.0 TB/s), top-k 65, top-p 140, min-p 41, greedy 37,
+// of every kind 90 (77 on the same logits, of which L2 keeps a part).
 //
 // Sums of weights do not depend on the order of atomics: they are whole numbers.  Within a
 // bin of width d, w = exp(-start) w' with w' in [1 - d, 1], and a bin sums
@@ -577,7 +578,7 @@ struct Sampler {
 };
 
 // The row that the cluster of this number takes: rows with a share p alone first, as they take two to three times as
-// long as others and would otherwise end last (256 rows of every kind: 87 us in their own order, 77 us so).
+// long as others and would otherwise end last (256 rows of every kind, the same logits: 87 us in their own order, 77 so).
 template <bool kF32>
 __device__ int64_t Sampler<kF32>::row_of(int64_t turn) {
     if (!a.sorted) return turn;
@@ -630,7 +631,8 @@ __device__ void Sampler<kF32>::run(int64_t r) {
     low = low > 0.f ? fminf(low, 1.f) : 0.f;
     const bool filtered = !greedy && (k > 0 || p < 1.f);
     const bool open = !greedy && !filtered && low == 0.f;
-    // noise of which most will be read later is on its way into L2 meanwhile
+    // the noise, which top-p's second pass reads beside the logits whether or not a token is kept, is on its way into L2
+    // meanwhile
     if (tid == 0 && !greedy && k == 0 && p < 1.f) {
         const int64_t n = min(static_cast<int64_t>(units), a.m * a.vocab / kPer - u0);
         if (n > 0 && in_bounds(u0 >= 0 && (u0 + n) * kPer <= a.m * a.vocab, a.status))
@@ -1111,7 +1113,8 @@ cudaError_t launch_typed(SampleArgs &a, const DevCtx &ctx, cudaStream_t stream) 
     constexpr int kPer = kF32 ? 4 : 8;
     // The largest cluster of which the resident CTAs hold all rows at once, or twice that number where rows may take
     // top-p, which takes longer; and slices of 2048 logits at least.  256 rows of 128256 fp32 logits in clusters of 1, 2, 4:
-    // every kind 113, 75, 91 us, but unfiltered 58, 67, 80, top-k 65, 68, 89, min-p 36, 41, 53, greedy 31, 37, 47.
+    // every kind 113, 75, 91 us (the same logits), but unfiltered 58, 67, 80, top-k 65, 68, 89, min-p 36, 41, 53, greedy
+    // 31, 37, 47.  Whether a top_p is given decides, not its values, which the host has not: all ones take as long.
     const int64_t ctas = (a.top_p ? 2 : 1) * kCtasPerSm * ctx.num_sms;
     int size = 1;
     while (size < kMaxCluster && a.m * size * 2 <= ctas && a.vocab > size * 4096) size *= 2;

@@ -583,8 +583,8 @@ int32_t bd_attention_decode(const bd_kv_cache *cache, const void *q, int32_t q_h
  * Results do not depend on timing.
  *
  *   logits       bf16 or float [m, vocab]   (read)
- *   noise        float [m, vocab]           (read where it can decide: at kept
- *                tokens)
+ *   noise        float [m, vocab]           (read; only that of kept tokens
+ *                has an effect)
  *   temperature  float [m] or NULL (1)      (read, device)
  *   top_k        int32 [m] or NULL (off)
  *   top_p, min_p float [m] or NULL (off)
