@@ -35,6 +35,13 @@ struct NormArgs {
     float eps, inv_n;
 };
 
+// A streaming load that is coherent with this kernel's writes: residual_out may be x.
+__device__ __forceinline__ uint4 ldg_once(const uint8_t *p) {
+    uint4 v;
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+    return v;
+}
+
 // Sum or maximum over the kWarps warps that share a row, the same value in every thread of theirs.
 template <int kWarps, bool kMax>
 __device__ __forceinline__ float row_reduce(float v, float *smem) {
@@ -79,7 +86,7 @@ __global__ void __launch_bounds__(kThreads, (kChunks == 1 ? 2048 : kChunks == 2 
         const int c = lane + u * kPerRow;
         uint4 xv = make_uint4(0, 0, 0, 0), rv = make_uint4(0, 0, 0, 0);
         if (c < chunks) {
-            xv = ldg_stream(a.x + base + c * 16);
+            xv = ldg_once(a.x + base + c * 16);
             if (a.residual) rv = *reinterpret_cast<const uint4 *>(a.residual + base + c * 16);
             if (!kLate) w[u] = ldg_keep(a.weight + static_cast<int64_t>(id) * a.n * 2 + c * 16);
         }

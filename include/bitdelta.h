@@ -535,7 +535,7 @@ int32_t bd_kv_read(const bd_kv_cache *cache, const int32_t *page_table, int32_t 
  *   q           bf16 [n_seqs, q_heads, head_dim]        (read)
  *   page_table  int32 [n_seqs, max_pages]               (read)
  *   lengths     int32 [n_seqs]                          (read)
- *   out         bf16 [n_seqs, q_heads, head_dim]        (written)
+ *   out         bf16 [n_seqs, q_heads, head_dim]        (written; not q)
  *   lse         float [n_seqs, q_heads] or NULL         (written)
  *   workspace   device buffer of at least bd_attention_workspace_size bytes,
  *               256-byte aligned, ZERO-FILLED before its first use; every call
