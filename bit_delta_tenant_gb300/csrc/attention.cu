@@ -470,7 +470,8 @@ __device__ __forceinline__ void stream(const AttnArgs &a, uint8_t *smem, const S
                         for (int c = 0; c < 2; ++c) {
                             ks[c] = __uint_as_float((kb >> 8 * c & 0xFFu) << 23);
                             vscale[i][c] = __uint_as_float((vb >> 8 * c & 0xFFu) << 23);
-                            vexp[i][c] = __uint_as_float(0x4B000000u | (vb >> 8 * c & 0xFFu)) - (8388608.f + 127.f);
+                            // a byte below the smallest scale's, as in slots never written: no weight overflows
+                            vexp[i][c] = fmaxf(__uint_as_float(0x4B000000u | (vb >> 8 * c & 0xFFu)) - (8388608.f + 127.f), -60.f);
                         }
                     }
 #pragma unroll

@@ -36,3 +36,23 @@ def test_small_values_beside_large_ones(ratio, dim, q_heads, kv_heads, lengths, 
     out, lse = run(pool, q)
     check(pool, q, out, lse)
     assert bd.bd_get_device_status() == bd.BD_OK
+
+
+@pytest.mark.parametrize("lengths,pages", [([1, 40, 200, 17], None), ([300, 33, 2, 700], 400)])
+@pytest.mark.parametrize("byte", [0, 1, 66])
+def test_a_cache_of_zeros(byte, lengths, pages):
+    """Slots that were never written, values and scale bytes zero (or a byte below the smallest scale's): zeros, and the
+    lse of scores that are all zero."""
+    pool = Pool(lengths, 2, 64, 16, "e4m3", seed=1)
+    for x in (pool.k, pool.v):
+        x.view(torch.uint8)[:] = 0
+    pool.k_scale[:], pool.v_scale[:] = byte, byte
+    if pages:
+        wide = np.full((len(lengths), pages), -1, np.int32)
+        wide[:, :pool.table.shape[1]] = pool.table
+        pool.table = wide
+    q = randn((len(lengths), 8, 64), 9).bfloat16()
+    out, lse = run(pool, q)
+    assert (out == 0).all()
+    # log(n): the sum is exact, the logarithm and a product round
+    assert np.all(np.abs(lse.cpu().double().numpy() - np.log(lengths)[:, None]) <= 2.0 ** -18)
