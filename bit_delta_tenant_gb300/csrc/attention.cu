@@ -37,7 +37,7 @@
 //
 // Measured (head_dim 128): 130001 tokens, 64 and 8 heads, bf16 89 us (6.0 TB/s: SMs' streams end between 64 and
 // 82 us, then the joins), 8 bits 56 (4.8 TB/s); sequences of up to 8191 tokens, lengths spread in their logarithm, 32
-// and 8 heads, 8 bits: 64 of them 33 us (3.7 TB/s), 200 85 (4.5 TB/s), one to six heads to a CTA that drains its ring
+// and 8 heads, 8 bits: 64 of them 34 us (3.6 TB/s), 200 86 (4.4 TB/s), one to six heads to a CTA that drains its ring
 // at each head's end before the next head's first copy; 200 of them in bf16 122 (6.1 TB/s); 777 tokens, bf16 8.2 us,
 // a chain of latencies.  More than 16 query heads to a KV head read it once per 16: 64 sequences of up to 4000 tokens,
 // one KV head, bf16, 16 query heads 13.1 us, 48 17.2.
