@@ -380,8 +380,8 @@ def _own(s):
     if cache is None:  # a program keeps the cache's handle
         cache = s["cache"] = bd.KVCache(s["k"], s["v"], s["k_scale"], s["v_scale"])
     if c["op"] == "store":
-        bd.bd_kv_append(cache, s["q"], s["new_k"], s["new_v"], s["positions"], s["table"], s["rope"], s["q_out"],
-                        seq_ids=s["seq_ids"], interleaved=c["interleaved"])
+        bd.bd_kv_append_rotary(cache, s["q"], s["new_k"], s["new_v"], s["positions"], s["table"], s["rope"], s["q_out"],
+                               seq_ids=s["seq_ids"], interleaved=c["interleaved"])
         bd.bd_kv_read(cache, s["table"], s["offsets"], s["k_out"], s["v_out"])
         return {"q": s["q_out"], "k": s["k_out"], "v": s["v_out"]}
     rule = dict(scale=1 / math.sqrt(c["dim"]), window=c["window"], cap=c["cap"], slopes=s["slopes"], first=s["first"], lse=s["lse"])
