@@ -42,6 +42,10 @@ BD_Y_BF16 = 0
 BD_Y_E4M3 = 1
 BD_KV_BF16 = 0
 BD_KV_E4M3 = 1
+BD_KV_E2M1 = 2
+BD_ROTARY_HALF = 0
+BD_ROTARY_INTERLEAVED = 1
+BD_ROTARY_MAX_DIM = 256
 BD_LOGITS_BF16 = 0
 BD_LOGITS_F32 = 1
 BD_NORM_MAX_N = 32768
@@ -80,6 +84,12 @@ class KVCacheDesc(ctypes.Structure):
     _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
                 ("v_scale", ctypes.c_void_p), ("n_pages", ctypes.c_int64), ("kv_heads", ctypes.c_int32),
                 ("head_dim", ctypes.c_int32), ("page_size", ctypes.c_int32), ("kv_type", ctypes.c_int32)]
+
+
+class ScoreRule(ctypes.Structure):
+    """bd_score_rule: what is made of a query's products with keys, and which keys it sees."""
+    _fields_ = [("scale", ctypes.c_float), ("cap", ctypes.c_float), ("slopes", ctypes.c_void_p), ("first", ctypes.c_void_p),
+                ("prefix", ctypes.c_void_p), ("window", ctypes.c_int32), ("reserved", ctypes.c_int32)]
 
 
 class BitDeltaError(RuntimeError):
@@ -165,6 +175,17 @@ def load_library(path: str | None = None):
         lib.bd_attention_workspace_size.restype = SZ
         lib.bd_attention_decode.argtypes = [CACHE, V, I32, V, V, I32, I32, F32, I32, V, V, V, SZ, V]
         lib.bd_attention_decode.restype = I32
+        F64, RULE = ctypes.c_double, ctypes.POINTER(ScoreRule)
+        lib.bd_kv_append_rotary.argtypes = [CACHE, V, I32, V, V, I64, V, V, V, I32, I32, V, I64, I32, I32, V, V]
+        lib.bd_kv_append_rotary.restype = I32
+        lib.bd_rotary_table.argtypes = [V, I64, I32, F64, F64, F64, F64, F64, F64, V]
+        lib.bd_rotary_table.restype = I32
+        lib.bd_attention_decode_scored.argtypes = [CACHE, V, I32, V, V, I32, I32, RULE, V, V, V, SZ, V]
+        lib.bd_attention_decode_scored.restype = I32
+        lib.bd_attention_prompt_workspace_size.argtypes = [CACHE, I32]
+        lib.bd_attention_prompt_workspace_size.restype = SZ
+        lib.bd_attention_prompt.argtypes = [CACHE, V, I32, V, I64, V, V, I32, I32, RULE, V, V, V, SZ, V]
+        lib.bd_attention_prompt.restype = I32
         lib.bd_sample.argtypes = [V, I32, I64, I64, V, V, V, V, V, V, V, V]
         lib.bd_sample.restype = I32
         _lib = lib
@@ -518,27 +539,31 @@ class KVCache:
 
     k, v: [n_pages, kv_heads, page_size, head_dim], bf16, or float8_e4m3fn with k_scale and
     v_scale, the exponent bytes of their rows' power-of-two scales, uint8 [n_pages, kv_heads,
-    page_size]."""
+    page_size].  4 bits: uint8 [n_pages, kv_heads, page_size, head_dim / 2], two values to a
+    byte, with the scale bytes of 16 values each, uint8 [n_pages, kv_heads, page_size,
+    head_dim / 16]."""
 
     def __init__(self, k: torch.Tensor, v: torch.Tensor, k_scale: torch.Tensor | None = None,
                  v_scale: torch.Tensor | None = None):
         if k.dim() != 4:
             raise ValueError("k: expected [n_pages, kv_heads, page_size, head_dim]")
-        if k.dtype not in (_BF16, _E4M3):
-            raise ValueError(f"k: expected torch.bfloat16 or torch.float8_e4m3fn, got {k.dtype}")
-        e4m3 = k.dtype == _E4M3
-        if e4m3 != (k_scale is not None) or e4m3 != (v_scale is not None):
-            raise ValueError("k_scale and v_scale come with an 8-bit cache, and only with one")
-        n_pages, self.kv_heads, self.page_size, self.head_dim = k.shape
+        if k.dtype not in (_BF16, _E4M3, _U8):
+            raise ValueError(f"k: expected torch.bfloat16, torch.float8_e4m3fn or torch.uint8 (4 bits), got {k.dtype}")
+        scaled, four = k.dtype != _BF16, k.dtype == _U8
+        if scaled != (k_scale is not None) or scaled != (v_scale is not None):
+            raise ValueError("k_scale and v_scale come with an 8-bit or 4-bit cache, and only with one")
+        n_pages, self.kv_heads, self.page_size, width = k.shape
+        self.head_dim = 2 * width if four else width
+        scales = (*k.shape[:3], self.head_dim // 16) if four else k.shape[:3]
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
         d = self.desc = KVCacheDesc()
         d.k, device = _first(k, "k", k.dtype)
         self.device = device
         d.v = _arg(v, "v", k.shape, k.dtype, device)
-        d.k_scale = _arg(k_scale, "k_scale", k.shape[:3], _U8, device)
-        d.v_scale = _arg(v_scale, "v_scale", k.shape[:3], _U8, device)
+        d.k_scale = _arg(k_scale, "k_scale", scales, _U8, device)
+        d.v_scale = _arg(v_scale, "v_scale", scales, _U8, device)
         d.n_pages, d.kv_heads, d.head_dim, d.page_size = n_pages, self.kv_heads, self.head_dim, self.page_size
-        d.kv_type = BD_KV_E4M3 if e4m3 else BD_KV_BF16
+        d.kv_type = BD_KV_E2M1 if four else BD_KV_E4M3 if scaled else BD_KV_BF16
         self._ref = ctypes.byref(d)
 
 
@@ -558,6 +583,16 @@ def bd_kv_append(cache: KVCache, q: torch.Tensor | None, k: torch.Tensor, v: tor
     Token i goes to position positions[i] of sequence seq_ids[i] (of sequence i without
     seq_ids); a negative position skips it.  `rope` is fp32 [positions, head_dim], cosines then
     sines; without it nothing is rotated and q and q_out are None.  q_out may be q."""
+    if rope is not None:
+        _arg(rope, "rope", (rope.shape[0], cache.head_dim), _F32, cache.device)
+    bd_kv_append_rotary(cache, q, k, v, positions, page_table, rope, q_out, seq_ids, stream=stream)
+
+
+def bd_kv_append_rotary(cache: KVCache, q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor, positions: torch.Tensor,
+                        page_table: torch.Tensor, rope: torch.Tensor | None, q_out: torch.Tensor | None,
+                        seq_ids: torch.Tensor | None = None, interleaved: bool = False, stream=None) -> None:
+    """bd_kv_append with `rope` [positions, n]: the first n elements of each head are rotated, element i with n / 2 + i, or
+    2i with 2i + 1 when `interleaved`."""
     n, dim, device = k.shape[0], cache.head_dim, cache.device
     kv_shape = (n, cache.kv_heads, dim)
     q_heads, qp, qo = 0, None, None
@@ -566,15 +601,36 @@ def bd_kv_append(cache: KVCache, q: torch.Tensor | None, k: torch.Tensor, v: tor
             raise ValueError("q, q_out: both [tokens, q_heads, head_dim], or neither")
         q_heads = q.shape[1]
         qp, qo = _arg(q, "q", (n, q_heads, dim), _BF16, device), _arg(q_out, "q_out", (n, q_heads, dim), _BF16, device)
-    rope_len = 0 if rope is None else rope.shape[0]
+    rope_len, rope_dim, rp = 0, 0, None
+    if rope is not None:
+        if rope.dim() != 2 or rope.shape[1] > dim:
+            raise ValueError(f"rope: expected [positions, {dim}] or fewer columns, got {tuple(rope.shape)}")
+        rope_len, rope_dim = rope.shape
+        rp = _arg(rope, "rope", rope.shape, _F32, device)
     table, n_seqs, max_pages = _table(page_table, device)
-    rc = (_lib or load_library()).bd_kv_append(
+    rc = (_lib or load_library()).bd_kv_append_rotary(
         cache._ref, qp, q_heads, _arg(k, "k", kv_shape, _BF16, device), _arg(v, "v", kv_shape, _BF16, device), n,
         None if seq_ids is None else _arg(seq_ids, "seq_ids", (n,), _I32, device),
-        _arg(positions, "positions", (n,), _I32, device), table, n_seqs, max_pages, None if rope is None else _arg(rope, "rope", (rope_len, dim), _F32, device), rope_len, qo,
-        _raw_stream(stream, device))
+        _arg(positions, "positions", (n,), _I32, device), table, n_seqs, max_pages, rp, rope_len, rope_dim,
+        BD_ROTARY_INTERLEAVED if interleaved else BD_ROTARY_HALF, qo, _raw_stream(stream, device))
     if rc:
         _check(rc, "bd_kv_append")
+
+
+def bd_rotary_table(table: torch.Tensor, base: float, factor: float = 1.0, original: float = 0.0, low: float = 1.0,
+                    high: float = 4.0, amplitude: float = 1.0, stream=None) -> None:
+    """Fill table, fp32 [positions, dim], with amplitude times the cosines, then the sines, of position * frequency.
+
+    The frequencies are base ** (-2i / dim); those of `low` turns and fewer over `original`
+    positions are divided by `factor`, those of `high` and more kept, the others in between
+    (original = 0: all divided)."""
+    tp, device = _first(table, "table", _F32)
+    if table.dim() != 2:
+        raise ValueError("table: expected [positions, dim]")
+    rc = (_lib or load_library()).bd_rotary_table(tp, table.shape[0], table.shape[1], base, factor, original, low, high, amplitude,
+                                                  _raw_stream(stream, device))
+    if rc:
+        _check(rc, "bd_rotary_table")
 
 
 def bd_kv_read(cache: KVCache, page_table: torch.Tensor, offsets: torch.Tensor, k_out: torch.Tensor,
@@ -595,26 +651,77 @@ def bd_attention_workspace_size(cache: KVCache, n_seqs: int, q_heads: int) -> in
     return int(load_library().bd_attention_workspace_size(cache._ref, n_seqs, q_heads))
 
 
+def _rule(cache: KVCache, q_heads: int, rows: int, n_seqs: int, scale, window, cap, slopes, first, prefix):
+    """bd_score_rule of a call with `rows` queries."""
+    device = cache.device
+    return ctypes.byref(ScoreRule(
+        cache.head_dim ** -0.5 if scale is None else scale, cap,
+        None if slopes is None else _arg(slopes, "slopes", (q_heads,), _F32, device),
+        None if first is None else _arg(first, "first", (rows,), _I32, device),
+        None if prefix is None else _arg(prefix, "prefix", (n_seqs,), _I32, device), max(-1, min(window, 0x7FFFFFFF)), 0))
+
+
 def bd_attention_decode(cache: KVCache, q: torch.Tensor, page_table: torch.Tensor, lengths: torch.Tensor,
                         out: torch.Tensor, workspace: torch.Tensor, scale: float | None = None, window: int = 0,
-                        lse: torch.Tensor | None = None, stream=None) -> None:
+                        lse: torch.Tensor | None = None, cap: float = 0.0, slopes: torch.Tensor | None = None,
+                        first: torch.Tensor | None = None, stream=None) -> None:
     """Attention of one query per sequence, q [n_seqs, q_heads, head_dim], over its first lengths[i] cached tokens.
 
     `scale` defaults to head_dim ** -0.5; `window` > 0 lets a query see the last `window` tokens only.
+    `cap` > 0 caps scores: cap * tanh(score / cap).  `slopes`, fp32 [q_heads], subtracts slope * distance;
+    `first`, int32 [n_seqs], is the first position that a query sees.
     `workspace` is a zero-filled device buffer of at least bd_attention_workspace_size bytes (left
     ready for the next call)."""
     device = cache.device
     table, n_seqs, max_pages = _table(page_table, device)
     q_heads = q.shape[1] if q.dim() == 3 else 0
     shape = (n_seqs, q_heads, cache.head_dim)
-    rc = (_lib or load_library()).bd_attention_decode(
-        cache._ref, _arg(q, "q", shape, _BF16, device), q_heads, table, _arg(lengths, "lengths", (n_seqs,), _I32, device),
-        n_seqs, max_pages, cache.head_dim ** -0.5 if scale is None else scale, max(-1, min(window, 0x7FFFFFFF)),
-        _arg(out, "out", shape, _BF16, device),
-        None if lse is None else _arg(lse, "lse", (n_seqs, q_heads), _F32, device),
-        _arg(workspace, "workspace", workspace.shape, workspace.dtype, device), workspace.nbytes, _raw_stream(stream, device))
+    lib = _lib or load_library()
+    qp, lens = _arg(q, "q", shape, _BF16, device), _arg(lengths, "lengths", (n_seqs,), _I32, device)
+    op, lp = _arg(out, "out", shape, _BF16, device), None if lse is None else _arg(lse, "lse", (n_seqs, q_heads), _F32, device)
+    wp = _arg(workspace, "workspace", workspace.shape, workspace.dtype, device)
+    if cap == 0.0 and slopes is None and first is None:
+        rc = lib.bd_attention_decode(cache._ref, qp, q_heads, table, lens, n_seqs, max_pages,
+                                     cache.head_dim ** -0.5 if scale is None else scale, max(-1, min(window, 0x7FFFFFFF)), op, lp, wp,
+                                     workspace.nbytes, _raw_stream(stream, device))
+    else:
+        rule = _rule(cache, q_heads, n_seqs, n_seqs, scale, window, cap, slopes, first, None)
+        rc = lib.bd_attention_decode_scored(cache._ref, qp, q_heads, table, lens, n_seqs, max_pages, rule, op, lp, wp, workspace.nbytes,
+                                            _raw_stream(stream, device))
     if rc:
         _check(rc, "bd_attention_decode")
+
+
+def bd_attention_prompt_workspace_size(cache: KVCache, q_heads: int) -> int:
+    """Bytes of the workspace of bd_attention_prompt (zero-filled once by the caller)."""
+    return int(load_library().bd_attention_prompt_workspace_size(cache._ref, q_heads))
+
+
+def bd_attention_prompt(cache: KVCache, q: torch.Tensor, offsets: torch.Tensor, page_table: torch.Tensor, lengths: torch.Tensor,
+                        out: torch.Tensor, workspace: torch.Tensor, scale: float | None = None, window: int = 0,
+                        lse: torch.Tensor | None = None, cap: float = 0.0, slopes: torch.Tensor | None = None,
+                        first: torch.Tensor | None = None, prefix: torch.Tensor | None = None, stream=None) -> None:
+    """Attention of the new tokens of several sequences, q [tokens, q_heads, head_dim], over their cached tokens.
+
+    Rows offsets[i] .. offsets[i + 1] - 1 of q are the last tokens of sequence i, whose cache holds
+    lengths[i] tokens, these among them; each sees the positions up to its own.  `scale`,
+    `window`, `cap` and `slopes` as for bd_attention_decode; `first`, int32 [tokens], is the first
+    position that each token sees (the start of its document), and tokens before position prefix[i]
+    of sequence i are seen by all of its queries.
+    `workspace` is a zero-filled device buffer of at least bd_attention_prompt_workspace_size bytes
+    (left ready for the next call)."""
+    device = cache.device
+    table, n_seqs, max_pages = _table(page_table, device)
+    total, q_heads = (q.shape[0], q.shape[1]) if q.dim() == 3 else (0, 0)
+    shape = (total, q_heads, cache.head_dim)
+    rc = (_lib or load_library()).bd_attention_prompt(
+        cache._ref, _arg(q, "q", shape, _BF16, device), q_heads, _arg(offsets, "offsets", (n_seqs + 1,), _I32, device), total, table,
+        _arg(lengths, "lengths", (n_seqs,), _I32, device), n_seqs, max_pages,
+        _rule(cache, q_heads, total, n_seqs, scale, window, cap, slopes, first, prefix), _arg(out, "out", shape, _BF16, device),
+        None if lse is None else _arg(lse, "lse", (total, q_heads), _F32, device),
+        _arg(workspace, "workspace", workspace.shape, workspace.dtype, device), workspace.nbytes, _raw_stream(stream, device))
+    if rc:
+        _check(rc, "bd_attention_prompt")
 
 
 def bd_sample(logits: torch.Tensor, noise: torch.Tensor, ids: torch.Tensor, temperature: torch.Tensor | None = None,

@@ -132,6 +132,20 @@ bool encode_tensor_map_2d(CUtensorMap *map, CUtensorMapDataType dtype, const voi
               swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool encode_tensor_map_3d(CUtensorMap *map, const void *base, uint64_t inner, uint64_t middle, uint64_t outer,
+                          uint64_t middle_stride_bytes, uint64_t outer_stride_bytes, uint32_t box_inner,
+                          uint32_t box_middle, uint32_t box_outer) {
+    EncodeTiledFn fn = encode_fn();
+    if (fn == nullptr) return false;
+    const cuuint64_t dims[3] = {inner, middle, outer};
+    const cuuint64_t strides[2] = {middle_stride_bytes, outer_stride_bytes};
+    const cuuint32_t box[3] = {box_inner, box_middle, box_outer};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 }  // namespace bd
 
 BD_API int32_t bd_version(void) { return 100; }

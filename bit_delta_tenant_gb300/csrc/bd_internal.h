@@ -229,15 +229,26 @@ cudaError_t launch_rmsnorm(const NormProblem &p, const DevCtx &ctx, cudaStream_t
 cudaError_t launch_kv_append(const bd_kv_cache &c, const void *q, int32_t q_heads, const void *k, const void *v,
                              int64_t n_tokens, const int32_t *seq_ids, const int32_t *positions,
                              const int32_t *page_table, int32_t n_seqs, int32_t max_pages, const float *rope,
-                             int64_t rope_len, void *q_out, const DevCtx &ctx, cudaStream_t stream);
+                             int64_t rope_len, int32_t rope_dim, int32_t interleaved, void *q_out, const DevCtx &ctx,
+                             cudaStream_t stream);
+// Turns per position of each pair, in 2^-64; false where one is not finite.
+bool rotary_steps(uint64_t *step, int32_t dim, double base, double factor, double original, double low, double high);
+cudaError_t launch_rotary_table(float *table, int64_t positions, int32_t dim, const uint64_t *step, float amplitude,
+                                const DevCtx &ctx, cudaStream_t stream);
 cudaError_t launch_kv_read(const bd_kv_cache &c, const int32_t *page_table, int32_t n_seqs, int32_t max_pages,
                            const int32_t *offsets, int64_t total, void *k_out, void *v_out, const DevCtx &ctx,
                            cudaStream_t stream);
 
 size_t attention_workspace_size(int num_sms);
 cudaError_t launch_attention(const bd_kv_cache &c, const void *q, int32_t q_heads, const int32_t *page_table,
-                             const int32_t *lengths, int32_t n_seqs, int32_t max_pages, float scale, int32_t window,
+                             const int32_t *lengths, int32_t n_seqs, int32_t max_pages, const bd_score_rule &rule,
                              void *out, float *lse, void *workspace, const DevCtx &ctx, cudaStream_t stream);
+
+size_t prompt_workspace_size(int num_sms, int head_dim);
+cudaError_t launch_prompt(const bd_kv_cache &c, const void *q, int32_t q_heads, const int32_t *offsets, int64_t total,
+                          const int32_t *page_table, const int32_t *lengths, int32_t n_seqs, int32_t max_pages,
+                          const bd_score_rule &rule, void *out, float *lse, void *workspace, const DevCtx &ctx,
+                          cudaStream_t stream);
 
 cudaError_t launch_sample(const void *logits, int32_t logits_type, int64_t m, int64_t vocab, const float *temperature,
                           const int32_t *top_k, const float *top_p, const float *min_p, const float *noise,
@@ -247,5 +258,9 @@ cudaError_t launch_sample(const void *logits, int32_t logits_type, int64_t m, in
 bool encode_tensor_map_2d(CUtensorMap *map, CUtensorMapDataType dtype, const void *base, uint64_t inner,
                           uint64_t outer, uint64_t row_stride_bytes, uint32_t box_inner, uint32_t box_outer,
                           CUtensorMapSwizzle swizzle);
+// Three dimensions of bf16, the innermost contiguous, 128-byte swizzle.
+bool encode_tensor_map_3d(CUtensorMap *map, const void *base, uint64_t inner, uint64_t middle, uint64_t outer,
+                          uint64_t middle_stride_bytes, uint64_t outer_stride_bytes, uint32_t box_inner,
+                          uint32_t box_middle, uint32_t box_outer);
 
 }  // namespace bd

@@ -8,6 +8,7 @@
 // Measured, 8 bits, heads of 128: 8 prompts of up to 4096 tokens, 64 and 8 heads, written in
 // 40 us (5.4 TB/s), 64 tokens, 32 and 8 heads, in 2.4 us; 64 sequences of 8 heads read in
 // 59 us (6.1 TB/s), 1000 tokens in bf16 in 3.4 us.
+#include <cuda_fp4.h>
 #include <cuda_fp8.h>
 
 #include <type_traits>
@@ -161,6 +162,178 @@ __global__ void __launch_bounds__(kAppendThreads, 5) kv_append_kernel(const Appe
     }
 }
 
+// The same for a rotation of the first 2 kHalf elements of a head or of neighbours, and for a 4-bit cache.  A lane holds
+// 16 neighbouring elements, a group of the 4-bit cache, so that neither a group's maximum nor its scale crosses lanes;
+// what an element is rotated with is read a second time, from L1, where it is not among the lane's own.  Its rows are
+// read before any row of the pass is written: the query may be rotated in place, and a row's lanes are one warp's.
+constexpr int kGroupAtOnce = 2;
+
+struct GroupArgs : AppendArgs {
+    int32_t rope_dim, interleaved;
+};
+
+// Scale byte of a group in 4 bits: top / 6 to the nearest of 5 bits of exponent and 3 of mantissa.
+__device__ __forceinline__ uint32_t group_scale_byte(float top) {
+    const float t = __fdiv_rn(top, 6.f);
+    if (t < 6.103515625e-5f) return static_cast<uint32_t>(__float2int_rn(t * 131072.f));  // below 2^-14: steps of 2^-17
+    const uint32_t b = __float_as_uint(t);
+    const uint32_t r = (b + 0x7FFFFu + (b >> 20 & 1u)) >> 20;  // 3 mantissa bits, ties to even
+    return min(r - ((127u - 15u) << 3), 0xF7u);
+}
+__device__ __forceinline__ float group_scale(uint32_t byte) { return __half2float(__ushort_as_half(static_cast<unsigned short>(byte << 7))); }
+
+template <int kDim, int kType>
+__global__ void __launch_bounds__(kAppendThreads) kv_append_group_kernel(const GroupArgs a) {
+    constexpr int kLanes = kDim / 16;  // lanes of one row
+    constexpr int kRowsPerPass = kAppendThreads / kLanes;
+    pdl_trigger_and_wait();
+    const int64_t t = blockIdx.x;
+    const int lane = threadIdx.x % kLanes, row0 = threadIdx.x / kLanes;
+    const int q_rows = a.q ? a.q_heads : 0;
+    const int rows = q_rows + 2 * a.kv_heads;
+    const int half = a.rope ? a.rope_dim / 2 : 0;
+    const bool turn = lane * 16 < 2 * half;  // a multiple of 16: all 16 elements or none
+    const bool exchange = turn && !a.interleaved;
+    uint4 in[kGroupAtOnce][2], with[kGroupAtOnce][2];
+    // piece w of this lane starts at element lane * 16 + 8 w; it is rotated with the piece at partner(w)
+    auto partner = [&](int w) {
+        const int e = lane * 16 + 8 * w;
+        return e < half ? e + half : e - half;
+    };
+    auto load = [&](int r0) {
+#pragma unroll
+        for (int u = 0; u < kGroupAtOnce; ++u) {
+            const int r = r0 + u * kRowsPerPass;
+            in[u][0] = in[u][1] = with[u][0] = with[u][1] = make_uint4(0, 0, 0, 0);
+            if (r >= rows) continue;
+            const bool is_v = r >= q_rows + a.kv_heads;
+            if (!in_bounds(r >= 0 && r < q_rows + 2 * a.kv_heads, a.status)) continue;
+            const uint8_t *src = r < q_rows ? a.q + (t * a.q_heads + r) * (kDim * 2)
+                                            : (is_v ? a.v : a.k) + (t * a.kv_heads + r - q_rows - (is_v ? a.kv_heads : 0)) * (kDim * 2);
+#pragma unroll
+            for (int w = 0; w < 2; ++w) {
+                in[u][w] = ldg_plain(src + lane * 32 + w * 16);
+                if (exchange && !is_v) with[u][w] = ldg_plain(src + partner(w) * 2);
+            }
+        }
+    };
+    load(row0);
+    const int32_t pos = a.positions[t];
+    if (pos < 0) return;  // padding
+    const int64_t seq = a.seq_ids ? a.seq_ids[t] : t;
+    const int64_t page_at = pos / a.page_size;
+    const int slot = pos % a.page_size;
+    int64_t page = -1;
+    if (seq >= 0 && seq < a.n_seqs && page_at < a.max_pages && (a.rope == nullptr || pos < a.rope_len))
+        page = a.page_table[seq * a.max_pages + page_at];
+    if (page < 0 || page >= a.n_pages) {
+        if (threadIdx.x == 0) flag_status(a.status, kDevBadIndex);
+        return;
+    }
+    // cosines and sines: of each element where halves are exchanged, of each pair (in the first 4) where neighbours are
+    float c[2][8] = {}, s[2][8] = {};
+    if (turn) {
+        const float *row = a.rope + pos * static_cast<int64_t>(a.rope_dim);
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+            const int e = lane * 16 + 8 * w;
+            const int at = a.interleaved ? e / 2 : (e < half ? e : e - half);
+#pragma unroll
+            for (int j = 0; j < 8; j += 4) {
+                if (a.interleaved && j) continue;
+                const float4 cv = __ldg(reinterpret_cast<const float4 *>(row + at + j));
+                const float4 sv = __ldg(reinterpret_cast<const float4 *>(row + half + at + j));
+                c[w][j] = cv.x, c[w][j + 1] = cv.y, c[w][j + 2] = cv.z, c[w][j + 3] = cv.w;
+                s[w][j] = sv.x, s[w][j + 1] = sv.y, s[w][j + 2] = sv.z, s[w][j + 3] = sv.w;
+            }
+        }
+    }
+    const int64_t slot_row = page * a.kv_heads * a.page_size + slot;
+    for (int r0 = row0; r0 - row0 < rows; r0 += kGroupAtOnce * kRowsPerPass) {  // as often for every lane: see the shuffles
+        if (r0 != row0) load(r0);
+        __syncwarp();  // what the row's other lanes read of it is read
+#pragma unroll
+        for (int u = 0; u < kGroupAtOnce; ++u) {
+            const int r = r0 + u * kRowsPerPass;
+            const bool is_q = r < q_rows, is_v = r >= q_rows + a.kv_heads;
+            float x[2][8];
+#pragma unroll
+            for (int w = 0; w < 2; ++w) {
+                unpack8(in[u][w], x[w]);
+                if (!turn || is_v) continue;
+                if (a.interleaved) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float lo = x[w][2 * j], hi = x[w][2 * j + 1];
+                        x[w][2 * j] = __fsub_rn(__fmul_rn(lo, c[w][j]), __fmul_rn(hi, s[w][j]));
+                        x[w][2 * j + 1] = __fadd_rn(__fmul_rn(hi, c[w][j]), __fmul_rn(lo, s[w][j]));
+                    }
+                } else {
+                    float y[8];
+                    unpack8(with[u][w], y);
+                    const bool low = lane * 16 + 8 * w < half;
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        x[w][j] = low ? __fsub_rn(__fmul_rn(x[w][j], c[w][j]), __fmul_rn(y[j], s[w][j]))
+                                      : __fadd_rn(__fmul_rn(x[w][j], c[w][j]), __fmul_rn(y[j], s[w][j]));
+                }
+            }
+            if (is_q && in_bounds(r < a.q_heads, a.status)) {
+                uint4 *dst = reinterpret_cast<uint4 *>(a.q_out + (t * a.q_heads + r) * (kDim * 2) + lane * 32);
+                dst[0] = pack8(x[0]), dst[1] = pack8(x[1]);
+            }
+            if (__all_sync(0xFFFFFFFFu, is_q || r >= rows)) continue;
+            float top = 0.f;
+            bool nan = false;
+            if constexpr (kType != BD_KV_BF16) {
+#pragma unroll
+                for (int w = 0; w < 2; ++w)
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        if (fabsf(x[w][j]) < INFINITY) top = fmaxf(top, fabsf(x[w][j]));
+                        nan |= x[w][j] != x[w][j];
+                    }
+            }
+            if constexpr (kType == BD_KV_E4M3) {  // a scale for the whole row
+#pragma unroll
+                for (int o = kLanes / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+            }
+            if (is_q || r >= rows) continue;
+            const int64_t at = slot_row + static_cast<int64_t>(r - q_rows - (is_v ? a.kv_heads : 0)) * a.page_size;
+            if (!in_bounds(at >= 0 && at < a.n_pages * a.kv_heads * a.page_size, a.status)) continue;
+            uint8_t *dst = is_v ? a.cv : a.ck, *scales = is_v ? a.cv_scale : a.ck_scale;
+            if constexpr (kType == BD_KV_BF16) {
+                uint4 *d = reinterpret_cast<uint4 *>(dst + at * (kDim * 2) + lane * 32);
+                d[0] = pack8(x[0]), d[1] = pack8(x[1]);
+            } else if constexpr (kType == BD_KV_E4M3) {
+                const int e = scale_byte(top);
+                const float inv = __uint_as_float(static_cast<uint32_t>(254 - e) << 23);  // 2^(127 - e), exact
+                uint32_t b[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    b[j] = __nv_cvt_float2_to_fp8x2(make_float2(x[j / 4][j % 4 * 2] * inv, x[j / 4][j % 4 * 2 + 1] * inv), __NV_SATFINITE,
+                                                    __NV_E4M3);
+                *reinterpret_cast<uint4 *>(dst + at * kDim + lane * 16) =
+                    make_uint4(b[0] | b[1] << 16, b[2] | b[3] << 16, b[4] | b[5] << 16, b[6] | b[7] << 16);
+                if (lane == 0) scales[at] = static_cast<uint8_t>(e);
+            } else {
+                const uint32_t byte = group_scale_byte(top);
+                // a quotient, not a product with 1 / s: many values of a group lie on a tie between two codes
+                const float scale = group_scale(byte);
+                auto over = [&](float v) { return byte ? __fdiv_rn(v, scale) : copysignf(0.f, v); };
+                uint32_t b[2] = {0, 0};
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const float2 y = make_float2(over(x[j / 4][j % 4 * 2]), over(x[j / 4][j % 4 * 2 + 1]));
+                    b[j / 4] |= static_cast<uint32_t>(__nv_cvt_float2_to_fp4x2(y, __NV_E2M1, cudaRoundNearest)) << j % 4 * 8;
+                }
+                *reinterpret_cast<uint2 *>(dst + at * (kDim / 2) + lane * 8) = make_uint2(b[0], b[1]);
+                scales[at * (kDim / 16) + lane] = static_cast<uint8_t>(nan ? 0xFFu : byte);
+            }
+        }
+    }
+}
+
 // ---- read ------------------------------------------------------------------------------
 
 constexpr int kReadThreads = 256;
@@ -184,10 +357,23 @@ __device__ __forceinline__ uint32_t e4m3x2_to_bf16x2(uint32_t two, float scale) 
     return pack_bf16x2(f.x * scale, f.y * scale);
 }
 
-template <int kDim, bool kE4m3>
+// Four bytes of 4-bit values times a scale, as bf16 pairs: 2 significant bits times 4 at most, exact.
+__device__ __forceinline__ uint4 e2m1x8_to_bf16x8(uint32_t eight, float scale) {
+    uint32_t out[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const __half2_raw h = __nv_cvt_fp4x2_to_halfraw2(static_cast<__nv_fp4x2_storage_t>(eight >> 8 * j & 0xFFu), __NV_E2M1);
+        const float2 f = __half22float2(__half2(h));
+        out[j] = pack_bf16x2(f.x * scale, f.y * scale);
+    }
+    return make_uint4(out[0], out[1], out[2], out[3]);
+}
+
+template <int kDim, int kType>
 __global__ void __launch_bounds__(kReadThreads) kv_read_kernel(const ReadArgs a) {
     constexpr int kChunk = kDim / 8;  // 8 elements: 16 bytes of the output
-    using Raw = typename std::conditional<kE4m3, uint2, uint4>::type;
+    constexpr bool kE4m3 = kType == BD_KV_E4M3;
+    using Raw = typename std::conditional<kE4m3, uint2, typename std::conditional<kType == BD_KV_E2M1, uint32_t, uint4>::type>::type;
     __shared__ int64_t first[kReadTokens];                // (page * kv_heads) * page_size + slot; -1: nothing, -2: zeros
     pdl_trigger_and_wait();
     const int64_t t0 = static_cast<int64_t>(blockIdx.x) * a.tokens;
@@ -232,6 +418,8 @@ __global__ void __launch_bounds__(kReadThreads) kv_read_kernel(const ReadArgs a)
                 if (f < 0 || !in_bounds(row < a.n_pages * a.kv_heads * a.page_size, a.status)) continue;
                 v[u][w] = __ldcs(reinterpret_cast<const Raw *>(w ? a.cv : a.ck) + row * kChunk + rest % kChunk);
                 if constexpr (kE4m3) s[u][w] = __uint_as_float(static_cast<uint32_t>((w ? a.cv_scale : a.ck_scale)[row]) << 23);
+                if constexpr (kType == BD_KV_E2M1)
+                    s[u][w] = group_scale((w ? a.cv_scale : a.ck_scale)[row * (kDim / 16) + rest % kChunk / 2]);
             }
         }
 #pragma unroll
@@ -241,8 +429,10 @@ __global__ void __launch_bounds__(kReadThreads) kv_read_kernel(const ReadArgs a)
             for (int w = 0; w < 2; ++w) {
                 uint4 *d = reinterpret_cast<uint4 *>(w ? a.v_out : a.k_out) + to[u];
                 const Raw x = v[u][w];
-                if constexpr (!kE4m3) {
+                if constexpr (kType == BD_KV_BF16) {
                     *d = x;
+                } else if constexpr (kType == BD_KV_E2M1) {
+                    *d = e2m1x8_to_bf16x8(x, s[u][w]);
                 } else {
                     const float f = s[u][w];
                     *d = make_uint4(e4m3x2_to_bf16x2(x.x & 0xFFFFu, f), e4m3x2_to_bf16x2(x.x >> 16, f),
@@ -272,8 +462,11 @@ cudaError_t launch_pdl(void (*kernel)(const Args), int64_t grid, int threads, co
 cudaError_t launch_kv_append(const bd_kv_cache &c, const void *q, int32_t q_heads, const void *k, const void *v,
                              int64_t n_tokens, const int32_t *seq_ids, const int32_t *positions,
                              const int32_t *page_table, int32_t n_seqs, int32_t max_pages, const float *rope,
-                             int64_t rope_len, void *q_out, const DevCtx &ctx, cudaStream_t stream) {
-    AppendArgs a;
+                             int64_t rope_len, int32_t rope_dim, int32_t interleaved, void *q_out, const DevCtx &ctx,
+                             cudaStream_t stream) {
+    GroupArgs a;
+    a.rope_dim = rope_dim;
+    a.interleaved = interleaved;
     a.q = static_cast<const uint8_t *>(q);
     a.k = static_cast<const uint8_t *>(k);
     a.v = static_cast<const uint8_t *>(v);
@@ -294,11 +487,22 @@ cudaError_t launch_kv_append(const bd_kv_cache &c, const void *q, int32_t q_head
     a.page_size = c.page_size;
     a.n_seqs = n_seqs;
     a.max_pages = max_pages;
-    const bool e = c.kv_type == BD_KV_E4M3;
-    if (c.head_dim == 128)
-        return launch_pdl(e ? kv_append_kernel<128, true> : kv_append_kernel<128, false>, n_tokens, kAppendThreads, a,
+    const bool e = c.kv_type == BD_KV_E4M3, wide = c.head_dim == 128;
+    if (c.kv_type == BD_KV_E2M1)
+        return launch_pdl(wide ? kv_append_group_kernel<128, BD_KV_E2M1> : kv_append_group_kernel<64, BD_KV_E2M1>, n_tokens,
+                          kAppendThreads, a, stream);
+    if (rope && (interleaved || rope_dim != c.head_dim)) {
+        if (wide)
+            return launch_pdl(e ? kv_append_group_kernel<128, BD_KV_E4M3> : kv_append_group_kernel<128, BD_KV_BF16>, n_tokens,
+                              kAppendThreads, a, stream);
+        return launch_pdl(e ? kv_append_group_kernel<64, BD_KV_E4M3> : kv_append_group_kernel<64, BD_KV_BF16>, n_tokens,
+                          kAppendThreads, a, stream);
+    }
+    const AppendArgs &whole = a;
+    if (wide)
+        return launch_pdl(e ? kv_append_kernel<128, true> : kv_append_kernel<128, false>, n_tokens, kAppendThreads, whole,
                           stream);
-    return launch_pdl(e ? kv_append_kernel<64, true> : kv_append_kernel<64, false>, n_tokens, kAppendThreads, a, stream);
+    return launch_pdl(e ? kv_append_kernel<64, true> : kv_append_kernel<64, false>, n_tokens, kAppendThreads, whole, stream);
 }
 
 cudaError_t launch_kv_read(const bd_kv_cache &c, const int32_t *page_table, int32_t n_seqs, int32_t max_pages,
@@ -326,10 +530,12 @@ cudaError_t launch_kv_read(const bd_kv_cache &c, const int32_t *page_table, int3
     a.per_token = static_cast<uint32_t>(c.kv_heads * (c.head_dim / 8));
     a.magic = static_cast<uint32_t>(((uint64_t{1} << 32) + a.per_token - 1) / a.per_token);  // exact for 16 x 16384 pieces
     const int64_t grid = (total + a.tokens - 1) / a.tokens;
-    const bool e = c.kv_type == BD_KV_E4M3;
-    if (c.head_dim == 128)
-        return launch_pdl(e ? kv_read_kernel<128, true> : kv_read_kernel<128, false>, grid, kReadThreads, a, stream);
-    return launch_pdl(e ? kv_read_kernel<64, true> : kv_read_kernel<64, false>, grid, kReadThreads, a, stream);
+    const bool e = c.kv_type == BD_KV_E4M3, wide = c.head_dim == 128;
+    if (c.kv_type == BD_KV_E2M1)
+        return launch_pdl(wide ? kv_read_kernel<128, BD_KV_E2M1> : kv_read_kernel<64, BD_KV_E2M1>, grid, kReadThreads, a, stream);
+    if (wide)
+        return launch_pdl(e ? kv_read_kernel<128, BD_KV_E4M3> : kv_read_kernel<128, BD_KV_BF16>, grid, kReadThreads, a, stream);
+    return launch_pdl(e ? kv_read_kernel<64, BD_KV_E4M3> : kv_read_kernel<64, BD_KV_BF16>, grid, kReadThreads, a, stream);
 }
 
 }  // namespace bd

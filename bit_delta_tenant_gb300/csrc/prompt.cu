@@ -1,0 +1,1105 @@
+// prompt.cu -- attention of prompts over a paged key-value cache, on the tensor cores.
+//
+//   o = sum_j exp(s_j - m) V_j / sum_j exp(s_j - m),  s_j the score rule of q . K_j
+//
+// Bound: tensor cores (4 head_dim products per seen pair; a block of 128 keys against 256 rows is 2048 clocks of
+// tcgen05 at head_dim 128, its 32768 exponentials about half of that), HBM or latency for a few queries.
+//
+// Work.  A row is one query of one head; the heads that share a KV head are rows of the same tile, so that K and V are
+// read once for all of them and a tile of 128 rows holds 128 / heads tokens.  A unit is two such tiles (256 rows) of
+// one sequence and KV head, or, where units are fewer than SMs, a piece of its keys; each CTA (one per SM) takes units
+// in turn, a sequence's last tiles first, as those see the most keys.  Pieces leave their unnormalised output, maximum and sum in
+// the workspace and a second kernel joins them in key order, so results do not depend on timing.
+//
+// A CTA.  Warps 0-3 and 4-7: the softmax of one tile each, a thread per row.  Warp 8: issues the products.  Warp 9: finds
+// the next unit and its blocks.  Warp 10 on: K and V of the cache to a ring of shared-memory tiles, by TMA in
+// bf16 (warp 10; warp 11 looks at the blocks that some row sees only in part), by six warps that convert 8-bit and 4-bit values.
+// S = Q K^T goes to tensor memory; a softmax thread reads its row, and writes the weights back there as the bf16 operand of
+// P V, whose accumulator stays in tensor memory.  The two tiles alternate: one's products run under the other's softmax.
+// The running maximum is raised only when a row passes it by 2^8, so that the output is seldom rescaled: weights
+// are at most 2^8, sums stay fp32.
+//
+// Values that a row does not see.  A weight of 0 does not hide an infinity or NaN of V.  Blocks that some row sees in part
+// are looked at: rows of V that nobody sees are zeroed, and where a finite number is missing in another one, the
+// block's P V is added up by the softmax threads, row by row over the keys that the row sees, instead of by the tensor cores.
+#include <cuda_fp4.h>
+#include <cuda_fp8.h>
+
+#include "bd_device.cuh"
+#include "bd_internal.h"
+#include "bd_rows.cuh"
+
+namespace bd {
+namespace {
+
+constexpr int kBlock = 128;  // keys of a block
+constexpr int kTileRows = 128;
+constexpr int64_t kMaxLength = 1 << 30;
+constexpr int kConvertWarps = 6;
+constexpr float kLazy = 8.f;  // by how much (in base 2) a row's scores may pass the maximum they are taken from
+
+template <int kType>
+constexpr int kThreadsOf = kType == BD_KV_BF16 ? 384 : (10 + kConvertWarps) * 32;
+template <int kDim>
+constexpr uint32_t kTileBytes = kBlock * kDim * 2;  // of K, V or Q in shared memory: columns in pieces of 64, swizzled
+template <int kDim>
+constexpr int kStages = kDim == 128 ? 5 : 8;
+template <int kDim>
+constexpr int kSmemBytes = 1024 + (2 + kStages<kDim>) * kTileBytes<kDim> + 1024;
+constexpr int kSlotRows = 2 * kTileRows;
+template <int kDim>
+constexpr int64_t kSlotFloats = kSlotRows * (kDim + 2);  // a piece's output, maxima and sums, tile by tile
+
+// A unit: tokens row0 .. of q (positions pos0 ..) against blocks blk0 .. of the sequence's keys.
+struct Unit {
+    int32_t seq, row0, tokens, pos0, len, prefix, vh;
+    int32_t blk0, blocks;  // blocks < 0: no more units
+    int32_t in_lo, in_hi;  // keys that every row that sees any sees
+    int32_t un_lo, un_hi;  // keys that some row sees
+    int32_t slot, parts;   // a piece's slot and how many there are, or -1 and 1
+    int32_t state;         // kFirstPiece; kGaps: some page id is out of range
+};
+constexpr int kFirstPiece = 1, kGaps = 2;
+static_assert(sizeof(Unit) == 64);
+
+struct PromptArgs {
+    const uint8_t *ck, *cv, *ck_scale, *cv_scale;
+    const int32_t *page_table, *offsets, *lengths, *first, *prefix;
+    const float *slopes;
+    uint8_t *out;
+    float *lse, *parts;
+    int4 *heads;  // of the joining kernel: per slot, {pieces, first row of q, tokens, KV head} of a unit's first piece
+    unsigned *status;
+    uint64_t wait_ns;
+    int64_t n_pages, total;
+    int32_t n_seqs, max_pages, page_size, kv_heads, q_heads;
+    int32_t group, subs, heads_tile, tile_tokens;  // query heads of a KV head, in `subs` lots of heads_tile; tokens of a tile
+    int32_t window, slots, box;                    // box: keys of one TMA copy
+    float scale_log2, cap, cap_in;
+    int32_t may_split, plain;                      // plain: scores are products times a positive scale
+};
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map, uint64_t *bar, int c0, int c1, int c2) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2)
+        : "memory");
+}
+__device__ __forceinline__ float tmem_ld_one(uint32_t taddr) {
+    uint32_t v;
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(v) : "r"(taddr));
+    tmem_ld_wait();
+    return __uint_as_float(v);
+}
+// Shared-memory descriptor of an operand whose rows are the product's inner dimension (V: 64 columns of a key side by
+// side, 128-byte swizzle): 8 keys are 1024 bytes, the next 64 columns lie a column piece further.
+__device__ __forceinline__ uint64_t sw128_rows_desc(uint32_t addr) {
+    uint64_t d = 0;
+    d |= static_cast<uint64_t>((addr & 0x3FFFFu) >> 4);
+    d |= static_cast<uint64_t>((kBlock * 128) >> 4) << 16;  // to the next 64 columns
+    d |= static_cast<uint64_t>(1024 >> 4) << 32;            // to the next 8 keys
+    d |= static_cast<uint64_t>(1) << 46;
+    d |= static_cast<uint64_t>(2) << 61;
+    return d;
+}
+// Byte of 16-byte chunk c (8 columns) of row r in a tile: pieces of 64 columns, chunks turned by the row.
+__device__ __forceinline__ uint32_t tile_at(int r, int c) { return (c / 8) * (kBlock * 128) + r * 128 + (((c % 8) ^ (r & 7)) << 4); }
+
+__device__ __forceinline__ bool not_finite(uint4 v) {  // of eight bf16 numbers
+    auto two = [](uint32_t x) { return (x & 0x7F80u) == 0x7F80u || (x & 0x7F800000u) == 0x7F800000u; };
+    return two(v.x) || two(v.y) || two(v.z) || two(v.w);
+}
+
+struct Smem {
+    uint64_t *full, *empty, *fixed;      // per stage
+    uint64_t *q_full, *q_empty, *s_full, *p_full, *o_full;  // per tile
+    uint64_t *u_full, *u_empty;          // per unit slot
+    Unit *unit;
+    volatile int *slow;                  // per stage: number (from 1) of the last load of a V that is not finite and not seen by all
+    volatile int *abort;
+    uint32_t *tmem;
+};
+
+// Bounded wait of a warp; on give-up the status word and the other roles are told.
+__device__ __forceinline__ bool wait_on(uint64_t *bar, uint32_t parity, const PromptArgs &a, volatile int *abort) {
+    const bool ok = mbar_wait(bar, parity, a.wait_ns, abort);
+    if (__all_sync(0xFFFFFFFFu, ok)) return true;
+    if (threadIdx.x % 32 == 0) {
+        *abort = 1;
+        flag_status(a.status, kDevTimeout);
+    }
+    return false;
+}
+
+// ---- units -----------------------------------------------------------------------------
+
+struct Sequence {
+    int32_t row0, n, len, prefix;
+    int32_t units, blocks;  // of a KV head: tiles' pairs, and blocks of the longest
+};
+__device__ __forceinline__ Sequence sequence_of(const PromptArgs &a, int64_t i) {
+    Sequence s = {};
+    const int32_t from = a.offsets[i], to = a.offsets[i + 1];
+    const int64_t most = min(static_cast<int64_t>(a.max_pages) * a.page_size, kMaxLength);
+    int64_t len = a.lengths[i];
+    if (from < 0 || to < from || to > a.total || len < 0 || len > most) flag_status(a.status, kDevBadIndex);
+    len = len < 0 ? 0 : len > most ? most : len;
+    s.len = static_cast<int32_t>(len);
+    if (from < 0 || to < from || to > a.total) return s;
+    s.row0 = from;
+    s.n = to - from;
+    if (s.n > s.len) flag_status(a.status, kDevBadIndex);
+    s.prefix = a.prefix ? max(0, min(a.prefix[i], s.len)) : 0;
+    const int pair = 2 * a.tile_tokens;
+    s.units = (s.n + pair - 1) / pair;
+    s.blocks = (s.len + kBlock - 1) / kBlock;
+    if (a.window > 0) s.blocks = static_cast<int32_t>(min(static_cast<int64_t>(s.blocks), (static_cast<int64_t>(a.window) + max(pair, s.prefix)) / kBlock + 2));
+    return s;
+}
+__device__ __forceinline__ int32_t pieces_of(const Sequence &s, int32_t most) { return s.blocks > most ? (s.blocks + most - 1) / most : 1; }
+
+__device__ __forceinline__ int64_t warp_sum(int64_t v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+    return v;
+}
+__device__ __forceinline__ int64_t warp_scan(int64_t v) {  // inclusive
+#pragma unroll
+    for (int o = 1; o < 32; o *= 2) {
+        const int64_t u = __shfl_up_sync(0xFFFFFFFFu, v, o);
+        if (static_cast<int>(threadIdx.x % 32) >= o) v += u;
+    }
+    return v;
+}
+
+// Warp 9.
+__device__ __forceinline__ void find_units(const PromptArgs &a, const Smem &s) {
+    const int lane = threadIdx.x % 32;
+    const int vheads = a.kv_heads * a.subs, pair = 2 * a.tile_tokens;
+    // blocks of a piece: as few as give every CTA a unit at most, where whole units leave CTAs without one
+    int32_t most = 1 << 30;
+    if (a.may_split) {
+        int64_t units = 0, blocks = 0;
+        for (int64_t i = lane; i < a.n_seqs; i += 32) {
+            const Sequence q = sequence_of(a, i);
+            units += q.units, blocks += static_cast<int64_t>(q.units) * q.blocks;
+        }
+        units = warp_sum(units) * vheads, blocks = warp_sum(blocks) * vheads;
+        if (units <= a.slots) {
+            most = max(4, static_cast<int32_t>((blocks + a.slots - 1) / a.slots));
+            while (true) {
+                int64_t pieces = 0;
+                for (int64_t i = lane; i < a.n_seqs; i += 32) {
+                    const Sequence q = sequence_of(a, i);
+                    pieces += static_cast<int64_t>(q.units) * pieces_of(q, most);
+                }
+                if (warp_sum(pieces) * vheads <= a.slots) break;
+                most += most / 16 + 1;
+            }
+        }
+    }
+    int64_t first = 0, before = 0;  // the 32 sequences looked at, and the units of those before them
+    Sequence q = {};
+    int64_t mine = 0, upto = 0;
+    auto look = [&] {
+        q = Sequence{};
+        if (first + lane < a.n_seqs) q = sequence_of(a, first + lane);
+        mine = static_cast<int64_t>(q.units) * pieces_of(q, most) * vheads;
+        upto = warp_scan(mine);
+    };
+    look();
+    int it = 0;
+    for (int64_t round = 0;; ++round) {
+        // each round in the other direction, as units grow lighter
+        const int64_t u = round * gridDim.x + (round % 2 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+        bool over = false;
+        while (true) {
+            const int64_t all = __shfl_sync(0xFFFFFFFFu, upto, 31);
+            if (u < before + all) break;
+            if (round * gridDim.x >= before + all && first + 32 >= a.n_seqs) {
+                over = true;
+                break;
+            }
+            if (first + 32 >= a.n_seqs) break;  // this round has no unit for this CTA
+            before += all, first += 32;
+            look();
+        }
+        Unit d = {};
+        d.blocks = -1;
+        const int64_t all = __shfl_sync(0xFFFFFFFFu, upto, 31);
+        if (!over && u >= before + all) continue;
+        if (!over) {
+            const unsigned holds = __ballot_sync(0xFFFFFFFFu, u < before + upto);
+            const int owner = __ffs(holds) - 1;
+            int64_t at = u - before - __shfl_sync(0xFFFFFFFFu, upto - mine, owner);
+            Sequence w;
+            w.row0 = __shfl_sync(0xFFFFFFFFu, q.row0, owner), w.n = __shfl_sync(0xFFFFFFFFu, q.n, owner);
+            w.len = __shfl_sync(0xFFFFFFFFu, q.len, owner), w.prefix = __shfl_sync(0xFFFFFFFFu, q.prefix, owner);
+            w.units = __shfl_sync(0xFFFFFFFFu, q.units, owner), w.blocks = __shfl_sync(0xFFFFFFFFu, q.blocks, owner);
+            const int pieces = pieces_of(w, most);
+            d.seq = static_cast<int32_t>(first + owner);
+            d.vh = static_cast<int32_t>(at % vheads);
+            at /= vheads;
+            const int piece = static_cast<int>(at % pieces);
+            const int tile = w.units - 1 - static_cast<int>(at / pieces);
+            d.row0 = w.row0 + tile * pair;
+            d.tokens = min(pair, w.n - tile * pair);
+            d.pos0 = w.len - w.n + tile * pair;
+            d.len = w.len, d.prefix = w.prefix;
+            // what its rows see
+            int un_lo = INT_MAX, un_hi = 0, in_lo = 0, in_hi = INT_MAX;
+            for (int t = lane; t < d.tokens; t += 32) {
+                const int p = d.pos0 + t;
+                if (p < 0) continue;
+                const int hi = max(p + 1, d.prefix);
+                int lo = a.window > 0 ? max(0, p - a.window + 1) : 0;
+                if (a.first && in_bounds(d.row0 + t < a.total, a.status)) lo = max(lo, a.first[d.row0 + t]);
+                if (lo >= hi) continue;
+                un_lo = min(un_lo, lo), un_hi = max(un_hi, hi), in_lo = max(in_lo, lo), in_hi = min(in_hi, hi);
+            }
+            un_lo = __reduce_min_sync(0xFFFFFFFFu, un_lo), un_hi = __reduce_max_sync(0xFFFFFFFFu, un_hi);
+            in_lo = __reduce_max_sync(0xFFFFFFFFu, in_lo), in_hi = __reduce_min_sync(0xFFFFFFFFu, in_hi);
+            int b0 = 0, b1 = 0;
+            if (un_lo < un_hi) b0 = un_lo / kBlock, b1 = (un_hi + kBlock - 1) / kBlock;
+            d.slot = -1, d.parts = 1;
+            if (pieces > 1) {
+                const int whole = b1 - b0, parts = max(1, (whole + most - 1) / most);
+                if (piece >= parts) continue;  // shorter than the sequence's longest
+                if (parts > 1) d.slot = static_cast<int32_t>(u), d.parts = parts;
+                b0 += piece * most;
+                b1 = min(b1, b0 + most);
+            }
+            d.blk0 = b0, d.blocks = b1 - b0;
+            d.in_lo = in_lo, d.in_hi = in_hi, d.un_lo = un_lo, d.un_hi = un_hi;
+            d.state = piece == 0 ? kFirstPiece : 0;
+            const int32_t *table = a.page_table + static_cast<int64_t>(d.seq) * a.max_pages;
+            bool gaps = false;
+            const int key0 = max(un_lo, b0 * kBlock), key1 = min(un_hi, b1 * kBlock);
+            if (key0 < key1) {
+                const int last = (key1 - 1) / a.page_size;
+#pragma unroll 4
+                for (int i = key0 / a.page_size + lane; i <= last; i += 32)
+                    if (in_bounds(i < a.max_pages, a.status)) gaps |= table[i] < 0 || table[i] >= a.n_pages;
+            }
+            if (__any_sync(0xFFFFFFFFu, gaps)) d.state |= kGaps;
+        }
+        if (!wait_on(&s.u_empty[it & 1], ((it >> 1) & 1) ^ 1, a, s.abort)) return;
+        if (lane == 0) {
+            s.unit[it & 1] = d;
+            mbar_arrive(&s.u_full[it & 1]);
+        }
+        __syncwarp();
+        ++it;
+        if (over) return;
+    }
+}
+
+// The next unit, or blocks < 0 after the last one and on give-up.
+__device__ __forceinline__ Unit next_unit(const PromptArgs &a, const Smem &s, int &it) {
+    Unit u;
+    u.blocks = -1;
+    if (!wait_on(&s.u_full[it & 1], (it >> 1) & 1, a, s.abort)) return u;
+    u = s.unit[it & 1];
+    __syncwarp();
+    if (threadIdx.x % 32 == 0) mbar_arrive(&s.u_empty[it & 1]);
+    ++it;
+    return u;
+}
+
+__device__ __forceinline__ bool seen_in_part(const Unit &u, int blk) { return blk * kBlock < u.in_lo || (blk + 1) * kBlock > u.in_hi; }
+
+// ---- warp 8: products --------------------------------------------------------------------
+
+template <int kDim, int kType>
+__device__ __forceinline__ void issue_products(const PromptArgs &a, const Smem &s, uint32_t tmem, uint32_t smem_q, uint32_t smem_kv) {
+    constexpr int kS = kStages<kDim>;
+    constexpr uint32_t kO = 2 * kBlock, kP = kDim == 128 ? 0 : 2 * kBlock + 2 * kDim;  // columns of O; of P where it is not in S's place
+    constexpr uint32_t idesc_s = idesc_bf16_f32(kTileRows, kBlock), idesc_o = idesc_bf16_f32(kTileRows, kDim) | 1u << 16;  // V: rows are keys
+    const bool leader = threadIdx.x % 32 == 0;
+    int it = 0, loads = 0;  // K and V tiles used so far
+    int q_n[2] = {0, 0}, p_n[2] = {0, 0};
+    bool ok = true;
+    auto scores = [&](int i, int stage) {  // S of tile i
+        if (leader) {
+            const uint64_t qd = sw128_kmajor_desc(smem_q + i * kTileBytes<kDim>), kd = sw128_kmajor_desc(smem_kv + stage * kTileBytes<kDim>);
+#pragma unroll
+            for (int k = 0; k < kDim / 16; ++k) {
+                const uint32_t at = k / 4 * (kBlock * 128 / 16) + k % 4 * 2;
+                tc_mma_f16_ss(tmem + i * kBlock, qd + at, kd + at, idesc_s, k > 0);
+            }
+            tc_commit(&s.s_full[i]);
+        }
+        __syncwarp();
+    };
+    auto start = [&](const Unit &u) {  // scores of a unit's first block
+        const int stage = loads % kS;
+        const int tiles = u.tokens > a.tile_tokens ? 2 : 1;
+        if (!wait_on(&s.full[stage], (loads / kS) & 1, a, s.abort)) return false;
+        for (int i = 0; i < tiles; ++i) {
+            if (!wait_on(&s.q_full[i], q_n[i] & 1, a, s.abort)) return false;
+            ++q_n[i];
+            tc_fence_after();
+            scores(i, stage);
+            if (u.blocks == 1 && leader) tc_commit(&s.q_empty[i]);
+        }
+        if (leader) tc_commit(&s.empty[stage]);
+        __syncwarp();
+        ++loads;
+        return true;
+    };
+    auto next = [&] {  // the next unit with something to see
+        Unit u;
+        do u = next_unit(a, s, it);
+        while (u.blocks == 0);
+        return u;
+    };
+    Unit u = next();
+    if (u.blocks > 0) ok = start(u);
+    while (ok && u.blocks > 0) {
+        const int tiles = u.tokens > a.tile_tokens ? 2 : 1;
+        for (int j = 0; j < u.blocks && ok; ++j) {
+            const int v_stage = loads % kS;
+            const uint32_t v_round = (loads / kS) & 1;
+            ++loads;
+            const bool part = seen_in_part(u, u.blk0 + j), more = j + 1 < u.blocks;
+            const int k_stage = loads % kS;
+            const uint32_t k_round = (loads / kS) & 1;
+            ok = wait_on(kType == BD_KV_BF16 && part ? &s.fixed[v_stage] : &s.full[v_stage], v_round, a, s.abort);
+            const bool slow = ok && part && s.slow[v_stage] == loads;  // its load's number from 1
+            for (int i = 0; i < tiles && ok; ++i) {
+                ok = wait_on(&s.p_full[i], p_n[i] & 1, a, s.abort);
+                if (!ok) break;
+                ++p_n[i];
+                tc_fence_after();
+                if (leader) {
+                    if (!slow) {
+                        const uint64_t vd = sw128_rows_desc(smem_kv + v_stage * kTileBytes<kDim>);
+                        const uint32_t p = tmem + (kDim == 128 ? i * kBlock : kP + i * (kBlock / 2));
+#pragma unroll
+                        for (int k = 0; k < kBlock / 16; ++k)
+                            tc_mma_f16_ts(tmem + kO + i * kDim, p + k * 8, vd + k * (16 * 128 / 16), idesc_o, j > 0 || k > 0);
+                    }
+                    tc_commit(&s.o_full[i]);
+                }
+                __syncwarp();
+                if (more) {
+                    if (i == 0) ok = wait_on(&s.full[k_stage], k_round, a, s.abort);
+                    if (!ok) break;
+                    scores(i, k_stage);
+                    if (j + 2 == u.blocks && leader) tc_commit(&s.q_empty[i]);
+                    __syncwarp();
+                }
+            }
+            if (!ok) break;
+            if (leader) {
+                tc_commit(&s.empty[v_stage]);
+                if (more) tc_commit(&s.empty[k_stage]);
+            }
+            __syncwarp();
+            if (more) ++loads;
+        }
+        if (!ok) break;
+        u = next();
+        if (u.blocks > 0) ok = start(u);
+    }
+    // no product may be in flight when tensor memory is freed, even after giving up
+    if (leader) {
+        tc_commit(s.o_full + 2);
+        mbar_wait(s.o_full + 2, 0, kDrainLimitNs, nullptr);
+    }
+    __syncwarp();
+}
+
+// ---- warp 10 and on: queries, keys and values ------------------------------------------------
+
+template <int kDim>
+__device__ __forceinline__ bool load_queries(const PromptArgs &a, const Smem &s, const CUtensorMap *map, uint32_t smem_q, const Unit &u, int (&q_n)[2]) {
+    const int tiles = u.tokens > a.tile_tokens ? 2 : 1;
+    for (int i = 0; i < tiles; ++i) {
+        if (!wait_on(&s.q_empty[i], (q_n[i] & 1) ^ 1, a, s.abort)) return false;
+        ++q_n[i];
+        if (threadIdx.x % 32 == 0) {
+            mbar_arrive_expect_tx(&s.q_full[i], a.heads_tile * a.tile_tokens * kDim * 2);
+            const int head = u.vh / a.subs * a.group + u.vh % a.subs * a.heads_tile;
+            for (int c = 0; c < kDim / 64; ++c)
+                tma_load_3d(smem_q + i * kTileBytes<kDim> + c * (kTileRows * 128), map, &s.q_full[i], c * 64, head, u.row0 + i * a.tile_tokens);
+        }
+        __syncwarp();
+    }
+    return true;
+}
+
+__device__ __forceinline__ void drain_queries(const Smem &s, const int (&q_n)[2]) {
+    for (int i = 0; i < 2; ++i)
+        if (q_n[i] > 0) mbar_wait(&s.q_full[i], (q_n[i] - 1) & 1, kDrainLimitNs, nullptr);
+}
+
+// bf16: copies of `box` keys and 64 columns.  Lane l looks up piece l of a block and copies it; a piece that no row sees or
+// whose page id is out of range is zeroed.
+template <int kDim>
+__device__ __forceinline__ void load_tiles(const PromptArgs &a, const Smem &s, const CUtensorMap *map_q, const CUtensorMap *map_k,
+                                           const CUtensorMap *map_v, uint32_t smem_q, uint8_t *kv) {
+    constexpr int kS = kStages<kDim>;
+    const int lane = threadIdx.x % 32;
+    const int per_block = kBlock / a.box;
+    int it = 0, loads = 0, q_n[2] = {0, 0};
+    bool ok = true;
+    while (ok) {
+        const Unit u = next_unit(a, s, it);
+        if (u.blocks < 0) break;
+        if (u.blocks == 0) continue;
+        const int32_t *table = a.page_table + static_cast<int64_t>(u.seq) * a.max_pages;
+        const int kvh = u.vh / a.subs;
+        auto page_of = [&](int j) {  // of this lane's piece of block blk0 + j; -1: none
+            const int key = (u.blk0 + j) * kBlock + lane * a.box;
+            if (lane >= per_block || j >= u.blocks || key >= u.un_hi || key + a.box <= u.un_lo) return -1;
+            const int at = key / a.page_size;
+            if (!in_bounds(at >= 0 && at < a.max_pages, a.status)) return -1;
+            const int32_t page = table[at];
+            if (page < 0 || page >= a.n_pages) {
+                flag_status(a.status, kDevBadIndex);
+                return -1;
+            }
+            return page;
+        };
+        int page = page_of(0);
+        if (!load_queries<kDim>(a, s, map_q, smem_q, u, q_n)) break;
+        for (int j = 0; j < u.blocks && ok; ++j) {
+            const int next_page = page_of(j + 1);
+            const int key = (u.blk0 + j) * kBlock + lane * a.box;
+            const unsigned there = __ballot_sync(0xFFFFFFFFu, page >= 0);
+            for (int w = 0; w < 2; ++w, ++loads) {
+                const int stage = loads % kS;
+                if (!wait_on(&s.empty[stage], ((loads / kS) & 1) ^ 1, a, s.abort)) {
+                    ok = false;
+                    break;
+                }
+                uint8_t *dst = kv + stage * kTileBytes<kDim>;
+                if (there != (per_block == 32 ? 0xFFFFFFFFu : (1u << per_block) - 1)) {
+                    for (int p = 0; p < per_block; ++p)
+                        if (!(there >> p & 1))
+                            for (int i = lane; i < a.box * (kDim / 8); i += 32)
+                                *reinterpret_cast<uint4 *>(dst + tile_at(p * a.box + i / (kDim / 8), i % (kDim / 8))) = make_uint4(0, 0, 0, 0);
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                }
+                if (lane == 0) mbar_arrive_expect_tx(&s.full[stage], __popc(there) * a.box * kDim * 2);
+                __syncwarp();
+                if (page >= 0)
+                    for (int c = 0; c < kDim / 64; ++c)
+                        tma_load_3d(smem_u32(dst) + c * (kBlock * 128) + lane * a.box * 128, w ? map_v : map_k, &s.full[stage], c * 64,
+                                    kvh * a.page_size + key % a.page_size, page);
+                __syncwarp();
+            }
+            page = next_page;
+        }
+    }
+    // copies in flight have to land before the CTA ends, also when another role gave up
+    for (int l = loads > kS ? loads - kS : 0; l < loads; ++l) mbar_wait(&s.full[l % kS], (l / kS) & 1, kDrainLimitNs, nullptr);
+    drain_queries(s, q_n);
+}
+
+// Warp 11: V of blocks that some row sees in part.
+template <int kDim>
+__device__ __forceinline__ void look_at_values(const PromptArgs &a, const Smem &s, uint8_t *kv) {
+    constexpr int kS = kStages<kDim>;
+    const int lane = threadIdx.x % 32;
+    int it = 0, loads = 0;
+    while (true) {
+        const Unit u = next_unit(a, s, it);
+        if (u.blocks < 0) return;
+        for (int l = 0; l < 2 * u.blocks; ++l, ++loads) {
+            const int stage = loads % kS, blk = u.blk0 + l / 2;
+            if (!wait_on(&s.full[stage], (loads / kS) & 1, a, s.abort)) return;
+            if (l % 2 && seen_in_part(u, blk)) {
+                uint8_t *tile = kv + stage * kTileBytes<kDim>;
+                bool bad = false;
+#pragma unroll 8
+                for (int i = lane; i < kBlock * (kDim / 8); i += 32) {
+                    uint4 *p = reinterpret_cast<uint4 *>(tile + tile_at(i / (kDim / 8), i % (kDim / 8)));
+                    const int key = blk * kBlock + i / (kDim / 8);
+                    if (key < u.un_lo || key >= u.un_hi) *p = make_uint4(0, 0, 0, 0);
+                    else bad |= not_finite(*p);
+                }
+                fence_proxy_async_smem();
+                bad = __any_sync(0xFFFFFFFFu, bad);
+                if (bad && lane == 0) s.slow[stage] = loads + 1;
+            }
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(&s.fixed[stage]);
+                mbar_arrive(&s.empty[stage]);
+            }
+        }
+    }
+}
+
+// 8 and 4 bits: raw values are read a tile ahead, 16 bytes at a time, and written as the bf16 numbers that they stand for.
+template <int kDim, int kType>
+__device__ __forceinline__ void convert_tiles(const PromptArgs &a, const Smem &s, const CUtensorMap *map_q, uint32_t smem_q, uint8_t *kv, int (&q_n)[2]) {
+    constexpr int kS = kStages<kDim>;
+    constexpr int kRow = kType == BD_KV_E4M3 ? kDim : kDim / 2;  // bytes of a key
+    constexpr int kScale = kType == BD_KV_E4M3 ? 1 : kDim / 16;
+    constexpr int kPer = kRow / 16;                              // 16-byte pieces of a key
+    constexpr int kThreads = kConvertWarps * 32;
+    constexpr int kEach = (kBlock * kPer + kThreads - 1) / kThreads;
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32 - 10, tid = threadIdx.x - 320;
+    int it = 0, loads = 0;
+    while (true) {
+        const Unit u = next_unit(a, s, it);
+        if (u.blocks < 0) return;
+        if (u.blocks == 0) continue;
+        if (warp == 0 && !load_queries<kDim>(a, s, map_q, smem_q, u, q_n)) return;
+        const int32_t *table = a.page_table + static_cast<int64_t>(u.seq) * a.max_pages;
+        const int kvh = u.vh / a.subs;
+        int32_t page[kEach];  // of this thread's pieces of a block; -1: none
+        auto pages_of = [&](int j) {
+#pragma unroll
+            for (int e = 0; e < kEach; ++e) {
+                const int i = tid + e * kThreads, key = (u.blk0 + j) * kBlock + i / kPer;
+                page[e] = -1;
+                if (i >= kBlock * kPer || j >= u.blocks || key < u.un_lo || key >= u.un_hi) continue;
+                const int at = key / a.page_size;
+                if (in_bounds(at >= 0 && at < a.max_pages, a.status)) page[e] = table[at];
+            }
+        };
+        uint4 raw[kEach];
+        uint32_t scale[kEach];
+        auto fetch = [&](int j, bool v) {
+#pragma unroll
+            for (int e = 0; e < kEach; ++e) {
+                const int i = tid + e * kThreads, key = (u.blk0 + j) * kBlock + i / kPer;
+                raw[e] = make_uint4(0, 0, 0, 0);
+                scale[e] = 0;
+                if (page[e] < 0 || page[e] >= a.n_pages) {
+                    if (i < kBlock * kPer && j < u.blocks && key >= u.un_lo && key < u.un_hi) flag_status(a.status, kDevBadIndex);
+                    continue;
+                }
+                const int64_t row = (static_cast<int64_t>(page[e]) * a.kv_heads + kvh) * a.page_size + key % a.page_size;
+                if (!in_bounds(row < a.n_pages * a.kv_heads * a.page_size, a.status)) continue;
+                raw[e] = __ldg(reinterpret_cast<const uint4 *>((v ? a.cv : a.ck) + row * kRow) + i % kPer);
+                const uint8_t *sc = (v ? a.cv_scale : a.ck_scale) + row * kScale;
+                scale[e] = kType == BD_KV_E4M3 ? __ldg(sc) : __ldg(reinterpret_cast<const uint16_t *>(sc) + i % kPer);
+            }
+        };
+        pages_of(0);
+        fetch(0, false);
+        for (int j = 0; j < u.blocks; ++j)
+            for (int w = 0; w < 2; ++w, ++loads) {
+                const int stage = loads % kS;
+                if (!wait_on(&s.empty[stage], ((loads / kS) & 1) ^ 1, a, s.abort)) return;
+                uint8_t *tile = kv + stage * kTileBytes<kDim>;
+                const bool look = w && seen_in_part(u, u.blk0 + j);
+                bool bad = false;
+#pragma unroll
+                for (int e = 0; e < kEach; ++e) {
+                    const int i = tid + e * kThreads;
+                    if (i >= kBlock * kPer) continue;
+                    constexpr int kOut = kType == BD_KV_E4M3 ? 2 : 4;  // 16-byte pieces written
+                    const uint32_t in[4] = {raw[e].x, raw[e].y, raw[e].z, raw[e].w};
+#pragma unroll
+                    for (int o = 0; o < kOut; ++o) {
+                        float f[8];
+                        if constexpr (kType == BD_KV_E4M3) {
+                            const float sc = __uint_as_float(scale[e] << 23);
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(in[2 * o + k / 2] >> k % 2 * 16 & 0xFFFFu), __NV_E4M3);
+                                const float2 x = __half22float2(__half2(h));
+                                f[2 * k] = x.x * sc, f[2 * k + 1] = x.y * sc;
+                            }
+                        } else {
+                            const float sc = __half2float(__ushort_as_half(static_cast<unsigned short>((scale[e] >> o / 2 * 8 & 0xFFu) << 7)));
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                const __half2_raw h = __nv_cvt_fp4x2_to_halfraw2(static_cast<__nv_fp4x2_storage_t>(in[o] >> k * 8 & 0xFFu), __NV_E2M1);
+                                const float2 x = __half22float2(__half2(h));
+                                f[2 * k] = x.x * sc, f[2 * k + 1] = x.y * sc;
+                            }
+                        }
+                        const uint4 y = pack8(f);
+                        if (look) bad |= not_finite(y);
+                        *reinterpret_cast<uint4 *>(tile + tile_at(i / kPer, i % kPer * kOut + o)) = y;
+                    }
+                }
+                // the next tile's values are under way while this one is used
+                if (w) pages_of(j + 1);
+                if (!w || j + 1 < u.blocks) fetch(w ? j + 1 : j, !w);
+                if (bad) s.slow[stage] = loads + 1;
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&s.full[stage]);
+            }
+    }
+}
+
+// ---- warps 0 to 7: softmax ----------------------------------------------------------------
+
+__device__ __forceinline__ void tmem_ld_x16(uint32_t taddr, uint32_t (&o)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(o[0]), "=r"(o[1]), "=r"(o[2]), "=r"(o[3]), "=r"(o[4]), "=r"(o[5]), "=r"(o[6]), "=r"(o[7]), "=r"(o[8]), "=r"(o[9]),
+          "=r"(o[10]), "=r"(o[11]), "=r"(o[12]), "=r"(o[13]), "=r"(o[14]), "=r"(o[15])
+        : "r"(taddr));
+}
+
+// A product's score in base 2 under the rule: `far` positions before the query.
+__device__ __forceinline__ float ruled(const PromptArgs &a, float v, float slope, float far) {
+    v *= a.scale_log2;
+    if (a.cap > 0.f) v = a.cap * (1.f - __fdividef(2.f, 1.f + ex2(v * a.cap_in)));
+    return fmaf(-slope, fabsf(far), v);
+}
+
+// The rows' output so far, times f.  Seldom run: apart, so that its registers are not the loop's.
+template <int kDim>
+__device__ __noinline__ void scale_output(uint32_t t_o, float f) {
+#pragma unroll 1
+    for (int c = 0; c < kDim; c += 16) {
+        uint32_t o[16];
+        tmem_ld_x16(t_o + c, o);
+        tmem_ld_wait();
+#pragma unroll
+        for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+        tmem_st_32x32b_x16(t_o + c, o);
+    }
+    tmem_st_wait();
+}
+
+// P V of a block whose V is not finite where some row does not see it: row by row over the keys [from, to) that the row
+// sees.  The scores are read again one by one from tensor memory.
+template <int kDim>
+__device__ __noinline__ void add_values(const PromptArgs &a, uint32_t t_s, uint32_t t_o, const uint8_t *v, bool fresh, int from, int to,
+                                        unsigned missing, float base, float slope, float far) {
+#pragma unroll 1
+    for (int c = 0; c < kDim; c += 16) {
+        uint32_t o[16] = {};
+        if (!fresh) tmem_ld_x16(t_o + c, o);
+        tmem_ld_wait();
+#pragma unroll 1
+        for (int k = 0; k < kBlock; ++k) {
+            const float score = ruled(a, tmem_ld_one(t_s + k), slope, far - static_cast<float>(k));
+            if (k >= from && k < to && !(missing >> k / 16 & 1)) {
+                const float w = ex2(score - base);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    float f[8];
+                    unpack8(*reinterpret_cast<const uint4 *>(v + tile_at(k, c / 8 + h)), f);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) o[8 * h + i] = __float_as_uint(fmaf(w, f[i], __uint_as_float(o[8 * h + i])));
+                }
+            }
+            __syncwarp();
+        }
+        tmem_st_32x32b_x16(t_o + c, o);
+    }
+    tmem_st_wait();
+}
+
+// Which of a block's 8 pieces of 16 keys have a page id out of range.
+__device__ __noinline__ unsigned missing_pieces(const PromptArgs &a, const Unit &u, int blk) {
+    const int lane = threadIdx.x % 32, key = blk * kBlock + lane * 16;
+    bool fine = true;
+    if (lane < 8 && key < u.un_hi && key + 16 > u.un_lo) {
+        const int at = key / a.page_size;
+        fine = false;
+        if (in_bounds(at >= 0 && at < a.max_pages, a.status)) {
+            const int32_t page = a.page_table[static_cast<int64_t>(u.seq) * a.max_pages + at];
+            fine = page >= 0 && page < a.n_pages;
+        }
+    }
+    return ~__ballot_sync(0xFFFFFFFFu, fine) & 0xFFu;
+}
+
+template <int kDim, int kType>
+__device__ __forceinline__ void softmax_rows(const PromptArgs &a, const Smem &s, uint32_t tmem, const uint8_t *kv) {
+    constexpr int kS = kStages<kDim>;
+    const int tile = threadIdx.x / 128, r = threadIdx.x % 128, lane = threadIdx.x % 32;
+    const uint32_t lane_base = tmem + (static_cast<uint32_t>(r / 32 * 32) << 16);
+    const uint32_t t_s = lane_base + tile * kBlock, t_o = lane_base + 2 * kBlock + tile * kDim;
+    const uint32_t t_p = kDim == 128 ? t_s : lane_base + 2 * kBlock + 2 * kDim + tile * (kBlock / 2);
+    int s_n = 0, blocks_before = 0;
+    for (int it = 0;; ++it) {
+        if (!wait_on(&s.u_full[it & 1], (it >> 1) & 1, a, s.abort)) return;
+        const Unit &u = s.unit[it & 1];  // held until its rows are written
+        const int blocks = u.blocks;
+        if (blocks < 0) return;
+        const bool mine = tile == 0 || u.tokens > a.tile_tokens;
+        if (mine) {
+            // this thread's row
+            const int token = r / a.heads_tile, t = tile * a.tile_tokens + token;
+            const int head_in = u.vh % a.subs * a.heads_tile + r - token * a.heads_tile, head = u.vh / a.subs * a.group + head_in;
+            const int64_t row = static_cast<int64_t>(u.row0) + t;
+            const int p = u.pos0 + t;
+            const bool write = token < a.tile_tokens && t < u.tokens && head_in < a.group &&
+                               in_bounds(row >= 0 && row < a.total && head < a.q_heads, a.status);
+            int lo = 0, hi = INT_MAX;  // rows without a query see everything, to no effect
+            float slope = 0.f;
+            bool none = false;
+            if (write) {
+                hi = max(p + 1, u.prefix);
+                lo = a.window > 0 ? max(0, p - a.window + 1) : 0;
+                if (a.first) lo = max(lo, a.first[row]);
+                none = p < 0 || lo >= hi;
+                if (none) lo = 0, hi = INT_MAX;
+                if (a.slopes) slope = a.slopes[head] * 1.44269504088896f;
+            }
+            const int key_first = u.blk0 * kBlock, in_lo = u.in_lo, in_hi = u.in_hi;
+            const bool gaps = u.state & kGaps;
+            float top = -INFINITY, sum = 0.f;
+            for (int j = 0; j < blocks; ++j) {
+                const int key0 = key_first + j * kBlock;
+                if (!wait_on(&s.s_full[tile], s_n & 1, a, s.abort)) return;
+                tc_fence_after();
+                uint32_t x[4][32];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) tmem_ld_32x32b_x32(t_s + c * 32, x[c]);
+                tmem_ld_wait();
+                const float far = static_cast<float>(p - key0);
+                if (!a.plain) {
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            x[c][i] = __float_as_uint(ruled(a, __uint_as_float(x[c][i]), slope, far - static_cast<float>(c * 32 + i)));
+                }
+                const int from = lo - key0, to = hi - key0;
+                unsigned missing = 0;
+                if (gaps) missing = missing_pieces(a, u, key0 / kBlock);
+                if (__any_sync(0xFFFFFFFFu, from > 0 || to < kBlock) || missing) {
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) {
+                            const int k = c * 32 + i;
+                            if (k < from || k >= to || (missing >> k / 16 & 1)) x[c][i] = 0xFF800000u;  // -infinity
+                        }
+                }
+                const float scale = a.plain ? a.scale_log2 : 1.f;
+                float most[4];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    most[c] = __uint_as_float(x[c][0]);
+#pragma unroll
+                    for (int i = 1; i < 32; ++i) most[c] = fmaxf(most[c], __uint_as_float(x[c][i]));
+                }
+                const float now = fmaxf(fmaxf(most[0], most[1]), fmaxf(most[2], most[3])) * scale;
+                const bool raise = now > top + kLazy || (top == -INFINITY && now > top);
+                if (__any_sync(0xFFFFFFFFu, raise)) {
+                    float fix = 1.f;
+                    if (raise) {
+                        if (top != -INFINITY) fix = ex2(top - now), sum *= fix;
+                        top = now;
+                    }
+                    if (__any_sync(0xFFFFFFFFu, fix != 1.f)) {  // not in the first block, where nothing was held yet
+                        if (!wait_on(&s.o_full[tile], (s_n - 1) & 1, a, s.abort)) return;
+                        tc_fence_after();
+                        scale_output<kDim>(t_o, fix);
+                    }
+                }
+                const float base = top == -INFINITY ? 0.f : top;
+                if (key0 < in_lo || key0 + kBlock > in_hi) {  // some row sees it in part: is V finite where it is not seen?
+                    const int load = 2 * (blocks_before + j) + 1, stage = load % kS;
+                    if (!wait_on(kType == BD_KV_BF16 ? &s.fixed[stage] : &s.full[stage], (load / kS) & 1, a, s.abort)) return;
+                    if (s.slow[stage] == load + 1) {
+                        if (j > 0 && !wait_on(&s.o_full[tile], (s_n - 1) & 1, a, s.abort)) return;
+                        tc_fence_after();
+                        add_values<kDim>(a, t_s, t_o, kv + stage * kTileBytes<kDim>, j == 0, from, to, missing, base, slope, far);
+                    }
+                }
+                float add[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t w[16];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const float e0 = ex2(fmaf(__uint_as_float(x[c][2 * i]), scale, -base));
+                        const float e1 = ex2(fmaf(__uint_as_float(x[c][2 * i + 1]), scale, -base));
+                        add[i % 4] += e0 + e1;
+                        w[i] = pack_bf16x2(e0, e1);
+                    }
+                    tmem_st_32x32b_x16(t_p + c * 16, w);
+                }
+                sum += (add[0] + add[1]) + (add[2] + add[3]);
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&s.p_full[tile]);
+                ++s_n;
+            }
+            // the unit's rows
+            if (blocks > 0) {
+                if (!wait_on(&s.o_full[tile], (s_n - 1) & 1, a, s.abort)) return;
+                tc_fence_after();
+            }
+            const bool whole = u.slot < 0;
+            float *part = nullptr;
+            if (!whole && in_bounds(u.slot < a.slots, a.status)) part = a.parts + u.slot * kSlotFloats<kDim> + tile * (kTileRows * (kDim + 2));
+            if (none || blocks == 0) sum = 0.f, top = -INFINITY;
+            const bool empty = sum == 0.f;
+            const float inv = empty ? 0.f : 1.f / sum;
+            uint8_t *dst = a.out + (row * a.q_heads + head) * (kDim * 2);
+#pragma unroll 1
+            for (int c = 0; c < kDim; c += 32) {
+                uint32_t o[32];
+                if (blocks > 0) {
+                    tmem_ld_32x32b_x32(t_o + c, o);
+                    tmem_ld_wait();
+                }
+                if (empty)
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) o[i] = 0;
+                if (whole) {
+                    if (write)
+#pragma unroll
+                        for (int i = 0; i < 32; i += 8) {
+                            float f[8];
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) f[k] = __uint_as_float(o[i + k]) * inv;
+                            *reinterpret_cast<uint4 *>(dst + (c + i) * 2) = pack8(f);
+                        }
+                } else if (part) {  // columns in fours, each of all rows side by side
+#pragma unroll
+                    for (int i = 0; i < 32; i += 4)
+                        reinterpret_cast<uint4 *>(part)[(c + i) / 4 * kTileRows + r] = make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+                }
+            }
+            if (whole) {
+                if (write && a.lse) a.lse[row * a.q_heads + head] = empty ? -INFINITY : (top + log2f(sum)) * 0.693147180559945f;
+            } else if (part) {
+                part[kTileRows * kDim + r] = top;
+                part[kTileRows * (kDim + 1) + r] = sum;
+                if (threadIdx.x == 0 && (u.state & kFirstPiece)) a.heads[u.slot] = make_int4(u.parts, u.row0, u.tokens, u.vh);
+            }
+            tc_fence_before();  // the reads of O come before the next unit's first product
+        }
+        blocks_before += blocks;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s.u_empty[it & 1]);
+    }
+}
+
+template <int kDim, int kType>
+__global__ void __launch_bounds__(kThreadsOf<kType>, 1)
+    prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
+                  const __grid_constant__ CUtensorMap map_v, const __grid_constant__ PromptArgs a) {
+    constexpr int kS = kStages<kDim>;
+    constexpr bool kConvert = kType != BD_KV_BF16;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t *kv = smem + 2 * kTileBytes<kDim>;
+    uint64_t *bars = reinterpret_cast<uint64_t *>(kv + kS * kTileBytes<kDim>);
+    Smem s;
+    s.full = bars, s.empty = bars + kS, s.fixed = bars + 2 * kS;
+    bars += 3 * kS;
+    s.q_full = bars, s.q_empty = bars + 2, s.s_full = bars + 4, s.p_full = bars + 6, s.o_full = bars + 8;  // o_full[2]: the last products
+    s.u_full = bars + 11, s.u_empty = bars + 13;
+    s.unit = reinterpret_cast<Unit *>(bars + 16);
+    s.slow = reinterpret_cast<volatile int *>(s.unit + 2);
+    s.abort = s.slow + kS;
+    s.tmem = const_cast<uint32_t *>(reinterpret_cast<volatile uint32_t *>(s.abort + 1));
+    static_assert((3 * kS + 16) * 8 + 2 * sizeof(Unit) + (kS + 2) * 4 <= 1024);
+    const int warp = threadIdx.x / 32;
+    pdl_trigger_and_wait();
+    if (threadIdx.x == 0) {
+        // where units are split, CTA b takes unit b alone: its slot holds no unit's first piece yet
+        if (a.may_split && in_bounds(static_cast<int>(blockIdx.x) < a.slots, a.status)) a.heads[blockIdx.x] = make_int4(0, 0, 0, 0);
+        for (int i = 0; i < kS; ++i) {
+            mbar_init(&s.full[i], kConvert ? kConvertWarps : 1);
+            mbar_init(&s.empty[i], kConvert ? 1 : 2);  // the products that read it, and warp 11
+            mbar_init(&s.fixed[i], 1);
+            s.slow[i] = 0;
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&s.q_full[i], 1), mbar_init(&s.q_empty[i], 1);
+            mbar_init(&s.s_full[i], 1), mbar_init(&s.p_full[i], 4), mbar_init(&s.o_full[i], 1);
+            mbar_init(&s.u_full[i], 1), mbar_init(&s.u_empty[i], 9 + (kConvert ? kConvertWarps : 2));
+        }
+        mbar_init(&s.o_full[2], 1);
+        *s.abort = 0;
+        mbar_fence_init();
+        tma_prefetch_desc(&map_q);
+        if (!kConvert) tma_prefetch_desc(&map_k), tma_prefetch_desc(&map_v);
+    }
+    if (warp == 8) {
+        tmem_alloc(s.tmem, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *s.tmem;
+    // a softmax thread holds a row of 128 scores: 384 threads start with 168 registers each, 512 with 128
+    if (warp < 8) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kConvert ? 184 : 216));
+    else asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    if (warp < 8) {
+        softmax_rows<kDim, kType>(a, s, tmem, kv);
+    } else if (warp == 8) {
+        issue_products<kDim, kType>(a, s, tmem, smem_u32(smem), smem_u32(kv));
+    } else if (warp == 9) {
+        find_units(a, s);
+    } else if constexpr (kConvert) {
+        int q_n[2] = {0, 0};
+        convert_tiles<kDim, kType>(a, s, &map_q, smem_u32(smem), kv, q_n);
+        drain_queries(s, q_n);  // warp 10's copies in flight land before the CTA ends, also after giving up
+    } else if (warp == 10) {
+        load_tiles<kDim>(a, s, &map_q, &map_k, &map_v, smem_u32(smem), kv);
+    } else {
+        look_at_values<kDim>(a, s, kv);
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 8) tmem_dealloc(tmem, 512);
+}
+
+// ---- join of the pieces ---------------------------------------------------------------------
+
+constexpr int kJoinThreads = 256;
+constexpr int kJoinRows = 32;
+
+// A CTA per slot, tile and 32 rows; a thread has a row and an eighth of its columns.  Pieces of a unit are vheads slots apart.
+template <int kDim>
+__global__ void __launch_bounds__(kJoinThreads) prompt_join_kernel(const __grid_constant__ PromptArgs a) {
+    pdl_trigger_and_wait();
+    const int4 h = a.heads[blockIdx.x];
+    const int pieces = h.x, tile = blockIdx.y / (kTileRows / kJoinRows);
+    if (pieces < 1) return;
+    const int r = blockIdx.y % (kTileRows / kJoinRows) * kJoinRows + threadIdx.x % kJoinRows, eighth = threadIdx.x / kJoinRows;
+    const int vheads = a.kv_heads * a.subs;
+    const int token = r / a.heads_tile, t = tile * a.tile_tokens + token, head_in = h.w % a.subs * a.heads_tile + r - token * a.heads_tile;
+    if (token >= a.tile_tokens || t >= h.z || head_in >= a.group) return;
+    const int64_t row = static_cast<int64_t>(h.y) + t;
+    const int head = h.w / a.subs * a.group + head_in;
+    if (!in_bounds(row < a.total && head < a.q_heads && blockIdx.x + (pieces - 1) * vheads < a.slots, a.status)) return;
+    auto part = [&](int q) { return a.parts + (blockIdx.x + static_cast<int64_t>(q) * vheads) * kSlotFloats<kDim> + tile * (kTileRows * (kDim + 2)); };
+    float top = -INFINITY;
+    for (int q = 0; q < pieces; ++q) top = fmaxf(top, part(q)[kTileRows * kDim + r]);
+    const float base = top == -INFINITY ? 0.f : top;
+    float sum = 0.f;
+    float4 o[kDim / 32] = {};
+    for (int q = 0; q < pieces; ++q) {
+        const float *p = part(q);
+        const float f = ex2(p[kTileRows * kDim + r] - base);
+        sum = fmaf(p[kTileRows * (kDim + 1) + r], f, sum);
+#pragma unroll
+        for (int i = 0; i < kDim / 32; ++i) {
+            const float4 y = reinterpret_cast<const float4 *>(p)[(eighth * (kDim / 32) + i) * kTileRows + r];
+            o[i].x = fmaf(y.x, f, o[i].x), o[i].y = fmaf(y.y, f, o[i].y), o[i].z = fmaf(y.z, f, o[i].z), o[i].w = fmaf(y.w, f, o[i].w);
+        }
+    }
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    uint2 *dst = reinterpret_cast<uint2 *>(a.out + (row * a.q_heads + head) * (kDim * 2)) + eighth * (kDim / 32);
+#pragma unroll
+    for (int i = 0; i < kDim / 32; ++i)
+        dst[i] = make_uint2(pack_bf16x2(o[i].x * inv, o[i].y * inv), pack_bf16x2(o[i].z * inv, o[i].w * inv));
+    if (a.lse && eighth == 0) a.lse[row * a.q_heads + head] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.693147180559945f;
+}
+
+template <int kDim>
+size_t part_bytes(int num_sms) { return (static_cast<size_t>(num_sms) * kSlotFloats<kDim> * 4 + 255) / 256 * 256; }
+
+template <class... Types, class... Args>
+cudaError_t launch_pdl(void (*kernel)(Types...), dim3 grid, int threads, int smem, cudaStream_t stream, const Args &...args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+template <int kDim, int kType>
+cudaError_t launch_typed(const PromptArgs &a, const CUtensorMap &q, const CUtensorMap &k, const CUtensorMap &v, const DevCtx &ctx,
+                         cudaStream_t stream) {
+    cudaError_t e = allow_smem<prompt_kernel<kDim, kType>>(kSmemBytes<kDim>, ctx.device);
+    if (e != cudaSuccess) return e;
+    e = launch_pdl(prompt_kernel<kDim, kType>, dim3(ctx.num_sms), kThreadsOf<kType>, kSmemBytes<kDim>, stream, q, k, v, a);
+    if (e != cudaSuccess || !a.may_split) return e;
+    return launch_pdl(prompt_join_kernel<kDim>, dim3(a.slots, 2 * kTileRows / kJoinRows), kJoinThreads, 0, stream, a);
+}
+
+template <int kDim>
+cudaError_t launch_dim(const PromptArgs &a, int type, const CUtensorMap &q, const CUtensorMap &k, const CUtensorMap &v, const DevCtx &ctx,
+                       cudaStream_t stream) {
+    if (type == BD_KV_E4M3) return launch_typed<kDim, BD_KV_E4M3>(a, q, k, v, ctx, stream);
+    if (type == BD_KV_E2M1) return launch_typed<kDim, BD_KV_E2M1>(a, q, k, v, ctx, stream);
+    return launch_typed<kDim, BD_KV_BF16>(a, q, k, v, ctx, stream);
+}
+
+}  // namespace
+
+size_t prompt_workspace_size(int num_sms, int head_dim) {
+    return (head_dim == 128 ? part_bytes<128>(num_sms) : part_bytes<64>(num_sms)) + static_cast<size_t>(num_sms) * sizeof(int4);
+}
+
+cudaError_t launch_prompt(const bd_kv_cache &c, const void *q, int32_t q_heads, const int32_t *offsets, int64_t total,
+                          const int32_t *page_table, const int32_t *lengths, int32_t n_seqs, int32_t max_pages,
+                          const bd_score_rule &rule, void *out, float *lse, void *workspace, const DevCtx &ctx,
+                          cudaStream_t stream) {
+    constexpr float kLog2e = 1.44269504088896f;
+    PromptArgs a = {};
+    a.ck = static_cast<const uint8_t *>(c.k);
+    a.cv = static_cast<const uint8_t *>(c.v);
+    a.ck_scale = c.k_scale;
+    a.cv_scale = c.v_scale;
+    a.page_table = page_table;
+    a.offsets = offsets;
+    a.lengths = lengths;
+    a.first = rule.first;
+    a.prefix = rule.prefix;
+    a.slopes = rule.slopes;
+    a.out = static_cast<uint8_t *>(out);
+    a.lse = lse;
+    a.parts = static_cast<float *>(workspace);
+    a.heads = reinterpret_cast<int4 *>(static_cast<uint8_t *>(workspace) +
+                                       (c.head_dim == 128 ? part_bytes<128>(ctx.num_sms) : part_bytes<64>(ctx.num_sms)));
+    a.status = ctx.status;
+    a.wait_ns = ctx.wait_ns;
+    a.n_pages = c.n_pages;
+    a.total = total;
+    a.n_seqs = n_seqs;
+    a.max_pages = max_pages;
+    a.page_size = c.page_size;
+    a.kv_heads = c.kv_heads;
+    a.q_heads = q_heads;
+    a.group = q_heads / c.kv_heads;
+    a.subs = (a.group + kTileRows - 1) / kTileRows;
+    a.heads_tile = (a.group + a.subs - 1) / a.subs;
+    a.tile_tokens = kTileRows / a.heads_tile;
+    a.window = rule.window;
+    a.slots = ctx.num_sms;
+    a.box = 16;
+    while (a.box < kBlock && c.page_size % (2 * a.box) == 0) a.box *= 2;
+    a.scale_log2 = rule.scale * kLog2e;
+    a.cap = rule.cap * kLog2e;
+    a.cap_in = rule.cap > 0.f ? 2.f / rule.cap : 0.f;
+    a.plain = rule.scale > 0.f && !(rule.cap > 0.f) && !rule.slopes;
+    // the units are at least this many (offsets[n_seqs] = total): more than CTAs are not split
+    const int64_t units = (total + 2 * a.tile_tokens - 1) / (2 * a.tile_tokens) * c.kv_heads * a.subs;
+    a.may_split = units <= ctx.num_sms && max_pages * static_cast<int64_t>(c.page_size) > 4 * kBlock;
+    CUtensorMap map_q, map_k, map_v;
+    if (!encode_tensor_map_3d(&map_q, q, c.head_dim, q_heads, total, c.head_dim * 2, static_cast<uint64_t>(q_heads) * c.head_dim * 2,
+                              64, a.heads_tile, a.tile_tokens))
+        return cudaErrorInvalidValue;
+    map_k = map_v = map_q;
+    if (c.kv_type == BD_KV_BF16) {
+        const uint64_t rows = static_cast<uint64_t>(c.kv_heads) * c.page_size, page = rows * c.head_dim * 2;
+        if (!encode_tensor_map_3d(&map_k, c.k, c.head_dim, rows, c.n_pages, c.head_dim * 2, page, 64, a.box, 1) ||
+            !encode_tensor_map_3d(&map_v, c.v, c.head_dim, rows, c.n_pages, c.head_dim * 2, page, 64, a.box, 1))
+            return cudaErrorInvalidValue;
+    }
+    return c.head_dim == 128 ? launch_dim<128>(a, c.kv_type, map_q, map_k, map_v, ctx, stream)
+                             : launch_dim<64>(a, c.kv_type, map_q, map_k, map_v, ctx, stream);
+}
+
+}  // namespace bd

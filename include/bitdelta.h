@@ -446,6 +446,18 @@ int32_t bd_rmsnorm(const void *x, const void *residual, const void *weight, cons
  * nearest even, infinities to +-448, NaN kept.  A floating-point format loses
  * nothing to a power-of-two scale, x / s and q * s are exact, and q * s is a
  * bf16 number (infinite from 2^128), so reading back into bf16 rounds nothing.
+ *   BD_KV_E2M1  4-bit values, two to a byte (element 2i in the low half), pools
+ *               uint8 [n_pages, kv_heads, page_size, head_dim / 2], and a scale for
+ *               each 16 elements of a row, uint8 [n_pages, kv_heads, page_size,
+ *               head_dim / 16]: 5 bits of exponent and 3 of mantissa, bits 7 to 14
+ *               of an fp16 number (value 2^(b/8 - 15) (1 + b%8 / 8), or
+ *               b 2^-17 for b < 8)
+ * A group is quantised as it is written: s is the group's largest finite |x|
+ * over 6 (fp32), to the nearest number that a scale byte holds (ties to the
+ * even byte), at most 61440; q = e2m1(x / s) (fp32), to the nearest of 0,
+ * 0.5, 1, 1.5, 2, 3, 4, 6, ties to even codes, beyond 6 to 6; s = 0 gives zeros.
+ * e2m1 has no NaN: a group that holds one takes scale byte 255, which reads as
+ * NaN in all 16 places.  q * s is a bf16 number, so reading back rounds nothing.
  *
  * A page table of no entries (n_seqs or max_pages 0: nothing cached yet) may be NULL.
  *
@@ -454,11 +466,11 @@ int32_t bd_rmsnorm(const void *x, const void *residual, const void *weight, cons
  * the call only.
  * ------------------------------------------------------------------------ */
 #define BD_KV_MAX_HEADS 1024
-typedef enum bd_kv_type { BD_KV_BF16 = 0, BD_KV_E4M3 = 1 } bd_kv_type;
+typedef enum bd_kv_type { BD_KV_BF16 = 0, BD_KV_E4M3 = 1, BD_KV_E2M1 = 2 } bd_kv_type;
 typedef struct bd_kv_cache {
-    void *k;            /* [n_pages, kv_heads, page_size, head_dim] */
+    void *k;            /* [n_pages, kv_heads, page_size, head_dim]; BD_KV_E2M1: head_dim / 2 bytes */
     void *v;
-    uint8_t *k_scale;   /* [n_pages, kv_heads, page_size], BD_KV_E4M3 only */
+    uint8_t *k_scale;   /* BD_KV_E4M3 [n_pages, kv_heads, page_size]; BD_KV_E2M1 [.., head_dim / 16] */
     uint8_t *v_scale;
     int64_t n_pages;
     int32_t kv_heads;
@@ -497,6 +509,43 @@ int32_t bd_kv_append(const bd_kv_cache *cache, const void *q, int32_t q_heads, c
                      int64_t n_tokens, const int32_t *seq_ids, const int32_t *positions, const int32_t *page_table,
                      int32_t n_seqs, int32_t max_pages, const float *rope, int64_t rope_len, void *q_out,
                      void *stream);
+
+/* The same with the rotated part of a head and the places of its pairs given:
+ * the first rope_dim elements of each head are rotated (d = rope_dim / 2 above),
+ * the others are taken as they are.  BD_ROTARY_HALF pairs element i with d + i,
+ * BD_ROTARY_INTERLEAVED element 2i with 2i + 1 (c and s of pair i as above).
+ *   rope        float [rope_len, rope_dim] or NULL           (read)
+ * rope_dim: a multiple of 16, 16 .. head_dim (not looked at without rope). */
+typedef enum bd_rotary_layout { BD_ROTARY_HALF = 0, BD_ROTARY_INTERLEAVED = 1 } bd_rotary_layout;
+
+int32_t bd_kv_append_rotary(const bd_kv_cache *cache, const void *q, int32_t q_heads, const void *k, const void *v,
+                            int64_t n_tokens, const int32_t *seq_ids, const int32_t *positions,
+                            const int32_t *page_table, int32_t n_seqs, int32_t max_pages, const float *rope,
+                            int64_t rope_len, int32_t rope_dim, int32_t rope_layout, void *q_out, void *stream);
+
+/* ------------------------------------------------------------------------ *
+ * Table of rotary positions, scaled for contexts longer than a model's own
+ *
+ *   f_i = base^(-2i / dim), 0 <= i < dim / 2
+ *   g_i = clamp((original * f_i / 2 pi - low) / (high - low), 0, 1)
+ *   f'_i = f_i (g_i + (1 - g_i) / factor)
+ *   table[p, i] = amplitude * cos(p f'_i),  table[p, dim / 2 + i] = amplitude * sin(p f'_i)
+ * original * f_i / 2 pi is the number of turns that pair i makes over the
+ * original context: pairs of `high` turns and more keep their frequency, those
+ * of `low` and fewer are slowed down by `factor`.  original = 0 slows all of them
+ * (positions interpolated), factor = 1 none.  Angles are kept as whole numbers of
+ * 2^-64 turns, so that far positions are as exact as near ones: within 2^-22 of
+ * the amplitude for positions below 2^28.
+ *   table       float [positions, dim]                       (written)
+ * dim: even, 2 .. BD_ROTARY_MAX_DIM; rows of a dim that is a multiple of 8 are
+ * written in 16-byte pieces.  base > 0, factor > 0, original >= 0, high > low,
+ * all of them and all f'_i finite.  positions = 0 launches nothing.
+ * Errors: BD_ERR_INVALID_ARG, BD_ERR_UNSUPPORTED_SHAPE, BD_ERR_MISALIGNED,
+ *         BD_ERR_CUDA.
+ * ------------------------------------------------------------------------ */
+#define BD_ROTARY_MAX_DIM 256
+int32_t bd_rotary_table(float *table, int64_t positions, int32_t dim, double base, double factor, double original,
+                        double low, double high, double amplitude, void *stream);
 
 /* ------------------------------------------------------------------------ *
  * Cache read-back
@@ -556,6 +605,78 @@ size_t bd_attention_workspace_size(const bd_kv_cache *cache, int32_t n_seqs, int
 int32_t bd_attention_decode(const bd_kv_cache *cache, const void *q, int32_t q_heads, const int32_t *page_table,
                             const int32_t *lengths, int32_t n_seqs, int32_t max_pages, float scale, int32_t window,
                             void *out, float *lse, void *workspace, size_t workspace_bytes, void *stream);
+
+/* ------------------------------------------------------------------------ *
+ * Scores that are capped, biased by distance, or hidden by more masks
+ *
+ * What a query of position p and head h makes of its product with the key of
+ * position j:
+ *   x = scale * sum_d q[d] K_j[d];  cap > 0: x = cap * tanh(x / cap)
+ *   s = x - slopes[h] * |p - j|     (slopes NULL: s = x)
+ * and which positions it sees:
+ *   j <= p, or j < prefix[i] for its sequence i (a prefix that sees itself whole)
+ *   j > p - window                  (window > 0)
+ *   j >= first[.]                   (the start of its document; one number per
+ *                                    query, negative ones count as 0)
+ * A query that sees nothing gives zeros and lse = -inf.  Scores are fp32; the
+ * capped ones are within 2^-21 of cap.  Slopes are finite.
+ * ------------------------------------------------------------------------ */
+typedef struct bd_score_rule {
+    float scale;
+    float cap;              /* 0: none */
+    const float *slopes;    /* [q_heads] or NULL                         (read, device) */
+    const int32_t *first;   /* one per query (decode: [n_seqs]) or NULL  (read, device) */
+    const int32_t *prefix;  /* [n_seqs] or NULL                          (read, device) */
+    int32_t window;         /* 0: all positions */
+    int32_t reserved;       /* 0 */
+} bd_score_rule;
+
+/* bd_attention_decode with a score rule (read during the call only).  The
+ * query's position is lengths[i] - 1, so a prefix hides nothing from it and is
+ * not looked at.  Errors: as bd_attention_decode. */
+int32_t bd_attention_decode_scored(const bd_kv_cache *cache, const void *q, int32_t q_heads, const int32_t *page_table,
+                                   const int32_t *lengths, int32_t n_seqs, int32_t max_pages,
+                                   const bd_score_rule *rule, void *out, float *lse, void *workspace,
+                                   size_t workspace_bytes, void *stream);
+
+/* ------------------------------------------------------------------------ *
+ * Attention of prompts: several new tokens per sequence over its cached keys
+ *
+ * Rows offsets[i] .. offsets[i + 1] - 1 of q are the last tokens of sequence i,
+ * in order: n of them at positions lengths[i] - n .. lengths[i] - 1, their own
+ * keys in the cache already (bd_kv_append comes first).  out and lse as
+ * bd_attention_decode gives them, with what the rule says; rule->first has
+ * `total` entries.  Rows from offsets[n_seqs] up to total are left as they are.
+ * Positions that no query of a sequence sees are not read into the result
+ * whatever they hold, and a value that a query does not see has no effect on
+ * its row, infinities and NaN included.
+ *
+ * Scores, softmax statistics and the output's sums are fp32.  The softmax
+ * weights enter V's product as bf16 (2^-8 of a weight at most); K and V of an 8-bit or
+ * 4-bit cache are multiplied as the bf16 numbers that they stand for.
+ *
+ *   q           bf16 [total, q_heads, head_dim]           (read)
+ *   offsets     int32 [n_seqs + 1], ascending from 0      (read)
+ *   page_table  int32 [n_seqs, max_pages]                 (read)
+ *   lengths     int32 [n_seqs]                            (read)
+ *   out         bf16 [total, q_heads, head_dim]           (written; not q)
+ *   lse         float [total, q_heads] or NULL            (written)
+ *   workspace   as for bd_attention_decode, of
+ *               bd_attention_prompt_workspace_size bytes
+ * A length below 0 or beyond max_pages * page_size or 2^30, more rows than the
+ * length, offsets that descend or pass total, or a page id out of range sets
+ * BD_ERR_BAD_INDEX: the length counts as the nearest allowed one, rows before
+ * position 0 see nothing, rows out of order are left out, and the keys of such a
+ * page count as unseen.
+ * Results do not depend on timing.
+ * Errors: as bd_attention_decode.
+ * ------------------------------------------------------------------------ */
+size_t bd_attention_prompt_workspace_size(const bd_kv_cache *cache, int32_t q_heads);
+
+int32_t bd_attention_prompt(const bd_kv_cache *cache, const void *q, int32_t q_heads, const int32_t *offsets,
+                            int64_t total, const int32_t *page_table, const int32_t *lengths, int32_t n_seqs,
+                            int32_t max_pages, const bd_score_rule *rule, void *out, float *lse, void *workspace,
+                            size_t workspace_bytes, void *stream);
 
 /* ------------------------------------------------------------------------ *
  * Draw of the next token, each row with its own settings
