@@ -25,6 +25,8 @@
 #include <cuda_fp4.h>
 #include <cuda_fp8.h>
 
+#include <type_traits>
+
 #include "bd_device.cuh"
 #include "bd_internal.h"
 #include "bd_rows.cuh"
@@ -84,6 +86,31 @@ __device__ __forceinline__ float ex2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+__device__ __forceinline__ uint64_t bits_of(float2 v) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(v.x), "f"(v.y));
+    return r;
+}
+__device__ __forceinline__ float2 pair_of(uint64_t v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ float2 fma2(float2 x, float2 y, float2 z) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(bits_of(x)), "l"(bits_of(y)), "l"(bits_of(z)));
+    return pair_of(r);
+}
+__device__ __forceinline__ float2 add2(float2 x, float2 y) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits_of(x)), "l"(bits_of(y)));
+    return pair_of(r);
+}
+__device__ __forceinline__ float max3(float x, float y, float z) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(y), "f"(z));
+    return r;
+}
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map, uint64_t *bar, int c0, int c1, int c2) {
     asm volatile(
         "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
@@ -115,6 +142,14 @@ __device__ __forceinline__ bool not_finite(uint4 v) {  // of eight bf16 numbers
     return two(v.x) || two(v.y) || two(v.z) || two(v.w);
 }
 
+// One lane of a converged warp.  (A branch on the lane's number instead costs about 150 clocks for each product issued:
+// the compiler does not see that one thread runs it, and the operands' descriptors have to be uniform.)
+__device__ __forceinline__ bool elect_one() {
+    uint32_t on;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(on));
+    return on != 0;
+}
+
 struct Smem {
     uint64_t *full, *empty, *fixed;      // per stage
     uint64_t *q_full, *q_empty, *s_full, *p_full, *o_full;  // per tile
@@ -127,7 +162,17 @@ struct Smem {
 
 // Bounded wait of a warp; on give-up the status word and the other roles are told.
 __device__ __forceinline__ bool wait_on(uint64_t *bar, uint32_t parity, const PromptArgs &a, volatile int *abort) {
-    const bool ok = mbar_wait(bar, parity, a.wait_ns, abort);
+    bool ok = mbar_try_wait(bar, parity);
+    if (!ok && a.wait_ns != 0) {
+        // the clock and the flag are looked at seldom: reading them takes longer than the wait is mostly over by
+        uint64_t begin = 0;
+        for (int polls = 1; !(ok = mbar_try_wait(bar, parity)); ++polls) {
+            if (polls % 64) continue;
+            const uint64_t now = globaltimer_ns();
+            if (begin == 0) begin = now;
+            if (*abort != 0 || now - begin > a.wait_ns) break;
+        }
+    }
     if (__all_sync(0xFFFFFFFFu, ok)) return true;
     if (threadIdx.x % 32 == 0) {
         *abort = 1;
@@ -315,100 +360,135 @@ __device__ __forceinline__ bool seen_in_part(const Unit &u, int blk) { return bl
 
 // ---- warp 8: products --------------------------------------------------------------------
 
-template <int kDim, int kType>
-__device__ __forceinline__ void issue_products(const PromptArgs &a, const Smem &s, uint32_t tmem, uint32_t smem_q, uint32_t smem_kv) {
-    constexpr int kS = kStages<kDim>;
-    constexpr uint32_t kO = 2 * kBlock, kP = kDim == 128 ? 0 : 2 * kBlock + 2 * kDim;  // columns of O; of P where it is not in S's place
-    constexpr uint32_t idesc_s = idesc_bf16_f32(kTileRows, kBlock), idesc_o = idesc_bf16_f32(kTileRows, kDim) | 1u << 16;  // V: rows are keys
-    const bool leader = threadIdx.x % 32 == 0;
-    int it = 0, loads = 0;  // K and V tiles used so far
-    int q_n[2] = {0, 0}, p_n[2] = {0, 0};
-    bool ok = true;
-    auto scores = [&](int i, int stage) {  // S of tile i
-        if (leader) {
-            const uint64_t qd = sw128_kmajor_desc(smem_q + i * kTileBytes<kDim>), kd = sw128_kmajor_desc(smem_kv + stage * kTileBytes<kDim>);
+extern __shared__ uint8_t smem_raw[];
+__device__ __forceinline__ uint32_t smem_base() { return (smem_u32(smem_raw) + 1023u) & ~1023u; }
+
+// Tensor memory is allocated whole, so its columns are counted from 0: S of the tiles, O of the tiles, and at head_dim 64
+// the weights P, which at head_dim 128 take S's place (products of one shape run in the order they are issued in).
+template <int kDim>
+struct Columns {
+    static constexpr uint32_t s = 0, o = 2 * kBlock, p = kDim == 128 ? 0 : 2 * kBlock + 2 * kDim, p_tile = kDim == 128 ? kBlock : kBlock / 2;
+};
+
+// S of a tile: Q K^T.
+template <int kDim, int kTile>
+__device__ __forceinline__ void issue_scores(int stage) {
+    constexpr uint32_t idesc = idesc_bf16_f32(kTileRows, kBlock);
+    const uint64_t q = sw128_kmajor_desc(smem_base() + kTile * kTileBytes<kDim>);
+    const uint64_t k = sw128_kmajor_desc(smem_base() + (2 + stage) * kTileBytes<kDim>);
 #pragma unroll
-            for (int k = 0; k < kDim / 16; ++k) {
-                const uint32_t at = k / 4 * (kBlock * 128 / 16) + k % 4 * 2;
-                tc_mma_f16_ss(tmem + i * kBlock, qd + at, kd + at, idesc_s, k > 0);
-            }
-            tc_commit(&s.s_full[i]);
+    for (int i = 0; i < kDim / 16; ++i) {
+        const uint32_t at = i / 4 * (kBlock * 128 / 16) + i % 4 * 2;
+        tc_mma_f16_ss(Columns<kDim>::s + kTile * kBlock, q + at, k + at, idesc, i > 0);
+    }
+}
+// Half of a tile's P V.
+template <int kDim, int kTile, int kHalf>
+__device__ __forceinline__ void issue_values(int stage, uint32_t accumulate) {
+    constexpr uint32_t idesc = idesc_bf16_f32(kTileRows, kDim) | 1u << 16;  // V's rows are keys
+    const uint64_t v = sw128_rows_desc(smem_base() + (2 + stage) * kTileBytes<kDim>);
+#pragma unroll
+    for (int i = kHalf * (kBlock / 32); i < (kHalf + 1) * (kBlock / 32); ++i)
+        tc_mma_f16_ts(Columns<kDim>::o + kTile * kDim, Columns<kDim>::p + kTile * Columns<kDim>::p_tile + i * 8, v + i * (16 * 128 / 16), idesc,
+                      i > 0 ? 1u : accumulate);
+}
+
+template <int kDim, int kType>
+__device__ __forceinline__ void issue_products(const PromptArgs &a, const Smem &s) {
+    constexpr int kS = kStages<kDim>;
+    int it = 0, p_n[2] = {0, 0}, q_n[2] = {0, 0};
+    int stage = 0;
+    uint32_t round = 0;  // of the next K or V tile
+    int loads = 0;
+    bool ok = true;
+    auto advance = [&] {
+        ++loads;
+        if (++stage == kS) stage = 0, round ^= 1;
+    };
+    auto scores = [&](auto tile, int at) {
+        if (elect_one()) {
+            issue_scores<kDim, tile()>(at);
+            tc_commit(&s.s_full[tile()]);
         }
         __syncwarp();
     };
+    std::integral_constant<int, 0> first;
+    std::integral_constant<int, 1> second;
+    auto start_tile = [&](auto tile, const Unit &u) {
+        if (!wait_on(&s.q_full[tile()], q_n[tile()] & 1, a, s.abort)) return false;
+        ++q_n[tile()];
+        tc_fence_after();
+        scores(tile, stage);
+        if (u.blocks == 1 && elect_one()) tc_commit(&s.q_empty[tile()]);
+        return true;
+    };
     auto start = [&](const Unit &u) {  // scores of a unit's first block
-        const int stage = loads % kS;
-        const int tiles = u.tokens > a.tile_tokens ? 2 : 1;
-        if (!wait_on(&s.full[stage], (loads / kS) & 1, a, s.abort)) return false;
-        for (int i = 0; i < tiles; ++i) {
-            if (!wait_on(&s.q_full[i], q_n[i] & 1, a, s.abort)) return false;
-            ++q_n[i];
-            tc_fence_after();
-            scores(i, stage);
-            if (u.blocks == 1 && leader) tc_commit(&s.q_empty[i]);
-        }
-        if (leader) tc_commit(&s.empty[stage]);
+        if (!wait_on(&s.full[stage], round, a, s.abort)) return false;
+        if (!start_tile(first, u)) return false;
+        if (u.tokens > a.tile_tokens && !start_tile(second, u)) return false;
+        if (elect_one()) tc_commit(&s.empty[stage]);
         __syncwarp();
-        ++loads;
+        advance();
         return true;
     };
     auto next = [&] {  // the next unit with something to see
         Unit u;
         do u = next_unit(a, s, it);
         while (u.blocks == 0);
+        // from lane 0: what the loops below run by is the same in all lanes
+        u.blocks = __shfl_sync(0xFFFFFFFFu, u.blocks, 0), u.tokens = __shfl_sync(0xFFFFFFFFu, u.tokens, 0);
+        u.blk0 = __shfl_sync(0xFFFFFFFFu, u.blk0, 0);
+        u.in_lo = __shfl_sync(0xFFFFFFFFu, u.in_lo, 0), u.in_hi = __shfl_sync(0xFFFFFFFFu, u.in_hi, 0);
         return u;
     };
     Unit u = next();
     if (u.blocks > 0) ok = start(u);
     while (ok && u.blocks > 0) {
-        const int tiles = u.tokens > a.tile_tokens ? 2 : 1;
+        const bool both = u.tokens > a.tile_tokens;
         for (int j = 0; j < u.blocks && ok; ++j) {
-            const int v_stage = loads % kS;
-            const uint32_t v_round = (loads / kS) & 1;
-            ++loads;
+            const int v_stage = stage;
+            const uint32_t v_round = round;
+            advance();
             const bool part = seen_in_part(u, u.blk0 + j), more = j + 1 < u.blocks;
-            const int k_stage = loads % kS;
-            const uint32_t k_round = (loads / kS) & 1;
             ok = wait_on(kType == BD_KV_BF16 && part ? &s.fixed[v_stage] : &s.full[v_stage], v_round, a, s.abort);
-            const bool slow = ok && part && s.slow[v_stage] == loads;  // its load's number from 1
-            for (int i = 0; i < tiles && ok; ++i) {
-                ok = wait_on(&s.p_full[i], p_n[i] & 1, a, s.abort);
-                if (!ok) break;
-                ++p_n[i];
+            const bool slow = ok && part && __any_sync(0xFFFFFFFFu, s.slow[v_stage] == loads);  // its load's number from 1
+            auto tile_products = [&](auto tile) {
+                constexpr int i = tile();
+                if (!wait_on(&s.p_full[2 * i], p_n[i] & 1, a, s.abort)) return false;
                 tc_fence_after();
-                if (leader) {
-                    if (!slow) {
-                        const uint64_t vd = sw128_rows_desc(smem_kv + v_stage * kTileBytes<kDim>);
-                        const uint32_t p = tmem + (kDim == 128 ? i * kBlock : kP + i * (kBlock / 2));
-#pragma unroll
-                        for (int k = 0; k < kBlock / 16; ++k)
-                            tc_mma_f16_ts(tmem + kO + i * kDim, p + k * 8, vd + k * (16 * 128 / 16), idesc_o, j > 0 || k > 0);
-                    }
+                if (!slow && elect_one()) issue_values<kDim, i, 0>(v_stage, j > 0);
+                __syncwarp();
+                if (!wait_on(&s.p_full[2 * i + 1], p_n[i] & 1, a, s.abort)) return false;
+                tc_fence_after();
+                ++p_n[i];
+                if (elect_one()) {
+                    if (!slow) issue_values<kDim, i, 1>(v_stage, 1);
                     tc_commit(&s.o_full[i]);
                 }
                 __syncwarp();
                 if (more) {
-                    if (i == 0) ok = wait_on(&s.full[k_stage], k_round, a, s.abort);
-                    if (!ok) break;
-                    scores(i, k_stage);
-                    if (j + 2 == u.blocks && leader) tc_commit(&s.q_empty[i]);
+                    if (i == 0 && !wait_on(&s.full[stage], round, a, s.abort)) return false;
+                    scores(tile, stage);
+                    if (j + 2 == u.blocks && elect_one()) tc_commit(&s.q_empty[i]);
                     __syncwarp();
                 }
-            }
+                return true;
+            };
+            ok = ok && tile_products(first) && (!both || tile_products(second));
             if (!ok) break;
-            if (leader) {
+            if (elect_one()) {
                 tc_commit(&s.empty[v_stage]);
-                if (more) tc_commit(&s.empty[k_stage]);
+                if (more) tc_commit(&s.empty[stage]);
             }
             __syncwarp();
-            if (more) ++loads;
+            if (more) advance();
         }
         if (!ok) break;
         u = next();
         if (u.blocks > 0) ok = start(u);
     }
     // no product may be in flight when tensor memory is freed, even after giving up
-    if (leader) {
+    if (elect_one()) {
         tc_commit(s.o_full + 2);
         mbar_wait(s.o_full + 2, 0, kDrainLimitNs, nullptr);
     }
@@ -785,7 +865,8 @@ __device__ __forceinline__ void softmax_rows(const PromptArgs &a, const Smem &s,
                 for (int c = 0; c < 4; ++c) {
                     most[c] = __uint_as_float(x[c][0]);
 #pragma unroll
-                    for (int i = 1; i < 32; ++i) most[c] = fmaxf(most[c], __uint_as_float(x[c][i]));
+                    for (int i = 1; i < 31; i += 2) most[c] = max3(most[c], __uint_as_float(x[c][i]), __uint_as_float(x[c][i + 1]));
+                    most[c] = fmaxf(most[c], __uint_as_float(x[c][31]));
                 }
                 const float now = fmaxf(fmaxf(most[0], most[1]), fmaxf(most[2], most[3])) * scale;
                 const bool raise = now > top + kLazy || (top == -INFINITY && now > top);
@@ -811,24 +892,27 @@ __device__ __forceinline__ void softmax_rows(const PromptArgs &a, const Smem &s,
                         add_values<kDim>(a, t_s, t_o, kv + stage * kTileBytes<kDim>, j == 0, from, to, missing, base, slope, far);
                     }
                 }
-                float add[4] = {0.f, 0.f, 0.f, 0.f};
+                float2 add[2] = {};
+                const float2 scale2 = make_float2(scale, scale), base2 = make_float2(-base, -base);
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
                     uint32_t w[16];
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
-                        const float e0 = ex2(fmaf(__uint_as_float(x[c][2 * i]), scale, -base));
-                        const float e1 = ex2(fmaf(__uint_as_float(x[c][2 * i + 1]), scale, -base));
-                        add[i % 4] += e0 + e1;
-                        w[i] = pack_bf16x2(e0, e1);
+                        float2 e = fma2(make_float2(__uint_as_float(x[c][2 * i]), __uint_as_float(x[c][2 * i + 1])), scale2, base2);
+                        e.x = ex2(e.x), e.y = ex2(e.y);
+                        add[i % 2] = add2(add[i % 2], e);
+                        w[i] = pack_bf16x2(e.x, e.y);
                     }
                     tmem_st_32x32b_x16(t_p + c * 16, w);
+                    if (c % 2) {  // 64 keys: their product may begin
+                        tmem_st_wait();
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&s.p_full[2 * tile + c / 2]);
+                    }
                 }
-                sum += (add[0] + add[1]) + (add[2] + add[3]);
-                tmem_st_wait();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&s.p_full[tile]);
+                sum += (add[0].x + add[1].x) + (add[0].y + add[1].y);
                 ++s_n;
             }
             // the unit's rows
@@ -889,20 +973,20 @@ __global__ void __launch_bounds__(kThreadsOf<kType>, 1)
                   const __grid_constant__ CUtensorMap map_v, const __grid_constant__ PromptArgs a) {
     constexpr int kS = kStages<kDim>;
     constexpr bool kConvert = kType != BD_KV_BF16;
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t *smem = smem_raw + (smem_base() - smem_u32(smem_raw));
     uint8_t *kv = smem + 2 * kTileBytes<kDim>;
     uint64_t *bars = reinterpret_cast<uint64_t *>(kv + kS * kTileBytes<kDim>);
     Smem s;
     s.full = bars, s.empty = bars + kS, s.fixed = bars + 2 * kS;
     bars += 3 * kS;
-    s.q_full = bars, s.q_empty = bars + 2, s.s_full = bars + 4, s.p_full = bars + 6, s.o_full = bars + 8;  // o_full[2]: the last products
-    s.u_full = bars + 11, s.u_empty = bars + 13;
-    s.unit = reinterpret_cast<Unit *>(bars + 16);
+    s.q_full = bars, s.q_empty = bars + 2, s.s_full = bars + 4, s.o_full = bars + 6;  // o_full[2]: the last products
+    s.p_full = bars + 9;                                                            // of each tile: the first and second 64 keys
+    s.u_full = bars + 13, s.u_empty = bars + 15;
+    s.unit = reinterpret_cast<Unit *>(bars + 17);
     s.slow = reinterpret_cast<volatile int *>(s.unit + 2);
     s.abort = s.slow + kS;
     s.tmem = const_cast<uint32_t *>(reinterpret_cast<volatile uint32_t *>(s.abort + 1));
-    static_assert((3 * kS + 16) * 8 + 2 * sizeof(Unit) + (kS + 2) * 4 <= 1024);
+    static_assert((3 * kS + 17) * 8 + 2 * sizeof(Unit) + (kS + 2) * 4 <= 1024);
     const int warp = threadIdx.x / 32;
     pdl_trigger_and_wait();
     if (threadIdx.x == 0) {
@@ -916,7 +1000,8 @@ __global__ void __launch_bounds__(kThreadsOf<kType>, 1)
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&s.q_full[i], 1), mbar_init(&s.q_empty[i], 1);
-            mbar_init(&s.s_full[i], 1), mbar_init(&s.p_full[i], 4), mbar_init(&s.o_full[i], 1);
+            mbar_init(&s.s_full[i], 1), mbar_init(&s.o_full[i], 1);
+            mbar_init(&s.p_full[2 * i], 4), mbar_init(&s.p_full[2 * i + 1], 4);
             mbar_init(&s.u_full[i], 1), mbar_init(&s.u_empty[i], 9 + (kConvert ? kConvertWarps : 2));
         }
         mbar_init(&s.o_full[2], 1);
@@ -932,14 +1017,14 @@ __global__ void __launch_bounds__(kThreadsOf<kType>, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = *s.tmem;
+    const uint32_t tmem = *s.tmem;  // 0: all of it is this CTA's
     // a softmax thread holds a row of 128 scores: 384 threads start with 168 registers each, 512 with 128
     if (warp < 8) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kConvert ? 184 : 216));
     else asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     if (warp < 8) {
-        softmax_rows<kDim, kType>(a, s, tmem, kv);
+        softmax_rows<kDim, kType>(a, s, 0, kv);
     } else if (warp == 8) {
-        issue_products<kDim, kType>(a, s, tmem, smem_u32(smem), smem_u32(kv));
+        issue_products<kDim, kType>(a, s);
     } else if (warp == 9) {
         find_units(a, s);
     } else if constexpr (kConvert) {
