@@ -123,17 +123,6 @@ __device__ __forceinline__ float tmem_ld_one(uint32_t taddr) {
     tmem_ld_wait();
     return __uint_as_float(v);
 }
-// Shared-memory descriptor of an operand whose rows are the product's inner dimension (V: 64 columns of a key side by
-// side, 128-byte swizzle): 8 keys are 1024 bytes, the next 64 columns lie a column piece further.
-__device__ __forceinline__ uint64_t sw128_rows_desc(uint32_t addr) {
-    uint64_t d = 0;
-    d |= static_cast<uint64_t>((addr & 0x3FFFFu) >> 4);
-    d |= static_cast<uint64_t>((kBlock * 128) >> 4) << 16;  // to the next 64 columns
-    d |= static_cast<uint64_t>(1024 >> 4) << 32;            // to the next 8 keys
-    d |= static_cast<uint64_t>(1) << 46;
-    d |= static_cast<uint64_t>(2) << 61;
-    return d;
-}
 // Byte of 16-byte chunk c (8 columns) of row r in a tile: pieces of 64 columns, chunks turned by the row.
 __device__ __forceinline__ uint32_t tile_at(int r, int c) { return (c / 8) * (kBlock * 128) + r * 128 + (((c % 8) ^ (r & 7)) << 4); }
 
@@ -142,8 +131,7 @@ __device__ __forceinline__ bool not_finite(uint4 v) {  // of eight bf16 numbers
     return two(v.x) || two(v.y) || two(v.z) || two(v.w);
 }
 
-// One lane of a converged warp.  (A branch on the lane's number instead costs about 150 clocks for each product issued:
-// the compiler does not see that one thread runs it, and the operands' descriptors have to be uniform.)
+// One lane of a converged warp.
 __device__ __forceinline__ bool elect_one() {
     uint32_t on;
     asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(on));
@@ -160,25 +148,27 @@ struct Smem {
     uint32_t *tmem;
 };
 
-// Bounded wait of a warp; on give-up the status word and the other roles are told.
-__device__ __forceinline__ bool wait_on(uint64_t *bar, uint32_t parity, const PromptArgs &a, volatile int *abort) {
-    bool ok = mbar_try_wait(bar, parity);
-    if (!ok && a.wait_ns != 0) {
-        // the clock and the flag are looked at seldom: reading them takes longer than the wait is mostly over by
+// Bounded wait of one thread; on give-up the status word and the other roles are told.
+__device__ __forceinline__ bool wait_alone(uint64_t *bar, uint32_t parity, const PromptArgs &a, volatile int *abort) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if (a.wait_ns != 0) {
+        // the clock and the flag are looked at seldom: most waits are over sooner than they are read
         uint64_t begin = 0;
-        for (int polls = 1; !(ok = mbar_try_wait(bar, parity)); ++polls) {
+        for (int polls = 1;; ++polls) {
+            if (mbar_try_wait(bar, parity)) return true;
             if (polls % 64) continue;
             const uint64_t now = globaltimer_ns();
             if (begin == 0) begin = now;
             if (*abort != 0 || now - begin > a.wait_ns) break;
         }
     }
-    if (__all_sync(0xFFFFFFFFu, ok)) return true;
-    if (threadIdx.x % 32 == 0) {
-        *abort = 1;
-        flag_status(a.status, kDevTimeout);
-    }
+    *abort = 1;
+    flag_status(a.status, kDevTimeout);
     return false;
+}
+// The same of a warp.
+__device__ __forceinline__ bool wait_on(uint64_t *bar, uint32_t parity, const PromptArgs &a, volatile int *abort) {
+    return __all_sync(0xFFFFFFFFu, wait_alone(bar, parity, a, abort));
 }
 
 // ---- units -----------------------------------------------------------------------------
@@ -370,129 +360,130 @@ struct Columns {
     static constexpr uint32_t s = 0, o = 2 * kBlock, p = kDim == 128 ? 0 : 2 * kBlock + 2 * kDim, p_tile = kDim == 128 ? kBlock : kBlock / 2;
 };
 
+// The products with a descriptor's lower word given: its upper word is one for all tiles, and one addition a product is left.
+constexpr uint32_t kDescHigh = (1024 >> 4) | 1u << 14 | 2u << 29;  // 1024 bytes to the next 8 rows, version 1, 128-byte swizzle
+__device__ __forceinline__ uint32_t desc_low(uint32_t addr, uint32_t leading) { return (addr & 0x3FFFFu) >> 4 | (leading >> 4) << 16; }
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\tmov.b64 da, {%1, %5};\n\tmov.b64 db, {%2, %5};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t}" ::"r"(d), "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "n"(kDescHigh)
+        : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 db;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\tmov.b64 db, {%2, %5};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n\t}" ::"r"(d), "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "n"(kDescHigh)
+        : "memory");
+}
 // S of a tile: Q K^T.
 template <int kDim, int kTile>
 __device__ __forceinline__ void issue_scores(int stage) {
     constexpr uint32_t idesc = idesc_bf16_f32(kTileRows, kBlock);
-    const uint64_t q = sw128_kmajor_desc(smem_base() + kTile * kTileBytes<kDim>);
-    const uint64_t k = sw128_kmajor_desc(smem_base() + (2 + stage) * kTileBytes<kDim>);
+    const uint32_t q = desc_low(smem_base() + kTile * kTileBytes<kDim>, 16), k = desc_low(smem_base() + (2 + stage) * kTileBytes<kDim>, 16);
 #pragma unroll
     for (int i = 0; i < kDim / 16; ++i) {
         const uint32_t at = i / 4 * (kBlock * 128 / 16) + i % 4 * 2;
-        tc_mma_f16_ss(Columns<kDim>::s + kTile * kBlock, q + at, k + at, idesc, i > 0);
+        mma_ss(Columns<kDim>::s + kTile * kBlock, q + at, k + at, idesc, i > 0);
     }
 }
-// Half of a tile's P V.
+// Half of a tile's P V; V's rows are the product's inner dimension, its next 64 columns a column piece further.
 template <int kDim, int kTile, int kHalf>
 __device__ __forceinline__ void issue_values(int stage, uint32_t accumulate) {
-    constexpr uint32_t idesc = idesc_bf16_f32(kTileRows, kDim) | 1u << 16;  // V's rows are keys
-    const uint64_t v = sw128_rows_desc(smem_base() + (2 + stage) * kTileBytes<kDim>);
+    constexpr uint32_t idesc = idesc_bf16_f32(kTileRows, kDim) | 1u << 16;
+    const uint32_t v = desc_low(smem_base() + (2 + stage) * kTileBytes<kDim>, kBlock * 128);
 #pragma unroll
     for (int i = kHalf * (kBlock / 32); i < (kHalf + 1) * (kBlock / 32); ++i)
-        tc_mma_f16_ts(Columns<kDim>::o + kTile * kDim, Columns<kDim>::p + kTile * Columns<kDim>::p_tile + i * 8, v + i * (16 * 128 / 16), idesc,
-                      i > 0 ? 1u : accumulate);
+        mma_ts(Columns<kDim>::o + kTile * kDim, Columns<kDim>::p + kTile * Columns<kDim>::p_tile + i * 8, v + i * (16 * 128 / 16), idesc,
+               i > 0 ? 1u : accumulate);
 }
 
+// Run by one thread.  Issuing a product stalls while a few are queued, so this thread's time is the tensor cores': with eight
+// softmax warps competing for the schedulers each instruction of it counts (a warp that elects a lane for each lot of
+// products took 137 clocks a product beside busy warps, one thread throughout 90, a thread chosen by its number 275).
 template <int kDim, int kType>
 __device__ __forceinline__ void issue_products(const PromptArgs &a, const Smem &s) {
     constexpr int kS = kStages<kDim>;
-    int it = 0, p_n[2] = {0, 0}, q_n[2] = {0, 0};
-    int stage = 0;
+    int it = 0;
+    uint32_t p_round[2] = {0, 0}, q_round[2] = {0, 0};
+    int stage = 0, loads = 0;
     uint32_t round = 0;  // of the next K or V tile
-    int loads = 0;
     bool ok = true;
     auto advance = [&] {
         ++loads;
         if (++stage == kS) stage = 0, round ^= 1;
     };
-    auto scores = [&](auto tile, int at) {
-        if (elect_one()) {
-            issue_scores<kDim, tile()>(at);
-            tc_commit(&s.s_full[tile()]);
-        }
-        __syncwarp();
-    };
     std::integral_constant<int, 0> first;
     std::integral_constant<int, 1> second;
-    auto start_tile = [&](auto tile, const Unit &u) {
-        if (!wait_on(&s.q_full[tile()], q_n[tile()] & 1, a, s.abort)) return false;
-        ++q_n[tile()];
-        tc_fence_after();
-        scores(tile, stage);
-        if (u.blocks == 1 && elect_one()) tc_commit(&s.q_empty[tile()]);
+    int blocks = 0, blk0 = 0, in_lo = 0, in_hi = 0;
+    bool both = false;
+    auto next = [&] {  // the next unit with something to see; false: none
+        do {
+            if (!wait_alone(&s.u_full[it & 1], (it >> 1) & 1, a, s.abort)) return false;
+            const Unit &u = s.unit[it & 1];
+            blocks = u.blocks, blk0 = u.blk0, in_lo = u.in_lo, in_hi = u.in_hi, both = u.tokens > a.tile_tokens;
+            mbar_arrive(&s.u_empty[it & 1]);
+            ++it;
+        } while (blocks == 0);
+        return blocks > 0;
+    };
+    auto start_tile = [&](auto tile) {
+        constexpr int i = tile();
+        if (!wait_alone(&s.q_full[i], q_round[i], a, s.abort)) return false;
+        q_round[i] ^= 1;
+        issue_scores<kDim, i>(stage);
+        tc_commit(&s.s_full[i]);
+        if (blocks == 1) tc_commit(&s.q_empty[i]);
         return true;
     };
-    auto start = [&](const Unit &u) {  // scores of a unit's first block
-        if (!wait_on(&s.full[stage], round, a, s.abort)) return false;
-        if (!start_tile(first, u)) return false;
-        if (u.tokens > a.tile_tokens && !start_tile(second, u)) return false;
-        if (elect_one()) tc_commit(&s.empty[stage]);
-        __syncwarp();
+    auto start = [&] {  // scores of a unit's first block
+        if (!wait_alone(&s.full[stage], round, a, s.abort)) return false;
+        if (!start_tile(first)) return false;
+        if (both && !start_tile(second)) return false;
+        tc_commit(&s.empty[stage]);
         advance();
         return true;
     };
-    auto next = [&] {  // the next unit with something to see
-        Unit u;
-        do u = next_unit(a, s, it);
-        while (u.blocks == 0);
-        // from lane 0: what the loops below run by is the same in all lanes
-        u.blocks = __shfl_sync(0xFFFFFFFFu, u.blocks, 0), u.tokens = __shfl_sync(0xFFFFFFFFu, u.tokens, 0);
-        u.blk0 = __shfl_sync(0xFFFFFFFFu, u.blk0, 0);
-        u.in_lo = __shfl_sync(0xFFFFFFFFu, u.in_lo, 0), u.in_hi = __shfl_sync(0xFFFFFFFFu, u.in_hi, 0);
-        return u;
-    };
-    Unit u = next();
-    if (u.blocks > 0) ok = start(u);
-    while (ok && u.blocks > 0) {
-        const bool both = u.tokens > a.tile_tokens;
-        for (int j = 0; j < u.blocks && ok; ++j) {
-            const int v_stage = stage;
+    while (ok && next()) {
+        ok = start();
+        for (int j = 0; ok && j < blocks; ++j) {
+            const int v_stage = stage, key0 = (blk0 + j) * kBlock;
             const uint32_t v_round = round;
             advance();
-            const bool part = seen_in_part(u, u.blk0 + j), more = j + 1 < u.blocks;
-            ok = wait_on(kType == BD_KV_BF16 && part ? &s.fixed[v_stage] : &s.full[v_stage], v_round, a, s.abort);
-            const bool slow = ok && part && __any_sync(0xFFFFFFFFu, s.slow[v_stage] == loads);  // its load's number from 1
+            const bool part = key0 < in_lo || key0 + kBlock > in_hi, more = j + 1 < blocks;
+            ok = wait_alone(kType == BD_KV_BF16 && part ? &s.fixed[v_stage] : &s.full[v_stage], v_round, a, s.abort);
+            const bool slow = part && s.slow[v_stage] == loads;  // its load's number from 1
             auto tile_products = [&](auto tile) {
                 constexpr int i = tile();
-                if (!wait_on(&s.p_full[2 * i], p_n[i] & 1, a, s.abort)) return false;
+                if (!wait_alone(&s.p_full[2 * i], p_round[i], a, s.abort)) return false;
                 tc_fence_after();
-                if (!slow && elect_one()) issue_values<kDim, i, 0>(v_stage, j > 0);
-                __syncwarp();
-                if (!wait_on(&s.p_full[2 * i + 1], p_n[i] & 1, a, s.abort)) return false;
+                if (!slow) issue_values<kDim, i, 0>(v_stage, j > 0);
+                if (!wait_alone(&s.p_full[2 * i + 1], p_round[i], a, s.abort)) return false;
                 tc_fence_after();
-                ++p_n[i];
-                if (elect_one()) {
-                    if (!slow) issue_values<kDim, i, 1>(v_stage, 1);
-                    tc_commit(&s.o_full[i]);
-                }
-                __syncwarp();
+                p_round[i] ^= 1;
+                if (!slow) issue_values<kDim, i, 1>(v_stage, 1);
+                tc_commit(&s.o_full[i]);
                 if (more) {
-                    if (i == 0 && !wait_on(&s.full[stage], round, a, s.abort)) return false;
-                    scores(tile, stage);
-                    if (j + 2 == u.blocks && elect_one()) tc_commit(&s.q_empty[i]);
-                    __syncwarp();
+                    if (i == 0 && !wait_alone(&s.full[stage], round, a, s.abort)) return false;
+                    issue_scores<kDim, i>(stage);
+                    tc_commit(&s.s_full[i]);
+                    if (j + 2 == blocks) tc_commit(&s.q_empty[i]);
                 }
                 return true;
             };
             ok = ok && tile_products(first) && (!both || tile_products(second));
             if (!ok) break;
-            if (elect_one()) {
-                tc_commit(&s.empty[v_stage]);
-                if (more) tc_commit(&s.empty[stage]);
+            tc_commit(&s.empty[v_stage]);
+            if (more) {
+                tc_commit(&s.empty[stage]);
+                advance();
             }
-            __syncwarp();
-            if (more) advance();
         }
-        if (!ok) break;
-        u = next();
-        if (u.blocks > 0) ok = start(u);
     }
     // no product may be in flight when tensor memory is freed, even after giving up
-    if (elect_one()) {
-        tc_commit(s.o_full + 2);
-        mbar_wait(s.o_full + 2, 0, kDrainLimitNs, nullptr);
-    }
-    __syncwarp();
+    tc_commit(s.o_full + 2);
+    mbar_wait(s.o_full + 2, 0, kDrainLimitNs, nullptr);
 }
 
 // ---- warp 10 and on: queries, keys and values ------------------------------------------------
@@ -1024,7 +1015,8 @@ __global__ void __launch_bounds__(kThreadsOf<kType>, 1)
     if (warp < 8) {
         softmax_rows<kDim, kType>(a, s, 0, kv);
     } else if (warp == 8) {
-        issue_products<kDim, kType>(a, s);
+        if (elect_one()) issue_products<kDim, kType>(a, s);
+        __syncwarp();
     } else if (warp == 9) {
         find_units(a, s);
     } else if constexpr (kConvert) {
