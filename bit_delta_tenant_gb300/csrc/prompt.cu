@@ -13,7 +13,8 @@
 //
 // A CTA.  Warps 0-3 and 4-7: the softmax of one tile each, a thread per row.  Warp 8: issues the products.  Warp 9: finds
 // the next unit and its blocks.  Warp 10 on: K and V of the cache to a ring of shared-memory tiles, by TMA in
-// bf16 (warp 10; warp 11 looks at the blocks that some row sees only in part), by six warps that convert 8-bit and 4-bit values.
+// bf16 (warp 10; warp 11 looks at the blocks that some row sees only in part); 8-bit and 4-bit values are copied as they are and
+// converted by warps 11 to 15.
 // S = Q K^T goes to tensor memory; a softmax thread reads its row, and writes the weights back there as the bf16 operand of
 // P V, whose accumulator stays in tensor memory.  The two tiles alternate: one's products run under the other's softmax.
 // The running maximum is raised only when a row passes it by 2^8, so that the output is seldom rescaled: weights
@@ -37,17 +38,26 @@ namespace {
 constexpr int kBlock = 128;  // keys of a block
 constexpr int kTileRows = 128;
 constexpr int64_t kMaxLength = 1 << 30;
-constexpr int kConvertWarps = 6;
+constexpr int kConvertWarps = 5;
 constexpr float kLazy = 8.f;  // by how much (in base 2) a row's scores may pass the maximum they are taken from
 
 template <int kType>
-constexpr int kThreadsOf = kType == BD_KV_BF16 ? 384 : (10 + kConvertWarps) * 32;
+constexpr int kThreadsOf = kType == BD_KV_BF16 ? 384 : (11 + kConvertWarps) * 32;
 template <int kDim>
 constexpr uint32_t kTileBytes = kBlock * kDim * 2;  // of K, V or Q in shared memory: columns in pieces of 64, swizzled
-template <int kDim>
-constexpr int kStages = kDim == 128 ? 5 : 8;
-template <int kDim>
-constexpr int kSmemBytes = 1024 + (2 + kStages<kDim>) * kTileBytes<kDim> + 1024;
+// K and V tiles in shared memory; 8 and 4 bits: and tiles as they are in the cache, with their scale bytes behind the values
+template <int kDim, int kType>
+constexpr int kStages = kDim == 128 ? (kType == BD_KV_BF16 ? 5 : 4) : (kType == BD_KV_BF16 ? 8 : 6);
+template <int kDim, int kType>
+constexpr int kRow = kType == BD_KV_BF16 ? 2 * kDim : kType == BD_KV_E4M3 ? kDim : kDim / 2;  // bytes of a key
+template <int kDim, int kType>
+constexpr int kScale = kType == BD_KV_BF16 ? 0 : kType == BD_KV_E4M3 ? 1 : kDim / 16;
+template <int kDim, int kType>
+constexpr int kRawSlots = kType == BD_KV_BF16 ? 0 : kDim == 64 ? 4 : kType == BD_KV_E4M3 ? 2 : 3;
+template <int kDim, int kType>
+constexpr int kRawBytes = kBlock * (kRow<kDim, kType> + kScale<kDim, kType>);
+template <int kDim, int kType>
+constexpr int kSmemBytes = 1024 + (2 + kStages<kDim, kType>) * kTileBytes<kDim> + kRawSlots<kDim, kType> * kRawBytes<kDim, kType> + 1024;
 constexpr int kSlotRows = 2 * kTileRows;
 template <int kDim>
 constexpr int64_t kSlotFloats = kSlotRows * (kDim + 2);  // a piece's output, maxima and sums, tile by tile
@@ -140,6 +150,8 @@ __device__ __forceinline__ bool elect_one() {
 
 struct Smem {
     uint64_t *full, *empty, *fixed;      // per stage
+    uint64_t *raw_full, *raw_empty;      // per slot of tiles as they are in the cache
+    uint8_t *raw;
     uint64_t *q_full, *q_empty, *s_full, *p_full, *o_full;  // per tile
     uint64_t *u_full, *u_empty;          // per unit slot
     Unit *unit;
@@ -404,7 +416,7 @@ __device__ __forceinline__ void issue_values(int stage, uint32_t accumulate) {
 // products took 137 clocks a product beside busy warps, one thread throughout 90, a thread chosen by its number 275).
 template <int kDim, int kType>
 __device__ __forceinline__ void issue_products(const PromptArgs &a, const Smem &s) {
-    constexpr int kS = kStages<kDim>;
+    constexpr int kS = kStages<kDim, kType>;
     int it = 0;
     uint32_t p_round[2] = {0, 0}, q_round[2] = {0, 0};
     int stage = 0, loads = 0;
@@ -505,17 +517,16 @@ __device__ __forceinline__ bool load_queries(const PromptArgs &a, const Smem &s,
     return true;
 }
 
-__device__ __forceinline__ void drain_queries(const Smem &s, const int (&q_n)[2]) {
-    for (int i = 0; i < 2; ++i)
-        if (q_n[i] > 0) mbar_wait(&s.q_full[i], (q_n[i] - 1) & 1, kDrainLimitNs, nullptr);
-}
-
-// bf16: copies of `box` keys and 64 columns.  Lane l looks up piece l of a block and copies it; a piece that no row sees or
-// whose page id is out of range is zeroed.
-template <int kDim>
+// Warp 10.  bf16: TMA copies of `box` keys and 64 columns to the tiles; 8 and 4 bits: plain copies of `box` keys and their scale
+// bytes.  Lane l looks up piece l of a block and copies it; a piece that no row sees or whose page id is out of range is
+// zeroed.
+template <int kDim, int kType>
 __device__ __forceinline__ void load_tiles(const PromptArgs &a, const Smem &s, const CUtensorMap *map_q, const CUtensorMap *map_k,
                                            const CUtensorMap *map_v, uint32_t smem_q, uint8_t *kv) {
-    constexpr int kS = kStages<kDim>;
+    constexpr bool kCopy = kType != BD_KV_BF16;
+    constexpr int kS = kCopy ? kRawSlots<kDim, kType> : kStages<kDim, kType>;
+    constexpr int kR = kRow<kDim, kType>, kSc = kScale<kDim, kType>;
+    uint64_t *full = kCopy ? s.raw_full : s.full, *empty = kCopy ? s.raw_empty : s.empty;
     const int lane = threadIdx.x % 32;
     const int per_block = kBlock / a.box;
     int it = 0, loads = 0, q_n[2] = {0, 0};
@@ -530,55 +541,71 @@ __device__ __forceinline__ void load_tiles(const PromptArgs &a, const Smem &s, c
             const int key = (u.blk0 + j) * kBlock + lane * a.box;
             if (lane >= per_block || j >= u.blocks || key >= u.un_hi || key + a.box <= u.un_lo) return -1;
             const int at = key / a.page_size;
-            if (!in_bounds(at >= 0 && at < a.max_pages, a.status)) return -1;
-            const int32_t page = table[at];
-            if (page < 0 || page >= a.n_pages) {
-                flag_status(a.status, kDevBadIndex);
-                return -1;
-            }
-            return page;
+            return in_bounds(at >= 0 && at < a.max_pages, a.status) ? table[at] : -1;
         };
-        int page = page_of(0);
+        int next_page = page_of(0);
         if (!load_queries<kDim>(a, s, map_q, smem_q, u, q_n)) break;
         for (int j = 0; j < u.blocks && ok; ++j) {
-            const int next_page = page_of(j + 1);
+            int page = next_page;
+            next_page = page_of(j + 1);  // not waited for until the next block
             const int key = (u.blk0 + j) * kBlock + lane * a.box;
+            if (page < 0 || page >= a.n_pages) {
+                if (lane < per_block && key < u.un_hi && key + a.box > u.un_lo) flag_status(a.status, kDevBadIndex);
+                page = -1;
+            }
             const unsigned there = __ballot_sync(0xFFFFFFFFu, page >= 0);
+            const int row_in = kvh * a.page_size + key % a.page_size;
             for (int w = 0; w < 2; ++w, ++loads) {
                 const int stage = loads % kS;
-                if (!wait_on(&s.empty[stage], ((loads / kS) & 1) ^ 1, a, s.abort)) {
+                if (!wait_on(&empty[stage], ((loads / kS) & 1) ^ 1, a, s.abort)) {
                     ok = false;
                     break;
                 }
-                uint8_t *dst = kv + stage * kTileBytes<kDim>;
-                if (there != (per_block == 32 ? 0xFFFFFFFFu : (1u << per_block) - 1)) {
+                uint8_t *dst = kCopy ? s.raw + stage * kRawBytes<kDim, kType> : kv + stage * kTileBytes<kDim>;
+                if (there != (1u << per_block) - 1) {
                     for (int p = 0; p < per_block; ++p)
-                        if (!(there >> p & 1))
-                            for (int i = lane; i < a.box * (kDim / 8); i += 32)
-                                *reinterpret_cast<uint4 *>(dst + tile_at(p * a.box + i / (kDim / 8), i % (kDim / 8))) = make_uint4(0, 0, 0, 0);
+                        if (!(there >> p & 1)) {
+                            if constexpr (kCopy) {
+                                for (int i = lane; i < a.box * kR / 16; i += 32)
+                                    reinterpret_cast<uint4 *>(dst + p * a.box * kR)[i] = make_uint4(0, 0, 0, 0);
+                                for (int i = lane; i < a.box * kSc / 16; i += 32)
+                                    reinterpret_cast<uint4 *>(dst + kBlock * kR + p * a.box * kSc)[i] = make_uint4(0, 0, 0, 0);
+                            } else {
+                                for (int i = lane; i < a.box * (kDim / 8); i += 32)
+                                    *reinterpret_cast<uint4 *>(dst + tile_at(p * a.box + i / (kDim / 8), i % (kDim / 8))) = make_uint4(0, 0, 0, 0);
+                            }
+                        }
                     fence_proxy_async_smem();
                     __syncwarp();
                 }
-                if (lane == 0) mbar_arrive_expect_tx(&s.full[stage], __popc(there) * a.box * kDim * 2);
+                if (lane == 0) mbar_arrive_expect_tx(&full[stage], __popc(there) * a.box * (kR + kSc));
                 __syncwarp();
-                if (page >= 0)
-                    for (int c = 0; c < kDim / 64; ++c)
-                        tma_load_3d(smem_u32(dst) + c * (kBlock * 128) + lane * a.box * 128, w ? map_v : map_k, &s.full[stage], c * 64,
-                                    kvh * a.page_size + key % a.page_size, page);
+                if (page >= 0) {
+                    if constexpr (kCopy) {
+                        const int64_t row = static_cast<int64_t>(page) * a.kv_heads * a.page_size + row_in;
+                        if (in_bounds(row + a.box <= a.n_pages * a.kv_heads * a.page_size, a.status)) {
+                            bulk_load(dst + lane * a.box * kR, (w ? a.cv : a.ck) + row * kR, a.box * kR, &full[stage]);
+                            bulk_load(dst + kBlock * kR + lane * a.box * kSc, (w ? a.cv_scale : a.ck_scale) + row * kSc, a.box * kSc, &full[stage]);
+                        }
+                    } else {
+                        for (int c = 0; c < kDim / 64; ++c)
+                            tma_load_3d(smem_u32(dst) + c * (kBlock * 128) + lane * a.box * 128, w ? map_v : map_k, &full[stage], c * 64, row_in, page);
+                    }
+                }
                 __syncwarp();
             }
-            page = next_page;
         }
     }
     // copies in flight have to land before the CTA ends, also when another role gave up
-    for (int l = loads > kS ? loads - kS : 0; l < loads; ++l) mbar_wait(&s.full[l % kS], (l / kS) & 1, kDrainLimitNs, nullptr);
-    drain_queries(s, q_n);
+    for (int l = loads > kS ? loads - kS : 0; l < loads; ++l) mbar_wait(&full[l % kS], (l / kS) & 1, kDrainLimitNs, nullptr);
+    for (int i = 0; i < 2; ++i)
+        if (q_n[i] > 0) mbar_wait(&s.q_full[i], (q_n[i] - 1) & 1, kDrainLimitNs, nullptr);
 }
 
 // Warp 11: V of blocks that some row sees in part.
 template <int kDim>
 __device__ __forceinline__ void look_at_values(const PromptArgs &a, const Smem &s, uint8_t *kv) {
-    constexpr int kS = kStages<kDim>;
+    constexpr int kS = kStages<kDim, BD_KV_BF16>;
     const int lane = threadIdx.x % 32;
     int it = 0, loads = 0;
     while (true) {
@@ -610,102 +637,74 @@ __device__ __forceinline__ void look_at_values(const PromptArgs &a, const Smem &
     }
 }
 
-// 8 and 4 bits: raw values are read a tile ahead, 16 bytes at a time, and written as the bf16 numbers that they stand for.
+// Warps 11 to 15: tiles as they are in the cache to the bf16 numbers that they stand for, 16 bytes at a time.
+__device__ __forceinline__ uint32_t bf16_pair(__half2_raw h, uint32_t scale) {  // times a scale given twice: exact in bf16
+    const float2 f = __half22float2(__half2(h));
+    uint32_t r;
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(pack_bf16x2(f.x, f.y)), "r"(scale));
+    return r;
+}
 template <int kDim, int kType>
-__device__ __forceinline__ void convert_tiles(const PromptArgs &a, const Smem &s, const CUtensorMap *map_q, uint32_t smem_q, uint8_t *kv, int (&q_n)[2]) {
-    constexpr int kS = kStages<kDim>;
-    constexpr int kRow = kType == BD_KV_E4M3 ? kDim : kDim / 2;  // bytes of a key
-    constexpr int kScale = kType == BD_KV_E4M3 ? 1 : kDim / 16;
-    constexpr int kPer = kRow / 16;                              // 16-byte pieces of a key
+__device__ __forceinline__ void convert_tiles(const PromptArgs &a, const Smem &s, uint8_t *kv) {
+    constexpr int kS = kStages<kDim, kType>, kRaw = kRawSlots<kDim, kType>, kSc = kScale<kDim, kType>;
+    constexpr int kPer = kRow<kDim, kType> / 16;       // 16-byte pieces of a key
+    constexpr int kOut = kType == BD_KV_E4M3 ? 2 : 4;  // and of bf16 that each makes
     constexpr int kThreads = kConvertWarps * 32;
-    constexpr int kEach = (kBlock * kPer + kThreads - 1) / kThreads;
-    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32 - 10, tid = threadIdx.x - 320;
+    const int lane = threadIdx.x % 32, tid = threadIdx.x - 11 * 32;
     int it = 0, loads = 0;
     while (true) {
         const Unit u = next_unit(a, s, it);
         if (u.blocks < 0) return;
-        if (u.blocks == 0) continue;
-        if (warp == 0 && !load_queries<kDim>(a, s, map_q, smem_q, u, q_n)) return;
-        const int32_t *table = a.page_table + static_cast<int64_t>(u.seq) * a.max_pages;
-        const int kvh = u.vh / a.subs;
-        int32_t page[kEach];  // of this thread's pieces of a block; -1: none
-        auto pages_of = [&](int j) {
+        for (int l = 0; l < 2 * u.blocks; ++l, ++loads) {
+            const int stage = loads % kS, slot = loads % kRaw, key0 = (u.blk0 + l / 2) * kBlock;
+            if (!wait_on(&s.raw_full[slot], (loads / kRaw) & 1, a, s.abort)) return;
+            if (!wait_on(&s.empty[stage], ((loads / kS) & 1) ^ 1, a, s.abort)) return;
+            uint8_t *tile = kv + stage * kTileBytes<kDim>;
+            const uint8_t *raw = s.raw + slot * kRawBytes<kDim, kType>, *scales = raw + kBlock * kRow<kDim, kType>;
+            const bool look = l % 2 && seen_in_part(u, u.blk0 + l / 2);
+            bool bad = false;
+#pragma unroll 2
+            for (int i = tid; i < kBlock * kPer; i += kThreads) {
+                const int key = i / kPer;
+                const uint4 x = reinterpret_cast<const uint4 *>(raw)[i];
+                const uint32_t in[4] = {x.x, x.y, x.z, x.w};
+                uint32_t scale[2];  // as a bf16 number, twice
+                if constexpr (kType == BD_KV_E4M3) {
+                    const uint32_t b = static_cast<uint32_t>(scales[key]) << 7;
+                    scale[0] = scale[1] = b | b << 16;
+                } else {
+                    const uint32_t two = *reinterpret_cast<const uint16_t *>(scales + key * kSc + i % kPer * 2);
 #pragma unroll
-            for (int e = 0; e < kEach; ++e) {
-                const int i = tid + e * kThreads, key = (u.blk0 + j) * kBlock + i / kPer;
-                page[e] = -1;
-                if (i >= kBlock * kPer || j >= u.blocks || key < u.un_lo || key >= u.un_hi) continue;
-                const int at = key / a.page_size;
-                if (in_bounds(at >= 0 && at < a.max_pages, a.status)) page[e] = table[at];
-            }
-        };
-        uint4 raw[kEach];
-        uint32_t scale[kEach];
-        auto fetch = [&](int j, bool v) {
-#pragma unroll
-            for (int e = 0; e < kEach; ++e) {
-                const int i = tid + e * kThreads, key = (u.blk0 + j) * kBlock + i / kPer;
-                raw[e] = make_uint4(0, 0, 0, 0);
-                scale[e] = 0;
-                if (page[e] < 0 || page[e] >= a.n_pages) {
-                    if (i < kBlock * kPer && j < u.blocks && key >= u.un_lo && key < u.un_hi) flag_status(a.status, kDevBadIndex);
-                    continue;
-                }
-                const int64_t row = (static_cast<int64_t>(page[e]) * a.kv_heads + kvh) * a.page_size + key % a.page_size;
-                if (!in_bounds(row < a.n_pages * a.kv_heads * a.page_size, a.status)) continue;
-                raw[e] = __ldg(reinterpret_cast<const uint4 *>((v ? a.cv : a.ck) + row * kRow) + i % kPer);
-                const uint8_t *sc = (v ? a.cv_scale : a.ck_scale) + row * kScale;
-                scale[e] = kType == BD_KV_E4M3 ? __ldg(sc) : __ldg(reinterpret_cast<const uint16_t *>(sc) + i % kPer);
-            }
-        };
-        pages_of(0);
-        fetch(0, false);
-        for (int j = 0; j < u.blocks; ++j)
-            for (int w = 0; w < 2; ++w, ++loads) {
-                const int stage = loads % kS;
-                if (!wait_on(&s.empty[stage], ((loads / kS) & 1) ^ 1, a, s.abort)) return;
-                uint8_t *tile = kv + stage * kTileBytes<kDim>;
-                const bool look = w && seen_in_part(u, u.blk0 + j);
-                bool bad = false;
-#pragma unroll
-                for (int e = 0; e < kEach; ++e) {
-                    const int i = tid + e * kThreads;
-                    if (i >= kBlock * kPer) continue;
-                    constexpr int kOut = kType == BD_KV_E4M3 ? 2 : 4;  // 16-byte pieces written
-                    const uint32_t in[4] = {raw[e].x, raw[e].y, raw[e].z, raw[e].w};
-#pragma unroll
-                    for (int o = 0; o < kOut; ++o) {
-                        float f[8];
-                        if constexpr (kType == BD_KV_E4M3) {
-                            const float sc = __uint_as_float(scale[e] << 23);
-#pragma unroll
-                            for (int k = 0; k < 4; ++k) {
-                                const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(in[2 * o + k / 2] >> k % 2 * 16 & 0xFFFFu), __NV_E4M3);
-                                const float2 x = __half22float2(__half2(h));
-                                f[2 * k] = x.x * sc, f[2 * k + 1] = x.y * sc;
-                            }
-                        } else {
-                            const float sc = __half2float(__ushort_as_half(static_cast<unsigned short>((scale[e] >> o / 2 * 8 & 0xFFu) << 7)));
-#pragma unroll
-                            for (int k = 0; k < 4; ++k) {
-                                const __half2_raw h = __nv_cvt_fp4x2_to_halfraw2(static_cast<__nv_fp4x2_storage_t>(in[o] >> k * 8 & 0xFFu), __NV_E2M1);
-                                const float2 x = __half22float2(__half2(h));
-                                f[2 * k] = x.x * sc, f[2 * k + 1] = x.y * sc;
-                            }
-                        }
-                        const uint4 y = pack8(f);
-                        if (look) bad |= not_finite(y);
-                        *reinterpret_cast<uint4 *>(tile + tile_at(i / kPer, i % kPer * kOut + o)) = y;
+                    for (int e = 0; e < 2; ++e) {
+                        const float f = __half2float(__ushort_as_half(static_cast<unsigned short>((two >> 8 * e & 0xFFu) << 7)));
+                        scale[e] = pack_bf16x2(f, f);
                     }
                 }
-                // the next tile's values are under way while this one is used
-                if (w) pages_of(j + 1);
-                if (!w || j + 1 < u.blocks) fetch(w ? j + 1 : j, !w);
-                if (bad) s.slow[stage] = loads + 1;
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&s.full[stage]);
+                const bool gone = look && (key0 + key < u.un_lo || key0 + key >= u.un_hi);
+#pragma unroll
+                for (int o = 0; o < kOut; ++o) {
+                    uint32_t y[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        if constexpr (kType == BD_KV_E4M3)
+                            y[k] = bf16_pair(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(in[2 * o + k / 2] >> k % 2 * 16 & 0xFFFFu), __NV_E4M3), scale[0]);
+                        else
+                            y[k] = bf16_pair(__nv_cvt_fp4x2_to_halfraw2(static_cast<__nv_fp4x2_storage_t>(in[o] >> k * 8 & 0xFFu), __NV_E2M1), scale[o / 2]);
+                        if (gone) y[k] = 0;
+                    }
+                    const uint4 out = make_uint4(y[0], y[1], y[2], y[3]);
+                    if (look) bad |= not_finite(out);
+                    *reinterpret_cast<uint4 *>(tile + tile_at(key, i % kPer * kOut + o)) = out;
+                }
             }
+            if (bad) s.slow[stage] = loads + 1;
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(&s.full[stage]);
+                mbar_arrive(&s.raw_empty[slot]);
+            }
+        }
     }
 }
 
@@ -788,7 +787,7 @@ __device__ __noinline__ unsigned missing_pieces(const PromptArgs &a, const Unit 
 
 template <int kDim, int kType>
 __device__ __forceinline__ void softmax_rows(const PromptArgs &a, const Smem &s, uint32_t tmem, const uint8_t *kv) {
-    constexpr int kS = kStages<kDim>;
+    constexpr int kS = kStages<kDim, kType>;
     const int tile = threadIdx.x / 128, r = threadIdx.x % 128, lane = threadIdx.x % 32;
     const uint32_t lane_base = tmem + (static_cast<uint32_t>(r / 32 * 32) << 16);
     const uint32_t t_s = lane_base + tile * kBlock, t_o = lane_base + 2 * kBlock + tile * kDim;
@@ -962,14 +961,17 @@ template <int kDim, int kType>
 __global__ void __launch_bounds__(kThreadsOf<kType>, 1)
     prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                   const __grid_constant__ CUtensorMap map_v, const __grid_constant__ PromptArgs a) {
-    constexpr int kS = kStages<kDim>;
+    constexpr int kS = kStages<kDim, kType>;
     constexpr bool kConvert = kType != BD_KV_BF16;
     uint8_t *smem = smem_raw + (smem_base() - smem_u32(smem_raw));
     uint8_t *kv = smem + 2 * kTileBytes<kDim>;
-    uint64_t *bars = reinterpret_cast<uint64_t *>(kv + kS * kTileBytes<kDim>);
     Smem s;
+    s.raw = kv + kS * kTileBytes<kDim>;
+    uint64_t *bars = reinterpret_cast<uint64_t *>(s.raw + kRawSlots<kDim, kType> * kRawBytes<kDim, kType>);
     s.full = bars, s.empty = bars + kS, s.fixed = bars + 2 * kS;
     bars += 3 * kS;
+    s.raw_full = bars, s.raw_empty = bars + 4;
+    bars += 8;
     s.q_full = bars, s.q_empty = bars + 2, s.s_full = bars + 4, s.o_full = bars + 6;  // o_full[2]: the last products
     s.p_full = bars + 9;                                                            // of each tile: the first and second 64 keys
     s.u_full = bars + 13, s.u_empty = bars + 15;
@@ -977,7 +979,7 @@ __global__ void __launch_bounds__(kThreadsOf<kType>, 1)
     s.slow = reinterpret_cast<volatile int *>(s.unit + 2);
     s.abort = s.slow + kS;
     s.tmem = const_cast<uint32_t *>(reinterpret_cast<volatile uint32_t *>(s.abort + 1));
-    static_assert((3 * kS + 17) * 8 + 2 * sizeof(Unit) + (kS + 2) * 4 <= 1024);
+    static_assert(kRawSlots<kDim, kType> <= 4 && (3 * kS + 25) * 8 + 2 * sizeof(Unit) + (kS + 2) * 4 <= 1024);
     const int warp = threadIdx.x / 32;
     pdl_trigger_and_wait();
     if (threadIdx.x == 0) {
@@ -993,8 +995,9 @@ __global__ void __launch_bounds__(kThreadsOf<kType>, 1)
             mbar_init(&s.q_full[i], 1), mbar_init(&s.q_empty[i], 1);
             mbar_init(&s.s_full[i], 1), mbar_init(&s.o_full[i], 1);
             mbar_init(&s.p_full[2 * i], 4), mbar_init(&s.p_full[2 * i + 1], 4);
-            mbar_init(&s.u_full[i], 1), mbar_init(&s.u_empty[i], 9 + (kConvert ? kConvertWarps : 2));
+            mbar_init(&s.u_full[i], 1), mbar_init(&s.u_empty[i], 10 + (kConvert ? kConvertWarps : 1));
         }
+        for (int i = 0; i < kRawSlots<kDim, kType>; ++i) mbar_init(&s.raw_full[i], 1), mbar_init(&s.raw_empty[i], kConvertWarps);
         mbar_init(&s.o_full[2], 1);
         *s.abort = 0;
         mbar_fence_init();
@@ -1019,12 +1022,10 @@ __global__ void __launch_bounds__(kThreadsOf<kType>, 1)
         __syncwarp();
     } else if (warp == 9) {
         find_units(a, s);
-    } else if constexpr (kConvert) {
-        int q_n[2] = {0, 0};
-        convert_tiles<kDim, kType>(a, s, &map_q, smem_u32(smem), kv, q_n);
-        drain_queries(s, q_n);  // warp 10's copies in flight land before the CTA ends, also after giving up
     } else if (warp == 10) {
-        load_tiles<kDim>(a, s, &map_q, &map_k, &map_v, smem_u32(smem), kv);
+        load_tiles<kDim, kType>(a, s, &map_q, &map_k, &map_v, smem_base(), kv);
+    } else if constexpr (kConvert) {
+        convert_tiles<kDim, kType>(a, s, kv);
     } else {
         look_at_values<kDim>(a, s, kv);
     }
@@ -1098,9 +1099,9 @@ cudaError_t launch_pdl(void (*kernel)(Types...), dim3 grid, int threads, int sme
 template <int kDim, int kType>
 cudaError_t launch_typed(const PromptArgs &a, const CUtensorMap &q, const CUtensorMap &k, const CUtensorMap &v, const DevCtx &ctx,
                          cudaStream_t stream) {
-    cudaError_t e = allow_smem<prompt_kernel<kDim, kType>>(kSmemBytes<kDim>, ctx.device);
+    cudaError_t e = allow_smem<prompt_kernel<kDim, kType>>(kSmemBytes<kDim, kType>, ctx.device);
     if (e != cudaSuccess) return e;
-    e = launch_pdl(prompt_kernel<kDim, kType>, dim3(ctx.num_sms), kThreadsOf<kType>, kSmemBytes<kDim>, stream, q, k, v, a);
+    e = launch_pdl(prompt_kernel<kDim, kType>, dim3(ctx.num_sms), kThreadsOf<kType>, kSmemBytes<kDim, kType>, stream, q, k, v, a);
     if (e != cudaSuccess || !a.may_split) return e;
     return launch_pdl(prompt_join_kernel<kDim>, dim3(a.slots, 2 * kTileRows / kJoinRows), kJoinThreads, 0, stream, a);
 }
