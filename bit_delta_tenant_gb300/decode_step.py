@@ -13,7 +13,8 @@ in a CUDA graph and replayed; positions advance on the device.
     python -m bit_delta_tenant_gb300.decode_step --layers 32 --sequences 64 --steps 64
 
 Weights are random: the shapes are those of the Llama-3-8B-shape stack.  Prompts are processed
-sequence by sequence in pieces; a piece attends to what is cached (bd_kv_read) by plain torch operations.
+sequence by sequence in pieces; a piece attends to what is cached, itself included (bd_attention_prompt).  The cache holds
+bf16, 8 or 4 bits; positions may be scaled for contexts beyond the model's own, scores capped.
 """
 from __future__ import annotations
 
@@ -37,18 +38,15 @@ class Shape:
     vocab: int = 128256
     eps: float = 1e-5
     rope_base: float = 5e5
+    rope_factor: float = 1.0    # by how much slow rotations are slowed down further, and the context
+    rope_original: int = 8192   # that the others are told from them by
+    score_cap: float = 0.0
 
     def matrices(self):
         """(name, n_out, n_in) of a layer's linears, as in workloads.LLAMA3_8B_STACK."""
         q, kv = self.q_heads * self.head_dim, self.kv_heads * self.head_dim
         return [("q", q, self.hidden), ("k", kv, self.hidden), ("v", kv, self.hidden), ("o", self.hidden, q),
                 ("gate", self.mlp, self.hidden), ("up", self.mlp, self.hidden), ("down", self.hidden, self.mlp)]
-
-
-def rope_table(positions: int, dim: int, base: float) -> torch.Tensor:
-    """fp32 [positions, dim]: cosines, then sines, of position * base^(-2i / dim)."""
-    angle = torch.arange(positions, dtype=torch.float64)[:, None] * base ** (-torch.arange(0, dim, 2, dtype=torch.float64) / dim)
-    return torch.cat([angle.cos(), angle.sin()], 1).float()
 
 
 class Matrix:
@@ -66,7 +64,7 @@ class Tenants:
     """The model, its variants, and the sequences being served with their cache."""
 
     def __init__(self, shape: Shape, n_variants: int, variants, max_tokens: int, page_size: int = 64,
-                 kv_e4m3: bool = False, seed: int = 0, device="cuda"):
+                 kv_e4m3: bool = False, seed: int = 0, device="cuda", kv_e2m1: bool = False):
         self.shape, self.n_variants, self.max_tokens = shape, n_variants, max_tokens
         g = synth.generator(seed, device)
         m = self.m = len(variants)
@@ -77,16 +75,22 @@ class Tenants:
         self.head = Matrix(s.vocab, s.hidden, n_variants, g)
         # norm weights of a layer's attention and MLP and of the head, per variant
         self.norms = (1 + 0.1 * torch.randn((2 * s.layers + 1, n_variants, s.hidden), generator=g, device=dev)).bfloat16()
-        self.rope = rope_table(max_tokens, s.head_dim, s.rope_base).to(dev)
+        self.rope = torch.empty((max_tokens, s.head_dim), device=dev)
+        bd.bd_rotary_table(self.rope, s.rope_base, factor=s.rope_factor, original=s.rope_original)
         pages = -(-max_tokens // page_size)
         order = torch.randperm(m * pages, generator=g, device=dev)  # a pool's free pages are in no order
         self.page_table = order.to(torch.int32).view(m, pages)
         pool = (m * pages, s.kv_heads, page_size, s.head_dim)
-        kv = torch.float8_e4m3fn if kv_e4m3 else torch.bfloat16
+        kv, scales = (torch.float8_e4m3fn, pool[:3]) if kv_e4m3 else (torch.bfloat16, None)
+        if kv_e2m1:  # two values to a byte, a scale byte for 16
+            if kv_e4m3:
+                raise ValueError("a cache holds 8 bits or 4")
+            kv, scales, pool = torch.uint8, (*pool[:3], s.head_dim // 16), (*pool[:3], s.head_dim // 2)
         self.caches = [bd.KVCache(torch.empty(pool, dtype=kv, device=dev), torch.empty(pool, dtype=kv, device=dev),
-                                  *([torch.empty(pool[:3], dtype=torch.uint8, device=dev) for _ in range(2)] if kv_e4m3 else []))
+                                  *([torch.empty(scales, dtype=torch.uint8, device=dev) for _ in range(2)] if scales else []))
                        for _ in range(s.layers)]
         self.attention_ws = torch.zeros((bd.bd_attention_workspace_size(self.caches[0], m, s.q_heads),), dtype=torch.uint8, device=dev)
+        self.prompt_ws = torch.zeros((bd.bd_attention_prompt_workspace_size(self.caches[0], s.q_heads),), dtype=torch.uint8, device=dev)
         self.linear_ws = {}
         self.modes = [bd.BD_ALPHA_SCALAR] * n_variants
         self.tokens = torch.zeros((m,), dtype=torch.int32, device=dev)     # each sequence's last token, not cached yet
@@ -151,16 +155,13 @@ class Tenants:
             tokens = prompt[start:min(start + piece, prompt.numel() - 1)]
             n, end = tokens.numel(), start + tokens.numel()
             positions = torch.arange(start, end, dtype=torch.int32, device=dev)
-            offsets = torch.tensor([0, end], dtype=torch.int32, device=dev)
-            hidden = torch.arange(end, device=dev)[None, :] > positions[:, None]
+            offsets = torch.tensor([0, n], dtype=torch.int32, device=dev)
+            length = torch.tensor([end], dtype=torch.int32, device=dev)
 
             def attend(cache, q):
-                k, v = (torch.empty((end, s.kv_heads, s.head_dim), dtype=torch.bfloat16, device=dev) for _ in range(2))
-                bd.bd_kv_read(cache, table, offsets, k, v)
-                qh = q.float().view(n, s.kv_heads, -1, s.head_dim).permute(1, 2, 0, 3)
-                scores = qh @ k.float().permute(1, 2, 0)[:, None] * s.head_dim ** -0.5
-                p = scores.masked_fill(hidden, -torch.inf).softmax(-1)
-                return (p @ v.float().permute(1, 0, 2)[:, None]).permute(2, 0, 1, 3).bfloat16().contiguous()
+                out = torch.empty_like(q)
+                bd.bd_attention_prompt(cache, q, offsets, table, length, out, self.prompt_ws, cap=s.score_cap)
+                return out
 
             self._layers(tokens, self.variants[i:i + 1].repeat(n), positions, attend,
                          torch.zeros((n,), dtype=torch.int32, device=dev), table)
@@ -173,7 +174,7 @@ class Tenants:
 
         def attend(cache, q):
             out = torch.empty_like(q)
-            bd.bd_attention_decode(cache, q, self.page_table, lengths, out, self.attention_ws)
+            bd.bd_attention_decode(cache, q, self.page_table, lengths, out, self.attention_ws, cap=self.shape.score_cap)
             return out
 
         x, h = self._layers(self.tokens, self.variants, self.positions, attend)
@@ -210,9 +211,11 @@ def main() -> None:
     ap.add_argument("--prompt", type=int, default=200, help="tokens of the longest prompt")
     ap.add_argument("--steps", type=int, default=64)
     ap.add_argument("--kv8", action="store_true", help="8-bit cache")
+    ap.add_argument("--kv4", action="store_true", help="4-bit cache")
+    ap.add_argument("--rope-factor", type=float, default=1.0, help="positions scaled for a context this many times the model's own")
     a = ap.parse_args()
     ids = synth.zipf_ids(a.sequences, a.variants, 1.1, 0).tolist()
-    t = Tenants(Shape(layers=a.layers), a.variants, ids, a.prompt + a.steps, kv_e4m3=a.kv8)
+    t = Tenants(Shape(layers=a.layers, rope_factor=a.rope_factor), a.variants, ids, a.prompt + a.steps, kv_e4m3=a.kv8, kv_e2m1=a.kv4)
     g = synth.generator(1, "cuda")
     for i in range(a.sequences):
         n = a.prompt - i * (a.prompt - 1) // a.sequences
