@@ -7,8 +7,8 @@
 //
 // Work.  A row is one query of one head; the heads that share a KV head are rows of the same tile, so that K and V are
 // read once for all of them and a tile of 128 rows holds 128 / heads tokens.  A unit is two such tiles (256 rows) of
-// one sequence and KV head, or, where units are fewer than SMs, a piece of its keys; each CTA (one per SM) takes units
-// in turn, a sequence's last tiles first, as those see the most keys.  Pieces leave their unnormalised output, maximum and sum in
+// one sequence and KV head, or, where units are fewer than SMs, a piece of its keys; each CTA (one per SM) takes the next
+// unit when it has finished one, those of most keys first.  Pieces leave their unnormalised output, maximum and sum in
 // the workspace and a second kernel joins them in key order, so results do not depend on timing.
 //
 // A CTA.  Warps 0-3 and 4-7: the softmax of one tile each, a thread per row.  Warp 8: issues the products.  Warp 9: finds
@@ -80,6 +80,7 @@ struct PromptArgs {
     const float *slopes;
     uint8_t *out;
     float *lse, *parts;
+    unsigned *taken;  // units taken, and CTAs that take no more
     int4 *heads;  // of the joining kernel: per slot, {pieces, first row of q, tokens, KV head} of a unit's first piece
     unsigned *status;
     uint64_t wait_ns;
@@ -136,9 +137,11 @@ __device__ __forceinline__ float tmem_ld_one(uint32_t taddr) {
 // Byte of 16-byte chunk c (8 columns) of row r in a tile: pieces of 64 columns, chunks turned by the row.
 __device__ __forceinline__ uint32_t tile_at(int r, int c) { return (c / 8) * (kBlock * 128) + r * 128 + (((c % 8) ^ (r & 7)) << 4); }
 
-__device__ __forceinline__ bool not_finite(uint4 v) {  // of eight bf16 numbers
-    auto two = [](uint32_t x) { return (x & 0x7F80u) == 0x7F80u || (x & 0x7F800000u) == 0x7F800000u; };
-    return two(v.x) || two(v.y) || two(v.z) || two(v.w);
+// 0 times each of a bf16 pair, added to `sum`: NaN from an infinity or NaN on.
+__device__ __forceinline__ uint32_t zero_times(uint32_t pair, uint32_t sum) {
+    uint32_t r;
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(pair), "r"(0u), "r"(sum));
+    return r;
 }
 
 // One lane of a converged warp.
@@ -224,18 +227,24 @@ __device__ __forceinline__ int64_t warp_scan(int64_t v) {  // inclusive
     return v;
 }
 
-// Warp 9.
+__device__ __forceinline__ int size_class(const Sequence &q) { return q.units > 0 ? 31 - __clz(max(q.blocks, 1)) : -1; }
+
+// Warp 9.  Units are numbered sequence by sequence, those of most keys first by powers of two, in each from its last tile to
+// its first (then pieces, then KV heads): whoever takes the next unit takes one of the largest that are left.
 __device__ __forceinline__ void find_units(const PromptArgs &a, const Smem &s) {
     const int lane = threadIdx.x % 32;
     const int vheads = a.kv_heads * a.subs, pair = 2 * a.tile_tokens;
     // blocks of a piece: as few as give every CTA a unit at most, where whole units leave CTAs without one
     int32_t most = 1 << 30;
+    unsigned classes = 0;
+    int64_t units = 0, blocks = 0;
+    for (int64_t i = lane; i < a.n_seqs; i += 32) {
+        const Sequence q = sequence_of(a, i);
+        if (q.units > 0) classes |= 1u << size_class(q);
+        units += q.units, blocks += static_cast<int64_t>(q.units) * q.blocks;
+    }
+    classes = __reduce_or_sync(0xFFFFFFFFu, classes);
     if (a.may_split) {
-        int64_t units = 0, blocks = 0;
-        for (int64_t i = lane; i < a.n_seqs; i += 32) {
-            const Sequence q = sequence_of(a, i);
-            units += q.units, blocks += static_cast<int64_t>(q.units) * q.blocks;
-        }
         units = warp_sum(units) * vheads, blocks = warp_sum(blocks) * vheads;
         if (units <= a.slots) {
             most = max(4, static_cast<int32_t>((blocks + a.slots - 1) / a.slots));
@@ -250,39 +259,38 @@ __device__ __forceinline__ void find_units(const PromptArgs &a, const Smem &s) {
             }
         }
     }
-    int64_t first = 0, before = 0;  // the 32 sequences looked at, and the units of those before them
+    int64_t first = a.n_seqs, before = 0;  // the 32 sequences looked at, and the units of those before them
+    int cls = 32;
     Sequence q = {};
-    int64_t mine = 0, upto = 0;
-    auto look = [&] {
+    int64_t mine = 0, upto = 0, all = 0;
+    auto look = [&] {  // at the next sequences; false: there are none
+        before += all;
+        first += 32;
+        if (first >= a.n_seqs) {
+            classes &= cls < 32 ? (1u << cls) - 1 : 0xFFFFFFFFu;
+            if (classes == 0) return false;
+            cls = 31 - __clz(classes);
+            first = 0;
+        }
         q = Sequence{};
         if (first + lane < a.n_seqs) q = sequence_of(a, first + lane);
-        mine = static_cast<int64_t>(q.units) * pieces_of(q, most) * vheads;
+        mine = size_class(q) == cls ? static_cast<int64_t>(q.units) * pieces_of(q, most) * vheads : 0;
         upto = warp_scan(mine);
+        all = __shfl_sync(0xFFFFFFFFu, upto, 31);
+        return true;
     };
-    look();
+    bool over = false;
     int it = 0;
-    for (int64_t round = 0;; ++round) {
-        // each round in the other direction, as units grow lighter
-        const int64_t u = round * gridDim.x + (round % 2 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
-        bool over = false;
-        while (true) {
-            const int64_t all = __shfl_sync(0xFFFFFFFFu, upto, 31);
-            if (u < before + all) break;
-            if (round * gridDim.x >= before + all && first + 32 >= a.n_seqs) {
-                over = true;
-                break;
-            }
-            if (first + 32 >= a.n_seqs) break;  // this round has no unit for this CTA
-            before += all, first += 32;
-            look();
-        }
+    for (int64_t round = 0; !over; ++round) {
+        // Where units may be split there are no more than CTAs, and CTA b takes unit b, whose slot is b.  Else the next one.
+        int64_t u = round * gridDim.x + blockIdx.x;
+        if (!a.may_split) u = __shfl_sync(0xFFFFFFFFu, lane == 0 ? atomicAdd(a.taken, 1u) : 0u, 0);
+        while (!over && u >= before + all) over = !look();
         Unit d = {};
         d.blocks = -1;
-        const int64_t all = __shfl_sync(0xFFFFFFFFu, upto, 31);
-        if (!over && u >= before + all) continue;
         if (!over) {
             const unsigned holds = __ballot_sync(0xFFFFFFFFu, u < before + upto);
-            const int owner = __ffs(holds) - 1;
+            const int owner = __ffs(holds) - 1;  // the first whose units reach beyond u
             int64_t at = u - before - __shfl_sync(0xFFFFFFFFu, upto - mine, owner);
             Sequence w;
             w.row0 = __shfl_sync(0xFFFFFFFFu, q.row0, owner), w.n = __shfl_sync(0xFFFFFFFFu, q.n, owner);
@@ -335,15 +343,16 @@ __device__ __forceinline__ void find_units(const PromptArgs &a, const Smem &s) {
             }
             if (__any_sync(0xFFFFFFFFu, gaps)) d.state |= kGaps;
         }
-        if (!wait_on(&s.u_empty[it & 1], ((it >> 1) & 1) ^ 1, a, s.abort)) return;
+        if (!wait_on(&s.u_empty[it & 1], ((it >> 1) & 1) ^ 1, a, s.abort)) break;
         if (lane == 0) {
             s.unit[it & 1] = d;
             mbar_arrive(&s.u_full[it & 1]);
         }
         __syncwarp();
         ++it;
-        if (over) return;
     }
+    // the last CTA to have taken all it takes leaves the count ready for the next call
+    if (!a.may_split && lane == 0 && atomicAdd(a.taken + 1, 1u) == gridDim.x - 1) a.taken[0] = a.taken[1] = 0;
 }
 
 // The next unit, or blocks < 0 after the last one and on give-up.
@@ -617,15 +626,23 @@ __device__ __forceinline__ void look_at_values(const PromptArgs &a, const Smem &
             if (l % 2 && seen_in_part(u, blk)) {
                 uint8_t *tile = kv + stage * kTileBytes<kDim>;
                 bool bad = false;
-#pragma unroll 8
-                for (int i = lane; i < kBlock * (kDim / 8); i += 32) {
-                    uint4 *p = reinterpret_cast<uint4 *>(tile + tile_at(i / (kDim / 8), i % (kDim / 8)));
-                    const int key = blk * kBlock + i / (kDim / 8);
-                    if (key < u.un_lo || key >= u.un_hi) *p = make_uint4(0, 0, 0, 0);
-                    else bad |= not_finite(*p);
+                // 0 times a number is added up: not 0 where one of them is not finite
+                uint32_t sum[4] = {0, 0, 0, 0};
+                const int from = max(0, u.un_lo - blk * kBlock), to = min(kBlock, u.un_hi - blk * kBlock);
+                if (from > 0 || to < kBlock) {
+                    for (int i = lane; i < kBlock * (kDim / 8); i += 32)
+                        if (i / (kDim / 8) < from || i / (kDim / 8) >= to)
+                            *reinterpret_cast<uint4 *>(tile + tile_at(i / (kDim / 8), i % (kDim / 8))) = make_uint4(0, 0, 0, 0);
+                    fence_proxy_async_smem();
+                    __syncwarp();
                 }
-                fence_proxy_async_smem();
-                bad = __any_sync(0xFFFFFFFFu, bad);
+#pragma unroll 16
+                for (int i = lane; i < kBlock * (kDim / 8); i += 32) {
+                    const uint4 x = *reinterpret_cast<const uint4 *>(tile + i * 16);
+                    sum[0] = zero_times(x.x, sum[0]), sum[1] = zero_times(x.y, sum[1]);
+                    sum[2] = zero_times(x.z, sum[2]), sum[3] = zero_times(x.w, sum[3]);
+                }
+                bad = __any_sync(0xFFFFFFFFu, ((sum[0] | sum[1] | sum[2] | sum[3]) & 0x7FFF7FFFu) != 0);
                 if (bad && lane == 0) s.slow[stage] = loads + 1;
             }
             __syncwarp();
@@ -662,7 +679,7 @@ __device__ __forceinline__ void convert_tiles(const PromptArgs &a, const Smem &s
             uint8_t *tile = kv + stage * kTileBytes<kDim>;
             const uint8_t *raw = s.raw + slot * kRawBytes<kDim, kType>, *scales = raw + kBlock * kRow<kDim, kType>;
             const bool look = l % 2 && seen_in_part(u, u.blk0 + l / 2);
-            bool bad = false;
+            uint32_t sum = 0;
 #pragma unroll 2
             for (int i = tid; i < kBlock * kPer; i += kThreads) {
                 const int key = i / kPer;
@@ -692,12 +709,13 @@ __device__ __forceinline__ void convert_tiles(const PromptArgs &a, const Smem &s
                             y[k] = bf16_pair(__nv_cvt_fp4x2_to_halfraw2(static_cast<__nv_fp4x2_storage_t>(in[o] >> k * 8 & 0xFFu), __NV_E2M1), scale[o / 2]);
                         if (gone) y[k] = 0;
                     }
-                    const uint4 out = make_uint4(y[0], y[1], y[2], y[3]);
-                    if (look) bad |= not_finite(out);
-                    *reinterpret_cast<uint4 *>(tile + tile_at(key, i % kPer * kOut + o)) = out;
+                    if (look)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) sum = zero_times(y[k], sum);
+                    *reinterpret_cast<uint4 *>(tile + tile_at(key, i % kPer * kOut + o)) = make_uint4(y[0], y[1], y[2], y[3]);
                 }
             }
-            if (bad) s.slow[stage] = loads + 1;
+            if (sum & 0x7FFF7FFFu) s.slow[stage] = loads + 1;
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) {
@@ -741,10 +759,9 @@ __device__ __noinline__ void scale_output(uint32_t t_o, float f) {
 }
 
 // P V of a block whose V is not finite where some row does not see it: row by row over the keys [from, to) that the row
-// sees.  The scores are read again one by one from tensor memory.
+// sees, whose weights are read from tensor memory in pairs.
 template <int kDim>
-__device__ __noinline__ void add_values(const PromptArgs &a, uint32_t t_s, uint32_t t_o, const uint8_t *v, bool fresh, int from, int to,
-                                        unsigned missing, float base, float slope, float far) {
+__device__ __noinline__ void add_values(uint32_t t_p, uint32_t t_o, const uint8_t *v, bool fresh, int from, int to, unsigned missing) {
 #pragma unroll 1
     for (int c = 0; c < kDim; c += 16) {
         uint32_t o[16] = {};
@@ -752,9 +769,9 @@ __device__ __noinline__ void add_values(const PromptArgs &a, uint32_t t_s, uint3
         tmem_ld_wait();
 #pragma unroll 1
         for (int k = 0; k < kBlock; ++k) {
-            const float score = ruled(a, tmem_ld_one(t_s + k), slope, far - static_cast<float>(k));
+            const uint32_t two = __float_as_uint(tmem_ld_one(t_p + k / 2));
             if (k >= from && k < to && !(missing >> k / 16 & 1)) {
-                const float w = ex2(score - base);
+                const float w = k % 2 ? bf16hi_to_f32(two) : bf16lo_to_f32(two);
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     float f[8];
@@ -873,15 +890,7 @@ __device__ __forceinline__ void softmax_rows(const PromptArgs &a, const Smem &s,
                     }
                 }
                 const float base = top == -INFINITY ? 0.f : top;
-                if (key0 < in_lo || key0 + kBlock > in_hi) {  // some row sees it in part: is V finite where it is not seen?
-                    const int load = 2 * (blocks_before + j) + 1, stage = load % kS;
-                    if (!wait_on(kType == BD_KV_BF16 ? &s.fixed[stage] : &s.full[stage], (load / kS) & 1, a, s.abort)) return;
-                    if (s.slow[stage] == load + 1) {
-                        if (j > 0 && !wait_on(&s.o_full[tile], (s_n - 1) & 1, a, s.abort)) return;
-                        tc_fence_after();
-                        add_values<kDim>(a, t_s, t_o, kv + stage * kTileBytes<kDim>, j == 0, from, to, missing, base, slope, far);
-                    }
-                }
+                const bool part = key0 < in_lo || key0 + kBlock > in_hi;  // some row sees the block in part
                 float2 add[2] = {};
                 const float2 scale2 = make_float2(scale, scale), base2 = make_float2(-base, -base);
 #pragma unroll
@@ -895,12 +904,25 @@ __device__ __forceinline__ void softmax_rows(const PromptArgs &a, const Smem &s,
                         w[i] = pack_bf16x2(e.x, e.y);
                     }
                     tmem_st_32x32b_x16(t_p + c * 16, w);
-                    if (c % 2) {  // 64 keys: their product may begin
+                    if (c % 2 && !part) {  // 64 keys: their product may begin
                         tmem_st_wait();
                         tc_fence_before();
                         __syncwarp();
                         if (lane == 0) mbar_arrive(&s.p_full[2 * tile + c / 2]);
                     }
+                }
+                if (part) {  // is V finite where it is not seen?
+                    const int load = 2 * (blocks_before + j) + 1, stage = load % kS;
+                    if (!wait_on(kType == BD_KV_BF16 ? &s.fixed[stage] : &s.full[stage], (load / kS) & 1, a, s.abort)) return;
+                    tmem_st_wait();
+                    if (s.slow[stage] == load + 1) {
+                        if (j > 0 && !wait_on(&s.o_full[tile], (s_n - 1) & 1, a, s.abort)) return;
+                        tc_fence_after();
+                        add_values<kDim>(t_p, t_o, kv + stage * kTileBytes<kDim>, j == 0, from, to, missing);
+                    }
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&s.p_full[2 * tile]), mbar_arrive(&s.p_full[2 * tile + 1]);
                 }
                 sum += (add[0].x + add[1].x) + (add[0].y + add[1].y);
                 ++s_n;
@@ -1117,7 +1139,7 @@ cudaError_t launch_dim(const PromptArgs &a, int type, const CUtensorMap &q, cons
 }  // namespace
 
 size_t prompt_workspace_size(int num_sms, int head_dim) {
-    return (head_dim == 128 ? part_bytes<128>(num_sms) : part_bytes<64>(num_sms)) + static_cast<size_t>(num_sms) * sizeof(int4);
+    return (head_dim == 128 ? part_bytes<128>(num_sms) : part_bytes<64>(num_sms)) + static_cast<size_t>(num_sms) * sizeof(int4) + 256;
 }
 
 cudaError_t launch_prompt(const bd_kv_cache &c, const void *q, int32_t q_heads, const int32_t *offsets, int64_t total,
@@ -1141,6 +1163,7 @@ cudaError_t launch_prompt(const bd_kv_cache &c, const void *q, int32_t q_heads, 
     a.parts = static_cast<float *>(workspace);
     a.heads = reinterpret_cast<int4 *>(static_cast<uint8_t *>(workspace) +
                                        (c.head_dim == 128 ? part_bytes<128>(ctx.num_sms) : part_bytes<64>(ctx.num_sms)));
+    a.taken = reinterpret_cast<unsigned *>(a.heads + ctx.num_sms);
     a.status = ctx.status;
     a.wait_ns = ctx.wait_ns;
     a.n_pages = c.n_pages;
