@@ -15,10 +15,10 @@
 // the next unit and its blocks.  Warp 10 on: K and V of the cache to a ring of shared-memory tiles, by TMA in
 // bf16 (warp 10; warp 11 looks at the blocks that some row sees only in part); 8-bit and 4-bit values are copied as they are and
 // converted by warps 11 to 15.
-// S = Q K^T goes to tensor memory; a softmax thread reads its row, and writes the weights back there as the bf16 operand of
+// S = Q K^T goes to tensor memory; a softmax thread reads its row, and writes the weights back there as the 16-bit operand of
 // P V, whose accumulator stays in tensor memory.  The two tiles alternate: one's products run under the other's softmax.
-// The running maximum is raised only when a row passes it by 2^8, so that the output is seldom rescaled: weights
-// are at most 2^8, sums stay fp32.
+// The running maximum is raised only when a row passes it by 2^8 (4 bits: 2^3), so that the output is seldom rescaled:
+// weights are at most that, sums stay fp32.
 //
 // Values that a row does not see.  A weight of 0 does not hide an infinity or NaN of V.  Blocks that some row sees in part
 // are looked at: rows of V that nobody sees are zeroed, and where a finite number is missing in another one, the
@@ -39,7 +39,15 @@ constexpr int kBlock = 128;  // keys of a block
 constexpr int kTileRows = 128;
 constexpr int64_t kMaxLength = 1 << 30;
 constexpr int kConvertWarps = 5;
-constexpr float kLazy = 8.f;  // by how much (in base 2) a row's scores may pass the maximum they are taken from
+// A 4-bit cache's values over 8 are fp16 numbers, whatever their scale, and take two operations a pair to make, bf16 ones five:
+// its products are of fp16, Q turned to fp16 in shared memory, each row times a power of two of its own, and the weights
+// times 2^kLift, so that small ones are kept (2^-11 of a weight down to 2^-26 of the largest, nothing below 2^-37).
+template <int kType>
+constexpr bool kHalf = kType == BD_KV_E2M1;
+template <int kType>
+constexpr float kLift = kHalf<kType> ? 12.f : 0.f;
+template <int kType>
+constexpr float kLazy = kHalf<kType> ? 3.f : 8.f;  // by how much (in base 2) a row's scores may pass the maximum they are taken from
 
 template <int kType>
 constexpr int kThreadsOf = kType == BD_KV_BF16 ? 384 : (11 + kConvertWarps) * 32;
@@ -90,6 +98,7 @@ struct PromptArgs {
     int32_t window, slots, box;                    // box: keys of one TMA copy
     float scale_log2, cap, cap_in;
     int32_t may_split, plain;                      // plain: scores are products times a positive scale
+    float v_unit;                                  // what V is given over
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -137,11 +146,32 @@ __device__ __forceinline__ float tmem_ld_one(uint32_t taddr) {
 // Byte of 16-byte chunk c (8 columns) of row r in a tile: pieces of 64 columns, chunks turned by the row.
 __device__ __forceinline__ uint32_t tile_at(int r, int c) { return (c / 8) * (kBlock * 128) + r * 128 + (((c % 8) ^ (r & 7)) << 4); }
 
-// 0 times each of a bf16 pair, added to `sum`: NaN from an infinity or NaN on.
+// 0 times each of a pair, added to `sum`: NaN from an infinity or NaN on.
+template <bool half>
 __device__ __forceinline__ uint32_t zero_times(uint32_t pair, uint32_t sum) {
     uint32_t r;
-    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(pair), "r"(0u), "r"(sum));
+    if constexpr (half) asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(pair), "r"(0u), "r"(sum));
+    else asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(pair), "r"(0u), "r"(sum));
     return r;
+}
+__device__ __forceinline__ uint32_t half2_times(uint32_t x, uint32_t y) {
+    uint32_t r;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
+    return r;
+}
+__device__ __forceinline__ uint32_t e2m1_pair(uint32_t byte) {  // the low byte's two values
+    uint32_t r;
+    asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, a;\n\t}" : "=r"(r) : "r"(byte));
+    return r;
+}
+__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+template <bool half>
+__device__ __forceinline__ float2 unpack_pair(uint32_t pair) {
+    if constexpr (half) return __half22float2(*reinterpret_cast<const __half2 *>(&pair));
+    else return make_float2(bf16lo_to_f32(pair), bf16hi_to_f32(pair));
 }
 
 // One lane of a converged warp.
@@ -155,7 +185,7 @@ struct Smem {
     uint64_t *full, *empty, *fixed;      // per stage
     uint64_t *raw_full, *raw_empty;      // per slot of tiles as they are in the cache
     uint8_t *raw;
-    uint64_t *q_full, *q_empty, *s_full, *p_full, *o_full;  // per tile
+    uint64_t *q_full, *q_ready, *q_empty, *s_full, *p_full, *o_full;  // per tile
     uint64_t *u_full, *u_empty;          // per unit slot
     Unit *unit;
     volatile int *slow;                  // per stage: number (from 1) of the last load of a V that is not finite and not seen by all
@@ -398,10 +428,12 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint3
         "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n\t}" ::"r"(d), "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "n"(kDescHigh)
         : "memory");
 }
+template <int kType>
+constexpr uint32_t idesc_of(int n) { return idesc_bf16_f32(kTileRows, n) & ~(kHalf<kType> ? 1u << 7 | 1u << 10 : 0u); }
 // S of a tile: Q K^T.
-template <int kDim, int kTile>
+template <int kDim, int kType, int kTile>
 __device__ __forceinline__ void issue_scores(int stage) {
-    constexpr uint32_t idesc = idesc_bf16_f32(kTileRows, kBlock);
+    constexpr uint32_t idesc = idesc_of<kType>(kBlock);
     const uint32_t q = desc_low(smem_base() + kTile * kTileBytes<kDim>, 16), k = desc_low(smem_base() + (2 + stage) * kTileBytes<kDim>, 16);
 #pragma unroll
     for (int i = 0; i < kDim / 16; ++i) {
@@ -410,12 +442,12 @@ __device__ __forceinline__ void issue_scores(int stage) {
     }
 }
 // Half of a tile's P V; V's rows are the product's inner dimension, its next 64 columns a column piece further.
-template <int kDim, int kTile, int kHalf>
+template <int kDim, int kType, int kTile, int kPart>
 __device__ __forceinline__ void issue_values(int stage, uint32_t accumulate) {
-    constexpr uint32_t idesc = idesc_bf16_f32(kTileRows, kDim) | 1u << 16;
+    constexpr uint32_t idesc = idesc_of<kType>(kDim) | 1u << 16;
     const uint32_t v = desc_low(smem_base() + (2 + stage) * kTileBytes<kDim>, kBlock * 128);
 #pragma unroll
-    for (int i = kHalf * (kBlock / 32); i < (kHalf + 1) * (kBlock / 32); ++i)
+    for (int i = kPart * (kBlock / 32); i < (kPart + 1) * (kBlock / 32); ++i)
         mma_ts(Columns<kDim>::o + kTile * kDim, Columns<kDim>::p + kTile * Columns<kDim>::p_tile + i * 8, v + i * (16 * 128 / 16), idesc,
                i > 0 ? 1u : accumulate);
 }
@@ -451,9 +483,9 @@ __device__ __forceinline__ void issue_products(const PromptArgs &a, const Smem &
     };
     auto start_tile = [&](auto tile) {
         constexpr int i = tile();
-        if (!wait_alone(&s.q_full[i], q_round[i], a, s.abort)) return false;
+        if (!wait_alone(kHalf<kType> ? &s.q_ready[i] : &s.q_full[i], q_round[i], a, s.abort)) return false;
         q_round[i] ^= 1;
-        issue_scores<kDim, i>(stage);
+        issue_scores<kDim, kType, i>(stage);
         tc_commit(&s.s_full[i]);
         if (blocks == 1) tc_commit(&s.q_empty[i]);
         return true;
@@ -479,15 +511,15 @@ __device__ __forceinline__ void issue_products(const PromptArgs &a, const Smem &
                 constexpr int i = tile();
                 if (!wait_alone(&s.p_full[2 * i], p_round[i], a, s.abort)) return false;
                 tc_fence_after();
-                if (!slow) issue_values<kDim, i, 0>(v_stage, j > 0);
+                if (!slow) issue_values<kDim, kType, i, 0>(v_stage, j > 0);
                 if (!wait_alone(&s.p_full[2 * i + 1], p_round[i], a, s.abort)) return false;
                 tc_fence_after();
                 p_round[i] ^= 1;
-                if (!slow) issue_values<kDim, i, 1>(v_stage, 1);
+                if (!slow) issue_values<kDim, kType, i, 1>(v_stage, 1);
                 tc_commit(&s.o_full[i]);
                 if (more) {
                     if (i == 0 && !wait_alone(&s.full[stage], round, a, s.abort)) return false;
-                    issue_scores<kDim, i>(stage);
+                    issue_scores<kDim, kType, i>(stage);
                     tc_commit(&s.s_full[i]);
                     if (j + 2 == blocks) tc_commit(&s.q_empty[i]);
                 }
@@ -639,8 +671,8 @@ __device__ __forceinline__ void look_at_values(const PromptArgs &a, const Smem &
 #pragma unroll 16
                 for (int i = lane; i < kBlock * (kDim / 8); i += 32) {
                     const uint4 x = *reinterpret_cast<const uint4 *>(tile + i * 16);
-                    sum[0] = zero_times(x.x, sum[0]), sum[1] = zero_times(x.y, sum[1]);
-                    sum[2] = zero_times(x.z, sum[2]), sum[3] = zero_times(x.w, sum[3]);
+                    sum[0] = zero_times<false>(x.x, sum[0]), sum[1] = zero_times<false>(x.y, sum[1]);
+                    sum[2] = zero_times<false>(x.z, sum[2]), sum[3] = zero_times<false>(x.w, sum[3]);
                 }
                 bad = __any_sync(0xFFFFFFFFu, ((sum[0] | sum[1] | sum[2] | sum[3]) & 0x7FFF7FFFu) != 0);
                 if (bad && lane == 0) s.slow[stage] = loads + 1;
@@ -654,7 +686,8 @@ __device__ __forceinline__ void look_at_values(const PromptArgs &a, const Smem &
     }
 }
 
-// Warps 11 to 15: tiles as they are in the cache to the bf16 numbers that they stand for, 16 bytes at a time.
+// Warps 11 to 15: tiles as they are in the cache to the bf16 numbers that they stand for, or fp16 ones of an eighth of that, 16 bytes
+// at a time.
 __device__ __forceinline__ uint32_t bf16_pair(__half2_raw h, uint32_t scale) {  // times a scale given twice: exact in bf16
     const float2 f = __half22float2(__half2(h));
     uint32_t r;
@@ -685,7 +718,7 @@ __device__ __forceinline__ void convert_tiles(const PromptArgs &a, const Smem &s
                 const int key = i / kPer;
                 const uint4 x = reinterpret_cast<const uint4 *>(raw)[i];
                 const uint32_t in[4] = {x.x, x.y, x.z, x.w};
-                uint32_t scale[2];  // as a bf16 number, twice
+                uint32_t scale[2];  // as a bf16 or fp16 number, twice
                 if constexpr (kType == BD_KV_E4M3) {
                     const uint32_t b = static_cast<uint32_t>(scales[key]) << 7;
                     scale[0] = scale[1] = b | b << 16;
@@ -693,8 +726,8 @@ __device__ __forceinline__ void convert_tiles(const PromptArgs &a, const Smem &s
                     const uint32_t two = *reinterpret_cast<const uint16_t *>(scales + key * kSc + i % kPer * 2);
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        const float f = __half2float(__ushort_as_half(static_cast<unsigned short>((two >> 8 * e & 0xFFu) << 7)));
-                        scale[e] = pack_bf16x2(f, f);
+                        const uint32_t b = (two >> 8 * e & 0xFFu) << 7;
+                        scale[e] = half2_times(b | b << 16, 0x30003000u);  // an eighth: exact, to 2^-20 of its subnormals
                     }
                 }
                 const bool gone = look && (key0 + key < u.un_lo || key0 + key >= u.un_hi);
@@ -706,12 +739,12 @@ __device__ __forceinline__ void convert_tiles(const PromptArgs &a, const Smem &s
                         if constexpr (kType == BD_KV_E4M3)
                             y[k] = bf16_pair(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(in[2 * o + k / 2] >> k % 2 * 16 & 0xFFFFu), __NV_E4M3), scale[0]);
                         else
-                            y[k] = bf16_pair(__nv_cvt_fp4x2_to_halfraw2(static_cast<__nv_fp4x2_storage_t>(in[o] >> k * 8 & 0xFFu), __NV_E2M1), scale[o / 2]);
+                            y[k] = half2_times(e2m1_pair(in[o] >> k * 8), scale[o / 2]);
                         if (gone) y[k] = 0;
                     }
                     if (look)
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) sum = zero_times(y[k], sum);
+                        for (int k = 0; k < 4; ++k) sum = zero_times<kHalf<kType>>(y[k], sum);
                     *reinterpret_cast<uint4 *>(tile + tile_at(key, i % kPer * kOut + o)) = make_uint4(y[0], y[1], y[2], y[3]);
                 }
             }
@@ -737,8 +770,8 @@ __device__ __forceinline__ void tmem_ld_x16(uint32_t taddr, uint32_t (&o)[16]) {
 }
 
 // A product's score in base 2 under the rule: `far` positions before the query.
-__device__ __forceinline__ float ruled(const PromptArgs &a, float v, float slope, float far) {
-    v *= a.scale_log2;
+__device__ __forceinline__ float ruled(const PromptArgs &a, float v, float scale, float slope, float far) {
+    v *= scale;
     if (a.cap > 0.f) v = a.cap * (1.f - __fdividef(2.f, 1.f + ex2(v * a.cap_in)));
     return fmaf(-slope, fabsf(far), v);
 }
@@ -760,7 +793,7 @@ __device__ __noinline__ void scale_output(uint32_t t_o, float f) {
 
 // P V of a block whose V is not finite where some row does not see it: row by row over the keys [from, to) that the row
 // sees, whose weights are read from tensor memory in pairs.
-template <int kDim>
+template <int kDim, bool half>
 __device__ __noinline__ void add_values(uint32_t t_p, uint32_t t_o, const uint8_t *v, bool fresh, int from, int to, unsigned missing) {
 #pragma unroll 1
     for (int c = 0; c < kDim; c += 16) {
@@ -771,13 +804,17 @@ __device__ __noinline__ void add_values(uint32_t t_p, uint32_t t_o, const uint8_
         for (int k = 0; k < kBlock; ++k) {
             const uint32_t two = __float_as_uint(tmem_ld_one(t_p + k / 2));
             if (k >= from && k < to && !(missing >> k / 16 & 1)) {
-                const float w = k % 2 ? bf16hi_to_f32(two) : bf16lo_to_f32(two);
+                const float w = k % 2 ? unpack_pair<half>(two).y : unpack_pair<half>(two).x;
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    float f[8];
-                    unpack8(*reinterpret_cast<const uint4 *>(v + tile_at(k, c / 8 + h)), f);
+                    const uint4 x = *reinterpret_cast<const uint4 *>(v + tile_at(k, c / 8 + h));
+                    const uint32_t in[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) o[8 * h + i] = __float_as_uint(fmaf(w, f[i], __uint_as_float(o[8 * h + i])));
+                    for (int i = 0; i < 4; ++i) {
+                        const float2 f = unpack_pair<half>(in[i]);
+                        o[8 * h + 2 * i] = __float_as_uint(fmaf(w, f.x, __uint_as_float(o[8 * h + 2 * i])));
+                        o[8 * h + 2 * i + 1] = __float_as_uint(fmaf(w, f.y, __uint_as_float(o[8 * h + 2 * i + 1])));
+                    }
                 }
             }
             __syncwarp();
@@ -802,6 +839,30 @@ __device__ __noinline__ unsigned missing_pieces(const PromptArgs &a, const Unit 
     return ~__ballot_sync(0xFFFFFFFFu, fine) & 0xFFu;
 }
 
+// A row of Q in shared memory to fp16, times the power of two that brings its largest value to [2^14, 2^15), so that values down to
+// 2^-31 of it are as they were; what the products have to be multiplied by (NaN for a row that is not finite).
+template <int kDim>
+__device__ __forceinline__ float query_to_half(uint8_t *q, int r) {
+    uint32_t top2 = 0;
+#pragma unroll 4
+    for (int c = 0; c < kDim / 8; ++c) {
+        const uint4 x = *reinterpret_cast<const uint4 *>(q + tile_at(r, c));
+        top2 = __vmaxu2(__vmaxu2(top2, x.x & 0x7FFF7FFFu), __vmaxu2(x.y & 0x7FFF7FFFu, __vmaxu2(x.z & 0x7FFF7FFFu, x.w & 0x7FFF7FFFu)));
+    }
+    const uint32_t top = max(top2 & 0xFFFFu, top2 >> 16);
+    int e = static_cast<int>(top >> 7);
+    e = e < 27 || e > 227 ? 127 : e;  // zeros, and rows next to zero or infinity
+    const float up = __uint_as_float(static_cast<uint32_t>(254 + 14 - e) << 23);
+#pragma unroll 4
+    for (int c = 0; c < kDim / 8; ++c) {
+        uint4 *p = reinterpret_cast<uint4 *>(q + tile_at(r, c));
+        const uint4 x = *p;
+        auto turn = [&](uint32_t v) { return pack_half2(bf16lo_to_f32(v) * up, bf16hi_to_f32(v) * up); };
+        *p = make_uint4(turn(x.x), turn(x.y), turn(x.z), turn(x.w));
+    }
+    return top >= 0x7F80u ? NAN : __uint_as_float(static_cast<uint32_t>(e - 14 + 3) << 23);  // keys enter as an eighth
+}
+
 template <int kDim, int kType>
 __device__ __forceinline__ void softmax_rows(const PromptArgs &a, const Smem &s, uint32_t tmem, const uint8_t *kv) {
     constexpr int kS = kStages<kDim, kType>;
@@ -810,6 +871,7 @@ __device__ __forceinline__ void softmax_rows(const PromptArgs &a, const Smem &s,
     const uint32_t t_s = lane_base + tile * kBlock, t_o = lane_base + 2 * kBlock + tile * kDim;
     const uint32_t t_p = kDim == 128 ? t_s : lane_base + 2 * kBlock + 2 * kDim + tile * (kBlock / 2);
     int s_n = 0, blocks_before = 0;
+    [[maybe_unused]] uint32_t q_round = 0;
     for (int it = 0;; ++it) {
         if (!wait_on(&s.u_full[it & 1], (it >> 1) & 1, a, s.abort)) return;
         const Unit &u = s.unit[it & 1];  // held until its rows are written
@@ -837,6 +899,16 @@ __device__ __forceinline__ void softmax_rows(const PromptArgs &a, const Smem &s,
             }
             const int key_first = u.blk0 * kBlock, in_lo = u.in_lo, in_hi = u.in_hi;
             const bool gaps = u.state & kGaps;
+            float unit = a.scale_log2;  // of a product
+            if constexpr (kHalf<kType>)
+                if (blocks > 0) {
+                    if (!wait_on(&s.q_full[tile], q_round, a, s.abort)) return;
+                    q_round ^= 1;
+                    unit *= query_to_half<kDim>(const_cast<uint8_t *>(kv) - (2 - tile) * kTileBytes<kDim>, r);
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&s.q_ready[tile]);
+                }
             float top = -INFINITY, sum = 0.f;
             for (int j = 0; j < blocks; ++j) {
                 const int key0 = key_first + j * kBlock;
@@ -852,7 +924,7 @@ __device__ __forceinline__ void softmax_rows(const PromptArgs &a, const Smem &s,
                     for (int c = 0; c < 4; ++c)
 #pragma unroll
                         for (int i = 0; i < 32; ++i)
-                            x[c][i] = __float_as_uint(ruled(a, __uint_as_float(x[c][i]), slope, far - static_cast<float>(c * 32 + i)));
+                            x[c][i] = __float_as_uint(ruled(a, __uint_as_float(x[c][i]), unit, slope, far - static_cast<float>(c * 32 + i)));
                 }
                 const int from = lo - key0, to = hi - key0;
                 unsigned missing = 0;
@@ -866,7 +938,7 @@ __device__ __forceinline__ void softmax_rows(const PromptArgs &a, const Smem &s,
                             if (k < from || k >= to || (missing >> k / 16 & 1)) x[c][i] = 0xFF800000u;  // -infinity
                         }
                 }
-                const float scale = a.plain ? a.scale_log2 : 1.f;
+                const float scale = a.plain ? unit : 1.f;
                 float most[4];
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
@@ -876,7 +948,7 @@ __device__ __forceinline__ void softmax_rows(const PromptArgs &a, const Smem &s,
                     most[c] = fmaxf(most[c], __uint_as_float(x[c][31]));
                 }
                 const float now = fmaxf(fmaxf(most[0], most[1]), fmaxf(most[2], most[3])) * scale;
-                const bool raise = now > top + kLazy || (top == -INFINITY && now > top);
+                const bool raise = now > top + kLazy<kType> || (top == -INFINITY && now > top);
                 if (__any_sync(0xFFFFFFFFu, raise)) {
                     float fix = 1.f;
                     if (raise) {
@@ -889,7 +961,7 @@ __device__ __forceinline__ void softmax_rows(const PromptArgs &a, const Smem &s,
                         scale_output<kDim>(t_o, fix);
                     }
                 }
-                const float base = top == -INFINITY ? 0.f : top;
+                const float base = (top == -INFINITY ? 0.f : top) - kLift<kType>;
                 const bool part = key0 < in_lo || key0 + kBlock > in_hi;  // some row sees the block in part
                 float2 add[2] = {};
                 const float2 scale2 = make_float2(scale, scale), base2 = make_float2(-base, -base);
@@ -901,7 +973,7 @@ __device__ __forceinline__ void softmax_rows(const PromptArgs &a, const Smem &s,
                         float2 e = fma2(make_float2(__uint_as_float(x[c][2 * i]), __uint_as_float(x[c][2 * i + 1])), scale2, base2);
                         e.x = ex2(e.x), e.y = ex2(e.y);
                         add[i % 2] = add2(add[i % 2], e);
-                        w[i] = pack_bf16x2(e.x, e.y);
+                        w[i] = kHalf<kType> ? pack_half2(e.x, e.y) : pack_bf16x2(e.x, e.y);
                     }
                     tmem_st_32x32b_x16(t_p + c * 16, w);
                     if (c % 2 && !part) {  // 64 keys: their product may begin
@@ -918,7 +990,7 @@ __device__ __forceinline__ void softmax_rows(const PromptArgs &a, const Smem &s,
                     if (s.slow[stage] == load + 1) {
                         if (j > 0 && !wait_on(&s.o_full[tile], (s_n - 1) & 1, a, s.abort)) return;
                         tc_fence_after();
-                        add_values<kDim>(t_p, t_o, kv + stage * kTileBytes<kDim>, j == 0, from, to, missing);
+                        add_values<kDim, kHalf<kType>>(t_p, t_o, kv + stage * kTileBytes<kDim>, j == 0, from, to, missing);
                     }
                     tc_fence_before();
                     __syncwarp();
@@ -937,7 +1009,8 @@ __device__ __forceinline__ void softmax_rows(const PromptArgs &a, const Smem &s,
             if (!whole && in_bounds(u.slot < a.slots, a.status)) part = a.parts + u.slot * kSlotFloats<kDim> + tile * (kTileRows * (kDim + 2));
             if (none || blocks == 0) sum = 0.f, top = -INFINITY;
             const bool empty = sum == 0.f;
-            const float inv = empty ? 0.f : 1.f / sum;
+            const float inv = empty ? 0.f : (kHalf<kType> ? 8.f : 1.f) / sum;
+            top -= kLift<kType>;
             uint8_t *dst = a.out + (row * a.q_heads + head) * (kDim * 2);
 #pragma unroll 1
             for (int c = 0; c < kDim; c += 32) {
@@ -997,11 +1070,12 @@ __global__ void __launch_bounds__(kThreadsOf<kType>, 1)
     s.q_full = bars, s.q_empty = bars + 2, s.s_full = bars + 4, s.o_full = bars + 6;  // o_full[2]: the last products
     s.p_full = bars + 9;                                                            // of each tile: the first and second 64 keys
     s.u_full = bars + 13, s.u_empty = bars + 15;
-    s.unit = reinterpret_cast<Unit *>(bars + 17);
+    s.q_ready = bars + 17;
+    s.unit = reinterpret_cast<Unit *>(bars + 19);
     s.slow = reinterpret_cast<volatile int *>(s.unit + 2);
     s.abort = s.slow + kS;
     s.tmem = const_cast<uint32_t *>(reinterpret_cast<volatile uint32_t *>(s.abort + 1));
-    static_assert(kRawSlots<kDim, kType> <= 4 && (3 * kS + 25) * 8 + 2 * sizeof(Unit) + (kS + 2) * 4 <= 1024);
+    static_assert(kRawSlots<kDim, kType> <= 4 && (3 * kS + 27) * 8 + 2 * sizeof(Unit) + (kS + 2) * 4 <= 1024);
     const int warp = threadIdx.x / 32;
     pdl_trigger_and_wait();
     if (threadIdx.x == 0) {
@@ -1014,7 +1088,7 @@ __global__ void __launch_bounds__(kThreadsOf<kType>, 1)
             s.slow[i] = 0;
         }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&s.q_full[i], 1), mbar_init(&s.q_empty[i], 1);
+            mbar_init(&s.q_full[i], 1), mbar_init(&s.q_ready[i], 4), mbar_init(&s.q_empty[i], 1);
             mbar_init(&s.s_full[i], 1), mbar_init(&s.o_full[i], 1);
             mbar_init(&s.p_full[2 * i], 4), mbar_init(&s.p_full[2 * i + 1], 4);
             mbar_init(&s.u_full[i], 1), mbar_init(&s.u_empty[i], 10 + (kConvert ? kConvertWarps : 1));
@@ -1092,7 +1166,7 @@ __global__ void __launch_bounds__(kJoinThreads) prompt_join_kernel(const __grid_
             o[i].x = fmaf(y.x, f, o[i].x), o[i].y = fmaf(y.y, f, o[i].y), o[i].z = fmaf(y.z, f, o[i].z), o[i].w = fmaf(y.w, f, o[i].w);
         }
     }
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    const float inv = sum == 0.f ? 0.f : a.v_unit / sum;
     uint2 *dst = reinterpret_cast<uint2 *>(a.out + (row * a.q_heads + head) * (kDim * 2)) + eighth * (kDim / 32);
 #pragma unroll
     for (int i = 0; i < kDim / 32; ++i)
@@ -1184,6 +1258,7 @@ cudaError_t launch_prompt(const bd_kv_cache &c, const void *q, int32_t q_heads, 
     a.scale_log2 = rule.scale * kLog2e;
     a.cap = rule.cap * kLog2e;
     a.cap_in = rule.cap > 0.f ? 2.f / rule.cap : 0.f;
+    a.v_unit = c.kv_type == BD_KV_E2M1 ? 8.f : 1.f;
     a.plain = rule.scale > 0.f && !(rule.cap > 0.f) && !rule.slopes;
     // the units are at least this many (offsets[n_seqs] = total): more than CTAs are not split
     const int64_t units = (total + 2 * a.tile_tokens - 1) / (2 * a.tile_tokens) * c.kv_heads * a.subs;
