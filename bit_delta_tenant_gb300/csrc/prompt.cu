@@ -50,7 +50,7 @@ template <int kType>
 constexpr float kLazy = kHalf<kType> ? 3.f : 8.f;  // by how much (in base 2) a row's scores may pass the maximum they are taken from
 
 template <int kType>
-constexpr int kThreadsOf = kType == BD_KV_BF16 ? 384 : (11 + kConvertWarps) * 32;
+constexpr int kThreadsOf = kType == BD_KV_BF16 ? 384 : 512;
 template <int kDim>
 constexpr uint32_t kTileBytes = kBlock * kDim * 2;  // of K, V or Q in shared memory: columns in pieces of 64, swizzled
 // K and V tiles in shared memory; 8 and 4 bits: and tiles as they are in the cache, with their scale bytes behind the values
@@ -146,12 +146,10 @@ __device__ __forceinline__ float tmem_ld_one(uint32_t taddr) {
 // Byte of 16-byte chunk c (8 columns) of row r in a tile: pieces of 64 columns, chunks turned by the row.
 __device__ __forceinline__ uint32_t tile_at(int r, int c) { return (c / 8) * (kBlock * 128) + r * 128 + (((c % 8) ^ (r & 7)) << 4); }
 
-// 0 times each of a pair, added to `sum`: NaN from an infinity or NaN on.
-template <bool half>
+// 0 times each of a bf16 pair, added to `sum`: NaN from an infinity or NaN on.
 __device__ __forceinline__ uint32_t zero_times(uint32_t pair, uint32_t sum) {
     uint32_t r;
-    if constexpr (half) asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(pair), "r"(0u), "r"(sum));
-    else asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(pair), "r"(0u), "r"(sum));
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(pair), "r"(0u), "r"(sum));
     return r;
 }
 __device__ __forceinline__ uint32_t half2_times(uint32_t x, uint32_t y) {
@@ -671,8 +669,8 @@ __device__ __forceinline__ void look_at_values(const PromptArgs &a, const Smem &
 #pragma unroll 16
                 for (int i = lane; i < kBlock * (kDim / 8); i += 32) {
                     const uint4 x = *reinterpret_cast<const uint4 *>(tile + i * 16);
-                    sum[0] = zero_times<false>(x.x, sum[0]), sum[1] = zero_times<false>(x.y, sum[1]);
-                    sum[2] = zero_times<false>(x.z, sum[2]), sum[3] = zero_times<false>(x.w, sum[3]);
+                    sum[0] = zero_times(x.x, sum[0]), sum[1] = zero_times(x.y, sum[1]);
+                    sum[2] = zero_times(x.z, sum[2]), sum[3] = zero_times(x.w, sum[3]);
                 }
                 bad = __any_sync(0xFFFFFFFFu, ((sum[0] | sum[1] | sum[2] | sum[3]) & 0x7FFF7FFFu) != 0);
                 if (bad && lane == 0) s.slow[stage] = loads + 1;
@@ -698,9 +696,15 @@ template <int kDim, int kType>
 __device__ __forceinline__ void convert_tiles(const PromptArgs &a, const Smem &s, uint8_t *kv) {
     constexpr int kS = kStages<kDim, kType>, kRaw = kRawSlots<kDim, kType>, kSc = kScale<kDim, kType>;
     constexpr int kPer = kRow<kDim, kType> / 16;       // 16-byte pieces of a key
-    constexpr int kOut = kType == BD_KV_E4M3 ? 2 : 4;  // and of bf16 that each makes
-    constexpr int kThreads = kConvertWarps * 32;
-    const int lane = threadIdx.x % 32, tid = threadIdx.x - 11 * 32;
+    constexpr int kOut = kType == BD_KV_E4M3 ? 2 : 4;  // and of 16-bit numbers that each makes
+    constexpr int kThreads = kConvertWarps * 32, kEach = (kBlock * kPer + kThreads - 1) / kThreads;
+    constexpr int kStep = kThreads / kPer;             // from a thread's key to its next
+    static_assert(kThreads % kPer == 0 && kStep % 4 == 0);
+    const int lane = threadIdx.x % 32, tid = threadIdx.x - 11 * 32, key_first = tid / kPer;
+    // The swizzle turns with the key: by nothing from one to the next, or by 4 pieces there and back
+    uint32_t at[kOut];
+#pragma unroll
+    for (int o = 0; o < kOut; ++o) at[o] = tile_at(key_first, tid % kPer * kOut + o);
     int it = 0, loads = 0;
     while (true) {
         const Unit u = next_unit(a, s, it);
@@ -708,47 +712,61 @@ __device__ __forceinline__ void convert_tiles(const PromptArgs &a, const Smem &s
         for (int l = 0; l < 2 * u.blocks; ++l, ++loads) {
             const int stage = loads % kS, slot = loads % kRaw, key0 = (u.blk0 + l / 2) * kBlock;
             if (!wait_on(&s.raw_full[slot], (loads / kRaw) & 1, a, s.abort)) return;
-            if (!wait_on(&s.empty[stage], ((loads / kS) & 1) ^ 1, a, s.abort)) return;
             uint8_t *tile = kv + stage * kTileBytes<kDim>;
             const uint8_t *raw = s.raw + slot * kRawBytes<kDim, kType>, *scales = raw + kBlock * kRow<kDim, kType>;
-            const bool look = l % 2 && seen_in_part(u, u.blk0 + l / 2);
-            uint32_t sum = 0;
-#pragma unroll 2
-            for (int i = tid; i < kBlock * kPer; i += kThreads) {
-                const int key = i / kPer;
-                const uint4 x = reinterpret_cast<const uint4 *>(raw)[i];
-                const uint32_t in[4] = {x.x, x.y, x.z, x.w};
-                uint32_t scale[2];  // as a bf16 or fp16 number, twice
-                if constexpr (kType == BD_KV_E4M3) {
-                    const uint32_t b = static_cast<uint32_t>(scales[key]) << 7;
-                    scale[0] = scale[1] = b | b << 16;
-                } else {
-                    const uint32_t two = *reinterpret_cast<const uint16_t *>(scales + key * kSc + i % kPer * 2);
+            uint4 in[kEach];
+            uint32_t sc[kEach];
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const uint32_t b = (two >> 8 * e & 0xFFu) << 7;
-                        scale[e] = half2_times(b | b << 16, 0x30003000u);  // an eighth: exact, to 2^-20 of its subnormals
+            for (int e = 0; e < kEach; ++e) {
+                in[e] = make_uint4(0, 0, 0, 0), sc[e] = 0;
+                if (key_first + e * kStep >= kBlock) continue;
+                in[e] = reinterpret_cast<const uint4 *>(raw)[tid + e * kThreads];
+                if constexpr (kType == BD_KV_E4M3) sc[e] = scales[key_first + e * kStep];
+                else sc[e] = *reinterpret_cast<const uint16_t *>(scales + (key_first + e * kStep) * kSc + tid % kPer * 2);
+            }
+            bool bad = false;
+            if (l % 2 && seen_in_part(u, u.blk0 + l / 2)) {  // rows that nobody sees are zeros; is another one not finite?
+#pragma unroll
+                for (int e = 0; e < kEach; ++e) {
+                    const int key = key0 + key_first + e * kStep;
+                    if (key < u.un_lo || key >= u.un_hi) in[e] = make_uint4(0, 0, 0, 0), sc[e] = 0;
+                    if constexpr (kType == BD_KV_E4M3) {  // a NaN byte, or a scale that may take a number past bf16's largest
+                        auto nan = [](uint32_t x) { return (((x & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) != 0; };
+                        bad |= nan(in[e].x) || nan(in[e].y) || nan(in[e].z) || nan(in[e].w) || sc[e] >= 246;
+                    } else {  // scales alone can be
+                        bad |= (sc[e] & 0xFFu) >= 0xF8u || sc[e] >> 8 >= 0xF8u;
                     }
                 }
-                const bool gone = look && (key0 + key < u.un_lo || key0 + key >= u.un_hi);
+            }
+            if (!wait_on(&s.empty[stage], ((loads / kS) & 1) ^ 1, a, s.abort)) return;
+            if (bad) s.slow[stage] = loads + 1;
+#pragma unroll
+            for (int e = 0; e < kEach; ++e) {
+                if (key_first + e * kStep >= kBlock) continue;
+                const uint32_t x[4] = {in[e].x, in[e].y, in[e].z, in[e].w};
+                uint32_t scale[2];  // as a bf16 or fp16 number, twice
+                if constexpr (kType == BD_KV_E4M3) {
+                    scale[0] = scale[1] = sc[e] << 7 | sc[e] << 23;
+                } else {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const uint32_t b = (sc[e] >> 8 * h & 0xFFu) << 7;
+                        scale[h] = half2_times(b | b << 16, 0x30003000u);  // an eighth: exact, to 2^-20 of its subnormals
+                    }
+                }
 #pragma unroll
                 for (int o = 0; o < kOut; ++o) {
                     uint32_t y[4];
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
                         if constexpr (kType == BD_KV_E4M3)
-                            y[k] = bf16_pair(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(in[2 * o + k / 2] >> k % 2 * 16 & 0xFFFFu), __NV_E4M3), scale[0]);
+                            y[k] = bf16_pair(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(x[2 * o + k / 2] >> k % 2 * 16 & 0xFFFFu), __NV_E4M3), scale[0]);
                         else
-                            y[k] = half2_times(e2m1_pair(in[o] >> k * 8), scale[o / 2]);
-                        if (gone) y[k] = 0;
+                            y[k] = half2_times(e2m1_pair(x[o] >> k * 8), scale[o / 2]);
                     }
-                    if (look)
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) sum = zero_times<kHalf<kType>>(y[k], sum);
-                    *reinterpret_cast<uint4 *>(tile + tile_at(key, i % kPer * kOut + o)) = make_uint4(y[0], y[1], y[2], y[3]);
+                    *reinterpret_cast<uint4 *>(tile + (at[o] ^ (kStep % 8 ? e % 2 * 64 : 0)) + e * kStep * 128) = make_uint4(y[0], y[1], y[2], y[3]);
                 }
             }
-            if (sum & 0x7FFF7FFFu) s.slow[stage] = loads + 1;
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) {
