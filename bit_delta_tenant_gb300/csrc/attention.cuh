@@ -196,9 +196,12 @@ template <int kDim, int kType>
 constexpr int stage_bytes() {  // K tile, V tile, and their scale bytes
     return 2 * kTileOf<kType> * (row_bytes<kDim, kType>() + scale_bytes<kDim, kType>());
 }
+// tiles in a warp's ring: one in use, the others in flight
+template <int kType>
+constexpr int kDepthOf = kType == kE2m1 ? 4 : kDepth;
 template <int kDim, int kType>
 constexpr int smem_bytes() {
-    return kWarps * kDepth * stage_bytes<kDim, kType>();
+    return kWarps * kDepthOf<kType> * stage_bytes<kDim, kType>();
 }
 
 // CTAs per SM: the second column tile of more than 8 heads takes the registers of the third CTA.
@@ -217,7 +220,7 @@ __device__ __forceinline__ void stream(const AttnArgs &a, uint8_t *smem, const S
     constexpr int kChunks = kRow / 16;
     constexpr int kPiece = 16 * kRow;             // bytes of 16 keys
     constexpr int kTileBytes = kSub * kPiece;
-    constexpr int kStage = stage_bytes<kDim, kType>();
+    constexpr int kStage = stage_bytes<kDim, kType>(), kRing = kDepthOf<kType>;
     constexpr int kHalves = kPack ? 1 : 2;   // column tiles of 8 heads
     constexpr int kSteps = kFour ? kDim / 16 : kRow / 32;  // k steps of Q K^T: 32 bytes of a key each (4 bits: 8)
     constexpr int kRowTiles = kDim / 16;     // row tiles of V^T P^T
@@ -230,7 +233,7 @@ __device__ __forceinline__ void stream(const AttnArgs &a, uint8_t *smem, const S
     const int vheads = a.kv_heads * a.subs;
     Span sp = span_of<kBlock, kScored>(a, b);
     int vh = alone ? 0 : static_cast<int>(quotient(begin - units_before * vheads, sp.units));
-    const uint32_t ring = smem_u32(smem) + warp * (kDepth * kStage);
+    const uint32_t ring = smem_u32(smem) + warp * (kRing * kStage);
     // Lane offsets that repeat: the swizzle turns with the row, so a copy has kTurns of them and a
     // fragment load one per chunk pair within 128 bytes; everything else is a constant.
     constexpr int kTurns = kChunks < 4 ? 1 : kChunks / 4, kPairs = kSteps < 4 ? kSteps : 4;
@@ -241,7 +244,7 @@ __device__ __forceinline__ void stream(const AttnArgs &a, uint8_t *smem, const S
 #pragma unroll
         for (int k = 0; k < kPairs; ++k)
             load_at[k] = ring + tile_at<kRow>(lane % 8 + lane / 16 * 8, 2 * k + lane / 8 % 2);
-    const uint8_t *ring_ptr = smem + warp * (kDepth * kStage);
+    const uint8_t *ring_ptr = smem + warp * (kRing * kStage);
 
     for (int64_t at = begin; at < end;) {
         if (alone) {
@@ -412,9 +415,9 @@ __device__ __forceinline__ void stream(const AttnArgs &a, uint8_t *smem, const S
         };
         // one tile: the copy of the next one is started, then this one is waited for and used
         auto step = [&](int j, const int slot) {
-            load(j + 1, slot ^ 1);
+            load(j + kRing - 1, (slot + kRing - 1) % kRing);
             cp_commit();
-            cp_wait<1>();
+            cp_wait<kRing - 1>();
             __syncwarp();
             const int key0 = key_first + j * stride_keys;
             if (key0 < sp.len && key0 + kTile > sp.start) {
@@ -695,11 +698,18 @@ __device__ __forceinline__ void stream(const AttnArgs &a, uint8_t *smem, const S
             bad &= ~(((1u << kSub) - 1) << slot * kSub);
             __syncwarp();  // the slot may be refilled
         };
-        load(0, 0);
-        cp_commit();
-        for (int j = 0; j < n; j += 2) {
-            step(j, 0);
-            if (j + 1 < n) step(j + 1, 1);
+#pragma unroll
+        for (int j = 0; j + 1 < kRing; ++j) {
+            load(j, j);
+            cp_commit();
+        }
+        if constexpr (kRing == 2) {
+            for (int j = 0; j < n; j += 2) {
+                step(j, 0);
+                if (j + 1 < n) step(j + 1, 1);
+            }
+        } else {  // the code of a step once: four times it is more than the instruction caches hold well
+            for (int j = 0; j < n; ++j) step(j, j % kRing);
         }
         cp_wait<0>();
         __syncwarp();
@@ -708,9 +718,9 @@ __device__ __forceinline__ void stream(const AttnArgs &a, uint8_t *smem, const S
         // the warps' states in shared memory, [warp][row][kStride], where a warp alone keeps to its ring
         constexpr int kUsed = 8 * kHalves;
         constexpr int kStride = kDim + 4;  // rows of heads 2t fall into different banks
-        static_assert(kUsed * kStride * 4 <= kDepth * kStage && kStage % 16 == 0);
+        static_assert(kUsed * kStride * 4 <= kRing * kStage && kStage % 16 == 0);
         float *merge = reinterpret_cast<float *>(smem);
-        float *own = alone ? reinterpret_cast<float *>(smem + warp * (kDepth * kStage)) : merge + warp * kUsed * kStride;
+        float *own = alone ? reinterpret_cast<float *>(smem + warp * (kRing * kStage)) : merge + warp * kUsed * kStride;
 #pragma unroll
         for (int h = 0; h < kHalves; ++h) {
             l[h] += __shfl_xor_sync(0xFFFFFFFFu, l[h], 1);

@@ -10,7 +10,7 @@ constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kRows = 16;  // query heads of one tile
 constexpr int kMaxCtasPerSm = 3;
-constexpr int kDepth = 2;  // tiles in a warp's ring: one in use, one in flight
+constexpr int kDepth = 2;  // tiles in a warp's ring: one in use, one in flight (4 bits: three)
 constexpr int64_t kMaxKeys = 1 << 30;  // the division by the page size is exact, positions stay int32
 constexpr int kSlotFloats = kRows * 128 + 2 * kRows;  // a part's output, maxima and sums
 constexpr int64_t kAloneKeys = 512;  // keys of a head that a warp may be given by itself

@@ -50,12 +50,44 @@ __device__ __forceinline__ int scale_byte(float top) {
     return min(max(e, 127 - 60), 127 + 120);
 }
 
+// Scale byte of a group in 4 bits: top / 6 to the nearest of 5 bits of exponent and 3 of mantissa.
+__device__ __forceinline__ uint32_t group_scale_byte(float top) {
+    const float t = __fdiv_rn(top, 6.f);
+    if (t < 6.103515625e-5f) return static_cast<uint32_t>(__float2int_rn(t * 131072.f));  // below 2^-14: steps of 2^-17
+    const uint32_t b = __float_as_uint(t);
+    const uint32_t r = (b + 0x7FFFFu + (b >> 20 & 1u)) >> 20;  // 3 mantissa bits, ties to even
+    return min(r - ((127u - 15u) << 3), 0xF7u);
+}
+__device__ __forceinline__ float group_scale(uint32_t byte) { return __half2float(__ushort_as_half(static_cast<unsigned short>(byte << 7))); }
+// Eight values of a group with its scale byte, in 4 bits.  A quotient, not a product with 1 / s: many values of a group lie on a
+// tie between two codes.
+__device__ __forceinline__ uint32_t eight_e2m1(const float (&x)[8], uint32_t byte) {
+    const float scale = group_scale(byte);
+    auto over = [&](float v) { return byte ? __fdiv_rn(v, scale) : copysignf(0.f, v); };
+    uint32_t b = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        b |= static_cast<uint32_t>(__nv_cvt_float2_to_fp4x2(make_float2(over(x[2 * j]), over(x[2 * j + 1])), __NV_E2M1, cudaRoundNearest)) << 8 * j;
+    return b;
+}
+// The largest finite magnitude of eight values, and whether one is NaN.
+__device__ __forceinline__ float finite_top(const float (&x)[8], bool &nan) {
+    float top = 0.f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        if (fabsf(x[j]) < INFINITY) top = fmaxf(top, fabsf(x[j]));
+        nan |= x[j] != x[j];
+    }
+    return top;
+}
+
 // One CTA per token; rows are its q heads, then k heads, then v heads.  A lane holds 8 elements of a row's lower
 // half and the 8 they are rotated with, so the rotation needs no exchange: with one 16-byte piece per lane, whose
 // partner is half a row of lanes away, the kernel was bound by its instructions (8 prompts of up to 4096 tokens, 64
 // and 8 heads: 49 us).
-template <int kDim, bool kE4m3>
+template <int kDim, int kType>
 __global__ void __launch_bounds__(kAppendThreads, 5) kv_append_kernel(const AppendArgs a) {
+    constexpr bool kE4m3 = kType == BD_KV_E4M3;
     constexpr int kLanes = kDim / 16;  // lanes of one row
     constexpr int kRowsPerPass = kAppendThreads / kLanes;
     pdl_trigger_and_wait();
@@ -136,13 +168,31 @@ __global__ void __launch_bounds__(kAppendThreads, 5) kv_append_kernel(const Appe
 #pragma unroll
                 for (int o = kLanes / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
             }
+            [[maybe_unused]] float top_y = 0.f;
+            [[maybe_unused]] int nan = 0;  // of the group in the lower half, and in the upper
+            if constexpr (kType == BD_KV_E2M1) {  // a group is two lanes' pieces of one half
+                bool n0 = false, n1 = false;
+                top = finite_top(x, n0), top_y = finite_top(y, n1);
+                nan = (n0 ? 1 : 0) | (n1 ? 2 : 0);
+                top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+                top_y = fmaxf(top_y, __shfl_xor_sync(0xFFFFFFFFu, top_y, 1));
+                nan |= __shfl_xor_sync(0xFFFFFFFFu, nan, 1);
+            }
             if (is_q || r >= rows) continue;
             const int64_t at = slot_row + static_cast<int64_t>(r - q_rows - (is_v ? a.kv_heads : 0)) * a.page_size;
             if (!in_bounds(at >= 0 && at < a.n_pages * a.kv_heads * a.page_size, a.status)) continue;
             uint8_t *dst = is_v ? a.cv : a.ck;
-            if constexpr (!kE4m3) {
+            if constexpr (kType == BD_KV_BF16) {
                 *reinterpret_cast<uint4 *>(dst + at * (kDim * 2) + lane * 16) = pack8(x);
                 *reinterpret_cast<uint4 *>(dst + at * (kDim * 2) + kDim + lane * 16) = pack8(y);
+            } else if constexpr (kType == BD_KV_E2M1) {
+                const uint32_t low = group_scale_byte(top), high = group_scale_byte(top_y);
+                *reinterpret_cast<uint32_t *>(dst + at * (kDim / 2) + lane * 4) = eight_e2m1(x, low);
+                *reinterpret_cast<uint32_t *>(dst + at * (kDim / 2) + kDim / 4 + lane * 4) = eight_e2m1(y, high);
+                if (lane % 2 == 0) {
+                    uint8_t *sc = (is_v ? a.cv_scale : a.ck_scale) + at * (kDim / 16) + lane / 2;
+                    sc[0] = static_cast<uint8_t>(nan & 1 ? 0xFFu : low), sc[kDim / 32] = static_cast<uint8_t>(nan & 2 ? 0xFFu : high);
+                }
             } else {
                 const int e = scale_byte(top);
                 const float inv = __uint_as_float(static_cast<uint32_t>(254 - e) << 23);  // 2^(127 - e), exact
@@ -162,25 +212,14 @@ __global__ void __launch_bounds__(kAppendThreads, 5) kv_append_kernel(const Appe
     }
 }
 
-// The same for a rotation of the first 2 kHalf elements of a head or of neighbours, and for a 4-bit cache.  A lane holds
-// 16 neighbouring elements, a group of the 4-bit cache, so that neither a group's maximum nor its scale crosses lanes;
-// what an element is rotated with is read a second time, from L1, where it is not among the lane's own.  Its rows are
+// The same for a rotation of part of a head or of neighbours.  A lane holds 16 neighbouring elements, a group of the 4-bit
+// cache, whatever the parts: what an element is rotated with is read a second time, from L1, where it is not among the lane's own.  Its rows are
 // read before any row of the pass is written: the query may be rotated in place, and a row's lanes are one warp's.
 constexpr int kGroupAtOnce = 2;
 
 struct GroupArgs : AppendArgs {
     int32_t rope_dim, interleaved;
 };
-
-// Scale byte of a group in 4 bits: top / 6 to the nearest of 5 bits of exponent and 3 of mantissa.
-__device__ __forceinline__ uint32_t group_scale_byte(float top) {
-    const float t = __fdiv_rn(top, 6.f);
-    if (t < 6.103515625e-5f) return static_cast<uint32_t>(__float2int_rn(t * 131072.f));  // below 2^-14: steps of 2^-17
-    const uint32_t b = __float_as_uint(t);
-    const uint32_t r = (b + 0x7FFFFu + (b >> 20 & 1u)) >> 20;  // 3 mantissa bits, ties to even
-    return min(r - ((127u - 15u) << 3), 0xF7u);
-}
-__device__ __forceinline__ float group_scale(uint32_t byte) { return __half2float(__ushort_as_half(static_cast<unsigned short>(byte << 7))); }
 
 template <int kDim, int kType>
 __global__ void __launch_bounds__(kAppendThreads) kv_append_group_kernel(const GroupArgs a) {
@@ -283,17 +322,9 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_group_kernel(const G
                 dst[0] = pack8(x[0]), dst[1] = pack8(x[1]);
             }
             if (__all_sync(0xFFFFFFFFu, is_q || r >= rows)) continue;
-            float top = 0.f;
             bool nan = false;
-            if constexpr (kType != BD_KV_BF16) {
-#pragma unroll
-                for (int w = 0; w < 2; ++w)
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        if (fabsf(x[w][j]) < INFINITY) top = fmaxf(top, fabsf(x[w][j]));
-                        nan |= x[w][j] != x[w][j];
-                    }
-            }
+            float top = 0.f;
+            if constexpr (kType != BD_KV_BF16) top = fmaxf(finite_top(x[0], nan), finite_top(x[1], nan));
             if constexpr (kType == BD_KV_E4M3) {  // a scale for the whole row
 #pragma unroll
                 for (int o = kLanes / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
@@ -318,16 +349,7 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_group_kernel(const G
                 if (lane == 0) scales[at] = static_cast<uint8_t>(e);
             } else {
                 const uint32_t byte = group_scale_byte(top);
-                // a quotient, not a product with 1 / s: many values of a group lie on a tie between two codes
-                const float scale = group_scale(byte);
-                auto over = [&](float v) { return byte ? __fdiv_rn(v, scale) : copysignf(0.f, v); };
-                uint32_t b[2] = {0, 0};
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const float2 y = make_float2(over(x[j / 4][j % 4 * 2]), over(x[j / 4][j % 4 * 2 + 1]));
-                    b[j / 4] |= static_cast<uint32_t>(__nv_cvt_float2_to_fp4x2(y, __NV_E2M1, cudaRoundNearest)) << j % 4 * 8;
-                }
-                *reinterpret_cast<uint2 *>(dst + at * (kDim / 2) + lane * 8) = make_uint2(b[0], b[1]);
+                *reinterpret_cast<uint2 *>(dst + at * (kDim / 2) + lane * 8) = make_uint2(eight_e2m1(x[0], byte), eight_e2m1(x[1], byte));
                 scales[at * (kDim / 16) + lane] = static_cast<uint8_t>(nan ? 0xFFu : byte);
             }
         }
@@ -457,6 +479,21 @@ cudaError_t launch_pdl(void (*kernel)(const Args), int64_t grid, int threads, co
     return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 
+template <int kDim>
+cudaError_t launch_append(int type, int64_t n, const AppendArgs &a, cudaStream_t stream) {
+    return launch_pdl(type == BD_KV_E2M1   ? kv_append_kernel<kDim, BD_KV_E2M1>
+                      : type == BD_KV_E4M3 ? kv_append_kernel<kDim, BD_KV_E4M3>
+                                           : kv_append_kernel<kDim, BD_KV_BF16>,
+                      n, kAppendThreads, a, stream);
+}
+template <int kDim>
+cudaError_t launch_append_group(int type, int64_t n, const GroupArgs &a, cudaStream_t stream) {
+    return launch_pdl(type == BD_KV_E2M1   ? kv_append_group_kernel<kDim, BD_KV_E2M1>
+                      : type == BD_KV_E4M3 ? kv_append_group_kernel<kDim, BD_KV_E4M3>
+                                           : kv_append_group_kernel<kDim, BD_KV_BF16>,
+                      n, kAppendThreads, a, stream);
+}
+
 }  // namespace
 
 cudaError_t launch_kv_append(const bd_kv_cache &c, const void *q, int32_t q_heads, const void *k, const void *v,
@@ -487,22 +524,9 @@ cudaError_t launch_kv_append(const bd_kv_cache &c, const void *q, int32_t q_head
     a.page_size = c.page_size;
     a.n_seqs = n_seqs;
     a.max_pages = max_pages;
-    const bool e = c.kv_type == BD_KV_E4M3, wide = c.head_dim == 128;
-    if (c.kv_type == BD_KV_E2M1)
-        return launch_pdl(wide ? kv_append_group_kernel<128, BD_KV_E2M1> : kv_append_group_kernel<64, BD_KV_E2M1>, n_tokens,
-                          kAppendThreads, a, stream);
-    if (rope && (interleaved || rope_dim != c.head_dim)) {
-        if (wide)
-            return launch_pdl(e ? kv_append_group_kernel<128, BD_KV_E4M3> : kv_append_group_kernel<128, BD_KV_BF16>, n_tokens,
-                              kAppendThreads, a, stream);
-        return launch_pdl(e ? kv_append_group_kernel<64, BD_KV_E4M3> : kv_append_group_kernel<64, BD_KV_BF16>, n_tokens,
-                          kAppendThreads, a, stream);
-    }
-    const AppendArgs &whole = a;
-    if (wide)
-        return launch_pdl(e ? kv_append_kernel<128, true> : kv_append_kernel<128, false>, n_tokens, kAppendThreads, whole,
-                          stream);
-    return launch_pdl(e ? kv_append_kernel<64, true> : kv_append_kernel<64, false>, n_tokens, kAppendThreads, whole, stream);
+    if (rope && (interleaved || rope_dim != c.head_dim))
+        return c.head_dim == 128 ? launch_append_group<128>(c.kv_type, n_tokens, a, stream) : launch_append_group<64>(c.kv_type, n_tokens, a, stream);
+    return c.head_dim == 128 ? launch_append<128>(c.kv_type, n_tokens, a, stream) : launch_append<64>(c.kv_type, n_tokens, a, stream);
 }
 
 cudaError_t launch_kv_read(const bd_kv_cache &c, const int32_t *page_table, int32_t n_seqs, int32_t max_pages,
