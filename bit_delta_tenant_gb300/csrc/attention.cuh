@@ -64,14 +64,16 @@ __device__ __forceinline__ void e4m3x4_to_half2x2(uint32_t four, uint32_t &lo, u
         : "=r"(lo), "=r"(hi)
         : "r"(four));
 }
-// Two bytes of e2m1 pairs (the low half of `two`) as two fp16 pairs.
-__device__ __forceinline__ void e2m1x4_to_half2x2(uint32_t two, uint32_t &lo, uint32_t &hi) {
+// Four bytes of e2m1 pairs as four fp16 pairs.
+__device__ __forceinline__ void e2m1x8_to_half2x4(uint32_t four, uint32_t (&h)[4]) {
     asm("{\n\t.reg .b8 a, b, c, d;\n\t"
-        "mov.b32 {a, b, c, d}, %2;\n\t"
+        "mov.b32 {a, b, c, d}, %4;\n\t"
         "cvt.rn.f16x2.e2m1x2 %0, a;\n\t"
-        "cvt.rn.f16x2.e2m1x2 %1, b;\n\t}"
-        : "=r"(lo), "=r"(hi)
-        : "r"(two));
+        "cvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %2, c;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+        : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+        : "r"(four));
 }
 __device__ __forceinline__ uint32_t hmul2(uint32_t x, uint32_t y) {
     uint32_t z;
@@ -448,15 +450,18 @@ __device__ __forceinline__ void stream(const AttnArgs &a, uint8_t *smem, const S
 #pragma unroll
                         for (int e = 0; e < 2; ++e) by[e] = hmul2(by[e] | by[e] << 16, 0x30003000u);  // an eighth
 #pragma unroll
-                        for (int k = 0; k < kSteps; ++k) {
-                            uint32_t b0, b1;
-                            e2m1x4_to_half2x2(w[k / 2] >> k % 2 * 16, b0, b1);
+                        for (int k = 0; k < kSteps; k += 2) {
+                            uint32_t b[4];
+                            e2m1x8_to_half2x4(w[k / 2], b);
                             const uint32_t f = by[kDim == 128 ? k / 4 : 0];
-                            b0 = hmul2(b0, f), b1 = hmul2(b1, f);
-                            if constexpr (kPack)
-                                mma16<true>(s[i], qa[0][k][0], 0, qa[0][k][1], 0, b0, b1);
-                            else
-                                mma16<true>(s[i], qa[0][k][0], qa[0][k][1], qa[0][k][2], qa[0][k][3], b0, b1);
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                const uint32_t b0 = hmul2(b[2 * e], f), b1 = hmul2(b[2 * e + 1], f);
+                                if constexpr (kPack)
+                                    mma16<true>(s[i], qa[0][k + e][0], 0, qa[0][k + e][1], 0, b0, b1);
+                                else
+                                    mma16<true>(s[i], qa[0][k + e][0], qa[0][k + e][1], qa[0][k + e][2], qa[0][k + e][3], b0, b1);
+                            }
                         }
                     }
                 } else {
@@ -620,14 +625,14 @@ __device__ __forceinline__ void stream(const AttnArgs &a, uint8_t *smem, const S
                         }
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
-                            uint32_t b[2];
-#pragma unroll
-                            for (int e = 0; e < 2; ++e) {
-                                const int r = u * 16 + i * 8 + t4 + 4 * e;
-                                b[e] = scales[(kTile + r) * kScale + g * kScale / 8];
-                                if (edge && !(key0 + r >= sp.start && key0 + r < sp.len && !(bad_here >> u & 1))) b[e] = 0;  // any byte
+                            const int r = u * 16 + i * 8 + t4;
+                            const uint8_t *sc = scales + (kTile + r) * kScale + g * kScale / 8;
+                            uint32_t b = sc[0] << 7 | static_cast<uint32_t>(sc[4 * kScale]) << 23;
+                            if (edge) {  // bytes of keys that are not seen may be anything
+                                auto seen = [&](int key) { return key >= sp.start && key < sp.len && !(bad_here >> u & 1); };
+                                b &= (seen(key0 + r) ? 0xFFFFu : 0u) | (seen(key0 + r + 4) ? 0xFFFF0000u : 0u);
                             }
-                            f[i] = hmul2(b[0] << 7 | b[1] << 23, 0x30003000u);  // an eighth
+                            f[i] = hmul2(b, 0x30003000u);  // an eighth
                         }
 #pragma unroll
                         for (int i = 0; i < kDim / 64; ++i) {
@@ -635,21 +640,15 @@ __device__ __forceinline__ void stream(const AttnArgs &a, uint8_t *smem, const S
                             const uint32_t n1 = (w[0][i] >> 4 & 0x0F0F0F0Fu) | (w[1][i] & 0xF0F0F0F0u);
                             const uint32_t n2 = (w[2][i] & 0x0F0F0F0Fu) | (w[3][i] & 0x0F0F0F0Fu) << 4;
                             const uint32_t n3 = (w[2][i] >> 4 & 0x0F0F0F0Fu) | (w[3][i] & 0xF0F0F0F0u);
+                            uint32_t v0[4], v1[4], v2[4], v3[4];  // byte d: dims 8i + 2d and 8i + 2d + 1, a row tile
+                            e2m1x8_to_half2x4(n0, v0), e2m1x8_to_half2x4(n1, v1);
+                            e2m1x8_to_half2x4(n2, v2), e2m1x8_to_half2x4(n3, v3);
 #pragma unroll
-                            for (int e = 0; e < 2; ++e) {  // bytes 2e and 2e + 1: dims 8i + 4e .., two row tiles
-                                uint32_t v0[2], v1[2], v2[2], v3[2];
-                                e2m1x4_to_half2x2(n0 >> 16 * e, v0[0], v0[1]);
-                                e2m1x4_to_half2x2(n1 >> 16 * e, v1[0], v1[1]);
-                                e2m1x4_to_half2x2(n2 >> 16 * e, v2[0], v2[1]);
-                                e2m1x4_to_half2x2(n3 >> 16 * e, v3[0], v3[1]);
+                            for (int d = 0; d < 4; ++d) {
+                                const uint32_t a0 = hmul2(v0[d], f[0]), a1 = hmul2(v1[d], f[0]);
+                                const uint32_t a2 = hmul2(v2[d], f[1]), a3 = hmul2(v3[d], f[1]);
 #pragma unroll
-                                for (int d = 0; d < 2; ++d) {
-                                    const uint32_t a0 = hmul2(v0[d], f[0]), a1 = hmul2(v1[d], f[0]);
-                                    const uint32_t a2 = hmul2(v2[d], f[1]), a3 = hmul2(v3[d], f[1]);
-#pragma unroll
-                                    for (int h = 0; h < kHalves; ++h)
-                                        mma16<true>(o[4 * i + 2 * e + d][h], a0, a1, a2, a3, p[h][0], p[h][1]);
-                                }
+                                for (int h = 0; h < kHalves; ++h) mma16<true>(o[4 * i + d][h], a0, a1, a2, a3, p[h][0], p[h][1]);
                             }
                         }
                     } else if constexpr (kE4m3) {
