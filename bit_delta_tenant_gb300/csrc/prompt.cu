@@ -185,6 +185,7 @@ struct Smem {
     uint8_t *raw;
     uint64_t *q_full, *q_ready, *q_empty, *s_full, *p_full, *o_full;  // per tile
     uint64_t *u_full, *u_empty;          // per unit slot
+    uint64_t *u_want;                    // warp 10 is ready for the next unit
     Unit *unit;
     volatile int *slow;                  // per stage: number (from 1) of the last load of a V that is not finite and not seen by all
     volatile int *abort;
@@ -266,8 +267,9 @@ __device__ __forceinline__ void find_units(const PromptArgs &a, const Smem &s) {
     int32_t most = 1 << 30;
     unsigned classes = 0;
     int64_t units = 0, blocks = 0;
+    Sequence q = {};
     for (int64_t i = lane; i < a.n_seqs; i += 32) {
-        const Sequence q = sequence_of(a, i);
+        q = sequence_of(a, i);
         if (q.units > 0) classes |= 1u << size_class(q);
         units += q.units, blocks += static_cast<int64_t>(q.units) * q.blocks;
     }
@@ -279,7 +281,7 @@ __device__ __forceinline__ void find_units(const PromptArgs &a, const Smem &s) {
             while (true) {
                 int64_t pieces = 0;
                 for (int64_t i = lane; i < a.n_seqs; i += 32) {
-                    const Sequence q = sequence_of(a, i);
+                    if (a.n_seqs > 32) q = sequence_of(a, i);
                     pieces += static_cast<int64_t>(q.units) * pieces_of(q, most);
                 }
                 if (warp_sum(pieces) * vheads <= a.slots) break;
@@ -289,7 +291,6 @@ __device__ __forceinline__ void find_units(const PromptArgs &a, const Smem &s) {
     }
     int64_t first = a.n_seqs, before = 0;  // the 32 sequences looked at, and the units of those before them
     int cls = 32;
-    Sequence q = {};
     int64_t mine = 0, upto = 0, all = 0;
     auto look = [&] {  // at the next sequences; false: there are none
         before += all;
@@ -300,8 +301,10 @@ __device__ __forceinline__ void find_units(const PromptArgs &a, const Smem &s) {
             cls = 31 - __clz(classes);
             first = 0;
         }
-        q = Sequence{};
-        if (first + lane < a.n_seqs) q = sequence_of(a, first + lane);
+        if (a.n_seqs > 32) {  // else each lane has its own still
+            q = Sequence{};
+            if (first + lane < a.n_seqs) q = sequence_of(a, first + lane);
+        }
         mine = size_class(q) == cls ? static_cast<int64_t>(q.units) * pieces_of(q, most) * vheads : 0;
         upto = warp_scan(mine);
         all = __shfl_sync(0xFFFFFFFFu, upto, 31);
@@ -310,7 +313,9 @@ __device__ __forceinline__ void find_units(const PromptArgs &a, const Smem &s) {
     bool over = false;
     int it = 0;
     for (int64_t round = 0; !over; ++round) {
-        // Where units may be split there are no more than CTAs, and CTA b takes unit b, whose slot is b.  Else the next one.
+        // Where units may be split there are no more than CTAs, and CTA b takes unit b, whose slot is b.  Else the next one, taken
+        // when warp 10 has started the last copies of the one before: a unit taken earlier waits here while other CTAs run dry.
+        if (!wait_on(s.u_want, it & 1, a, s.abort)) break;
         int64_t u = round * gridDim.x + blockIdx.x;
         if (!a.may_split) u = __shfl_sync(0xFFFFFFFFu, lane == 0 ? atomicAdd(a.taken, 1u) : 0u, 0);
         while (!over && u >= before + all) over = !look();
@@ -571,6 +576,7 @@ __device__ __forceinline__ void load_tiles(const PromptArgs &a, const Smem &s, c
     int it = 0, loads = 0, q_n[2] = {0, 0};
     bool ok = true;
     while (ok) {
+        if (lane == 0) mbar_arrive(s.u_want);
         const Unit u = next_unit(a, s, it);
         if (u.blocks < 0) break;
         if (u.blocks == 0) continue;
@@ -1089,16 +1095,15 @@ __global__ void __launch_bounds__(kThreadsOf<kType>, 1)
     s.p_full = bars + 9;                                                            // of each tile: the first and second 64 keys
     s.u_full = bars + 13, s.u_empty = bars + 15;
     s.q_ready = bars + 17;
-    s.unit = reinterpret_cast<Unit *>(bars + 19);
+    s.u_want = bars + 19;
+    s.unit = reinterpret_cast<Unit *>(bars + 20);
     s.slow = reinterpret_cast<volatile int *>(s.unit + 2);
     s.abort = s.slow + kS;
     s.tmem = const_cast<uint32_t *>(reinterpret_cast<volatile uint32_t *>(s.abort + 1));
-    static_assert(kRawSlots<kDim, kType> <= 4 && (3 * kS + 27) * 8 + 2 * sizeof(Unit) + (kS + 2) * 4 <= 1024);
+    static_assert(kRawSlots<kDim, kType> <= 4 && (3 * kS + 28) * 8 + 2 * sizeof(Unit) + (kS + 2) * 4 <= 1024);
     const int warp = threadIdx.x / 32;
-    pdl_trigger_and_wait();
+    pdl_trigger();
     if (threadIdx.x == 0) {
-        // where units are split, CTA b takes unit b alone: its slot holds no unit's first piece yet
-        if (a.may_split && in_bounds(static_cast<int>(blockIdx.x) < a.slots, a.status)) a.heads[blockIdx.x] = make_int4(0, 0, 0, 0);
         for (int i = 0; i < kS; ++i) {
             mbar_init(&s.full[i], kConvert ? kConvertWarps : 1);
             mbar_init(&s.empty[i], kConvert ? 1 : 2);  // the products that read it, and warp 11
@@ -1113,6 +1118,7 @@ __global__ void __launch_bounds__(kThreadsOf<kType>, 1)
         }
         for (int i = 0; i < kRawSlots<kDim, kType>; ++i) mbar_init(&s.raw_full[i], 1), mbar_init(&s.raw_empty[i], kConvertWarps);
         mbar_init(&s.o_full[2], 1);
+        mbar_init(s.u_want, 1);
         *s.abort = 0;
         mbar_fence_init();
         tma_prefetch_desc(&map_q);
@@ -1123,6 +1129,9 @@ __global__ void __launch_bounds__(kThreadsOf<kType>, 1)
         tmem_relinquish();
     }
     tc_fence_before();
+    pdl_wait();  // what came before on the stream is complete; the set-up above needed nothing of it
+    // where units are split, CTA b takes unit b alone: its slot holds no unit's first piece yet
+    if (threadIdx.x == 0 && a.may_split && in_bounds(static_cast<int>(blockIdx.x) < a.slots, a.status)) a.heads[blockIdx.x] = make_int4(0, 0, 0, 0);
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *s.tmem;  // 0: all of it is this CTA's
