@@ -848,6 +848,8 @@ __device__ __noinline__ void add_values(uint32_t t_p, uint32_t t_o, const uint8_
     tmem_st_wait();
 }
 
+__device__ __forceinline__ uint32_t bits_below(int n) { return n >= 32 ? 0xFFFFFFFFu : n <= 0 ? 0u : (1u << n) - 1; }
+
 // Which of a block's 8 pieces of 16 keys have a page id out of range.
 __device__ __noinline__ unsigned missing_pieces(const PromptArgs &a, const Unit &u, int blk) {
     const int lane = threadIdx.x % 32, key = blk * kBlock + lane * 16;
@@ -955,12 +957,12 @@ __device__ __forceinline__ void softmax_rows(const PromptArgs &a, const Smem &s,
                 if (gaps) missing = missing_pieces(a, u, key0 / kBlock);
                 if (__any_sync(0xFFFFFFFFu, from > 0 || to < kBlock) || missing) {
 #pragma unroll
-                    for (int c = 0; c < 4; ++c)
+                    for (int c = 0; c < 4; ++c) {  // a bit for each key
+                        const uint32_t gone = (missing >> 2 * c & 1 ? 0xFFFFu : 0u) | (missing >> 2 * c & 2 ? 0xFFFF0000u : 0u);
+                        const uint32_t seen = bits_below(to - c * 32) & ~bits_below(from - c * 32) & ~gone;
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) {
-                            const int k = c * 32 + i;
-                            if (k < from || k >= to || (missing >> k / 16 & 1)) x[c][i] = 0xFF800000u;  // -infinity
-                        }
+                        for (int i = 0; i < 32; ++i) x[c][i] = seen >> i & 1 ? x[c][i] : 0xFF800000u;  // -infinity
+                    }
                 }
                 const float scale = a.plain ? unit : 1.f;
                 float most[4];
