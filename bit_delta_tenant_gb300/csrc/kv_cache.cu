@@ -5,9 +5,10 @@
 // read once and each output written once, in 16-byte pieces.  Written: a lane holds both
 // halves of what is rotated together, so only a row's maximum is exchanged, by shuffles.
 // Read: a CTA finds the places of its tokens once and then copies pieces in the output's order.
-// Measured, 8 bits, heads of 128: 8 prompts of up to 4096 tokens, 64 and 8 heads, written in
-// 40 us (5.4 TB/s), 64 tokens, 32 and 8 heads, in 2.4 us; 64 sequences of 8 heads read in
-// 59 us (6.1 TB/s), 1000 tokens in bf16 in 3.4 us.
+// Measured, heads of 128: 8 prompts of up to 4096 tokens, 64 and 8 heads, written in 8 bits in 40 us (5.4 TB/s), 64
+// tokens, 32 and 8 heads, in 2.4 us; 64 sequences of 8 heads read in 8 bits in 59 us (6.1 TB/s), 1000 tokens in bf16 in 3.4 us;
+// the same prompts written in 4 bits and read back 55 us (4.3 TB/s), 71 with the kernel for any layout, which reads each
+// value of q and k twice.
 #include <cuda_fp4.h>
 #include <cuda_fp8.h>
 

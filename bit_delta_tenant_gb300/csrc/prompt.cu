@@ -23,6 +23,14 @@
 // Values that a row does not see.  A weight of 0 does not hide an infinity or NaN of V.  Blocks that some row sees in part
 // are looked at: rows of V that nobody sees are zeroed, and where a finite number is missing in another one, the
 // block's P V is added up by the softmax threads, row by row over the keys that the row sees, instead of by the tensor cores.
+//
+// Measured (head_dim 128, 32 and 8 heads unless said): one prompt of 8192 tokens, bf16, 389 us (1.41 PFLOP/s, 0.74 of
+// cuBLAS's burst): a block takes about 3500 clocks, its products 2048: the thread that issues them shares its scheduler with two
+// softmax warps.  333 tokens 17 us: launch, set-up, three blocks one after the other, output.  Over 8 and 4 bits a block takes
+// about half as long again: the 64 KB that are stored to shared memory for it contend with the products' reads
+// of their operands (48 tokens over 65000, 64 and 8 heads: bf16 116 us, 8 bits 188, 4 bits 186; without conversions, on
+// whatever the tiles held, 135).  Capped scores cost two transcendental operations more each: 9 ragged prompts of up to 1500
+// tokens over up to 1000, 8 bits, 91 us, 56 uncapped.
 #include <cuda_fp4.h>
 #include <cuda_fp8.h>
 

@@ -6,6 +6,7 @@
 // number, times the position wraps where a turn is complete, so the product is the exact remainder of the angle and
 // needs no 64-bit floating point, of which this GPU has little; from one of a thread's positions to its next it is an
 // addition.  Its upper 32 bits are enough for fp32 results.  The frequencies are the host's, in 64 bits.
+// Measured: 131072 x 128 12.9 us (5.2 TB/s); a product and a conversion of 64 bits and sincospif for each pair took 31.7.
 #include <math.h>
 
 #include "bd_device.cuh"
