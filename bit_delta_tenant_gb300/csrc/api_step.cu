@@ -132,7 +132,8 @@ BD_API int32_t bd_kv_read(const bd_kv_cache *cache, const int32_t *page_table, i
 namespace {
 
 bool bad_rule(const bd_score_rule *r) {
-    return !r || r->window < 0 || !(r->scale - r->scale == 0.f) || !(r->cap >= 0.f) || !(r->cap - r->cap == 0.f) || r->reserved != 0;
+    if (!r || r->window < 0 || !(r->scale - r->scale == 0.f) || r->reserved != 0) return true;
+    return !(r->cap == 0.f || (r->cap >= 0x1p-100f && r->cap <= 0x1p100f));  // 1 / cap and cap in base 2 stay finite
 }
 
 int32_t check_heads(const bd_kv_cache *c, int32_t n_seqs, int32_t q_heads) {

@@ -925,7 +925,7 @@ __device__ __forceinline__ void softmax_rows(const PromptArgs &a, const Smem &s,
             bool none = false;
             if (write) {
                 hi = max(p + 1, u.prefix);
-                lo = a.window > 0 ? max(0, p - a.window + 1) : 0;
+                lo = a.window > 0 && p >= a.window ? p - a.window + 1 : 0;
                 if (a.first) lo = max(lo, a.first[row]);
                 none = p < 0 || lo >= hi;
                 if (none) lo = 0, hi = INT_MAX;

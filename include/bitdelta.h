@@ -623,7 +623,7 @@ int32_t bd_attention_decode(const bd_kv_cache *cache, const void *q, int32_t q_h
  * ------------------------------------------------------------------------ */
 typedef struct bd_score_rule {
     float scale;
-    float cap;              /* 0: none */
+    float cap;              /* 0: none; else 2^-100 .. 2^100 */
     const float *slopes;    /* [q_heads] or NULL                         (read, device) */
     const int32_t *first;   /* one per query (decode: [n_seqs]) or NULL  (read, device) */
     const int32_t *prefix;  /* [n_seqs] or NULL                          (read, device) */

@@ -126,6 +126,20 @@ def test_rows_of_no_sequence_stay_as_they_are():
     assert (out[50:] == 3).all() and (lse[50:] == 3).all()
 
 
+@pytest.mark.parametrize("window", [0x7FFFFFFF, 1 << 40])
+def test_the_largest_window_and_no_lse(window):
+    """More rows than the sequence is long, whose first positions lie below 0, with a window as wide as there is."""
+    pool, q = case("bf16", 64, 4, 2, [20, 30], [0, 10], page=16, seed=3)
+    want, _ = run(pool, q, [20, 30], lengths=[5, 40])
+    out, _ = run(pool, q, [20, 30], lengths=[5, 40], window=window)
+    assert torch.equal(out, want)
+    cache = pool.cache()
+    ws = torch.zeros(bd.bd_attention_prompt_workspace_size(cache, 4), dtype=torch.uint8, device="cuda")
+    bd.bd_attention_prompt(cache, q.cuda(), offsets_of([20, 30]), torch.from_numpy(pool.table).cuda(), torch.tensor([5, 40], dtype=torch.int32).cuda(), out.zero_(), ws)
+    assert torch.equal(out, want)
+    bd.bd_get_device_status()
+
+
 def test_nothing_cached_and_no_rows():
     pool, q = case("bf16", 64, 4, 2, [5, 3], [0, 0], page=16, seed=3)
     out, lse = run(pool, q, [5, 3], lengths=[0, 0])

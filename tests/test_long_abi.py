@@ -63,7 +63,7 @@ def rule(**kw):
     return bd.ScoreRule(**{**dict(scale=1.0, cap=0.0, slopes=0, first=0, prefix=0, window=0, reserved=0), **kw})
 
 
-BAD_RULES = [None] + [rule(**kw) for kw in (dict(scale=NAN), dict(scale=INF), dict(cap=-1.0), dict(cap=NAN), dict(cap=INF), dict(window=-1), dict(reserved=1))]
+BAD_RULES = [None] + [rule(**kw) for kw in (dict(scale=NAN), dict(scale=INF), dict(cap=-1.0), dict(cap=NAN), dict(cap=INF), dict(cap=1e-40), dict(cap=3e38), dict(window=-1), dict(reserved=1))]
 ODD_RULES = [rule(slopes=A + 2), rule(first=A + 1), rule(prefix=A + 3)]
 
 
