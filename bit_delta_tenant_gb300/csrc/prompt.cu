@@ -963,7 +963,8 @@ __device__ __forceinline__ void softmax_rows(const PromptArgs &a, const Smem &s,
                 const int from = lo - key0, to = hi - key0;
                 unsigned missing = 0;
                 if (gaps) missing = missing_pieces(a, u, key0 / kBlock);
-                if (__any_sync(0xFFFFFFFFu, from > 0 || to < kBlock) || missing) {
+                const bool part = key0 < in_lo || key0 + kBlock > in_hi;  // some row sees the block in part
+                if (part || missing) {
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {  // a bit for each key
                         const uint32_t gone = (missing >> 2 * c & 1 ? 0xFFFFu : 0u) | (missing >> 2 * c & 2 ? 0xFFFF0000u : 0u);
@@ -973,15 +974,18 @@ __device__ __forceinline__ void softmax_rows(const PromptArgs &a, const Smem &s,
                     }
                 }
                 const float scale = a.plain ? unit : 1.f;
-                float most[4];
+                float most[8];  // chains short enough to hide an operation's latency
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    most[c] = __uint_as_float(x[c][0]);
-#pragma unroll
-                    for (int i = 1; i < 31; i += 2) most[c] = max3(most[c], __uint_as_float(x[c][i]), __uint_as_float(x[c][i + 1]));
-                    most[c] = fmaxf(most[c], __uint_as_float(x[c][31]));
+                for (int c = 0; c < 8; ++c) {
+                    const uint32_t(&v)[32] = x[c / 2];
+                    most[c] = fmaxf(__uint_as_float(v[c % 2 * 16]), __uint_as_float(v[c % 2 * 16 + 1]));
                 }
-                const float now = fmaxf(fmaxf(most[0], most[1]), fmaxf(most[2], most[3])) * scale;
+#pragma unroll
+                for (int i = 2; i < 16; i += 2)
+#pragma unroll
+                    for (int c = 0; c < 8; ++c)
+                        most[c] = max3(most[c], __uint_as_float(x[c / 2][c % 2 * 16 + i]), __uint_as_float(x[c / 2][c % 2 * 16 + i + 1]));
+                const float now = fmaxf(max3(most[0], most[1], most[2]), max3(max3(most[3], most[4], most[5]), most[6], most[7])) * scale;
                 const bool raise = now > top + kLazy<kType> || (top == -INFINITY && now > top);
                 if (__any_sync(0xFFFFFFFFu, raise)) {
                     float fix = 1.f;
@@ -996,7 +1000,6 @@ __device__ __forceinline__ void softmax_rows(const PromptArgs &a, const Smem &s,
                     }
                 }
                 const float base = (top == -INFINITY ? 0.f : top) - kLift<kType>;
-                const bool part = key0 < in_lo || key0 + kBlock > in_hi;  // some row sees the block in part
                 float2 add[2] = {};
                 const float2 scale2 = make_float2(scale, scale), base2 = make_float2(-base, -base);
 #pragma unroll
