@@ -91,7 +91,9 @@ __device__ __forceinline__ float ex2(float x) {  // 2^x, 0 for -inf
 }
 // cap tanh(x / cap), x and cap in base 2 and `in` = 2 log2(e) / cap: 1 - 2 / (1 + e^2y), within 2^-22 of cap.
 __device__ __forceinline__ float capped(float x, float cap, float in) {
-    return cap * (1.f - __fdividef(2.f, 1.f + ex2(x * in)));
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + ex2(x * in)));  // of infinity 0
+    return fmaf(-2.f * cap, r, cap);
 }
 // A bf16 pair times `up` as e4m3 bytes, and 16 times what they leave as e4m3 bytes.  In fp16 the
 // scaled values (at most 256, 8 bits) and the differences are exact down to 2^-24.

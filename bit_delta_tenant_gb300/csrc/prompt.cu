@@ -134,6 +134,11 @@ __device__ __forceinline__ float2 add2(float2 x, float2 y) {
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits_of(x)), "l"(bits_of(y)));
     return pair_of(r);
 }
+__device__ __forceinline__ float2 mul2(float2 x, float2 y) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits_of(x)), "l"(bits_of(y)));
+    return pair_of(r);
+}
 __device__ __forceinline__ float max3(float x, float y, float z) {
     float r;
     asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(y), "f"(z));
@@ -801,11 +806,18 @@ __device__ __forceinline__ void tmem_ld_x16(uint32_t taddr, uint32_t (&o)[16]) {
         : "r"(taddr));
 }
 
-// A product's score in base 2 under the rule: `far` positions before the query.
-__device__ __forceinline__ float ruled(const PromptArgs &a, float v, float scale, float slope, float far) {
-    v *= scale;
-    if (a.cap > 0.f) v = a.cap * (1.f - __fdividef(2.f, 1.f + ex2(v * a.cap_in)));
-    return fmaf(-slope, fabsf(far), v);
+// cap tanh of two products, `in` = 2 log2(e) scale / cap: with e = exp(-2 |y|), tanh |y| = 2 / (1 + e) - 1.  The reciprocal is
+// Newton's, two steps from (98 - 80 e + 32 e^2) / 99, which is within 1/99 for e in [0, 1]: the transcendental unit, with an
+// exponential here and one for the weight, is the busier one.
+__device__ __forceinline__ float2 capped(float2 x, float2 in, float cap) {
+    const float2 y = mul2(x, in), e = make_float2(ex2(-fabsf(y.x)), ex2(-fabsf(y.y)));
+    const float2 one = make_float2(1.f, 1.f), minus = make_float2(-1.f, -1.f);
+    const float2 q = fma2(e, minus, minus);  // -(1 + e)
+    float2 r = fma2(e, fma2(e, make_float2(32.f / 99, 32.f / 99), make_float2(-80.f / 99, -80.f / 99)), make_float2(98.f / 99, 98.f / 99));
+    r = fma2(r, fma2(q, r, one), r);
+    r = fma2(r, fma2(q, r, one), r);
+    r = fma2(r, make_float2(2.f * cap, 2.f * cap), make_float2(-cap, -cap));
+    return make_float2(copysignf(r.x, y.x), copysignf(r.y, y.y));
 }
 
 // The rows' output so far, times f.  Seldom run: apart, so that its registers are not the loop's.
@@ -954,11 +966,23 @@ __device__ __forceinline__ void softmax_rows(const PromptArgs &a, const Smem &s,
                 tmem_ld_wait();
                 const float far = static_cast<float>(p - key0);
                 if (!a.plain) {
+                    // to scores in base 2
+                    const float in = a.cap > 0.f ? unit * a.cap_in : unit;
+                    const float2 in2 = make_float2(in, in);
 #pragma unroll
                     for (int c = 0; c < 4; ++c)
 #pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            x[c][i] = __float_as_uint(ruled(a, __uint_as_float(x[c][i]), unit, slope, far - static_cast<float>(c * 32 + i)));
+                        for (int i = 0; i < 32; i += 2) {
+                            float2 v = make_float2(__uint_as_float(x[c][i]), __uint_as_float(x[c][i + 1]));
+                            v = a.cap > 0.f ? capped(v, in2, a.cap) : mul2(v, in2);
+                            x[c][i] = __float_as_uint(v.x), x[c][i + 1] = __float_as_uint(v.y);
+                        }
+                    if (a.slopes)
+#pragma unroll
+                        for (int c = 0; c < 4; ++c)
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                x[c][i] = __float_as_uint(fmaf(-slope, fabsf(far - static_cast<float>(c * 32 + i)), __uint_as_float(x[c][i])));
                 }
                 const int from = lo - key0, to = hi - key0;
                 unsigned missing = 0;
