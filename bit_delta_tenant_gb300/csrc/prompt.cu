@@ -960,30 +960,33 @@ __device__ __forceinline__ void softmax_rows(const PromptArgs &a, const Smem &s,
                 const int key0 = key_first + j * kBlock;
                 if (!wait_on(&s.s_full[tile], s_n & 1, a, s.abort)) return;
                 tc_fence_after();
+                if (!a.plain) {  // to scores in base 2, in place, 32 at a time: less code than all at once
+                    const float far = static_cast<float>(p - key0), in = a.cap > 0.f ? unit * a.cap_in : unit;
+                    const float2 in2 = make_float2(in, in);
+#pragma unroll 1
+                    for (int c = 0; c < kBlock; c += 32) {
+                        uint32_t v[32];
+                        tmem_ld_32x32b_x32(t_s + c, v);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int i = 0; i < 32; i += 2) {
+                            float2 y = make_float2(__uint_as_float(v[i]), __uint_as_float(v[i + 1]));
+                            y = a.cap > 0.f ? capped(y, in2, a.cap) : mul2(y, in2);
+                            v[i] = __float_as_uint(y.x), v[i + 1] = __float_as_uint(y.y);
+                        }
+                        if (a.slopes) {
+                            const float first = far - static_cast<float>(c);
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(fmaf(-slope, fabsf(first - static_cast<float>(i)), __uint_as_float(v[i])));
+                        }
+                        tmem_st_32x32b_x32(t_s + c, v);
+                    }
+                    tmem_st_wait();
+                }
                 uint32_t x[4][32];
 #pragma unroll
                 for (int c = 0; c < 4; ++c) tmem_ld_32x32b_x32(t_s + c * 32, x[c]);
                 tmem_ld_wait();
-                const float far = static_cast<float>(p - key0);
-                if (!a.plain) {
-                    // to scores in base 2
-                    const float in = a.cap > 0.f ? unit * a.cap_in : unit;
-                    const float2 in2 = make_float2(in, in);
-#pragma unroll
-                    for (int c = 0; c < 4; ++c)
-#pragma unroll
-                        for (int i = 0; i < 32; i += 2) {
-                            float2 v = make_float2(__uint_as_float(x[c][i]), __uint_as_float(x[c][i + 1]));
-                            v = a.cap > 0.f ? capped(v, in2, a.cap) : mul2(v, in2);
-                            x[c][i] = __float_as_uint(v.x), x[c][i + 1] = __float_as_uint(v.y);
-                        }
-                    if (a.slopes)
-#pragma unroll
-                        for (int c = 0; c < 4; ++c)
-#pragma unroll
-                            for (int i = 0; i < 32; ++i)
-                                x[c][i] = __float_as_uint(fmaf(-slope, fabsf(far - static_cast<float>(c * 32 + i)), __uint_as_float(x[c][i])));
-                }
                 const int from = lo - key0, to = hi - key0;
                 unsigned missing = 0;
                 if (gaps) missing = missing_pieces(a, u, key0 / kBlock);
