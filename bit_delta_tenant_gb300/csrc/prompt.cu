@@ -806,6 +806,18 @@ __device__ __forceinline__ void tmem_ld_x16(uint32_t taddr, uint32_t (&o)[16]) {
         : "r"(taddr));
 }
 
+// Waits for the loads so far; what is read of v comes after.
+__device__ __forceinline__ void tmem_ld_wait_for(uint32_t (&v)[32]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+        : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]),
+          "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]),
+          "+r"(v[15]), "+r"(v[16]), "+r"(v[17]), "+r"(v[18]), "+r"(v[19]), "+r"(v[20]), "+r"(v[21]),
+          "+r"(v[22]), "+r"(v[23]), "+r"(v[24]), "+r"(v[25]), "+r"(v[26]), "+r"(v[27]), "+r"(v[28]),
+          "+r"(v[29]), "+r"(v[30]), "+r"(v[31])
+        :
+        : "memory");
+}
+
 // cap tanh of two products, `in` = 2 log2(e) scale / cap: with e = exp(-2 |y|), tanh |y| = 2 / (1 + e) - 1.  The reciprocal is
 // Newton's, two steps from (98 - 80 e + 32 e^2) / 99, which is within 1/99 for e in [0, 1]: the transcendental unit, with an
 // exponential here and one for the weight, is the busier one.
@@ -964,56 +976,82 @@ __device__ __forceinline__ void softmax_rows(const PromptArgs &a, const Smem &s,
                 unsigned missing = 0;
                 if (gaps) missing = missing_pieces(a, u, key0 / kBlock);
                 const bool part = key0 < in_lo || key0 + kBlock > in_hi;  // some row sees the block in part
-                if (!a.plain || part || missing) {
-                    // The rule and the masks, in place in tensor memory, 32 keys at a time: all at once is more code than the
-                    // instruction caches hold beside the loop's (9 ragged prompts, capped, 82 us against 74; 8192 tokens 382, 377).
-                    const float far = static_cast<float>(p - key0), in = a.cap > 0.f ? unit * a.cap_in : unit;
-                    const float2 in2 = make_float2(in, in);
-#pragma unroll 1
-                    for (int c = 0; c < kBlock; c += 32) {
-                        uint32_t v[32];
-                        tmem_ld_32x32b_x32(t_s + c, v);
-                        tmem_ld_wait();
-                        if (!a.plain)
+                const bool rewrite = !a.plain || part || missing;
+                const float far = static_cast<float>(p - key0), in = a.cap > 0.f ? unit * a.cap_in : unit;
+                auto rule = [&](uint32_t(&v)[32], int c) {  // on the scores of keys c ..
+                    if (!a.plain) {
+                        const float2 in2 = make_float2(in, in);
 #pragma unroll
-                            for (int i = 0; i < 32; i += 2) {
-                                float2 y = make_float2(__uint_as_float(v[i]), __uint_as_float(v[i + 1]));
-                                y = a.cap > 0.f ? capped(y, in2, a.cap) : mul2(y, in2);
-                                v[i] = __float_as_uint(y.x), v[i + 1] = __float_as_uint(y.y);
-                            }
-                        if (a.slopes) {
-                            const float first = far - static_cast<float>(c);
-#pragma unroll
-                            for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(fmaf(-slope, fabsf(first - static_cast<float>(i)), __uint_as_float(v[i])));
+                        for (int i = 0; i < 32; i += 2) {
+                            float2 y = make_float2(__uint_as_float(v[i]), __uint_as_float(v[i + 1]));
+                            y = a.cap > 0.f ? capped(y, in2, a.cap) : mul2(y, in2);
+                            v[i] = __float_as_uint(y.x), v[i + 1] = __float_as_uint(y.y);
                         }
-                        if (part || missing) {  // a bit for each key
-                            const unsigned two = missing >> c / 16;
-                            const uint32_t gone = (two & 1 ? 0xFFFFu : 0u) | (two & 2 ? 0xFFFF0000u : 0u);
-                            const uint32_t seen = bits_below(to - c) & ~bits_below(from - c) & ~gone;
-#pragma unroll
-                            for (int i = 0; i < 32; ++i) v[i] = seen >> i & 1 ? v[i] : 0xFF800000u;  // -infinity
-                        }
-                        tmem_st_32x32b_x32(t_s + c, v);
                     }
-                    tmem_st_wait();
-                }
-                uint32_t x[4][32];
+                    if (a.slopes) {
+                        const float first = far - static_cast<float>(c);
 #pragma unroll
-                for (int c = 0; c < 4; ++c) tmem_ld_32x32b_x32(t_s + c * 32, x[c]);
-                tmem_ld_wait();
+                        for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(fmaf(-slope, fabsf(first - static_cast<float>(i)), __uint_as_float(v[i])));
+                    }
+                    if (part || missing) {  // a bit for each key
+                        const unsigned two = missing >> c / 16;
+                        const uint32_t gone = (two & 1 ? 0xFFFFu : 0u) | (two & 2 ? 0xFFFF0000u : 0u);
+                        const uint32_t seen = bits_below(to - c) & ~bits_below(from - c) & ~gone;
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) v[i] = seen >> i & 1 ? v[i] : 0xFF800000u;  // -infinity
+                    }
+                    tmem_st_32x32b_x32(t_s + c, v);
+                };
+                // The rule and the masks are applied in place in tensor memory, 32 keys at a time: all at once is more code than the
+                // instruction caches hold beside the loop's (9 ragged prompts, capped, 82 us against 74).  Over bf16 a row is then held in
+                // registers; beside the warps that convert there are too few for that and too little room for its code, and it is
+                // read twice, 32 scores at a time with the next under way (8192 tokens: bf16 371 us held, 413 read twice; 4 bits
+                // 675 and 606).
+                constexpr bool kHeld = kType == BD_KV_BF16;
+                uint32_t x[kHeld ? 4 : 2][32];
+                float most[8];
+#pragma unroll
+                for (int c = 0; c < 8; ++c) most[c] = -INFINITY;  // chains short enough to hide an operation's latency
+                auto look = [&](const uint32_t(&v)[32], float *m) {
+#pragma unroll
+                    for (int i = 0; i < 32; i += 8)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) m[k] = max3(m[k], __uint_as_float(v[i + k]), __uint_as_float(v[i + k + 4]));
+                };
+                if constexpr (kHeld) {
+                    if (rewrite) {
+#pragma unroll 1
+                        for (int c = 0; c < kBlock; c += 32) {
+                            tmem_ld_32x32b_x32(t_s + c, x[0]);
+                            tmem_ld_wait_for(x[0]);
+                            rule(x[0], c);
+                        }
+                        tmem_st_wait();
+                    }
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) tmem_ld_32x32b_x32(t_s + c * 32, x[c]);
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) tmem_ld_wait_for(x[c]);
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) look(x[c], most + c % 2 * 4);
+                } else {
+                    tmem_ld_32x32b_x32(t_s, x[0]);
+#pragma unroll 1
+                    for (int c = 0; c < kBlock; c += 64) {
+                        tmem_ld_wait_for(x[0]);
+                        tmem_ld_32x32b_x32(t_s + c + 32, x[1]);
+                        if (rewrite) rule(x[0], c);
+                        look(x[0], most);
+                        tmem_ld_wait_for(x[1]);
+                        if (rewrite) tmem_st_wait();
+                        tmem_ld_32x32b_x32(t_s + (c + 64) % kBlock, x[0]);  // the next, or the first again
+                        if (rewrite) rule(x[1], c + 32);
+                        look(x[1], most + 4);
+                    }
+                    if (rewrite) tmem_st_wait();
+                }
                 const float scale = a.plain ? unit : 1.f;
-                float most[8];  // chains short enough to hide an operation's latency
-#pragma unroll
-                for (int c = 0; c < 8; ++c) {
-                    const uint32_t(&v)[32] = x[c / 2];
-                    most[c] = fmaxf(__uint_as_float(v[c % 2 * 16]), __uint_as_float(v[c % 2 * 16 + 1]));
-                }
-#pragma unroll
-                for (int i = 2; i < 16; i += 2)
-#pragma unroll
-                    for (int c = 0; c < 8; ++c)
-                        most[c] = max3(most[c], __uint_as_float(x[c / 2][c % 2 * 16 + i]), __uint_as_float(x[c / 2][c % 2 * 16 + i + 1]));
-                const float now = fmaxf(max3(most[0], most[1], most[2]), max3(max3(most[3], most[4], most[5]), most[6], most[7])) * scale;
+                const float now = fmaxf(max3(max3(most[0], most[1], most[2]), most[3], most[4]), max3(most[5], most[6], most[7])) * scale;
                 const bool raise = now > top + kLazy<kType> || (top == -INFINITY && now > top);
                 if (__any_sync(0xFFFFFFFFu, raise)) {
                     float fix = 1.f;
@@ -1024,28 +1062,47 @@ __device__ __forceinline__ void softmax_rows(const PromptArgs &a, const Smem &s,
                     if (__any_sync(0xFFFFFFFFu, fix != 1.f)) {  // not in the first block, where nothing was held yet
                         if (!wait_on(&s.o_full[tile], (s_n - 1) & 1, a, s.abort)) return;
                         tc_fence_after();
+                        if constexpr (!kHeld) tmem_ld_wait_for(x[0]);
                         scale_output<kDim>(t_o, fix);
                     }
                 }
                 const float base = (top == -INFINITY ? 0.f : top) - kLift<kType>;
                 float2 add[2] = {};
-                const float2 scale2 = make_float2(scale, scale), base2 = make_float2(-base, -base);
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
+                auto weights = [&](const uint32_t(&v)[32], int c) {  // of keys c ..
+                    const float2 scale2 = make_float2(scale, scale), base2 = make_float2(-base, -base);
                     uint32_t w[16];
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
-                        float2 e = fma2(make_float2(__uint_as_float(x[c][2 * i]), __uint_as_float(x[c][2 * i + 1])), scale2, base2);
+                        float2 e = fma2(make_float2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), scale2, base2);
                         e.x = ex2(e.x), e.y = ex2(e.y);
                         add[i % 2] = add2(add[i % 2], e);
                         w[i] = kHalf<kType> ? pack_half2(e.x, e.y) : pack_bf16x2(e.x, e.y);
                     }
-                    tmem_st_32x32b_x16(t_p + c * 16, w);
-                    if (c % 2 && !part) {  // 64 keys: their product may begin
-                        tmem_st_wait();
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&s.p_full[2 * tile + c / 2]);
+                    tmem_st_32x32b_x16(t_p + c / 2, w);
+                };
+                auto hand_over = [&](int half) {  // 64 keys: their product may begin
+                    if (part) return;
+                    tmem_st_wait();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&s.p_full[2 * tile + half]);
+                };
+                if constexpr (kHeld) {
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        weights(x[c], c * 32);
+                        if (c % 2) hand_over(c / 2);
+                    }
+                } else {
+#pragma unroll 1
+                    for (int c = 0; c < kBlock; c += 64) {
+                        tmem_ld_wait_for(x[0]);
+                        tmem_ld_32x32b_x32(t_s + c + 32, x[1]);
+                        weights(x[0], c);
+                        tmem_ld_wait_for(x[1]);
+                        if (c == 0) tmem_ld_32x32b_x32(t_s + 64, x[0]);
+                        weights(x[1], c + 32);
+                        hand_over(c / 64);
                     }
                 }
                 if (part) {  // is V finite where it is not seen?
