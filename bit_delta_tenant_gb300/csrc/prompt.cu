@@ -24,13 +24,13 @@
 // are looked at: rows of V that nobody sees are zeroed, and where a finite number is missing in another one, the
 // block's P V is added up by the softmax threads, row by row over the keys that the row sees, instead of by the tensor cores.
 //
-// Measured (head_dim 128, 32 and 8 heads unless said): one prompt of 8192 tokens, bf16, 389 us (1.41 PFLOP/s, 0.74 of
-// cuBLAS's burst): a block takes about 3500 clocks, its products 2048: the thread that issues them shares its scheduler with two
-// softmax warps.  333 tokens 17 us: launch, set-up, three blocks one after the other, output.  Over 8 and 4 bits a block takes
-// about half as long again: the 64 KB that are stored to shared memory for it contend with the products' reads
-// of their operands (48 tokens over 65000, 64 and 8 heads: bf16 116 us, 8 bits 188, 4 bits 186; without conversions, on
-// whatever the tiles held, 135).  Capped scores cost two transcendental operations more each: 9 ragged prompts of up to 1500
-// tokens over up to 1000, 8 bits, 91 us, 56 uncapped.
+// Measured (head_dim 128, 32 and 8 heads unless said): one prompt of 8192 tokens, bf16, 368 us (1.49 PFLOP/s, 0.78 of
+// cuBLAS's burst): a block takes about 3200 clocks, its products 2048; a tile's softmax and its own products follow each other,
+// and the thread that issues them shares its scheduler with two softmax warps.  333 tokens 17 us: launch, set-up, three blocks
+// one after the other, output.  Over 8 and 4 bits a block takes half as long again: the 64 KB that are stored to shared
+// memory for it contend with the products' reads of their operands (48 tokens over 65000, 64 and 8 heads: bf16 109 us, 8 bits 159,
+// 4 bits 168).  Capped scores cost an exponential and a dozen multiplications more each: 9 ragged prompts of up to 1500 tokens
+// over up to 1000, 8 bits, 77 us, 53 uncapped.
 #include <cuda_fp4.h>
 #include <cuda_fp8.h>
 
@@ -1299,8 +1299,9 @@ __global__ void __launch_bounds__(kJoinThreads) prompt_join_kernel(const __grid_
     if (a.lse && eighth == 0) a.lse[row * a.q_heads + head] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.693147180559945f;
 }
 
+size_t table_bytes(int num_sms) { return (static_cast<size_t>(num_sms) * sizeof(int4) + 255) / 256 * 256; }
 template <int kDim>
-size_t part_bytes(int num_sms) { return (static_cast<size_t>(num_sms) * kSlotFloats<kDim> * 4 + 255) / 256 * 256; }
+size_t part_bytes(int num_sms) { return static_cast<size_t>(num_sms) * kSlotFloats<kDim> * 4; }
 
 template <class... Types, class... Args>
 cudaError_t launch_pdl(void (*kernel)(Types...), dim3 grid, int threads, int smem, cudaStream_t stream, const Args &...args) {
@@ -1337,8 +1338,9 @@ cudaError_t launch_dim(const PromptArgs &a, int type, const CUtensorMap &q, cons
 
 }  // namespace
 
+// The counts come first, so that they are where every call looks for them, whatever its head_dim.
 size_t prompt_workspace_size(int num_sms, int head_dim) {
-    return (head_dim == 128 ? part_bytes<128>(num_sms) : part_bytes<64>(num_sms)) + static_cast<size_t>(num_sms) * sizeof(int4) + 256;
+    return 256 + table_bytes(num_sms) + (head_dim == 128 ? part_bytes<128>(num_sms) : part_bytes<64>(num_sms));
 }
 
 cudaError_t launch_prompt(const bd_kv_cache &c, const void *q, int32_t q_heads, const int32_t *offsets, int64_t total,
@@ -1359,10 +1361,10 @@ cudaError_t launch_prompt(const bd_kv_cache &c, const void *q, int32_t q_heads, 
     a.slopes = rule.slopes;
     a.out = static_cast<uint8_t *>(out);
     a.lse = lse;
-    a.parts = static_cast<float *>(workspace);
-    a.heads = reinterpret_cast<int4 *>(static_cast<uint8_t *>(workspace) +
-                                       (c.head_dim == 128 ? part_bytes<128>(ctx.num_sms) : part_bytes<64>(ctx.num_sms)));
-    a.taken = reinterpret_cast<unsigned *>(a.heads + ctx.num_sms);
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    a.taken = reinterpret_cast<unsigned *>(ws);
+    a.heads = reinterpret_cast<int4 *>(ws + 256);
+    a.parts = reinterpret_cast<float *>(ws + 256 + table_bytes(ctx.num_sms));
     a.status = ctx.status;
     a.wait_ns = ctx.wait_ns;
     a.n_pages = c.n_pages;

@@ -126,6 +126,18 @@ def test_rows_of_no_sequence_stay_as_they_are():
     assert (out[50:] == 3).all() and (lse[50:] == 3).all()
 
 
+def test_one_workspace_for_caches_of_either_head_dim():
+    """Split and whole units in turn, on the workspace of the larger head_dim."""
+    cases = [case("bf16", 128, 16, 2, [5], [5000], seed=1), case("bf16", 64, 16, 2, [900], [0], seed=2), case("e2m1", 64, 16, 2, [3], [4000], seed=3),
+             case("e4m3", 128, 16, 2, [900], [0], seed=4)]
+    want = [run(pool, q, [q.shape[0]]) for pool, q in cases]
+    ws = torch.zeros(bd.bd_attention_prompt_workspace_size(cases[0][0].cache(), 16), dtype=torch.uint8, device="cuda")
+    for i in (0, 1, 2, 1, 3, 0, 2, 3, 1):
+        got = run(*cases[i], [cases[i][1].shape[0]], ws=ws)
+        assert all(torch.equal(a, b) for a, b in zip(got, want[i])), i
+    assert bd.bd_get_device_status() == bd.BD_OK
+
+
 @pytest.mark.parametrize("window", [0x7FFFFFFF, 1 << 40])
 def test_the_largest_window_and_no_lse(window):
     """More rows than the sequence is long, whose first positions lie below 0, with a window as wide as there is."""
