@@ -101,7 +101,7 @@ cudaError_t launch_attention(const bd_kv_cache &c, const void *q, int32_t q_head
     a.slopes = rule.slopes;
     a.first = rule.first;
     a.cap = rule.cap * kLog2e;
-    a.cap_in = rule.cap > 0.f ? 2.f / rule.cap : 0.f;
+    a.cap_in = rule.cap > 0.f ? 1.f / a.cap : 0.f;
     const bool scored = rule.cap > 0.f || rule.slopes || rule.first, pack = a.group <= 8;
     if (c.kv_type == BD_KV_E2M1) return launch_attention_four(a, scored, c.head_dim, pack, ctx, stream);
     return scored ? launch_attention_scored(a, c.kv_type, c.head_dim, pack, ctx, stream)

@@ -89,11 +89,16 @@ __device__ __forceinline__ float ex2(float x) {  // 2^x, 0 for -inf
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-// cap tanh(x / cap), x and cap in base 2 and `in` = 2 log2(e) / cap: 1 - 2 / (1 + e^2y), within 2^-22 of cap.
-__device__ __forceinline__ float capped(float x, float cap, float in) {
+// cap tanh(x / cap), x and cap in base 2, y = x / cap: its series where y is small, whose next term is below 2^-23 of y, else
+// 1 - 2 / (1 + e^2y), within 2^-22 of cap.
+__device__ __forceinline__ float capped(float x, float cap, float by_cap) {
+    const float y = x * by_cap, z = y * y;
+    float p = fmaf(z, 62.f / 2835, -17.f / 315);
+    p = fmaf(z, p, 2.f / 15);
+    p = fmaf(z, p, -1.f / 3);
     float r;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + ex2(x * in)));  // of infinity 0
-    return fmaf(-2.f * cap, r, cap);
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + ex2(y * 2.88539008177793f)));  // of infinity 0
+    return fabsf(y) < 0.3125f ? fmaf(x * z, p, x) : fmaf(-2.f * cap, r, cap);
 }
 // A bf16 pair times `up` as e4m3 bytes, and 16 times what they leave as e4m3 bytes.  In fp16 the
 // scaled values (at most 256, 8 bits) and the differences are exact down to 2^-24.

@@ -33,7 +33,7 @@ struct AttnArgs {
     float scale_log2;                 // scale * log2(e): scores are kept in base 2
     const float *slopes;              // a score rule's; NULL: none
     const int32_t *first;
-    float cap, cap_in;                // cap * log2(e), and 2 log2(e) / that; 0: no cap
+    float cap, cap_in;                // cap * log2(e), and 1 / that; 0: no cap
 };
 
 
