@@ -25,7 +25,7 @@
 // block's P V is added up by the softmax threads, row by row over the keys that the row sees, instead of by the tensor cores.
 //
 // Measured (head_dim 128, 32 and 8 heads unless said): one prompt of 8192 tokens, bf16, 368 us (1.49 PFLOP/s, 0.78 of
-// cuBLAS's burst): a block takes about 3200 clocks, its products 2048; a tile's softmax and its own products follow each other,
+// cuBLAS's burst): a block takes about 2900 clocks, its products 2048; a tile's softmax and its own products follow each other,
 // and the thread that issues them shares its scheduler with two softmax warps.  333 tokens 17 us: launch, set-up, three blocks
 // one after the other, output.  Over 8 and 4 bits a block takes half as long again: the 64 KB that are stored to shared
 // memory for it contend with the products' reads of their operands (48 tokens over 65000, 64 and 8 heads: bf16 109 us, 8 bits 159,
