@@ -709,7 +709,7 @@ def bd_attention_prompt(cache: KVCache, q: torch.Tensor, offsets: torch.Tensor, 
     position that each token sees (the start of its document), and tokens before position prefix[i]
     of sequence i are seen by all of its queries.
     `workspace` is a zero-filled device buffer of at least bd_attention_prompt_workspace_size bytes
-    (left ready for the next call)."""
+    (left ready for the next call, of bd_attention_decode too)."""
     device = cache.device
     table, n_seqs, max_pages = _table(page_table, device)
     total, q_heads = (q.shape[0], q.shape[1]) if q.dim() == 3 else (0, 0)

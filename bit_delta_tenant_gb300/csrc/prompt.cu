@@ -1338,9 +1338,10 @@ cudaError_t launch_dim(const PromptArgs &a, int type, const CUtensorMap &q, cons
 
 }  // namespace
 
-// The counts come first, so that they are where every call looks for them, whatever its head_dim.
+// Behind what single tokens' attention uses, so that one workspace does for both.  The counts come first, so that they are where
+// every call looks for them, whatever its head_dim.
 size_t prompt_workspace_size(int num_sms, int head_dim) {
-    return 256 + table_bytes(num_sms) + (head_dim == 128 ? part_bytes<128>(num_sms) : part_bytes<64>(num_sms));
+    return attention_workspace_size(num_sms) + 256 + table_bytes(num_sms) + (head_dim == 128 ? part_bytes<128>(num_sms) : part_bytes<64>(num_sms));
 }
 
 cudaError_t launch_prompt(const bd_kv_cache &c, const void *q, int32_t q_heads, const int32_t *offsets, int64_t total,
@@ -1361,7 +1362,7 @@ cudaError_t launch_prompt(const bd_kv_cache &c, const void *q, int32_t q_heads, 
     a.slopes = rule.slopes;
     a.out = static_cast<uint8_t *>(out);
     a.lse = lse;
-    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    uint8_t *ws = static_cast<uint8_t *>(workspace) + attention_workspace_size(ctx.num_sms);
     a.taken = reinterpret_cast<unsigned *>(ws);
     a.heads = reinterpret_cast<int4 *>(ws + 256);
     a.parts = reinterpret_cast<float *>(ws + 256 + table_bytes(ctx.num_sms));

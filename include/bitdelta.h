@@ -664,7 +664,8 @@ int32_t bd_attention_decode_scored(const bd_kv_cache *cache, const void *q, int3
  *   out         bf16 [total, q_heads, head_dim]           (written; not q)
  *   lse         float [total, q_heads] or NULL            (written)
  *   workspace   as for bd_attention_decode, of
- *               bd_attention_prompt_workspace_size bytes
+ *               bd_attention_prompt_workspace_size bytes, and one that
+ *               serves bd_attention_decode in between as well
  * A length below 0 or beyond max_pages * page_size or 2^30, more rows than the
  * length, offsets that descend or pass total, or a page id out of range sets
  * BD_ERR_BAD_INDEX: the length counts as the nearest allowed one, rows before

@@ -138,6 +138,27 @@ def test_one_workspace_for_caches_of_either_head_dim():
     assert bd.bd_get_device_status() == bd.BD_OK
 
 
+def test_one_workspace_for_prompts_and_single_tokens():
+    """A prompt's, used by single tokens' attention in between: many parts of one sequence, whole and split units."""
+    cases = [case("bf16", 128, 16, 2, [5], [5000], seed=1), case("e4m3", 64, 16, 2, [900], [0], seed=2)]
+    one, q = case("bf16", 128, 32, 2, [1], [40000], seed=3)
+    q, cache, table, lens = q.cuda(), one.cache(), torch.from_numpy(one.table).cuda(), torch.tensor(one.lengths, dtype=torch.int32, device="cuda")
+
+    def token(ws):
+        out = torch.empty_like(q)
+        bd.bd_attention_decode(cache, q, table, lens, out, ws)
+        return out
+
+    want = [run(pool, x, [x.shape[0]]) for pool, x in cases]
+    first = token(torch.zeros(bd.bd_attention_workspace_size(cache, 1, 32), dtype=torch.uint8, device="cuda"))
+    ws = torch.zeros(bd.bd_attention_prompt_workspace_size(cache, 32), dtype=torch.uint8, device="cuda")
+    for i in (0, 1, 1, 0, 1):
+        assert torch.equal(token(ws), first), i
+        assert all(torch.equal(a, b) for a, b in zip(run(*cases[i], [cases[i][1].shape[0]], ws=ws), want[i])), i
+    assert torch.equal(token(ws), first)
+    assert bd.bd_get_device_status() == bd.BD_OK
+
+
 @pytest.mark.parametrize("window", [0x7FFFFFFF, 1 << 40])
 def test_the_largest_window_and_no_lse(window):
     """More rows than the sequence is long, whose first positions lie below 0, with a window as wide as there is."""
