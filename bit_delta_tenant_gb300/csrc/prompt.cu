@@ -15,8 +15,9 @@
 // the next unit and its blocks.  Warp 10 on: K and V of the cache to a ring of shared-memory tiles, by TMA in
 // bf16 (warp 10; warp 11 looks at the blocks that some row sees only in part); 8-bit and 4-bit values are copied as they are and
 // converted by warps 11 to 15.
-// S = Q K^T goes to tensor memory; a softmax thread reads its row, and writes the weights back there as the 16-bit operand of
-// P V, whose accumulator stays in tensor memory.  The two tiles alternate: one's products run under the other's softmax.
+// S = Q K^T goes to tensor memory; a softmax thread reads its row, and writes the weights back there as 16-bit operands of
+// P V, whose accumulator stays in tensor memory: a weight is a 16-bit number and the 16-bit rest, two products, so that no more is lost
+// than in single tokens' attention (2^-16 of a weight; one bf16 number, 2^-8, costs a third less time in long prompts).  The two tiles alternate: one's products run under the other's softmax.
 // The running maximum is raised only when a row passes it by 2^8 (4 bits: 2^3), so that the output is seldom rescaled:
 // weights are at most that, sums stay fp32.
 //
@@ -49,7 +50,7 @@ constexpr int64_t kMaxLength = 1 << 30;
 constexpr int kConvertWarps = 5;
 // A 4-bit cache's values over 8 are fp16 numbers, whatever their scale, and take two operations a pair to make, bf16 ones five:
 // its products are of fp16, Q turned to fp16 in shared memory, each row times a power of two of its own, and the weights
-// times 2^kLift, so that small ones are kept (2^-11 of a weight down to 2^-26 of the largest, nothing below 2^-37).
+// times 2^kLift, so that small ones are kept (two parts are off by 2^-22 of a weight, or by 2^-37 of the largest).
 template <int kType>
 constexpr bool kHalf = kType == BD_KV_E2M1;
 template <int kType>
@@ -420,12 +421,10 @@ __device__ __forceinline__ bool seen_in_part(const Unit &u, int blk) { return bl
 extern __shared__ uint8_t smem_raw[];
 __device__ __forceinline__ uint32_t smem_base() { return (smem_u32(smem_raw) + 1023u) & ~1023u; }
 
-// Tensor memory is allocated whole, so its columns are counted from 0: S of the tiles, O of the tiles, and at head_dim 64
-// the weights P, which at head_dim 128 take S's place (products of one shape run in the order they are issued in).
-template <int kDim>
-struct Columns {
-    static constexpr uint32_t s = 0, o = 2 * kBlock, p = kDim == 128 ? 0 : 2 * kBlock + 2 * kDim, p_tile = kDim == 128 ? kBlock : kBlock / 2;
-};
+// Tensor memory is allocated whole, so its columns are counted from 0: S of the tiles, then O of the tiles.  The weights take the
+// place of the scores that they are made of: for each 16 keys 8 columns of first parts, 8 of second parts.
+constexpr uint32_t kColS = 0, kColO = 2 * kBlock;
+__device__ __forceinline__ constexpr uint32_t weight_at(int key) { return key / 16 * 16 + key % 16 / 2; }  // second part: + 8
 
 // The products with a descriptor's lower word given: its upper word is one for all tiles, and one addition a product is left.
 constexpr uint32_t kDescHigh = (1024 >> 4) | 1u << 14 | 2u << 29;  // 1024 bytes to the next 8 rows, version 1, 128-byte swizzle
@@ -454,18 +453,21 @@ __device__ __forceinline__ void issue_scores(int stage) {
 #pragma unroll
     for (int i = 0; i < kDim / 16; ++i) {
         const uint32_t at = i / 4 * (kBlock * 128 / 16) + i % 4 * 2;
-        mma_ss(Columns<kDim>::s + kTile * kBlock, q + at, k + at, idesc, i > 0);
+        mma_ss(kColS + kTile * kBlock, q + at, k + at, idesc, i > 0);
     }
 }
-// Half of a tile's P V; V's rows are the product's inner dimension, its next 64 columns a column piece further.
+// Half of a tile's P V, each 16 keys' first and second parts; V's rows are the product's inner dimension, its next 64 columns a
+// column piece further.
 template <int kDim, int kType, int kTile, int kPart>
 __device__ __forceinline__ void issue_values(int stage, uint32_t accumulate) {
     constexpr uint32_t idesc = idesc_of<kType>(kDim) | 1u << 16;
     const uint32_t v = desc_low(smem_base() + (2 + stage) * kTileBytes<kDim>, kBlock * 128);
 #pragma unroll
     for (int i = kPart * (kBlock / 32); i < (kPart + 1) * (kBlock / 32); ++i)
-        mma_ts(Columns<kDim>::o + kTile * kDim, Columns<kDim>::p + kTile * Columns<kDim>::p_tile + i * 8, v + i * (16 * 128 / 16), idesc,
-               i > 0 ? 1u : accumulate);
+#pragma unroll
+        for (int second = 0; second < 2; ++second)
+            mma_ts(kColO + kTile * kDim, kColS + kTile * kBlock + weight_at(i * 16) + second * 8, v + i * (16 * 128 / 16), idesc,
+                   i + second > 0 ? 1u : accumulate);
 }
 
 // Run by one thread.  Issuing a product stalls while a few are queued, so this thread's time is the tensor cores': with eight
@@ -476,6 +478,7 @@ __device__ __forceinline__ void issue_products(const PromptArgs &a, const Smem &
     constexpr int kS = kStages<kDim, kType>;
     int it = 0;
     uint32_t p_round[2] = {0, 0}, q_round[2] = {0, 0};
+    uint32_t o_round[2] = {1, 1};  // of a tile's last products; there are none yet
     int stage = 0, loads = 0;
     uint32_t round = 0;  // of the next K or V tile
     bool ok = true;
@@ -497,10 +500,14 @@ __device__ __forceinline__ void issue_products(const PromptArgs &a, const Smem &
         } while (blocks == 0);
         return blocks > 0;
     };
+    // Scores take the place of the last weights.  Products of one shape run in the order they are issued in; at head_dim 64 the
+    // two are of different shapes.
+    auto scores_free = [&](auto tile) { return kDim == 128 || wait_alone(&s.o_full[tile()], o_round[tile()], a, s.abort); };
     auto start_tile = [&](auto tile) {
         constexpr int i = tile();
         if (!wait_alone(kHalf<kType> ? &s.q_ready[i] : &s.q_full[i], q_round[i], a, s.abort)) return false;
         q_round[i] ^= 1;
+        if (!scores_free(tile)) return false;
         issue_scores<kDim, kType, i>(stage);
         tc_commit(&s.s_full[i]);
         if (blocks == 1) tc_commit(&s.q_empty[i]);
@@ -533,8 +540,10 @@ __device__ __forceinline__ void issue_products(const PromptArgs &a, const Smem &
                 p_round[i] ^= 1;
                 if (!slow) issue_values<kDim, kType, i, 1>(v_stage, 1);
                 tc_commit(&s.o_full[i]);
+                o_round[i] ^= 1;
                 if (more) {
                     if (i == 0 && !wait_alone(&s.full[stage], round, a, s.abort)) return false;
+                    if (!scores_free(tile)) return false;
                     issue_scores<kDim, kType, i>(stage);
                     tc_commit(&s.s_full[i]);
                     if (j + 2 == blocks) tc_commit(&s.q_empty[i]);
@@ -848,7 +857,7 @@ __device__ __noinline__ void scale_output(uint32_t t_o, float f) {
 }
 
 // P V of a block whose V is not finite where some row does not see it: row by row over the keys [from, to) that the row
-// sees, whose weights are read from tensor memory in pairs.
+// sees, whose weights are read from tensor memory in pairs, first and second parts.
 template <int kDim, bool half>
 __device__ __noinline__ void add_values(uint32_t t_p, uint32_t t_o, const uint8_t *v, bool fresh, int from, int to, unsigned missing) {
 #pragma unroll 1
@@ -858,9 +867,10 @@ __device__ __noinline__ void add_values(uint32_t t_p, uint32_t t_o, const uint8_
         tmem_ld_wait();
 #pragma unroll 1
         for (int k = 0; k < kBlock; ++k) {
-            const uint32_t two = __float_as_uint(tmem_ld_one(t_p + k / 2));
+            const float2 one = unpack_pair<half>(__float_as_uint(tmem_ld_one(t_p + weight_at(k))));
+            const float2 two = unpack_pair<half>(__float_as_uint(tmem_ld_one(t_p + weight_at(k) + 8)));
             if (k >= from && k < to && !(missing >> k / 16 & 1)) {
-                const float w = k % 2 ? unpack_pair<half>(two).y : unpack_pair<half>(two).x;
+                const float w = k % 2 ? one.y + two.y : one.x + two.x;
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     const uint4 x = *reinterpret_cast<const uint4 *>(v + tile_at(k, c / 8 + h));
@@ -927,7 +937,6 @@ __device__ __forceinline__ void softmax_rows(const PromptArgs &a, const Smem &s,
     const int tile = threadIdx.x / 128, r = threadIdx.x % 128, lane = threadIdx.x % 32;
     const uint32_t lane_base = tmem + (static_cast<uint32_t>(r / 32 * 32) << 16);
     const uint32_t t_s = lane_base + tile * kBlock, t_o = lane_base + 2 * kBlock + tile * kDim;
-    const uint32_t t_p = kDim == 128 ? t_s : lane_base + 2 * kBlock + 2 * kDim + tile * (kBlock / 2);
     int s_n = 0, blocks_before = 0;
     [[maybe_unused]] uint32_t q_round = 0;
     for (int it = 0;; ++it) {
@@ -1070,15 +1079,20 @@ __device__ __forceinline__ void softmax_rows(const PromptArgs &a, const Smem &s,
                 float2 add[2] = {};
                 auto weights = [&](const uint32_t(&v)[32], int c) {  // of keys c ..
                     const float2 scale2 = make_float2(scale, scale), base2 = make_float2(-base, -base);
-                    uint32_t w[16];
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        float2 e = fma2(make_float2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), scale2, base2);
-                        e.x = ex2(e.x), e.y = ex2(e.y);
-                        add[i % 2] = add2(add[i % 2], e);
-                        w[i] = kHalf<kType> ? pack_half2(e.x, e.y) : pack_bf16x2(e.x, e.y);
+                    for (int k = 0; k < 32; k += 16) {
+                        uint32_t w[16];  // first parts, second parts
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            float2 e = fma2(make_float2(__uint_as_float(v[k + 2 * i]), __uint_as_float(v[k + 2 * i + 1])), scale2, base2);
+                            e.x = ex2(e.x), e.y = ex2(e.y);
+                            add[i % 2] = add2(add[i % 2], e);
+                            w[i] = kHalf<kType> ? pack_half2(e.x, e.y) : pack_bf16x2(e.x, e.y);
+                            const float2 left = fma2(unpack_pair<kHalf<kType>>(w[i]), make_float2(-1.f, -1.f), e);  // exact
+                            w[8 + i] = kHalf<kType> ? pack_half2(left.x, left.y) : pack_bf16x2(left.x, left.y);
+                        }
+                        tmem_st_32x32b_x16(t_s + c + k, w);
                     }
-                    tmem_st_32x32b_x16(t_p + c / 2, w);
                 };
                 auto hand_over = [&](int half) {  // 64 keys: their product may begin
                     if (part) return;
@@ -1112,7 +1126,7 @@ __device__ __forceinline__ void softmax_rows(const PromptArgs &a, const Smem &s,
                     if (s.slow[stage] == load + 1) {
                         if (j > 0 && !wait_on(&s.o_full[tile], (s_n - 1) & 1, a, s.abort)) return;
                         tc_fence_after();
-                        add_values<kDim, kHalf<kType>>(t_p, t_o, kv + stage * kTileBytes<kDim>, j == 0, from, to, missing);
+                        add_values<kDim, kHalf<kType>>(t_s, t_o, kv + stage * kTileBytes<kDim>, j == 0, from, to, missing);
                     }
                     tc_fence_before();
                     __syncwarp();

@@ -652,10 +652,10 @@ int32_t bd_attention_decode_scored(const bd_kv_cache *cache, const void *q, int3
  * its row, infinities and NaN included.
  *
  * Scores, softmax statistics and the output's sums are fp32.  The softmax
- * weights enter V's product as bf16 (2^-8 of a weight at most); K and V of an 8-bit
- * cache are multiplied as the bf16 numbers that they stand for.  Over a 4-bit cache
- * the products are of fp16: weights to 2^-11 (nothing below 2^-37 of the largest), q to
- * 2^-31 of its head's largest value.
+ * weights enter V's product as two 16-bit parts each (2^-16 of a weight or better);
+ * K and V of an 8-bit cache are multiplied as the bf16 numbers that they stand for.
+ * Over a 4-bit cache the products are of fp16: weights to 2^-22, or to 2^-37 of the
+ * largest, q to 2^-31 of its head's largest value.
  *
  *   q           bf16 [total, q_heads, head_dim]           (read)
  *   offsets     int32 [n_seqs + 1], ascending from 0      (read)
