@@ -44,11 +44,11 @@
 //
 // 4 bits.  K and V over 8 are fp16 numbers, exactly, whatever their scale: two values are converted and multiplied by their
 // group's scale in two operations, and the products are of fp16 with q times a power of two of its own (values down to 2^-31 of
-// its head's largest as they were) and the weights times 2^15 (2^-11 of a weight down to 2^-29 of the largest).  A lane reads
+// its head's largest as they were) and the weights times 2^15 in two fp16 parts (2^-22 of a weight, or 2^-40 of the largest).  A lane reads
 // a quarter of a key's 64 bytes for S and a sixteenth of four keys' for O, whose scale is one: a column group of 16.  Bound:
-// the conversions and their multiplications, 128 operations of two clocks for 16 keys beside about 300 others: 130001 tokens,
-// 64 and 8 heads, 49.6 us (3.0 TB/s), 64 sequences of up to 8191, 32 and 8 heads, biased by distance, 32 (2.1 TB/s); with one
-// tile in flight instead of three 50 and 36.
+// latency and issue; the conversions and their multiplications are 128 operations of two clocks for 16 keys beside about 300
+// others: 130001 tokens, 64 and 8 heads, 54.6 us (2.7 TB/s), 64 sequences of up to 8191, 32 and 8 heads, biased by distance, 34.9
+// (2.0 TB/s); 49.6 and 32 with weights of one part, then with one tile in flight instead of three 50 and 36.
 // A score rule (attention_scored.cu) takes two more transcendental operations for a capped score: 777 tokens, bf16, capped, 9.2 us.
 #include "attention.h"
 

@@ -599,15 +599,13 @@ __device__ __forceinline__ void stream(const AttnArgs &a, uint8_t *smem, const S
 #pragma unroll
                 for (int u = 0; u < kSub; ++u) {
                     uint32_t p[kHalves][2];
-                    [[maybe_unused]] uint32_t p2[kHalves][2];  // P^T and its remainder
+                    uint32_t p2[kHalves][2];  // P^T and its remainder
 #pragma unroll
                     for (int h = 0; h < kHalves; ++h)
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
                             const float x = s[2 * u + i][2 * h], y = s[2 * u + i][2 * h + 1];
-                            if constexpr (kFour) {
-                                p[h][i] = pack_half2(x, y);
-                            } else if constexpr (kE4m3) {
+                            if constexpr (kFour || kE4m3) {
                                 p[h][i] = pack_half2(x, y);
                                 const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&p[h][i]));
                                 p2[h][i] = pack_half2(x - f.x, y - f.y);
@@ -655,7 +653,10 @@ __device__ __forceinline__ void stream(const AttnArgs &a, uint8_t *smem, const S
                                 const uint32_t a0 = hmul2(v0[d], f[0]), a1 = hmul2(v1[d], f[0]);
                                 const uint32_t a2 = hmul2(v2[d], f[1]), a3 = hmul2(v3[d], f[1]);
 #pragma unroll
-                                for (int h = 0; h < kHalves; ++h) mma16<true>(o[4 * i + d][h], a0, a1, a2, a3, p[h][0], p[h][1]);
+                                for (int h = 0; h < kHalves; ++h) {
+                                    mma16<true>(o[4 * i + d][h], a0, a1, a2, a3, p[h][0], p[h][1]);
+                                    mma16<true>(o[4 * i + d][h], a0, a1, a2, a3, p2[h][0], p2[h][1]);
+                                }
                             }
                         }
                     } else if constexpr (kE4m3) {
