@@ -307,7 +307,8 @@ __device__ __forceinline__ void stream(const AttnArgs &a, uint8_t *smem, const S
                 if (a.slopes && on) slope[half] = a.slopes[kvh * a.group + row0 + g + half * 8] * 1.44269504088896f;
             if constexpr (kFour) {
                 // lane t's quarter of a head, four dims to a step: fp16, times a power of two that brings the head's
-                // largest value to [2^14, 2^15), so that values down to 2^-31 of it are as they were
+                // largest value to [2^14, 2^15), so that values down to 2^-31 of it are as they were.  2^127 is the largest such power:
+                // times that, bf16's smallest number is 2^-6 and a head of small numbers is as it was
                 uint2 v[kSteps];
                 uint32_t top2 = 0;
 #pragma unroll
@@ -318,8 +319,7 @@ __device__ __forceinline__ void stream(const AttnArgs &a, uint8_t *smem, const S
                 top2 = __vmaxu2(top2, __shfl_xor_sync(0xFFFFFFFFu, top2, 1));
                 top2 = __vmaxu2(top2, __shfl_xor_sync(0xFFFFFFFFu, top2, 2));
                 const uint32_t top = max(top2 & 0xFFFFu, top2 >> 16);
-                int e = static_cast<int>(top >> 7);
-                e = e < 27 || e > 227 ? 127 : e;
+                const int e = max(14, min(254, static_cast<int>(top >> 7)));
                 const float up = __uint_as_float(static_cast<uint32_t>(254 + 14 - e) << 23);
                 // scale bytes enter as an eighth of their value
                 rscale[half] = top >= 0x7F80u ? NAN : a.scale_log2 * __uint_as_float(static_cast<uint32_t>(e - 14 + 3) << 23);
@@ -350,9 +350,9 @@ __device__ __forceinline__ void stream(const AttnArgs &a, uint8_t *smem, const S
                 top2 = __vmaxu2(top2, __shfl_xor_sync(0xFFFFFFFFu, top2, 1));
                 top2 = __vmaxu2(top2, __shfl_xor_sync(0xFFFFFFFFu, top2, 2));
                 const uint32_t top = max(top2 & 0xFFFFu, top2 >> 16);
-                // 2^(e - 127) <= largest < 2^(e - 126); rows of zeros, next to zero or next to infinity take e = 127
-                int e = static_cast<int>(top >> 7);
-                e = e < 27 || e > 227 ? 127 : e;
+                // 2^(e - 127) <= largest < 2^(e - 126), from 2^-119 on: times 2^126, smaller rows are multiples of 2^-7 whose
+                // parts are exact
+                const int e = max(8, min(254, static_cast<int>(top >> 7)));
                 const float up = __uint_as_float(static_cast<uint32_t>(254 + 7 - e) << 23);  // to [128, 256)
                 // neither infinity nor NaN has an e4m3 form that keeps it through a product: such a head is NaN throughout
                 rscale[half] = top >= 0x7F80u ? NAN : a.scale_log2 * __uint_as_float(static_cast<uint32_t>(e - 7) << 23);

@@ -908,7 +908,8 @@ __device__ __noinline__ unsigned missing_pieces(const PromptArgs &a, const Unit 
 }
 
 // A row of Q in shared memory to fp16, times the power of two that brings its largest value to [2^14, 2^15), so that values down to
-// 2^-31 of it are as they were; what the products have to be multiplied by (NaN for a row that is not finite).
+// 2^-31 of it are as they were; what the products have to be multiplied by (NaN for a row that is not finite).  2^127 is the largest
+// such power: times that, bf16's smallest number is 2^-6 and a row of small numbers is as it was.
 template <int kDim>
 __device__ __forceinline__ float query_to_half(uint8_t *q, int r) {
     uint32_t top2 = 0;
@@ -918,8 +919,7 @@ __device__ __forceinline__ float query_to_half(uint8_t *q, int r) {
         top2 = __vmaxu2(__vmaxu2(top2, x.x & 0x7FFF7FFFu), __vmaxu2(x.y & 0x7FFF7FFFu, __vmaxu2(x.z & 0x7FFF7FFFu, x.w & 0x7FFF7FFFu)));
     }
     const uint32_t top = max(top2 & 0xFFFFu, top2 >> 16);
-    int e = static_cast<int>(top >> 7);
-    e = e < 27 || e > 227 ? 127 : e;  // zeros, and rows next to zero or infinity
+    const int e = max(14, min(254, static_cast<int>(top >> 7)));
     const float up = __uint_as_float(static_cast<uint32_t>(254 + 14 - e) << 23);
 #pragma unroll 4
     for (int c = 0; c < kDim / 8; ++c) {
@@ -972,6 +972,8 @@ __device__ __forceinline__ void softmax_rows(const PromptArgs &a, const Smem &s,
                     if (!wait_on(&s.q_full[tile], q_round, a, s.abort)) return;
                     q_round ^= 1;
                     unit *= query_to_half<kDim>(const_cast<uint8_t *>(kv) - (2 - tile) * kTileBytes<kDim>, r);
+                    // plain scores are multiplied by it after the masks: it may not be 0.  Products are below 2^36, so these scores are 0
+                    if (a.plain && unit < 0x1p-126f) unit = 0x1p-126f;
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&s.q_ready[tile]);
