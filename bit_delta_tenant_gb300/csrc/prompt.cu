@@ -827,18 +827,58 @@ __device__ __forceinline__ void tmem_ld_wait_for(uint32_t (&v)[32]) {
         : "memory");
 }
 
-// cap tanh of two products, `in` = 2 log2(e) scale / cap: with e = exp(-2 |y|), tanh |y| = 2 / (1 + e) - 1.  The reciprocal is
+// cap tanh of two products given as y = 2 log2(e) / cap times their scores.  Small ones by the tangent's series (from |y| = kSmall on
+// the next term passes 2^-23 of the value), whose error is relative to the score, not to cap.
+constexpr float kSmall = 0.9f;  // scores of 0.31 cap
+__device__ __forceinline__ float2 capped_small(float2 y, float cap) {
+    const float2 x = mul2(y, make_float2(0.34657359027997f, 0.34657359027997f)), z = mul2(x, x);  // ln(2) / 2
+    float2 p = fma2(z, make_float2(62.f / 2835, 62.f / 2835), make_float2(-17.f / 315, -17.f / 315));
+    p = fma2(z, p, make_float2(2.f / 15, 2.f / 15));
+    p = fma2(z, p, make_float2(-1.f / 3, -1.f / 3));
+    return mul2(fma2(mul2(x, z), p, x), make_float2(cap, cap));
+}
+// Any: with e = exp(-2 |x|), tanh |x| = 2 / (1 + e) - 1.  The reciprocal is
 // Newton's, two steps from (98 - 80 e + 32 e^2) / 99, which is within 1/99 for e in [0, 1]: the transcendental unit, with an
 // exponential here and one for the weight, is the busier one.
-__device__ __forceinline__ float2 capped(float2 x, float2 in, float cap) {
-    const float2 y = mul2(x, in), e = make_float2(ex2(-fabsf(y.x)), ex2(-fabsf(y.y)));
+__device__ __forceinline__ float2 capped(float2 y, float cap) {
+    const float2 e = make_float2(ex2(-fabsf(y.x)), ex2(-fabsf(y.y)));
     const float2 one = make_float2(1.f, 1.f), minus = make_float2(-1.f, -1.f);
     const float2 q = fma2(e, minus, minus);  // -(1 + e)
     float2 r = fma2(e, fma2(e, make_float2(32.f / 99, 32.f / 99), make_float2(-80.f / 99, -80.f / 99)), make_float2(98.f / 99, 98.f / 99));
     r = fma2(r, fma2(q, r, one), r);
     r = fma2(r, fma2(q, r, one), r);
     r = fma2(r, make_float2(2.f * cap, 2.f * cap), make_float2(-cap, -cap));
-    return make_float2(copysignf(r.x, y.x), copysignf(r.y, y.y));
+    const float2 small = capped_small(y, cap);
+    return make_float2(fabsf(y.x) < kSmall ? small.x : copysignf(r.x, y.x), fabsf(y.y) < kSmall ? small.y : copysignf(r.y, y.y));
+}
+
+// A row's products to capped scores, in place.  `in`: 2 log2(e) / cap of a product's score.  Apart: beside the rest of a softmax thread's loop
+// its code and registers slow down calls without a cap too.
+__device__ __noinline__ void cap_scores(uint32_t t_s, float in, float cap) {
+#pragma unroll 1
+    for (int c = 0; c < kBlock; c += 32) {
+        uint32_t v[32];
+        tmem_ld_32x32b_x32(t_s + c, v);
+        tmem_ld_wait_for(v);
+        float largest = 0.f;
+#pragma unroll
+        for (int i = 0; i < 32; i += 2) {
+            const float2 y = mul2(make_float2(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), make_float2(in, in));
+            largest = max3(largest, fabsf(y.x), fabsf(y.y));
+            v[i] = __float_as_uint(y.x), v[i + 1] = __float_as_uint(y.y);
+        }
+        auto each = [&](auto cap_of) {
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) {
+                const float2 y = cap_of(make_float2(__uint_as_float(v[i]), __uint_as_float(v[i + 1])));
+                v[i] = __float_as_uint(y.x), v[i + 1] = __float_as_uint(y.y);
+            }
+        };
+        if (__any_sync(0xFFFFFFFFu, largest >= kSmall)) each([&](float2 y) { return capped(y, cap); });
+        else each([&](float2 y) { return capped_small(y, cap); });
+        tmem_st_32x32b_x32(t_s + c, v);
+    }
+    tmem_st_wait();
 }
 
 // The rows' output so far, times f.  Seldom run: apart, so that its registers are not the loop's.
@@ -987,15 +1027,14 @@ __device__ __forceinline__ void softmax_rows(const PromptArgs &a, const Smem &s,
                 unsigned missing = 0;
                 if (gaps) missing = missing_pieces(a, u, key0 / kBlock);
                 const bool part = key0 < in_lo || key0 + kBlock > in_hi;  // some row sees the block in part
-                const bool rewrite = !a.plain || part || missing;
-                const float far = static_cast<float>(p - key0), in = a.cap > 0.f ? unit * a.cap_in : unit;
+                if (a.cap > 0.f) cap_scores(t_s, unit * a.cap_in, a.cap);
+                const bool rewrite = !(a.plain || a.cap > 0.f) || a.slopes || part || missing;
+                const float far = static_cast<float>(p - key0);
                 auto rule = [&](uint32_t(&v)[32], int c) {  // on the scores of keys c ..
-                    if (!a.plain) {
-                        const float2 in2 = make_float2(in, in);
+                    if (!a.plain && !(a.cap > 0.f)) {
 #pragma unroll
                         for (int i = 0; i < 32; i += 2) {
-                            float2 y = make_float2(__uint_as_float(v[i]), __uint_as_float(v[i + 1]));
-                            y = a.cap > 0.f ? capped(y, in2, a.cap) : mul2(y, in2);
+                            const float2 y = mul2(make_float2(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), make_float2(unit, unit));
                             v[i] = __float_as_uint(y.x), v[i + 1] = __float_as_uint(y.y);
                         }
                     }
@@ -1013,7 +1052,7 @@ __device__ __forceinline__ void softmax_rows(const PromptArgs &a, const Smem &s,
                     }
                     tmem_st_32x32b_x32(t_s + c, v);
                 };
-                // The rule and the masks are applied in place in tensor memory, 32 keys at a time: all at once is more code than the
+                // Caps, biases and masks are applied in place in tensor memory, 32 keys at a time: all at once is more code than the
                 // instruction caches hold beside the loop's (9 ragged prompts, capped, 82 us against 74).  Over bf16 a row is then held in
                 // registers; beside the warps that convert there are too few for that and too little room for its code, and it is
                 // read twice, 32 scores at a time with the next under way (8192 tokens: bf16 371 us held, 413 read twice; 4 bits

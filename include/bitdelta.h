@@ -619,7 +619,7 @@ int32_t bd_attention_decode(const bd_kv_cache *cache, const void *q, int32_t q_h
  *   j >= first[.]                   (the start of its document; one number per
  *                                    query, negative ones count as 0)
  * A query that sees nothing gives zeros and lse = -inf.  Scores are fp32; the
- * capped ones are within 2^-21 of cap.  Slopes are finite.
+ * cap leaves them within 2^-21 of cap and within 2^-19 of themselves.  Slopes are finite.
  * ------------------------------------------------------------------------ */
 typedef struct bd_score_rule {
     float scale;
