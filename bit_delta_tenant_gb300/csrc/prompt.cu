@@ -235,15 +235,17 @@ struct Sequence {
     int32_t row0, n, len, prefix;
     int32_t units, blocks;  // of a KV head: tiles' pairs, and blocks of the longest
 };
-__device__ __forceinline__ Sequence sequence_of(const PromptArgs &a, int64_t i) {
+// `ordered`: false where its offsets are no rows of q.
+__device__ __forceinline__ Sequence sequence_of(const PromptArgs &a, int64_t i, bool &ordered) {
     Sequence s = {};
     const int32_t from = a.offsets[i], to = a.offsets[i + 1];
     const int64_t most = min(static_cast<int64_t>(a.max_pages) * a.page_size, kMaxLength);
     int64_t len = a.lengths[i];
-    if (from < 0 || to < from || to > a.total || len < 0 || len > most) flag_status(a.status, kDevBadIndex);
+    ordered = from >= 0 && to >= from && to <= a.total;
+    if (!ordered || len < 0 || len > most || (i == 0 && from != 0)) flag_status(a.status, kDevBadIndex);
     len = len < 0 ? 0 : len > most ? most : len;
     s.len = static_cast<int32_t>(len);
-    if (from < 0 || to < from || to > a.total) return s;
+    if (!ordered) return s;
     s.row0 = from;
     s.n = to - from;
     if (s.n > s.len) flag_status(a.status, kDevBadIndex);
@@ -270,6 +272,32 @@ __device__ __forceinline__ int64_t warp_scan(int64_t v) {  // inclusive
     return v;
 }
 
+// A pass over the sequences, 32 at a time, a lane each.  Sequences that begin before an offset that came earlier are left out, so that no two
+// have a row in common.
+struct Pass {
+    bool disorder = false;
+    int32_t top = INT_MIN;  // of the offsets so far, from the first disorder on
+    __device__ __forceinline__ Sequence take(const PromptArgs &a, int64_t i) {
+        Sequence s = {};
+        bool ordered = true;
+        if (i < a.n_seqs) s = sequence_of(a, i, ordered);
+        disorder |= __any_sync(0xFFFFFFFFu, !ordered);
+        if (disorder) {  // until now the offsets ascended to this lot's first
+            const int32_t from = i < a.n_seqs ? a.offsets[i] : INT_MIN;
+            int32_t most = from;
+#pragma unroll
+            for (int o = 1; o < 32; o *= 2) {
+                const int32_t u = __shfl_up_sync(0xFFFFFFFFu, most, o);
+                if (static_cast<int>(threadIdx.x % 32) >= o) most = max(most, u);
+            }
+            most = max(most, top);
+            if (from < most) s = Sequence{};
+            top = __shfl_sync(0xFFFFFFFFu, most, 31);
+        }
+        return s;
+    }
+};
+
 __device__ __forceinline__ int size_class(const Sequence &q) { return q.units > 0 ? 31 - __clz(max(q.blocks, 1)) : -1; }
 
 // Warp 9.  Units are numbered sequence by sequence, those of most keys first by powers of two, in each from its last tile to
@@ -282,8 +310,9 @@ __device__ __forceinline__ void find_units(const PromptArgs &a, const Smem &s) {
     unsigned classes = 0;
     int64_t units = 0, blocks = 0;
     Sequence q = {};
-    for (int64_t i = lane; i < a.n_seqs; i += 32) {
-        q = sequence_of(a, i);
+    Pass pass;
+    for (int64_t i = lane; i - lane < a.n_seqs; i += 32) {
+        q = pass.take(a, i);
         if (q.units > 0) classes |= 1u << size_class(q);
         units += q.units, blocks += static_cast<int64_t>(q.units) * q.blocks;
     }
@@ -294,8 +323,9 @@ __device__ __forceinline__ void find_units(const PromptArgs &a, const Smem &s) {
             most = max(4, static_cast<int32_t>((blocks + a.slots - 1) / a.slots));
             while (true) {
                 int64_t pieces = 0;
-                for (int64_t i = lane; i < a.n_seqs; i += 32) {
-                    if (a.n_seqs > 32) q = sequence_of(a, i);
+                pass = Pass{};
+                for (int64_t i = lane; i - lane < a.n_seqs; i += 32) {
+                    if (a.n_seqs > 32) q = pass.take(a, i);
                     pieces += static_cast<int64_t>(q.units) * pieces_of(q, most);
                 }
                 if (warp_sum(pieces) * vheads <= a.slots) break;
@@ -314,11 +344,9 @@ __device__ __forceinline__ void find_units(const PromptArgs &a, const Smem &s) {
             if (classes == 0) return false;
             cls = 31 - __clz(classes);
             first = 0;
+            pass = Pass{};
         }
-        if (a.n_seqs > 32) {  // else each lane has its own still
-            q = Sequence{};
-            if (first + lane < a.n_seqs) q = sequence_of(a, first + lane);
-        }
+        if (a.n_seqs > 32) q = pass.take(a, first + lane);  // else each lane has its own still
         mine = size_class(q) == cls ? static_cast<int64_t>(q.units) * pieces_of(q, most) * vheads : 0;
         upto = warp_scan(mine);
         all = __shfl_sync(0xFFFFFFFFu, upto, 31);

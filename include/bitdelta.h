@@ -667,10 +667,11 @@ int32_t bd_attention_decode_scored(const bd_kv_cache *cache, const void *q, int3
  *               bd_attention_prompt_workspace_size bytes, and one that
  *               serves bd_attention_decode in between as well
  * A length below 0 or beyond max_pages * page_size or 2^30, more rows than the
- * length, offsets that descend or pass total, or a page id out of range sets
- * BD_ERR_BAD_INDEX: the length counts as the nearest allowed one, rows before
- * position 0 see nothing, rows out of order are left out, and the keys of such a
- * page count as unseen.
+ * length, offsets that do not begin with 0, descend or pass total, or a page id out of
+ * range sets BD_ERR_BAD_INDEX: the length counts as the nearest allowed one, rows
+ * before position 0 see nothing, and the keys of such a page count as unseen.  A
+ * sequence is left out (its rows stay as they are) where its offsets descend, lie
+ * outside 0 .. total, or begin below one that came earlier, so that no row is written twice.
  * Results do not depend on timing.
  * Errors: as bd_attention_decode.
  * ------------------------------------------------------------------------ */
