@@ -96,7 +96,7 @@ BD_API int32_t bd_kv_append(const bd_kv_cache *cache, const void *q, int32_t q_h
 BD_API int32_t bd_rotary_table(float *table, int64_t positions, int32_t dim, double base, double factor, double original,
                                double low, double high, double amplitude, void *stream) {
     if (positions < 0 || dim < 1 || (positions > 0 && !table)) return BD_ERR_INVALID_ARG;
-    for (const double v : {base, factor, original, low, high, amplitude})
+    for (const double v : {base, factor, original, low, high, static_cast<double>(static_cast<float>(amplitude))})
         if (!(v - v == 0)) return BD_ERR_INVALID_ARG;
     if (!(base > 0) || !(factor > 0) || !(original >= 0) || !(high > low)) return BD_ERR_INVALID_ARG;
     if (dim % 2 != 0 || dim > BD_ROTARY_MAX_DIM || positions >= BD_MAX_DIM) return BD_ERR_UNSUPPORTED_SHAPE;

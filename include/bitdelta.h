@@ -539,7 +539,7 @@ int32_t bd_kv_append_rotary(const bd_kv_cache *cache, const void *q, int32_t q_h
  *   table       float [positions, dim]                       (written)
  * dim: even, 2 .. BD_ROTARY_MAX_DIM; rows of a dim that is a multiple of 8 are
  * written in 16-byte pieces.  base > 0, factor > 0, original >= 0, high > low,
- * all of them and all f'_i finite.  positions = 0 launches nothing.
+ * all of them and all f'_i finite, amplitude as a float.  positions = 0 launches nothing.
  * Errors: BD_ERR_INVALID_ARG, BD_ERR_UNSUPPORTED_SHAPE, BD_ERR_MISALIGNED,
  *         BD_ERR_CUDA.
  * ------------------------------------------------------------------------ */
