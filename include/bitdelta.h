@@ -535,7 +535,8 @@ int32_t bd_kv_append_rotary(const bd_kv_cache *cache, const void *q, int32_t q_h
  * of `low` and fewer are slowed down by `factor`.  original = 0 slows all of them
  * (positions interpolated), factor = 1 none.  Angles are kept as whole numbers of
  * 2^-64 turns, so that far positions are as exact as near ones: within 2^-22 of
- * the amplitude for positions below 2^28.
+ * the amplitude where p f'_i is below 2^27 (positions below 2^27 at frequencies of
+ * at most 1); beyond that the 64-bit frequencies' own rounding shows, 2^-50 p f'_i.
  *   table       float [positions, dim]                       (written)
  * dim: even, 2 .. BD_ROTARY_MAX_DIM; rows of a dim that is a multiple of 8 are
  * written in 16-byte pieces.  base > 0, factor > 0, original >= 0, high > low,
