@@ -653,7 +653,8 @@ int32_t bd_attention_decode_scored(const bd_kv_cache *cache, const void *q, int3
  * its row, infinities and NaN included.
  *
  * Scores, softmax statistics and the output's sums are fp32.  The softmax
- * weights enter V's product as two 16-bit parts each (2^-16 of a weight or better);
+ * weights enter V's product as two 16-bit parts each (2^-16 of a weight or better;
+ * an infinite V that a query sees may therefore give NaN);
  * K and V of an 8-bit cache are multiplied as the bf16 numbers that they stand for.
  * Over a 4-bit cache the products are of fp16: weights to 2^-22, or to 2^-37 of the
  * largest, q to 2^-31 of its head's largest value.
