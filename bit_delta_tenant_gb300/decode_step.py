@@ -49,6 +49,12 @@ class Shape:
                 ("gate", self.mlp, self.hidden), ("up", self.mlp, self.hidden), ("down", self.hidden, self.mlp)]
 
 
+def rope_table(positions: int, dim: int, base: float) -> torch.Tensor:
+    """fp32 [positions, dim] on the CPU: cosines, then sines, of position * base^(-2i / dim), as bd_rotary_table makes them unscaled."""
+    angle = torch.arange(positions, dtype=torch.float64)[:, None] * base ** (-torch.arange(0, dim, 2, dtype=torch.float64) / dim)
+    return torch.cat([angle.cos(), angle.sin()], 1).float()
+
+
 class Matrix:
     """A base matrix and its variants' packed deltas."""
 
