@@ -1080,13 +1080,10 @@ __device__ __forceinline__ void softmax_rows(const PromptArgs &a, const Smem &s,
                     }
                     tmem_st_32x32b_x32(t_s + c, v);
                 };
-                // Caps, biases and masks are applied in place in tensor memory, 32 keys at a time: all at once is more code than the
-                // instruction caches hold beside the loop's (9 ragged prompts, capped, 82 us against 74).  Over bf16 a row is then held in
-                // registers; beside the warps that convert there are too few for that and too little room for its code, and it is
-                // read twice, 32 scores at a time with the next under way (8192 tokens: bf16 371 us held, 413 read twice; 4 bits
-                // 675 and 606).
-                constexpr bool kHeld = kType == BD_KV_BF16;
-                uint32_t x[kHeld ? 4 : 2][32];
+                // Caps, biases and masks are applied in place in tensor memory, 32 keys at a time, and the scores are read twice, 32 at a
+                // time with the next under way: a row held in registers and its code unrolled are more than the registers and the
+                // instruction caches have room for (8192 tokens, bf16: 486 us, 526 held).
+                uint32_t x[2][32];
                 float most[8];
 #pragma unroll
                 for (int c = 0; c < 8; ++c) most[c] = -INFINITY;  // chains short enough to hide an operation's latency
@@ -1096,38 +1093,20 @@ __device__ __forceinline__ void softmax_rows(const PromptArgs &a, const Smem &s,
 #pragma unroll
                         for (int k = 0; k < 4; ++k) m[k] = max3(m[k], __uint_as_float(v[i + k]), __uint_as_float(v[i + k + 4]));
                 };
-                if constexpr (kHeld) {
-                    if (rewrite) {
+                tmem_ld_32x32b_x32(t_s, x[0]);
 #pragma unroll 1
-                        for (int c = 0; c < kBlock; c += 32) {
-                            tmem_ld_32x32b_x32(t_s + c, x[0]);
-                            tmem_ld_wait_for(x[0]);
-                            rule(x[0], c);
-                        }
-                        tmem_st_wait();
-                    }
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) tmem_ld_32x32b_x32(t_s + c * 32, x[c]);
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) tmem_ld_wait_for(x[c]);
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) look(x[c], most + c % 2 * 4);
-                } else {
-                    tmem_ld_32x32b_x32(t_s, x[0]);
-#pragma unroll 1
-                    for (int c = 0; c < kBlock; c += 64) {
-                        tmem_ld_wait_for(x[0]);
-                        tmem_ld_32x32b_x32(t_s + c + 32, x[1]);
-                        if (rewrite) rule(x[0], c);
-                        look(x[0], most);
-                        tmem_ld_wait_for(x[1]);
-                        if (rewrite) tmem_st_wait();
-                        tmem_ld_32x32b_x32(t_s + (c + 64) % kBlock, x[0]);  // the next, or the first again
-                        if (rewrite) rule(x[1], c + 32);
-                        look(x[1], most + 4);
-                    }
+                for (int c = 0; c < kBlock; c += 64) {
+                    tmem_ld_wait_for(x[0]);
+                    tmem_ld_32x32b_x32(t_s + c + 32, x[1]);
+                    if (rewrite) rule(x[0], c);
+                    look(x[0], most);
+                    tmem_ld_wait_for(x[1]);
                     if (rewrite) tmem_st_wait();
+                    tmem_ld_32x32b_x32(t_s + (c + 64) % kBlock, x[0]);  // the next, or the first again
+                    if (rewrite) rule(x[1], c + 32);
+                    look(x[1], most + 4);
                 }
+                if (rewrite) tmem_st_wait();
                 const float scale = a.plain ? unit : 1.f;
                 const float now = fmaxf(max3(max3(most[0], most[1], most[2]), most[3], most[4]), max3(most[5], most[6], most[7])) * scale;
                 const bool raise = now > top + kLazy<kType> || (top == -INFINITY && now > top);
@@ -1140,7 +1119,7 @@ __device__ __forceinline__ void softmax_rows(const PromptArgs &a, const Smem &s,
                     if (__any_sync(0xFFFFFFFFu, fix != 1.f)) {  // not in the first block, where nothing was held yet
                         if (!wait_on(&s.o_full[tile], (s_n - 1) & 1, a, s.abort)) return;
                         tc_fence_after();
-                        if constexpr (!kHeld) tmem_ld_wait_for(x[0]);
+                        tmem_ld_wait_for(x[0]);
                         scale_output<kDim>(t_o, fix);
                     }
                 }
@@ -1170,23 +1149,15 @@ __device__ __forceinline__ void softmax_rows(const PromptArgs &a, const Smem &s,
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&s.p_full[2 * tile + half]);
                 };
-                if constexpr (kHeld) {
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        weights(x[c], c * 32);
-                        if (c % 2) hand_over(c / 2);
-                    }
-                } else {
 #pragma unroll 1
-                    for (int c = 0; c < kBlock; c += 64) {
-                        tmem_ld_wait_for(x[0]);
-                        tmem_ld_32x32b_x32(t_s + c + 32, x[1]);
-                        weights(x[0], c);
-                        tmem_ld_wait_for(x[1]);
-                        if (c == 0) tmem_ld_32x32b_x32(t_s + 64, x[0]);
-                        weights(x[1], c + 32);
-                        hand_over(c / 64);
-                    }
+                for (int c = 0; c < kBlock; c += 64) {
+                    tmem_ld_wait_for(x[0]);
+                    tmem_ld_32x32b_x32(t_s + c + 32, x[1]);
+                    weights(x[0], c);
+                    tmem_ld_wait_for(x[1]);
+                    if (c == 0) tmem_ld_32x32b_x32(t_s + 64, x[0]);
+                    weights(x[1], c + 32);
+                    hand_over(c / 64);
                 }
                 if (part) {  // is V finite where it is not seen?
                     const int load = 2 * (blocks_before + j) + 1, stage = load % kS;
@@ -1316,7 +1287,7 @@ __global__ void __launch_bounds__(kThreadsOf<kType>, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *s.tmem;  // 0: all of it is this CTA's
-    // a softmax thread holds a row of 128 scores: 384 threads start with 168 registers each, 512 with 128
+    // softmax threads hold most: 384 threads start with 168 registers each, 512 with 128
     if (warp < 8) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kConvert ? 184 : 216));
     else asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     if (warp < 8) {
