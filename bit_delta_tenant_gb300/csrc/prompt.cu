@@ -2,8 +2,8 @@
 //
 //   o = sum_j exp(s_j - m) V_j / sum_j exp(s_j - m),  s_j the score rule of q . K_j
 //
-// Bound: tensor cores (4 head_dim products per seen pair; a block of 128 keys against 256 rows is 2048 clocks of
-// tcgen05 at head_dim 128, its 32768 exponentials about half of that), HBM or latency for a few queries.
+// Bound: tensor cores (4 head_dim products per seen pair, and 2 head_dim for the second parts of its weights; a block of 128 keys against
+// 256 rows is 3072 clocks of tcgen05 at head_dim 128, its 32768 exponentials about a third of that), HBM or latency for a few queries.
 //
 // Work.  A row is one query of one head; the heads that share a KV head are rows of the same tile, so that K and V are
 // read once for all of them and a tile of 128 rows holds 128 / heads tokens.  A unit is two such tiles (256 rows) of
@@ -16,8 +16,9 @@
 // bf16 (warp 10; warp 11 looks at the blocks that some row sees only in part); 8-bit and 4-bit values are copied as they are and
 // converted by warps 11 to 15.
 // S = Q K^T goes to tensor memory; a softmax thread reads its row, and writes the weights back there as 16-bit operands of
-// P V, whose accumulator stays in tensor memory: a weight is a 16-bit number and the 16-bit rest, two products, so that no more is lost
-// than in single tokens' attention (2^-16 of a weight; one bf16 number, 2^-8, costs a third less time in long prompts).  The two tiles alternate: one's products run under the other's softmax.
+// P V, whose accumulator stays in tensor memory.  The two tiles alternate: one's products run under the other's softmax.
+// A weight is a 16-bit number and the 16-bit rest, two products, so that no more is lost than in single tokens' attention: 2^-16 of it
+// (one bf16 number: 2^-8, outputs off by 2.2e-3 where their own rounding is 1.6e-3, 8192 tokens in 391 us instead of 521).
 // The running maximum is raised only when a row passes it by 2^8 (4 bits: 2^3), so that the output is seldom rescaled:
 // weights are at most that, sums stay fp32.
 //
@@ -25,13 +26,13 @@
 // are looked at: rows of V that nobody sees are zeroed, and where a finite number is missing in another one, the
 // block's P V is added up by the softmax threads, row by row over the keys that the row sees, instead of by the tensor cores.
 //
-// Measured (head_dim 128, 32 and 8 heads unless said): one prompt of 8192 tokens, bf16, 368 us (1.49 PFLOP/s, 0.78 of
-// cuBLAS's burst): a block takes about 2900 clocks, its products 2048; a tile's softmax and its own products follow each other,
-// and the thread that issues them shares its scheduler with two softmax warps.  333 tokens 17 us: launch, set-up, three blocks
-// one after the other, output.  Over 8 and 4 bits a block takes half as long again: the 64 KB that are stored to shared
-// memory for it contend with the products' reads of their operands (48 tokens over 65000, 64 and 8 heads: bf16 109 us, 8 bits 159,
-// 4 bits 168).  Capped scores cost an exponential and a dozen multiplications more each: 9 ragged prompts of up to 1500 tokens
-// over up to 1000, 8 bits, 77 us, 53 uncapped.
+// Measured (head_dim 128, 32 and 8 heads unless said): one prompt of 8192 tokens, bf16, 485 us in short runs, 521 at the power cap (1.13
+// and 1.06 PFLOP/s without the second parts' products, 1.7 and 1.6 with them): a block takes about 3800 clocks, its products 3072; a
+// tile's softmax and its own products follow each other, and the thread that issues them shares its scheduler with two softmax warps.
+// 333 tokens 17.8 us: launch, set-up, three blocks one after the other, output.  Over 8 and 4 bits the 64 KB that are stored to shared
+// memory for a block contend with the products' reads of their operands (8192 tokens 621 and 728 us; 48 tokens over 65000, 64 and 8 heads: bf16
+// 140 us, 8 bits 180, 4 bits 200).  Caps cost a pass of their own over the scores, with an exponential where they are not small: 9 ragged
+// prompts of up to 1500 tokens over up to 1000, 8 bits, 84 us, 59 uncapped.
 #include <cuda_fp4.h>
 #include <cuda_fp8.h>
 
@@ -355,8 +356,10 @@ __device__ __forceinline__ void find_units(const PromptArgs &a, const Smem &s) {
     bool over = false;
     int it = 0;
     for (int64_t round = 0; !over; ++round) {
-        // Where units may be split there are no more than CTAs, and CTA b takes unit b, whose slot is b.  Else the next one, taken
-        // when warp 10 has started the last copies of the one before: a unit taken earlier waits here while other CTAs run dry.
+        // Where units are split there are no more than CTAs, and CTA b takes unit b, whose slot is b.  The host, which has no lengths, also
+        // says that they may be split for batches of short pieces that make more units than CTAs: none is split then, and CTAs take
+        // them in turn.  Else the next one, taken when warp 10 has started the last copies of the one before: a unit taken
+        // earlier waits here while other CTAs run dry.
         if (!wait_on(s.u_want, it & 1, a, s.abort)) break;
         int64_t u = round * gridDim.x + blockIdx.x;
         if (!a.may_split) u = __shfl_sync(0xFFFFFFFFu, lane == 0 ? atomicAdd(a.taken, 1u) : 0u, 0);
@@ -1442,7 +1445,9 @@ cudaError_t launch_prompt(const bd_kv_cache &c, const void *q, int32_t q_heads, 
     a.cap_in = rule.cap > 0.f ? 2.f / rule.cap : 0.f;
     a.v_unit = c.kv_type == BD_KV_E2M1 ? 8.f : 1.f;
     a.plain = rule.scale > 0.f && !(rule.cap > 0.f) && !rule.slopes;
-    // the units are at least this many (offsets[n_seqs] = total): more than CTAs are not split
+    // The units are at least this many (offsets[n_seqs] = total): more than CTAs are not split.  Sequences of less than a unit's tokens make
+    // more, a unit each: past the number of CTAs the time steps up to whole sequences' keys in turn (4 tokens or fewer of each over up to
+    // 30000, 8 KV heads, bf16: 16 sequences 129 us, 18 214, 20 446, 64 477)
     const int64_t units = (total + 2 * a.tile_tokens - 1) / (2 * a.tile_tokens) * c.kv_heads * a.subs;
     a.may_split = units <= ctx.num_sms && max_pages * static_cast<int64_t>(c.page_size) > 4 * kBlock;
     CUtensorMap map_q, map_k, map_v;
