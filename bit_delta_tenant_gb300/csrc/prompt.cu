@@ -3,7 +3,7 @@
 //   o = sum_j exp(s_j - m) V_j / sum_j exp(s_j - m),  s_j the score rule of q . K_j
 //
 // Bound: tensor cores (4 head_dim products per seen pair, and 2 head_dim for the second parts of its weights; a block of 128 keys against
-// 256 rows is 3072 clocks of tcgen05 at head_dim 128, its 32768 exponentials about a third of that), HBM or latency for a few queries.
+// 256 rows is 1.5 x 2048 clocks of tcgen05 at head_dim 128, its 32768 exponentials about a third of that), HBM or latency for a few queries.
 //
 // Work.  A row is one query of one head; the heads that share a KV head are rows of the same tile, so that K and V are
 // read once for all of them and a tile of 128 rows holds 128 / heads tokens.  A unit is two such tiles (256 rows) of
@@ -27,7 +27,7 @@
 // block's P V is added up by the softmax threads, row by row over the keys that the row sees, instead of by the tensor cores.
 //
 // Measured (head_dim 128, 32 and 8 heads unless said): one prompt of 8192 tokens, bf16, 485 us in short runs, 521 at the power cap (1.13
-// and 1.06 PFLOP/s without the second parts' products, 1.7 and 1.6 with them): a block takes about 3800 clocks, its products 3072; a
+// and 1.06 PFLOP/s without the second parts' products, 1.7 and 1.6 with them): a block takes about 3800 clocks, its products 1.5 x 2048; a
 // tile's softmax and its own products follow each other, and the thread that issues them shares its scheduler with two softmax warps.
 // 333 tokens 17.8 us: launch, set-up, three blocks one after the other, output.  Over 8 and 4 bits the 64 KB that are stored to shared
 // memory for a block contend with the products' reads of their operands (8192 tokens 621 and 728 us; 48 tokens over 65000, 64 and 8 heads: bf16
